@@ -508,6 +508,200 @@ gattn_status gattn_layer_set_events(gattn_layer *layer, void *const *events, int
 gattn_status gattn_layer_set_test_wait(gattn_layer *layer, int64_t wait_limit_ns,
                                        int32_t withhold_stage);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Packed sequences: the prompt pass of a gated full-attention layer and the
+ * gated delta-rule layers that stand beside it in the hybrid stack (Atlas
+ * spark_model/forward/qwen3_5/mod.rs: forward_full_attention, and the
+ * linear-attention layer's gated_delta_rule_decode).
+ *
+ * Conventions shared by the four entry points below:
+ *   - Sequences of different lengths are packed along one row axis: sequence s
+ *     owns rows cu_rows[s] .. cu_rows[s+1]-1 of every row tensor.  cu_rows is
+ *     (device) int32 [num_seqs + 1], non-decreasing, its last entry at most
+ *     total_rows, the rows that the tensors hold.  Rows before cu_rows[0] and
+ *     at or past cu_rows[num_seqs] are neither read nor written.  A sequence
+ *     may have no rows.
+ *   - Tensors are described by a base pointer and element strides of the row
+ *     ("token") and of the head; the elements of a head are contiguous.  bf16
+ *     and fp32 rows: base 16-byte aligned, strides positive multiples of 8
+ *     elements.  Slices of a wider projection output are such tensors.
+ *   - Outputs must not overlap inputs unless an entry point says so.
+ *   - `status` (device) uint32 [1], may be NULL: the kernels OR GATTN_STATUS_*
+ *     bits into it (never clear it), so that a caller can read it when it
+ *     likes; GATTN_STATUS_RANGE marks a sequence that was skipped because its
+ *     rows, positions or slot lie outside what the descriptor holds.
+ *   - No handle, no allocation, no synchronization, no workspace: calls on
+ *     different streams share nothing, and every call can be captured into a
+ *     CUDA graph.  The launches go to the current device, which must be the
+ *     one the pointers belong to.
+ *   - num_seqs == 0 or total_rows == 0 launches nothing (but see gattn_delta_*).
+ * Errors of every entry point, before anything is launched: GATTN_E_INVALID_ARG
+ * for a NULL pointer, a size, stride or alignment outside these rules, and
+ * GATTN_E_UNSUPPORTED for shapes stated there; GATTN_E_CUDA when a launch fails.
+ * ---------------------------------------------------------------------------
+ */
+enum { GATTN_STATUS_RANGE = 1, GATTN_STATUS_TIMEOUT = 2 };
+
+/*
+ * The rows of a prompt between the projections and the attention: per-head QK
+ * RMSNorm, partial RoPE and the KV append, as steps 3 to 6 of gattn_layer_step
+ * do them, for any number of rows.  Row i of sequence s has position
+ * p = cache_pos[s] + i:
+ *   q_out[row][h]           = bf16(RoPE_p(RMSNorm(q[row][h]) * q_norm))
+ *   k_cache[slot][hk][p]    = bf16(RoPE_p(RMSNorm(k[row][hk]) * k_norm))
+ *   v_cache[slot][hk][p]    = bf16(v[row][hk])
+ * The gate half of a doubled q_proj stays where it is: q is the projection
+ * output with q_stride_head = 2 * head_dim.
+ *   x_dtype       GATTN_DTYPE_F32 or GATTN_DTYPE_BF16: type of q, k and v
+ *   slots         (device) int32 [num_seqs] or NULL (slot = s): the cache row of
+ *                 each sequence.  A slot may appear once; a later sequence that
+ *                 names it again is skipped.
+ *   q_out         bf16 [total_rows][num_heads][head_dim] by strides
+ *   k_cache, v_cache  bf16, element (slot, hk, p, j) at base + slot*stride_batch +
+ *                 hk*stride_head + p*stride_token + j, as gattn_kv_desc, each
+ *                 with strides of its own
+ * A sequence is skipped (its q_out rows zero, its cache untouched,
+ * GATTN_STATUS_RANGE) when cache_pos < 0, cache_pos + rows > cache_capacity, or
+ * its slot is outside [0, cache_batch) or taken.  head_dim: a multiple of 64 up
+ * to 256 (else GATTN_E_UNSUPPORTED).  Rotary dims, theta and eps as in
+ * gattn_cfg.
+ */
+typedef struct gattn_prompt_rows_desc {
+    int32_t num_heads, num_kv_heads, head_dim;
+    float partial_rotary_factor, rope_theta, rms_eps;
+    int32_t x_dtype;
+    int32_t num_seqs;
+    int32_t total_rows;
+    const int32_t *cu_rows;
+    const int32_t *cache_pos;
+    const int32_t *slots;
+    const void *q, *k, *v;
+    int64_t q_stride_token, q_stride_head;
+    int64_t k_stride_token, k_stride_head;
+    int64_t v_stride_token, v_stride_head;
+    const uint16_t *q_norm, *k_norm;      /* bf16 [head_dim] (device) */
+    void *q_out;
+    int64_t o_stride_token, o_stride_head;
+    void *k_cache, *v_cache;
+    int32_t cache_batch, cache_capacity;
+    int64_t kc_stride_token, kc_stride_head, kc_stride_batch;
+    int64_t vc_stride_token, vc_stride_head, vc_stride_batch;
+    uint32_t *status;
+} gattn_prompt_rows_desc;
+
+gattn_status gattn_prompt_rows(const gattn_prompt_rows_desc *desc, gattn_stream stream);
+
+/*
+ * Causal attention of packed prompt rows with grouped heads and the output
+ * gate:
+ *   out[row][h] = bf16( sum_j softmax_j(scale * q[row][h] . k_j) v_j  *  sigmoid(gate[row][h]) )
+ * over the keys j of the row's sequence that it may see; query head h reads KV
+ * head h / (num_heads / num_kv_heads).  Where the keys come from:
+ *   cache_pos != NULL  a cache [kv_batch][num_kv_heads][kv_rows] by strides:
+ *                      sequence s reads cache row slots[s] (NULL: s), and its
+ *                      row i sees positions 0 .. cache_pos[s] + i (the new
+ *                      rows' keys are in the cache, see gattn_prompt_rows).
+ *                      Slots may repeat: nothing is written there.
+ *   cache_pos == NULL  packed keys of kv_rows rows (kv_batch 1): sequence s owns
+ *                      key rows cu_kv[s] .. cu_kv[s+1]-1 (cu_kv NULL: cu_rows),
+ *                      and its row i sees the first i + 1 + (keys - rows) of
+ *                      them: the last row sees all.
+ * A row that sees no key gives zeros.  Values and keys that a row does not see
+ * do not reach it, whatever they hold (NaN and infinities included).
+ *   q, k, v       bf16
+ *   gate          gate_dtype (GATTN_DTYPE_F32 or _BF16), or NULL for no gate
+ *   out           bf16
+ *   scale         finite, > 0
+ *   max_kv        a hint: the most keys of any sequence (0: unknown).  It only
+ *                 chooses how the work is split, never the result's validity.
+ * A sequence is skipped (out rows zero, GATTN_STATUS_RANGE) when its slot,
+ * positions or key rows lie outside the keys' tensor.  head_dim: a multiple of
+ * 64 up to 256; num_heads * head_dim <= 65536 (else GATTN_E_UNSUPPORTED).
+ */
+typedef struct gattn_prompt_attention_desc {
+    int32_t num_heads, num_kv_heads, head_dim;
+    float scale;
+    int32_t num_seqs;
+    int32_t total_rows;
+    const int32_t *cu_rows;
+    const int32_t *cu_kv;
+    const int32_t *cache_pos;
+    const int32_t *slots;
+    const void *q;
+    int64_t q_stride_token, q_stride_head;
+    const void *k, *v;
+    int32_t kv_batch, kv_rows;
+    int64_t k_stride_token, k_stride_head, k_stride_batch;
+    int64_t v_stride_token, v_stride_head, v_stride_batch;
+    const void *gate;
+    int32_t gate_dtype;
+    int32_t max_kv;
+    int64_t g_stride_token, g_stride_head;
+    void *out;
+    int64_t o_stride_token, o_stride_head;
+    uint32_t *status;
+} gattn_prompt_attention_desc;
+
+gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *desc, gattn_stream stream);
+
+/*
+ * The gated delta rule.  Per value head h (key head h / (num_v_heads /
+ * num_k_heads)) a state S of k_dim x v_dim, and per row of a sequence, in order:
+ *   S <- exp(g) S
+ *   w  = beta (v - S^T k)
+ *   S <- S + k w^T
+ *   out = bf16(scale S^T q)
+ * with q and k divided by sqrt(sum x^2 + l2_eps) first when qk_l2norm is set.
+ *   q, k          bf16 [total_rows][num_k_heads][k_dim] by strides
+ *   v, out        bf16 [total_rows][num_v_heads][v_dim] by strides
+ *   g, beta       fp32 [total_rows][num_v_heads], row strides >= num_v_heads; g is
+ *                 the natural logarithm of the decay
+ *   cu_rows       NULL: every sequence has total_rows / num_seqs rows
+ *   state         fp32 [num_slots][num_v_heads][k_dim][v_dim], slot stride
+ *                 state_stride (elements, a multiple of 4); the state before
+ *                 the first row; NULL: zeros
+ *   state_out     the state after the last row, same layout; equal to state
+ *                 (in place), a buffer of its own, or NULL (not kept: drafted
+ *                 rows that may be rejected).  A sequence without rows copies
+ *                 its state.
+ *   slots         (device) int32 [num_seqs] or NULL (slot = s).  A slot may appear
+ *                 once; a later sequence that names it again is skipped, as is
+ *                 one outside [0, num_slots) (out rows zero, state untouched,
+ *                 GATTN_STATUS_RANGE).
+ * gattn_delta_prompt is for prompts: it works through the rows in chunks.
+ * gattn_delta_step is for one to a few new rows of many sequences: it works
+ * row by row.  Both take any lengths and differ in rounding only.
+ * num_seqs > 0 with total_rows == 0 copies the states.  k_dim 64 or 128; v_dim a
+ * multiple of 32 up to 256 (else GATTN_E_UNSUPPORTED).
+ */
+typedef struct gattn_delta_desc {
+    int32_t num_k_heads, num_v_heads, k_dim, v_dim;
+    float scale;
+    int32_t qk_l2norm;
+    float l2_eps;
+    int32_t num_seqs;
+    int32_t total_rows;
+    int32_t num_slots;
+    const int32_t *cu_rows;
+    const int32_t *slots;
+    const void *q, *k, *v;
+    int64_t q_stride_token, q_stride_head;
+    int64_t k_stride_token, k_stride_head;
+    int64_t v_stride_token, v_stride_head;
+    const float *g, *beta;
+    int64_t g_stride_token, beta_stride_token;
+    const float *state;
+    float *state_out;
+    int64_t state_stride;
+    void *out;
+    int64_t o_stride_token, o_stride_head;
+    uint32_t *status;
+} gattn_delta_desc;
+
+gattn_status gattn_delta_prompt(const gattn_delta_desc *desc, gattn_stream stream);
+gattn_status gattn_delta_step(const gattn_delta_desc *desc, gattn_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

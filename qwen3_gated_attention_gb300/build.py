@@ -14,6 +14,8 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+# the packed-sequence operators (prompt pass, delta rule)
+CSRC_SEQ = os.path.join(PKG, "csrc_seq")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgattn.so")
@@ -28,11 +30,13 @@ def _nvcc():
 
 
 def _sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
+    return [os.path.join(d, f) for d in (CSRC, CSRC_SEQ) for f in sorted(os.listdir(d))
+            if f.endswith((".cu", ".cpp"))]
 
 
 def _headers():
-    hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    hs = [os.path.join(d, f) for d in (CSRC, CSRC_SEQ) for f in os.listdir(d)
+          if f.endswith((".cuh", ".h"))]
     hs.append(os.path.join(INCLUDE, "gattn.h"))
     return hs
 
@@ -43,7 +47,7 @@ def _compile(src, nvcc, verbose_ptxas):
     if os.path.exists(obj) and os.path.getmtime(obj) >= newest_dep:
         return obj, None
     cmd = [nvcc, "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
-           "-I", CSRC, "-c", src, "-o", obj + ".tmp"]
+           "-I", CSRC, "-I", CSRC_SEQ, "-c", src, "-o", obj + ".tmp"]
     if src.endswith(".cpp"):
         cmd = [nvcc, "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-c", src, "-o",
                obj + ".tmp"]

@@ -1,6 +1,8 @@
 """Device-memory plumbing around the C ABI: torch owns the buffers (weights in the
 interchange layout, bf16 caches, inputs, outputs); every computation goes
-through ``gattn.layer_step`` and friends."""
+through ``gattn.layer_step`` and friends.  ``DeviceLayer`` holds one layer;
+``prompt_rows``, ``prompt_attention``, ``delta_prompt`` and ``delta_step`` call
+the packed-sequence operators on tensors."""
 from __future__ import annotations
 
 import numpy as np
@@ -189,3 +191,238 @@ def x_to_device(spec, x: np.ndarray, device="cuda:0") -> torch.Tensor:
 
 def bf16_tensor_to_f64(t: torch.Tensor) -> np.ndarray:
     return t.float().cpu().numpy().astype(np.float64)
+
+
+# -------------------------------------------------------- packed sequences
+#
+# Torch forms of the packed-sequence entry points: shapes and strides are read
+# off the tensors, the launch goes to the current stream of their device (or to
+# `stream`, a cudaStream_t handle of that device).  Slices of a wider projection
+# output are passed as they are, nothing is copied.
+
+_DTYPES = {torch.float32: gattn.DTYPE_F32, torch.bfloat16: gattn.DTYPE_BF16}
+
+
+def _need(ok, message):
+    if not ok:
+        raise ValueError(message)
+
+
+def _on(t: torch.Tensor, name: str, device, dtypes, dim: int):
+    _need(isinstance(t, torch.Tensor) and t.device == device,
+          f"{name} must be a tensor on {device}")
+    _need(t.dtype in dtypes, f"{name} has type {t.dtype}, not one of {dtypes}")
+    _need(t.dim() == dim, f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(token, head) strides of a [rows][heads][elements] tensor.  A dimension of
+    one or no entries may have any stride: a valid one stands in for it."""
+    _need(t.shape[2] <= 1 or t.stride(2) == 1, f"{name}: the elements of a head must be contiguous")
+    head = t.stride(1) if t.shape[1] > 1 else max(8, t.shape[2])
+    tok = t.stride(0) if t.shape[0] > 1 else max(8, t.shape[1] * t.shape[2])
+    return tok, head
+
+
+def _planes(t: torch.Tensor, name: str):
+    """(token, head, batch) strides of a [batch][heads][tokens][elements] cache."""
+    _need(t.shape[3] <= 1 or t.stride(3) == 1, f"{name}: the elements of a head must be contiguous")
+    tok = t.stride(2) if t.shape[2] > 1 else max(8, t.shape[3])
+    head = t.stride(1) if t.shape[1] > 1 else max(8, t.shape[2] * t.shape[3])
+    batch = t.stride(0) if t.shape[0] > 1 else max(8, t.shape[1] * t.shape[2] * t.shape[3])
+    return tok, head, batch
+
+
+def _index(t, name, device, n):
+    if t is None:
+        return None
+    _on(t, name, device, (torch.int32,), 1)
+    _need(t.shape[0] == n and t.is_contiguous(), f"{name} must be {n} contiguous int32")
+    return t.data_ptr()
+
+
+def _cu(t, name, device):
+    _on(t, name, device, (torch.int32,), 1)
+    _need(t.shape[0] >= 1 and t.is_contiguous(), f"{name} must be contiguous int32 [num_seqs + 1]")
+    return t.data_ptr(), t.shape[0] - 1
+
+
+def _status(t, device):
+    if t is None:
+        return None
+    _need(isinstance(t, torch.Tensor) and t.device == device and t.dtype == torch.int32 and
+          t.numel() == 1, "status must be one int32 on the tensors' device")
+    return t.data_ptr()
+
+
+def _call(fn, desc, device, stream):
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        fn(desc, stream)
+    else:
+        with torch.cuda.device(device):
+            fn(desc, stream)
+
+
+def prompt_rows(q, k, v, q_norm, k_norm, k_cache, v_cache, cu_rows, cache_pos, *,
+                partial_rotary_factor, rope_theta, rms_eps, q_out=None, slots=None, status=None,
+                stream=None):
+    """QK RMSNorm, partial RoPE and KV append of packed rows (gattn_prompt_rows).
+
+    q [T][H][d], k and v [T][Hk][d] (fp32 or bf16); q_norm, k_norm bf16 [d];
+    k_cache, v_cache bf16 [B][Hk][capacity][d] views, written at cache_pos[s] + i;
+    cu_rows int32 [n + 1], cache_pos and slots int32 [n].  Returns q_out, bf16
+    [T][H][d] (allocated when not given)."""
+    dev = q.device
+    _on(q, "q", dev, tuple(_DTYPES), 3)
+    T, H, d = q.shape
+    for t, name in ((k, "k"), (v, "v")):
+        _on(t, name, dev, (q.dtype,), 3)
+    Hk = k.shape[1]
+    _need(k.shape == (T, Hk, d) and v.shape == (T, Hk, d), "k and v must be [T][Hk][d]")
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        _on(t, name, dev, (torch.bfloat16,), 1)
+        _need(t.shape == (d,) and t.is_contiguous(), f"{name} must be contiguous [d]")
+        _need(t.data_ptr() % 16 == 0, f"{name} must be 16-byte aligned")
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _on(t, name, dev, (torch.bfloat16,), 4)
+    B, _, cap, _ = k_cache.shape
+    _need(k_cache.shape == (B, Hk, cap, d) and v_cache.shape == (B, Hk, cap, d),
+          "k_cache and v_cache must be [B][Hk][capacity][d]")
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+    _on(q_out, "q_out", dev, (torch.bfloat16,), 3)
+    _need(q_out.shape == (T, H, d), "q_out must be [T][H][d]")
+    cu, n = _cu(cu_rows, "cu_rows", dev)
+    desc = gattn.gattn_prompt_rows_desc(
+        H, Hk, d, partial_rotary_factor, rope_theta, rms_eps, _DTYPES[q.dtype], n, T, cu,
+        _index(cache_pos, "cache_pos", dev, n), _index(slots, "slots", dev, n), q.data_ptr(),
+        k.data_ptr(), v.data_ptr(), *_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"),
+        q_norm.data_ptr(), k_norm.data_ptr(), q_out.data_ptr(), *_rows(q_out, "q_out"),
+        k_cache.data_ptr(), v_cache.data_ptr(), B, cap, *_planes(k_cache, "k_cache"),
+        *_planes(v_cache, "v_cache"), _status(status, dev))
+    if n and T:
+        _call(gattn.prompt_rows, desc, dev, stream)
+    return q_out
+
+
+def prompt_attention(q, k, v, cu_rows, *, cu_kv=None, cache_pos=None, slots=None, gate=None,
+                     scale=None, max_kv=0, out=None, status=None, stream=None):
+    """Causal attention of packed rows with the output gate (gattn_prompt_attention).
+
+    q [T][H][d] bf16.  Without cache_pos: k, v [Tk][Hk][d] bf16 packed by cu_kv
+    (default cu_rows).  With cache_pos int32 [n]: k, v are caches [B][Hk][rows][d]
+    bf16 that already hold the new rows, slots int32 [n] their cache rows.  gate
+    [T][H][d] fp32 or bf16 before its sigmoid, or None.  scale defaults to
+    d ** -0.5; max_kv is a hint.  Returns out, bf16 [T][H][d]."""
+    dev = q.device
+    _on(q, "q", dev, (torch.bfloat16,), 3)
+    T, H, d = q.shape
+    cached = cache_pos is not None
+    for t, name in ((k, "k"), (v, "v")):
+        _on(t, name, dev, (torch.bfloat16,), 4 if cached else 3)
+    _need(k.shape == v.shape and k.shape[-1] == d, "k and v must have one shape, with q's head_dim")
+    Hk = k.shape[1]
+    if cached:
+        B, rows = k.shape[0], k.shape[2]
+        kst, vst = _planes(k, "k"), _planes(v, "v")
+    else:
+        B, rows = 1, k.shape[0]
+        kst, vst = _rows(k, "k") + (8,), _rows(v, "v") + (8,)
+    gst, gp, gdt = (8, 8), None, gattn.DTYPE_BF16
+    if gate is not None:
+        _on(gate, "gate", dev, tuple(_DTYPES), 3)
+        _need(gate.shape == q.shape, "gate must have q's shape")
+        gst, gp, gdt = _rows(gate, "gate"), gate.data_ptr(), _DTYPES[gate.dtype]
+    if out is None:
+        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+    _on(out, "out", dev, (torch.bfloat16,), 3)
+    _need(out.shape == q.shape, "out must have q's shape")
+    cu, n = _cu(cu_rows, "cu_rows", dev)
+    ckv = None
+    if cu_kv is not None:
+        ckv, nk = _cu(cu_kv, "cu_kv", dev)
+        _need(nk == n, "cu_kv and cu_rows must have one length")
+    if rows == 0:
+        # no keys at all: every row of a sequence is empty
+        _need(not cached, "a cache must hold at least one row")
+        k = v = q
+        kst = vst = (8, 8, 8)
+        rows = 1
+    desc = gattn.gattn_prompt_attention_desc(
+        H, Hk, d, d ** -0.5 if scale is None else scale, n, T, cu, ckv,
+        _index(cache_pos, "cache_pos", dev, n), _index(slots, "slots", dev, n), q.data_ptr(),
+        *_rows(q, "q"), k.data_ptr(), v.data_ptr(), B, rows, *kst, *vst, gp, gdt, max_kv, *gst,
+        out.data_ptr(), *_rows(out, "out"), _status(status, dev))
+    if n and T:
+        _call(gattn.prompt_attention, desc, dev, stream)
+    return out
+
+
+def _delta(fn, q, k, v, g, beta, cu_rows, num_seqs, state, state_out, slots, scale, qk_l2norm,
+           l2_eps, out, status, stream):
+    dev = q.device
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _on(t, name, dev, (torch.bfloat16,), 3)
+    T, Hk, dk = q.shape
+    Hv, dv = v.shape[1:]
+    _need(k.shape == q.shape and v.shape[0] == T, "k must have q's shape, v as many rows")
+    for t, name in ((g, "g"), (beta, "beta")):
+        _on(t, name, dev, (torch.float32,), 2)
+        _need(t.shape == (T, Hv) and (Hv <= 1 or t.stride(1) == 1),
+              f"{name} must be [T][Hv] with contiguous heads")
+    if cu_rows is not None:
+        cu, n = _cu(cu_rows, "cu_rows", dev)
+        _need(num_seqs is None or num_seqs == n, "num_seqs and cu_rows disagree")
+    else:
+        _need(num_seqs is not None, "num_seqs is needed without cu_rows")
+        cu, n = None, num_seqs
+    nslots, stride = 0, 0
+    for t, name in ((state, "state"), (state_out, "state_out")):
+        if t is None:
+            continue
+        _on(t, name, dev, (torch.float32,), 4)
+        _need(t.shape[1:] == (Hv, dk, dv) and t.shape[0] >= 1 and t[0].is_contiguous(),
+              f"{name} must be [slots][Hv][dk][dv] with contiguous slots")
+        st = t.stride(0) if t.shape[0] > 1 else Hv * dk * dv
+        _need(nslots in (0, t.shape[0]) and stride in (0, st),
+              "state and state_out must have one shape and stride")
+        nslots, stride = t.shape[0], st
+    if out is None:
+        out = torch.empty((T, Hv, dv), dtype=torch.bfloat16, device=dev)
+    _on(out, "out", dev, (torch.bfloat16,), 3)
+    _need(out.shape == v.shape, "out must have v's shape")
+    desc = gattn.gattn_delta_desc(
+        Hk, Hv, dk, dv, dk ** -0.5 if scale is None else scale, int(bool(qk_l2norm)), l2_eps, n, T,
+        nslots, cu, _index(slots, "slots", dev, n), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        *_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"), g.data_ptr(), beta.data_ptr(),
+        g.stride(0) if T > 1 else Hv, beta.stride(0) if T > 1 else Hv,
+        state.data_ptr() if state is not None else None,
+        state_out.data_ptr() if state_out is not None else None, stride, out.data_ptr(),
+        *_rows(out, "out"), _status(status, dev))
+    if n:
+        _call(fn, desc, dev, stream)
+    return out
+
+
+def delta_prompt(q, k, v, g, beta, cu_rows=None, *, num_seqs=None, state=None, state_out=None,
+                 slots=None, scale=None, qk_l2norm=False, l2_eps=1e-6, out=None, status=None,
+                 stream=None):
+    """The gated delta rule over packed prompts (gattn_delta_prompt).
+
+    q, k [T][Hk][dk] and v [T][Hv][dv] bf16; g (log decay) and beta fp32 [T][Hv];
+    cu_rows int32 [n + 1], or num_seqs sequences of T / num_seqs rows; state and
+    state_out fp32 [slots][Hv][dk][dv] (one tensor for both: in place); slots
+    int32 [n].  scale defaults to dk ** -0.5.  Returns out, bf16 [T][Hv][dv]."""
+    return _delta(gattn.delta_prompt, q, k, v, g, beta, cu_rows, num_seqs, state, state_out, slots,
+                  scale, qk_l2norm, l2_eps, out, status, stream)
+
+
+def delta_step(q, k, v, g, beta, cu_rows=None, *, num_seqs=None, state=None, state_out=None,
+               slots=None, scale=None, qk_l2norm=False, l2_eps=1e-6, out=None, status=None,
+               stream=None):
+    """The gated delta rule for one to a few new rows of many sequences
+    (gattn_delta_step); arguments as delta_prompt."""
+    return _delta(gattn.delta_step, q, k, v, g, beta, cu_rows, num_seqs, state, state_out, slots,
+                  scale, qk_l2norm, l2_eps, out, status, stream)

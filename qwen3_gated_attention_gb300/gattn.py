@@ -35,8 +35,12 @@ EXPORTS = (
     "gattn_layer_step_block", "gattn_kv_register_turbo4v",
     "gattn_turbo4_codebook", "gattn_turbo4_quantize_device", "gattn_layer_set_mask",
     "gattn_kv_register_turbo4", "gattn_layer_step_kernels", "gattn_layer_set_test_wait",
-    "gattn_layer_step_host",
+    "gattn_layer_step_host", "gattn_prompt_rows", "gattn_prompt_attention", "gattn_delta_prompt",
+    "gattn_delta_step",
 )
+
+# bits of the packed-sequence operators' status word
+STATUS_RANGE, STATUS_TIMEOUT = 1, 2
 
 
 class GattnError(RuntimeError):
@@ -93,6 +97,69 @@ class gattn_taps(C.Structure):
     _fields_ = [("y", C.c_void_p), ("attn", C.c_void_p)]
 
 
+def _fields(text):
+    """ctypes fields of a descriptor: "type: name name" per line (i32, i64, f32, ptr)."""
+    kinds = {"i32": C.c_int32, "i64": C.c_int64, "f32": C.c_float, "ptr": C.c_void_p}
+    out = []
+    for line in text.strip().splitlines():
+        kind, names = line.split(":")
+        out += [(n, kinds[kind.strip()]) for n in names.split()]
+    return out
+
+
+class gattn_prompt_rows_desc(C.Structure):
+    _fields_ = _fields("""
+        i32: num_heads num_kv_heads head_dim
+        f32: partial_rotary_factor rope_theta rms_eps
+        i32: x_dtype num_seqs total_rows
+        ptr: cu_rows cache_pos slots q k v
+        i64: q_stride_token q_stride_head k_stride_token k_stride_head v_stride_token v_stride_head
+        ptr: q_norm k_norm q_out
+        i64: o_stride_token o_stride_head
+        ptr: k_cache v_cache
+        i32: cache_batch cache_capacity
+        i64: kc_stride_token kc_stride_head kc_stride_batch
+        i64: vc_stride_token vc_stride_head vc_stride_batch
+        ptr: status""")
+
+
+class gattn_prompt_attention_desc(C.Structure):
+    _fields_ = _fields("""
+        i32: num_heads num_kv_heads head_dim
+        f32: scale
+        i32: num_seqs total_rows
+        ptr: cu_rows cu_kv cache_pos slots q
+        i64: q_stride_token q_stride_head
+        ptr: k v
+        i32: kv_batch kv_rows
+        i64: k_stride_token k_stride_head k_stride_batch
+        i64: v_stride_token v_stride_head v_stride_batch
+        ptr: gate
+        i32: gate_dtype max_kv
+        i64: g_stride_token g_stride_head
+        ptr: out
+        i64: o_stride_token o_stride_head
+        ptr: status""")
+
+
+class gattn_delta_desc(C.Structure):
+    _fields_ = _fields("""
+        i32: num_k_heads num_v_heads k_dim v_dim
+        f32: scale
+        i32: qk_l2norm
+        f32: l2_eps
+        i32: num_seqs total_rows num_slots
+        ptr: cu_rows slots q k v
+        i64: q_stride_token q_stride_head k_stride_token k_stride_head v_stride_token v_stride_head
+        ptr: g beta
+        i64: g_stride_token beta_stride_token
+        ptr: state state_out
+        i64: state_stride
+        ptr: out
+        i64: o_stride_token o_stride_head
+        ptr: status""")
+
+
 _lib = None
 
 
@@ -138,6 +205,10 @@ def lib():
         L.gattn_kv_register_turbo4.argtypes = [p, C.POINTER(gattn_kv_turbo4_desc), C.POINTER(p)]
         L.gattn_layer_set_test_wait.argtypes = [p, i64, i32]
         L.gattn_layer_step_host.argtypes = [p, p, p, p, i32, i32, p, p]
+        L.gattn_prompt_rows.argtypes = [C.POINTER(gattn_prompt_rows_desc), p]
+        L.gattn_prompt_attention.argtypes = [C.POINTER(gattn_prompt_attention_desc), p]
+        L.gattn_delta_prompt.argtypes = [C.POINTER(gattn_delta_desc), p]
+        L.gattn_delta_step.argtypes = [C.POINTER(gattn_delta_desc), p]
         for name in ("gattn_cfg_validate", "gattn_layer_create", "gattn_layer_set_weights",
                      "gattn_kv_register", "gattn_layer_step", "gattn_layer_poll_status",
                      "gattn_layer_set_taps", "gattn_pack_affine_host", "gattn_unpack_codes_device",
@@ -146,7 +217,8 @@ def lib():
                      "gattn_layer_step_block", "gattn_kv_register_turbo4v",
                      "gattn_turbo4_codebook", "gattn_turbo4_quantize_device",
                      "gattn_layer_set_mask", "gattn_kv_register_turbo4",
-                     "gattn_layer_set_test_wait", "gattn_layer_step_host"):
+                     "gattn_layer_set_test_wait", "gattn_layer_step_host", "gattn_prompt_rows",
+                     "gattn_prompt_attention", "gattn_delta_prompt", "gattn_delta_step"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -329,6 +401,28 @@ def layer_set_test_wait(layer: int, wait_limit_ns: int = 0, withhold_stage: bool
     waits (0 restores the default) and whether CTA 0 of the q|k|v projection
     withholds its last weight stage so that one wait runs out."""
     _check(lib().gattn_layer_set_test_wait(layer, int(wait_limit_ns), 1 if withhold_stage else 0))
+
+
+# -------------------------------------------------------- packed sequences
+
+def prompt_rows(desc: gattn_prompt_rows_desc, stream: int = 0) -> None:
+    """QK RMSNorm, partial RoPE and KV append of packed prompt rows."""
+    _check(lib().gattn_prompt_rows(C.byref(desc), stream))
+
+
+def prompt_attention(desc: gattn_prompt_attention_desc, stream: int = 0) -> None:
+    """Causal gated attention of packed prompt rows."""
+    _check(lib().gattn_prompt_attention(C.byref(desc), stream))
+
+
+def delta_prompt(desc: gattn_delta_desc, stream: int = 0) -> None:
+    """The gated delta rule over packed prompts (chunked)."""
+    _check(lib().gattn_delta_prompt(C.byref(desc), stream))
+
+
+def delta_step(desc: gattn_delta_desc, stream: int = 0) -> None:
+    """The gated delta rule for a few new rows of many sequences (row by row)."""
+    _check(lib().gattn_delta_step(C.byref(desc), stream))
 
 
 # ------------------------------------------------------------ host helpers
