@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "gattn.h"
 
@@ -69,6 +71,24 @@ struct DeltaArgs {
     float scale, l2_eps;
     int l2norm;
 };
+
+// Lets a kernel take `bytes` of dynamic shared memory on the current device, once
+// per device (`done`: a bit for each of the first 64).
+template <class F>
+inline cudaError_t allow_smem(F *fn, int bytes, std::atomic<unsigned long long> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit))
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t s);
 cudaError_t launch_prompt_attn(const PromptAttnArgs &a, cudaStream_t s);
