@@ -201,67 +201,77 @@ def bf16_tensor_to_f64(t: torch.Tensor) -> np.ndarray:
 # output are passed as they are, nothing is copied.
 
 _DTYPES = {torch.float32: gattn.DTYPE_F32, torch.bfloat16: gattn.DTYPE_BF16}
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _need(ok, message):
-    if not ok:
-        raise ValueError(message)
+def _refuse(t, name, dev, dtypes, shape, what="must have shape"):
+    """The message for a tensor that _rows, _planes or _flat does not take."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} lies on {t.device}, not beside the first tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, not one of {dtypes}")
+    raise ValueError(f"{name} {what} {shape} (got {tuple(t.shape)}, strides {t.stride()})")
 
 
-def _on(t: torch.Tensor, name: str, device, dtypes, dim: int):
-    _need(isinstance(t, torch.Tensor) and t.device == device,
-          f"{name} must be a tensor on {device}")
-    _need(t.dtype in dtypes, f"{name} has type {t.dtype}, not one of {dtypes}")
-    _need(t.dim() == dim, f"{name} must have {dim} dimensions, got {tuple(t.shape)}")
+# A dimension of one or no entries may have any stride: a valid one stands in.
+
+def _rows(t, name, dev, dtypes, shape=None):
+    """(address, token stride, head stride) of a [rows][heads][elements] tensor."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes:
+        _refuse(t, name, dev, dtypes, shape)
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or (shape is not None and sh != shape):
+        _refuse(t, name, dev, dtypes, shape or "[rows][heads][elements]")
+    if st[2] != 1 and sh[2] > 1:
+        _refuse(t, name, dev, dtypes, shape, "needs contiguous elements:")
+    return (t.data_ptr(), st[0] if sh[0] > 1 else max(8, sh[1] * sh[2]),
+            st[1] if sh[1] > 1 else max(8, sh[2]))
 
 
-def _rows(t: torch.Tensor, name: str):
-    """(token, head) strides of a [rows][heads][elements] tensor.  A dimension of
-    one or no entries may have any stride: a valid one stands in for it."""
-    _need(t.shape[2] <= 1 or t.stride(2) == 1, f"{name}: the elements of a head must be contiguous")
-    head = t.stride(1) if t.shape[1] > 1 else max(8, t.shape[2])
-    tok = t.stride(0) if t.shape[0] > 1 else max(8, t.shape[1] * t.shape[2])
-    return tok, head
+def _planes(t, name, dev, dtypes, shape=None):
+    """(address, token, head, batch stride) of a [batch][heads][tokens][elements] tensor."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes:
+        _refuse(t, name, dev, dtypes, shape)
+    sh, st = t.shape, t.stride()
+    if len(sh) != 4 or (shape is not None and sh != shape):
+        _refuse(t, name, dev, dtypes, shape or "[batch][heads][tokens][elements]")
+    if st[3] != 1 and sh[3] > 1:
+        _refuse(t, name, dev, dtypes, shape, "needs contiguous elements:")
+    return (t.data_ptr(), st[2] if sh[2] > 1 else max(8, sh[3]),
+            st[1] if sh[1] > 1 else max(8, sh[2] * sh[3]),
+            st[0] if sh[0] > 1 else max(8, sh[1] * sh[2] * sh[3]))
 
 
-def _planes(t: torch.Tensor, name: str):
-    """(token, head, batch) strides of a [batch][heads][tokens][elements] cache."""
-    _need(t.shape[3] <= 1 or t.stride(3) == 1, f"{name}: the elements of a head must be contiguous")
-    tok = t.stride(2) if t.shape[2] > 1 else max(8, t.shape[3])
-    head = t.stride(1) if t.shape[1] > 1 else max(8, t.shape[2] * t.shape[3])
-    batch = t.stride(0) if t.shape[0] > 1 else max(8, t.shape[1] * t.shape[2] * t.shape[3])
-    return tok, head, batch
-
-
-def _index(t, name, device, n):
+def _flat(t, name, dev, dtypes, n):
+    """Address of a contiguous vector of n entries; 0 for None."""
     if t is None:
-        return None
-    _on(t, name, device, (torch.int32,), 1)
-    _need(t.shape[0] == n and t.is_contiguous(), f"{name} must be {n} contiguous int32")
+        return 0
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes or
+            t.shape != (n,) or not t.is_contiguous()):
+        _refuse(t, name, dev, dtypes, f"[{n}], contiguous")
     return t.data_ptr()
 
 
-def _cu(t, name, device):
-    _on(t, name, device, (torch.int32,), 1)
-    _need(t.shape[0] >= 1 and t.is_contiguous(), f"{name} must be contiguous int32 [num_seqs + 1]")
+def _cu(t, name, dev):
+    """(address, sequences) of the row offsets."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.int32 or
+            t.dim() != 1 or t.shape[0] < 1 or not t.is_contiguous()):
+        _refuse(t, name, dev, _I32, "[num_seqs + 1], contiguous")
     return t.data_ptr(), t.shape[0] - 1
 
 
-def _status(t, device):
-    if t is None:
-        return None
-    _need(isinstance(t, torch.Tensor) and t.device == device and t.dtype == torch.int32 and
-          t.numel() == 1, "status must be one int32 on the tensors' device")
-    return t.data_ptr()
-
-
-def _call(fn, desc, device, stream):
+def _call(fn, desc, dev, stream):
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev:
         fn(desc, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             fn(desc, stream)
 
 
@@ -272,36 +282,31 @@ def prompt_rows(q, k, v, q_norm, k_norm, k_cache, v_cache, cu_rows, cache_pos, *
 
     q [T][H][d], k and v [T][Hk][d] (fp32 or bf16); q_norm, k_norm bf16 [d];
     k_cache, v_cache bf16 [B][Hk][capacity][d] views, written at cache_pos[s] + i;
-    cu_rows int32 [n + 1], cache_pos and slots int32 [n].  Returns q_out, bf16
-    [T][H][d] (allocated when not given)."""
-    dev = q.device
-    _on(q, "q", dev, tuple(_DTYPES), 3)
+    cu_rows int32 [n + 1], cache_pos and slots int32 [n]; status int32 [1].
+    Returns q_out, bf16 [T][H][d] (allocated when not given)."""
+    dev = q.get_device()
+    qa = _rows(q, "q", dev, _DTYPES)
     T, H, d = q.shape
-    for t, name in ((k, "k"), (v, "v")):
-        _on(t, name, dev, (q.dtype,), 3)
-    Hk = k.shape[1]
-    _need(k.shape == (T, Hk, d) and v.shape == (T, Hk, d), "k and v must be [T][Hk][d]")
-    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        _on(t, name, dev, (torch.bfloat16,), 1)
-        _need(t.shape == (d,) and t.is_contiguous(), f"{name} must be contiguous [d]")
-        _need(t.data_ptr() % 16 == 0, f"{name} must be 16-byte aligned")
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _on(t, name, dev, (torch.bfloat16,), 4)
-    B, _, cap, _ = k_cache.shape
-    _need(k_cache.shape == (B, Hk, cap, d) and v_cache.shape == (B, Hk, cap, d),
-          "k_cache and v_cache must be [B][Hk][capacity][d]")
+    dtype = q.dtype
+    Hk = k.shape[1] if k.dim() == 3 else 0
+    ka = _rows(k, "k", dev, (dtype,), (T, Hk, d))
+    va = _rows(v, "v", dev, (dtype,), (T, Hk, d))
+    kc = _planes(k_cache, "k_cache", dev, _BF16)
+    B, _, cap, _ = shape = k_cache.shape
+    if shape != (B, Hk, cap, d):
+        _refuse(k_cache, "k_cache", dev, _BF16, (B, Hk, cap, d))
+    vc = _planes(v_cache, "v_cache", dev, _BF16, shape)
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
-    _on(q_out, "q_out", dev, (torch.bfloat16,), 3)
-    _need(q_out.shape == (T, H, d), "q_out must be [T][H][d]")
+        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+    oa = _rows(q_out, "q_out", dev, _BF16, (T, H, d))
     cu, n = _cu(cu_rows, "cu_rows", dev)
-    desc = gattn.gattn_prompt_rows_desc(
-        H, Hk, d, partial_rotary_factor, rope_theta, rms_eps, _DTYPES[q.dtype], n, T, cu,
-        _index(cache_pos, "cache_pos", dev, n), _index(slots, "slots", dev, n), q.data_ptr(),
-        k.data_ptr(), v.data_ptr(), *_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"),
-        q_norm.data_ptr(), k_norm.data_ptr(), q_out.data_ptr(), *_rows(q_out, "q_out"),
-        k_cache.data_ptr(), v_cache.data_ptr(), B, cap, *_planes(k_cache, "k_cache"),
-        *_planes(v_cache, "v_cache"), _status(status, dev))
+    desc = gattn.gattn_prompt_rows_desc.pack(
+        H, Hk, d, partial_rotary_factor, rope_theta, rms_eps, _DTYPES[dtype], n, T, cu,
+        _flat(cache_pos, "cache_pos", dev, _I32, n), _flat(slots, "slots", dev, _I32, n),
+        qa[0], ka[0], va[0], qa[1], qa[2], ka[1], ka[2], va[1], va[2],
+        _flat(q_norm, "q_norm", dev, _BF16, d), _flat(k_norm, "k_norm", dev, _BF16, d), oa[0],
+        oa[1], oa[2], kc[0], vc[0], B, cap, kc[1], kc[2], kc[3], vc[1], vc[2], vc[3],
+        _flat(status, "status", dev, _I32, 1))
     if n and T:
         _call(gattn.prompt_rows, desc, dev, stream)
     return q_out
@@ -315,46 +320,42 @@ def prompt_attention(q, k, v, cu_rows, *, cu_kv=None, cache_pos=None, slots=None
     (default cu_rows).  With cache_pos int32 [n]: k, v are caches [B][Hk][rows][d]
     bf16 that already hold the new rows, slots int32 [n] their cache rows.  gate
     [T][H][d] fp32 or bf16 before its sigmoid, or None.  scale defaults to
-    d ** -0.5; max_kv is a hint.  Returns out, bf16 [T][H][d]."""
-    dev = q.device
-    _on(q, "q", dev, (torch.bfloat16,), 3)
-    T, H, d = q.shape
-    cached = cache_pos is not None
-    for t, name in ((k, "k"), (v, "v")):
-        _on(t, name, dev, (torch.bfloat16,), 4 if cached else 3)
-    _need(k.shape == v.shape and k.shape[-1] == d, "k and v must have one shape, with q's head_dim")
-    Hk = k.shape[1]
-    if cached:
-        B, rows = k.shape[0], k.shape[2]
-        kst, vst = _planes(k, "k"), _planes(v, "v")
+    d ** -0.5; max_kv is a hint; status int32 [1].  Returns out, bf16 [T][H][d]."""
+    dev = q.get_device()
+    qa = _rows(q, "q", dev, _BF16)
+    T, H, d = shape = q.shape
+    if cache_pos is not None:
+        ka = _planes(k, "k", dev, _BF16)
+        B, Hk, rows, _ = k.shape
+        va = _planes(v, "v", dev, _BF16, (B, Hk, rows, d))
     else:
-        B, rows = 1, k.shape[0]
-        kst, vst = _rows(k, "k") + (8,), _rows(v, "v") + (8,)
-    gst, gp, gdt = (8, 8), None, gattn.DTYPE_BF16
+        ka = _rows(k, "k", dev, _BF16) + (8,)
+        B, (rows, Hk, _) = 1, k.shape
+        va = _rows(v, "v", dev, _BF16, (rows, Hk, d)) + (8,)
+    if k.shape[-1] != d:
+        _refuse(k, "k", dev, _BF16, d, "must have q's head_dim")
     if gate is not None:
-        _on(gate, "gate", dev, tuple(_DTYPES), 3)
-        _need(gate.shape == q.shape, "gate must have q's shape")
-        gst, gp, gdt = _rows(gate, "gate"), gate.data_ptr(), _DTYPES[gate.dtype]
+        ga, gdt = _rows(gate, "gate", dev, _DTYPES, shape), _DTYPES[gate.dtype]
+    else:
+        ga, gdt = (0, 8, 8), gattn.DTYPE_BF16
     if out is None:
-        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
-    _on(out, "out", dev, (torch.bfloat16,), 3)
-    _need(out.shape == q.shape, "out must have q's shape")
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    oa = _rows(out, "out", dev, _BF16, shape)
     cu, n = _cu(cu_rows, "cu_rows", dev)
-    ckv = None
+    ckv = 0
     if cu_kv is not None:
         ckv, nk = _cu(cu_kv, "cu_kv", dev)
-        _need(nk == n, "cu_kv and cu_rows must have one length")
+        if nk != n:
+            _refuse(cu_kv, "cu_kv", dev, _I32, n + 1, "must have cu_rows's length")
     if rows == 0:
-        # no keys at all: every row of a sequence is empty
-        _need(not cached, "a cache must hold at least one row")
-        k = v = q
-        kst = vst = (8, 8, 8)
-        rows = 1
-    desc = gattn.gattn_prompt_attention_desc(
+        # no keys at all (every row is empty): q stands in for their address
+        ka = va = (qa[0], 8, 8, 8)
+        B, rows = 1, 1
+    desc = gattn.gattn_prompt_attention_desc.pack(
         H, Hk, d, d ** -0.5 if scale is None else scale, n, T, cu, ckv,
-        _index(cache_pos, "cache_pos", dev, n), _index(slots, "slots", dev, n), q.data_ptr(),
-        *_rows(q, "q"), k.data_ptr(), v.data_ptr(), B, rows, *kst, *vst, gp, gdt, max_kv, *gst,
-        out.data_ptr(), *_rows(out, "out"), _status(status, dev))
+        _flat(cache_pos, "cache_pos", dev, _I32, n), _flat(slots, "slots", dev, _I32, n), qa[0],
+        qa[1], qa[2], ka[0], va[0], B, rows, ka[1], ka[2], ka[3], va[1], va[2], va[3], ga[0], gdt,
+        max_kv, ga[1], ga[2], oa[0], oa[1], oa[2], _flat(status, "status", dev, _I32, 1))
     if n and T:
         _call(gattn.prompt_attention, desc, dev, stream)
     return out
@@ -362,45 +363,52 @@ def prompt_attention(q, k, v, cu_rows, *, cu_kv=None, cache_pos=None, slots=None
 
 def _delta(fn, q, k, v, g, beta, cu_rows, num_seqs, state, state_out, slots, scale, qk_l2norm,
            l2_eps, out, status, stream):
-    dev = q.device
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _on(t, name, dev, (torch.bfloat16,), 3)
-    T, Hk, dk = q.shape
+    dev = q.get_device()
+    qa = _rows(q, "q", dev, _BF16)
+    T, Hk, dk = shape = q.shape
+    ka = _rows(k, "k", dev, _BF16, shape)
+    va = _rows(v, "v", dev, _BF16)
     Hv, dv = v.shape[1:]
-    _need(k.shape == q.shape and v.shape[0] == T, "k must have q's shape, v as many rows")
+    if v.shape[0] != T:
+        _refuse(v, "v", dev, _BF16, T, "must have q's rows:")
+    gst = []
     for t, name in ((g, "g"), (beta, "beta")):
-        _on(t, name, dev, (torch.float32,), 2)
-        _need(t.shape == (T, Hv) and (Hv <= 1 or t.stride(1) == 1),
-              f"{name} must be [T][Hv] with contiguous heads")
+        if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.float32 or
+                t.shape != (T, Hv) or (Hv > 1 and t.stride(1) != 1)):
+            _refuse(t, name, dev, _F32, (T, Hv))
+        gst.append(t.stride(0) if T > 1 else Hv)
     if cu_rows is not None:
         cu, n = _cu(cu_rows, "cu_rows", dev)
-        _need(num_seqs is None or num_seqs == n, "num_seqs and cu_rows disagree")
+        if num_seqs is not None and num_seqs != n:
+            raise ValueError("num_seqs and cu_rows disagree")
+    elif num_seqs is None:
+        raise ValueError("num_seqs is needed without cu_rows")
     else:
-        _need(num_seqs is not None, "num_seqs is needed without cu_rows")
-        cu, n = None, num_seqs
-    nslots, stride = 0, 0
+        cu, n = 0, num_seqs
+    nslots = stride = sp = so = 0
     for t, name in ((state, "state"), (state_out, "state_out")):
         if t is None:
             continue
-        _on(t, name, dev, (torch.float32,), 4)
-        _need(t.shape[1:] == (Hv, dk, dv) and t.shape[0] >= 1 and t[0].is_contiguous(),
-              f"{name} must be [slots][Hv][dk][dv] with contiguous slots")
-        st = t.stride(0) if t.shape[0] > 1 else Hv * dk * dv
-        _need(nslots in (0, t.shape[0]) and stride in (0, st),
-              "state and state_out must have one shape and stride")
+        if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.float32 or
+                t.dim() != 4 or t.shape[1:] != (Hv, dk, dv) or not t.shape[0] or
+                not (t.is_contiguous() or t[0].is_contiguous())):
+            _refuse(t, name, dev, _F32, (nslots or "slots", Hv, dk, dv))
+        st = t.stride(0) if t.shape[0] > 1 else max(stride, Hv * dk * dv)
+        if nslots and (nslots != t.shape[0] or stride != st):
+            raise ValueError("state and state_out must have one shape and stride")
         nslots, stride = t.shape[0], st
+        if name == "state":
+            sp = t.data_ptr()
+        else:
+            so = t.data_ptr()
     if out is None:
-        out = torch.empty((T, Hv, dv), dtype=torch.bfloat16, device=dev)
-    _on(out, "out", dev, (torch.bfloat16,), 3)
-    _need(out.shape == v.shape, "out must have v's shape")
-    desc = gattn.gattn_delta_desc(
-        Hk, Hv, dk, dv, dk ** -0.5 if scale is None else scale, int(bool(qk_l2norm)), l2_eps, n, T,
-        nslots, cu, _index(slots, "slots", dev, n), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-        *_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"), g.data_ptr(), beta.data_ptr(),
-        g.stride(0) if T > 1 else Hv, beta.stride(0) if T > 1 else Hv,
-        state.data_ptr() if state is not None else None,
-        state_out.data_ptr() if state_out is not None else None, stride, out.data_ptr(),
-        *_rows(out, "out"), _status(status, dev))
+        out = torch.empty((T, Hv, dv), dtype=torch.bfloat16, device=q.device)
+    oa = _rows(out, "out", dev, _BF16, (T, Hv, dv))
+    desc = gattn.gattn_delta_desc.pack(
+        Hk, Hv, dk, dv, dk ** -0.5 if scale is None else scale, 1 if qk_l2norm else 0, l2_eps, n, T,
+        nslots, cu, _flat(slots, "slots", dev, _I32, n), qa[0], ka[0], va[0], qa[1], qa[2], ka[1],
+        ka[2], va[1], va[2], g.data_ptr(), beta.data_ptr(), gst[0], gst[1], sp, so, stride, oa[0],
+        oa[1], oa[2], _flat(status, "status", dev, _I32, 1))
     if n:
         _call(fn, desc, dev, stream)
     return out

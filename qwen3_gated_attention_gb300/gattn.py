@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -98,7 +99,9 @@ class gattn_taps(C.Structure):
 
 
 def _fields(text):
-    """ctypes fields of a descriptor: "type: name name" per line (i32, i64, f32, ptr)."""
+    """ctypes fields of a descriptor: "type: name name" per line (i32, i64, f32, ptr).
+    A descriptor may also be packed in one go, which takes a fraction of the time of
+    filling the structure: DESC.pack(*values) with 0 for a null pointer."""
     kinds = {"i32": C.c_int32, "i64": C.c_int64, "f32": C.c_float, "ptr": C.c_void_p}
     out = []
     for line in text.strip().splitlines():
@@ -107,6 +110,15 @@ def _fields(text):
     return out
 
 
+def _packer(cls):
+    codes = {C.c_int32: "i", C.c_int64: "q", C.c_float: "f", C.c_void_p: "P"}
+    st = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0q")
+    assert st.size == C.sizeof(cls)
+    cls.pack = staticmethod(st.pack)
+    return cls
+
+
+@_packer
 class gattn_prompt_rows_desc(C.Structure):
     _fields_ = _fields("""
         i32: num_heads num_kv_heads head_dim
@@ -123,6 +135,7 @@ class gattn_prompt_rows_desc(C.Structure):
         ptr: status""")
 
 
+@_packer
 class gattn_prompt_attention_desc(C.Structure):
     _fields_ = _fields("""
         i32: num_heads num_kv_heads head_dim
@@ -142,6 +155,7 @@ class gattn_prompt_attention_desc(C.Structure):
         ptr: status""")
 
 
+@_packer
 class gattn_delta_desc(C.Structure):
     _fields_ = _fields("""
         i32: num_k_heads num_v_heads k_dim v_dim
@@ -205,10 +219,10 @@ def lib():
         L.gattn_kv_register_turbo4.argtypes = [p, C.POINTER(gattn_kv_turbo4_desc), C.POINTER(p)]
         L.gattn_layer_set_test_wait.argtypes = [p, i64, i32]
         L.gattn_layer_step_host.argtypes = [p, p, p, p, i32, i32, p, p]
-        L.gattn_prompt_rows.argtypes = [C.POINTER(gattn_prompt_rows_desc), p]
-        L.gattn_prompt_attention.argtypes = [C.POINTER(gattn_prompt_attention_desc), p]
-        L.gattn_delta_prompt.argtypes = [C.POINTER(gattn_delta_desc), p]
-        L.gattn_delta_step.argtypes = [C.POINTER(gattn_delta_desc), p]
+        L.gattn_prompt_rows.argtypes = [p, p]
+        L.gattn_prompt_attention.argtypes = [p, p]
+        L.gattn_delta_prompt.argtypes = [p, p]
+        L.gattn_delta_step.argtypes = [p, p]
         for name in ("gattn_cfg_validate", "gattn_layer_create", "gattn_layer_set_weights",
                      "gattn_kv_register", "gattn_layer_step", "gattn_layer_poll_status",
                      "gattn_layer_set_taps", "gattn_pack_affine_host", "gattn_unpack_codes_device",
@@ -404,25 +418,33 @@ def layer_set_test_wait(layer: int, wait_limit_ns: int = 0, withhold_stage: bool
 
 
 # -------------------------------------------------------- packed sequences
+#
+# Each takes its descriptor as the structure or as the bytes of DESC.pack().
 
-def prompt_rows(desc: gattn_prompt_rows_desc, stream: int = 0) -> None:
-    """QK RMSNorm, partial RoPE and KV append of packed prompt rows."""
-    _check(lib().gattn_prompt_rows(C.byref(desc), stream))
-
-
-def prompt_attention(desc: gattn_prompt_attention_desc, stream: int = 0) -> None:
-    """Causal gated attention of packed prompt rows."""
-    _check(lib().gattn_prompt_attention(C.byref(desc), stream))
+def _desc(d):
+    return d if type(d) is bytes else C.byref(d)
 
 
-def delta_prompt(desc: gattn_delta_desc, stream: int = 0) -> None:
-    """The gated delta rule over packed prompts (chunked)."""
-    _check(lib().gattn_delta_prompt(C.byref(desc), stream))
+def prompt_rows(desc, stream: int = 0) -> None:
+    """QK RMSNorm, partial RoPE and KV append of packed prompt rows
+    (gattn_prompt_rows_desc)."""
+    _check(lib().gattn_prompt_rows(_desc(desc), stream))
 
 
-def delta_step(desc: gattn_delta_desc, stream: int = 0) -> None:
-    """The gated delta rule for a few new rows of many sequences (row by row)."""
-    _check(lib().gattn_delta_step(C.byref(desc), stream))
+def prompt_attention(desc, stream: int = 0) -> None:
+    """Causal gated attention of packed prompt rows (gattn_prompt_attention_desc)."""
+    _check(lib().gattn_prompt_attention(_desc(desc), stream))
+
+
+def delta_prompt(desc, stream: int = 0) -> None:
+    """The gated delta rule over packed prompts, in chunks (gattn_delta_desc)."""
+    _check(lib().gattn_delta_prompt(_desc(desc), stream))
+
+
+def delta_step(desc, stream: int = 0) -> None:
+    """The gated delta rule for a few new rows of many sequences, row by row
+    (gattn_delta_desc)."""
+    _check(lib().gattn_delta_step(_desc(desc), stream))
 
 
 # ------------------------------------------------------------ host helpers
