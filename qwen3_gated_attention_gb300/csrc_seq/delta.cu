@@ -107,6 +107,4 @@ cudaError_t launch_rows(const DeltaArgs &a, cudaStream_t s)
 
 cudaError_t launch_delta_step(const DeltaArgs &a, cudaStream_t s) { return launch_rows(a, s); }
 
-cudaError_t launch_delta_prompt(const DeltaArgs &a, cudaStream_t s) { return launch_rows(a, s); }
-
 }  // namespace gattn

@@ -1,0 +1,656 @@
+// delta_chunk.cu -- the gated delta rule over prompts, 32 rows at a time.
+//
+// With G_i the running sum of the log decays inside a chunk, a_i = e^{G_i}, and S
+// the state before it, the rows of a chunk are
+//   W = T diag(beta) (V - diag(a) K S),  T = (I + L)^-1,
+//   L_ij = beta_i e^{G_i - G_j} k_i.k_j  (j < i),
+//   O = diag(a) Q S + A W,  A_ij = e^{G_i - G_j} q_i.k_j  (j <= i),
+//   S <- e^{G_C} S + K^T diag(e^{G_C - G_j}) W.
+// T and A depend on the rows alone, so helper warps prepare them (and the
+// tiles) up to four chunks ahead; what is serial is the chain over S.  The columns
+// of S are independent: a chain warp owns 16 of them and keeps S^T [16][k_dim] in
+// fp32 accumulator registers.  Every product takes its left operand from
+// registers that the product before it left there (S^T K^T, Y^T T^T, W^T K), so
+// the chain needs no shared memory of its own and no barrier between warps.
+//
+// Precision: the tensor cores multiply 16-bit floats.  K and Q rows are bf16 and
+// become fp16 exactly up to a power of two per row; S, Y, W, T and A are split
+// into two fp16 parts each (22 bits; 11 + 11), two products where the other
+// operand is exact, three where both are split, so the chain keeps fp32-like
+// accuracy.  fp16's range is covered by a power of two per state column that
+// follows the column's size.
+#include "seq.cuh"
+#include "tc5.cuh"
+
+namespace gattn {
+
+namespace {
+
+constexpr int kC = 32;             // rows of a chunk
+constexpr int kStages = 4;         // one per helper warp
+constexpr int kTS = 40;            // row stride of T and A (halves): conflict-free ldmatrix
+constexpr int kLS = 36;            // row stride of L (floats)
+constexpr float kMinG = -200.f;    // e^-200 is 0 in fp32, sums of 32 stay exact enough
+
+template <int DK, int NCW>
+struct Stage {
+    __half k[kC][DK + 8], q[kC][DK + 8];           // first bf16, then fp16 in place
+    __nv_bfloat16 v[kC][16 * NCW + 8];
+    __half t_hi[kC][kTS], t_lo[kC][kTS];           // T^T: [j][i]
+    __half a_hi[kC][kTS], a_lo[kC][kTS];           // A^T: [j][i]
+    float ar[kC], beta[kC], cr[kC], a[kC], sq[kC]; // per row, see the chain
+    float gamma;
+    int lo, hi, more;                              // rows of the chunk this is for; more of it follow
+    // the helper's own
+    float lt[kC][kLS];                             // L^T: [j][i]
+    float gh[kC], gl[kC], r[kC], kk[kC], qq[kC];
+};
+
+template <int DK, int NCW>
+struct Shared {
+    Stage<DK, NCW> st[kStages];
+    uint64_t full[kStages], empty[kStages];
+    int abort;
+};
+
+__device__ __forceinline__ void cp16_zfill(void *dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// (x0, x1) as hi + lo fp16 pairs
+__device__ __forceinline__ void split_h2(float x0, float x1, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const float2 f = __half22float2(h);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = pack_h2(x0 - f.x, x1 - f.y);
+}
+
+// A fragments (hi, lo) of one k16 step from two neighbouring accumulator tiles
+__device__ __forceinline__ void split_frag(const float (&c0)[4], const float (&c1)[4], uint32_t (&hi)[4],
+                                           uint32_t (&lo)[4])
+{
+    split_h2(c0[0], c0[1], hi[0], lo[0]);
+    split_h2(c0[2], c0[3], hi[1], lo[1]);
+    split_h2(c1[0], c1[1], hi[2], lo[2]);
+    split_h2(c1[2], c1[3], hi[3], lo[3]);
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    mma_f16(d, a, b0, b1, d);
+}
+
+// Largest magnitude (bf16 bits) of a row of 16-byte units.
+template <int U>
+__device__ __forceinline__ unsigned row_top(const void *row)
+{
+    const uint4 *p = static_cast<const uint4 *>(row);
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const uint4 u = p[i];
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                                     __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
+    }
+    return max(top & 0xFFFFu, top >> 16);
+}
+
+// One row of bf16 in shared memory becomes fp16 with the row's largest element
+// brought to [1, 2): returns the power of two taken out.  A lane per row.
+template <int DK>
+__device__ __forceinline__ float row_to_half(__half *row, unsigned top)
+{
+    uint4 *p = reinterpret_cast<uint4 *>(row);
+    int e = (int)(top >> 7);
+    e = e == 255 ? 127 : min(max(e, 1), 253);     // infinities and NaN pass as they are
+    const float f = __int_as_float((254 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < DK / 8; ++i) {
+        const uint4 u = p[i];
+        p[i] = make_uint4(pack_h2(bf16_lo(u.x) * f, bf16_hi(u.x) * f), pack_h2(bf16_lo(u.y) * f, bf16_hi(u.y) * f),
+                          pack_h2(bf16_lo(u.z) * f, bf16_hi(u.z) * f), pack_h2(bf16_lo(u.w) * f, bf16_hi(u.w) * f));
+    }
+    return __int_as_float(e << 23);
+}
+
+// Everything of rows [lo, hi) of the chunk at t0 that does not depend on the
+// state, by one warp; the chunk's other rows count as absent.  A row whose key,
+// value, decay or strength is not finite has to be the first of its part: 0 * NaN
+// would carry it to the rows before it.  When there is one in between, nothing is
+// prepared and its index is returned, else hi.
+template <int DK, int NCW>
+__device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &s, int t0, int lo, int hi, int h,
+                                            int hk, int col0)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr int KU = DK / 8, VU = 2 * NCW;      // 16-byte units of a row
+    {
+        const __nv_bfloat16 *kp = a.k + hk * a.ks.head, *qp = a.q + hk * a.qs.head;
+#pragma unroll
+        for (int i = 0; i < KU; ++i) {
+            const int u = lane + 32 * i, r = u / KU, c = (u % KU) * 8;
+            const bool ok = r >= lo && r < hi;
+            const long long row = t0 + (ok ? r : lo);
+            cp16_zfill(&s.k[r][c], kp + row * a.ks.tok + c, ok);
+            cp16_zfill(&s.q[r][c], qp + row * a.qs.tok + c, ok);
+        }
+        const __nv_bfloat16 *vp = a.v + h * a.vs.head + col0;
+#pragma unroll
+        for (int i = 0; i < VU; ++i) {
+            const int u = lane + 32 * i, r = u / VU, c = (u % VU) * 8;
+            const bool ok = r >= lo && r < hi;
+            cp16_zfill(&s.v[r][c], vp + (t0 + (ok ? r : lo)) * a.vs.tok + c, ok);
+        }
+    }
+    const bool on = lane >= lo && lane < hi;
+    const float beta = on ? a.beta[(long long)(t0 + lane) * a.bt + h] : 0.f;
+    float gr = on ? a.g[(long long)(t0 + lane) * a.gt + h] : 0.f;
+    gr = gr < kMinG ? kMinG : gr;
+    // the sums in double, as a float pair: differences of far sums stay exact
+    double G = gr;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, G, o);
+        if (lane >= o)
+            G += x;
+    }
+    const double Gc = __shfl_sync(0xffffffffu, G, 31);
+    const float gh = (float)G, gl = (float)(G - (double)gh);
+    s.gh[lane] = gh;
+    s.gl[lane] = gl;
+    const float ai = expf((float)G), ci = expf((float)(Gc - G));
+    cp_async_wait_all();
+    __syncwarp();
+    const unsigned topk = row_top<KU>(&s.k[lane][0]);
+    const bool bad = lane > lo && lane < hi &&
+                     (topk >= 0x7F80u || row_top<VU>(&s.v[lane][0]) >= 0x7F80u ||
+                      !(fabsf(gr) < INFINITY) || !(fabsf(beta) < INFINITY));
+    const unsigned bads = __ballot_sync(0xffffffffu, bad);
+    if (bads)
+        return __ffs(bads) - 1;
+    const float ek = row_to_half<DK>(&s.k[lane][0], topk);
+    const float eq = row_to_half<DK>(&s.q[lane][0], row_top<KU>(&s.q[lane][0]));
+    __syncwarp();
+
+    // K K^T, K Q^T (row j, column i >= j) and the diagonal blocks of Q Q^T
+    float kk[2][4][4] = {}, kq[2][4][4] = {}, qq[2][2][4] = {};
+    const int ar = (lane & 7) + ((lane >> 3) & 1) * 8, ac = (lane >> 4) * 8;
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+        uint32_t fk[2][4], fq[2][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            ldsm_x4(fk[mt], smem_u32(&s.k[mt * 16 + ar][ks * 16 + ac]));
+            ldsm_x4(fq[mt], smem_u32(&s.q[mt * 16 + ar][ks * 16 + ac]));
+        }
+        // the A fragment of 16 rows holds the B fragments of its two 8-row halves
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 2 * mt; nt < 4; ++nt) {
+                mma(kk[mt][nt], fk[mt], fk[nt / 2][nt & 1], fk[nt / 2][(nt & 1) + 2]);
+                mma(kq[mt][nt], fk[mt], fq[nt / 2][nt & 1], fq[nt / 2][(nt & 1) + 2]);
+                if (nt / 2 == mt)
+                    mma(qq[mt][nt & 1], fq[mt], fq[mt][nt & 1], fq[mt][(nt & 1) + 2]);
+            }
+    }
+    // squared norms: the diagonals
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = mt * 16 + g + (e >> 1) * 8, j = mt * 16 + n * 8 + 2 * t + (e & 1);
+                if (i == j) {
+                    s.kk[i] = kk[mt][2 * mt + n][e];
+                    s.qq[i] = qq[mt][n][e];
+                }
+            }
+    __syncwarp();
+    // k = K 2^e / sqrt(sum + eps): in units of the stored row
+    const float r = !on ? 0.f : a.l2norm ? rsqrtf(s.kk[lane] + a.l2_eps / (ek * ek)) : ek;
+    const float rq = !on ? 0.f : a.l2norm ? rsqrtf(s.qq[lane] + a.l2_eps / (eq * eq)) : eq;
+    s.r[lane] = r;
+    s.beta[lane] = beta;
+    s.a[lane] = ai;
+    s.ar[lane] = ai * r;
+    s.cr[lane] = ci * r;
+    s.sq[lane] = a.scale * rq;
+    if (lane == 31)
+        s.gamma = ai;
+    __syncwarp();
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 2 * mt; nt < 4; ++nt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int j = mt * 16 + g + half * 8, i0 = nt * 8 + 2 * t;
+                const float rj = s.r[j], ghj = s.gh[j], glj = s.gl[j];
+                float l[2], w[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = i0 + e;
+                    const float d = i >= j ? expf((s.gh[i] - ghj) + (s.gl[i] - glj)) * rj : 0.f;
+                    l[e] = i > j ? d * s.r[i] * s.beta[i] * kk[mt][nt][half * 2 + e] : 0.f;
+                    w[e] = i >= j ? d * kq[mt][nt][half * 2 + e] : 0.f;
+                }
+                *reinterpret_cast<float2 *>(&s.lt[j][i0]) = make_float2(l[0], l[1]);
+                uint32_t wh, wl;
+                split_h2(w[0], w[1], wh, wl);
+                *reinterpret_cast<uint32_t *>(&s.a_hi[j][i0]) = wh;
+                *reinterpret_cast<uint32_t *>(&s.a_lo[j][i0]) = wl;
+            }
+    __syncwarp();
+    // column `lane` of T = (I + L)^-1 by forward substitution: once x_m is known
+    // it is taken out of every later row
+    float x[kC];
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+        x[i] = i == lane ? 1.f : 0.f;
+#pragma unroll
+    for (int m = 0; m < kC - 1; ++m) {
+        const float xm = x[m];
+#pragma unroll
+        for (int i4 = (m + 1) / 4; i4 < kC / 4; ++i4) {
+            const float4 l = *reinterpret_cast<const float4 *>(&s.lt[m][i4 * 4]);
+            const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i4 * 4 + e > m)
+                    x[i4 * 4 + e] = fmaf(-lv[e], xm, x[i4 * 4 + e]);
+        }
+    }
+#pragma unroll
+    for (int i8 = 0; i8 < kC / 8; ++i8) {
+        uint32_t xh[4], xl[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            split_h2(x[i8 * 8 + 2 * e], x[i8 * 8 + 2 * e + 1], xh[e], xl[e]);
+        *reinterpret_cast<uint4 *>(&s.t_hi[lane][i8 * 8]) = make_uint4(xh[0], xh[1], xh[2], xh[3]);
+        *reinterpret_cast<uint4 *>(&s.t_lo[lane][i8 * 8]) = make_uint4(xl[0], xl[1], xl[2], xl[3]);
+    }
+    return hi;
+}
+
+// The sequence of a rank, longest first where a warp can sort them (up to 64).
+__device__ __forceinline__ int ranked_seq(const SeqArgs &q, int rank)
+{
+    if (!q.cu || q.n > 64)
+        return rank;
+    const int lane = threadIdx.x & 31;
+    int r0, len[2], above[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        len[k] = -1;
+        if (lane + 32 * k < q.n)
+            seq_rows(q, lane + 32 * k, r0, len[k]);
+    }
+    for (int i = 0; i < q.n; ++i) {
+        const int li = __shfl_sync(0xffffffffu, i < 32 ? len[0] : len[1], i & 31);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            above[k] += li > len[k] || (li == len[k] && i < lane + 32 * k);
+    }
+    const unsigned m0 = __ballot_sync(0xffffffffu, lane < q.n && above[0] == rank);
+    const unsigned m1 = __ballot_sync(0xffffffffu, lane + 32 < q.n && above[1] == rank);
+    return m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
+}
+
+template <int NCW>
+constexpr int chunk_threads()
+{
+    return NCW == 2 ? 256 : (NCW + 4) * 32;
+}
+
+template <int DK, int NCW>
+__global__ void __launch_bounds__(chunk_threads<NCW>(), 1)
+delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
+{
+    extern __shared__ __align__(128) uint8_t raw[];
+    auto &sh = *reinterpret_cast<Shared<DK, NCW> *>(raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int parts = a.dv / (16 * NCW);
+    const int part = blockIdx.x % parts, h = (blockIdx.x / parts) % a.Hv;
+    const int s = ranked_seq(a.sq, blockIdx.x / parts / a.Hv);
+    const int hk = h / (a.Hv / a.Hk), col0 = part * 16 * NCW;
+    int r0, len;
+    seq_rows(a.sq, s, r0, len);
+    const int slot = seq_slot_warp(a.sq, s, true);
+    if (slot < 0) {
+        if (threadIdx.x == 0)
+            seq_flag(a.sq, GATTN_STATUS_RANGE);
+        __nv_bfloat16 *out = a.out + (long long)h * a.os.head + col0;
+        for (int i = threadIdx.x; i < len * 2 * NCW; i += blockDim.x)
+            *reinterpret_cast<uint4 *>(out + (r0 + i / (2 * NCW)) * a.os.tok + (i % (2 * NCW)) * 8) =
+                make_uint4(0, 0, 0, 0);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], NCW);
+        }
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    volatile int *abort = &sh.abort;
+    const int chunks = (len + kC - 1) / kC;
+    if (warp >= NCW) {
+        // helpers: with two chain warps they take the other two schedulers
+        const int w = NCW == 2 ? (warp < 4 ? warp - 2 : warp - 4) : warp - NCW;
+        if (NCW == 2 && (warp == 4 || warp == 5))
+            return;
+        Stage<DK, NCW> &st = sh.st[w];
+        int use = 0, lo = 0, hi = 0;
+        for (int c = w; c < chunks;) {
+            // a part of the chunk: all of it, but for rows that are not finite
+            const int rows = min(kC, len - c * kC);
+            if (hi <= lo) {
+                hi = rows;
+                if (use > 0 && !__all_sync(0xffffffffu, tc5_wait(&sh.empty[w], (use - 1) & 1, abort)))
+                    break;
+            }
+            const int end = prepare_rows<DK, NCW>(a, st, r0 + c * kC, lo, hi, h, hk, col0);
+            if (end < hi) {
+                __syncwarp();
+                hi = end;
+                continue;
+            }
+            if (lane == 0) {
+                st.lo = lo;
+                st.hi = hi;
+                st.more = hi < rows;
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.full[w]);
+            ++use;
+            lo = hi < rows ? hi : 0;
+            hi = 0;
+            c += lo ? 0 : kStages;
+        }
+        return;
+    }
+    // ------------------------------------------------------------------- the chain
+    // accumulator tile j holds S^T: rows (columns of S) g and g + 8, k-elements
+    // 8 j + 2 t and the next
+    float S[DK / 8][4];
+    const long long so = slot * a.state_stride + (long long)h * DK * a.dv + col0 + warp * 16 + g;
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            S[j][e] = a.state ? a.state[so + (long long)(8 * j + 2 * t + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
+    float unit[2] = {1.f, 1.f}, inv_unit[2] = {1.f, 1.f};   // S of rows g, g + 8 in these units
+    __nv_bfloat16 *out = a.out + (long long)h * a.os.head + col0 + warp * 16 + g;
+    // ldmatrix lane addresses: rows of a tile pair (plain), k rows of one step (trans)
+    const int pr = (lane & 7) + (lane >> 4) * 8, pc = ((lane >> 3) & 1) * 8;
+    const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = (lane >> 4) * 8;
+    bool ok = true;
+    unsigned phase = 0;                // per stage
+    for (int c = 0; c < chunks;) {
+        const int w = c % kStages;
+        ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
+        if (!ok)
+            break;
+        phase ^= 1u << w;
+        Stage<DK, NCW> &st = sh.st[w];
+        float v[4][4];
+#pragma unroll
+        for (int n2 = 0; n2 < 2; ++n2) {
+            uint32_t x[4];
+            // rows of the tile are packed rows, its columns ours: transposed
+            ldsm_x4_trans(x, smem_u32(&st.v[n2 * 16 + pr][warp * 16 + pc]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int nt = n2 * 2 + (e >> 1), hf = e & 1;
+                v[nt][hf * 2] = bf16_lo(x[e]);
+                v[nt][hf * 2 + 1] = bf16_hi(x[e]);
+            }
+        }
+        // keep each column's largest magnitude, values included, between 2^-1 and 2^7
+        float mx[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < DK / 8; ++j) {
+            mx[0] = fmaxf(mx[0], fmaxf(fabsf(S[j][0]), fabsf(S[j][1])));
+            mx[1] = fmaxf(mx[1], fmaxf(fabsf(S[j][2]), fabsf(S[j][3])));
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            float mv = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                mv = fmaxf(mv, fmaxf(fabsf(v[nt][2 * hf]), fabsf(v[nt][2 * hf + 1])));
+            mx[hf] = fmaxf(mx[hf], mv * inv_unit[hf]);
+            mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
+            mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
+        }
+        const bool off = (mx[0] > 0.f && (mx[0] < 0.5f || mx[0] > 128.f)) ||
+                         (mx[1] > 0.f && (mx[1] < 0.5f || mx[1] > 128.f));
+        if (__any_sync(0xffffffffu, off)) {
+            float f[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                // bring the maximum to [8, 16), in steps and within limits that keep
+                // every power of two finite
+                int e = (__float_as_int(mx[hf]) >> 23) - 130;
+                e = mx[hf] > 0.f && (mx[hf] < 0.5f || mx[hf] > 128.f) ? min(max(e, -60), 60) : 0;
+                const int ue = (__float_as_int(unit[hf]) >> 23) - 127;
+                e = min(max(e, -100 - ue), 100 - ue);
+                f[hf] = __int_as_float((127 - e) << 23);
+                unit[hf] = __int_as_float((127 + ue + e) << 23);
+                inv_unit[hf] = __int_as_float((127 - ue - e) << 23);
+            }
+#pragma unroll
+            for (int j = 0; j < DK / 8; ++j) {
+                S[j][0] *= f[0];
+                S[j][1] *= f[0];
+                S[j][2] *= f[1];
+                S[j][3] *= f[1];
+            }
+        }
+        // K S and Q S
+        float X[4][4] = {}, O[4][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+            uint32_t hi[4], lo[4], b[2][4];
+            split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
+#pragma unroll
+            for (int n2 = 0; n2 < 2; ++n2)
+                ldsm_x4(b[n2], smem_u32(&st.k[n2 * 16 + pr][ks * 16 + pc]));
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                mma(X[nt], hi, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                mma(X[nt], lo, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+#pragma unroll
+            for (int n2 = 0; n2 < 2; ++n2)
+                ldsm_x4(b[n2], smem_u32(&st.q[n2 * 16 + pr][ks * 16 + pc]));
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                mma(O[nt], hi, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+                mma(O[nt], lo, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+        }
+        // Y = beta (V - a K S), then W = T Y
+        float W[4][4] = {};
+        {
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const float2 ar = *reinterpret_cast<const float2 *>(&st.ar[nt * 8 + 2 * t]);
+                const float2 be = *reinterpret_cast<const float2 *>(&st.beta[nt * 8 + 2 * t]);
+                const float2 aa = *reinterpret_cast<const float2 *>(&st.a[nt * 8 + 2 * t]);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    X[nt][2 * hf] = be.x * (v[nt][2 * hf] * inv_unit[hf] - ar.x * X[nt][2 * hf]);
+                    X[nt][2 * hf + 1] = be.y * (v[nt][2 * hf + 1] * inv_unit[hf] - ar.y * X[nt][2 * hf + 1]);
+                    O[nt][2 * hf] *= aa.x;
+                    O[nt][2 * hf + 1] *= aa.y;
+                }
+            }
+            uint32_t hi[2][4], lo[2][4];
+            split_frag(X[0], X[1], hi[0], lo[0]);
+            split_frag(X[2], X[3], hi[1], lo[1]);
+            // T is lower triangular: rows 0-15 of the product need the first step only
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int n2 = kk; n2 < 2; ++n2) {
+                    uint32_t th[4], tl[4];
+                    ldsm_x4_trans(th, smem_u32(&st.t_hi[kk * 16 + tr][n2 * 16 + tc]));
+                    ldsm_x4_trans(tl, smem_u32(&st.t_lo[kk * 16 + tr][n2 * 16 + tc]));
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        mma(W[n2 * 2 + n], hi[kk], th[2 * n], th[2 * n + 1]);
+                        mma(W[n2 * 2 + n], lo[kk], th[2 * n], th[2 * n + 1]);
+                        mma(W[n2 * 2 + n], hi[kk], tl[2 * n], tl[2 * n + 1]);
+                    }
+                }
+        }
+        // S <- gamma S + (c r W)^T K
+        {
+            float P[4][4];
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const float2 cr = *reinterpret_cast<const float2 *>(&st.cr[nt * 8 + 2 * t]);
+                P[nt][0] = W[nt][0] * cr.x;
+                P[nt][1] = W[nt][1] * cr.y;
+                P[nt][2] = W[nt][2] * cr.x;
+                P[nt][3] = W[nt][3] * cr.y;
+            }
+            uint32_t hi[2][4], lo[2][4];
+            split_frag(P[0], P[1], hi[0], lo[0]);
+            split_frag(P[2], P[3], hi[1], lo[1]);
+            const float gamma = st.gamma;
+#pragma unroll
+            for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    S[j][e] *= gamma;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int j2 = 0; j2 < DK / 16; ++j2) {
+                    uint32_t b[4];
+                    ldsm_x4_trans(b, smem_u32(&st.k[kk * 16 + tr][j2 * 16 + tc]));
+                    mma(S[2 * j2], hi[kk], b[0], b[1]);
+                    mma(S[2 * j2 + 1], hi[kk], b[2], b[3]);
+                    mma(S[2 * j2], lo[kk], b[0], b[1]);
+                    mma(S[2 * j2 + 1], lo[kk], b[2], b[3]);
+                }
+        }
+        // O = a Q S + A W
+        {
+            uint32_t hi[2][4], lo[2][4];
+            split_frag(W[0], W[1], hi[0], lo[0]);
+            split_frag(W[2], W[3], hi[1], lo[1]);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int n2 = kk; n2 < 2; ++n2) {
+                    uint32_t ah[4], al[4];
+                    ldsm_x4_trans(ah, smem_u32(&st.a_hi[kk * 16 + tr][n2 * 16 + tc]));
+                    ldsm_x4_trans(al, smem_u32(&st.a_lo[kk * 16 + tr][n2 * 16 + tc]));
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        mma(O[n2 * 2 + n], hi[kk], ah[2 * n], ah[2 * n + 1]);
+                        mma(O[n2 * 2 + n], lo[kk], ah[2 * n], ah[2 * n + 1]);
+                        mma(O[n2 * 2 + n], hi[kk], al[2 * n], al[2 * n + 1]);
+                    }
+                }
+        }
+        const int lo = st.lo, hi = st.hi;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = nt * 8 + 2 * t + e;
+                const float f = st.sq[i];
+                if (i >= lo && i < hi) {
+                    __nv_bfloat16 *o = out + (long long)(r0 + c * kC + i) * a.os.tok;
+                    o[0] = __float2bfloat16_rn(O[nt][e] * f * unit[0]);
+                    o[8] = __float2bfloat16_rn(O[nt][2 + e] * f * unit[1]);
+                }
+            }
+        c += st.more ? 0 : 1;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.empty[w]);
+    }
+    if (!ok) {
+        if (lane == 0)
+            seq_flag(a.sq, GATTN_STATUS_TIMEOUT);
+        return;
+    }
+    if (a.state_out && (len > 0 || a.state_out != a.state))
+#pragma unroll
+        for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                a.state_out[so + (long long)(8 * j + 2 * t + (e & 1)) * a.dv + (e >> 1) * 8] =
+                    S[j][e] * unit[e >> 1];
+}
+
+template <int DK, int NCW>
+cudaError_t launch(const DeltaArgs &a, cudaStream_t s)
+{
+    auto *fn = delta_chunk_kernel<DK, NCW>;
+    constexpr int smem = sizeof(Shared<DK, NCW>);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(fn, smem, done);
+    if (e != cudaSuccess)
+        return e;
+    const long long grid = (long long)a.sq.n * a.Hv * (a.dv / (16 * NCW));
+    if (grid > 0x7fffffff)
+        return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(chunk_threads<NCW>());
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+template <int DK>
+cudaError_t launch_dk(const DeltaArgs &a, cudaStream_t s)
+{
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
+    // columns per CTA: as many as keep every SM busy, since a CTA's helpers do the
+    // same work for any number of them
+    const long long cols = (long long)a.sq.n * a.Hv * a.dv;
+    if (a.dv % 128 == 0 && cols / 64 > sms)
+        return launch<DK, 8>(a, s);
+    if (a.dv % 64 == 0 && cols / 32 > sms)
+        return launch<DK, 4>(a, s);
+    return launch<DK, 2>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_delta_prompt(const DeltaArgs &a, cudaStream_t s)
+{
+    return a.dk == 64 ? launch_dk<64>(a, s) : launch_dk<128>(a, s);
+}
+
+}  // namespace gattn

@@ -189,6 +189,35 @@ def test_foreign_rows_do_not_reach_a_sequence(name):
     assert torch.equal(s2[[0, 2]], so[[0, 2]]) and out[17:23].isnan().all()
 
 
+@pytest.mark.parametrize("name", ["prompt", "step"])
+@pytest.mark.parametrize("what", ["v", "k", "q", "g", "beta"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_before_a_spoilt_one_stay_as_they_were(name, what, bad):
+    """A row that is not finite reaches the rows after it, in the columns it
+    touches, and none before it."""
+    c = _case(1, 2, 64, 32, [70], 10)
+    base, _ = _run(name, c)
+    d = dict(c, y=c["y"].clone(), g=c["g"].clone(), beta=c["beta"].clone())
+    for row, col in ((41, 5), (45, 7)):
+        if what in ("g", "beta"):
+            d[what][row] = bad
+        else:
+            d["y"][row, {"q": 0, "k": 64, "v": 128}[what] + col] = bad
+    out, _ = _run(name, d)
+    assert torch.equal(out[:41], base[:41])
+    if what == "q":                                  # its own row's answer only
+        keep = [i for i in range(70) if i not in (41, 45)]
+        assert torch.equal(out[keep], base[keep]) and not out[[41, 45]].isfinite().any()
+    elif what == "v":
+        cols = [j for j in range(32) if j not in (5, 7)]
+        assert torch.allclose(out[:, :, cols].float(), base[:, :, cols].float(), rtol=2.0 ** -7, atol=2.0 ** -13)
+        assert torch.equal(out[:, 1], base[:, 1])    # the other head has its own values
+        assert not out[41:, 0, 5].isfinite().any() and not out[45:, 0, 7].isfinite().any()
+        assert torch.allclose(out[:45, 0, 7].float(), base[:45, 0, 7].float(), rtol=2.0 ** -7, atol=2.0 ** -13)
+    else:
+        assert not out[45:].isfinite().any()
+
+
 def test_uniform_lengths_and_graph():
     c = _case(2, 4, 128, 128, [4] * 6, 8)
     y = c["y"].cuda()
