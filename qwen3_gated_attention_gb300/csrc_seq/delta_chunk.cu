@@ -29,29 +29,53 @@ namespace {
 constexpr int kC = 32;             // rows of a chunk
 constexpr int kStages = 4;         // one per helper warp
 constexpr int kTS = 40;            // row stride of T and A (halves): conflict-free ldmatrix
-constexpr int kLS = 36;            // row stride of L (floats)
-constexpr float kMinG = -200.f;    // e^-200 is 0 in fp32, sums of 32 stay exact enough
+constexpr int kLS = 20;            // row stride of L's diagonal blocks (floats)
+constexpr float kMinG = -200.f;    // e^-200 is 0 in fp32
 
+// Every array starts on a 16-byte boundary: they are read in 16-byte vectors.
 template <int DK, int NCW>
-struct Stage {
-    __half k[kC][DK + 8], q[kC][DK + 8];           // first bf16, then fp16 in place
-    __nv_bfloat16 v[kC][16 * NCW + 8];
-    __half t_hi[kC][kTS], t_lo[kC][kTS];           // T^T: [j][i]
-    __half a_hi[kC][kTS], a_lo[kC][kTS];           // A^T: [j][i]
-    float ar[kC], beta[kC], cr[kC], a[kC], sq[kC]; // per row, see the chain
-    float gamma;
-    int lo, hi, more;                              // rows of the chunk this is for; more of it follow
+struct alignas(16) Stage {
+    alignas(16) __half k[kC][DK + 8];              // first bf16, then fp16 in place
+    alignas(16) __half q[kC][DK + 8];
+    alignas(16) __nv_bfloat16 v[kC][16 * NCW + 8];
+    alignas(16) __half t_hi[kC][kTS];              // T^T: [j][i]
+    alignas(16) __half t_lo[kC][kTS];
+    alignas(16) __half a_hi[kC][kTS];              // A^T: [j][i]
+    alignas(16) __half a_lo[kC][kTS];
+    alignas(16) float ar[kC];                      // per row, see the chain
+    alignas(16) float beta[kC];
+    alignas(16) float cr[kC];
+    alignas(16) float a[kC];
+    alignas(16) float sq[kC];
     // the helper's own
-    float lt[kC][kLS];                             // L^T: [j][i]
-    float gh[kC], gl[kC], r[kC], kk[kC], qq[kC];
+    alignas(16) float lt[kC][kLS];                 // diagonal blocks of L^T: [j][i % 16]
+    alignas(16) float gh[kC];
+    alignas(16) float gl[kC];
+    alignas(16) float r[kC];
+    alignas(16) float kk[kC];
+    alignas(16) float qq[kC];
+    float gamma, vtop;                             // decay of the chunk; largest |v|
+    int lo, hi, more;                              // rows of the chunk this is for; more of it follow
 };
 
 template <int DK, int NCW>
-struct Shared {
+struct alignas(16) Shared {
     Stage<DK, NCW> st[kStages];
+    alignas(16) __nv_bfloat16 o[NCW][kC][24];      // a chain warp's rows of the output
     uint64_t full[kStages], empty[kStages];
     int abort;
 };
+static_assert((kTS * 2) % 16 == 0 && (kLS * 4) % 16 == 0 && sizeof(Stage<128, 2>) % 16 == 0 &&
+                  sizeof(Stage<64, 8>) % 16 == 0,
+              "vectors of 16 bytes");
+
+// Stores four 8x8 fragments transposed: memory rows are the fragments' columns.
+__device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a),
+                 "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
 
 __device__ __forceinline__ void cp16_zfill(void *dst, const void *src, bool valid)
 {
@@ -114,7 +138,7 @@ __device__ __forceinline__ float row_to_half(__half *row, unsigned top)
     int e = (int)(top >> 7);
     e = e == 255 ? 127 : min(max(e, 1), 253);     // infinities and NaN pass as they are
     const float f = __int_as_float((254 - e) << 23);
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < DK / 8; ++i) {
         const uint4 u = p[i];
         p[i] = make_uint4(pack_h2(bf16_lo(u.x) * f, bf16_hi(u.x) * f), pack_h2(bf16_lo(u.y) * f, bf16_hi(u.y) * f),
@@ -136,7 +160,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     constexpr int KU = DK / 8, VU = 2 * NCW;      // 16-byte units of a row
     {
         const __nv_bfloat16 *kp = a.k + hk * a.ks.head, *qp = a.q + hk * a.qs.head;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < KU; ++i) {
             const int u = lane + 32 * i, r = u / KU, c = (u % KU) * 8;
             const bool ok = r >= lo && r < hi;
@@ -145,7 +169,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
             cp16_zfill(&s.q[r][c], qp + row * a.qs.tok + c, ok);
         }
         const __nv_bfloat16 *vp = a.v + h * a.vs.head + col0;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < VU; ++i) {
             const int u = lane + 32 * i, r = u / VU, c = (u % VU) * 8;
             const bool ok = r >= lo && r < hi;
@@ -156,8 +180,9 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     const float beta = on ? a.beta[(long long)(t0 + lane) * a.bt + h] : 0.f;
     float gr = on ? a.g[(long long)(t0 + lane) * a.gt + h] : 0.f;
     gr = gr < kMinG ? kMinG : gr;
-    // the sums in double, as a float pair: differences of far sums stay exact
-    double G = gr;
+    // the sums in double and in units of log2 e, then as a float pair: differences
+    // of far sums stay exact
+    double G = (double)gr * 1.4426950408889634;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const double x = __shfl_up_sync(0xffffffffu, G, o);
@@ -168,12 +193,13 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     const float gh = (float)G, gl = (float)(G - (double)gh);
     s.gh[lane] = gh;
     s.gl[lane] = gl;
-    const float ai = expf((float)G), ci = expf((float)(Gc - G));
+    const float ai = ex2(gh), ci = ex2((float)(Gc - G));
     cp_async_wait_all();
     __syncwarp();
     const unsigned topk = row_top<KU>(&s.k[lane][0]);
+    const unsigned topv = row_top<VU>(&s.v[lane][0]);
     const bool bad = lane > lo && lane < hi &&
-                     (topk >= 0x7F80u || row_top<VU>(&s.v[lane][0]) >= 0x7F80u ||
+                     (topk >= 0x7F80u || topv >= 0x7F80u ||
                       !(fabsf(gr) < INFINITY) || !(fabsf(beta) < INFINITY));
     const unsigned bads = __ballot_sync(0xffffffffu, bad);
     if (bads)
@@ -185,7 +211,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     // K K^T, K Q^T (row j, column i >= j) and the diagonal blocks of Q Q^T
     float kk[2][4][4] = {}, kq[2][4][4] = {}, qq[2][2][4] = {};
     const int ar = (lane & 7) + ((lane >> 3) & 1) * 8, ac = (lane >> 4) * 8;
-#pragma unroll
+#pragma unroll 2
     for (int ks = 0; ks < DK / 16; ++ks) {
         uint32_t fk[2][4], fq[2][4];
 #pragma unroll
@@ -227,59 +253,113 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     s.ar[lane] = ai * r;
     s.cr[lane] = ci * r;
     s.sq[lane] = a.scale * rq;
-    if (lane == 31)
+    const unsigned vtop = __reduce_max_sync(0xffffffffu, topv);
+    if (lane == 31) {
         s.gamma = ai;
+        s.vtop = __uint_as_float(vtop << 16);
+    }
     __syncwarp();
+    float2 ghi[4], gli[4], rb[4];
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        const int i0 = nt * 8 + 2 * t;
+        ghi[nt] = *reinterpret_cast<const float2 *>(&s.gh[i0]);
+        gli[nt] = *reinterpret_cast<const float2 *>(&s.gl[i0]);
+        const float2 ri = *reinterpret_cast<const float2 *>(&s.r[i0]);
+        const float2 bi = *reinterpret_cast<const float2 *>(&s.beta[i0]);
+        rb[nt] = make_float2(ri.x * bi.x, ri.y * bi.y);
+    }
+    uint32_t bh[2][2], bl[2][2];       // L of rows 16-31, columns 0-15, as a B operand
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int nt = 2 * mt; nt < 4; ++nt)
+        for (int half = 0; half < 2; ++half) {
+            const int j = mt * 16 + g + half * 8;
+            const float rj = s.r[j], ghj = s.gh[j], glj = s.gl[j];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int j = mt * 16 + g + half * 8, i0 = nt * 8 + 2 * t;
-                const float rj = s.r[j], ghj = s.gh[j], glj = s.gl[j];
-                float l[2], w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = i0 + e;
-                    const float d = i >= j ? expf((s.gh[i] - ghj) + (s.gl[i] - glj)) * rj : 0.f;
-                    l[e] = i > j ? d * s.r[i] * s.beta[i] * kk[mt][nt][half * 2 + e] : 0.f;
-                    w[e] = i >= j ? d * kq[mt][nt][half * 2 + e] : 0.f;
-                }
-                *reinterpret_cast<float2 *>(&s.lt[j][i0]) = make_float2(l[0], l[1]);
+            for (int nt = 2 * mt; nt < 4; ++nt) {
+                const int i0 = nt * 8 + 2 * t;
+                const float d0 = i0 >= j ? ex2((ghi[nt].x - ghj) + (gli[nt].x - glj)) * rj : 0.f;
+                const float d1 = i0 + 1 >= j ? ex2((ghi[nt].y - ghj) + (gli[nt].y - glj)) * rj : 0.f;
+                const float l0 = i0 > j ? d0 * rb[nt].x * kk[mt][nt][half * 2] : 0.f;
+                const float l1 = i0 + 1 > j ? d1 * rb[nt].y * kk[mt][nt][half * 2 + 1] : 0.f;
+                if (nt / 2 == mt)
+                    *reinterpret_cast<float2 *>(&s.lt[j][i0 - mt * 16]) = make_float2(l0, l1);
+                else
+                    split_h2(l0, l1, bh[half][nt & 1], bl[half][nt & 1]);
                 uint32_t wh, wl;
-                split_h2(w[0], w[1], wh, wl);
+                split_h2(i0 >= j ? d0 * kq[mt][nt][half * 2] : 0.f,
+                         i0 + 1 >= j ? d1 * kq[mt][nt][half * 2 + 1] : 0.f, wh, wl);
                 *reinterpret_cast<uint32_t *>(&s.a_hi[j][i0]) = wh;
                 *reinterpret_cast<uint32_t *>(&s.a_lo[j][i0]) = wl;
             }
+        }
     __syncwarp();
-    // column `lane` of T = (I + L)^-1 by forward substitution: once x_m is known
-    // it is taken out of every later row
-    float x[kC];
+    // T = (I + L)^-1.  Its two 16 x 16 diagonal blocks by forward substitution, a
+    // column per lane: once x_m is known it is taken out of every later row
+    {
+        const int base = lane & 16;
+        float x[16];
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
-        x[i] = i == lane ? 1.f : 0.f;
+        for (int i = 0; i < 16; ++i)
+            x[i] = i == (lane & 15) ? 1.f : 0.f;
 #pragma unroll
-    for (int m = 0; m < kC - 1; ++m) {
-        const float xm = x[m];
+        for (int m = 0; m < 15; ++m) {
+            const float xm = x[m];
 #pragma unroll
-        for (int i4 = (m + 1) / 4; i4 < kC / 4; ++i4) {
-            const float4 l = *reinterpret_cast<const float4 *>(&s.lt[m][i4 * 4]);
-            const float lv[4] = {l.x, l.y, l.z, l.w};
+            for (int i4 = (m + 1) / 4; i4 < 4; ++i4) {
+                const float4 l = *reinterpret_cast<const float4 *>(&s.lt[base + m][i4 * 4]);
+                const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (i4 * 4 + e > m)
+                        x[i4 * 4 + e] = fmaf(-lv[e], xm, x[i4 * 4 + e]);
+            }
+        }
+#pragma unroll
+        for (int i8 = 0; i8 < 2; ++i8) {
+            uint32_t xh[4], xl[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (i4 * 4 + e > m)
-                    x[i4 * 4 + e] = fmaf(-lv[e], xm, x[i4 * 4 + e]);
+                split_h2(x[i8 * 8 + 2 * e], x[i8 * 8 + 2 * e + 1], xh[e], xl[e]);
+            *reinterpret_cast<uint4 *>(&s.t_hi[lane][base + i8 * 8]) = make_uint4(xh[0], xh[1], xh[2], xh[3]);
+            *reinterpret_cast<uint4 *>(&s.t_lo[lane][base + i8 * 8]) = make_uint4(xl[0], xl[1], xl[2], xl[3]);
         }
     }
+    __syncwarp();
+    // the block below them: T21 = -T22 (L21 T11), associated as (T22 L21) T11
+    {
+        const int pr = (lane & 7) + (lane >> 4) * 8, pc = ((lane >> 3) & 1) * 8;
+        uint32_t fh[4], fl[4];
+        // T22 [i][n] from its transpose
+        ldsm_x4_trans(fh, smem_u32(&s.t_hi[16 + pr][16 + pc]));
+        ldsm_x4_trans(fl, smem_u32(&s.t_lo[16 + pr][16 + pc]));
+        float p[2][4] = {}, q[2][4] = {};
 #pragma unroll
-    for (int i8 = 0; i8 < kC / 8; ++i8) {
+        for (int n = 0; n < 2; ++n) {
+            mma(p[n], fh, bh[n][0], bh[n][1]);
+            mma(p[n], fl, bh[n][0], bh[n][1]);
+            mma(p[n], fh, bl[n][0], bl[n][1]);
+        }
+        split_frag(p[0], p[1], fh, fl);
+        uint32_t th[4], tl[4];
+        ldsm_x4(th, smem_u32(&s.t_hi[pr][pc]));
+        ldsm_x4(tl, smem_u32(&s.t_lo[pr][pc]));
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            mma(q[n], fh, th[2 * n], th[2 * n + 1]);
+            mma(q[n], fl, th[2 * n], th[2 * n + 1]);
+            mma(q[n], fh, tl[2 * n], tl[2 * n + 1]);
+        }
+        // q [i][j], stored as T^T [j][16 + i]
         uint32_t xh[4], xl[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            split_h2(x[i8 * 8 + 2 * e], x[i8 * 8 + 2 * e + 1], xh[e], xl[e]);
-        *reinterpret_cast<uint4 *>(&s.t_hi[lane][i8 * 8]) = make_uint4(xh[0], xh[1], xh[2], xh[3]);
-        *reinterpret_cast<uint4 *>(&s.t_lo[lane][i8 * 8]) = make_uint4(xl[0], xl[1], xl[2], xl[3]);
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                split_h2(-q[n][2 * half], -q[n][2 * half + 1], xh[2 * n + half], xl[2 * n + half]);
+        stsm_x4_trans(smem_u32(&s.t_hi[pr][16 + pc]), xh[0], xh[1], xh[2], xh[3]);
+        stsm_x4_trans(smem_u32(&s.t_lo[pr][16 + pc]), xl[0], xl[1], xl[2], xl[3]);
     }
     return hi;
 }
@@ -394,13 +474,47 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[j][e] = a.state ? a.state[so + (long long)(8 * j + 2 * t + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
-    float unit[2] = {1.f, 1.f}, inv_unit[2] = {1.f, 1.f};   // S of rows g, g + 8 in these units
-    __nv_bfloat16 *out = a.out + (long long)h * a.os.head + col0 + warp * 16 + g;
+    // rows g and g + 8 of S are held in units of a power of two each, so that the
+    // parts fit fp16: what is dropped is below 2^-24 of the unit, as in an fp32 sum
+    float unit[2] = {1.f, 1.f}, inv_unit[2] = {1.f, 1.f};
+    // the power of two that takes m into [8, 16), within limits that keep units
+    // finite; 1 for 0, infinities and NaN
+    auto refit = [&](int hf, float m) {
+        int e = m > 0.f && m < INFINITY ? min(max((__float_as_int(m) >> 23) - 130, -60), 60) : 0;
+        const int ue = (__float_as_int(unit[hf]) >> 23) - 127;
+        e = min(max(e, -100 - ue), 100 - ue);
+        unit[hf] = __int_as_float((127 + ue + e) << 23);
+        inv_unit[hf] = __int_as_float((127 - ue - e) << 23);
+        return __int_as_float((127 - e) << 23);
+    };
+    auto scale_rows = [&](float f0, float f1) {
+#pragma unroll
+        for (int j = 0; j < DK / 8; ++j) {
+            S[j][0] *= f0;
+            S[j][1] *= f0;
+            S[j][2] *= f1;
+            S[j][3] *= f1;
+        }
+    };
+    auto quad_max = [&](float m) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    };
+    float top0[2] = {0.f, 0.f};        // the initial state's columns
+#pragma unroll
+    for (int j = 0; j < DK / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            top0[e >> 1] = fmaxf(top0[e >> 1], fabsf(S[j][e]));
+    top0[0] = quad_max(top0[0]);
+    top0[1] = quad_max(top0[1]);
+    __nv_bfloat16 *out = a.out + (long long)(r0 + lane) * a.os.tok + (long long)h * a.os.head + col0 + warp * 16;
     // ldmatrix lane addresses: rows of a tile pair (plain), k rows of one step (trans)
     const int pr = (lane & 7) + (lane >> 4) * 8, pc = ((lane >> 3) & 1) * 8;
     const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = (lane >> 4) * 8;
     bool ok = true;
     unsigned phase = 0;                // per stage
+    bool first = true;
     for (int c = 0; c < chunks;) {
         const int w = c % kStages;
         ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
@@ -421,53 +535,30 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 v[nt][hf * 2 + 1] = bf16_hi(x[e]);
             }
         }
-        // keep each column's largest magnitude, values included, between 2^-1 and 2^7
-        float mx[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < DK / 8; ++j) {
-            mx[0] = fmaxf(mx[0], fmaxf(fabsf(S[j][0]), fabsf(S[j][1])));
-            mx[1] = fmaxf(mx[1], fmaxf(fabsf(S[j][2]), fabsf(S[j][3])));
-        }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            float mv = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                mv = fmaxf(mv, fmaxf(fabsf(v[nt][2 * hf]), fabsf(v[nt][2 * hf + 1])));
-            mx[hf] = fmaxf(mx[hf], mv * inv_unit[hf]);
-            mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 1));
-            mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
-        }
-        const bool off = (mx[0] > 0.f && (mx[0] < 0.5f || mx[0] > 128.f)) ||
-                         (mx[1] > 0.f && (mx[1] < 0.5f || mx[1] > 128.f));
-        if (__any_sync(0xffffffffu, off)) {
-            float f[2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                // bring the maximum to [8, 16), in steps and within limits that keep
-                // every power of two finite
-                int e = (__float_as_int(mx[hf]) >> 23) - 130;
-                e = mx[hf] > 0.f && (mx[hf] < 0.5f || mx[hf] > 128.f) ? min(max(e, -60), 60) : 0;
-                const int ue = (__float_as_int(unit[hf]) >> 23) - 127;
-                e = min(max(e, -100 - ue), 100 - ue);
-                f[hf] = __int_as_float((127 - e) << 23);
-                unit[hf] = __int_as_float((127 + ue + e) << 23);
-                inv_unit[hf] = __int_as_float((127 - ue - e) << 23);
+        const float vtop = st.vtop;
+        if (first || vtop * inv_unit[0] > 4096.f || vtop * inv_unit[1] > 4096.f) {
+            // the first rows, or values far above the state
+            const bool big0 = vtop * inv_unit[0] > 4096.f, big1 = vtop * inv_unit[1] > 4096.f;
+            const float m0 = first ? (top0[0] > 0.f ? top0[0] : vtop) : big0 ? vtop * inv_unit[0] : 0.f;
+            const float m1 = first ? (top0[1] > 0.f ? top0[1] : vtop) : big1 ? vtop * inv_unit[1] : 0.f;
+            const float f0 = refit(0, m0), f1 = refit(1, m1);
+            scale_rows(f0, f1);
+            if (first) {               // the values once more, in the state's units
+                const float n0 = vtop * inv_unit[0], n1 = vtop * inv_unit[1];
+                scale_rows(refit(0, n0 > 4096.f ? n0 : 0.f), refit(1, n1 > 4096.f ? n1 : 0.f));
             }
-#pragma unroll
-            for (int j = 0; j < DK / 8; ++j) {
-                S[j][0] *= f[0];
-                S[j][1] *= f[0];
-                S[j][2] *= f[1];
-                S[j][3] *= f[1];
-            }
+            first = false;
         }
         // K S and Q S
         float X[4][4] = {}, O[4][4] = {};
+        __half2 top[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
             uint32_t hi[4], lo[4], b[2][4];
             split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                top[e & 1] = __hmax2(top[e & 1], __habs2(*reinterpret_cast<const __half2 *>(&hi[e])));
 #pragma unroll
             for (int n2 = 0; n2 < 2; ++n2)
                 ldsm_x4(b[n2], smem_u32(&st.k[n2 * 16 + pr][ks * 16 + pc]));
@@ -523,6 +614,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 }
         }
         // S <- gamma S + (c r W)^T K
+        float ounit[2];
         {
             float P[4][4];
 #pragma unroll
@@ -533,15 +625,38 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 P[nt][2] = W[nt][2] * cr.x;
                 P[nt][3] = W[nt][3] * cr.y;
             }
+            // what S will hold: its decayed size, or what is written now
+            const float gamma = st.gamma;
+            float f[2], m[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const float2 th = __half22float2(top[hf]);
+                m[hf] = fmaxf(th.x, th.y) * gamma;
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+                    m[hf] = fmaxf(m[hf], fmaxf(fabsf(P[nt][2 * hf]), fabsf(P[nt][2 * hf + 1])));
+                m[hf] = quad_max(m[hf]);
+                f[hf] = gamma;
+            }
+            ounit[0] = unit[0];
+            ounit[1] = unit[1];
+            auto out_of = [](float x) { return x > 0.f && (x < 0.5f || x > 32.f); };
+            if (__any_sync(0xffffffffu, out_of(m[0]) || out_of(m[1]))) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float x = refit(hf, out_of(m[hf]) ? m[hf] : 0.f);
+                    f[hf] *= x;
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) {
+                        P[nt][2 * hf] *= x;
+                        P[nt][2 * hf + 1] *= x;
+                    }
+                }
+            }
             uint32_t hi[2][4], lo[2][4];
             split_frag(P[0], P[1], hi[0], lo[0]);
             split_frag(P[2], P[3], hi[1], lo[1]);
-            const float gamma = st.gamma;
-#pragma unroll
-            for (int j = 0; j < DK / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    S[j][e] *= gamma;
+            scale_rows(f[0], f[1]);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -574,19 +689,28 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                     }
                 }
         }
-        const int lo = st.lo, hi = st.hi;
+        // through shared memory: a row of 16 columns per lane
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int n2 = 0; n2 < 2; ++n2) {
+            uint32_t x[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = nt * 8 + 2 * t + e;
-                const float f = st.sq[i];
-                if (i >= lo && i < hi) {
-                    __nv_bfloat16 *o = out + (long long)(r0 + c * kC + i) * a.os.tok;
-                    o[0] = __float2bfloat16_rn(O[nt][e] * f * unit[0]);
-                    o[8] = __float2bfloat16_rn(O[nt][2 + e] * f * unit[1]);
-                }
+            for (int n = 0; n < 2; ++n) {
+                const int nt = n2 * 2 + n;
+                const float2 f = *reinterpret_cast<const float2 *>(&st.sq[nt * 8 + 2 * t]);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                    x[n * 2 + hf] = pack_bf16x2(O[nt][2 * hf] * f.x * ounit[hf], O[nt][2 * hf + 1] * f.y * ounit[hf]);
             }
+            stsm_x4_trans(smem_u32(&sh.o[warp][n2 * 16 + pr][pc]), x[0], x[1], x[2], x[3]);
+        }
+        const int lo = st.lo, hi = st.hi;
+        __syncwarp();
+        if (lane >= lo && lane < hi) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(&sh.o[warp][lane][0]);
+            uint4 *dst = reinterpret_cast<uint4 *>(out + (long long)c * kC * a.os.tok);
+            dst[0] = src[0];
+            dst[1] = src[1];
+        }
         c += st.more ? 0 : 1;
         __syncwarp();
         if (lane == 0)
