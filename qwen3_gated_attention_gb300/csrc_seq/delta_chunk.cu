@@ -120,7 +120,7 @@ __device__ __forceinline__ unsigned row_top(const void *row)
 {
     const uint4 *p = static_cast<const uint4 *>(row);
     unsigned top = 0;
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < U; ++i) {
         const uint4 u = p[i];
         top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
@@ -138,7 +138,7 @@ __device__ __forceinline__ float row_to_half(__half *row, unsigned top)
     int e = (int)(top >> 7);
     e = e == 255 ? 127 : min(max(e, 1), 253);     // infinities and NaN pass as they are
     const float f = __int_as_float((254 - e) << 23);
-#pragma unroll 4
+#pragma unroll 1
     for (int i = 0; i < DK / 8; ++i) {
         const uint4 u = p[i];
         p[i] = make_uint4(pack_h2(bf16_lo(u.x) * f, bf16_hi(u.x) * f), pack_h2(bf16_lo(u.y) * f, bf16_hi(u.y) * f),
@@ -160,20 +160,20 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     constexpr int KU = DK / 8, VU = 2 * NCW;      // 16-byte units of a row
     {
         const __nv_bfloat16 *kp = a.k + hk * a.ks.head, *qp = a.q + hk * a.qs.head;
-#pragma unroll 4
-        for (int i = 0; i < KU; ++i) {
-            const int u = lane + 32 * i, r = u / KU, c = (u % KU) * 8;
+        const int c = (lane % KU) * 8;
+#pragma unroll 1
+        for (int r = lane / KU; r < kC; r += 32 / KU) {
             const bool ok = r >= lo && r < hi;
             const long long row = t0 + (ok ? r : lo);
             cp16_zfill(&s.k[r][c], kp + row * a.ks.tok + c, ok);
             cp16_zfill(&s.q[r][c], qp + row * a.qs.tok + c, ok);
         }
         const __nv_bfloat16 *vp = a.v + h * a.vs.head + col0;
-#pragma unroll 4
-        for (int i = 0; i < VU; ++i) {
-            const int u = lane + 32 * i, r = u / VU, c = (u % VU) * 8;
+        const int cv = (lane % VU) * 8;
+#pragma unroll 1
+        for (int r = lane / VU; r < kC; r += 32 / VU) {
             const bool ok = r >= lo && r < hi;
-            cp16_zfill(&s.v[r][c], vp + (t0 + (ok ? r : lo)) * a.vs.tok + c, ok);
+            cp16_zfill(&s.v[r][cv], vp + (t0 + (ok ? r : lo)) * a.vs.tok + cv, ok);
         }
     }
     const bool on = lane >= lo && lane < hi;
@@ -211,7 +211,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     // K K^T, K Q^T (row j, column i >= j) and the diagonal blocks of Q Q^T
     float kk[2][4][4] = {}, kq[2][4][4] = {}, qq[2][2][4] = {};
     const int ar = (lane & 7) + ((lane >> 3) & 1) * 8, ac = (lane >> 4) * 8;
-#pragma unroll 2
+#pragma unroll 1
     for (int ks = 0; ks < DK / 16; ++ks) {
         uint32_t fk[2][4], fq[2][4];
 #pragma unroll
@@ -234,14 +234,10 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = mt * 16 + g + (e >> 1) * 8, j = mt * 16 + n * 8 + 2 * t + (e & 1);
-                if (i == j) {
-                    s.kk[i] = kk[mt][2 * mt + n][e];
-                    s.qq[i] = qq[mt][n][e];
-                }
+        for (int e = 0; e < 4; ++e)
+            if (g == 2 * t + (e & 1)) {
+                s.kk[mt * 16 + g + (e >> 1) * 8] = kk[mt][2 * mt + (e >> 1)][e];
+                s.qq[mt * 16 + g + (e >> 1) * 8] = qq[mt][e >> 1][e];
             }
     __syncwarp();
     // k = K 2^e / sqrt(sum + eps): in units of the stored row
