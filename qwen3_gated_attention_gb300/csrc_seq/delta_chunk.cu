@@ -27,7 +27,6 @@ namespace gattn {
 namespace {
 
 constexpr int kC = 32;             // rows of a chunk
-constexpr int kStages = 4;         // one per helper warp
 constexpr int kTS = 40;            // row stride of T and A (halves): conflict-free ldmatrix
 constexpr int kLS = 20;            // row stride of L's diagonal blocks (floats)
 constexpr float kMinG = -200.f;    // e^-200 is 0 in fp32
@@ -58,11 +57,33 @@ struct alignas(16) Stage {
     int lo, hi, more;                              // rows of the chunk this is for; more of it follow
 };
 
+// The warps of a CTA: NCW chain warps, with two of them as many output warps (the
+// serial chain then carries K S and the state's update only), and helper warps
+// with a stage each.
+template <int NCW>
+struct Roles {
+    static constexpr bool SPLIT = NCW == 2;
+    static constexpr int OUT = SPLIT ? NCW : 0;
+    static constexpr int HELP = SPLIT ? 6 : 4;
+    static constexpr int THREADS = (NCW + OUT + HELP) * 32;
+};
+
+// What a chain warp hands its output warp: S in parts, as operands, and W.
+template <int DK>
+struct alignas(16) Handed {
+    uint4 s[DK / 16][2][32];
+    float4 w[4][32];
+    float2 unit[32];
+};
+
 template <int DK, int NCW>
 struct alignas(16) Shared {
-    Stage<DK, NCW> st[kStages];
+    using R = Roles<NCW>;
+    Stage<DK, NCW> st[R::HELP];
     alignas(16) __nv_bfloat16 o[NCW][kC][24];      // a chain warp's rows of the output
-    uint64_t full[kStages], empty[kStages];
+    Handed<DK> to[R::SPLIT ? NCW : 1];
+    uint64_t full[R::HELP], empty[R::HELP];
+    uint64_t s_full[2], w_full[2], taken[2];
     int abort;
 };
 static_assert((kTS * 2) % 16 == 0 && (kLS * 4) % 16 == 0 && sizeof(Stage<128, 2>) % 16 == 0 &&
@@ -384,16 +405,11 @@ __device__ __forceinline__ int ranked_seq(const SeqArgs &q, int rank)
     return m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
 }
 
-template <int NCW>
-constexpr int chunk_threads()
-{
-    return NCW == 2 ? 256 : (NCW + 4) * 32;
-}
-
 template <int DK, int NCW>
-__global__ void __launch_bounds__(chunk_threads<NCW>(), 1)
+__global__ void __launch_bounds__(Roles<NCW>::THREADS, 1)
 delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
 {
+    using R = Roles<NCW>;
     extern __shared__ __align__(128) uint8_t raw[];
     auto &sh = *reinterpret_cast<Shared<DK, NCW> *>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -414,9 +430,14 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < R::HELP; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], NCW);
+            mbar_init(&sh.empty[i], NCW + R::OUT);
+        }
+        for (int i = 0; i < R::OUT; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.w_full[i], 1);
+            mbar_init(&sh.taken[i], 1);
         }
         sh.abort = 0;
         fence_mbar_init();
@@ -424,11 +445,8 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     __syncthreads();
     volatile int *abort = &sh.abort;
     const int chunks = (len + kC - 1) / kC;
-    if (warp >= NCW) {
-        // helpers: with two chain warps they take the other two schedulers
-        const int w = NCW == 2 ? (warp < 4 ? warp - 2 : warp - 4) : warp - NCW;
-        if (NCW == 2 && (warp == 4 || warp == 5))
-            return;
+    if (warp >= NCW + R::OUT) {
+        const int w = warp - NCW - R::OUT;
         Stage<DK, NCW> &st = sh.st[w];
         int use = 0, lo = 0, hi = 0;
         for (int c = w; c < chunks;) {
@@ -456,7 +474,124 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             ++use;
             lo = hi < rows ? hi : 0;
             hi = 0;
-            c += lo ? 0 : kStages;
+            c += lo ? 0 : R::HELP;
+        }
+        return;
+    }
+    // ldmatrix lane addresses: rows of a tile pair (plain), k rows of one step (trans)
+    const int pr = (lane & 7) + (lane >> 4) * 8, pc = ((lane >> 3) & 1) * 8;
+    const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = (lane >> 4) * 8;
+    const int cw = warp % NCW;             // whose 16 columns
+    __nv_bfloat16 *out = a.out + (long long)(r0 + lane) * a.os.tok + (long long)h * a.os.head + col0 + cw * 16;
+    // one k16 step of (16 columns of S) x (32 rows of K or Q)
+    auto times_rows = [&](float (&D)[4][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                          const __half (*rows)[DK + 8], int ks) {
+        uint32_t b[2][4];
+#pragma unroll
+        for (int n2 = 0; n2 < 2; ++n2)
+            ldsm_x4(b[n2], smem_u32(&rows[n2 * 16 + pr][ks * 16 + pc]));
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            mma(D[nt], hi, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            mma(D[nt], lo, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+    };
+    // D += X M^T for a lower triangular M [i][j], held transposed in two parts: its
+    // rows 0-15 need the first k16 step only
+    auto times_lower = [&](float (&D)[4][4], const float (&X)[4][4], const __half (*mh)[kTS],
+                           const __half (*ml)[kTS]) {
+        uint32_t hi[2][4], lo[2][4];
+        split_frag(X[0], X[1], hi[0], lo[0]);
+        split_frag(X[2], X[3], hi[1], lo[1]);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int n2 = kk; n2 < 2; ++n2) {
+                uint32_t th[4], tl[4];
+                ldsm_x4_trans(th, smem_u32(&mh[kk * 16 + tr][n2 * 16 + tc]));
+                ldsm_x4_trans(tl, smem_u32(&ml[kk * 16 + tr][n2 * 16 + tc]));
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    mma(D[n2 * 2 + n], hi[kk], th[2 * n], th[2 * n + 1]);
+                    mma(D[n2 * 2 + n], lo[kk], th[2 * n], th[2 * n + 1]);
+                    mma(D[n2 * 2 + n], hi[kk], tl[2 * n], tl[2 * n + 1]);
+                }
+            }
+    };
+    // O = scale (a Q S + A W), O holding Q S, and its rows' way out through shared
+    // memory: a row of 16 columns per lane
+    auto finish_rows = [&](float (&O)[4][4], const float (&W)[4][4], const Stage<DK, NCW> &st, int c, float u0,
+                           float u1) {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            const float2 aa = *reinterpret_cast<const float2 *>(&st.a[nt * 8 + 2 * t]);
+            O[nt][0] *= aa.x;
+            O[nt][1] *= aa.y;
+            O[nt][2] *= aa.x;
+            O[nt][3] *= aa.y;
+        }
+        times_lower(O, W, st.a_hi, st.a_lo);
+#pragma unroll
+        for (int n2 = 0; n2 < 2; ++n2) {
+            uint32_t x[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int nt = n2 * 2 + n;
+                const float2 f = *reinterpret_cast<const float2 *>(&st.sq[nt * 8 + 2 * t]);
+                x[n * 2] = pack_bf16x2(O[nt][0] * f.x * u0, O[nt][1] * f.y * u0);
+                x[n * 2 + 1] = pack_bf16x2(O[nt][2] * f.x * u1, O[nt][3] * f.y * u1);
+            }
+            stsm_x4_trans(smem_u32(&sh.o[cw][n2 * 16 + pr][pc]), x[0], x[1], x[2], x[3]);
+        }
+        __syncwarp();
+        if (lane >= st.lo && lane < st.hi) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(&sh.o[cw][lane][0]);
+            uint4 *dst = reinterpret_cast<uint4 *>(out + (long long)c * kC * a.os.tok);
+            dst[0] = src[0];
+            dst[1] = src[1];
+        }
+    };
+    bool ok = true;
+    unsigned phase = 0;                    // per stage
+    if (R::SPLIT && warp >= NCW) {
+        // ------------------------------------------------ output warps
+        Handed<DK> &from = sh.to[R::SPLIT ? cw : 0];
+        for (int c = 0, turn = 0; c < chunks; turn ^= 1) {
+            const int w = c % R::HELP;
+            ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort) &&
+                                             tc5_wait(&sh.s_full[cw & 1], turn, abort));
+            if (!ok)
+                break;
+            phase ^= 1u << w;
+            Stage<DK, NCW> &st = sh.st[w];
+            float O[4][4] = {}, W[4][4];
+#pragma unroll 2
+            for (int ks = 0; ks < DK / 16; ++ks) {
+                const uint4 uh = from.s[ks][0][lane], ul = from.s[ks][1][lane];
+                const uint32_t hi[4] = {uh.x, uh.y, uh.z, uh.w}, lo[4] = {ul.x, ul.y, ul.z, ul.w};
+                times_rows(O, hi, lo, st.q, ks);
+            }
+            ok = __all_sync(0xffffffffu, tc5_wait(&sh.w_full[cw & 1], turn, abort));
+            if (!ok)
+                break;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const float4 x = from.w[nt][lane];
+                W[nt][0] = x.x;
+                W[nt][1] = x.y;
+                W[nt][2] = x.z;
+                W[nt][3] = x.w;
+            }
+            const float2 u = from.unit[lane];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.taken[cw & 1]);
+            finish_rows(O, W, st, c, u.x, u.y);
+            c += st.more ? 0 : 1;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.empty[w]);
         }
         return;
     }
@@ -504,15 +639,10 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             top0[e >> 1] = fmaxf(top0[e >> 1], fabsf(S[j][e]));
     top0[0] = quad_max(top0[0]);
     top0[1] = quad_max(top0[1]);
-    __nv_bfloat16 *out = a.out + (long long)(r0 + lane) * a.os.tok + (long long)h * a.os.head + col0 + warp * 16;
-    // ldmatrix lane addresses: rows of a tile pair (plain), k rows of one step (trans)
-    const int pr = (lane & 7) + (lane >> 4) * 8, pc = ((lane >> 3) & 1) * 8;
-    const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = (lane >> 4) * 8;
-    bool ok = true;
-    unsigned phase = 0;                // per stage
     bool first = true;
-    for (int c = 0; c < chunks;) {
-        const int w = c % kStages;
+    Handed<DK> &to = sh.to[R::SPLIT ? cw : 0];
+    for (int c = 0, turn = 0; c < chunks; turn ^= 1) {
+        const int w = c % R::HELP;
         ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
         if (!ok)
             break;
@@ -523,7 +653,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         for (int n2 = 0; n2 < 2; ++n2) {
             uint32_t x[4];
             // rows of the tile are packed rows, its columns ours: transposed
-            ldsm_x4_trans(x, smem_u32(&st.v[n2 * 16 + pr][warp * 16 + pc]));
+            ldsm_x4_trans(x, smem_u32(&st.v[n2 * 16 + pr][cw * 16 + pc]));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int nt = n2 * 2 + (e >> 1), hf = e & 1;
@@ -543,71 +673,57 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 const float n0 = vtop * inv_unit[0], n1 = vtop * inv_unit[1];
                 scale_rows(refit(0, n0 > 4096.f ? n0 : 0.f), refit(1, n1 > 4096.f ? n1 : 0.f));
             }
-            first = false;
         }
-        // K S and Q S
+        // K S (and Q S)
         float X[4][4] = {}, O[4][4] = {};
         __half2 top[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
+        if (R::SPLIT && !first) {
+            ok = __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1], turn ^ 1, abort));
+            if (!ok)
+                break;
+        }
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
-            uint32_t hi[4], lo[4], b[2][4];
+            uint32_t hi[4], lo[4];
             split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
+            if (R::SPLIT) {
+                to.s[ks][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                to.s[ks][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 top[e & 1] = __hmax2(top[e & 1], __habs2(*reinterpret_cast<const __half2 *>(&hi[e])));
-#pragma unroll
-            for (int n2 = 0; n2 < 2; ++n2)
-                ldsm_x4(b[n2], smem_u32(&st.k[n2 * 16 + pr][ks * 16 + pc]));
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                mma(X[nt], hi, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                mma(X[nt], lo, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
-#pragma unroll
-            for (int n2 = 0; n2 < 2; ++n2)
-                ldsm_x4(b[n2], smem_u32(&st.q[n2 * 16 + pr][ks * 16 + pc]));
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                mma(O[nt], hi, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                mma(O[nt], lo, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+            times_rows(X, hi, lo, st.k, ks);
+            if (!R::SPLIT)
+                times_rows(O, hi, lo, st.q, ks);
         }
+        if (R::SPLIT) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.s_full[cw & 1]);
+        }
+        first = false;
         // Y = beta (V - a K S), then W = T Y
-        float W[4][4] = {};
-        {
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const float2 ar = *reinterpret_cast<const float2 *>(&st.ar[nt * 8 + 2 * t]);
-                const float2 be = *reinterpret_cast<const float2 *>(&st.beta[nt * 8 + 2 * t]);
-                const float2 aa = *reinterpret_cast<const float2 *>(&st.a[nt * 8 + 2 * t]);
+        for (int nt = 0; nt < 4; ++nt) {
+            const float2 ar = *reinterpret_cast<const float2 *>(&st.ar[nt * 8 + 2 * t]);
+            const float2 be = *reinterpret_cast<const float2 *>(&st.beta[nt * 8 + 2 * t]);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    X[nt][2 * hf] = be.x * (v[nt][2 * hf] * inv_unit[hf] - ar.x * X[nt][2 * hf]);
-                    X[nt][2 * hf + 1] = be.y * (v[nt][2 * hf + 1] * inv_unit[hf] - ar.y * X[nt][2 * hf + 1]);
-                    O[nt][2 * hf] *= aa.x;
-                    O[nt][2 * hf + 1] *= aa.y;
-                }
+            for (int hf = 0; hf < 2; ++hf) {
+                X[nt][2 * hf] = be.x * (v[nt][2 * hf] * inv_unit[hf] - ar.x * X[nt][2 * hf]);
+                X[nt][2 * hf + 1] = be.y * (v[nt][2 * hf + 1] * inv_unit[hf] - ar.y * X[nt][2 * hf + 1]);
             }
-            uint32_t hi[2][4], lo[2][4];
-            split_frag(X[0], X[1], hi[0], lo[0]);
-            split_frag(X[2], X[3], hi[1], lo[1]);
-            // T is lower triangular: rows 0-15 of the product need the first step only
+        }
+        float W[4][4] = {};
+        times_lower(W, X, st.t_hi, st.t_lo);
+        if (R::SPLIT) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int n2 = kk; n2 < 2; ++n2) {
-                    uint32_t th[4], tl[4];
-                    ldsm_x4_trans(th, smem_u32(&st.t_hi[kk * 16 + tr][n2 * 16 + tc]));
-                    ldsm_x4_trans(tl, smem_u32(&st.t_lo[kk * 16 + tr][n2 * 16 + tc]));
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma(W[n2 * 2 + n], hi[kk], th[2 * n], th[2 * n + 1]);
-                        mma(W[n2 * 2 + n], lo[kk], th[2 * n], th[2 * n + 1]);
-                        mma(W[n2 * 2 + n], hi[kk], tl[2 * n], tl[2 * n + 1]);
-                    }
-                }
+            for (int nt = 0; nt < 4; ++nt)
+                to.w[nt][lane] = make_float4(W[nt][0], W[nt][1], W[nt][2], W[nt][3]);
+            to.unit[lane] = make_float2(unit[0], unit[1]);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.w_full[cw & 1]);
         }
         // S <- gamma S + (c r W)^T K
         float ounit[2];
@@ -665,48 +781,8 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                     mma(S[2 * j2 + 1], lo[kk], b[2], b[3]);
                 }
         }
-        // O = a Q S + A W
-        {
-            uint32_t hi[2][4], lo[2][4];
-            split_frag(W[0], W[1], hi[0], lo[0]);
-            split_frag(W[2], W[3], hi[1], lo[1]);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int n2 = kk; n2 < 2; ++n2) {
-                    uint32_t ah[4], al[4];
-                    ldsm_x4_trans(ah, smem_u32(&st.a_hi[kk * 16 + tr][n2 * 16 + tc]));
-                    ldsm_x4_trans(al, smem_u32(&st.a_lo[kk * 16 + tr][n2 * 16 + tc]));
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma(O[n2 * 2 + n], hi[kk], ah[2 * n], ah[2 * n + 1]);
-                        mma(O[n2 * 2 + n], lo[kk], ah[2 * n], ah[2 * n + 1]);
-                        mma(O[n2 * 2 + n], hi[kk], al[2 * n], al[2 * n + 1]);
-                    }
-                }
-        }
-        // through shared memory: a row of 16 columns per lane
-#pragma unroll
-        for (int n2 = 0; n2 < 2; ++n2) {
-            uint32_t x[4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int nt = n2 * 2 + n;
-                const float2 f = *reinterpret_cast<const float2 *>(&st.sq[nt * 8 + 2 * t]);
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-                    x[n * 2 + hf] = pack_bf16x2(O[nt][2 * hf] * f.x * ounit[hf], O[nt][2 * hf + 1] * f.y * ounit[hf]);
-            }
-            stsm_x4_trans(smem_u32(&sh.o[warp][n2 * 16 + pr][pc]), x[0], x[1], x[2], x[3]);
-        }
-        const int lo = st.lo, hi = st.hi;
-        __syncwarp();
-        if (lane >= lo && lane < hi) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(&sh.o[warp][lane][0]);
-            uint4 *dst = reinterpret_cast<uint4 *>(out + (long long)c * kC * a.os.tok);
-            dst[0] = src[0];
-            dst[1] = src[1];
-        }
+        if (!R::SPLIT)
+            finish_rows(O, W, st, c, ounit[0], ounit[1]);
         c += st.more ? 0 : 1;
         __syncwarp();
         if (lane == 0)
@@ -741,7 +817,7 @@ cudaError_t launch(const DeltaArgs &a, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(chunk_threads<NCW>());
+    cfg.blockDim = dim3(Roles<NCW>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     return cudaLaunchKernelEx(&cfg, fn, a);
