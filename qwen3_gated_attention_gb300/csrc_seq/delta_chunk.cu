@@ -141,7 +141,7 @@ __device__ __forceinline__ unsigned row_top(const void *row)
 {
     const uint4 *p = static_cast<const uint4 *>(row);
     unsigned top = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int i = 0; i < U; ++i) {
         const uint4 u = p[i];
         top = __vmaxu2(top, __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
@@ -159,7 +159,7 @@ __device__ __forceinline__ float row_to_half(__half *row, unsigned top)
     int e = (int)(top >> 7);
     e = e == 255 ? 127 : min(max(e, 1), 253);     // infinities and NaN pass as they are
     const float f = __int_as_float((254 - e) << 23);
-#pragma unroll 1
+#pragma unroll 2
     for (int i = 0; i < DK / 8; ++i) {
         const uint4 u = p[i];
         p[i] = make_uint4(pack_h2(bf16_lo(u.x) * f, bf16_hi(u.x) * f), pack_h2(bf16_lo(u.y) * f, bf16_hi(u.y) * f),
@@ -182,7 +182,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     {
         const __nv_bfloat16 *kp = a.k + hk * a.ks.head, *qp = a.q + hk * a.qs.head;
         const int c = (lane % KU) * 8;
-#pragma unroll 1
+#pragma unroll 2
         for (int r = lane / KU; r < kC; r += 32 / KU) {
             const bool ok = r >= lo && r < hi;
             const long long row = t0 + (ok ? r : lo);
@@ -483,19 +483,20 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, tc = (lane >> 4) * 8;
     const int cw = warp % NCW;             // whose 16 columns
     __nv_bfloat16 *out = a.out + (long long)(r0 + lane) * a.os.tok + (long long)h * a.os.head + col0 + cw * 16;
-    // one k16 step of (16 columns of S) x (32 rows of K or Q)
-    auto times_rows = [&](float (&D)[4][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
-                          const __half (*rows)[DK + 8], int ks) {
-        uint32_t b[2][4];
+    // one k16 step of (16 columns of S) x (32 rows of K or Q), and its operand
+    auto load_rows = [&](uint32_t (&b)[2][4], const __half (*rows)[DK + 8], int ks) {
 #pragma unroll
         for (int n2 = 0; n2 < 2; ++n2)
             ldsm_x4(b[n2], smem_u32(&rows[n2 * 16 + pr][ks * 16 + pc]));
+    };
+    auto times_rows = [&](float (&D)[4][4], float (&E)[4][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                          const uint32_t (&b)[2][4]) {
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
             mma(D[nt], hi, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
-            mma(D[nt], lo, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+            mma(E[nt], lo, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
     };
     // D += X M^T for a lower triangular M [i][j], held transposed in two parts: its
     // rows 0-15 need the first k16 step only
@@ -570,7 +571,9 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             for (int ks = 0; ks < DK / 16; ++ks) {
                 const uint4 uh = from.s[ks][0][lane], ul = from.s[ks][1][lane];
                 const uint32_t hi[4] = {uh.x, uh.y, uh.z, uh.w}, lo[4] = {ul.x, ul.y, ul.z, ul.w};
-                times_rows(O, hi, lo, st.q, ks);
+                uint32_t b[2][4];
+                load_rows(b, st.q, ks);
+                times_rows(O, O, hi, lo, b);
             }
             ok = __all_sync(0xffffffffu, tc5_wait(&sh.w_full[cw & 1], turn, abort));
             if (!ok)
@@ -682,9 +685,16 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             if (!ok)
                 break;
         }
+        uint32_t bk[2][2][4], bq[2][4];
+        float X2[4][4] = {};               // the low parts' sums, apart: shorter chains
+        load_rows(bk[0], st.k, 0);
 #pragma unroll
         for (int ks = 0; ks < DK / 16; ++ks) {
             uint32_t hi[4], lo[4];
+            if (ks + 1 < DK / 16)
+                load_rows(bk[(ks + 1) & 1], st.k, ks + 1);
+            if (!R::SPLIT)
+                load_rows(bq, st.q, ks);
             split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
             if (R::SPLIT) {
                 to.s[ks][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -693,10 +703,19 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 top[e & 1] = __hmax2(top[e & 1], __habs2(*reinterpret_cast<const __half2 *>(&hi[e])));
-            times_rows(X, hi, lo, st.k, ks);
+            if (R::SPLIT)
+                times_rows(X, X2, hi, lo, bk[ks & 1]);
+            else
+                times_rows(X, X, hi, lo, bk[ks & 1]);
             if (!R::SPLIT)
-                times_rows(O, hi, lo, st.q, ks);
+                times_rows(O, O, hi, lo, bq);
         }
+        if (R::SPLIT)
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    X[nt][e] += X2[nt][e];
         if (R::SPLIT) {
             __syncwarp();
             if (lane == 0)
