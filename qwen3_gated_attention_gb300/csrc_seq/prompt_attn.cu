@@ -47,7 +47,7 @@ struct Cfg {
     struct Tables {              // behind the ring
         uint64_t full[SLOTS], empty[SLOTS];
         uint64_t part[SLOTS];    // a value slot that warps 6-7 look through has landed
-        uint64_t q_full, s_full[2], p_ready[2], pv_done;
+        uint64_t q_full, q_done, g_full, s_full[2], p_ready[2], pv_done;
         uint32_t tmem;
         int abort, fixes;
         int s, level;            // the tile: sequence and place, or s < 0
@@ -142,7 +142,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, D > 128 ? 1 : 2)
 prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                   int hp_log2)
+                   const __grid_constant__ CUtensorMap gmap, int hp_log2)
 {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -170,6 +170,8 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                 mbar_init(&T.part[i], 1);
             }
             mbar_init(&T.q_full, 1);
+            mbar_init(&T.q_done, 1);
+            mbar_init(&T.g_full, 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&T.s_full[i], 1);
                 mbar_init(&T.p_ready[i], 128);
@@ -288,9 +290,17 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                     load_v(b);
                 }
             }
-            if (*abort) {
-                // every copy has landed before the shared memory is given up
-                int none = 0;
+            // a bf16 gate tile takes the queries' place once the last scores are done
+            int none = 0;
+            if (a.gate && !a.gate_f32 && go && tc5_wait(&T.q_done, 0, abort)) {
+                mbar_arrive_expect_tx(&T.g_full, C::QB);
+                for (int c = 0; c < C::CH; ++c)
+                    tma3d(smem_u32(qs) + c * (kM * 128), &gmap, c * 64, head0, t.row0, &T.g_full);
+                tc5_wait(&T.g_full, 0, &none);
+            }
+            // every copy has landed before the shared memory is given up, also when
+            // a wait ran out
+            {
                 tc5_wait(&T.q_full, 0, &none);
                 for (int i = max(0, n - C::SLOTS); i < n; ++i) {
                     const int sl = i % C::SLOTS;
@@ -322,6 +332,8 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                 }
                 if (go)
                     tc5_commit(&T.s_full[C::NS == 2 ? b & 1 : 0]);
+                if (go && b == t.nb - 1)
+                    tc5_commit(&T.q_done);
             };
             auto values = [&](int b) {
                 const int pb = C::NS == 2 ? b & 1 : 0;
@@ -372,29 +384,42 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                 bool go = tc5_wait(&T.part[sl], phase >> sl & 1, abort);
                 phase ^= 1u << sl;
                 uint4 *p = reinterpret_cast<uint4 *>(ring + sl * kSlot);
-                for (int i = w * 32 + lane; go && i < C::VK * D / 8; i += 64) {
-                    const uint4 u = p[i];
-                    uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                constexpr int UNITS = C::VK * D / 8;
+                static_assert(UNITS % 256 == 0, "four units a thread and turn");
+                for (int i0 = w * 32 + lane; go && i0 < UNITS; i0 += 256) {
+                    uint4 u[4];
                     bool hit = false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        hit |= not_finite16(x[e]) || not_finite16(x[e] >> 16);
+                    for (int k = 0; k < 4; ++k)
+                        u[k] = p[i0 + 64 * k];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // a set exponent field is largest: one packed maximum finds it
+                        const unsigned top = __vmaxu2(__vmaxu2(u[k].x & 0x7FFF7FFFu, u[k].y & 0x7FFF7FFFu),
+                                                      __vmaxu2(u[k].z & 0x7FFF7FFFu, u[k].w & 0x7FFF7FFFu));
+                        hit |= (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u;
+                    }
                     if (!hit)
                         continue;
-                    // 16-byte unit i: chunk of 64 columns, key row, unit within the
-                    // row, swizzled by the row
-                    const int c = i / (C::VK * 8), key = (i / 8) % C::VK, un = (i & 7) ^ (key & 7);
-                    const int kidx = (b - part0) * kN + g * C::VK + key;
+#pragma unroll 1
+                    for (int i = i0; i < i0 + 256; i += 64) {
+                        const uint4 v = p[i];
+                        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        // 16-byte unit i: chunk of 64 columns, key row, unit within the
+                        // row, swizzled by the row
+                        const int c = i / (C::VK * 8), key = (i / 8) % C::VK, un = (i & 7) ^ (key & 7);
+                        const int kidx = (b - part0) * kN + g * C::VK + key;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t h = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-                        if (!not_finite16(h))
-                            continue;
-                        const int what = (h & 0x7F) ? 0 : (h >> 15) ? 2 : 1;
-                        atomic_min16(&T.fix_at[what][c * 64 + un * 8 + e], kidx);
-                        x[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t h = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                            if (!not_finite16(h))
+                                continue;
+                            const int what = (h & 0x7F) ? 0 : (h >> 15) ? 2 : 1;
+                            atomic_min16(&T.fix_at[what][c * 64 + un * 8 + e], kidx);
+                            x[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                        }
+                        p[i] = make_uint4(x[0], x[1], x[2], x[3]);
                     }
-                    p[i] = make_uint4(x[0], x[1], x[2], x[3]);
                     *(volatile int *)&T.fixes = 1;
                 }
                 fence_proxy_async_smem();
@@ -501,6 +526,9 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
         if (t.nb > 1)
             go = go && tc5_wait(&T.pv_done, (t.nb - 2) & 1, abort);
         go = go && tc5_wait(&T.pv_done, (t.nb - 1) & 1, abort);
+        const bool gate_here = a.gate && !a.gate_f32;
+        if (gate_here)
+            go = go && tc5_wait(&T.g_full, 0, abort);
         go = __all_sync(0xffffffffu, go);
         if (go) {
             tc5_fence_after();
@@ -545,7 +573,12 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                             g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w;
                             g[4] = w.x; g[5] = w.y; g[6] = w.z; g[7] = w.w;
                         } else {
-                            ld_bf16x8(static_cast<const __nv_bfloat16 *>(a.gate) + go_ + q * 32 + e * 8, g);
+                            // chunk of 64 elements, row, 16-byte unit swizzled by the row
+                            const int r = threadIdx.x;
+                            ld_bf16x8(reinterpret_cast<const __nv_bfloat16 *>(
+                                          qs + (q >> 1) * (kM * 128) + r * 128 +
+                                          ((((q & 1) * 4 + e) ^ (r & 7)) << 4)),
+                                      g);
                         }
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -622,7 +655,7 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     while (hp_log2 < 7 && (a.H / a.Hk) % (2 << hp_log2) == 0)
         ++hp_log2;
     const int hp = 1 << hp_log2, tpt = kM >> hp_log2;
-    CUtensorMap qm, km, vm;
+    CUtensorMap qm, km, vm, gm;
     const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.sq.total};
     const cuuint64_t qst[2] = {(cuuint64_t)a.qs.head * 2, (cuuint64_t)a.qs.tok * 2};
     const cuuint32_t qb[3] = {64, (cuuint32_t)hp, (cuuint32_t)tpt};
@@ -630,6 +663,10 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     const cuuint64_t kst[3] = {(cuuint64_t)a.kt * 2, (cuuint64_t)a.kh * 2, (cuuint64_t)a.kb * 2};
     const cuuint64_t vst[3] = {(cuuint64_t)a.vt * 2, (cuuint64_t)a.vh * 2, (cuuint64_t)a.vb * 2};
     const cuuint32_t kb[4] = {64, kN, 1, 1}, vb[4] = {64, C::VK, 1, 1};
+    const bool gate = a.gate && !a.gate_f32;
+    const cuuint64_t gst[2] = {(cuuint64_t)a.gs.head * 2, (cuuint64_t)a.gs.tok * 2};
+    if (!encode(&gm, 3, gate ? a.gate : a.q, qd, gate ? gst : qst, qb))
+        return cudaErrorInvalidValue;
     if (!encode(&qm, 3, a.q, qd, qst, qb) || !encode(&km, 4, a.k, kd, kst, kb) ||
         !encode(&vm, 4, a.v, kd, vst, vb))
         return cudaErrorInvalidValue;
@@ -643,7 +680,7 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, fn, a, qm, km, vm, hp_log2);
+    return cudaLaunchKernelEx(&cfg, fn, a, qm, km, vm, gm, hp_log2);
 }
 
 }  // namespace
