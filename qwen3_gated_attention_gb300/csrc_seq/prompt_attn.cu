@@ -47,7 +47,7 @@ struct Cfg {
     struct Tables {              // behind the ring
         uint64_t full[SLOTS], empty[SLOTS];
         uint64_t part[SLOTS];    // a value slot that warps 6-7 look through has landed
-        uint64_t q_full, q_done, g_full, s_full[2], p_ready[2], pv_done;
+        uint64_t q_full, q_done, g_full, o_done, s_full[2], p_ready[2], pv_done;
         uint32_t tmem;
         int abort, fixes;
         int s, level;            // the tile: sequence and place, or s < 0
@@ -171,6 +171,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             }
             mbar_init(&T.q_full, 1);
             mbar_init(&T.q_done, 1);
+            mbar_init(&T.o_done, 1);
             mbar_init(&T.g_full, 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&T.s_full[i], 1);
@@ -354,7 +355,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                                    b > 0 || g > 0 || k > 0);
                     tc5_commit(&T.empty[sl]);
                 }
-                tc5_commit(&T.pv_done);
+                tc5_commit(b == t.nb - 1 ? &T.o_done : &T.pv_done);
             };
             if (C::NS == 2) {
                 scores(0);
@@ -521,11 +522,9 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             mbar_arrive(&T.p_ready[pb]);
         }
         // ------------------------------------------------------------- epilogue
-        // both of the last two phases, in order: a parity alone does not tell phase
-        // n from n - 2
-        if (t.nb > 1)
-            go = go && tc5_wait(&T.pv_done, (t.nb - 2) & 1, abort);
-        go = go && tc5_wait(&T.pv_done, (t.nb - 1) & 1, abort);
+        // a barrier of its own: by now the last phases of pv_done may both be over,
+        // and a parity does not tell phase n from n - 2
+        go = go && tc5_wait(&T.o_done, 0, abort);
         const bool gate_here = a.gate && !a.gate_f32;
         if (gate_here)
             go = go && tc5_wait(&T.g_full, 0, abort);
