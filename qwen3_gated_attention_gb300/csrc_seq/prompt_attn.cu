@@ -1,21 +1,31 @@
 // prompt_attn.cu -- causal attention of packed prompt rows with grouped heads and
 // the sigmoid output gate, on the tensor cores.
 //
-// A CTA owns 128 query rows: 128/hp consecutive tokens of one sequence times hp
-// query heads of one KV group (hp: the power of two in the group's size), so that
-// a tile of keys serves every head it can.  It walks the keys it sees in blocks
-// of 128 with the running maximum m and sum l of the softmax (base 2):
+// A pair of CTAs (cta_group::2) owns 256 query rows, 128 each: consecutive tokens
+// of one sequence times hp query heads of one KV group (hp: the power of two in the
+// group's size), so that a tile of keys serves every head it can.  The pair walks
+// the keys it sees in blocks of 128 with the running maximum m and sum l of the
+// softmax (base 2):
 //   S = Q K^T,  p = 2^(c (s - m)),  l <- l a + sum p,  O <- O a + P V,
 // a = 2^(c (m_old - m)).  S and O stay in tensor memory; P goes back into S's
 // columns as bf16 (one rounding per probability) and is the A operand of P V.
+// Each CTA loads half of a block: 64 of its keys, and half of the value columns.
+// That halves what one SM reads from L2 and from its own shared memory per MMA
+// (with one CTA a tile, M = 128, the MMAs waited for their operands: a block took
+// 3800 cycles instead of the 2048 of its products at head_dim 256).
 // The reference m of a row only moves when its maximum has grown by more than 2^8
 // (p <= 256 keeps its relative precision in bf16 and in the fp32 sums), so O is
 // rescaled a few times per row instead of once per block.
 //
-// Warps 0-3 softmax and epilogue (a thread per row), 4 copies, 5 issues the MMAs,
-// 6-7 look through the values of blocks that some row sees only part of: a value
-// that is not finite would spoil rows that do not see it (0 * NaN), so it is
-// replaced by zero there, and the rows that do see it get it back at the end.
+// The grid is persistent, one CTA per SM; tiles are dealt longest first.  Per CTA:
+// warps 0-7 softmax and epilogue (a thread per row and half of the columns), 8
+// copies, 9 issues the MMAs (of the pair, in the even CTA), 11 finds tiles; 10 looks
+// through the values of blocks that some row sees only part of: a value that is
+// not finite would spoil rows that do not see it (0 * NaN), so it is replaced by
+// zero there, and the rows that do see it get it back at the end.
+//
+// Few rows over many keys: clusters of 2, 4 or 8 CTAs, each pair taking a share of
+// the blocks; the partial (m, l, O) are joined through distributed shared memory.
 #include <algorithm>
 
 #include <cudaTypedefs.h>
@@ -27,109 +37,192 @@ namespace gattn {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kM = 128;          // query rows of a tile
-constexpr int kN = 128;          // keys of a block
-constexpr int kSlot = 16384;     // bytes of a ring slot
-constexpr float kGrow = 8.f;     // log2 growth of a row's maximum that moves its reference
+constexpr int kSoft = 8;                    // softmax warps
+constexpr int kWarps = kSoft + 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kM = 128;                     // query rows of a CTA
+constexpr int kN = 128;                     // keys of a block
+constexpr int kSlot = 16384;                // bytes of a ring slot
+constexpr int kCols = 512;                  // TMEM columns: two score buffers and O
+constexpr int kOCol = 2 * kN;
+constexpr float kGrow = 8.f;                // log2 growth of a row's maximum that moves its reference
+
+// A tile as one CTA of the pair sees it.
+struct Tile {
+    int s;                                  // sequence, or -1: no more tiles
+    int row0, rows;                         // packed row of its first token, tokens it owns
+    int slot, kv0;                          // batch row and first key row of the sequence
+    int seen0;                              // keys its first token sees (may be <= 0)
+    int b0, nb;                             // first key block and blocks (this CTA pair's share)
+    int part0;                              // from this block on some row of the pair sees only part
+    int level;
+};
 
 template <int D>
 struct Cfg {
-    static constexpr int NS = D > 128 ? 2 : 1;               // score buffers
-    static constexpr int CH = D / 64;                        // 64-element chunks of a head
-    static constexpr int VK = D == 64 ? 128 : (D == 128 ? 64 : 32);   // keys per value slot
-    static constexpr int NV = kN / VK;                       // value slots per block
+    static constexpr int CH = D / 64;               // 64-element chunks of a head
+    static constexpr int KS = (CH + 1) / 2;         // slots of a block's 64 keys: two chunks each
+    static constexpr int CV = (D / 2 + 63) / 64;    // chunks of the CTA's value columns
+    static constexpr int VK = kN / CV;              // keys per value slot
+    static constexpr int VS = CV;                   // value slots per block
     static constexpr int QB = kM * D * 2;
-    static constexpr int SLOTS = D == 256 ? 10 : (D == 192 ? 10 : (D == 128 ? 5 : 6));
-    static constexpr int COLS = D > 128 ? 512 : 256;         // TMEM columns
-    static constexpr int O_COL = NS * kN;
-    static_assert(O_COL + D <= COLS, "TMEM");
-    struct Tables {              // behind the ring
+    static constexpr int SLOTS = D == 256 ? 9 : 10;
+    static constexpr int HC = D / 2;                // O columns per softmax thread
+    static constexpr int ST = D + 4;                // row stride of staged partial sums (floats)
+    struct alignas(16) Tables {                     // behind the ring
         uint64_t full[SLOTS], empty[SLOTS];
-        uint64_t part[SLOTS];    // a value slot that warps 6-7 look through has landed
-        uint64_t q_full, q_done, g_full, o_done, s_full[2], p_ready[2], pv_done;
+        uint64_t part[SLOTS];                       // a value slot that warp 10 looks through
+        uint64_t q_full, q_free, s_full[2], p_ready[2], pv_done, o_done, o_free, t_full[2], t_empty[2];
+        float mx[2][2][kM];                         // block parity, column half, row
+        float lsum[2][2][kM];                       // tile parity, column half, row
+        Tile tile[2];
         uint32_t tmem;
-        int abort, fixes;
-        int s, level;            // the tile: sequence and place, or s < 0
-        // per value column, first key (from the first partly seen block on) that
-        // holds NaN, +inf, -inf; 0xFFFF: none
-        uint16_t fix_at[3][D];
+        int abort;
+        int fixes[2];                               // per tile parity
+        // per value column, first key (from part0 on) that holds NaN, +inf, -inf;
+        // 0xFFFF: none
+        uint16_t fix_at[2][3][D];
     };
     static constexpr int SMEM = QB + SLOTS * kSlot + (int)sizeof(Tables);
-    // two CTAs of up to 128 elements share an SM (1 KB of each is the system's)
-    static_assert(SMEM <= (D > 128 ? 227 : 113) * 1024, "shared memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(kM * ST * 4 <= SLOTS * kSlot, "partial sums fit the ring");
+    static_assert(kOCol + D <= kCols, "TMEM");
 };
 
-// What a CTA works on.
-struct Tile {
-    int row0, rows;              // packed row of its first token, tokens it owns
-    int slot, kv0;               // batch row and first key row of the sequence
-    int seen0;                   // keys the first token sees (may be <= 0)
-    int nb;                      // key blocks
+// What the order of the tiles needs of a sequence.
+struct SeqKeys {
+    int r0, len, slot;
+    long long past, kv0;        // keys before its first row; its first key row
+    bool ok;
+    __device__ __forceinline__ int tiles(int tp) const { return (len + tp - 1) / tp; }
+    // tiles with at least x key blocks (x >= 1), the last ones
+    __device__ __forceinline__ int at_least(int x, int tp) const
+    {
+        if (len == 0)
+            return 0;
+        if (x == 0)
+            return tiles(tp);
+        const long long need = (long long)(x - 1) * kN + 1 - past;
+        if (!ok || len < need)
+            return 0;
+        const int below = need <= 0 ? 0 : (int)((need + tp - 1) / tp) - 1;
+        return tiles(tp) - min(below, tiles(tp) - 1);
+    }
+    __device__ __forceinline__ int most() const
+    {
+        return ok && len > 0 && past + len > 0 ? (int)((past + len + kN - 1) / kN) : 0;
+    }
 };
 
-// Sequence and level (tile within the sequence) of the rank-th tile, tiles in
-// order of falling level, so that the longest causal rows start first.  Warp 0.
-__device__ void find_tile(const SeqArgs &q, int tpt, long long rank, int &s_out, int &level_out)
+__device__ __forceinline__ SeqKeys seq_keys(const PromptAttnArgs &a, int s)
 {
-    const int lane = threadIdx.x & 31;
-    auto tiles = [&](int s) {
-        int r0, len;
-        seq_rows(q, s, r0, len);
-        return (len + tpt - 1) / tpt;
-    };
-    const int mine = lane < q.n ? tiles(lane) : 0;      // the first 32 stay in registers
-    int most = mine;
-    for (int s = lane + 32; s < q.n; s += 32)
-        most = max(most, tiles(s));
-    most = __reduce_max_sync(0xffffffffu, most);
-    // tiles at `level` or above
-    auto above = [&](int level) {
-        int c = max(0, mine - level);
-        for (int s = lane + 32; s < q.n; s += 32)
-            c += max(0, tiles(s) - level);
-        return (long long)__reduce_add_sync(0xffffffffu, c);
-    };
-    s_out = -1;
-    level_out = 0;
-    if (rank >= above(0))
-        return;
-    int lo = 0, hi = most - 1;                          // above(lo) > rank
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (above(mid) > rank)
-            lo = mid;
-        else
-            hi = mid - 1;
+    SeqKeys q;
+    seq_rows(a.sq, s, q.r0, q.len);
+    q.kv0 = 0;
+    q.slot = 0;
+    if (a.pos) {
+        q.slot = a.sq.slots ? a.sq.slots[s] : s;
+        q.past = a.pos[s];
+        q.ok = q.slot >= 0 && q.slot < a.kv_batch && q.past >= 0 && q.past + q.len <= a.kv_rows;
+    } else {
+        q.kv0 = a.cu_kv[s];
+        const long long kv1 = a.cu_kv[s + 1];
+        q.past = kv1 - q.kv0 - q.len;
+        q.ok = q.kv0 >= 0 && kv1 >= q.kv0 && kv1 <= a.kv_rows;
     }
-    int idx = (int)(rank - above(lo + 1));
-    for (int s0 = 0; s0 < q.n; s0 += 32) {
-        const int s = s0 + lane;
-        const bool has = s < q.n && (s0 ? tiles(s) : mine) > lo;
-        const unsigned m = __ballot_sync(0xffffffffu, has);
-        const int c = __popc(m);
-        if (idx < c) {
-            // the idx-th set bit
-            unsigned x = m;
-            for (int i = 0; i < idx; ++i)
-                x &= x - 1;
-            s_out = s0 + __ffs(x) - 1;
-            level_out = lo;
-            return;
-        }
-        idx -= c;
-    }
+    return q;
 }
 
-// 16-bit minimum in shared memory (no such atomic exists)
-__device__ void atomic_min16(uint16_t *p, uint32_t v)
+// Deals the tiles out by rank; called by one whole warp with rising ranks.
+struct Dealer {
+    SeqKeys mine;               // up to 32 sequences: the lane's own
+    int base = 0;               // more: the lane's sequences are base + lane, ...
+    long long before = 0;       // ... with this many tiles before them
+
+    // Sequence and level (tile within it) of the rank-th tile; false: none.  Up to
+    // 32 sequences in order of falling key blocks, more in their own order.
+    __device__ bool find(const PromptAttnArgs &a, int tp, long long rank, bool first, SeqKeys &q, int &s,
+                         int &level)
+    {
+        const int lane = threadIdx.x & 31, n = a.sq.n;
+        const unsigned all = 0xffffffffu;
+        if (n <= 32) {
+            if (first) {
+                mine = seq_keys(a, min(lane, n - 1));
+                if (lane >= n)
+                    mine.len = 0;
+            }
+            auto count = [&](int x) { return (long long)__reduce_add_sync(all, mine.at_least(x, tp)); };
+            if (rank >= count(0))
+                return false;
+            int lo = 0, hi = __reduce_max_sync(all, mine.most());   // count(lo) > rank
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (count(mid) > rank)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int idx = (int)(rank - count(lo + 1));
+            // tiles of exactly lo blocks, by lane
+            const int c = mine.at_least(lo, tp) - mine.at_least(lo + 1, tp);
+            int sum = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(all, sum, o);
+                if (lane >= o)
+                    sum += x;
+            }
+            const int l = __ffs(__ballot_sync(all, idx < sum)) - 1;
+            level = __shfl_sync(all, mine.tiles(tp) - mine.at_least(lo, tp) + idx - (sum - c), l);
+            s = l;
+        } else {
+            for (;;) {
+                if (base >= n)
+                    return false;
+                int r0, len = 0;
+                if (base + lane < n)
+                    seq_rows(a.sq, base + lane, r0, len);
+                const int c = (len + tp - 1) / tp;
+                int sum = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(all, sum, o);
+                    if (lane >= o)
+                        sum += x;
+                }
+                const int total = __shfl_sync(all, sum, 31);
+                if (rank - before < total) {
+                    const int idx = (int)(rank - before);
+                    const int l = __ffs(__ballot_sync(all, idx < sum)) - 1;
+                    // its longest rows first
+                    level = __shfl_sync(all, sum - 1 - idx, l);
+                    s = base + l;
+                    break;
+                }
+                before += total;
+                base += 32;
+            }
+        }
+        q = seq_keys(a, s);
+        return true;
+    }
+};
+
+// 16-bit minimum in the shared memory of a CTA of the cluster (no such atomic exists)
+__device__ void atomic_min16(uint32_t addr, uint32_t v)
 {
-    unsigned *w = reinterpret_cast<unsigned *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
-    const int sh = (reinterpret_cast<uintptr_t>(p) & 2) * 8;
-    unsigned old = *(volatile unsigned *)w;
+    const uint32_t w = addr & ~3u;
+    const int sh = (addr & 2) * 8;
+    unsigned old;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(old) : "r"(w) : "memory");
     while (((old >> sh) & 0xFFFFu) > v) {
         const unsigned next = (old & ~(0xFFFFu << sh)) | (v << sh);
-        const unsigned got = atomicCAS(w, old, next);
+        unsigned got;
+        asm volatile("atom.relaxed.cluster.shared::cluster.cas.b32 %0, [%1], %2, %3;"
+                     : "=r"(got)
+                     : "r"(w), "r"(old), "r"(next)
+                     : "memory");
         if (got == old)
             break;
         old = got;
@@ -138,430 +231,569 @@ __device__ void atomic_min16(uint16_t *p, uint32_t v)
 
 __device__ __forceinline__ bool not_finite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
+__device__ __forceinline__ float4 ld_dsmem_v4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+// Whether `ok` holds in all `threads` of named barrier `id`.
+__device__ __forceinline__ bool named_bar_and(int id, int threads, bool ok)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)ok), "r"(id), "r"(threads)
+                 : "memory");
+    return r != 0;
+}
+
+// f *= sigmoid(g), for 8 values
+__device__ __forceinline__ void gate8(float (&f)[32], int at, const float (&g)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[at + i] = __fdividef(f[at + i], 1.f + __expf(-g[i]));
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&g)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        g[2 * i] = bf16_lo(w[i]);
+        g[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[32], int at)
+{
+    return make_uint4(pack_bf16x2(f[at], f[at + 1]), pack_bf16x2(f[at + 2], f[at + 3]),
+                      pack_bf16x2(f[at + 4], f[at + 5]), pack_bf16x2(f[at + 6], f[at + 7]));
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, D > 128 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, 1)
 prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                   const __grid_constant__ CUtensorMap gmap, int hp_log2)
+                   int hp_log2, int split)
 {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *const qs = smem, *const ring = smem + C::QB;
     typename C::Tables &T = *reinterpret_cast<typename C::Tables *>(smem + C::QB + C::SLOTS * kSlot);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank(), half = rank & 1, lead = rank & ~1u;
+    const uint16_t pair = (uint16_t)(3u << lead);
+    const int share = (int)rank >> 1;                  // which part of the blocks
     const int hp = 1 << hp_log2, tpt = kM >> hp_log2;
     const int groups = a.H >> hp_log2;
-    const int hg = blockIdx.x % groups;
-    const long long rank = blockIdx.x / groups;
-    const int head0 = hg << hp_log2, kvh = head0 / (a.H / a.Hk);
+    auto at_lead = [&](uint64_t *bar) { return dsmem_addr(bar, lead); };
 
-    if (warp == 0) {
-        int s, level;
-        find_tile(a.sq, tpt, rank, s, level);
-        if (lane == 0) {
-            T.s = s;
-            T.level = level;
+    if (warp == 8 && lane == 0) {
+        for (int i = 0; i < C::SLOTS; ++i) {
+            mbar_init(&T.full[i], 2);                  // a producer or guard of each CTA
+            mbar_init(&T.empty[i], 1);
+            mbar_init(&T.part[i], 1);
         }
-    } else if (warp == 4) {
-        if (lane == 0) {
-            for (int i = 0; i < C::SLOTS; ++i) {
-                mbar_init(&T.full[i], 1);
-                mbar_init(&T.empty[i], 1);
-                mbar_init(&T.part[i], 1);
-            }
-            mbar_init(&T.q_full, 1);
-            mbar_init(&T.q_done, 1);
-            mbar_init(&T.o_done, 1);
-            mbar_init(&T.g_full, 1);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&T.s_full[i], 1);
-                mbar_init(&T.p_ready[i], 128);
-            }
-            mbar_init(&T.pv_done, 1);
-            T.abort = 0;
-            T.fixes = 0;
-            fence_mbar_init();
-            prefetch_tensormap(&qmap);
-            prefetch_tensormap(&kmap);
-            prefetch_tensormap(&vmap);
+        mbar_init(&T.q_full, 2);
+        mbar_init(&T.q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&T.s_full[i], 1);
+            mbar_init(&T.p_ready[i], 2 * kSoft);
+            mbar_init(&T.t_full[i], 1);
+            mbar_init(&T.t_empty[i], 3 + 2 * kSoft);   // 8, 9, 10 here, the softmax of both CTAs
+            T.fixes[i] = 0;
         }
-    } else if (warp >= 6) {
-        for (int i = threadIdx.x - 192; i < 3 * D; i += 64)
-            (&T.fix_at[0][0])[i] = 0xFFFF;
+        mbar_init(&T.pv_done, 1);
+        mbar_init(&T.o_done, 1);
+        mbar_init(&T.o_free, 2 * kSoft);
+        T.abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&qmap);
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+    } else if (warp == 9) {
+        tmem_alloc(&T.tmem, kCols);
+    } else if (warp == 10) {
+        for (int i = lane; i < 2 * 3 * D; i += 32)
+            (&T.fix_at[0][0][0])[i] = 0xFFFF;
     }
+    tc5_fence_before();
     __syncthreads();
-    const int s = T.s;
-    if (s < 0)
-        return;
-    Tile t;
-    int r0, len;
-    seq_rows(a.sq, s, r0, len);
-    t.row0 = r0 + T.level * tpt;
-    t.rows = min(tpt, len - T.level * tpt);
-    long long kv0 = 0, keys;
-    bool ok;
-    t.slot = 0;
-    if (a.pos) {
-        t.slot = a.sq.slots ? a.sq.slots[s] : s;
-        const long long p0 = a.pos[s];
-        keys = p0 + len;
-        ok = t.slot >= 0 && t.slot < a.kv_batch && p0 >= 0 && keys <= a.kv_rows;
-    } else {
-        kv0 = a.cu_kv[s];
-        const long long kv1 = a.cu_kv[s + 1];
-        keys = kv1 - kv0;
-        ok = kv0 >= 0 && kv1 >= kv0 && kv1 <= a.kv_rows;
-    }
-    if (!ok && threadIdx.x == 0)
-        seq_flag(a.sq, GATTN_STATUS_RANGE);
-    t.kv0 = (int)kv0;
-    // |keys - len| < 2^31: both are counts of rows
-    t.seen0 = ok ? (int)(keys - len) + T.level * tpt + 1 : -(1 << 30);
-    const int seen_last = t.seen0 + t.rows - 1;
-    t.nb = seen_last > 0 ? (seen_last + kN - 1) / kN : 0;
-
-    const int tok = threadIdx.x >> hp_log2, hd = threadIdx.x & (hp - 1);   // of warps 0-3
-    if (t.nb == 0) {
-        if (threadIdx.x < kM && tok < t.rows) {
-            uint4 *o = reinterpret_cast<uint4 *>(a.out + (long long)(t.row0 + tok) * a.os.tok +
-                                                 (long long)(head0 + hd) * a.os.head);
-            for (int i = 0; i < D / 8; ++i)
-                o[i] = make_uint4(0, 0, 0, 0);
-        }
-        return;
-    }
-    if (warp == 5)
-        tmem_alloc(&T.tmem, C::COLS);
-    __syncthreads();
+    cluster_sync();
     tc5_fence_after();
     const uint32_t tmem = T.tmem;
     volatile int *abort = &T.abort;
-    // blocks from here on some row of the tile sees only in part
-    const int part0 = t.seen0 > 0 ? t.seen0 / kN : 0;
+    // the it-th tile's description
+    auto next_tile = [&](int it, Tile &t) {
+        if (!tc5_wait(&T.t_full[it & 1], (it >> 1) & 1, abort))
+            return false;
+        t = T.tile[it & 1];
+        return t.s >= 0;
+    };
 
-    if (warp == 4) {
+    if (warp == 11) {
+        // ------------------------------------------------------------- tiles
+        const int tp = 2 * tpt;
+        const long long clusters = gridDim.x / (2 * split), c = blockIdx.x / (2 * split);
+        Dealer deal;
+        for (int it = 0;; ++it) {
+            if (it >= 2 && !__all_sync(0xffffffffu, tc5_wait(&T.t_empty[it & 1], ((it >> 1) - 1) & 1, abort)))
+                break;
+            // every other round backwards, so that nobody keeps getting the longer ones
+            const long long r = it * clusters + (it & 1 ? clusters - 1 - c : c);
+            SeqKeys q;
+            Tile t;
+            bool some = (split == 1 || it == 0) && deal.find(a, tp, r / groups, it == 0, q, t.s, t.level);
+            if (some) {
+                const int tok0 = t.level * tp;
+                const long long last = q.ok ? q.past + min(q.len, tok0 + tp) : 0;
+                const int nb = last > 0 ? (int)((last + kN - 1) / kN) : 0;
+                const int each = (nb + split - 1) / split;
+                t.b0 = min(nb, share * each);
+                t.nb = min(nb, t.b0 + each) - t.b0;
+                const long long seen = q.past + tok0 + 1;
+                t.part0 = seen > 0 ? (int)(seen / kN) : 0;
+                t.row0 = q.r0 + tok0 + (int)half * tpt;
+                t.rows = max(0, min(tpt, q.len - tok0 - (int)half * tpt));
+                t.slot = q.slot;
+                t.kv0 = (int)q.kv0;
+                t.seen0 = q.ok ? (int)(seen + half * tpt) : -(1 << 30);
+                // the group of heads, beside the level
+                t.level = (int)(r % groups);
+                if (!q.ok && lane == 0)
+                    seq_flag(a.sq, GATTN_STATUS_RANGE);
+            } else {
+                t.s = -1;
+            }
+            if (lane == 0) {
+                T.tile[it & 1] = t;
+                mbar_arrive(&T.t_full[it & 1]);
+            }
+            __syncwarp();
+            if (!some)
+                break;
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------- copies
         if (lane == 0) {
-            mbar_arrive_expect_tx(&T.q_full, C::QB);
-            for (int c = 0; c < C::CH; ++c)
-                tma3d(smem_u32(qs) + c * (kM * 128), &qmap, c * 64, head0, t.row0, &T.q_full);
-            int n = 0;                 // slots filled so far
+            int n = 0, used = 0;                // slots filled so far, tiles that had blocks
             uint32_t in_part = 0, pphase = 0;   // per slot: its last load signals part[]; part[]'s phase
             bool go = true;
-            // waits for the next slot and announces `bytes` on the barrier its load signals
-            auto fill = [&](uint32_t bytes, bool part, uint64_t *&bar) -> uint32_t {
-                const int sl = n % C::SLOTS;
-                if (n >= C::SLOTS && !tc5_wait(&T.empty[sl], ((n / C::SLOTS) - 1) & 1, abort)) {
-                    go = false;
-                    return 0;
-                }
-                bar = part ? &T.part[sl] : &T.full[sl];
-                in_part = part ? in_part | 1u << sl : in_part & ~(1u << sl);
-                pphase ^= part ? 1u << sl : 0u;
-                mbar_arrive_expect_tx(bar, bytes);
-                ++n;
-                return smem_u32(ring) + sl * kSlot;
-            };
-            uint64_t *bar = nullptr;
-            auto load_k = [&](int b) {
-                for (int c = 0; c < C::CH && go; ++c) {
-                    const uint32_t p = fill(kN * 128, false, bar);
-                    if (go)
-                        tma4d(p, &kmap, c * 64, t.kv0 + b * kN, kvh, t.slot, bar);
-                }
-            };
-            auto load_v = [&](int b) {
-                for (int g = 0; g < C::NV && go; ++g) {
-                    const uint32_t p = fill(C::VK * D * 2, b >= part0, bar);
-                    if (go)
-                        for (int c = 0; c < C::CH; ++c)
-                            tma4d(p + c * (C::VK * 128), &vmap, c * 64, t.kv0 + b * kN + g * C::VK, kvh,
-                                  t.slot, bar);
-                }
-            };
-            if (C::NS == 2) {
-                load_k(0);
-                for (int b = 1; b < t.nb && go; ++b) {
-                    load_k(b);
-                    load_v(b - 1);
-                }
-                load_v(t.nb - 1);
-            } else {
-                for (int b = 0; b < t.nb && go; ++b) {
-                    load_k(b);
-                    load_v(b);
-                }
-            }
-            // a bf16 gate tile takes the queries' place once the last scores are done
+            Tile t;
             int none = 0;
-            if (a.gate && !a.gate_f32 && go && tc5_wait(&T.q_done, 0, abort)) {
-                mbar_arrive_expect_tx(&T.g_full, C::QB);
-                for (int c = 0; c < C::CH; ++c)
-                    tma3d(smem_u32(qs) + c * (kM * 128), &gmap, c * 64, head0, t.row0, &T.g_full);
-                tc5_wait(&T.g_full, 0, &none);
-            }
-            // every copy has landed before the shared memory is given up, also when
-            // a wait ran out
-            {
-                tc5_wait(&T.q_full, 0, &none);
-                for (int i = max(0, n - C::SLOTS); i < n; ++i) {
-                    const int sl = i % C::SLOTS;
-                    if (in_part >> sl & 1)
-                        tc5_wait(&T.part[sl], (pphase >> sl & 1) ^ 1, &none);
-                    else
-                        tc5_wait(&T.full[sl], (i / C::SLOTS) & 1, &none);
-                }
-            }
-        }
-    } else if (warp == 5) {
-        if (lane == 0) {
-            constexpr uint32_t id_s = tc5_idesc(kM, kN, false), id_o = tc5_idesc(kM, D, true);
-            int n = 0;                 // slots consumed so far
-            bool go = tc5_wait(&T.q_full, 0, abort);
-            auto scores = [&](int b) {
-                const uint32_t d = tmem + (C::NS == 2 ? (b & 1) * kN : 0);
-                for (int c = 0; c < C::CH && go; ++c, ++n) {
-                    const int sl = n % C::SLOTS;
-                    go = tc5_wait(&T.full[sl], (n / C::SLOTS) & 1, abort);
-                    if (!go)
-                        break;
-                    const uint64_t da = tc5_desc(smem_u32(qs) + c * (kM * 128), 16, 1024);
-                    const uint64_t db = tc5_desc(smem_u32(ring) + sl * kSlot, 16, 1024);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc5_mma_ss(d, da + 2 * k, db + 2 * k, id_s, c > 0 || k > 0);
-                    tc5_commit(&T.empty[sl]);
-                }
-                if (go)
-                    tc5_commit(&T.s_full[C::NS == 2 ? b & 1 : 0]);
-                if (go && b == t.nb - 1)
-                    tc5_commit(&T.q_done);
-            };
-            auto values = [&](int b) {
-                const int pb = C::NS == 2 ? b & 1 : 0;
-                go = go && tc5_wait(&T.p_ready[pb], (C::NS == 2 ? b >> 1 : b) & 1, abort);
-                if (!go)
-                    return;
-                tc5_fence_after();
-                const uint32_t p = tmem + pb * kN, d = tmem + C::O_COL;
-                for (int g = 0; g < C::NV; ++g, ++n) {
-                    const int sl = n % C::SLOTS;
-                    go = tc5_wait(&T.full[sl], (n / C::SLOTS) & 1, abort);
-                    if (!go)
-                        return;
-                    const uint64_t db = tc5_desc(smem_u32(ring) + sl * kSlot, C::VK * 128, 1024);
-#pragma unroll
-                    for (int k = 0; k < C::VK / 16; ++k)
-                        tc5_mma_ts(d, p + (g * C::VK + k * 16) / 2, db + k * (2048 >> 4), id_o,
-                                   b > 0 || g > 0 || k > 0);
-                    tc5_commit(&T.empty[sl]);
-                }
-                tc5_commit(b == t.nb - 1 ? &T.o_done : &T.pv_done);
-            };
-            if (C::NS == 2) {
-                scores(0);
-                for (int b = 1; b < t.nb && go; ++b) {
-                    scores(b);
-                    values(b - 1);
-                }
-                values(t.nb - 1);
-            } else {
-                for (int b = 0; b < t.nb && go; ++b) {
-                    scores(b);
-                    values(b);
-                }
-            }
-        }
-    } else if (warp >= 6) {
-        // look through the values of partly seen blocks
-        int n = 0;
-        uint32_t phase = 0;        // per slot: parity of its next part[] phase
-        const int w = warp - 6;
-        // slots are filled in the order K0 [K1 V0] [K2 V1] ... (two score buffers)
-        // or K0 V0 K1 V1 ...: the first value slot of block b
-        for (int b = part0; b < t.nb; ++b) {
-            n = C::NS == 2 ? min(b + 2, t.nb) * C::CH + b * C::NV : (b + 1) * C::CH + b * C::NV;
-            for (int g = 0; g < C::NV; ++g, ++n) {
-                const int sl = n % C::SLOTS;
-                bool go = tc5_wait(&T.part[sl], phase >> sl & 1, abort);
-                phase ^= 1u << sl;
-                uint4 *p = reinterpret_cast<uint4 *>(ring + sl * kSlot);
-                constexpr int UNITS = C::VK * D / 8;
-                static_assert(UNITS % 256 == 0, "four units a thread and turn");
-                for (int i0 = w * 32 + lane; go && i0 < UNITS; i0 += 256) {
-                    uint4 u[4];
-                    bool hit = false;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        u[k] = p[i0 + 64 * k];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // a set exponent field is largest: one packed maximum finds it
-                        const unsigned top = __vmaxu2(__vmaxu2(u[k].x & 0x7FFF7FFFu, u[k].y & 0x7FFF7FFFu),
-                                                      __vmaxu2(u[k].z & 0x7FFF7FFFu, u[k].w & 0x7FFF7FFFu));
-                        hit |= (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u;
+            for (int it = 0; go && next_tile(it, t); ++it) {
+                if (t.nb > 0) {
+                    const int head0 = t.level << hp_log2, kvh = head0 / (a.H / a.Hk);
+                    go = used == 0 || tc5_wait(&T.q_free, (used - 1) & 1, abort);
+                    ++used;
+                    if (go) {
+                        if (half == 0)
+                            mbar_arrive_expect_tx(&T.q_full, 2 * C::QB);
+                        else
+                            mbar_arrive_cluster(at_lead(&T.q_full));
+                        for (int ch = 0; ch < C::CH; ++ch)
+                            tma3d(smem_u32(qs) + ch * (kM * 128), &qmap, ch * 64, head0, t.row0,
+                                  at_lead(&T.q_full));
                     }
-                    if (!hit)
-                        continue;
-#pragma unroll 1
-                    for (int i = i0; i < i0 + 256; i += 64) {
-                        const uint4 v = p[i];
-                        uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                        // 16-byte unit i: chunk of 64 columns, key row, unit within the
-                        // row, swizzled by the row
-                        const int c = i / (C::VK * 8), key = (i / 8) % C::VK, un = (i & 7) ^ (key & 7);
-                        const int kidx = (b - part0) * kN + g * C::VK + key;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t h = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-                            if (!not_finite16(h))
-                                continue;
-                            const int what = (h & 0x7F) ? 0 : (h >> 15) ? 2 : 1;
-                            atomic_min16(&T.fix_at[what][c * 64 + un * 8 + e], kidx);
-                            x[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                    // waits for the next slot and announces `bytes` on the barrier its load
+                    // signals: the even CTA's full[], or one's own part[]
+                    uint32_t bar = 0;
+                    auto fill = [&](uint32_t bytes, bool part) -> uint32_t {
+                        const int sl = n % C::SLOTS;
+                        if (n >= C::SLOTS && !tc5_wait(&T.empty[sl], ((n / C::SLOTS) - 1) & 1, abort)) {
+                            go = false;
+                            return 0;
                         }
-                        p[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        in_part = part ? in_part | 1u << sl : in_part & ~(1u << sl);
+                        pphase ^= part ? 1u << sl : 0u;
+                        if (part) {
+                            bar = smem_u32(&T.part[sl]);
+                            mbar_arrive_expect_tx(&T.part[sl], bytes);
+                        } else {
+                            bar = at_lead(&T.full[sl]);
+                            if (half == 0)
+                                mbar_arrive_expect_tx(&T.full[sl], 2 * bytes);
+                            else
+                                mbar_arrive_cluster(bar);
+                        }
+                        ++n;
+                        return smem_u32(ring) + sl * kSlot;
+                    };
+                    auto load_k = [&](int b) {
+                        for (int ch = 0; ch < C::CH && go; ch += 2) {
+                            const int two = min(2, C::CH - ch);
+                            const uint32_t p = fill(two * 8192, false);
+                            for (int x = 0; x < two && go; ++x)
+                                tma4d(p + x * 8192, &kmap, (ch + x) * 64,
+                                      t.kv0 + (t.b0 + b) * kN + (int)half * 64, kvh, t.slot, bar);
+                        }
+                    };
+                    auto load_v = [&](int b) {
+                        for (int g = 0; g < C::VS && go; ++g) {
+                            const uint32_t p = fill(C::VK * C::CV * 128, t.b0 + b >= t.part0);
+                            for (int ch = 0; ch < C::CV && go; ++ch)
+                                tma4d(p + ch * (C::VK * 128), &vmap, (int)half * (D / 2) + ch * 64,
+                                      t.kv0 + (t.b0 + b) * kN + g * C::VK, kvh, t.slot, bar);
+                        }
+                    };
+                    load_k(0);
+                    for (int b = 1; b < t.nb && go; ++b) {
+                        load_k(b);
+                        load_v(b - 1);
                     }
-                    *(volatile int *)&T.fixes = 1;
+                    load_v(t.nb - 1);
                 }
-                fence_proxy_async_smem();
-                named_bar_sync(1, 64);
-                if (threadIdx.x == 6 * 32)
-                    mbar_arrive(&T.full[sl]);
+                mbar_arrive(&T.t_empty[it & 1]);
             }
+            // arrivals on this CTA's barriers that MMAs still owe it
+            for (int i = max(0, n - C::SLOTS); i < n && !*abort; ++i)
+                tc5_wait(&T.empty[i % C::SLOTS], (i / C::SLOTS) & 1, abort);
+            if (used > 0 && !*abort)
+                tc5_wait(&T.q_free, (used - 1) & 1, abort);
+            // every copy has landed before the shared memory is given up, also when a
+            // wait ran out (the odd CTA's are seen through the even one's barriers)
+            if (*abort && half == 0 && used > 0)
+                tc5_wait(&T.q_full, (used - 1) & 1, &none);
+            for (int i = max(0, n - C::SLOTS); i < n && *abort; ++i) {
+                const int sl = i % C::SLOTS;
+                if (in_part >> sl & 1)
+                    tc5_wait(&T.part[sl], (pphase >> sl & 1) ^ 1, &none);
+                else if (half == 0)
+                    tc5_wait(&T.full[sl], (i / C::SLOTS) & 1, &none);
+            }
+        }
+    } else if (warp == 9) {
+        // --------------------------------------------------------------- MMAs
+        if (lane == 0) {
+            constexpr uint32_t id_s = tc5_idesc(2 * kM, kN, false), id_o = tc5_idesc(2 * kM, D, true);
+            int n = 0, gb = 0, used = 0;        // slots, blocks and tiles so far
+            bool go = true;
+            Tile t;
+            for (int it = 0; go && next_tile(it, t); ++it) {
+                if (half == 0 && t.nb > 0) {
+                    go = tc5_wait(&T.q_full, used & 1, abort);
+                    auto scores = [&](int b) {
+                        const uint32_t d = tmem + ((gb + b) & 1) * kN;
+                        for (int ch = 0; ch < C::CH && go; ++ch) {
+                            const int sl = n % C::SLOTS;
+                            if ((ch & 1) == 0)
+                                go = tc5_wait(&T.full[sl], (n / C::SLOTS) & 1, abort);
+                            if (!go)
+                                return;
+                            tc5_fence_after();
+                            const uint64_t da = tc5_desc(smem_u32(qs) + ch * (kM * 128), 16, 1024);
+                            const uint64_t db = tc5_desc(smem_u32(ring) + sl * kSlot + (ch & 1) * 8192, 16, 1024);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc5_mma_ss(d, da + 2 * k, db + 2 * k, id_s, ch > 0 || k > 0);
+                            if ((ch & 1) || ch == C::CH - 1) {
+                                tc5_commit(&T.empty[sl], pair);
+                                ++n;
+                            }
+                        }
+                        tc5_commit(&T.s_full[(gb + b) & 1], pair);
+                        if (b == t.nb - 1)
+                            tc5_commit(&T.q_free, pair);
+                    };
+                    auto values = [&](int b) {
+                        const int pb = (gb + b) & 1;
+                        go = go && tc5_wait(&T.p_ready[pb], ((gb + b) >> 1) & 1, abort);
+                        if (b == 0 && used > 0)
+                            go = go && tc5_wait(&T.o_free, (used - 1) & 1, abort);
+                        if (!go)
+                            return;
+                        tc5_fence_after();
+                        const uint32_t d = tmem + kOCol;
+                        for (int g = 0; g < C::VS; ++g, ++n) {
+                            const int sl = n % C::SLOTS;
+                            go = tc5_wait(&T.full[sl], (n / C::SLOTS) & 1, abort);
+                            if (!go)
+                                return;
+                            const uint64_t db = tc5_desc(smem_u32(ring) + sl * kSlot, C::VK * 128, 1024);
+#pragma unroll
+                            for (int k = 0; k < C::VK / 16; ++k) {
+                                // probabilities of keys 0-63 stand in columns 0-31 of the
+                                // buffer, those of keys 64-127 in columns 64-95
+                                const int key = g * C::VK + k * 16;
+                                tc5_mma_ts(d, tmem + pb * kN + (key & 64) + (key & 63) / 2,
+                                           db + k * (2048 >> 4), id_o, b > 0 || g > 0 || k > 0);
+                            }
+                            tc5_commit(&T.empty[sl], pair);
+                        }
+                        // the last product has a barrier of its own: a parity does not tell
+                        // phase n from n - 2
+                        tc5_commit(b == t.nb - 1 ? &T.o_done : &T.pv_done, pair);
+                    };
+                    scores(0);
+                    for (int b = 1; b < t.nb && go; ++b) {
+                        scores(b);
+                        values(b - 1);
+                    }
+                    values(t.nb - 1);
+                    gb += t.nb;
+                    ++used;
+                }
+                mbar_arrive(&T.t_empty[it & 1]);
+            }
+            if (*abort && half == 0) {
+                // the MMAs that were issued are done before their memory is freed
+                int none = 0;
+                mbar_init(&T.q_free, 1);
+                fence_mbar_init();
+                tc5_commit(&T.q_free, (uint16_t)(1u << rank));
+                tc5_wait(&T.q_free, 0, &none);
+            }
+        }
+    } else if (warp == 10) {
+        // --------------------------- values of blocks that are seen only in part
+        int n0 = 0;                // slots before this tile
+        uint32_t phase = 0;        // per slot: parity of its next part[] phase
+        Tile t;
+        for (int it = 0; next_tile(it, t); ++it) {
+            for (int b = max(0, t.part0 - t.b0); b < t.nb; ++b) {
+                // slots are filled in the order K0 [K1 V0] [K2 V1] ...
+                int n = n0 + min(b + 2, t.nb) * C::KS + b * C::VS;
+                for (int g = 0; g < C::VS; ++g, ++n) {
+                    const int sl = n % C::SLOTS;
+                    const bool go = tc5_wait(&T.part[sl], phase >> sl & 1, abort);
+                    phase ^= 1u << sl;
+                    uint4 *p = reinterpret_cast<uint4 *>(ring + sl * kSlot);
+                    constexpr int UNITS = C::VK * C::CV * 8;
+                    static_assert(UNITS % 128 == 0, "four units a thread and turn");
+                    for (int i0 = lane; go && i0 < UNITS; i0 += 128) {
+                        uint4 u[4];
+                        bool hit = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            u[k] = p[i0 + 32 * k];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            // a set exponent field is largest: one packed maximum finds it
+                            const unsigned top = __vmaxu2(__vmaxu2(u[k].x & 0x7FFF7FFFu, u[k].y & 0x7FFF7FFFu),
+                                                          __vmaxu2(u[k].z & 0x7FFF7FFFu, u[k].w & 0x7FFF7FFFu));
+                            hit |= (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u;
+                        }
+                        if (!hit)
+                            continue;
+#pragma unroll 1
+                        for (int i = i0; i < i0 + 128; i += 32) {
+                            const uint4 v = p[i];
+                            uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                            // 16-byte unit i: chunk of 64 columns, key row, unit within the
+                            // row, swizzled by the row
+                            const int ch = i / (C::VK * 8), key = (i / 8) % C::VK, un = (i & 7) ^ (key & 7);
+                            const int kidx = (t.b0 + b - t.part0) * kN + g * C::VK + key;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t h = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                                if (!not_finite16(h))
+                                    continue;
+                                const int what = (h & 0x7F) ? 0 : (h >> 15) ? 2 : 1;
+                                const int col = (int)half * (D / 2) + ch * 64 + un * 8 + e;
+                                for (uint32_t to = lead; col < D && to < lead + 2; ++to)
+                                    atomic_min16(dsmem_addr(&T.fix_at[it & 1][what][col], to), kidx);
+                                x[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                            }
+                            p[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                        for (uint32_t to = lead; to < lead + 2; ++to)
+                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                                             dsmem_addr(&T.fixes[it & 1], to)),
+                                         "r"(1)
+                                         : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_release_cluster(at_lead(&T.full[sl]));
+                }
+            }
+            n0 += t.nb * (C::KS + C::VS);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&T.t_empty[it & 1]);
         }
     } else {
-        // ------------------------------------------------ softmax: a thread per row
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        // ---------------------- softmax: a thread per row and half of the columns
+        const int row = (warp & 3) * 32 + lane, hf = warp >> 2;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int tok = row >> hp_log2, hd = row & (hp - 1);
         const float c = a.scale_log2;
-        const int seen = t.seen0 + tok;           // keys this row sees
-        float m = -INFINITY;                      // the row's reference
-        float l = 0.f;
+        int gb = 0, used = 0, pvs = 0;      // blocks, tiles with blocks, products but last ones
         bool go = true;
-        for (int b = 0; b < t.nb; ++b) {
-            const int pb = C::NS == 2 ? b & 1 : 0;
-            const uint32_t S = tmem + lanes + pb * kN;
-            go = tc5_wait(&T.s_full[pb], (C::NS == 2 ? b >> 1 : b) & 1, abort);
-            go = __all_sync(0xffffffffu, go);
+        Tile t;
+        for (int it = 0;; ++it) {
+            // one decision for all, so that the barriers below are met by everybody:
+            // a wait that gives up skips work, never a barrier
+            go = named_bar_and(6, kSoft * 32, next_tile(it, t) && go);
             if (!go)
                 break;
-            tc5_fence_after();
-            const int lim = b >= part0 ? seen - b * kN : kN;    // visible columns
-            uint32_t r[32];
-            float mx = -INFINITY;
-#pragma unroll
-            for (int q = 0; q < kN / 32; ++q) {
-                tmem_ld32(r, S + q * 32);
-                tmem_wait_ld();
-                if (b >= part0) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        mx = fmaxf(mx, q * 32 + i < lim ? __uint_as_float(r[i]) : -INFINITY);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        mx = fmaxf(mx, __uint_as_float(r[i]));
+            const int head = (t.level << hp_log2) + hd;
+            const bool mine = tok < t.rows;
+            const int seen = t.seen0 + tok;           // keys this row sees
+            float m = -INFINITY;                      // the row's reference
+            float l = 0.f;                            // sum over this thread's columns
+            for (int b = 0; b < t.nb; ++b, ++gb) {
+                const int pb = gb & 1;
+                const uint32_t S = tmem + lanes + pb * kN + hf * 64;
+                go = __all_sync(0xffffffffu, go && tc5_wait(&T.s_full[pb], (gb >> 1) & 1, abort));
+                if (!go) {
+                    named_bar_sync(2 + (warp & 3), 64);
+                    continue;
                 }
-            }
-            // move the reference on the first block and when the maximum outgrows it
-            float alpha = 1.f;
-            const bool move = mx > m && (m == -INFINITY || (mx - m) * c > kGrow);
-            if (move) {
-                alpha = m == -INFINITY ? 0.f : ex2((m - mx) * c);
-                m = mx;
-            }
-            if (b > 0 && __any_sync(0xffffffffu, move)) {
-                go = __all_sync(0xffffffffu, tc5_wait(&T.pv_done, (b - 1) & 1, abort));
-                if (!go)
-                    break;
                 tc5_fence_after();
-                l *= alpha;
+                const bool part = t.b0 + b >= t.part0;
+                const int lim = part ? seen - (t.b0 + b) * kN - hf * 64 : 64;    // visible columns
+                uint32_t r0[32], r1[32];
+                float mx = -INFINITY;
+                tmem_ld32(r0, S);
+                tmem_ld32(r1, S + 32);
+                tmem_wait_ld();
+                if (part) {
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    tmem_ld32(r, tmem + lanes + C::O_COL + q * 32);
+                    for (int i = 0; i < 32; ++i) {
+                        r0[i] = i < lim ? r0[i] : 0xFF800000u;
+                        r1[i] = i + 32 < lim ? r1[i] : 0xFF800000u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    mx = fmaxf(mx, fmaxf(__uint_as_float(r0[i]), __uint_as_float(r1[i])));
+                // the row's maximum over both halves
+                T.mx[pb][hf][row] = mx;
+                named_bar_sync(2 + (warp & 3), 64);
+                mx = fmaxf(mx, T.mx[pb][hf ^ 1][row]);
+                // move the reference on the first block and when the maximum outgrows it
+                float alpha = 1.f;
+                const bool move = mx > m && (m == -INFINITY || (mx - m) * c > kGrow);
+                if (move) {
+                    alpha = m == -INFINITY ? 0.f : ex2((m - mx) * c);
+                    m = mx;
+                }
+                if (b > 0 && __any_sync(0xffffffffu, move)) {
+                    go = __all_sync(0xffffffffu, tc5_wait(&T.pv_done, (pvs + b - 1) & 1, abort));
+                    if (!go)
+                        continue;
+                    tc5_fence_after();
+                    l *= alpha;
+#pragma unroll 1
+                    for (int q = 0; q < C::HC / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(o, tmem + lanes + kOCol + hf * C::HC + q * 32);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(tmem + lanes + kOCol + hf * C::HC + q * 32, o);
+                    }
+                }
+                // a row without a visible key so far has reference -inf: against 0
+                // its masked scores give p = 0
+                const float ref = m == -INFINITY ? 0.f : m;
+                const uint64_t nref = pack2(-ref, -ref), cc = pack2(c, c);
+                uint64_t sum0 = 0, sum1 = 0;
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint64_t x0 =
+                        mul2(add2(pack2(__uint_as_float(r0[2 * i]), __uint_as_float(r0[2 * i + 1])), nref), cc);
+                    const uint64_t x1 =
+                        mul2(add2(pack2(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1])), nref), cc);
+                    float e0, e1, e2, e3;
+                    unpack2(x0, e0, e1);
+                    unpack2(x1, e2, e3);
+                    e0 = ex2(e0);
+                    e1 = ex2(e1);
+                    e2 = ex2(e2);
+                    e3 = ex2(e3);
+                    sum0 = add2(sum0, pack2(e0, e1));
+                    sum1 = add2(sum1, pack2(e2, e3));
+                    pk[i] = pack_bf16x2(e0, e1);
+                    pk[16 + i] = pack_bf16x2(e2, e3);
+                }
+                tmem_st32(S, pk);
+                float s0, s1;
+                unpack2(add2(sum0, sum1), s0, s1);
+                l += s0 + s1;
+                tmem_wait_st();
+                tc5_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(at_lead(&T.p_ready[pb]));
+            }
+            pvs += max(0, t.nb - 1);
+            // ------------------------------------------------------------- epilogue
+            const long long orow = t.row0 + tok;
+            const long long go_ = orow * a.gs.tok + (long long)head * a.gs.head + hf * C::HC;
+            __nv_bfloat16 *o = a.out + orow * a.os.tok + (long long)head * a.os.head + hf * C::HC;
+            const bool gated = a.gate && seen > 0 && mine;
+            uint4 gate[C::HC / 8];
+            if (gated && !a.gate_f32 && split == 1) {
+#pragma unroll
+                for (int i = 0; i < C::HC / 8; ++i)
+                    gate[i] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.gate) + go_)[i];
+            }
+            T.lsum[it & 1][hf][row] = l;
+            named_bar_sync(2 + (warp & 3), 64);
+            l += T.lsum[it & 1][hf ^ 1][row];
+            if (t.nb > 0) {
+                go = __all_sync(0xffffffffu, go && tc5_wait(&T.o_done, used & 1, abort));
+                tc5_fence_after();
+                ++used;
+            }
+            const float inv = seen > 0 ? 1.f / l : 0.f;
+            const bool fixes = go && *(volatile int *)&T.fixes[it & 1] != 0;
+            const int from = seen - t.part0 * kN;     // keys seen in the partly seen blocks
+            float *const stage = reinterpret_cast<float *>(ring) + row * C::ST + hf * C::HC;
+#pragma unroll
+            for (int q = 0; q < C::HC / 32; ++q) {
+                if (!go)
+                    continue;
+                float f[32];
+                if (t.nb > 0) {
+                    uint32_t r[32];
+                    tmem_ld32(r, tmem + lanes + kOCol + hf * C::HC + q * 32);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                    tmem_st32(tmem + lanes + C::O_COL + q * 32, r);
-                }
-            }
-            // a row without a visible key so far has reference -inf: against 0
-            // its masked scores give p = 0
-            const float ref = m == -INFINITY ? 0.f : m;
-            const uint64_t nref = pack2(-ref, -ref), cc = pack2(c, c);
-            uint64_t sum = 0;
-#pragma unroll
-            for (int q = 0; q < kN / 32; ++q) {
-                uint32_t pk[16];
-                tmem_ld32(r, S + q * 32);
-                tmem_wait_ld();
-                if (b >= part0) {
+                        f[i] = __uint_as_float(r[i]);
+                } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (q * 32 + i >= lim)
-                            r[i] = 0xFF800000u;
+                        f[i] = 0.f;
                 }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint64_t x = mul2(
-                        add2(pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), nref), cc);
-                    float e0, e1;
-                    unpack2(x, e0, e1);
-                    e0 = ex2(e0);
-                    e1 = ex2(e1);
-                    sum = add2(sum, pack2(e0, e1));
-                    pk[i] = pack_bf16x2(e0, e1);
-                }
-                tmem_st16(S + q * 16, pk);
-            }
-            float s0, s1;
-            unpack2(sum, s0, s1);
-            l += s0 + s1;
-            tmem_wait_st();
-            tc5_fence_before();
-            mbar_arrive(&T.p_ready[pb]);
-        }
-        // ------------------------------------------------------------- epilogue
-        // a barrier of its own: by now the last phases of pv_done may both be over,
-        // and a parity does not tell phase n from n - 2
-        go = go && tc5_wait(&T.o_done, 0, abort);
-        const bool gate_here = a.gate && !a.gate_f32;
-        if (gate_here)
-            go = go && tc5_wait(&T.g_full, 0, abort);
-        go = __all_sync(0xffffffffu, go);
-        if (go) {
-            tc5_fence_after();
-            const bool mine = tok < t.rows;
-            const float inv = seen > 0 ? 1.f / l : 0.f;
-            const bool fixes = *(volatile int *)&T.fixes != 0;
-            const long long row = t.row0 + tok;
-            __nv_bfloat16 *o = a.out + row * a.os.tok + (long long)(head0 + hd) * a.os.head;
-            const long long go_ = row * a.gs.tok + (long long)(head0 + hd) * a.gs.head;
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t r[32];
-                tmem_ld32(r, tmem + lanes + C::O_COL + q * 32);
-                tmem_wait_ld();
-                if (!mine)
-                    continue;
-                float f[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    f[i] = seen > 0 ? __uint_as_float(r[i]) * inv : 0.f;
                 if (fixes) {
-                    const int from = seen - part0 * kN;   // keys seen in the partly seen blocks
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         // values that are not finite, for the rows that see them
-                        if (from > T.fix_at[0][q * 32 + i])
+                        const int col = hf * C::HC + q * 32 + i;
+                        if (from > T.fix_at[it & 1][0][col])
                             f[i] = __int_as_float(0x7fffffff);
-                        if (from > T.fix_at[1][q * 32 + i])
+                        if (from > T.fix_at[it & 1][1][col])
                             f[i] += INFINITY;
-                        if (from > T.fix_at[2][q * 32 + i])
+                        if (from > T.fix_at[it & 1][2][col])
                             f[i] -= INFINITY;
                     }
                 }
-                if (a.gate && seen > 0) {
+                if (split > 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float4 *>(stage + q * 32 + 4 * i) =
+                            make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                    continue;
+                }
+                if (!mine)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    f[i] = seen > 0 ? f[i] * inv : 0.f;
+                if (gated) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float g[8];
@@ -572,45 +804,101 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                             g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w;
                             g[4] = w.x; g[5] = w.y; g[6] = w.z; g[7] = w.w;
                         } else {
-                            // chunk of 64 elements, row, 16-byte unit swizzled by the row
-                            const int r = threadIdx.x;
-                            ld_bf16x8(reinterpret_cast<const __nv_bfloat16 *>(
-                                          qs + (q >> 1) * (kM * 128) + r * 128 +
-                                          ((((q & 1) * 4 + e) ^ (r & 7)) << 4)),
-                                      g);
+                            unpack8(gate[q * 4 + e], g);
                         }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            f[e * 8 + i] = __fdividef(f[e * 8 + i], 1.f + __expf(-g[i]));
+                        gate8(f, e * 8, g);
                     }
                 }
                 uint4 *ov = reinterpret_cast<uint4 *>(o + q * 32);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    ov[e] = make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                       pack_bf16x2(f[8 * e + 4], f[8 * e + 5]),
-                                       pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
+                    ov[e] = pack8(f, e * 8);
             }
-        }
-        tc5_fence_before();
-    }
-    __syncwarp();
-    __syncthreads();
-    if (warp == 5) {
-        tc5_fence_after();
-        if (*abort) {
-            // the MMAs that were issued are done before their memory is freed
-            if (lane == 0) {
-                int none = 0;
-                mbar_init(&T.q_full, 1);
-                fence_mbar_init();
-                tc5_commit(&T.q_full);
-                tc5_wait(&T.q_full, 0, &none);
-                seq_flag(a.sq, GATTN_STATUS_TIMEOUT);
+            tc5_fence_before();
+            if (named_bar_and(6, kSoft * 32, fixes)) {
+                // this tile's columns again, before its successor but one uses them
+                for (int i = threadIdx.x; i < 3 * D; i += kSoft * 32)
+                    (&T.fix_at[it & 1][0][0])[i] = 0xFFFF;
+                if (threadIdx.x == 0)
+                    T.fixes[it & 1] = 0;
+            }
+            if (split > 1 && hf == 0) {
+                T.mx[0][0][row] = m;
+                T.lsum[1][0][row] = l;                // (the only tile's own have parity 0)
             }
             __syncwarp();
+            if (lane == 0) {
+                if (t.nb > 0)
+                    mbar_arrive_cluster(at_lead(&T.o_free));
+                mbar_arrive_cluster(dsmem_addr(&T.t_empty[it & 1], lead));
+                mbar_arrive_cluster(dsmem_addr(&T.t_empty[it & 1], lead + 1));
+            }
+            if (split > 1) {
+                break;                                // one tile per cluster
+            }
         }
-        tmem_free(tmem, C::COLS);
+    }
+    __syncwarp();
+    if (split > 1) {
+        // ------------------------------------------- join the shares of the blocks
+        cluster_sync();
+        const Tile t = T.tile[0];
+        if (warp < kSoft && t.s >= 0 && !*abort) {
+            // rows of this CTA's half that this share joins
+            const int each = kM / split;
+            for (int row = share * each + warp; row < (share + 1) * each; row += kSoft) {
+                const int tok = row >> hp_log2, hd = row & (hp - 1);
+                if (tok >= t.rows)
+                    continue;
+                const int head = (t.level << hp_log2) + hd, seen = t.seen0 + tok;
+                const long long orow = t.row0 + tok;
+                float top = -INFINITY, m[4], l = 0.f;
+                for (int p = 0; p < split; ++p) {
+                    m[p & 3] = ld_dsmem(dsmem_addr(&T.mx[0][0][row], 2 * p + half));
+                    top = fmaxf(top, m[p & 3]);
+                }
+                const float ref = top == -INFINITY ? 0.f : top;
+                for (int p = 0; p < split; ++p) {
+                    m[p & 3] = ex2((m[p & 3] - ref) * a.scale_log2);
+                    l += m[p & 3] * ld_dsmem(dsmem_addr(&T.lsum[1][0][row], 2 * p + half));
+                }
+                const float inv = 1.f / l;
+                for (int j = lane * 4; j < D; j += 128) {
+                    float f[4] = {};
+                    for (int p = 0; p < split; ++p) {
+                        const float4 x = ld_dsmem_v4(
+                            dsmem_addr(reinterpret_cast<float *>(ring) + row * C::ST + j, 2 * p + half));
+                        const float w = m[p & 3];
+                        f[0] += w * x.x;
+                        f[1] += w * x.y;
+                        f[2] += w * x.z;
+                        f[3] += w * x.w;
+                    }
+                    const long long go_ = orow * a.gs.tok + (long long)head * a.gs.head + j;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[i] = seen > 0 ? f[i] * inv : 0.f;
+                        if (a.gate && seen > 0) {
+                            const float g = a.gate_f32
+                                                ? static_cast<const float *>(a.gate)[go_ + i]
+                                                : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.gate)[go_ + i]);
+                            f[i] = __fdividef(f[i], 1.f + __expf(-g));
+                        }
+                    }
+                    *reinterpret_cast<uint2 *>(a.out + orow * a.os.tok + (long long)head * a.os.head + j) =
+                        make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+                }
+            }
+        }
+        __syncwarp();
+    }
+    cluster_sync();
+    tc5_fence_after();
+    if (warp == 9) {
+        if (*abort && lane == 0)
+            seq_flag(a.sq, GATTN_STATUS_TIMEOUT);
+        __syncwarp();
+        tmem_free(tmem, kCols);
     }
 }
 
@@ -645,41 +933,56 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     using C = Cfg<D>;
     auto *fn = prompt_attn_kernel<D>;
     static std::atomic<unsigned long long> done{0};
-    const cudaError_t attr = allow_smem(fn, C::SMEM, done);
-    if (attr != cudaSuccess)
-        return attr;
+    cudaError_t e = allow_smem(fn, C::SMEM, done);
+    if (e != cudaSuccess)
+        return e;
     if (!encoder())
         return cudaErrorNotSupported;
+    int dev = 0, sms = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
     int hp_log2 = 0;
     while (hp_log2 < 7 && (a.H / a.Hk) % (2 << hp_log2) == 0)
         ++hp_log2;
     const int hp = 1 << hp_log2, tpt = kM >> hp_log2;
-    CUtensorMap qm, km, vm, gm;
+    CUtensorMap qm, km, vm;
     const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.sq.total};
     const cuuint64_t qst[2] = {(cuuint64_t)a.qs.head * 2, (cuuint64_t)a.qs.tok * 2};
     const cuuint32_t qb[3] = {64, (cuuint32_t)hp, (cuuint32_t)tpt};
     const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)a.kv_rows, (cuuint64_t)a.Hk, (cuuint64_t)a.kv_batch};
     const cuuint64_t kst[3] = {(cuuint64_t)a.kt * 2, (cuuint64_t)a.kh * 2, (cuuint64_t)a.kb * 2};
     const cuuint64_t vst[3] = {(cuuint64_t)a.vt * 2, (cuuint64_t)a.vh * 2, (cuuint64_t)a.vb * 2};
-    const cuuint32_t kb[4] = {64, kN, 1, 1}, vb[4] = {64, C::VK, 1, 1};
-    const bool gate = a.gate && !a.gate_f32;
-    const cuuint64_t gst[2] = {(cuuint64_t)a.gs.head * 2, (cuuint64_t)a.gs.tok * 2};
-    if (!encode(&gm, 3, gate ? a.gate : a.q, qd, gate ? gst : qst, qb))
-        return cudaErrorInvalidValue;
+    const cuuint32_t kb[4] = {64, 64, 1, 1}, vb[4] = {64, C::VK, 1, 1};
     if (!encode(&qm, 3, a.q, qd, qst, qb) || !encode(&km, 4, a.k, kd, kst, kb) ||
         !encode(&vm, 4, a.v, kd, vst, vb))
         return cudaErrorInvalidValue;
-    // at most one partly filled tile per sequence
-    const long long tiles = a.sq.total / tpt + std::min<long long>(a.sq.n, a.sq.total);
-    const long long grid = tiles * (a.H >> hp_log2);
-    if (grid > 0x7fffffff)
+    // tiles of a pair, at most one partly filled per sequence
+    const long long tiles =
+        (a.sq.total / (2 * tpt) + std::min<long long>(a.sq.n, a.sq.total)) * (a.H >> hp_log2);
+    const long long most = a.max_kv > 0 ? std::min(a.max_kv, a.kv_rows) : a.kv_rows;
+    // shares of the key blocks: while the pairs leave SMs idle and a share keeps
+    // 512 keys
+    int split = 1;
+    while (split < 4 && tiles * 2 * split < sms && most / (2 * split) >= 512)
+        split *= 2;
+    const long long clusters = split == 1 ? std::min<long long>(tiles, sms / 2) : tiles;
+    if (clusters * 2 * split > 0x7fffffff)
         return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2 * split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)(clusters * 2 * split));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, fn, a, qm, km, vm, gm, hp_log2);
+    return cudaLaunchKernelEx(&cfg, fn, a, qm, km, vm, hp_log2, split);
 }
 
 }  // namespace

@@ -9,7 +9,10 @@ namespace gattn {
 // ------------------------------------------------------------ bounded waits
 
 // Waits for the phase with the given parity; gives up after kWaitLimitNs or when
-// another thread of the CTA gave up (*abort), and then returns false.
+// another thread of the CTA gave up (*abort), and then returns false.  What the
+// barriers here guard is written and read by tensor cores and copies, which their
+// own fences order; a wait or arrival with cluster scope would add a memory fence
+// of several hundred cycles each.
 __device__ __forceinline__ bool tc5_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
     if (mbar_try(bar, parity))
@@ -26,21 +29,37 @@ __device__ __forceinline__ bool tc5_wait(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
+// One arrival on a barrier given by its shared::cluster address.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// The same after everything this thread wrote, for the whole cluster to see.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
 // --------------------------------------------------------------------- TMEM
 
-// Allocates `cols` TMEM columns (a power of two >= 32) for the CTA; whole warp.
+// The cta_group::2 forms work on a pair of CTAs (cluster ranks 2 i and 2 i + 1): both
+// allocate and free the same columns, MMAs are issued by the even one.
+
+// Allocates `cols` TMEM columns (a power of two >= 32) of the pair; a whole warp in
+// each CTA.
 __device__ __forceinline__ void tmem_alloc(uint32_t *smem_slot, uint32_t cols)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(smem_slot)),
                  "r"(cols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
                  : "memory");
 }
 
@@ -99,7 +118,7 @@ __device__ __forceinline__ uint64_t tc5_desc(uint32_t addr, uint32_t leading, ui
            ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor of kind::f16: bf16 operands, fp32 accumulator.
+// Instruction descriptor of kind::f16: bf16 operands, fp32 accumulator; M rows of the pair.
 __host__ __device__ constexpr uint32_t tc5_idesc(int M, int N, bool b_mn_major)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u) |
@@ -110,7 +129,7 @@ __host__ __device__ constexpr uint32_t tc5_idesc(int M, int N, bool b_mn_major)
 __device__ __forceinline__ void tc5_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
                  "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
                  : "memory");
 }
@@ -119,35 +138,38 @@ __device__ __forceinline__ void tc5_mma_ss(uint32_t d, uint64_t a, uint64_t b, u
 __device__ __forceinline__ void tc5_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
                  "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
                  : "memory");
 }
 
-// The mbarrier gets one arrival when every MMA this thread issued is done.
-__device__ __forceinline__ void tc5_commit(uint64_t *bar)
+// The barrier at this offset gets one arrival in every CTA of `mask` (cluster ranks)
+// when every MMA this thread issued is done.
+__device__ __forceinline__ void tc5_commit(uint64_t *bar, uint16_t mask)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_u32(bar))
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+                 "[%0], %1;" ::"r"(smem_u32(bar)),
+                 "h"(mask)
                  : "memory");
 }
 
 // -------------------------------------------------------------- tiled copies
 
-__device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
+// The barrier (a shared::cluster address) may be the other CTA's of the pair.
+__device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
                  : "memory");
 }
 
 __device__ __forceinline__ void tma4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
-                                      uint64_t *bar)
+                                      uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+    asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
                  " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
                  : "memory");
 }
 
