@@ -19,10 +19,14 @@
 //
 // The grid is persistent, one CTA per SM; tiles are dealt longest first.  Per CTA:
 // warps 0-7 softmax and epilogue (a thread per row and half of the columns), 8
-// copies, 9 issues the MMAs (of the pair, in the even CTA), 11 finds tiles; 10 looks
-// through the values of blocks that some row sees only part of: a value that is
-// not finite would spoil rows that do not see it (0 * NaN), so it is replaced by
-// zero there, and the rows that do see it get it back at the end.
+// copies, 9 issues the MMAs (of the pair, in the even CTA), 10 stores, 11 finds tiles.
+// The gate tile comes through the ring like the keys and values; the rows take its
+// place and leave from there, so that no thread reads or writes scattered rows.
+//
+// Blocks that some row sees only part of: a value that is not finite would spoil
+// rows that do not see it (0 * NaN).  The softmax warps look through the values of
+// such a block before its product, put zero in such a value's place, and the rows
+// that do see it get it back at the end.
 //
 // Few rows over many keys: clusters of 2, 4 or 8 CTAs, each pair taking a share of
 // the blocks; the partial (m, l, O) are joined through distributed shared memory.
@@ -71,8 +75,8 @@ struct Cfg {
     static constexpr int ST = D + 4;                // row stride of staged partial sums (floats)
     struct alignas(16) Tables {                     // behind the ring
         uint64_t full[SLOTS], empty[SLOTS];
-        uint64_t part[SLOTS];                       // a value slot that warp 10 looks through
-        uint64_t q_full, q_free, s_full[2], p_ready[2], pv_done, o_done, o_free, t_full[2], t_empty[2];
+        uint64_t part[SLOTS];                       // loads that the softmax warps read
+        uint64_t q_full, q_free, s_full[2], p_ready[2], pv_done, o_done, o_free, out_ready, t_full[2], t_empty[2];
         float mx[2][2][kM];                         // block parity, column half, row
         float lsum[2][2][kM];                       // tile parity, column half, row
         Tile tile[2];
@@ -280,6 +284,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap omap,
                    int hp_log2, int split)
 {
     using C = Cfg<D>;
@@ -296,7 +301,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
 
     if (warp == 8 && lane == 0) {
         for (int i = 0; i < C::SLOTS; ++i) {
-            mbar_init(&T.full[i], 2);                  // a producer or guard of each CTA
+            mbar_init(&T.full[i], 2);                  // the producers of both CTAs
             mbar_init(&T.empty[i], 1);
             mbar_init(&T.part[i], 1);
         }
@@ -312,6 +317,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
         mbar_init(&T.pv_done, 1);
         mbar_init(&T.o_done, 1);
         mbar_init(&T.o_free, 2 * kSoft);
+        mbar_init(&T.out_ready, kSoft);
         T.abort = 0;
         fence_mbar_init();
         prefetch_tensormap(&qmap);
@@ -413,8 +419,13 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                         in_part = part ? in_part | 1u << sl : in_part & ~(1u << sl);
                         pphase ^= part ? 1u << sl : 0u;
                         if (part) {
+                            // the softmax warps wait for these bytes; full[] only keeps step
                             bar = smem_u32(&T.part[sl]);
-                            mbar_arrive_expect_tx(&T.part[sl], bytes);
+                            if (bytes)
+                                mbar_arrive_expect_tx(&T.part[sl], bytes);
+                            else
+                                mbar_arrive(&T.part[sl]);
+                            mbar_arrive_cluster(at_lead(&T.full[sl]));
                         } else {
                             bar = at_lead(&T.full[sl]);
                             if (half == 0)
@@ -448,6 +459,13 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                         load_v(b - 1);
                     }
                     load_v(t.nb - 1);
+                    // the rows' way out, with the gate where it is bf16
+                    const bool gate = a.gate && !a.gate_f32;
+                    for (int ch = 0; ch < C::CH && go && split == 1; ++ch) {
+                        const uint32_t p = fill(gate ? kM * 128 : 0, true);
+                        if (go && gate)
+                            tma3d(p, &gmap, ch * 64, head0, t.row0, bar);
+                    }
                 }
                 mbar_arrive(&T.t_empty[it & 1]);
             }
@@ -464,7 +482,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                 const int sl = i % C::SLOTS;
                 if (in_part >> sl & 1)
                     tc5_wait(&T.part[sl], (pphase >> sl & 1) ^ 1, &none);
-                else if (half == 0)
+                if (half == 0)
                     tc5_wait(&T.full[sl], (i / C::SLOTS) & 1, &none);
             }
         }
@@ -537,6 +555,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                     }
                     values(t.nb - 1);
                     gb += t.nb;
+                    n += split == 1 ? C::CH : 0;
                     ++used;
                 }
                 mbar_arrive(&T.t_empty[it & 1]);
@@ -551,74 +570,50 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             }
         }
     } else if (warp == 10) {
-        // --------------------------- values of blocks that are seen only in part
-        int n0 = 0;                // slots before this tile
-        uint32_t phase = 0;        // per slot: parity of its next part[] phase
+        // ------------------------------------------------------------- stores
+        int n0 = 0, used = 0;
         Tile t;
-        for (int it = 0; next_tile(it, t); ++it) {
-            for (int b = max(0, t.part0 - t.b0); b < t.nb; ++b) {
-                // slots are filled in the order K0 [K1 V0] [K2 V1] ...
-                int n = n0 + min(b + 2, t.nb) * C::KS + b * C::VS;
-                for (int g = 0; g < C::VS; ++g, ++n) {
-                    const int sl = n % C::SLOTS;
-                    const bool go = tc5_wait(&T.part[sl], phase >> sl & 1, abort);
-                    phase ^= 1u << sl;
-                    uint4 *p = reinterpret_cast<uint4 *>(ring + sl * kSlot);
-                    constexpr int UNITS = C::VK * C::CV * 8;
-                    static_assert(UNITS % 128 == 0, "four units a thread and turn");
-                    for (int i0 = lane; go && i0 < UNITS; i0 += 128) {
-                        uint4 u[4];
-                        bool hit = false;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            u[k] = p[i0 + 32 * k];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            // a set exponent field is largest: one packed maximum finds it
-                            const unsigned top = __vmaxu2(__vmaxu2(u[k].x & 0x7FFF7FFFu, u[k].y & 0x7FFF7FFFu),
-                                                          __vmaxu2(u[k].z & 0x7FFF7FFFu, u[k].w & 0x7FFF7FFFu));
-                            hit |= (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u;
-                        }
-                        if (!hit)
-                            continue;
-#pragma unroll 1
-                        for (int i = i0; i < i0 + 128; i += 32) {
-                            const uint4 v = p[i];
-                            uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                            // 16-byte unit i: chunk of 64 columns, key row, unit within the
-                            // row, swizzled by the row
-                            const int ch = i / (C::VK * 8), key = (i / 8) % C::VK, un = (i & 7) ^ (key & 7);
-                            const int kidx = (t.b0 + b - t.part0) * kN + g * C::VK + key;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t h = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-                                if (!not_finite16(h))
-                                    continue;
-                                const int what = (h & 0x7F) ? 0 : (h >> 15) ? 2 : 1;
-                                const int col = (int)half * (D / 2) + ch * 64 + un * 8 + e;
-                                for (uint32_t to = lead; col < D && to < lead + 2; ++to)
-                                    atomic_min16(dsmem_addr(&T.fix_at[it & 1][what][col], to), kidx);
-                                x[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                            }
-                            p[i] = make_uint4(x[0], x[1], x[2], x[3]);
-                        }
-                        for (uint32_t to = lead; to < lead + 2; ++to)
-                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                                             dsmem_addr(&T.fixes[it & 1], to)),
-                                         "r"(1)
-                                         : "memory");
+        for (int it = 0; split == 1; ++it) {
+            if (!__all_sync(0xffffffffu, next_tile(it, t)))
+                break;
+            if (t.nb > 0) {
+                n0 += t.nb * (C::KS + C::VS);
+                const int head0 = t.level << hp_log2;
+                if (!__all_sync(0xffffffffu, tc5_wait(&T.out_ready, used & 1, abort)))
+                    break;
+                ++used;
+                if (t.rows == tpt) {
+                    if (lane == 0) {
+                        for (int ch = 0; ch < C::CH; ++ch)
+                            tma_store3d(&omap, smem_u32(ring) + (n0 + ch) % C::SLOTS * kSlot, ch * 64, head0, t.row0);
+                        tma_store_commit();
+                        tma_store_wait_read();
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_release_cluster(at_lead(&T.full[sl]));
+                } else {
+                    // the rows there are: a 16-byte unit per lane, eight to a row
+                    const int rows = t.rows << hp_log2;
+#pragma unroll 4
+                    for (int i = lane; i < rows * C::CH * 8; i += 32) {
+                        const int ch = i / (rows * 8), row = i / 8 % rows, un = i & 7;
+                        const uint4 u = *reinterpret_cast<const uint4 *>(
+                            ring + (n0 + ch) % C::SLOTS * kSlot + row * 128 + ((un ^ (row & 7)) << 4));
+                        *reinterpret_cast<uint4 *>(a.out + (long long)(t.row0 + (row >> hp_log2)) * a.os.tok +
+                                                   (long long)(head0 + (row & (hp - 1))) * a.os.head + ch * 64 +
+                                                   un * 8) = u;
+                    }
                 }
+                __syncwarp();
+                if (lane == 0)
+                    for (int ch = 0; ch < C::CH; ++ch)
+                        mbar_arrive(&T.empty[(n0 + ch) % C::SLOTS]);
+                n0 += C::CH;
             }
-            n0 += t.nb * (C::KS + C::VS);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&T.t_empty[it & 1]);
         }
+        if (lane == 0)
+            tma_store_wait();
     } else {
         // ---------------------- softmax: a thread per row and half of the columns
         const int row = (warp & 3) * 32 + lane, hf = warp >> 2;
@@ -626,7 +621,53 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
         const int tok = row >> hp_log2, hd = row & (hp - 1);
         const float c = a.scale_log2;
         int gb = 0, used = 0, pvs = 0;      // blocks, tiles with blocks, products but last ones
+        int n0 = 0;                         // slots before this tile
+        uint32_t phase = 0;                 // per slot: parity of its next part[] phase
         bool go = true;
+        // values of a slot that are not finite: remembered for both CTAs, zero here
+        auto look_through = [&](uint8_t *slot, int key0, int par) {
+            uint4 *p = reinterpret_cast<uint4 *>(slot);
+            constexpr int PER = C::VK * C::CV * 8 / (kSoft * 32);     // 16-byte units a thread
+            uint4 u[PER];
+            bool hit = false;
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+                u[k] = p[threadIdx.x + k * kSoft * 32];
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                // a set exponent field is largest: one packed maximum finds it
+                const unsigned top = __vmaxu2(__vmaxu2(u[k].x & 0x7FFF7FFFu, u[k].y & 0x7FFF7FFFu),
+                                              __vmaxu2(u[k].z & 0x7FFF7FFFu, u[k].w & 0x7FFF7FFFu));
+                hit |= (top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u;
+            }
+            if (!hit)
+                return;
+#pragma unroll 1
+            for (int i = threadIdx.x; i < PER * kSoft * 32; i += kSoft * 32) {
+                const uint4 v = p[i];
+                uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                // 16-byte unit i: chunk of 64 columns, key row, unit within the row,
+                // swizzled by the row
+                const int ch = i / (C::VK * 8), key = (i / 8) % C::VK, un = (i & 7) ^ (key & 7);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t h = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                    if (!not_finite16(h))
+                        continue;
+                    const int what = (h & 0x7F) ? 0 : (h >> 15) ? 2 : 1;
+                    const int col = (int)half * (D / 2) + ch * 64 + un * 8 + e;
+                    for (uint32_t to = lead; col < D && to < lead + 2; ++to)
+                        atomic_min16(dsmem_addr(&T.fix_at[par][what][col], to), key0 + key);
+                    x[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+                p[i] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            for (uint32_t to = lead; to < lead + 2; ++to)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_addr(&T.fixes[par], to)), "r"(1)
+                             : "memory");
+            fence_proxy_async_smem();
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        };
         Tile t;
         for (int it = 0;; ++it) {
             // one decision for all, so that the barriers below are met by everybody:
@@ -721,6 +762,18 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                 float s0, s1;
                 unpack2(add2(sum0, sum1), s0, s1);
                 l += s0 + s1;
+                if (part) {
+                    // slots are filled in the order K0 [K1 V0] [K2 V1] ...
+                    int n = n0 + min(b + 2, t.nb) * C::KS + b * C::VS;
+#pragma unroll 1
+                    for (int g = 0; g < C::VS; ++g, ++n) {
+                        const int sl = n % C::SLOTS;
+                        go = __all_sync(0xffffffffu, tc5_wait(&T.part[sl], phase >> sl & 1, abort)) && go;
+                        phase ^= 1u << sl;
+                        if (go)
+                            look_through(ring + sl * kSlot, (t.b0 + b - t.part0) * kN + g * C::VK, it & 1);
+                    }
+                }
                 tmem_wait_st();
                 tc5_fence_before();
                 __syncwarp();
@@ -733,11 +786,15 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             const long long go_ = orow * a.gs.tok + (long long)head * a.gs.head + hf * C::HC;
             __nv_bfloat16 *o = a.out + orow * a.os.tok + (long long)head * a.os.head + hf * C::HC;
             const bool gated = a.gate && seen > 0 && mine;
-            uint4 gate[C::HC / 8];
-            if (gated && !a.gate_f32 && split == 1) {
-#pragma unroll
-                for (int i = 0; i < C::HC / 8; ++i)
-                    gate[i] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.gate) + go_)[i];
+            n0 += t.nb * (C::KS + C::VS);
+            if (t.nb > 0 && split == 1) {
+                // the slots that hold the gate and take the rows
+#pragma unroll 1
+                for (int ch = 0; ch < C::CH; ++ch) {
+                    const int sl = (n0 + ch) % C::SLOTS;
+                    go = __all_sync(0xffffffffu, go && tc5_wait(&T.part[sl], phase >> sl & 1, abort));
+                    phase ^= 1u << sl;
+                }
             }
             T.lsum[it & 1][hf][row] = l;
             named_bar_sync(2 + (warp & 3), 64);
@@ -788,11 +845,22 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                             make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
                     continue;
                 }
-                if (!mine)
+                if (t.nb == 0) {
+                    if (mine)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4 *>(o + q * 32)[e] = make_uint4(0, 0, 0, 0);
                     continue;
+                }
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     f[i] = seen > 0 ? f[i] * inv : 0.f;
+                const int col0 = hf * C::HC + q * 32;
+                uint8_t *const line = ring + (n0 + (col0 >> 6)) % C::SLOTS * kSlot + row * 128;
+                uint4 *unit[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    unit[e] = reinterpret_cast<uint4 *>(line + ((((col0 & 63) / 8 + e) ^ (row & 7)) << 4));
                 if (gated) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -804,15 +872,18 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                             g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w;
                             g[4] = w.x; g[5] = w.y; g[6] = w.z; g[7] = w.w;
                         } else {
-                            unpack8(gate[q * 4 + e], g);
+                            unpack8(*unit[e], g);
                         }
                         gate8(f, e * 8, g);
                     }
                 }
-                uint4 *ov = reinterpret_cast<uint4 *>(o + q * 32);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    ov[e] = pack8(f, e * 8);
+                    *unit[e] = pack8(f, e * 8);
+            }
+            if (t.nb > 0 && split == 1) {
+                n0 += C::CH;
+                fence_proxy_async_smem();
             }
             tc5_fence_before();
             if (named_bar_and(6, kSoft * 32, fixes)) {
@@ -828,8 +899,10 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             }
             __syncwarp();
             if (lane == 0) {
-                if (t.nb > 0)
+                if (t.nb > 0) {
                     mbar_arrive_cluster(at_lead(&T.o_free));
+                    mbar_arrive(&T.out_ready);
+                }
                 mbar_arrive_cluster(dsmem_addr(&T.t_empty[it & 1], lead));
                 mbar_arrive_cluster(dsmem_addr(&T.t_empty[it & 1], lead + 1));
             }
@@ -948,7 +1021,7 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     while (hp_log2 < 7 && (a.H / a.Hk) % (2 << hp_log2) == 0)
         ++hp_log2;
     const int hp = 1 << hp_log2, tpt = kM >> hp_log2;
-    CUtensorMap qm, km, vm;
+    CUtensorMap qm, km, vm, gm, om;
     const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.sq.total};
     const cuuint64_t qst[2] = {(cuuint64_t)a.qs.head * 2, (cuuint64_t)a.qs.tok * 2};
     const cuuint32_t qb[3] = {64, (cuuint32_t)hp, (cuuint32_t)tpt};
@@ -956,6 +1029,11 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     const cuuint64_t kst[3] = {(cuuint64_t)a.kt * 2, (cuuint64_t)a.kh * 2, (cuuint64_t)a.kb * 2};
     const cuuint64_t vst[3] = {(cuuint64_t)a.vt * 2, (cuuint64_t)a.vh * 2, (cuuint64_t)a.vb * 2};
     const cuuint32_t kb[4] = {64, 64, 1, 1}, vb[4] = {64, C::VK, 1, 1};
+    const bool gate = a.gate && !a.gate_f32;
+    const cuuint64_t gst[2] = {(cuuint64_t)a.gs.head * 2, (cuuint64_t)a.gs.tok * 2};
+    const cuuint64_t ost[2] = {(cuuint64_t)a.os.head * 2, (cuuint64_t)a.os.tok * 2};
+    if (!encode(&gm, 3, gate ? a.gate : a.q, qd, gate ? gst : qst, qb) || !encode(&om, 3, a.out, qd, ost, qb))
+        return cudaErrorInvalidValue;
     if (!encode(&qm, 3, a.q, qd, qst, qb) || !encode(&km, 4, a.k, kd, kst, kb) ||
         !encode(&vm, 4, a.v, kd, vst, vb))
         return cudaErrorInvalidValue;
@@ -982,7 +1060,7 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, fn, a, qm, km, vm, hp_log2, split);
+    return cudaLaunchKernelEx(&cfg, fn, a, qm, km, vm, gm, om, hp_log2, split);
 }
 
 }  // namespace

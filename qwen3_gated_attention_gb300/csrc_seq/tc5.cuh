@@ -35,12 +35,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// The same after everything this thread wrote, for the whole cluster to see.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t addr)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
 // --------------------------------------------------------------------- TMEM
 
 // The cta_group::2 forms work on a pair of CTAs (cluster ranks 2 i and 2 i + 1): both
@@ -172,6 +166,19 @@ __device__ __forceinline__ void tma4d(uint32_t dst, const CUtensorMap *map, int 
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
                  : "memory");
 }
+
+// Stores: committed as a group; wait_read lets the shared memory be reused, wait is
+// for the writes themselves.
+__device__ __forceinline__ void tma_store3d(const CUtensorMap *map, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // --------------------------------------------------------------- packed math
 
