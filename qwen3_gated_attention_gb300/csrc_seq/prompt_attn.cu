@@ -145,7 +145,7 @@ struct Dealer {
 
     // Sequence and level (tile within it) of the rank-th tile; false: none.  Up to
     // 32 sequences in order of falling key blocks, more in their own order.
-    __device__ bool find(const PromptAttnArgs &a, int tp, long long rank, bool first, SeqKeys &q, int &s,
+    __device__ __noinline__ bool find(const PromptAttnArgs &a, int tp, long long rank, bool first, SeqKeys &q, int &s,
                          int &level)
     {
         const int lane = threadIdx.x & 31, n = a.sq.n;
@@ -256,28 +256,43 @@ __device__ __forceinline__ bool named_bar_and(int id, int threads, bool ok)
     return r != 0;
 }
 
-// f *= sigmoid(g), for 8 values
-__device__ __forceinline__ void gate8(float (&f)[32], int at, const float (&g)[8])
+__device__ __forceinline__ float rcp(float x)
 {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        f[at + i] = __fdividef(f[at + i], 1.f + __expf(-g[i]));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&g)[8])
+// 1 / (1 + e^-g)
+__device__ __forceinline__ float sigmoid(float g) { return rcp(1.f + ex2(-1.4426950408889634f * g)); }
+
+// f *= sigmoid(g) for four pairs, a pair with one reciprocal, 1/a = b (1/(a b)): the
+// epilogue is bound by the special function unit.  No branch within, so that the
+// pairs overlap.
+__device__ __forceinline__ void gate4(uint64_t (&f)[4], const uint64_t (&g)[4])
 {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float x[8], r[8];
+    bool fits = true;                                // products stay finite; false for NaN
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        g[2 * i] = bf16_lo(w[i]);
-        g[2 * i + 1] = bf16_hi(w[i]);
+        unpack2(mul2(g[i], pack2(-1.4426950408889634f, -1.4426950408889634f)), x[2 * i], x[2 * i + 1]);
+        fits = fits && x[2 * i] <= 60.f && x[2 * i + 1] <= 60.f;
     }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[32], int at)
-{
-    return make_uint4(pack_bf16x2(f[at], f[at + 1]), pack_bf16x2(f[at + 2], f[at + 3]),
-                      pack_bf16x2(f[at + 4], f[at + 5]), pack_bf16x2(f[at + 6], f[at + 7]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpack2(add2(pack2(ex2(x[2 * i]), ex2(x[2 * i + 1])), pack2(1.f, 1.f)), a, b);
+        const float ab = rcp(a * b);
+        r[2 * i] = ab * b;
+        r[2 * i + 1] = ab * a;
+    }
+    if (!fits)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r[i] = rcp(1.f + ex2(x[i]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = mul2(f[i], pack2(r[2 * i], r[2 * i + 1]));
 }
 
 template <int D>
@@ -329,6 +344,13 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
         for (int i = lane; i < 2 * 3 * D; i += 32)
             (&T.fix_at[0][0][0])[i] = 0xFFFF;
     }
+    // tiles are dealt round by round, every other round backwards, so that nobody
+    // keeps getting the longer ones; the first is looked for while the CTAs meet
+    const long long clusters = gridDim.x / (2 * split), place = blockIdx.x / (2 * split);
+    Dealer deal;
+    SeqKeys q;
+    int seq = -1, level = 0;
+    bool some = warp == 11 && deal.find(a, 2 * tpt, place / groups, true, q, seq, level);
     tc5_fence_before();
     __syncthreads();
     cluster_sync();
@@ -346,16 +368,15 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
     if (warp == 11) {
         // ------------------------------------------------------------- tiles
         const int tp = 2 * tpt;
-        const long long clusters = gridDim.x / (2 * split), c = blockIdx.x / (2 * split);
-        Dealer deal;
         for (int it = 0;; ++it) {
+            const long long r = it * clusters + (it & 1 ? clusters - 1 - place : place);
+            if (it > 0)
+                some = split == 1 && deal.find(a, tp, r / groups, false, q, seq, level);
             if (it >= 2 && !__all_sync(0xffffffffu, tc5_wait(&T.t_empty[it & 1], ((it >> 1) - 1) & 1, abort)))
                 break;
-            // every other round backwards, so that nobody keeps getting the longer ones
-            const long long r = it * clusters + (it & 1 ? clusters - 1 - c : c);
-            SeqKeys q;
             Tile t;
-            bool some = (split == 1 || it == 0) && deal.find(a, tp, r / groups, it == 0, q, t.s, t.level);
+            t.s = seq;
+            t.level = level;
             if (some) {
                 const int tok0 = t.level * tp;
                 const long long last = q.ok ? q.past + min(q.len, tok0 + tp) : 0;
@@ -591,15 +612,16 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                     }
                 } else {
                     // the rows there are: a 16-byte unit per lane, eight to a row
-                    const int rows = t.rows << hp_log2;
+                    const int rows = t.rows << hp_log2, un = lane & 7;
+                    for (int ch = 0; ch < C::CH; ++ch) {
+                        const uint8_t *from = ring + (n0 + ch) % C::SLOTS * kSlot;
+                        __nv_bfloat16 *to = a.out + (long long)t.row0 * a.os.tok + (long long)head0 * a.os.head +
+                                            ch * 64 + un * 8;
 #pragma unroll 4
-                    for (int i = lane; i < rows * C::CH * 8; i += 32) {
-                        const int ch = i / (rows * 8), row = i / 8 % rows, un = i & 7;
-                        const uint4 u = *reinterpret_cast<const uint4 *>(
-                            ring + (n0 + ch) % C::SLOTS * kSlot + row * 128 + ((un ^ (row & 7)) << 4));
-                        *reinterpret_cast<uint4 *>(a.out + (long long)(t.row0 + (row >> hp_log2)) * a.os.tok +
-                                                   (long long)(head0 + (row & (hp - 1))) * a.os.head + ch * 64 +
-                                                   un * 8) = u;
+                        for (int row = lane >> 3; row < rows; row += 4)
+                            *reinterpret_cast<uint4 *>(to + (row >> hp_log2) * a.os.tok +
+                                                       (row & (hp - 1)) * a.os.head) =
+                                *reinterpret_cast<const uint4 *>(from + row * 128 + ((un ^ (row & 7)) << 4));
                     }
                 }
                 __syncwarp();
@@ -785,7 +807,6 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             const long long orow = t.row0 + tok;
             const long long go_ = orow * a.gs.tok + (long long)head * a.gs.head + hf * C::HC;
             __nv_bfloat16 *o = a.out + orow * a.os.tok + (long long)head * a.os.head + hf * C::HC;
-            const bool gated = a.gate && seen > 0 && mine;
             n0 += t.nb * (C::KS + C::VS);
             if (t.nb > 0 && split == 1) {
                 // the slots that hold the gate and take the rows
@@ -808,78 +829,105 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             const bool fixes = go && *(volatile int *)&T.fixes[it & 1] != 0;
             const int from = seen - t.part0 * kN;     // keys seen in the partly seen blocks
             float *const stage = reinterpret_cast<float *>(ring) + row * C::ST + hf * C::HC;
-#pragma unroll
-            for (int q = 0; q < C::HC / 32; ++q) {
+            // sixteen columns at a time in a rolled loop: this code runs once a tile, and
+            // unrolled it costs more in instruction fetches than it computes
+            const uint64_t inv2 = pack2(inv, inv);
+            const bool gate_smem = a.gate && !a.gate_f32;
+            uint32_t nx[16];
+            if (go && t.nb > 0)
+                tmem_ld16(nx, tmem + lanes + kOCol + hf * C::HC);
+#pragma unroll 1
+            for (int q = 0; q < C::HC; q += 16) {
                 if (!go)
                     continue;
-                float f[32];
+                uint64_t f[8];
+                const int col0 = hf * C::HC + q;
                 if (t.nb > 0) {
-                    uint32_t r[32];
-                    tmem_ld32(r, tmem + lanes + kOCol + hf * C::HC + q * 32);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        f[i] = __uint_as_float(r[i]);
+                    for (int i = 0; i < 8; ++i)
+                        f[i] = pack2(__uint_as_float(nx[2 * i]), __uint_as_float(nx[2 * i + 1]));
+                    if (q + 16 < C::HC)
+                        tmem_ld16(nx, tmem + lanes + kOCol + col0 + 16);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        f[i] = 0.f;
+                    for (int i = 0; i < 8; ++i)
+                        f[i] = 0;
                 }
                 if (fixes) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         // values that are not finite, for the rows that see them
-                        const int col = hf * C::HC + q * 32 + i;
-                        if (from > T.fix_at[it & 1][0][col])
-                            f[i] = __int_as_float(0x7fffffff);
-                        if (from > T.fix_at[it & 1][1][col])
-                            f[i] += INFINITY;
-                        if (from > T.fix_at[it & 1][2][col])
-                            f[i] -= INFINITY;
+                        float x[2];
+                        unpack2(f[i], x[0], x[1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (from > T.fix_at[it & 1][0][col0 + 2 * i + e])
+                                x[e] = __int_as_float(0x7fffffff);
+                            if (from > T.fix_at[it & 1][1][col0 + 2 * i + e])
+                                x[e] += INFINITY;
+                            if (from > T.fix_at[it & 1][2][col0 + 2 * i + e])
+                                x[e] -= INFINITY;
+                        }
+                        f[i] = pack2(x[0], x[1]);
                     }
                 }
                 if (split > 1) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4 *>(stage + q * 32 + 4 * i) =
-                            make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<ulonglong2 *>(stage + q + 4 * i) = make_ulonglong2(f[2 * i], f[2 * i + 1]);
                     continue;
                 }
                 if (t.nb == 0) {
                     if (mine)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<uint4 *>(o + q * 32)[e] = make_uint4(0, 0, 0, 0);
+                        for (int e = 0; e < 2; ++e)
+                            reinterpret_cast<uint4 *>(o + q)[e] = make_uint4(0, 0, 0, 0);
                     continue;
                 }
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    f[i] = seen > 0 ? f[i] * inv : 0.f;
-                const int col0 = hf * C::HC + q * 32;
                 uint8_t *const line = ring + (n0 + (col0 >> 6)) % C::SLOTS * kSlot + row * 128;
-                uint4 *unit[4];
+                uint4 *unit[2];
+                uint64_t g[2][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 2; ++e) {
                     unit[e] = reinterpret_cast<uint4 *>(line + ((((col0 & 63) / 8 + e) ^ (row & 7)) << 4));
-                if (gated) {
+                    if (gate_smem) {
+                        const uint4 u = *unit[e];
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float g[8];
-                        if (a.gate_f32) {
-                            const float4 *gp = reinterpret_cast<const float4 *>(
-                                static_cast<const float *>(a.gate) + go_ + q * 32 + e * 8);
-                            const float4 u = gp[0], w = gp[1];
-                            g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w;
-                            g[4] = w.x; g[5] = w.y; g[6] = w.z; g[7] = w.w;
-                        } else {
-                            unpack8(*unit[e], g);
+                        for (int i = 0; i < 4; ++i)
+                            g[e][i] = pack2(bf16_lo(w[i]), bf16_hi(w[i]));
+                    } else {
+                        ulonglong2 u = make_ulonglong2(0, 0), w = u;
+                        if (a.gate && mine) {
+                            const ulonglong2 *gp = reinterpret_cast<const ulonglong2 *>(
+                                static_cast<const float *>(a.gate) + go_ + q + e * 8);
+                            u = gp[0];
+                            w = gp[1];
                         }
-                        gate8(f, e * 8, g);
+                        g[e][0] = u.x;
+                        g[e][1] = u.y;
+                        g[e][2] = w.x;
+                        g[e][3] = w.y;
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *unit[e] = pack8(f, e * 8);
+                for (int e = 0; e < 2; ++e) {
+                    uint64_t x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = mul2(f[4 * e + i], inv2);
+                    if (a.gate)
+                        gate4(x, g[e]);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x0, x1;
+                        unpack2(x[i], x0, x1);
+                        w[i] = seen > 0 ? pack_bf16x2(x0, x1) : 0u;
+                    }
+                    *unit[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
             if (t.nb > 0 && split == 1) {
                 n0 += C::CH;
@@ -955,7 +1003,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                             const float g = a.gate_f32
                                                 ? static_cast<const float *>(a.gate)[go_ + i]
                                                 : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.gate)[go_ + i]);
-                            f[i] = __fdividef(f[i], 1.f + __expf(-g));
+                            f[i] *= sigmoid(g);
                         }
                     }
                     *reinterpret_cast<uint2 *>(a.out + orow * a.os.tok + (long long)head * a.os.head + j) =
