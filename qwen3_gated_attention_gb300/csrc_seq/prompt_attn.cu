@@ -829,34 +829,31 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             const bool fixes = go && *(volatile int *)&T.fixes[it & 1] != 0;
             const int from = seen - t.part0 * kN;     // keys seen in the partly seen blocks
             float *const stage = reinterpret_cast<float *>(ring) + row * C::ST + hf * C::HC;
-            // sixteen columns at a time in a rolled loop: this code runs once a tile, and
+            // 32 columns at a time in a rolled loop: this code runs once a tile, and
             // unrolled it costs more in instruction fetches than it computes
             const uint64_t inv2 = pack2(inv, inv);
             const bool gate_smem = a.gate && !a.gate_f32;
-            uint32_t nx[16];
-            if (go && t.nb > 0)
-                tmem_ld16(nx, tmem + lanes + kOCol + hf * C::HC);
 #pragma unroll 1
-            for (int q = 0; q < C::HC; q += 16) {
+            for (int q = 0; q < C::HC; q += 32) {
                 if (!go)
                     continue;
-                uint64_t f[8];
+                uint64_t f[16];
                 const int col0 = hf * C::HC + q;
                 if (t.nb > 0) {
+                    uint32_t nx[32];
+                    tmem_ld32(nx, tmem + lanes + kOCol + col0);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < 16; ++i)
                         f[i] = pack2(__uint_as_float(nx[2 * i]), __uint_as_float(nx[2 * i + 1]));
-                    if (q + 16 < C::HC)
-                        tmem_ld16(nx, tmem + lanes + kOCol + col0 + 16);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < 16; ++i)
                         f[i] = 0;
                 }
                 if (fixes) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         // values that are not finite, for the rows that see them
                         float x[2];
                         unpack2(f[i], x[0], x[1]);
@@ -874,22 +871,22 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                 }
                 if (split > 1) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<ulonglong2 *>(stage + q + 4 * i) = make_ulonglong2(f[2 * i], f[2 * i + 1]);
                     continue;
                 }
                 if (t.nb == 0) {
                     if (mine)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
+                        for (int e = 0; e < 4; ++e)
                             reinterpret_cast<uint4 *>(o + q)[e] = make_uint4(0, 0, 0, 0);
                     continue;
                 }
                 uint8_t *const line = ring + (n0 + (col0 >> 6)) % C::SLOTS * kSlot + row * 128;
-                uint4 *unit[2];
-                uint64_t g[2][4];
+                uint4 *unit[4];
+                uint64_t g[4][4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     unit[e] = reinterpret_cast<uint4 *>(line + ((((col0 & 63) / 8 + e) ^ (row & 7)) << 4));
                     if (gate_smem) {
                         const uint4 u = *unit[e];
@@ -912,7 +909,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     uint64_t x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
