@@ -266,33 +266,39 @@ __device__ __forceinline__ float rcp(float x)
 // 1 / (1 + e^-g)
 __device__ __forceinline__ float sigmoid(float g) { return rcp(1.f + ex2(-1.4426950408889634f * g)); }
 
-// f *= sigmoid(g) for four pairs, a pair with one reciprocal, 1/a = b (1/(a b)): the
-// epilogue is bound by the special function unit.  No branch within, so that the
-// pairs overlap.
-__device__ __forceinline__ void gate4(uint64_t (&f)[4], const uint64_t (&g)[4])
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    float x[8], r[8];
-    bool fits = true;                                // products stay finite; false for NaN
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// f *= sigmoid(g) for eight values, two with one reciprocal, 1/a = b (1/(a b)).  No
+// branch within but for gates below -41 or NaN, so that they overlap.
+__device__ __forceinline__ void gate8(float (&f)[8], const float (&g)[8])
+{
+    float x[8], a[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        unpack2(mul2(g[i], pack2(-1.4426950408889634f, -1.4426950408889634f)), x[2 * i], x[2 * i + 1]);
-        fits = fits && x[2 * i] <= 60.f && x[2 * i + 1] <= 60.f;
+    for (int i = 0; i < 8; ++i) {
+        x[i] = g[i] * -1.4426950408889634f;
+        a[i] = 1.f + ex2(x[i]);
     }
+    // each at most 2^60: the products stay finite
+    const float top = max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])),
+                              max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7])));
+    if (top <= 60.f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a, b;
-        unpack2(add2(pack2(ex2(x[2 * i]), ex2(x[2 * i + 1])), pack2(1.f, 1.f)), a, b);
-        const float ab = rcp(a * b);
-        r[2 * i] = ab * b;
-        r[2 * i + 1] = ab * a;
-    }
-    if (!fits)
+        for (int i = 0; i < 8; i += 2) {
+            const float ab = rcp(a[i] * a[i + 1]);
+            f[i] *= ab * a[i + 1];
+            f[i + 1] *= ab * a[i];
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            r[i] = rcp(1.f + ex2(x[i]));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f[i] = mul2(f[i], pack2(r[2 * i], r[2 * i + 1]));
+            f[i] *= rcp(a[i]);
+    }
 }
 
 template <int D>
@@ -831,48 +837,42 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
             float *const stage = reinterpret_cast<float *>(ring) + row * C::ST + hf * C::HC;
             // 32 columns at a time in a rolled loop: this code runs once a tile, and
             // unrolled it costs more in instruction fetches than it computes
-            const uint64_t inv2 = pack2(inv, inv);
             const bool gate_smem = a.gate && !a.gate_f32;
 #pragma unroll 1
             for (int q = 0; q < C::HC; q += 32) {
                 if (!go)
                     continue;
-                uint64_t f[16];
+                float f[32];
                 const int col0 = hf * C::HC + q;
                 if (t.nb > 0) {
                     uint32_t nx[32];
                     tmem_ld32(nx, tmem + lanes + kOCol + col0);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        f[i] = pack2(__uint_as_float(nx[2 * i]), __uint_as_float(nx[2 * i + 1]));
+                    for (int i = 0; i < 32; ++i)
+                        f[i] = __uint_as_float(nx[i]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        f[i] = 0;
+                    for (int i = 0; i < 32; ++i)
+                        f[i] = 0.f;
                 }
                 if (fixes) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 32; ++i) {
                         // values that are not finite, for the rows that see them
-                        float x[2];
-                        unpack2(f[i], x[0], x[1]);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if (from > T.fix_at[it & 1][0][col0 + 2 * i + e])
-                                x[e] = __int_as_float(0x7fffffff);
-                            if (from > T.fix_at[it & 1][1][col0 + 2 * i + e])
-                                x[e] += INFINITY;
-                            if (from > T.fix_at[it & 1][2][col0 + 2 * i + e])
-                                x[e] -= INFINITY;
-                        }
-                        f[i] = pack2(x[0], x[1]);
+                        if (from > T.fix_at[it & 1][0][col0 + i])
+                            f[i] = __int_as_float(0x7fffffff);
+                        if (from > T.fix_at[it & 1][1][col0 + i])
+                            f[i] += INFINITY;
+                        if (from > T.fix_at[it & 1][2][col0 + i])
+                            f[i] -= INFINITY;
                     }
                 }
                 if (split > 1) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<ulonglong2 *>(stage + q + 4 * i) = make_ulonglong2(f[2 * i], f[2 * i + 1]);
+                        *reinterpret_cast<float4 *>(stage + q + 4 * i) =
+                            make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
                     continue;
                 }
                 if (t.nb == 0) {
@@ -884,7 +884,7 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                 }
                 uint8_t *const line = ring + (n0 + (col0 >> 6)) % C::SLOTS * kSlot + row * 128;
                 uint4 *unit[4];
-                uint64_t g[4][4];
+                float g[4][8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     unit[e] = reinterpret_cast<uint4 *>(line + ((((col0 & 63) / 8 + e) ^ (row & 7)) << 4));
@@ -892,37 +892,34 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                         const uint4 u = *unit[e];
                         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            g[e][i] = pack2(bf16_lo(w[i]), bf16_hi(w[i]));
+                        for (int i = 0; i < 4; ++i) {
+                            g[e][2 * i] = bf16_lo(w[i]);
+                            g[e][2 * i + 1] = bf16_hi(w[i]);
+                        }
                     } else {
-                        ulonglong2 u = make_ulonglong2(0, 0), w = u;
+                        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), w = u;
                         if (a.gate && mine) {
-                            const ulonglong2 *gp = reinterpret_cast<const ulonglong2 *>(
+                            const float4 *gp = reinterpret_cast<const float4 *>(
                                 static_cast<const float *>(a.gate) + go_ + q + e * 8);
                             u = gp[0];
                             w = gp[1];
                         }
-                        g[e][0] = u.x;
-                        g[e][1] = u.y;
-                        g[e][2] = w.x;
-                        g[e][3] = w.y;
+                        g[e][0] = u.x; g[e][1] = u.y; g[e][2] = u.z; g[e][3] = u.w;
+                        g[e][4] = w.x; g[e][5] = w.y; g[e][6] = w.z; g[e][7] = w.w;
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    uint64_t x[4];
+                    float x[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[i] = mul2(f[4 * e + i], inv2);
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = f[8 * e + i] * inv;
                     if (a.gate)
-                        gate4(x, g[e]);
+                        gate8(x, g[e]);
                     uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x0, x1;
-                        unpack2(x[i], x0, x1);
-                        w[i] = seen > 0 ? pack_bf16x2(x0, x1) : 0u;
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = seen > 0 ? pack_bf16x2(x[2 * i], x[2 * i + 1]) : 0u;
                     *unit[e] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
