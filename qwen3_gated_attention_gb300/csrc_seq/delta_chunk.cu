@@ -845,10 +845,8 @@ cudaError_t launch(const DeltaArgs &a, cudaStream_t s)
 template <int DK>
 cudaError_t launch_dk(const DeltaArgs &a, cudaStream_t s)
 {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess)
         return e;
     // columns per CTA: as many as keep every SM busy, since a CTA's helpers do the

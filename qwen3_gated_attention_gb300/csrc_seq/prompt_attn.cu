@@ -1053,10 +1053,8 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
         return e;
     if (!encoder())
         return cudaErrorNotSupported;
-    int dev = 0, sms = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    e = sm_count(&sms);
     if (e != cudaSuccess)
         return e;
     int hp_log2 = 0;

@@ -90,6 +90,24 @@ inline cudaError_t allow_smem(F *fn, int bytes, std::atomic<unsigned long long> 
     return e;
 }
 
+inline cudaError_t sm_count(int *n)
+{
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
+// A plain launch that reports its own status only.
+template <class... K, class... A>
+inline cudaError_t launch_seq(void (*f)(K...), dim3 grid, dim3 block, cudaStream_t s, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, f, static_cast<A &&>(args)...);
+}
+
 cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t s);
 cudaError_t launch_prompt_attn(const PromptAttnArgs &a, cudaStream_t s);
 cudaError_t launch_delta_step(const DeltaArgs &a, cudaStream_t s);
