@@ -16,54 +16,46 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kFly = 4;            // head rows in flight per group of lanes
 
-// Eight elements as they come from memory.
+// Two runs of four elements as they come from memory.
 template <bool F32>
 struct Raw {
-    uint4 u[F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const void *base, long long off)
+    uint32_t w[F32 ? 8 : 4];
+    __device__ __forceinline__ void load(const void *base, long long off0, long long off1)
     {
-        const uint4 *p = F32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + off)
-                             : reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + off);
-        u[0] = __ldcs(p);
-        if (F32)
-            u[F32 ? 1 : 0] = __ldcs(p + 1);
+        if (F32) {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + off0));
+            const uint4 b = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + off1));
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            w[F32 ? 4 : 0] = b.x; w[F32 ? 5 : 1] = b.y; w[F32 ? 6 : 2] = b.z; w[F32 ? 7 : 3] = b.w;
+        } else {
+            const uint2 a = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(base) + off0));
+            const uint2 b = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(base) + off1));
+            w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+        }
     }
     __device__ __forceinline__ void clear()
     {
-        u[0] = make_uint4(0, 0, 0, 0);
-        u[F32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < (F32 ? 8 : 4); ++i)
+            w[i] = 0;
     }
     __device__ __forceinline__ void get(float (&f)[8]) const
     {
-        if (F32) {
-            const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[F32].x, u[F32].y, u[F32].z, u[F32].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = __uint_as_float(w[i]);
-        } else {
-            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = bf16_lo(w[i]);
-                f[2 * i + 1] = bf16_hi(w[i]);
-            }
-        }
+        for (int i = 0; i < 8; ++i)
+            f[i] = F32 ? __uint_as_float(w[F32 ? i : 0]) : i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
     }
 };
 
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8])
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d)
 {
-    uint4 u;
-    u.x = pack_bf16x2(f[0], f[1]);
-    u.y = pack_bf16x2(f[2], f[3]);
-    u.z = pack_bf16x2(f[4], f[5]);
-    u.w = pack_bf16x2(f[6], f[7]);
-    *reinterpret_cast<uint4 *>(p) = u;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
 // A group of d/8 lanes (padded to a power of two) per head row, eight elements a
-// lane.  FAST: rd/2 is a multiple of 8, so a rotary partner is the same element of
-// another lane; otherwise partners meet in shared memory.
+// lane, in two runs of four.  FAST: rd/2 is a multiple of 4; the first rd/8 lanes of
+// a group then take a run from each rotary half, so partners meet in a lane.
+// Otherwise the runs are neighbours and partners meet in shared memory.
 template <bool F32, bool FAST>
 __global__ void __launch_bounds__(kWarps * 32, F32 ? 2 : 3)
 prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
@@ -109,32 +101,30 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
     const int j0 = sub * 8;
     const bool act = j0 < a.d;
     const float inv_d = 1.f / (float)a.d;
-    float cosv[8], sinv[8];
-    Raw<false> wq, wk;
-    wq.clear();
-    wk.clear();
-    if (act) {
-        wq.load(a.q_norm, j0);
-        wk.load(a.k_norm, j0);
+    const bool rot = FAST && j0 < a.rd;
+    const int o0 = rot ? sub * 4 : j0, o1 = rot ? half + sub * 4 : j0 + 4;   // the two runs
+    float wq[8], wk[8], cosv[FAST ? 4 : 8], sinv[FAST ? 4 : 8];
+    {
+        Raw<false> w;
+        w.clear();
+        if (act)
+            w.load(a.q_norm, o0, o1);
+        w.get(wq);
+        if (act)
+            w.load(a.k_norm, o0, o1);
+        w.get(wk);
     }
-    // y cos + partner (-sin or sin); 1 and 0 past the rotary elements
-    int mate = lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int j = j0 + i;
-        if (j < half) {
-            cosv[i] = cs[j].x;
-            sinv[i] = -cs[j].y;
-        } else if (j < a.rd) {
-            cosv[i] = cs[j - half].x;
-            sinv[i] = cs[j - half].y;
+    for (int i = 0; i < (FAST ? 4 : 8); ++i) {
+        const int j = FAST ? o0 + i : j0 + i;
+        if (FAST) {
+            cosv[i] = rot ? cs[j].x : 1.f;
+            sinv[i] = rot ? cs[j].y : 0.f;
         } else {
-            cosv[i] = 1.f;
-            sinv[i] = 0.f;
+            cosv[i] = j < a.rd ? cs[j < half ? j : j - half].x : 1.f;
+            sinv[i] = j < a.rd ? (j < half ? -cs[j].y : cs[j - half].y) : 0.f;
         }
     }
-    if (FAST && j0 < a.rd)
-        mate = j0 < half ? lane + half / 8 : lane - half / 8;
     float *const buf = FAST ? nullptr : swap[warp] + at * lpu * 8;
     const int units = a.H + 2 * a.Hk, step = parts * upw;
     for (int u0 = part * upw + at; u0 - at < units; u0 += kFly * step) {
@@ -147,7 +137,8 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
                 const int kind = u < a.H ? 0 : (u < a.H + a.Hk ? 1 : 2);
                 const RowStride st = kind == 0 ? a.qs : (kind == 1 ? a.ks : a.vs);
                 const int head = kind == 0 ? u : (kind == 1 ? u - a.H : u - a.H - a.Hk);
-                raw[f].load(kind == 0 ? a.q : (kind == 1 ? a.k : a.v), t * st.tok + head * st.head + j0);
+                raw[f].load(kind == 0 ? a.q : (kind == 1 ? a.k : a.v), t * st.tok + head * st.head + o0,
+                            t * st.tok + head * st.head + o1);
             }
         }
 #pragma unroll
@@ -167,43 +158,51 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
                 ss += __shfl_xor_sync(0xffffffffu, ss, o);
             if (kind < 2 || upw > 1) {
                 const float inv = rsqrtf(ss * inv_d + a.eps);
-                float y[8], z[8], w[8];
-                if (kind == 0)
-                    wq.get(w);
-                else
-                    wk.get(w);
+                float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    y[i] = x[i] * (inv * w[i]);
+                    y[i] = x[i] * (inv * (kind == 0 ? wq[i] : wk[i]));
                 if (FAST) {
+                    if (kind < 2) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        z[i] = __shfl_sync(0xffffffffu, y[i], mate);
+                        for (int i = 0; i < 8; ++i)
+                            x[i] = y[i];
+                        if (rot)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                x[i] = y[i] * cosv[i] - y[i + 4] * sinv[i];
+                                x[i + 4] = y[i + 4] * cosv[i] + y[i] * sinv[i];
+                            }
+                    }
                 } else {
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         buf[j0 + i] = y[i];
                     __syncwarp();
+                    if (kind < 2)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int j = j0 + i;
-                        z[i] = j < a.rd ? buf[j < half ? j + half : j - half] : 0.f;
-                    }
+                        for (int i = 0; i < 8; ++i) {
+                            const int j = j0 + i;
+                            x[i] = j < a.rd ? y[i] * cosv[FAST ? 0 : i] +
+                                                  buf[j < half ? j + half : j - half] * sinv[FAST ? 0 : i]
+                                            : y[i];
+                        }
                 }
-                if (kind < 2)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = j0 + i < a.rd ? y[i] * cosv[i] + z[i] * sinv[i] : y[i];
             }
             if (!act || u >= units)
                 continue;
+            __nv_bfloat16 *to;
             if (kind == 0)
-                store8(a.q_out + t * a.os.tok + u * a.os.head + j0, x);
-            else if (ok && kind == 1)
-                store8(a.kc + slot * a.kcb + (u - a.H) * a.kch + p * a.kct + j0, x);
-            else if (ok)
-                store8(a.vc + slot * a.vcb + (u - a.H - a.Hk) * a.vch + p * a.vct + j0, x);
+                to = a.q_out + t * a.os.tok + u * a.os.head;
+            else if (!ok)
+                continue;
+            else if (kind == 1)
+                to = a.kc + slot * a.kcb + (u - a.H) * a.kch + p * a.kct;
+            else
+                to = a.vc + slot * a.vcb + (u - a.H - a.Hk) * a.vch + p * a.vct;
+            store4(to + o0, x[0], x[1], x[2], x[3]);
+            store4(to + o1, x[4], x[5], x[6], x[7]);
         }
     }
 }
@@ -221,7 +220,7 @@ cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t 
     const int parts = (long long)a.sq.total * 2 >= (long long)sms * 32 ? 2 : 8;
     const long long jobs = (long long)a.sq.total * parts;
     const dim3 grid((unsigned)((jobs + kWarps - 1) / kWarps)), block(kWarps * 32);
-    const bool fast = (a.rd / 2) % 8 == 0;
+    const bool fast = (a.rd / 2) % 4 == 0;
     auto *fn = x_f32 ? (fast ? prompt_rows_kernel<true, true> : prompt_rows_kernel<true, false>)
                      : (fast ? prompt_rows_kernel<false, true> : prompt_rows_kernel<false, false>);
     return launch_seq(fn, grid, block, s, a, parts);
