@@ -77,6 +77,11 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
     const bool ok = slot >= 0 && p0 >= 0 && p0 + len <= a.cap;
     if (!ok && lane == 0)
         seq_flag(a.sq, GATTN_STATUS_RANGE);
+    // the row's own place in q, k and v
+    const long long esz = F32 ? 4 : 2;
+    const char *const qrow = static_cast<const char *>(a.q) + t * a.qs.tok * esz;
+    const char *const krow = static_cast<const char *>(a.k) + t * a.ks.tok * esz;
+    const char *const vrow = static_cast<const char *>(a.v) + t * a.vs.tok * esz;
     const int half = a.rd / 2;
     float2 *const cs = table[warp];
     for (int i = lane; i < half; i += 32) {
@@ -126,84 +131,92 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
         }
     }
     float *const buf = FAST ? nullptr : swap[warp] + at * lpu * 8;
-    const int units = a.H + 2 * a.Hk, step = parts * upw;
-    for (int u0 = part * upw + at; u0 - at < units; u0 += kFly * step) {
-        Raw<F32> raw[kFly];
+    const int step = parts * upw, first = part * upw + at;
+    // `heads` head rows from `src` to `dst`, normed and turned by weights w
+    auto normed = [&](const void *src, long long src_head, __nv_bfloat16 *dst, long long dst_head, int heads,
+                      const float (&w)[8]) {
+        long long so = (long long)first * src_head;
+        __nv_bfloat16 *to = dst + (long long)first * dst_head;
+        for (int u0 = first; u0 - at < heads; u0 += kFly * step) {
+            Raw<F32> raw[kFly];
 #pragma unroll
-        for (int f = 0; f < kFly; ++f) {
-            const int u = u0 + f * step;
-            raw[f].clear();
-            if (act && ok && u < units) {
-                const int kind = u < a.H ? 0 : (u < a.H + a.Hk ? 1 : 2);
-                const RowStride st = kind == 0 ? a.qs : (kind == 1 ? a.ks : a.vs);
-                const int head = kind == 0 ? u : (kind == 1 ? u - a.H : u - a.H - a.Hk);
-                raw[f].load(kind == 0 ? a.q : (kind == 1 ? a.k : a.v), t * st.tok + head * st.head + o0,
-                            t * st.tok + head * st.head + o1);
+            for (int f = 0; f < kFly; ++f) {
+                raw[f].clear();
+                if (act && ok && u0 + f * step < heads)
+                    raw[f].load(src, so + o0, so + o1);
+                so += step * src_head;
             }
-        }
 #pragma unroll
-        for (int f = 0; f < kFly; ++f) {
-            const int u = u0 + f * step;
-            if (u - at >= units)               // the whole warp is past the last unit
-                break;
-            const int kind = u < a.H ? 0 : (u < a.H + a.Hk ? 1 : 2);
-            float x[8];
-            raw[f].get(x);
-            // (values come along so that every lane meets the shuffles)
-            float ss = 0.f;
+            for (int f = 0; f < kFly; ++f, to += step * dst_head) {
+                const int u = u0 + f * step;
+                if (u - at >= heads)           // the whole warp is past the last one
+                    continue;
+                float x[8], y[8];
+                raw[f].get(x);
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                ss = fmaf(x[i], x[i], ss);
-            for (int o = lpu / 2; o; o >>= 1)
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (kind < 2 || upw > 1) {
-                const float inv = rsqrtf(ss * inv_d + a.eps);
-                float y[8];
+                for (int i = 0; i < 8; i += 2) {
+                    s0 = fmaf(x[i], x[i], s0);
+                    s1 = fmaf(x[i + 1], x[i + 1], s1);
+                }
+                float ss = s0 + s1;
+                for (int o = lpu / 2; o; o >>= 1)
+                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float inv = ok ? rsqrtf(ss * inv_d + a.eps) : 0.f;   // skipped rows: zeros
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    y[i] = x[i] * (inv * (kind == 0 ? wq[i] : wk[i]));
+                    y[i] = x[i] * (inv * w[i]);
                 if (FAST) {
-                    if (kind < 2) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            x[i] = y[i];
-                        if (rot)
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = y[i];
+                    if (rot)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                x[i] = y[i] * cosv[i] - y[i + 4] * sinv[i];
-                                x[i + 4] = y[i + 4] * cosv[i] + y[i] * sinv[i];
-                            }
-                    }
+                        for (int i = 0; i < 4; ++i) {
+                            x[i] = y[i] * cosv[i] - y[i + 4] * sinv[i];
+                            x[i + 4] = y[i + 4] * cosv[i] + y[i] * sinv[i];
+                        }
                 } else {
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         buf[j0 + i] = y[i];
                     __syncwarp();
-                    if (kind < 2)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int j = j0 + i;
-                            x[i] = j < a.rd ? y[i] * cosv[FAST ? 0 : i] +
-                                                  buf[j < half ? j + half : j - half] * sinv[FAST ? 0 : i]
-                                            : y[i];
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        const int j = j0 + i;
+                        x[i] = j < a.rd ? y[i] * cosv[FAST ? 0 : i] +
+                                              buf[j < half ? j + half : j - half] * sinv[FAST ? 0 : i]
+                                        : y[i];
+                    }
+                }
+                if (act && u < heads) {
+                    store4(to + o0, x[0], x[1], x[2], x[3]);
+                    store4(to + o1, x[4], x[5], x[6], x[7]);
                 }
             }
-            if (!act || u >= units)
-                continue;
-            __nv_bfloat16 *to;
-            if (kind == 0)
-                to = a.q_out + t * a.os.tok + u * a.os.head;
-            else if (!ok)
-                continue;
-            else if (kind == 1)
-                to = a.kc + slot * a.kcb + (u - a.H) * a.kch + p * a.kct;
-            else
-                to = a.vc + slot * a.vcb + (u - a.H - a.Hk) * a.vch + p * a.vct;
-            store4(to + o0, x[0], x[1], x[2], x[3]);
-            store4(to + o1, x[4], x[5], x[6], x[7]);
         }
+    };
+    normed(qrow, a.qs.head, a.q_out + t * a.os.tok, a.os.head, a.H, wq);
+    if (!ok)
+        return;
+    normed(krow, a.ks.head, a.kc + slot * a.kcb + p * a.kct, a.kch, a.Hk, wk);
+    __nv_bfloat16 *const vc = a.vc + slot * a.vcb + p * a.vct;
+    for (int u0 = first; u0 < a.Hk; u0 += kFly * step) {
+        Raw<F32> raw[kFly];
+#pragma unroll
+        for (int f = 0; f < kFly; ++f)
+            if (act && u0 + f * step < a.Hk)
+                raw[f].load(vrow, (u0 + f * step) * a.vs.head + j0, (u0 + f * step) * a.vs.head + j0 + 4);
+#pragma unroll
+        for (int f = 0; f < kFly; ++f)
+            if (act && u0 + f * step < a.Hk) {
+                float x[8];
+                raw[f].get(x);
+                __nv_bfloat16 *to = vc + (u0 + f * step) * a.vch + j0;
+                store4(to, x[0], x[1], x[2], x[3]);
+                store4(to + 4, x[4], x[5], x[6], x[7]);
+            }
     }
 }
 

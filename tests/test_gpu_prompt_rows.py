@@ -136,6 +136,16 @@ def test_sequences_outside_the_cache_are_skipped(past, slots, skipped):
     assert int(status) == 1
 
 
+def test_skipped_rows_are_zero_without_epsilon():
+    c = _case(4, 2, 64, [8, 2], [0, -3], 16, BF, 0.5, 5)
+    y, kc, vc = c["y"].cuda(), c["kc"].cuda(), c["vc"].cuda()
+    q, k, v = _split(c, y)
+    out = _dev().prompt_rows(q, k, v, c["qn"].cuda(), c["kn"].cuda(), kc, vc, cu_of(c["lens"], "cuda"),
+                             torch.tensor(c["past"], dtype=torch.int32, device="cuda"),
+                             partial_rotary_factor=0.5, rope_theta=THETA, rms_eps=0.0)
+    assert (out[8:] == 0).all() and out[:8].isfinite().all() and (out[:8] != 0).any()
+
+
 def test_many_sequences():
     lens = [(7 * i) % 5 for i in range(1500)]
     c = _case(2, 1, 64, lens, [i % 3 for i in range(1500)], 16, BF, 0.25, 4)
