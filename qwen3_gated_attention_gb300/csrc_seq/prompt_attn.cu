@@ -93,73 +93,83 @@ struct Cfg {
     static_assert(kOCol + D <= kCols, "TMEM");
 };
 
-// What the order of the tiles needs of a sequence.
+// What the order of the tiles needs of a sequence.  All of it fits 32 bits: counts of
+// rows.  A tile of a pair has tp = 1 << tl tokens.
 struct SeqKeys {
-    int r0, len, slot;
-    long long past, kv0;        // keys before its first row; its first key row
+    int r0, len, slot, kv0;
+    int past;                   // keys before its first row (negative: rows that see none)
     bool ok;
-    __device__ __forceinline__ int tiles(int tp) const { return (len + tp - 1) / tp; }
-    // tiles with at least x key blocks (x >= 1), the last ones
-    __device__ __forceinline__ int at_least(int x, int tp) const
+    __device__ __forceinline__ int tiles(int tl) const { return (len + (1 << tl) - 1) >> tl; }
+    // key blocks of its last tile
+    __device__ __forceinline__ int most() const { return past + len > 0 ? (past + len + kN - 1) / kN : 0; }
+    // tiles with at least x key blocks: the last ones
+    __device__ __forceinline__ int at_least(int x, int tl) const
     {
-        if (len == 0)
+        const int n = tiles(tl);
+        if (x == 0 || n == 0)
+            return n;
+        const int need = (x - 1) * kN + 1 - past;       // tokens that reach x blocks
+        if (len < need)
             return 0;
-        if (x == 0)
-            return tiles(tp);
-        const long long need = (long long)(x - 1) * kN + 1 - past;
-        if (!ok || len < need)
-            return 0;
-        const int below = need <= 0 ? 0 : (int)((need + tp - 1) / tp) - 1;
-        return tiles(tp) - min(below, tiles(tp) - 1);
-    }
-    __device__ __forceinline__ int most() const
-    {
-        return ok && len > 0 && past + len > 0 ? (int)((past + len + kN - 1) / kN) : 0;
+        return n - min(need <= 0 ? 0 : ((need + (1 << tl) - 1) >> tl) - 1, n - 1);
     }
 };
 
 __device__ __forceinline__ SeqKeys seq_keys(const PromptAttnArgs &a, int s)
 {
     SeqKeys q;
-    seq_rows(a.sq, s, q.r0, q.len);
-    q.kv0 = 0;
+    long long past, kv0 = 0;
     q.slot = 0;
     if (a.pos) {
+        seq_rows(a.sq, s, q.r0, q.len);
         q.slot = a.sq.slots ? a.sq.slots[s] : s;
-        q.past = a.pos[s];
-        q.ok = q.slot >= 0 && q.slot < a.kv_batch && q.past >= 0 && q.past + q.len <= a.kv_rows;
+        past = a.pos[s];
+        q.ok = q.slot >= 0 && q.slot < a.kv_batch && past >= 0 && past + q.len <= a.kv_rows;
     } else {
-        q.kv0 = a.cu_kv[s];
+        kv0 = a.cu_kv[s];
         const long long kv1 = a.cu_kv[s + 1];
-        q.past = kv1 - q.kv0 - q.len;
-        q.ok = q.kv0 >= 0 && kv1 >= q.kv0 && kv1 <= a.kv_rows;
+        seq_rows(a.sq, s, q.r0, q.len);
+        past = kv1 - kv0 - q.len;
+        q.ok = kv0 >= 0 && kv1 >= kv0 && kv1 <= a.kv_rows;
     }
+    q.past = q.ok ? (int)past : -(1 << 30);             // a skipped sequence sees nothing
+    q.kv0 = (int)kv0;
     return q;
 }
 
 // Deals the tiles out by rank; called by one whole warp with rising ranks.
 struct Dealer {
     SeqKeys mine;               // up to 32 sequences: the lane's own
-    int base = 0;               // more: the lane's sequences are base + lane, ...
-    long long before = 0;       // ... with this many tiles before them
+    int base;                   // more: the lane's sequences are base + lane, ...
+    int before;                 // ... with this many tiles before them
 
+    __device__ __forceinline__ void start(const PromptAttnArgs &a)
+    {
+        base = before = 0;
+        mine = seq_keys(a, min((int)(threadIdx.x & 31), a.sq.n - 1));
+        if ((threadIdx.x & 31) >= a.sq.n)
+            mine.len = 0;
+    }
     // Sequence and level (tile within it) of the rank-th tile; false: none.  Up to
     // 32 sequences in order of falling key blocks, more in their own order.
-    __device__ __noinline__ bool find(const PromptAttnArgs &a, int tp, long long rank, bool first, SeqKeys &q, int &s,
-                         int &level)
+    __device__ __forceinline__ bool find(const PromptAttnArgs &a, int tl, int rank, SeqKeys &q, int &s, int &level)
     {
         const int lane = threadIdx.x & 31, n = a.sq.n;
         const unsigned all = 0xffffffffu;
-        if (n <= 32) {
-            if (first) {
-                mine = seq_keys(a, min(lane, n - 1));
-                if (lane >= n)
-                    mine.len = 0;
+        auto scan = [&](int c) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(all, c, o);
+                if (lane >= o)
+                    c += x;
             }
-            auto count = [&](int x) { return (long long)__reduce_add_sync(all, mine.at_least(x, tp)); };
+            return c;
+        };
+        if (n <= 32) {
+            auto count = [&](int x) { return (int)__reduce_add_sync(all, mine.at_least(x, tl)); };
             if (rank >= count(0))
                 return false;
-            int lo = 0, hi = __reduce_max_sync(all, mine.most());   // count(lo) > rank
+            int lo = 0, hi = __reduce_max_sync(all, mine.len > 0 ? mine.most() : 0);   // count(lo) > rank
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (count(mid) > rank)
@@ -167,49 +177,39 @@ struct Dealer {
                 else
                     hi = mid - 1;
             }
-            const int idx = (int)(rank - count(lo + 1));
             // tiles of exactly lo blocks, by lane
-            const int c = mine.at_least(lo, tp) - mine.at_least(lo + 1, tp);
-            int sum = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(all, sum, o);
-                if (lane >= o)
-                    sum += x;
-            }
-            const int l = __ffs(__ballot_sync(all, idx < sum)) - 1;
-            level = __shfl_sync(all, mine.tiles(tp) - mine.at_least(lo, tp) + idx - (sum - c), l);
-            s = l;
-        } else {
-            for (;;) {
-                if (base >= n)
-                    return false;
-                int r0, len = 0;
-                if (base + lane < n)
-                    seq_rows(a.sq, base + lane, r0, len);
-                const int c = (len + tp - 1) / tp;
-                int sum = c;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int x = __shfl_up_sync(all, sum, o);
-                    if (lane >= o)
-                        sum += x;
-                }
-                const int total = __shfl_sync(all, sum, 31);
-                if (rank - before < total) {
-                    const int idx = (int)(rank - before);
-                    const int l = __ffs(__ballot_sync(all, idx < sum)) - 1;
-                    // its longest rows first
-                    level = __shfl_sync(all, sum - 1 - idx, l);
-                    s = base + l;
-                    break;
-                }
-                before += total;
-                base += 32;
-            }
+            const int over = mine.at_least(lo + 1, tl), here = mine.at_least(lo, tl);
+            const int idx = rank - (int)__reduce_add_sync(all, over);
+            const int sum = scan(here - over);
+            s = __ffs(__ballot_sync(all, idx < sum)) - 1;
+            level = __shfl_sync(all, mine.tiles(tl) - here + idx - (sum - (here - over)), s);
+            q.r0 = __shfl_sync(all, mine.r0, s);
+            q.len = __shfl_sync(all, mine.len, s);
+            q.slot = __shfl_sync(all, mine.slot, s);
+            q.kv0 = __shfl_sync(all, mine.kv0, s);
+            q.past = __shfl_sync(all, mine.past, s);
+            q.ok = __shfl_sync(all, (int)mine.ok, s);
+            return true;
         }
-        q = seq_keys(a, s);
-        return true;
+        for (;;) {
+            if (base >= n)
+                return false;
+            int r0, len = 0;
+            if (base + lane < n)
+                seq_rows(a.sq, base + lane, r0, len);
+            const int sum = scan((len + (1 << tl) - 1) >> tl);
+            const int total = __shfl_sync(all, sum, 31);
+            if (rank - before < total) {
+                const int idx = rank - before;
+                const int l = __ffs(__ballot_sync(all, idx < sum)) - 1;
+                level = __shfl_sync(all, sum - 1 - idx, l);     // its longest rows first
+                s = base + l;
+                q = seq_keys(a, s);
+                return true;
+            }
+            before += total;
+            base += 32;
+        }
     }
 };
 
@@ -350,13 +350,9 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
         for (int i = lane; i < 2 * 3 * D; i += 32)
             (&T.fix_at[0][0][0])[i] = 0xFFFF;
     }
-    // tiles are dealt round by round, every other round backwards, so that nobody
-    // keeps getting the longer ones; the first is looked for while the CTAs meet
-    const long long clusters = gridDim.x / (2 * split), place = blockIdx.x / (2 * split);
     Dealer deal;
-    SeqKeys q;
-    int seq = -1, level = 0;
-    bool some = warp == 11 && deal.find(a, 2 * tpt, place / groups, true, q, seq, level);
+    if (warp == 11)
+        deal.start(a);                                 // its loads pass while the CTAs meet
     tc5_fence_before();
     __syncthreads();
     cluster_sync();
@@ -373,32 +369,34 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
 
     if (warp == 11) {
         // ------------------------------------------------------------- tiles
-        const int tp = 2 * tpt;
+        // dealt round by round, every other round backwards, so that nobody keeps
+        // getting the longer ones
+        const int tl = 8 - hp_log2, clusters = gridDim.x / (2 * split), place = blockIdx.x / (2 * split);
         for (int it = 0;; ++it) {
-            const long long r = it * clusters + (it & 1 ? clusters - 1 - place : place);
-            if (it > 0)
-                some = split == 1 && deal.find(a, tp, r / groups, false, q, seq, level);
+            const unsigned r = (unsigned)it * clusters + (it & 1 ? clusters - 1 - place : place);
+            const int group = r % (unsigned)groups;
+            SeqKeys q;
+            Tile t;
+            const bool some = (split == 1 || it == 0) && r < 0x80000000u &&
+                              deal.find(a, tl, r / (unsigned)groups, q, t.s, t.level);
             if (it >= 2 && !__all_sync(0xffffffffu, tc5_wait(&T.t_empty[it & 1], ((it >> 1) - 1) & 1, abort)))
                 break;
-            Tile t;
-            t.s = seq;
-            t.level = level;
             if (some) {
-                const int tok0 = t.level * tp;
-                const long long last = q.ok ? q.past + min(q.len, tok0 + tp) : 0;
-                const int nb = last > 0 ? (int)((last + kN - 1) / kN) : 0;
-                const int each = (nb + split - 1) / split;
+                const int tok0 = t.level << tl;
+                const int last = q.past + min(q.len, tok0 + (1 << tl));
+                const int nb = last > 0 ? (last + kN - 1) / kN : 0;
+                const int each = split == 1 ? nb : split == 2 ? (nb + 1) >> 1 : (nb + 3) >> 2;
                 t.b0 = min(nb, share * each);
                 t.nb = min(nb, t.b0 + each) - t.b0;
-                const long long seen = q.past + tok0 + 1;
-                t.part0 = seen > 0 ? (int)(seen / kN) : 0;
+                const int seen = q.past + tok0 + 1;
+                t.part0 = seen > 0 ? seen / kN : 0;
                 t.row0 = q.r0 + tok0 + (int)half * tpt;
                 t.rows = max(0, min(tpt, q.len - tok0 - (int)half * tpt));
                 t.slot = q.slot;
-                t.kv0 = (int)q.kv0;
-                t.seen0 = q.ok ? (int)(seen + half * tpt) : -(1 << 30);
+                t.kv0 = q.kv0;
+                t.seen0 = seen + (int)half * tpt;
                 // the group of heads, beside the level
-                t.level = (int)(r % groups);
+                t.level = group;
                 if (!q.ok && lane == 0)
                     seq_flag(a.sq, GATTN_STATUS_RANGE);
             } else {
@@ -1087,7 +1085,7 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     while (split < 4 && tiles * 2 * split < sms && most / (2 * split) >= 512)
         split *= 2;
     const long long clusters = split == 1 ? std::min<long long>(tiles, sms / 2) : tiles;
-    if (clusters * 2 * split > 0x7fffffff)
+    if (tiles * 2 * split > 0x7fffffff)
         return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
