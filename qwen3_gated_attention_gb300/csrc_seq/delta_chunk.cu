@@ -7,11 +7,11 @@
 //   O = diag(a) Q S + A W,  A_ij = e^{G_i - G_j} q_i.k_j  (j <= i),
 //   S <- e^{G_C} S + K^T diag(e^{G_C - G_j}) W.
 // T and A depend on the rows alone, so helper warps prepare them (and the
-// tiles) up to four chunks ahead; what is serial is the chain over S.  The columns
+// tiles) four to six chunks ahead; what is serial is the chain over S.  The columns
 // of S are independent: a chain warp owns 16 of them and keeps S^T [16][k_dim] in
-// fp32 accumulator registers.  Every product takes its left operand from
-// registers that the product before it left there (S^T K^T, Y^T T^T, W^T K), so
-// the chain needs no shared memory of its own and no barrier between warps.
+// fp32 accumulator registers (with 32 columns a CTA, two warps with half of k_dim
+// each).  Every product takes its left operand from registers that the product
+// before it left there (S^T K^T, Y^T T^T, W^T K).
 //
 // Precision: the tensor cores multiply 16-bit floats.  K and Q rows are bf16 and
 // become fp16 exactly up to a power of two per row; S, Y, W, T and A are split
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kC = 32;             // rows of a chunk
 constexpr int kTS = 40;            // row stride of T and A (halves): conflict-free ldmatrix
-constexpr int kLS = 20;            // row stride of L's diagonal blocks (floats)
+constexpr int kLS = 16;            // row stride of L's diagonal blocks (floats)
 constexpr float kMinG = -200.f;    // e^-200 is 0 in fp32
 
 // Every array starts on a 16-byte boundary: they are read in 16-byte vectors.
@@ -47,28 +47,29 @@ struct alignas(16) Stage {
     alignas(16) float a[kC];
     alignas(16) float sq[kC];
     // the helper's own
-    alignas(16) float lt[kC][kLS];                 // diagonal blocks of L^T: [j][i % 16]
+    alignas(16) float lt[kC][kLS];                 // diagonal blocks of L^T: [j][i - j - 1]
     alignas(16) float gh[kC];
     alignas(16) float gl[kC];
     alignas(16) float r[kC];
-    alignas(16) float kk[kC];
-    alignas(16) float qq[kC];
     float gamma, vtop;                             // decay of the chunk; largest |v|
     int lo, hi, more;                              // rows of the chunk this is for; more of it follow
 };
 
-// The warps of a CTA: NCW chain warps, with two of them as many output warps (the
-// serial chain then carries K S and the state's update only), and helper warps
-// with a stage each.
+// The warps of a CTA: a chain warp per 16 of its NCW * 16 state columns, and helper
+// warps with a stage each.  With two such groups of columns the serial chain gets
+// all that shortens it: two warps per group, half of the state's rows each, that
+// add up their shares of K S, and an output warp per group for Q S and A W.
 template <int NCW>
 struct Roles {
     static constexpr bool SPLIT = NCW == 2;
+    static constexpr int KH = SPLIT ? 2 : 1;       // chain warps per group of columns
+    static constexpr int CHAIN = NCW * KH;
     static constexpr int OUT = SPLIT ? NCW : 0;
     static constexpr int HELP = SPLIT ? 6 : 4;
-    static constexpr int THREADS = (NCW + OUT + HELP) * 32;
+    static constexpr int THREADS = (CHAIN + OUT + HELP) * 32;
 };
 
-// What a chain warp hands its output warp: S in parts, as operands, and W.
+// What chain warps hand their output warp: S in parts, as operands, and W.
 template <int DK>
 struct alignas(16) Handed {
     uint4 s[DK / 16][2][32];
@@ -76,14 +77,21 @@ struct alignas(16) Handed {
     float2 unit[32];
 };
 
+// What a chain warp hands the other one of its columns: its share of K S and of the
+// columns' largest elements.
+struct alignas(16) Share {
+    float4 x[4][32];
+    float2 top[32];
+};
+
 template <int DK, int NCW>
 struct alignas(16) Shared {
     using R = Roles<NCW>;
     Stage<DK, NCW> st[R::HELP];
-    alignas(16) __nv_bfloat16 o[NCW][kC][24];      // a chain warp's rows of the output
     Handed<DK> to[R::SPLIT ? NCW : 1];
+    Share share[R::SPLIT ? NCW : 1][R::KH];
     uint64_t full[R::HELP], empty[R::HELP];
-    uint64_t s_full[2], w_full[2], taken[2];
+    uint64_t s_full[2], w_full[2], taken[2], shared[2][2], read[2][2];
     int abort;
 };
 static_assert((kTS * 2) % 16 == 0 && (kLS * 4) % 16 == 0 && sizeof(Stage<128, 2>) % 16 == 0 &&
@@ -150,22 +158,35 @@ __device__ __forceinline__ unsigned row_top(const void *row)
     return max(top & 0xFFFFu, top >> 16);
 }
 
-// One row of bf16 in shared memory becomes fp16 with the row's largest element
-// brought to [1, 2): returns the power of two taken out.  A lane per row.
+// A bf16 row of K and one of Q in shared memory become fp16 with their largest
+// elements brought to [1, 2): returns the powers of two taken out and the rows' sums
+// of squares in their units.  A lane per pair of rows; topk, topq: the largest
+// magnitudes.
 template <int DK>
-__device__ __forceinline__ float row_to_half(__half *row, unsigned top)
+__device__ __forceinline__ float4 rows_to_half(__half *krow, __half *qrow, unsigned topk, unsigned topq)
 {
-    uint4 *p = reinterpret_cast<uint4 *>(row);
-    int e = (int)(top >> 7);
-    e = e == 255 ? 127 : min(max(e, 1), 253);     // infinities and NaN pass as they are
-    const float f = __int_as_float((254 - e) << 23);
-#pragma unroll 2
+    uint4 *kp = reinterpret_cast<uint4 *>(krow), *qp = reinterpret_cast<uint4 *>(qrow);
+    int ek = (int)(topk >> 7), eq = (int)(topq >> 7);
+    ek = ek == 255 ? 127 : min(max(ek, 1), 253);     // infinities and NaN pass as they are
+    eq = eq == 255 ? 127 : min(max(eq, 1), 253);
+    const float fk = __int_as_float((254 - ek) << 23), fq = __int_as_float((254 - eq) << 23);
+    float kk[2] = {0.f, 0.f}, qq[2] = {0.f, 0.f};
+    auto half_pair = [](uint32_t u, float f, float (&sum)[2]) {
+        const uint32_t h = pack_h2(bf16_lo(u) * f, bf16_hi(u) * f);
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        sum[0] = fmaf(x.x, x.x, sum[0]);
+        sum[1] = fmaf(x.y, x.y, sum[1]);
+        return h;
+    };
+#pragma unroll 1
     for (int i = 0; i < DK / 8; ++i) {
-        const uint4 u = p[i];
-        p[i] = make_uint4(pack_h2(bf16_lo(u.x) * f, bf16_hi(u.x) * f), pack_h2(bf16_lo(u.y) * f, bf16_hi(u.y) * f),
-                          pack_h2(bf16_lo(u.z) * f, bf16_hi(u.z) * f), pack_h2(bf16_lo(u.w) * f, bf16_hi(u.w) * f));
+        const uint4 u = kp[i], w = qp[i];
+        kp[i] = make_uint4(half_pair(u.x, fk, kk), half_pair(u.y, fk, kk), half_pair(u.z, fk, kk),
+                           half_pair(u.w, fk, kk));
+        qp[i] = make_uint4(half_pair(w.x, fq, qq), half_pair(w.y, fq, qq), half_pair(w.z, fq, qq),
+                           half_pair(w.w, fq, qq));
     }
-    return __int_as_float(e << 23);
+    return make_float4(__int_as_float(ek << 23), __int_as_float(eq << 23), kk[0] + kk[1], qq[0] + qq[1]);
 }
 
 // Everything of rows [lo, hi) of the chunk at t0 that does not depend on the
@@ -201,20 +222,21 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     const float beta = on ? a.beta[(long long)(t0 + lane) * a.bt + h] : 0.f;
     float gr = on ? a.g[(long long)(t0 + lane) * a.gt + h] : 0.f;
     gr = gr < kMinG ? kMinG : gr;
-    // the sums in double and in units of log2 e, then as a float pair: differences
-    // of far sums stay exact
-    double G = (double)gr * 1.4426950408889634;
+    // the sums in units of log2 e and as float pairs: differences of far sums stay exact
+    float gh = gr * 1.44269502f, gl = fmaf(gr, 1.44269502f, -gh) + gr * 1.92596299e-8f;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, G, o);
-        if (lane >= o)
-            G += x;
+        const float h2 = __shfl_up_sync(0xffffffffu, gh, o), l2 = __shfl_up_sync(0xffffffffu, gl, o);
+        if (lane >= o) {
+            const float sum = gh + h2, b = sum - gh;
+            gl += l2 + ((gh - (sum - b)) + (h2 - b));
+            gh = sum;
+        }
     }
-    const double Gc = __shfl_sync(0xffffffffu, G, 31);
-    const float gh = (float)G, gl = (float)(G - (double)gh);
+    const float gch = __shfl_sync(0xffffffffu, gh, 31), gcl = __shfl_sync(0xffffffffu, gl, 31);
     s.gh[lane] = gh;
     s.gl[lane] = gl;
-    const float ai = ex2(gh), ci = ex2((float)(Gc - G));
+    const float ai = ex2(gh + gl), ci = ex2((gch - gh) + (gcl - gl));
     cp_async_wait_all();
     __syncwarp();
     const unsigned topk = row_top<KU>(&s.k[lane][0]);
@@ -225,45 +247,10 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     const unsigned bads = __ballot_sync(0xffffffffu, bad);
     if (bads)
         return __ffs(bads) - 1;
-    const float ek = row_to_half<DK>(&s.k[lane][0], topk);
-    const float eq = row_to_half<DK>(&s.q[lane][0], row_top<KU>(&s.q[lane][0]));
-    __syncwarp();
-
-    // K K^T, K Q^T (row j, column i >= j) and the diagonal blocks of Q Q^T
-    float kk[2][4][4] = {}, kq[2][4][4] = {}, qq[2][2][4] = {};
-    const int ar = (lane & 7) + ((lane >> 3) & 1) * 8, ac = (lane >> 4) * 8;
-#pragma unroll 1
-    for (int ks = 0; ks < DK / 16; ++ks) {
-        uint32_t fk[2][4], fq[2][4];
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            ldsm_x4(fk[mt], smem_u32(&s.k[mt * 16 + ar][ks * 16 + ac]));
-            ldsm_x4(fq[mt], smem_u32(&s.q[mt * 16 + ar][ks * 16 + ac]));
-        }
-        // the A fragment of 16 rows holds the B fragments of its two 8-row halves
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int nt = 2 * mt; nt < 4; ++nt) {
-                mma(kk[mt][nt], fk[mt], fk[nt / 2][nt & 1], fk[nt / 2][(nt & 1) + 2]);
-                mma(kq[mt][nt], fk[mt], fq[nt / 2][nt & 1], fq[nt / 2][(nt & 1) + 2]);
-                if (nt / 2 == mt)
-                    mma(qq[mt][nt & 1], fq[mt], fq[mt][nt & 1], fq[mt][(nt & 1) + 2]);
-            }
-    }
-    // squared norms: the diagonals
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (g == 2 * t + (e & 1)) {
-                s.kk[mt * 16 + g + (e >> 1) * 8] = kk[mt][2 * mt + (e >> 1)][e];
-                s.qq[mt * 16 + g + (e >> 1) * 8] = qq[mt][e >> 1][e];
-            }
-    __syncwarp();
+    const float4 row = rows_to_half<DK>(&s.k[lane][0], &s.q[lane][0], topk, row_top<KU>(&s.q[lane][0]));
     // k = K 2^e / sqrt(sum + eps): in units of the stored row
-    const float r = !on ? 0.f : a.l2norm ? rsqrtf(s.kk[lane] + a.l2_eps / (ek * ek)) : ek;
-    const float rq = !on ? 0.f : a.l2norm ? rsqrtf(s.qq[lane] + a.l2_eps / (eq * eq)) : eq;
+    const float r = !on ? 0.f : a.l2norm ? rsqrtf(row.z + a.l2_eps / (row.x * row.x)) : row.x;
+    const float rq = !on ? 0.f : a.l2norm ? rsqrtf(row.w + a.l2_eps / (row.y * row.y)) : row.y;
     s.r[lane] = r;
     s.beta[lane] = beta;
     s.a[lane] = ai;
@@ -276,44 +263,64 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
         s.vtop = __uint_as_float(vtop << 16);
     }
     __syncwarp();
-    float2 ghi[4], gli[4], rb[4];
+    // The 16 x 8 tiles of K K^T and K Q^T (row j, column i) that hold some i >= j, and
+    // from each its part of L and of A.  A loop that stays rolled: with it the code of
+    // all roles stays small enough for the SM's instruction cache
+    uint32_t bh[2][2], bl[2][2];       // L of rows 16-31, columns 0-15, as a B operand
+    const int ar = (lane & 7) + ((lane >> 3) & 1) * 8, ac = (lane >> 4) * 8;
+    const __half *brow = (lane < 16 ? &s.k[0][0] : &s.q[0][0]) + (lane & 7) * (DK + 8) + ((lane >> 3) & 1) * 8;
+#pragma unroll 1
+    for (int tile = 0; tile < 6; ++tile) {
+        const int mt = tile >> 2, nt = tile - 2 * mt;
+        float kk[4] = {}, kq[4] = {};
+        const uint32_t pa = smem_u32(&s.k[mt * 16 + ar][ac]), pb = smem_u32(brow + nt * 8 * (DK + 8));
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
+        for (int ks = 0; ks < DK / 16; ++ks) {
+            uint32_t fa[4], fb[4];
+            ldsm_x4(fa, pa + ks * 32);
+            ldsm_x4(fb, pb + ks * 32);
+            mma(kk, fa, fb[0], fb[1]);
+            mma(kq, fa, fb[2], fb[3]);
+        }
         const int i0 = nt * 8 + 2 * t;
-        ghi[nt] = *reinterpret_cast<const float2 *>(&s.gh[i0]);
-        gli[nt] = *reinterpret_cast<const float2 *>(&s.gl[i0]);
+        const float2 ghi = *reinterpret_cast<const float2 *>(&s.gh[i0]);
+        const float2 gli = *reinterpret_cast<const float2 *>(&s.gl[i0]);
         const float2 ri = *reinterpret_cast<const float2 *>(&s.r[i0]);
         const float2 bi = *reinterpret_cast<const float2 *>(&s.beta[i0]);
-        rb[nt] = make_float2(ri.x * bi.x, ri.y * bi.y);
-    }
-    uint32_t bh[2][2], bl[2][2];       // L of rows 16-31, columns 0-15, as a B operand
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+        uint32_t vh[2], vl[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int j = mt * 16 + g + half * 8;
             const float rj = s.r[j], ghj = s.gh[j], glj = s.gl[j];
-#pragma unroll
-            for (int nt = 2 * mt; nt < 4; ++nt) {
-                const int i0 = nt * 8 + 2 * t;
-                const float d0 = i0 >= j ? ex2((ghi[nt].x - ghj) + (gli[nt].x - glj)) * rj : 0.f;
-                const float d1 = i0 + 1 >= j ? ex2((ghi[nt].y - ghj) + (gli[nt].y - glj)) * rj : 0.f;
-                const float l0 = i0 > j ? d0 * rb[nt].x * kk[mt][nt][half * 2] : 0.f;
-                const float l1 = i0 + 1 > j ? d1 * rb[nt].y * kk[mt][nt][half * 2 + 1] : 0.f;
-                if (nt / 2 == mt)
-                    *reinterpret_cast<float2 *>(&s.lt[j][i0 - mt * 16]) = make_float2(l0, l1);
-                else
-                    split_h2(l0, l1, bh[half][nt & 1], bl[half][nt & 1]);
-                uint32_t wh, wl;
-                split_h2(i0 >= j ? d0 * kq[mt][nt][half * 2] : 0.f,
-                         i0 + 1 >= j ? d1 * kq[mt][nt][half * 2 + 1] : 0.f, wh, wl);
-                *reinterpret_cast<uint32_t *>(&s.a_hi[j][i0]) = wh;
-                *reinterpret_cast<uint32_t *>(&s.a_lo[j][i0]) = wl;
-            }
+            const float d0 = i0 >= j ? ex2((ghi.x - ghj) + (gli.x - glj)) * rj : 0.f;
+            const float d1 = i0 + 1 >= j ? ex2((ghi.y - ghj) + (gli.y - glj)) * rj : 0.f;
+            const float l0 = d0 * (ri.x * bi.x) * kk[half * 2];
+            const float l1 = d1 * (ri.y * bi.y) * kk[half * 2 + 1];
+            if (tile != 2 && tile != 3) {      // a diagonal block's: column j from its row j + 1 on
+                float *lt = &s.lt[j][i0 - j - 1];
+                if (i0 > j)
+                    lt[0] = l0;
+                if (i0 + 1 > j)
+                    lt[1] = l1;
+            } else
+                split_h2(l0, l1, vh[half], vl[half]);
+            uint32_t wh, wl;
+            split_h2(i0 >= j ? d0 * kq[half * 2] : 0.f, i0 + 1 >= j ? d1 * kq[half * 2 + 1] : 0.f, wh, wl);
+            *reinterpret_cast<uint32_t *>(&s.a_hi[j][i0]) = wh;
+            *reinterpret_cast<uint32_t *>(&s.a_lo[j][i0]) = wl;
         }
+        if (tile == 2) {
+            bh[0][0] = vh[0], bl[0][0] = vl[0];
+            bh[1][0] = vh[1], bl[1][0] = vl[1];
+        } else if (tile == 3) {
+            bh[0][1] = vh[0], bl[0][1] = vl[0];
+            bh[1][1] = vh[1], bl[1][1] = vl[1];
+        }
+    }
     __syncwarp();
     // T = (I + L)^-1.  Its two 16 x 16 diagonal blocks by forward substitution, a
-    // column per lane: once x_m is known it is taken out of every later row
+    // column per lane: x[0] is the next unknown, taken out of every later row while
+    // those move up by one.  Rows past the block's last are never used
     {
         const int base = lane & 16;
         float x[16];
@@ -321,26 +328,25 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
         for (int i = 0; i < 16; ++i)
             x[i] = i == (lane & 15) ? 1.f : 0.f;
 #pragma unroll
-        for (int m = 0; m < 15; ++m) {
-            const float xm = x[m];
+        for (int m = 0; m < 16; m += 2) {
+            float xm[2];
 #pragma unroll
-            for (int i4 = (m + 1) / 4; i4 < 4; ++i4) {
-                const float4 l = *reinterpret_cast<const float4 *>(&s.lt[base + m][i4 * 4]);
-                const float lv[4] = {l.x, l.y, l.z, l.w};
+            for (int e = 0; e < 2; ++e) {
+                xm[e] = x[0];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (i4 * 4 + e > m)
-                        x[i4 * 4 + e] = fmaf(-lv[e], xm, x[i4 * 4 + e]);
+                for (int i4 = 0; i4 < 4; ++i4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(&s.lt[base + m + e][i4 * 4]);
+                    const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (i4 * 4 + k < 15)
+                            x[i4 * 4 + k] = fmaf(-lv[k], xm[e], x[i4 * 4 + k + 1]);
+                }
             }
-        }
-#pragma unroll
-        for (int i8 = 0; i8 < 2; ++i8) {
-            uint32_t xh[4], xl[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                split_h2(x[i8 * 8 + 2 * e], x[i8 * 8 + 2 * e + 1], xh[e], xl[e]);
-            *reinterpret_cast<uint4 *>(&s.t_hi[lane][base + i8 * 8]) = make_uint4(xh[0], xh[1], xh[2], xh[3]);
-            *reinterpret_cast<uint4 *>(&s.t_lo[lane][base + i8 * 8]) = make_uint4(xl[0], xl[1], xl[2], xl[3]);
+            uint32_t xh, xl;
+            split_h2(xm[0], xm[1], xh, xl);
+            *reinterpret_cast<uint32_t *>(&s.t_hi[lane][base + m]) = xh;
+            *reinterpret_cast<uint32_t *>(&s.t_lo[lane][base + m]) = xl;
         }
     }
     __syncwarp();
@@ -432,12 +438,16 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     if (threadIdx.x == 0) {
         for (int i = 0; i < R::HELP; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], NCW + R::OUT);
+            mbar_init(&sh.empty[i], R::CHAIN + R::OUT);
         }
         for (int i = 0; i < R::OUT; ++i) {
-            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_full[i], R::KH);
             mbar_init(&sh.w_full[i], 1);
             mbar_init(&sh.taken[i], 1);
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(&sh.shared[i][k], 1);
+                mbar_init(&sh.read[i][k], 1);
+            }
         }
         sh.abort = 0;
         fence_mbar_init();
@@ -445,8 +455,8 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     __syncthreads();
     volatile int *abort = &sh.abort;
     const int chunks = (len + kC - 1) / kC;
-    if (warp >= NCW + R::OUT) {
-        const int w = warp - NCW - R::OUT;
+    if (warp >= R::CHAIN + R::OUT) {
+        const int w = warp - R::CHAIN - R::OUT;
         Stage<DK, NCW> &st = sh.st[w];
         int use = 0, lo = 0, hi = 0;
         for (int c = w; c < chunks;) {
@@ -520,9 +530,9 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 }
             }
     };
-    // O = scale (a Q S + A W), O holding Q S, and its rows' way out through shared
-    // memory: a row of 16 columns per lane
-    auto finish_rows = [&](float (&O)[4][4], const float (&W)[4][4], const Stage<DK, NCW> &st, int c, float u0,
+    // O = scale (a Q S + A W), O holding Q S, and its rows' way out through where
+    // their values were: a row of 16 columns per lane
+    auto finish_rows = [&](float (&O)[4][4], const float (&W)[4][4], Stage<DK, NCW> &st, int c, float u0,
                            float u1) {
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -543,11 +553,11 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 x[n * 2] = pack_bf16x2(O[nt][0] * f.x * u0, O[nt][1] * f.y * u0);
                 x[n * 2 + 1] = pack_bf16x2(O[nt][2] * f.x * u1, O[nt][3] * f.y * u1);
             }
-            stsm_x4_trans(smem_u32(&sh.o[cw][n2 * 16 + pr][pc]), x[0], x[1], x[2], x[3]);
+            stsm_x4_trans(smem_u32(&st.v[n2 * 16 + pr][cw * 16 + pc]), x[0], x[1], x[2], x[3]);
         }
         __syncwarp();
         if (lane >= st.lo && lane < st.hi) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(&sh.o[cw][lane][0]);
+            const uint4 *src = reinterpret_cast<const uint4 *>(&st.v[lane][cw * 16]);
             uint4 *dst = reinterpret_cast<uint4 *>(out + (long long)c * kC * a.os.tok);
             dst[0] = src[0];
             dst[1] = src[1];
@@ -555,7 +565,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     };
     bool ok = true;
     unsigned phase = 0;                    // per stage
-    if (R::SPLIT && warp >= NCW) {
+    if (R::SPLIT && warp >= R::CHAIN) {
         // ------------------------------------------------ output warps
         Handed<DK> &from = sh.to[R::SPLIT ? cw : 0];
         for (int c = 0, turn = 0; c < chunks; turn ^= 1) {
@@ -601,10 +611,12 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     // ------------------------------------------------------------------- the chain
     // accumulator tile j holds S^T: rows (columns of S) g and g + 8, k-elements
     // 8 j + 2 t and the next
-    float S[DK / 8][4];
-    const long long so = slot * a.state_stride + (long long)h * DK * a.dv + col0 + warp * 16 + g;
+    constexpr int ROWS = DK / R::KH;       // of the state, in this warp
+    const int half = warp / NCW;           // which of them
+    float S[ROWS / 8][4];
+    const long long so = slot * a.state_stride + ((long long)h * DK + half * ROWS) * a.dv + col0 + cw * 16 + g;
 #pragma unroll
-    for (int j = 0; j < DK / 8; ++j)
+    for (int j = 0; j < ROWS / 8; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             S[j][e] = a.state ? a.state[so + (long long)(8 * j + 2 * t + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
@@ -623,7 +635,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     };
     auto scale_rows = [&](float f0, float f1) {
 #pragma unroll
-        for (int j = 0; j < DK / 8; ++j) {
+        for (int j = 0; j < ROWS / 8; ++j) {
             S[j][0] *= f0;
             S[j][1] *= f0;
             S[j][2] *= f1;
@@ -636,15 +648,51 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     };
     float top0[2] = {0.f, 0.f};        // the initial state's columns
 #pragma unroll
-    for (int j = 0; j < DK / 8; ++j)
+    for (int j = 0; j < ROWS / 8; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             top0[e >> 1] = fmaxf(top0[e >> 1], fabsf(S[j][e]));
+    // X and top of the column's two halves together; false if the wait ran out
+    int turns = 0;
+    auto add_shares = [&](float (&X)[4][4], float (&top)[2]) {
+        Share &mine = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? half : 0];
+        Share &other = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? half ^ 1 : 0];
+        if (turns > 0 && !__all_sync(0xffffffffu, tc5_wait(&sh.read[cw & 1][half], (turns - 1) & 1, abort)))
+            return false;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            mine.x[nt][lane] = make_float4(X[nt][0], X[nt][1], X[nt][2], X[nt][3]);
+        mine.top[lane] = make_float2(top[0], top[1]);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.shared[cw & 1][half ^ 1]);
+        if (!__all_sync(0xffffffffu, tc5_wait(&sh.shared[cw & 1][half], turns & 1, abort)))
+            return false;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+            const float4 x = other.x[nt][lane];
+            X[nt][0] += x.x;
+            X[nt][1] += x.y;
+            X[nt][2] += x.z;
+            X[nt][3] += x.w;
+        }
+        top[0] = fmaxf(top[0], other.top[lane].x);
+        top[1] = fmaxf(top[1], other.top[lane].y);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.read[cw & 1][half ^ 1]);
+        ++turns;
+        return true;
+    };
+    if (R::SPLIT) {
+        float none[4][4] = {};
+        ok = add_shares(none, top0);
+    }
     top0[0] = quad_max(top0[0]);
     top0[1] = quad_max(top0[1]);
     bool first = true;
     Handed<DK> &to = sh.to[R::SPLIT ? cw : 0];
-    for (int c = 0, turn = 0; c < chunks; turn ^= 1) {
+    for (int c = 0, turn = 0; ok && c < chunks; turn ^= 1) {
         const int w = c % R::HELP;
         ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
         if (!ok)
@@ -687,18 +735,19 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         }
         uint32_t bk[2][2][4], bq[2][4];
         float X2[4][4] = {};               // the low parts' sums, apart: shorter chains
-        load_rows(bk[0], st.k, 0);
+        const int ks0 = half * (ROWS / 16);
+        load_rows(bk[0], st.k, ks0);
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks) {
+        for (int ks = 0; ks < ROWS / 16; ++ks) {
             uint32_t hi[4], lo[4];
-            if (ks + 1 < DK / 16)
-                load_rows(bk[(ks + 1) & 1], st.k, ks + 1);
+            if (ks + 1 < ROWS / 16)
+                load_rows(bk[(ks + 1) & 1], st.k, ks0 + ks + 1);
             if (!R::SPLIT)
                 load_rows(bq, st.q, ks);
             split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
             if (R::SPLIT) {
-                to.s[ks][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                to.s[ks][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                to.s[ks0 + ks][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                to.s[ks0 + ks][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -716,10 +765,19 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     X[nt][e] += X2[nt][e];
+        float m[2];                        // the columns' largest elements
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const float2 th = __half22float2(top[hf]);
+            m[hf] = fmaxf(th.x, th.y);
+        }
         if (R::SPLIT) {
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.s_full[cw & 1]);
+            ok = add_shares(X, m);
+            if (!ok)
+                break;
         }
         first = false;
         // Y = beta (V - a K S), then W = T Y
@@ -735,7 +793,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         }
         float W[4][4] = {};
         times_lower(W, X, st.t_hi, st.t_lo);
-        if (R::SPLIT) {
+        if (R::SPLIT && half == 0) {
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt)
                 to.w[nt][lane] = make_float4(W[nt][0], W[nt][1], W[nt][2], W[nt][3]);
@@ -758,11 +816,10 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             }
             // what S will hold: its decayed size, or what is written now
             const float gamma = st.gamma;
-            float f[2], m[2];
+            float f[2];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const float2 th = __half22float2(top[hf]);
-                m[hf] = fmaxf(th.x, th.y) * gamma;
+                m[hf] *= gamma;
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt)
                     m[hf] = fmaxf(m[hf], fmaxf(fabsf(P[nt][2 * hf]), fabsf(P[nt][2 * hf + 1])));
@@ -791,9 +848,9 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int j2 = 0; j2 < DK / 16; ++j2) {
+                for (int j2 = 0; j2 < ROWS / 16; ++j2) {
                     uint32_t b[4];
-                    ldsm_x4_trans(b, smem_u32(&st.k[kk * 16 + tr][j2 * 16 + tc]));
+                    ldsm_x4_trans(b, smem_u32(&st.k[kk * 16 + tr][half * ROWS + j2 * 16 + tc]));
                     mma(S[2 * j2], hi[kk], b[0], b[1]);
                     mma(S[2 * j2 + 1], hi[kk], b[2], b[3]);
                     mma(S[2 * j2], lo[kk], b[0], b[1]);
@@ -814,7 +871,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     }
     if (a.state_out && (len > 0 || a.state_out != a.state))
 #pragma unroll
-        for (int j = 0; j < DK / 8; ++j)
+        for (int j = 0; j < ROWS / 8; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 a.state_out[so + (long long)(8 * j + 2 * t + (e & 1)) * a.dv + (e >> 1) * 8] =
