@@ -525,7 +525,10 @@ gattn_status gattn_layer_set_test_wait(gattn_layer *layer, int64_t wait_limit_ns
  *   - Tensors are described by a base pointer and element strides of the row
  *     ("token") and of the head; the elements of a head are contiguous.  bf16
  *     and fp32 rows: base 16-byte aligned, strides positive multiples of 8
- *     elements.  Slices of a wider projection output are such tensors.
+ *     elements.  Slices of a wider projection output are such tensors.  An
+ *     output's strides must keep its rows apart (the larger stride spans all
+ *     steps of the smaller).
+ *   - Offsets, positions, slots and status are 4-byte aligned.
  *   - Outputs must not overlap inputs unless an entry point says so.
  *   - `status` (device) uint32 [1], may be NULL: the kernels OR GATTN_STATUS_*
  *     bits into it (never clear it), so that a caller can read it when it
@@ -564,8 +567,9 @@ enum { GATTN_STATUS_RANGE = 1, GATTN_STATUS_TIMEOUT = 2 };
  * A sequence is skipped (its q_out rows zero, its cache untouched,
  * GATTN_STATUS_RANGE) when cache_pos < 0, cache_pos + rows > cache_capacity, or
  * its slot is outside [0, cache_batch) or taken.  head_dim: a multiple of 64 up
- * to 256 (else GATTN_E_UNSUPPORTED).  Rotary dims, theta and eps as in
- * gattn_cfg.
+ * to 256; cache_capacity up to 2^24, where positions are exact in fp32 (else
+ * GATTN_E_UNSUPPORTED).  Rotary dims, theta and eps as in gattn_cfg; q_norm and
+ * k_norm are 16-byte aligned.
  */
 typedef struct gattn_prompt_rows_desc {
     int32_t num_heads, num_kv_heads, head_dim;
@@ -652,7 +656,9 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *desc, gat
  *   w  = beta (v - S^T k)
  *   S <- S + k w^T
  *   out = bf16(scale S^T q)
- * with q and k divided by sqrt(sum x^2 + l2_eps) first when qk_l2norm is set.
+ * with q and k divided by sqrt(sum x^2 + l2_eps) first when qk_l2norm is set
+ * (l2_eps >= 0; the sum is an fp32 number: with l2_eps 0 its square root must not
+ * vanish).
  *   q, k          bf16 [total_rows][num_k_heads][k_dim] by strides
  *   v, out        bf16 [total_rows][num_v_heads][v_dim] by strides
  *   g, beta       fp32 [total_rows][num_v_heads], row strides >= num_v_heads; g is

@@ -74,7 +74,8 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
     seq_rows(a.sq, s, r0, len);
     const int slot = seq_slot_warp(a.sq, s, true);
     const long long p0 = a.pos[s], p = p0 + (t - r0);
-    const bool ok = slot >= 0 && p0 >= 0 && p0 + len <= a.cap;
+    // the last two hold for any row, if the offsets do not fall
+    const bool ok = slot >= 0 && p0 >= 0 && p0 + len <= a.cap && t >= r0 && t - r0 < len;
     if (!ok && lane == 0)
         seq_flag(a.sq, GATTN_STATUS_RANGE);
     // the row's own place in q, k and v

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "seq.cuh"
 
@@ -54,6 +55,31 @@ gattn_status check_rows(const char *name, const void *p, int64_t tok, int64_t he
     return GATTN_OK;
 }
 
+// Rows that are written: no two of them may share memory.
+gattn_status check_out(const char *name, const void *p, int64_t tok, int64_t head, int64_t d, int64_t rows,
+                       int64_t heads)
+{
+    CHECK(check_rows(name, p, tok, head));
+    // the nearer of the two steps spans a head row, the farther one all of the nearer's:
+    // out >= (n_in - 1) in + d
+    const int64_t in = tok < head ? tok : head, out = tok < head ? head : tok;
+    const int64_t n_in = tok < head ? rows : heads, n_out = tok < head ? heads : rows;
+    if ((n_in > 1 && in < d) || (n_out > 1 && out < d) ||
+        (n_in > 1 && n_out > 1 && (out - d) / in < n_in - 1))
+        return bad(GATTN_E_INVALID_ARG, "%s strides %lld, %lld make its rows overlap", name, (long long)tok,
+                   (long long)head);
+    return GATTN_OK;
+}
+
+// Device arrays of 32-bit words; NULL passes.
+gattn_status check_words(std::initializer_list<const void *> p)
+{
+    for (const void *x : p)
+        if (reinterpret_cast<uintptr_t>(x) & 3)
+            return bad(GATTN_E_INVALID_ARG, "offsets, positions, slots and status must be 4-byte aligned");
+    return GATTN_OK;
+}
+
 gattn_status check_seqs(int32_t n, int32_t total)
 {
     if (n < 0 || total < 0)
@@ -94,17 +120,23 @@ gattn_status gattn_prompt_rows(const gattn_prompt_rows_desc *p, gattn_stream str
     CHECK(check_rows("q", p->q, p->q_stride_token, p->q_stride_head));
     CHECK(check_rows("k", p->k, p->k_stride_token, p->k_stride_head));
     CHECK(check_rows("v", p->v, p->v_stride_token, p->v_stride_head));
-    CHECK(check_rows("q_out", p->q_out, p->o_stride_token, p->o_stride_head));
-    CHECK(check_rows("k_cache", p->k_cache, p->kc_stride_token, p->kc_stride_head));
-    CHECK(check_rows("v_cache", p->v_cache, p->vc_stride_token, p->vc_stride_head));
+    CHECK(check_out("q_out", p->q_out, p->o_stride_token, p->o_stride_head, p->head_dim, p->total_rows,
+                    p->num_heads));
+    CHECK(check_out("k_cache", p->k_cache, p->kc_stride_token, p->kc_stride_head, p->head_dim,
+                    p->cache_capacity, p->num_kv_heads));
+    CHECK(check_out("v_cache", p->v_cache, p->vc_stride_token, p->vc_stride_head, p->head_dim,
+                    p->cache_capacity, p->num_kv_heads));
     CHECK(check_rows("k_cache", p->k_cache, p->kc_stride_batch, 8));
     CHECK(check_rows("v_cache", p->v_cache, p->vc_stride_batch, 8));
+    CHECK(check_words({p->cu_rows, p->cache_pos, p->slots, p->status}));
     if (misaligned(p->q_norm) || misaligned(p->k_norm))
         return bad(GATTN_E_INVALID_ARG, "q_norm and k_norm must be 16-byte aligned");
     if (!p->cu_rows || !p->cache_pos || !p->q_norm || !p->k_norm)
         return bad(GATTN_E_INVALID_ARG, "cu_rows, cache_pos, q_norm or k_norm is NULL");
     if (p->cache_batch <= 0 || p->cache_capacity <= 0)
         return bad(GATTN_E_INVALID_ARG, "cache_batch and cache_capacity must be > 0");
+    if (p->cache_capacity > (1 << 24))
+        return bad(GATTN_E_UNSUPPORTED, "cache_capacity %d: positions are exact up to 2^24", p->cache_capacity);
     if (p->num_seqs == 0 || p->total_rows == 0)
         return GATTN_OK;
     PromptRowsArgs a{};
@@ -161,7 +193,9 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *p, gattn_
     CHECK(check_rows("v", p->v, p->v_stride_token, p->v_stride_head));
     CHECK(check_rows("k", p->k, p->k_stride_batch, 8));
     CHECK(check_rows("v", p->v, p->v_stride_batch, 8));
-    CHECK(check_rows("out", p->out, p->o_stride_token, p->o_stride_head));
+    CHECK(check_out("out", p->out, p->o_stride_token, p->o_stride_head, p->head_dim, p->total_rows,
+                    p->num_heads));
+    CHECK(check_words({p->cu_rows, p->cu_kv, p->cache_pos, p->slots, p->status}));
     if (p->gate) {
         CHECK(check_rows("gate", p->gate, p->g_stride_token, p->g_stride_head));
         if (p->gate_dtype != GATTN_DTYPE_F32 && p->gate_dtype != GATTN_DTYPE_BF16)
@@ -227,7 +261,8 @@ static gattn_status delta_args(const gattn_delta_desc *p, DeltaArgs &a)
         CHECK(check_rows("q", p->q, p->q_stride_token, p->q_stride_head));
         CHECK(check_rows("k", p->k, p->k_stride_token, p->k_stride_head));
         CHECK(check_rows("v", p->v, p->v_stride_token, p->v_stride_head));
-        CHECK(check_rows("out", p->out, p->o_stride_token, p->o_stride_head));
+        CHECK(check_out("out", p->out, p->o_stride_token, p->o_stride_head, p->v_dim, p->total_rows,
+                        p->num_v_heads));
         if (!p->g || !p->beta)
             return bad(GATTN_E_INVALID_ARG, "g or beta is NULL");
         if ((reinterpret_cast<uintptr_t>(p->g) | reinterpret_cast<uintptr_t>(p->beta)) & 3)
@@ -235,6 +270,7 @@ static gattn_status delta_args(const gattn_delta_desc *p, DeltaArgs &a)
         if (p->g_stride_token < p->num_v_heads || p->beta_stride_token < p->num_v_heads)
             return bad(GATTN_E_INVALID_ARG, "g and beta row strides must be >= num_v_heads");
     }
+    CHECK(check_words({p->cu_rows, p->slots, p->status}));
     if (!p->cu_rows && p->num_seqs > 0 && p->total_rows % p->num_seqs)
         return bad(GATTN_E_INVALID_ARG, "without cu_rows total_rows must be a multiple of num_seqs");
     if (p->state || p->state_out) {

@@ -130,3 +130,40 @@ def test_tensor_checks():
         _refused(device.prompt_rows, {**ok, **change})
     with pytest.raises(ValueError, match="CUDA device"):
         device.prompt_rows(**ok)
+
+
+def test_outputs_whose_rows_share_memory():
+    """Two rows of an output in one place would be a race."""
+    for make, call, bad, good in (
+            (_attn, "prompt_attention",
+             [dict(o_stride_head=32), dict(o_stride_token=64), dict(o_stride_token=192), dict(o_stride_head=504),
+              dict(o_stride_token=2 ** 37, o_stride_head=2 ** 37)],
+             [dict(o_stride_head=512, o_stride_token=64), dict(o_stride_head=8, num_heads=1, num_kv_heads=1),
+              dict(o_stride_token=8, total_rows=1), dict(o_stride_head=2 ** 37), dict(o_stride_token=2 ** 37)]),
+            (_rows, "prompt_rows",
+             [dict(o_stride_head=32), dict(kc_stride_token=32), dict(vc_stride_head=1016), dict(vc_stride_token=128)],
+             [dict(kc_stride_token=128, kc_stride_head=64), dict(cache_capacity=17, vc_stride_head=1088,
+                                                                kc_stride_head=1088)]),
+            (_delta, "delta_step", [dict(o_stride_head=32), dict(o_stride_token=192)], [dict(o_stride_token=264)])):
+        fn = getattr(gattn, call)
+        for change in bad:
+            with pytest.raises(gattn.GattnError) as e:
+                fn(make(**change))
+            assert e.value.status == 1 and "overlap" in gattn.last_error(), change
+        for change in good:
+            fn(make(**change))
+
+
+def test_words_off_their_boundary_and_far_positions():
+    for make, call, names in ((_rows, "prompt_rows", ("cu_rows", "cache_pos", "slots", "status")),
+                              (_attn, "prompt_attention", ("cu_rows", "cu_kv", "status")),
+                              (_delta, "delta_prompt", ("cu_rows", "slots", "status"))):
+        for name in names:
+            with pytest.raises(gattn.GattnError) as e:
+                getattr(gattn, call)(make(**{name: P + 2}))
+            assert e.value.status == 1 and "4-byte" in gattn.last_error(), name
+    big = dict(kc_stride_head=2 ** 31, vc_stride_head=2 ** 31)
+    gattn.prompt_rows(_rows(cache_capacity=1 << 24, **big))
+    with pytest.raises(gattn.GattnError) as e:
+        gattn.prompt_rows(_rows(cache_capacity=(1 << 24) + 1, **big))
+    assert e.value.status == 2
