@@ -159,8 +159,8 @@ __device__ __forceinline__ unsigned row_top(const void *row)
 }
 
 // A bf16 row of K and one of Q in shared memory become fp16 with their largest
-// elements brought to [1, 2): returns the powers of two taken out and the rows' sums
-// of squares in their units.  A lane per pair of rows; topk, topq: the largest
+// elements brought to [1, 2): returns the powers of two multiplied by and the sums of
+// squares of the result.  A lane per pair of rows; topk, topq: the largest
 // magnitudes.
 template <int DK>
 __device__ __forceinline__ float4 rows_to_half(__half *krow, __half *qrow, unsigned topk, unsigned topq)
@@ -186,7 +186,7 @@ __device__ __forceinline__ float4 rows_to_half(__half *krow, __half *qrow, unsig
         qp[i] = make_uint4(half_pair(w.x, fq, qq), half_pair(w.y, fq, qq), half_pair(w.z, fq, qq),
                            half_pair(w.w, fq, qq));
     }
-    return make_float4(__int_as_float(ek << 23), __int_as_float(eq << 23), kk[0] + kk[1], qq[0] + qq[1]);
+    return make_float4(fk, fq, kk[0] + kk[1], qq[0] + qq[1]);
 }
 
 // Everything of rows [lo, hi) of the chunk at t0 that does not depend on the
@@ -248,9 +248,10 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     if (bads)
         return __ffs(bads) - 1;
     const float4 row = rows_to_half<DK>(&s.k[lane][0], &s.q[lane][0], topk, row_top<KU>(&s.q[lane][0]));
-    // k = K 2^e / sqrt(sum + eps): in units of the stored row
-    const float r = !on ? 0.f : a.l2norm ? rsqrtf(row.z + a.l2_eps / (row.x * row.x)) : row.x;
-    const float rq = !on ? 0.f : a.l2norm ? rsqrtf(row.w + a.l2_eps / (row.y * row.y)) : row.y;
+    // k = K 2^e / sqrt(4^e sum + eps) in terms of the stored row, 2^-e at hand
+    auto power = [](float inv) { return __int_as_float((254 << 23) - __float_as_int(inv)); };
+    const float r = !on ? 0.f : a.l2norm ? rsqrtf(row.z + a.l2_eps * row.x * row.x) : power(row.x);
+    const float rq = !on ? 0.f : a.l2norm ? rsqrtf(row.w + a.l2_eps * row.y * row.y) : power(row.y);
     s.r[lane] = r;
     s.beta[lane] = beta;
     s.a[lane] = ai;
@@ -430,7 +431,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         if (threadIdx.x == 0)
             seq_flag(a.sq, GATTN_STATUS_RANGE);
         __nv_bfloat16 *out = a.out + (long long)h * a.os.head + col0;
-        for (int i = threadIdx.x; i < len * 2 * NCW; i += blockDim.x)
+        for (long long i = threadIdx.x; i < (long long)len * 2 * NCW; i += blockDim.x)
             *reinterpret_cast<uint4 *>(out + (r0 + i / (2 * NCW)) * a.os.tok + (i % (2 * NCW)) * 8) =
                 make_uint4(0, 0, 0, 0);
         return;
@@ -713,17 +714,21 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             }
         }
         const float vtop = st.vtop;
-        if (first || vtop * inv_unit[0] > 4096.f || vtop * inv_unit[1] > 4096.f) {
-            // the first rows, or values far above the state
-            const bool big0 = vtop * inv_unit[0] > 4096.f, big1 = vtop * inv_unit[1] > 4096.f;
-            const float m0 = first ? (top0[0] > 0.f ? top0[0] : vtop) : big0 ? vtop * inv_unit[0] : 0.f;
-            const float m1 = first ? (top0[1] > 0.f ? top0[1] : vtop) : big1 ? vtop * inv_unit[1] : 0.f;
-            const float f0 = refit(0, m0), f1 = refit(1, m1);
-            scale_rows(f0, f1);
-            if (first) {               // the values once more, in the state's units
-                const float n0 = vtop * inv_unit[0], n1 = vtop * inv_unit[1];
-                scale_rows(refit(0, n0 > 4096.f ? n0 : 0.f), refit(1, n1 > 4096.f ? n1 : 0.f));
+        if (__any_sync(0xffffffffu, first || vtop * inv_unit[0] > 4096.f || vtop * inv_unit[1] > 4096.f)) {
+            // the first rows, or values far above the state: each column by its own
+            float f[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float m = 0.f;
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+                    m = fmaxf(m, fmaxf(fabsf(v[nt][2 * hf]), fabsf(v[nt][2 * hf + 1])));
+                m = quad_max(m);
+                f[hf] = first ? refit(hf, top0[hf] > 0.f ? top0[hf] : m) : 1.f;
+                m *= inv_unit[hf];
+                f[hf] *= refit(hf, m > 4096.f ? m : 0.f);
             }
+            scale_rows(f[0], f[1]);
         }
         // K S (and Q S)
         float X[4][4] = {}, O[4][4] = {};

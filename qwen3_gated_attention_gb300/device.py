@@ -263,6 +263,14 @@ def _cu(t, name, dev):
     return t.data_ptr(), t.shape[0] - 1
 
 
+def _output(shape, like, stream):
+    """A bf16 tensor whose memory belongs to the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+
+
 def _call(fn, desc, dev, stream):
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
@@ -297,7 +305,7 @@ def prompt_rows(q, k, v, q_norm, k_norm, k_cache, v_cache, cu_rows, cache_pos, *
         _refuse(k_cache, "k_cache", dev, _BF16, (B, Hk, cap, d))
     vc = _planes(v_cache, "v_cache", dev, _BF16, shape)
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        q_out = _output((T, H, d), q, stream)
     oa = _rows(q_out, "q_out", dev, _BF16, (T, H, d))
     cu, n = _cu(cu_rows, "cu_rows", dev)
     desc = gattn.gattn_prompt_rows_desc.pack(
@@ -339,7 +347,7 @@ def prompt_attention(q, k, v, cu_rows, *, cu_kv=None, cache_pos=None, slots=None
     else:
         ga, gdt = (0, 8, 8), gattn.DTYPE_BF16
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        out = _output(shape, q, stream)
     oa = _rows(out, "out", dev, _BF16, shape)
     cu, n = _cu(cu_rows, "cu_rows", dev)
     ckv = 0
@@ -402,7 +410,7 @@ def _delta(fn, q, k, v, g, beta, cu_rows, num_seqs, state, state_out, slots, sca
         else:
             so = t.data_ptr()
     if out is None:
-        out = torch.empty((T, Hv, dv), dtype=torch.bfloat16, device=q.device)
+        out = _output((T, Hv, dv), q, stream)
     oa = _rows(out, "out", dev, _BF16, (T, Hv, dv))
     desc = gattn.gattn_delta_desc.pack(
         Hk, Hv, dk, dv, dk ** -0.5 if scale is None else scale, 1 if qk_l2norm else 0, l2_eps, n, T,
