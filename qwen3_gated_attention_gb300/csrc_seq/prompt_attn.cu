@@ -31,6 +31,7 @@
 // Few rows over many keys: clusters of 2, 4 or 8 CTAs, each pair taking a share of
 // the blocks; the partial (m, l, O) are joined through distributed shared memory.
 #include <algorithm>
+#include <cmath>
 
 #include <cudaTypedefs.h>
 
@@ -1079,11 +1080,23 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     const long long tiles =
         (a.sq.total / (2 * tpt) + std::min<long long>(a.sq.n, a.sq.total)) * (a.H >> hp_log2);
     const long long most = a.max_kv > 0 ? std::min(a.max_kv, a.kv_rows) : a.kv_rows;
-    // shares of the key blocks: while the pairs leave SMs idle and a share keeps
-    // 512 keys
+    // Shares of the key blocks: as many as shorten the longest way through them, at
+    // 256 keys a share or more.  Of clusters of 2, 4 and 8 CTAs 76, 36 and 15 fit at
+    // once; later ones start where others end, so a share's time counts between its
+    // waves and their whole number.  Measured with 16 heads of 256 over 4 KV heads, 8
+    // rows a sequence, by 1, 2 and 4 shares: one sequence (4 tiles) over 1000 keys
+    // 22.9, 20.2 and 18.0 us, over 16000 keys 206, 112 and 64 us; 8 sequences over
+    // 8000 keys 111, 66 and 118 us; 16 sequences over 8000 keys 112, 129 and 196 us
     int split = 1;
-    while (split < 4 && tiles * 2 * split < sms && most / (2 * split) >= 512)
-        split *= 2;
+    double best = 0;
+    for (int x = 1; x <= 4; x *= 2) {
+        const double fit = sms * (x == 1 ? 76 : x == 2 ? 36 : 15) / 152.0;
+        const double waves = tiles / fit, time = (waves <= 1 ? 1 : (waves + std::ceil(waves)) / 2) / x;
+        if (x == 1 || (most / x >= 256 && time < 0.92 * best)) {
+            split = x;
+            best = time;
+        }
+    }
     const long long clusters = split == 1 ? std::min<long long>(tiles, sms / 2) : tiles;
     if (tiles * 2 * split > 0x7fffffff)
         return cudaErrorInvalidConfiguration;

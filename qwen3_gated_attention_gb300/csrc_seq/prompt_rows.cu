@@ -7,6 +7,8 @@
 // read once and written once.  A warp works alone on (a part of) one packed row, so
 // nothing waits at a barrier: it finds the row's sequence, forms the row's angles
 // once, and takes kFly head rows at a time, their loads in flight together.
+#include <cmath>
+
 #include "seq.cuh"
 
 namespace gattn {
@@ -229,9 +231,18 @@ cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t 
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess)
         return e;
-    // warps per row: two keep the row's own work (angles, sequence) small against
-    // its bytes; eight while there are too few rows to fill the GPU
-    const int parts = (long long)a.sq.total * 2 >= (long long)sms * 32 ? 2 : 8;
+    // Warps per row: each repeats the row's own work (its angles, its sequence), so as
+    // few as keep the GPU full once (24 warps an SM; fp32 rows, with more registers,
+    // 16), or two where one fills its waves to less than 85 %.  16 + 4 + 4
+    // heads of 256, by 1, 2, 4 and 8 warps a row: 37 rows 11.6, 7.7, 5.7 and 5.2 us; 600
+    // rows 11.7, 7.9, 6.9 and 9.7; 2400 rows 15.6, 18.4, 19.2, 26.6; 9600 rows 53.4,
+    // 59.4, 70.6 and 104 us; 8240 rows of 32 + 8 + 8 heads, by 1 and 2: 93.6 and 88 us
+    const double fit = sms * (x_f32 ? 16. : 24.), waves = a.sq.total / fit;
+    int parts = 1;
+    while (parts < 8 && waves * 2 * parts <= 1)
+        parts *= 2;
+    if (waves > 1 && waves < 0.85 * std::ceil(waves))
+        parts = 2;
     const long long jobs = (long long)a.sq.total * parts;
     const dim3 grid((unsigned)((jobs + kWarps - 1) / kWarps)), block(kWarps * 32);
     const bool fast = (a.rd / 2) % 4 == 0;
