@@ -14,11 +14,14 @@
 // before it left there (S^T K^T, Y^T T^T, W^T K).
 //
 // Precision: the tensor cores multiply 16-bit floats.  K and Q rows are bf16 and
-// become fp16 exactly up to a power of two per row; S, Y, W, T and A are split
-// into two fp16 parts each (22 bits; 11 + 11), two products where the other
-// operand is exact, three where both are split, so the chain keeps fp32-like
-// accuracy.  fp16's range is covered by a power of two per state column that
-// follows the column's size.
+// become fp16 exactly up to a power of two per row.  In the chain S, Y, W and T are
+// split into two fp16 parts each (22 bits; 11 + 11), two products where the other
+// operand is exact, three where both are split, so the state keeps fp32-like
+// accuracy.  The answers O are rounded to bf16 (8 bits) at the end and to nowhere
+// else, so for them S, W and A count with the upper part alone (11 bits, off by at
+// most 2^-12 a term; errors of the terms of a sum are independent, and stay an eighth
+// of the last rounding).  fp16's range is covered by a power of two per state column
+// that follows the column's size.
 #include "seq.cuh"
 #include "tc5.cuh"
 
@@ -39,8 +42,7 @@ struct alignas(16) Stage {
     alignas(16) __nv_bfloat16 v[kC][16 * NCW + 8];
     alignas(16) __half t_hi[kC][kTS];              // T^T: [j][i]
     alignas(16) __half t_lo[kC][kTS];
-    alignas(16) __half a_hi[kC][kTS];              // A^T: [j][i]
-    alignas(16) __half a_lo[kC][kTS];
+    alignas(16) __half aq[kC][kTS];                // A^T: [j][i]
     alignas(16) float ar[kC];                      // per row, see the chain
     alignas(16) float beta[kC];
     alignas(16) float cr[kC];
@@ -69,10 +71,10 @@ struct Roles {
     static constexpr int THREADS = (CHAIN + OUT + HELP) * 32;
 };
 
-// What chain warps hand their output warp: S in parts, as operands, and W.
+// What chain warps hand their output warp: S's upper parts, as operands, and W.
 template <int DK>
 struct alignas(16) Handed {
-    uint4 s[DK / 16][2][32];
+    uint4 s[DK / 16][32];
     float4 w[4][32];
     float2 unit[32];
 };
@@ -305,10 +307,8 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
                     lt[1] = l1;
             } else
                 split_h2(l0, l1, vh[half], vl[half]);
-            uint32_t wh, wl;
-            split_h2(i0 >= j ? d0 * kq[half * 2] : 0.f, i0 + 1 >= j ? d1 * kq[half * 2 + 1] : 0.f, wh, wl);
-            *reinterpret_cast<uint32_t *>(&s.a_hi[j][i0]) = wh;
-            *reinterpret_cast<uint32_t *>(&s.a_lo[j][i0]) = wl;
+            *reinterpret_cast<uint32_t *>(&s.aq[j][i0]) =
+                pack_h2(i0 >= j ? d0 * kq[half * 2] : 0.f, i0 + 1 >= j ? d1 * kq[half * 2 + 1] : 0.f);
         }
         if (tile == 2) {
             bh[0][0] = vh[0], bl[0][0] = vl[0];
@@ -531,6 +531,12 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 }
             }
     };
+    // one k16 step of Q S: the state's upper part alone
+    auto times_queries = [&](float (&D)[4][4], const uint32_t (&hi)[4], const uint32_t (&b)[2][4]) {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            mma(D[nt], hi, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
+    };
     // O = scale (a Q S + A W), O holding Q S, and its rows' way out through where
     // their values were: a row of 16 columns per lane
     auto finish_rows = [&](float (&O)[4][4], const float (&W)[4][4], Stage<DK, NCW> &st, int c, float u0,
@@ -543,7 +549,19 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             O[nt][2] *= aa.x;
             O[nt][3] *= aa.y;
         }
-        times_lower(O, W, st.a_hi, st.a_lo);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const float (&w0)[4] = W[2 * kk], (&w1)[4] = W[2 * kk + 1];
+            const uint32_t w[4] = {pack_h2(w0[0], w0[1]), pack_h2(w0[2], w0[3]), pack_h2(w1[0], w1[1]),
+                                   pack_h2(w1[2], w1[3])};
+#pragma unroll
+            for (int n2 = kk; n2 < 2; ++n2) {
+                uint32_t x[4];
+                ldsm_x4_trans(x, smem_u32(&st.aq[kk * 16 + tr][n2 * 16 + tc]));
+                mma(O[n2 * 2], w, x[0], x[1]);
+                mma(O[n2 * 2 + 1], w, x[2], x[3]);
+            }
+        }
 #pragma unroll
         for (int n2 = 0; n2 < 2; ++n2) {
             uint32_t x[4];
@@ -580,11 +598,11 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             float O[4][4] = {}, W[4][4];
 #pragma unroll 2
             for (int ks = 0; ks < DK / 16; ++ks) {
-                const uint4 uh = from.s[ks][0][lane], ul = from.s[ks][1][lane];
-                const uint32_t hi[4] = {uh.x, uh.y, uh.z, uh.w}, lo[4] = {ul.x, ul.y, ul.z, ul.w};
+                const uint4 u = from.s[ks][lane];
+                const uint32_t hi[4] = {u.x, u.y, u.z, u.w};
                 uint32_t b[2][4];
                 load_rows(b, st.q, ks);
-                times_rows(O, O, hi, lo, b);
+                times_queries(O, hi, b);
             }
             ok = __all_sync(0xffffffffu, tc5_wait(&sh.w_full[cw & 1], turn, abort));
             if (!ok)
@@ -750,10 +768,8 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             if (!R::SPLIT)
                 load_rows(bq, st.q, ks);
             split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
-            if (R::SPLIT) {
-                to.s[ks0 + ks][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                to.s[ks0 + ks][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
+            if (R::SPLIT)
+                to.s[ks0 + ks][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 top[e & 1] = __hmax2(top[e & 1], __habs2(*reinterpret_cast<const __half2 *>(&hi[e])));
@@ -762,7 +778,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             else
                 times_rows(X, X, hi, lo, bk[ks & 1]);
             if (!R::SPLIT)
-                times_rows(O, O, hi, lo, bq);
+                times_queries(O, hi, bq);
         }
         if (R::SPLIT)
 #pragma unroll
