@@ -11,7 +11,9 @@
 // added up over the groups by shuffles: no shared memory, no barrier, and warps at
 // different points cover each other's latencies.  (A CTA per head with the sums in
 // shared memory spent a fifth of its time at barriers: 39 us for 32 sequences of 4
-// rows and 32 heads of 128 x 128.)
+// rows and 32 heads of 128 x 128.)  32 sequences of one row take 25 us, 79 % of the copy
+// rate over 134 MB of state; of four rows 38 us, 53 %: a row adds 4 us of arithmetic
+// and shuffles to each warp's way.  One sequence of one row: 3.7 us.
 #include "seq.cuh"
 #include "tc5.cuh"
 

@@ -22,6 +22,14 @@
 // most 2^-12 a term; errors of the terms of a sum are independent, and stay an eighth
 // of the last rounding).  fp16's range is covered by a power of two per state column
 // that follows the column's size.
+//
+// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 225 us
+// (1.76 us a chunk; its mma.sync instructions alone 0.6 us of it, the rest what each
+// of them waits for), 8 sequences of 1 to 1024 rows 114 us, the 1024 rows being the
+// longest chain (3.5 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
+// slower: the state's update fused with the next chunk's K S (415 us: spills), rows
+// brought in by bulk copies (96 small ones a chunk), helpers with unrolled loops
+// (their code pushes the chain's out of the instruction cache: 267 to 320 us).
 #include "seq.cuh"
 #include "tc5.cuh"
 
@@ -928,7 +936,10 @@ cudaError_t launch_dk(const DeltaArgs &a, cudaStream_t s)
     if (e != cudaSuccess)
         return e;
     // columns per CTA: as many as keep every SM busy, since a CTA's helpers do the
-    // same work for any number of them
+    // same work for any number of them.  Sequences of 1024 rows with 32 heads of 128 x
+    // 128, by 32, 64 and 128 columns: one 61, 77 and 110 us; two 120, 78 and 111; four
+    // 241, 157 and 113; sixteen 842, 543 and 446 (six helpers instead of four at 64
+    // columns take registers from the chain: 83 us)
     const long long cols = (long long)a.sq.n * a.Hv * a.dv;
     if (a.dv % 128 == 0 && cols / 64 > sms)
         return launch<DK, 8>(a, s);
