@@ -166,8 +166,11 @@ gattn_status gattn_prompt_rows(const gattn_prompt_rows_desc *p, gattn_stream str
     a.d = p->head_dim;
     a.rd = rd;
     a.eps = p->rms_eps;
+    // theta^(-2i/rd), by the power anew every 8th time: a few ulp of a double apart
+    const double step = std::pow((double)p->rope_theta, -2.0 / rd);
+    double f = 1.;
     for (int i = 0; i < rd / 2; ++i) {
-        const double f = std::pow((double)p->rope_theta, -2.0 * i / rd);
+        f = i % 8 ? f * step : std::pow((double)p->rope_theta, -2.0 * i / rd);
         a.inv_freq[i].x = (float)f;
         a.inv_freq[i].y = (float)(f - (double)a.inv_freq[i].x);
     }

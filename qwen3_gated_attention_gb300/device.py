@@ -203,6 +203,7 @@ def bf16_tensor_to_f64(t: torch.Tensor) -> np.ndarray:
 _DTYPES = {torch.float32: gattn.DTYPE_F32, torch.bfloat16: gattn.DTYPE_BF16}
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _refuse(t, name, dev, dtypes, shape, what="must have shape"):
@@ -276,7 +277,7 @@ def _call(fn, desc, dev, stream):
         raise ValueError("the tensors must be on a CUDA device")
     if stream is None:
         stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         fn(desc, stream)
     else:
         with torch.cuda.device(dev):
@@ -369,22 +370,39 @@ def prompt_attention(q, k, v, cu_rows, *, cu_kv=None, cache_pos=None, slots=None
     return out
 
 
+def _per_head(t, name, dev, T, Hv):
+    """(address, row stride) of g or beta."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.float32 or
+            t.shape != (T, Hv)):
+        _refuse(t, name, dev, _F32, (T, Hv))
+    st = t.stride()
+    if st[1] != 1 and Hv > 1:
+        _refuse(t, name, dev, _F32, (T, Hv))
+    return t.data_ptr(), st[0] if T > 1 else Hv
+
+
+def _states(t, name, dev, Hv, dk, dv):
+    """(address, slots, slot stride) of a state tensor."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.float32:
+        _refuse(t, name, dev, _F32, ("slots", Hv, dk, dv))
+    n = t.shape[0] if t.dim() == 4 else 0
+    if n < 1 or t.shape != (n, Hv, dk, dv) or not (t.is_contiguous() or t[0].is_contiguous()):
+        _refuse(t, name, dev, _F32, ("slots", Hv, dk, dv))
+    return t.data_ptr(), n, t.stride(0) if n > 1 else Hv * dk * dv
+
+
 def _delta(fn, q, k, v, g, beta, cu_rows, num_seqs, state, state_out, slots, scale, qk_l2norm,
            l2_eps, out, status, stream):
     dev = q.get_device()
-    qa = _rows(q, "q", dev, _BF16)
+    qp, qt, qh = _rows(q, "q", dev, _BF16)
     T, Hk, dk = shape = q.shape
-    ka = _rows(k, "k", dev, _BF16, shape)
-    va = _rows(v, "v", dev, _BF16)
-    Hv, dv = v.shape[1:]
-    if v.shape[0] != T:
+    kp, kt, kh = _rows(k, "k", dev, _BF16, shape)
+    vp, vt, vh = _rows(v, "v", dev, _BF16)
+    Tv, Hv, dv = v.shape
+    if Tv != T:
         _refuse(v, "v", dev, _BF16, T, "must have q's rows:")
-    gst = []
-    for t, name in ((g, "g"), (beta, "beta")):
-        if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.float32 or
-                t.shape != (T, Hv) or (Hv > 1 and t.stride(1) != 1)):
-            _refuse(t, name, dev, _F32, (T, Hv))
-        gst.append(t.stride(0) if T > 1 else Hv)
+    gp, gt = _per_head(g, "g", dev, T, Hv)
+    bp, bt = _per_head(beta, "beta", dev, T, Hv)
     if cu_rows is not None:
         cu, n = _cu(cu_rows, "cu_rows", dev)
         if num_seqs is not None and num_seqs != n:
@@ -393,30 +411,21 @@ def _delta(fn, q, k, v, g, beta, cu_rows, num_seqs, state, state_out, slots, sca
         raise ValueError("num_seqs is needed without cu_rows")
     else:
         cu, n = 0, num_seqs
-    nslots = stride = sp = so = 0
-    for t, name in ((state, "state"), (state_out, "state_out")):
-        if t is None:
-            continue
-        if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.float32 or
-                t.dim() != 4 or t.shape[1:] != (Hv, dk, dv) or not t.shape[0] or
-                not (t.is_contiguous() or t[0].is_contiguous())):
-            _refuse(t, name, dev, _F32, (nslots or "slots", Hv, dk, dv))
-        st = t.stride(0) if t.shape[0] > 1 else max(stride, Hv * dk * dv)
-        if nslots and (nslots != t.shape[0] or stride != st):
+    sp = so = nslots = stride = 0
+    if state is not None:
+        sp, nslots, stride = _states(state, "state", dev, Hv, dk, dv)
+    if state_out is not None:
+        so, n_out, stride_out = _states(state_out, "state_out", dev, Hv, dk, dv)
+        if sp and (n_out != nslots or stride_out != stride):
             raise ValueError("state and state_out must have one shape and stride")
-        nslots, stride = t.shape[0], st
-        if name == "state":
-            sp = t.data_ptr()
-        else:
-            so = t.data_ptr()
+        nslots, stride = n_out, stride_out
     if out is None:
         out = _output((T, Hv, dv), q, stream)
-    oa = _rows(out, "out", dev, _BF16, (T, Hv, dv))
+    op, ot, oh = _rows(out, "out", dev, _BF16, (T, Hv, dv))
     desc = gattn.gattn_delta_desc.pack(
         Hk, Hv, dk, dv, dk ** -0.5 if scale is None else scale, 1 if qk_l2norm else 0, l2_eps, n, T,
-        nslots, cu, _flat(slots, "slots", dev, _I32, n), qa[0], ka[0], va[0], qa[1], qa[2], ka[1],
-        ka[2], va[1], va[2], g.data_ptr(), beta.data_ptr(), gst[0], gst[1], sp, so, stride, oa[0],
-        oa[1], oa[2], _flat(status, "status", dev, _I32, 1))
+        nslots, cu, _flat(slots, "slots", dev, _I32, n), qp, kp, vp, qt, qh, kt, kh, vt, vh, gp, bp,
+        gt, bt, sp, so, stride, op, ot, oh, _flat(status, "status", dev, _I32, 1))
     if n:
         _call(fn, desc, dev, stream)
     return out
