@@ -98,10 +98,12 @@ template <int DK, int NCW>
 struct alignas(16) Shared {
     using R = Roles<NCW>;
     Stage<DK, NCW> st[R::HELP];
-    Handed<DK> to[R::SPLIT ? NCW : 1];
-    Share share[R::SPLIT ? NCW : 1][R::KH];
+    // by turns, so that nobody waits for what was handed on before to be read
+    Handed<DK> to[R::SPLIT ? NCW : 1][R::KH];
+    Share share[R::SPLIT ? NCW : 1][R::KH][R::KH];         // [columns][turn][half]
     uint64_t full[R::HELP], empty[R::HELP];
-    uint64_t s_full[2], w_full[2], taken[2], shared[2][2], read[2][2];
+    uint64_t s_full[2][2], w_full[2][2], taken[2][2];      // [columns][turn]
+    uint64_t shared[2][2][2];                              // [columns][turn][half]
     int abort;
 };
 static_assert((kTS * 2) % 16 == 0 && (kLS * 4) % 16 == 0 && sizeof(Stage<128, 2>) % 16 == 0 &&
@@ -450,12 +452,12 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             mbar_init(&sh.empty[i], R::CHAIN + R::OUT);
         }
         for (int i = 0; i < R::OUT; ++i) {
-            mbar_init(&sh.s_full[i], R::KH);
-            mbar_init(&sh.w_full[i], 1);
-            mbar_init(&sh.taken[i], 1);
             for (int k = 0; k < 2; ++k) {
-                mbar_init(&sh.shared[i][k], 1);
-                mbar_init(&sh.read[i][k], 1);
+                mbar_init(&sh.s_full[i][k], R::KH);
+                mbar_init(&sh.w_full[i][k], 1);
+                mbar_init(&sh.taken[i][k], 1);
+                mbar_init(&sh.shared[i][k][0], 1);
+                mbar_init(&sh.shared[i][k][1], 1);
             }
         }
         sh.abort = 0;
@@ -594,11 +596,11 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     unsigned phase = 0;                    // per stage
     if (R::SPLIT && warp >= R::CHAIN) {
         // ------------------------------------------------ output warps
-        Handed<DK> &from = sh.to[R::SPLIT ? cw : 0];
-        for (int c = 0, turn = 0; c < chunks; turn ^= 1) {
-            const int w = c % R::HELP;
+        for (int c = 0, use = 0; c < chunks; ++use) {
+            const int w = c % R::HELP, turn = use & 1, ph = use >> 1 & 1;
+            Handed<DK> &from = sh.to[R::SPLIT ? cw : 0][R::SPLIT ? turn : 0];
             ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort) &&
-                                             tc5_wait(&sh.s_full[cw & 1], turn, abort));
+                                             tc5_wait(&sh.s_full[cw & 1][turn], ph, abort));
             if (!ok)
                 break;
             phase ^= 1u << w;
@@ -612,7 +614,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 load_rows(b, st.q, ks);
                 times_queries(O, hi, b);
             }
-            ok = __all_sync(0xffffffffu, tc5_wait(&sh.w_full[cw & 1], turn, abort));
+            ok = __all_sync(0xffffffffu, tc5_wait(&sh.w_full[cw & 1][turn], ph, abort));
             if (!ok)
                 break;
 #pragma unroll
@@ -626,7 +628,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             const float2 u = from.unit[lane];
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&sh.taken[cw & 1]);
+                mbar_arrive(&sh.taken[cw & 1][turn]);
             finish_rows(O, W, st, c, u.x, u.y);
             c += st.more ? 0 : 1;
             __syncwarp();
@@ -679,21 +681,25 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             top0[e >> 1] = fmaxf(top0[e >> 1], fabsf(S[j][e]));
-    // X and top of the column's two halves together; false if the wait ran out
+    // X and top of the column's two halves together; false if the wait ran out.  A
+    // buffer comes round again after the other half has answered for the one between.
+    // `tell`, if any, hears that this warp's S has been handed on
     int turns = 0;
-    auto add_shares = [&](float (&X)[4][4], float (&top)[2]) {
-        Share &mine = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? half : 0];
-        Share &other = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? half ^ 1 : 0];
-        if (turns > 0 && !__all_sync(0xffffffffu, tc5_wait(&sh.read[cw & 1][half], (turns - 1) & 1, abort)))
-            return false;
+    auto add_shares = [&](float (&X)[4][4], float (&top)[2], uint64_t *tell) {
+        Share &mine = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? turns & 1 : 0][R::SPLIT ? half : 0];
+        Share &other = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? turns & 1 : 0][R::SPLIT ? half ^ 1 : 0];
+        uint64_t (&bar)[2] = sh.shared[cw & 1][turns & 1];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
             mine.x[nt][lane] = make_float4(X[nt][0], X[nt][1], X[nt][2], X[nt][3]);
         mine.top[lane] = make_float2(top[0], top[1]);
         __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&sh.shared[cw & 1][half ^ 1]);
-        if (!__all_sync(0xffffffffu, tc5_wait(&sh.shared[cw & 1][half], turns & 1, abort)))
+        if (lane == 0) {
+            mbar_arrive(&bar[half ^ 1]);
+            if (tell)
+                mbar_arrive(tell);
+        }
+        if (!__all_sync(0xffffffffu, tc5_wait(&bar[half], turns >> 1 & 1, abort)))
             return false;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -705,22 +711,19 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         }
         top[0] = fmaxf(top[0], other.top[lane].x);
         top[1] = fmaxf(top[1], other.top[lane].y);
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&sh.read[cw & 1][half ^ 1]);
         ++turns;
         return true;
     };
     if (R::SPLIT) {
         float none[4][4] = {};
-        ok = add_shares(none, top0);
+        ok = add_shares(none, top0, nullptr);
     }
     top0[0] = quad_max(top0[0]);
     top0[1] = quad_max(top0[1]);
     bool first = true;
-    Handed<DK> &to = sh.to[R::SPLIT ? cw : 0];
-    for (int c = 0, turn = 0; ok && c < chunks; turn ^= 1) {
-        const int w = c % R::HELP;
+    for (int c = 0, use = 0; ok && c < chunks; ++use) {
+        const int w = c % R::HELP, turn = use & 1;
+        Handed<DK> &to = sh.to[R::SPLIT ? cw : 0][R::SPLIT ? turn : 0];
         ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
         if (!ok)
             break;
@@ -759,8 +762,8 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         // K S (and Q S)
         float X[4][4] = {}, O[4][4] = {};
         __half2 top[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
-        if (R::SPLIT && !first) {
-            ok = __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1], turn ^ 1, abort));
+        if (R::SPLIT && use >= 2) {
+            ok = __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1][turn], (use >> 1 & 1) ^ 1, abort));
             if (!ok)
                 break;
         }
@@ -801,10 +804,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             m[hf] = fmaxf(th.x, th.y);
         }
         if (R::SPLIT) {
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.s_full[cw & 1]);
-            ok = add_shares(X, m);
+            ok = add_shares(X, m, &sh.s_full[cw & 1][turn]);
             if (!ok)
                 break;
         }
@@ -829,7 +829,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             to.unit[lane] = make_float2(unit[0], unit[1]);
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&sh.w_full[cw & 1]);
+                mbar_arrive(&sh.w_full[cw & 1][turn]);
         }
         // S <- gamma S + (c r W)^T K
         float ounit[2];
