@@ -23,8 +23,8 @@
 // of the last rounding).  fp16's range is covered by a power of two per state column
 // that follows the column's size.
 //
-// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 225 us
-// (1.76 us a chunk; its mma.sync instructions alone 0.6 us of it, the rest what each
+// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 221 us
+// (1.73 us a chunk; its mma.sync instructions alone 0.3 us of it, the rest what each
 // of them waits for), 8 sequences of 1 to 1024 rows 114 us, the 1024 rows being the
 // longest chain (3.5 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
 // slower: the state's update fused with the next chunk's K S (415 us: spills), rows
