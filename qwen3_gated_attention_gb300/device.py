@@ -268,7 +268,9 @@ def _output(shape, like, stream):
     """A bf16 tensor whose memory belongs to the stream that will write it."""
     if stream is None:
         return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
+    own = (torch.cuda.ExternalStream(stream, device=like.device) if stream
+           else torch.cuda.default_stream(like.device))        # handle 0
+    with torch.cuda.stream(own):
         return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
 
 

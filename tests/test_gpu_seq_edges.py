@@ -272,3 +272,26 @@ def test_one_graph_of_all_with_other_lengths_at_each_replay():
         for a, b in zip(got[:4], want[:4]):
             assert torch.equal(a[:T], b[:T]) and not a[T:].any()
         assert all(torch.equal(a, b) for a, b in zip(own, fresh))
+
+
+@pytest.mark.parametrize("own", [True, False], ids=["stream", "default"])
+def test_an_output_belongs_to_the_stream_that_writes_it(own):
+    """Memory freed on the stream that is current must not come back as the output of
+    a call on another stream while the first still writes it."""
+    dv = _dev()
+    x, kc, vc, _ = _stack_inputs(96)
+    cu, pos = R.cu_of([40, 0, 1, 49], "cuda"), _i32(3, 0, 100, 9)
+    want = dv.prompt_attention(x["q"], kc, vc, cu, cache_pos=pos)
+    side, s = torch.cuda.Stream(), torch.cuda.Stream() if own else torch.cuda.default_stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy = torch.empty(1 << 28, device="cuda")
+        for _ in range(20):
+            busy.fill_(1.0)
+        late = torch.empty_like(want)
+        late.fill_(7.0)                    # behind the busy work
+        at = late.data_ptr()
+        del late
+        out = dv.prompt_attention(x["q"], kc, vc, cu, cache_pos=pos, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    assert out.data_ptr() != at and torch.equal(out, want)
