@@ -5,20 +5,20 @@
 //   (y_i, y_{i+rd/2}) <- (y_i cos - y_{i+rd/2} sin, y_{i+rd/2} cos + y_i sin),
 // angle p * theta^(-2i/rd); values are copied.  Bound by memory: every element is
 // read once and written once.  A warp works alone on (a part of) one packed row, so
-// nothing waits at a barrier: it finds the row's sequence, forms the row's angles
-// once, and takes kFly head rows at a time, their loads in flight together.  8240 rows
-// of 32 + 8 + 8 heads of 256 take 88 us, 4.6 TB/s or 67 % of the copy rate (a CTA per
-// row and head with barriers 144 us; one head row at a time 188 us); what is left is
-// the latency of a warp's rounds at 24 warps an SM.  37 rows of 16 + 4 + 4 heads: 5.0 us.
-#include <cmath>
-
+// nothing waits at a barrier, and always has kFly head rows on their way while it works
+// on the kFly before them, from the queries through the keys to the values; the first
+// set out before the row's sequence and angles are known.  8240 rows of 32 + 8 + 8 heads
+// of 256 take 75 us, 5.4 TB/s or 80 % of the copy rate (a CTA per row and head with
+// barriers 144 us; a warp that loads, then works 88 us; one head row at a time 188 us);
+// more loads on their way or more warps cost registers: 82 us with 24 warps an SM.  37
+// rows of 16 + 4 + 4 heads: 4.5 us.
 #include "seq.cuh"
 
 namespace gattn {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kFly = 4;            // head rows in flight per group of lanes
 
 // Two runs of four elements as they come from memory.
@@ -62,7 +62,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float
 // a group then take a run from each rotary half, so partners meet in a lane.
 // Otherwise the runs are neighbours and partners meet in shared memory.
 template <bool F32, bool FAST>
-__global__ void __launch_bounds__(kWarps * 32, F32 ? 2 : 3)
+__global__ void __launch_bounds__(kWarps * 32, F32 ? 4 : 5)
 prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
 {
     __shared__ float2 table[kWarps][128];
@@ -72,6 +72,33 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
     const int t = (int)(job / parts), part = (int)(job % parts);
     if (t >= a.sq.total)
         return;
+    const int lpu = a.d == 64 ? 8 : (a.d == 128 ? 16 : 32);   // lanes per head row
+    const int sub = lane & (lpu - 1), at = lane / lpu, upw = 32 / lpu;
+    const int j0 = sub * 8;
+    const bool act = j0 < a.d;
+    const int half = a.rd / 2;
+    const bool rot = FAST && j0 < a.rd;
+    const int o0 = rot ? sub * 4 : j0, o1 = rot ? half + sub * 4 : j0 + 4;   // the two runs
+    const int step = parts * upw, first = part * upw + at;
+    // the row's own place in q, k and v
+    const long long esz = F32 ? 4 : 2;
+    const char *const qrow = static_cast<const char *>(a.q) + t * a.qs.tok * esz;
+    const char *const krow = static_cast<const char *>(a.k) + t * a.ks.tok * esz;
+    const char *const vrow = static_cast<const char *>(a.v) + t * a.vs.tok * esz;
+    // the head rows on their way: always kFly ahead of the ones at work, across q, k
+    // and v, the first before anything else is known of the row
+    Raw<F32> nxt[kFly];
+    auto fetch = [&](const void *src, long long src_head, int u0, int heads, int r0, int r1) {
+        long long so = (long long)u0 * src_head;
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            nxt[f].clear();
+            if (act && u0 + f * step < heads)
+                nxt[f].load(src, so + r0, so + r1);
+            so += step * src_head;
+        }
+    };
+    fetch(qrow, a.qs.head, first, a.H, o0, o1);
     const int s = find_seq_warp(a.sq, t);
     if (s < 0)
         return;
@@ -83,12 +110,6 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
     const bool ok = slot >= 0 && p0 >= 0 && p0 + len <= a.cap && t >= r0 && t - r0 < len;
     if (!ok && lane == 0)
         seq_flag(a.sq, GATTN_STATUS_RANGE);
-    // the row's own place in q, k and v
-    const long long esz = F32 ? 4 : 2;
-    const char *const qrow = static_cast<const char *>(a.q) + t * a.qs.tok * esz;
-    const char *const krow = static_cast<const char *>(a.k) + t * a.ks.tok * esz;
-    const char *const vrow = static_cast<const char *>(a.v) + t * a.vs.tok * esz;
-    const int half = a.rd / 2;
     float2 *const cs = table[warp];
     for (int i = lane; i < half; i += 32) {
         // The angle p * inv_freq as an unevaluated float pair, reduced modulo
@@ -107,23 +128,14 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
         cs[i] = make_float2(c, sn);
     }
     __syncwarp();
-    const int lpu = a.d == 64 ? 8 : (a.d == 128 ? 16 : 32);   // lanes per head row
-    const int sub = lane & (lpu - 1), at = lane / lpu, upw = 32 / lpu;
-    const int j0 = sub * 8;
-    const bool act = j0 < a.d;
     const float inv_d = 1.f / (float)a.d;
-    const bool rot = FAST && j0 < a.rd;
-    const int o0 = rot ? sub * 4 : j0, o1 = rot ? half + sub * 4 : j0 + 4;   // the two runs
-    float wq[8], wk[8], cosv[FAST ? 4 : 8], sinv[FAST ? 4 : 8];
-    {
-        Raw<false> w;
-        w.clear();
-        if (act)
-            w.load(a.q_norm, o0, o1);
-        w.get(wq);
-        if (act)
-            w.load(a.k_norm, o0, o1);
-        w.get(wk);
+    float cosv[FAST ? 4 : 8], sinv[FAST ? 4 : 8];
+    Raw<false> wq, wk;
+    wq.clear();
+    wk.clear();
+    if (act) {
+        wq.load(a.q_norm, o0, o1);
+        wk.load(a.k_norm, o0, o1);
     }
 #pragma unroll
     for (int i = 0; i < (FAST ? 4 : 8); ++i) {
@@ -137,27 +149,30 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
         }
     }
     float *const buf = FAST ? nullptr : swap[warp] + at * lpu * 8;
-    const int step = parts * upw, first = part * upw + at;
-    // `heads` head rows from `src` to `dst`, normed and turned by weights w
+    // `heads` head rows from `src`, the first of them on their way, to `dst`, normed and
+    // turned by weights w; `then` fetches what comes after
     auto normed = [&](const void *src, long long src_head, __nv_bfloat16 *dst, long long dst_head, int heads,
-                      const float (&w)[8]) {
-        long long so = (long long)first * src_head;
+                      const Raw<false> &weight, auto then) {
         __nv_bfloat16 *to = dst + (long long)first * dst_head;
-        for (int u0 = first; u0 - at < heads; u0 += kFly * step) {
+        for (int u0 = first; u0 - at < heads || u0 == first; u0 += kFly * step) {
             Raw<F32> raw[kFly];
 #pragma unroll
             for (int f = 0; f < kFly; ++f) {
-                raw[f].clear();
-                if (act && ok && u0 + f * step < heads)
-                    raw[f].load(src, so + o0, so + o1);
-                so += step * src_head;
+                raw[f] = nxt[f];
+                if (!ok)
+                    raw[f].clear();
             }
+            if (u0 - at + kFly * step < heads)
+                fetch(src, src_head, u0 + kFly * step, heads, o0, o1);
+            else
+                then();
 #pragma unroll
             for (int f = 0; f < kFly; ++f, to += step * dst_head) {
                 const int u = u0 + f * step;
                 if (u - at >= heads)           // the whole warp is past the last one
                     continue;
-                float x[8], y[8];
+                float x[8], y[8], w[8];
+                weight.get(w);
                 raw[f].get(x);
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -203,17 +218,20 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
             }
         }
     };
-    normed(qrow, a.qs.head, a.q_out + t * a.os.tok, a.os.head, a.H, wq);
+    normed(qrow, a.qs.head, a.q_out + t * a.os.tok, a.os.head, a.H, wq,
+           [&] { fetch(krow, a.ks.head, first, a.Hk, o0, o1); });
     if (!ok)
         return;
-    normed(krow, a.ks.head, a.kc + slot * a.kcb + p * a.kct, a.kch, a.Hk, wk);
+    normed(krow, a.ks.head, a.kc + slot * a.kcb + p * a.kct, a.kch, a.Hk, wk,
+           [&] { fetch(vrow, a.vs.head, first, a.Hk, j0, j0 + 4); });
     __nv_bfloat16 *const vc = a.vc + slot * a.vcb + p * a.vct;
     for (int u0 = first; u0 < a.Hk; u0 += kFly * step) {
         Raw<F32> raw[kFly];
 #pragma unroll
         for (int f = 0; f < kFly; ++f)
-            if (act && u0 + f * step < a.Hk)
-                raw[f].load(vrow, (u0 + f * step) * a.vs.head + j0, (u0 + f * step) * a.vs.head + j0 + 4);
+            raw[f] = nxt[f];
+        if (u0 + kFly * step < a.Hk)
+            fetch(vrow, a.vs.head, u0 + kFly * step, a.Hk, j0, j0 + 4);
 #pragma unroll
         for (int f = 0; f < kFly; ++f)
             if (act && u0 + f * step < a.Hk) {
@@ -235,17 +253,13 @@ cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t 
     if (e != cudaSuccess)
         return e;
     // Warps per row: each repeats the row's own work (its angles, its sequence), so as
-    // few as keep the GPU full once (24 warps an SM; fp32 rows, with more registers,
-    // 16), or two where one fills its waves to less than 85 %.  16 + 4 + 4
-    // heads of 256, by 1, 2, 4 and 8 warps a row: 37 rows 11.6, 7.7, 5.7 and 5.2 us; 600
-    // rows 11.7, 7.9, 6.9 and 9.7; 2400 rows 15.6, 18.4, 19.2, 26.6; 9600 rows 53.4,
-    // 59.4, 70.6 and 104 us; 8240 rows of 32 + 8 + 8 heads, by 1 and 2: 93.6 and 88 us
-    const double fit = sms * (x_f32 ? 16. : 24.), waves = a.sq.total / fit;
+    // few as fill the GPU once (20 warps an SM; fp32 rows, with more registers, 16).
+    // 16 + 4 + 4 heads of 256, by 1, 2, 4 and 8 warps a row: 37 rows 10.1, 6.7, 5.1 and
+    // 4.8 us; 600 rows 10.3, 7.6, 6.5 and 9.7; 1200 rows 11.3, 8.9, 11.1 and 15.1; 9600
+    // rows 49.0, 50.9, 62.3 and 91.0
     int parts = 1;
-    while (parts < 8 && waves * 2 * parts <= 1)
+    while (parts < 8 && (long long)a.sq.total * 2 * parts <= (long long)sms * (x_f32 ? 16 : 20))
         parts *= 2;
-    if (waves > 1 && waves < 0.85 * std::ceil(waves))
-        parts = 2;
     const long long jobs = (long long)a.sq.total * parts;
     const dim3 grid((unsigned)((jobs + kWarps - 1) / kWarps)), block(kWarps * 32);
     const bool fast = (a.rd / 2) % 4 == 0;
