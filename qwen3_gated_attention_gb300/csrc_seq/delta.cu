@@ -14,6 +14,8 @@
 // rows and 32 heads of 128 x 128.)  32 sequences of one row take 25 us, 79 % of the copy
 // rate over 134 MB of state; of four rows 38 us, 53 %: a row adds 4 us of arithmetic
 // and shuffles to each warp's way.  One sequence of one row: 3.7 us.
+#include <algorithm>
+
 #include "seq.cuh"
 #include "tc5.cuh"
 
@@ -46,39 +48,32 @@ __device__ __forceinline__ void unpack_row(const uint4 (&u)[N], float (&f)[8 * N
 }
 
 template <int DK>
-__global__ void __launch_bounds__(kWarps * 32) delta_rows_kernel(const __grid_constant__ DeltaArgs a)
+__global__ void __launch_bounds__(kWarps * 32, 3) delta_rows_kernel(const __grid_constant__ DeltaArgs a)
 {
     constexpr int RPT = DK / 8;                   // k-elements of a lane
-    const int lane = threadIdx.x & 31, grp = lane >> 2;
+    __shared__ ulonglong2 ahead[kWarps][RPT][32]; // the next job's state: a lane's own elements
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane >> 2;
     const int parts = a.dv / 16;
-    const long long job = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int h = (int)(job / parts % a.Hv), hk = h / (a.Hv / a.Hk);
-    const long long sl = job / parts / a.Hv;
-    if (sl >= a.sq.n)
-        return;
-    const int s = (int)sl, col = (int)(job % parts) * 16 + (lane & 3) * 4;
-    int r0, len;
-    seq_rows(a.sq, s, r0, len);
-    const int slot = seq_slot_warp(a.sq, s, true);
-    __nv_bfloat16 *out = a.out + (long long)h * a.os.head + col;
-    if (slot < 0) {
-        if (lane == 0)
-            seq_flag(a.sq, GATTN_STATUS_RANGE);
-        for (int t = r0 + grp; t < r0 + len; t += 8)
-            *reinterpret_cast<uint2 *>(out + (long long)t * a.os.tok) = make_uint2(0, 0);
-        return;
-    }
-    const long long so = slot * a.state_stride + ((long long)h * DK + grp * RPT) * a.dv + col;
-    uint64_t S[RPT][2];                           // columns (0, 1) and (2, 3)
-#pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        const ulonglong2 x = a.state ? *reinterpret_cast<const ulonglong2 *>(a.state + so + (long long)i * a.dv)
-                                     : make_ulonglong2(0, 0);
-        S[i][0] = x.x;
-        S[i][1] = x.y;
-    }
-    auto load = [&](int t) {
+    const long long jobs = (long long)a.sq.n * a.Hv * parts, stride = (long long)gridDim.x * kWarps;
+    ulonglong2 (*const buf)[32] = ahead[warp];
+    struct Job {
+        int h, col, r0, len, slot;
+    };
+    auto find = [&](long long job) {
+        Job j;
+        const int s = (int)(job / parts / a.Hv);
+        j.h = (int)(job / parts % a.Hv);
+        j.col = (int)(job % parts) * 16 + (lane & 3) * 4;
+        seq_rows(a.sq, s, j.r0, j.len);
+        j.slot = seq_slot_warp(a.sq, s, true);
+        return j;
+    };
+    auto place = [&](const Job &j) {
+        return j.slot * a.state_stride + ((long long)j.h * DK + grp * RPT) * a.dv + j.col;
+    };
+    auto load = [&](const Job &j, int t) {
         RowIn<RPT> r;
+        const int hk = j.h / (a.Hv / a.Hk);
         const uint4 *kp = reinterpret_cast<const uint4 *>(a.k + t * a.ks.tok + hk * a.ks.head + grp * RPT);
         const uint4 *qp = reinterpret_cast<const uint4 *>(a.q + t * a.qs.tok + hk * a.qs.head + grp * RPT);
 #pragma unroll
@@ -86,81 +81,138 @@ __global__ void __launch_bounds__(kWarps * 32) delta_rows_kernel(const __grid_co
             r.k[n] = kp[n];
             r.q[n] = qp[n];
         }
-        r.v = *reinterpret_cast<const uint2 *>(a.v + t * a.vs.tok + h * a.vs.head + col);
-        r.g = a.g[t * a.gt + h];
-        r.beta = a.beta[t * a.bt + h];
+        r.v = *reinterpret_cast<const uint2 *>(a.v + t * a.vs.tok + j.h * a.vs.head + j.col);
+        r.g = a.g[t * a.gt + j.h];
+        r.beta = a.beta[t * a.bt + j.h];
         return r;
     };
+    long long job = (long long)blockIdx.x * kWarps + warp;
+    if (job >= jobs)
+        return;
+    Job cur = find(job);
+    uint64_t S[RPT][2];                           // columns (0, 1) and (2, 3)
     RowIn<RPT> in;
-    if (len > 0)
-        in = load(r0);
-    for (int r = 0; r < len; ++r) {
-        float k[RPT], q[RPT];
-        unpack_row(in.k, k);
-        unpack_row(in.q, q);
-        const uint2 v = in.v;
-        const float de = expf(in.g), be = in.beta;
-        if (r + 1 < len)
-            in = load(r0 + r + 1);
-        float kk = 0.f, qq = 0.f, kq = 0.f;
-        uint64_t dk[2] = {0, 0}, dq[2] = {0, 0};
+    {
+        const long long so = place(cur);
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            kk = fmaf(k[i], k[i], kk);
-            qq = fmaf(q[i], q[i], qq);
-            kq = fmaf(k[i], q[i], kq);
-            const uint64_t k2 = pack2(k[i], k[i]), q2 = pack2(q[i], q[i]);
-            dk[0] = fma2(S[i][0], k2, dk[0]);
-            dk[1] = fma2(S[i][1], k2, dk[1]);
-            dq[0] = fma2(S[i][0], q2, dq[0]);
-            dq[1] = fma2(S[i][1], q2, dq[1]);
+            const ulonglong2 x = a.state && cur.slot >= 0
+                                     ? *reinterpret_cast<const ulonglong2 *>(a.state + so + (long long)i * a.dv)
+                                     : make_ulonglong2(0, 0);
+            S[i][0] = x.x;
+            S[i][1] = x.y;
         }
-        float x[11] = {kk, qq, kq};
-        unpack2(dk[0], x[3], x[4]);
-        unpack2(dk[1], x[5], x[6]);
-        unpack2(dq[0], x[7], x[8]);
-        unpack2(dq[1], x[9], x[10]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-            for (int e = 0; e < 11; ++e)
-                x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
-        // k and q count divided by their norms: fk, fq stand beside the sums
-        const float fk = a.l2norm ? 1.f / sqrtf(x[0] + a.l2_eps) : 1.f;
-        const float fq = a.l2norm ? 1.f / sqrtf(x[1] + a.l2_eps) : 1.f;
-        const float dfk = de * fk;
-        const float w0 = be * (bf16_lo(v.x) - dfk * x[3]), w1 = be * (bf16_hi(v.x) - dfk * x[4]);
-        const float w2 = be * (bf16_lo(v.y) - dfk * x[5]), w3 = be * (bf16_hi(v.y) - dfk * x[6]);
-        const uint64_t u0 = pack2(fk * w0, fk * w1), u1 = pack2(fk * w2, fk * w3), d2 = pack2(de, de);
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            const uint64_t k2 = pack2(k[i], k[i]);
-            S[i][0] = fma2(k2, u0, mul2(S[i][0], d2));
-            S[i][1] = fma2(k2, u1, mul2(S[i][1], d2));
-        }
-        if (grp == 0) {
-            const float p = x[2] * fk, sc = a.scale * fq;
-            *reinterpret_cast<uint2 *>(out + (long long)(r0 + r) * a.os.tok) =
-                make_uint2(pack_bf16x2(sc * fmaf(p, w0, de * x[7]), sc * fmaf(p, w1, de * x[8])),
-                           pack_bf16x2(sc * fmaf(p, w2, de * x[9]), sc * fmaf(p, w3, de * x[10])));
-        }
+        if (cur.slot >= 0 && cur.len > 0)
+            in = load(cur, cur.r0);
     }
-    if (a.state_out && (len > 0 || a.state_out != a.state))
+    for (;;) {
+        job += stride;
+        const bool more = job < jobs;
+        Job nxt = cur;
+        if (more) {
+            nxt = find(job);
+            __syncwarp();                         // the buffer has been read
+            if (a.state && nxt.slot >= 0) {
+                const float *from = a.state + place(nxt);
 #pragma unroll
-        for (int i = 0; i < RPT; ++i)
-            *reinterpret_cast<ulonglong2 *>(a.state_out + so + (long long)i * a.dv) =
-                make_ulonglong2(S[i][0], S[i][1]);
+                for (int i = 0; i < RPT; ++i)
+                    cp_async<16>(&buf[i][lane], from + (long long)i * a.dv);
+            }
+        }
+        const bool rows_next = more && nxt.slot >= 0 && nxt.len > 0;
+        const int len = cur.slot >= 0 ? cur.len : 0;
+        __nv_bfloat16 *out = a.out + (long long)cur.h * a.os.head + cur.col;
+        if (cur.slot < 0) {
+            if (lane == 0)
+                seq_flag(a.sq, GATTN_STATUS_RANGE);
+            for (int t = cur.r0 + grp; t < cur.r0 + cur.len; t += 8)
+                *reinterpret_cast<uint2 *>(out + (long long)t * a.os.tok) = make_uint2(0, 0);
+        }
+        if (len == 0 && rows_next)
+            in = load(nxt, nxt.r0);
+        for (int r = 0; r < len; ++r) {
+            float k[RPT], q[RPT];
+            unpack_row(in.k, k);
+            unpack_row(in.q, q);
+            const uint2 v = in.v;
+            const float de = expf(in.g), be = in.beta;
+            if (r + 1 < len)
+                in = load(cur, cur.r0 + r + 1);
+            else if (rows_next)
+                in = load(nxt, nxt.r0);
+            float kk = 0.f, qq = 0.f, kq = 0.f;
+            uint64_t dk[2] = {0, 0}, dq[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                kk = fmaf(k[i], k[i], kk);
+                qq = fmaf(q[i], q[i], qq);
+                kq = fmaf(k[i], q[i], kq);
+                const uint64_t k2 = pack2(k[i], k[i]), q2 = pack2(q[i], q[i]);
+                dk[0] = fma2(S[i][0], k2, dk[0]);
+                dk[1] = fma2(S[i][1], k2, dk[1]);
+                dq[0] = fma2(S[i][0], q2, dq[0]);
+                dq[1] = fma2(S[i][1], q2, dq[1]);
+            }
+            float x[11] = {kk, qq, kq};
+            unpack2(dk[0], x[3], x[4]);
+            unpack2(dk[1], x[5], x[6]);
+            unpack2(dq[0], x[7], x[8]);
+            unpack2(dq[1], x[9], x[10]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 11; ++e)
+                    x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
+            // k and q count divided by their norms: fk, fq stand beside the sums
+            const float fk = a.l2norm ? 1.f / sqrtf(x[0] + a.l2_eps) : 1.f;
+            const float fq = a.l2norm ? 1.f / sqrtf(x[1] + a.l2_eps) : 1.f;
+            const float dfk = de * fk;
+            const float w0 = be * (bf16_lo(v.x) - dfk * x[3]), w1 = be * (bf16_hi(v.x) - dfk * x[4]);
+            const float w2 = be * (bf16_lo(v.y) - dfk * x[5]), w3 = be * (bf16_hi(v.y) - dfk * x[6]);
+            const uint64_t u0 = pack2(fk * w0, fk * w1), u1 = pack2(fk * w2, fk * w3), d2 = pack2(de, de);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+                const uint64_t k2 = pack2(k[i], k[i]);
+                S[i][0] = fma2(k2, u0, mul2(S[i][0], d2));
+                S[i][1] = fma2(k2, u1, mul2(S[i][1], d2));
+            }
+            if (grp == 0) {
+                const float p = x[2] * fk, sc = a.scale * fq;
+                *reinterpret_cast<uint2 *>(out + (long long)(cur.r0 + r) * a.os.tok) =
+                    make_uint2(pack_bf16x2(sc * fmaf(p, w0, de * x[7]), sc * fmaf(p, w1, de * x[8])),
+                               pack_bf16x2(sc * fmaf(p, w2, de * x[9]), sc * fmaf(p, w3, de * x[10])));
+            }
+        }
+        if (cur.slot >= 0 && a.state_out && (len > 0 || a.state_out != a.state)) {
+            float *to = a.state_out + place(cur);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i)
+                *reinterpret_cast<ulonglong2 *>(to + (long long)i * a.dv) = make_ulonglong2(S[i][0], S[i][1]);
+        }
+        if (!more)
+            return;
+        cp_async_wait_all();
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+            const ulonglong2 x = a.state && nxt.slot >= 0 ? buf[i][lane] : make_ulonglong2(0, 0);
+            S[i][0] = x.x;
+            S[i][1] = x.y;
+        }
+        cur = nxt;
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_delta_step(const DeltaArgs &a, cudaStream_t s)
 {
-    const long long jobs = (long long)a.sq.n * a.Hv * (a.dv / 16);
-    if (jobs / kWarps >= 0x7fffffff)
-        return cudaErrorInvalidConfiguration;
+    int sms = 0;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess)
+        return e;
+    const long long ctas = ((long long)a.sq.n * a.Hv * (a.dv / 16) + kWarps - 1) / kWarps;
     return launch_seq(a.dk == 64 ? delta_rows_kernel<64> : delta_rows_kernel<128>,
-                      dim3((unsigned)((jobs + kWarps - 1) / kWarps)), dim3(kWarps * 32), s, a);
+                      dim3((unsigned)std::min<long long>(ctas, 3 * sms)), dim3(kWarps * 32), s, a);
 }
 
 }  // namespace gattn
