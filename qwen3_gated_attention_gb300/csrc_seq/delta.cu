@@ -9,11 +9,15 @@
 // whole sectors).  One pass over it gives both sums of a row,
 //   S^T k and S^T q  (out = scale (e^g S^T q + (q.k) w)),
 // added up over the groups by shuffles: no shared memory, no barrier, and warps at
-// different points cover each other's latencies.  (A CTA per head with the sums in
-// shared memory spent a fifth of its time at barriers: 39 us for 32 sequences of 4
-// rows and 32 heads of 128 x 128.)  32 sequences of one row take 25 us, 79 % of the copy
-// rate over 134 MB of state; of four rows 38 us, 53 %: a row adds 4 us of arithmetic
-// and shuffles to each warp's way.  One sequence of one row: 3.7 us.
+// different points cover each other's latencies.  A warp takes one such job after
+// another; the next one's state and first row are on their way while it works.
+//
+// 32 sequences and 32 heads of 128 x 128: one row each 25 us, 80 % of the copy rate over
+// 134 MB of state; four rows 37 us, 55 %: a row adds 4 us, its 560 instructions at three
+// warps a scheduler.  One sequence of one row: 3.5 us.  (A CTA per head with the sums in
+// shared memory spent a fifth of its time at barriers: 39 us for the four rows; each job
+// a warp of its own 25.4 and 38.9 us; pairs along k instead of along the columns made
+// no difference.)
 #include <algorithm>
 
 #include "seq.cuh"
@@ -53,17 +57,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) delta_rows_kernel(const __grid
     constexpr int RPT = DK / 8;                   // k-elements of a lane
     __shared__ ulonglong2 ahead[kWarps][RPT][32]; // the next job's state: a lane's own elements
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane >> 2;
-    const int parts = a.dv / 16;
-    const long long jobs = (long long)a.sq.n * a.Hv * parts, stride = (long long)gridDim.x * kWarps;
+    // all of it below 2^31, see the launch
+    const unsigned parts = a.dv / 16, heads = a.Hv, per_key = a.Hv / a.Hk;
+    const unsigned jobs = a.sq.n * heads * parts, stride = gridDim.x * kWarps;
     ulonglong2 (*const buf)[32] = ahead[warp];
     struct Job {
         int h, col, r0, len, slot;
     };
-    auto find = [&](long long job) {
+    auto find = [&](unsigned job) {
         Job j;
-        const int s = (int)(job / parts / a.Hv);
-        j.h = (int)(job / parts % a.Hv);
-        j.col = (int)(job % parts) * 16 + (lane & 3) * 4;
+        const unsigned sh = job / parts, s = sh / heads;
+        j.h = sh - s * heads;
+        j.col = (job - sh * parts) * 16 + (lane & 3) * 4;
         seq_rows(a.sq, s, j.r0, j.len);
         j.slot = seq_slot_warp(a.sq, s, true);
         return j;
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) delta_rows_kernel(const __grid
     };
     auto load = [&](const Job &j, int t) {
         RowIn<RPT> r;
-        const int hk = j.h / (a.Hv / a.Hk);
+        const int hk = (unsigned)j.h / per_key;
         const uint4 *kp = reinterpret_cast<const uint4 *>(a.k + t * a.ks.tok + hk * a.ks.head + grp * RPT);
         const uint4 *qp = reinterpret_cast<const uint4 *>(a.q + t * a.qs.tok + hk * a.qs.head + grp * RPT);
 #pragma unroll
@@ -86,7 +91,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) delta_rows_kernel(const __grid
         r.beta = a.beta[t * a.bt + j.h];
         return r;
     };
-    long long job = (long long)blockIdx.x * kWarps + warp;
+    unsigned job = blockIdx.x * kWarps + warp;
     if (job >= jobs)
         return;
     Job cur = find(job);
@@ -210,7 +215,9 @@ cudaError_t launch_delta_step(const DeltaArgs &a, cudaStream_t s)
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess)
         return e;
-    const long long ctas = ((long long)a.sq.n * a.Hv * (a.dv / 16) + kWarps - 1) / kWarps;
+    const long long jobs = (long long)a.sq.n * a.Hv * (a.dv / 16), ctas = (jobs + kWarps - 1) / kWarps;
+    if (jobs > 0x7fffffff - 3 * kWarps * sms)
+        return cudaErrorInvalidConfiguration;
     return launch_seq(a.dk == 64 ? delta_rows_kernel<64> : delta_rows_kernel<128>,
                       dim3((unsigned)std::min<long long>(ctas, 3 * sms)), dim3(kWarps * 32), s, a);
 }
