@@ -295,3 +295,38 @@ def test_an_output_belongs_to_the_stream_that_writes_it(own):
         out = dv.prompt_attention(x["q"], kc, vc, cu, cache_pos=pos, stream=s.cuda_stream)
     torch.cuda.synchronize()
     assert out.data_ptr() != at and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 96)])
+@pytest.mark.parametrize("how", ["apart", "inplace", "no_state", "not_kept"])
+def test_more_states_than_warps(dk, dv, how):
+    """A warp takes several (sequence, head, columns) in turn, with empty and skipped
+    sequences among them."""
+    n = 44
+    lens = [(3 * i) % 4 for i in range(n)]
+    slots = [(7 * i) % 50 for i in range(n)]
+    slots[5], slots[9], slots[20], slots[43] = -1, slots[8], 50, slots[0]
+    skipped = (5, 9, 20, 43)
+    if how == "no_state":
+        slots, skipped = None, ()
+    c = _case(4, 8, dk, dv, lens, dk + dv + 7, slots=slots, nslots=50 if slots else None, extra=2)
+    out, so = _run("step", c, state=how != "no_state", inplace=how == "inplace",
+                   keep=how not in ("not_kept", "no_state"))
+    if how != "inplace":
+        _check(c, out, so, state=how != "no_state", skipped=skipped)
+        return
+    # in place: the same, and what no sequence owns as it was
+    want, apart = _run("step", c)
+    assert torch.equal(out, want)
+    own = [slots[i] for i in range(n) if i not in skipped]
+    assert torch.equal(so[own], apart[own])
+    rest = [i for i in range(50) if i not in own]
+    assert torch.equal(so[rest], c["S"][rest])
+
+
+@pytest.mark.parametrize("T", [700, 1450])
+@pytest.mark.parametrize("H,Hk,d,x_dtype", [(9, 3, 192, BF), (4, 1, 64, torch.float32)])
+def test_rows_by_two_and_four_warps(T, H, Hk, d, x_dtype):
+    from tests import test_gpu_prompt_rows as P
+    c = P._case(H, Hk, d, [T - 301, 0, 300, 1], [5, 2, 0, 9], T, x_dtype, 0.25, T)
+    P._check(c, P._run(c))
