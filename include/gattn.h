@@ -526,8 +526,8 @@ gattn_status gattn_layer_set_test_wait(gattn_layer *layer, int64_t wait_limit_ns
  *     ("token") and of the head; the elements of a head are contiguous.  bf16
  *     and fp32 rows: base 16-byte aligned, strides positive multiples of 8
  *     elements.  Slices of a wider projection output are such tensors.  An
- *     output's strides must keep its rows apart (the larger stride spans all
- *     steps of the smaller).
+ *     output's strides, those of a cache that is written among them, must keep
+ *     its rows apart: in order of size, each spans all steps of the smaller ones.
  *   - Offsets, positions, slots and status are 4-byte aligned.
  *   - Outputs must not overlap inputs unless an entry point says so.
  *   - `status` (device) uint32 [1], may be NULL: the kernels OR GATTN_STATUS_*

@@ -1,5 +1,6 @@
 // seq_api.cu -- host side of the packed-sequence entry points of gattn.h:
 // argument checks and parameter blocks.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -55,20 +56,41 @@ gattn_status check_rows(const char *name, const void *p, int64_t tok, int64_t he
     return GATTN_OK;
 }
 
-// Rows that are written: no two of them may share memory.
+// One axis of a tensor that is written: its step in elements and its entries.
+struct Axis {
+    int64_t step, n;
+};
+
+// Rows of d elements that are written: no two of them may share memory.  From the
+// nearest step on, each has to span all that the nearer ones reach.
+gattn_status check_apart(const char *name, int64_t d, std::initializer_list<Axis> axes)
+{
+    Axis a[3];
+    int n = 0;
+    for (const Axis &x : axes)
+        if (x.n > 1)
+            a[n++] = x;
+    std::sort(a, a + n, [](const Axis &x, const Axis &y) { return x.step < y.step; });
+    // steps stay below 2^38 and entries below 2^31: with a span of at most 2^62 so far,
+    // the next one is compared by division and cannot overflow before it is refused
+    int64_t span = d;
+    for (int i = 0; i < n; ++i) {
+        if (a[i].step < span)
+            return bad(GATTN_E_INVALID_ARG, "%s strides make its rows overlap (a step of %lld within %lld elements)",
+                       name, (long long)a[i].step, (long long)span);
+        if (a[i].n - 1 > ((1ll << 62) - span) / a[i].step)
+            span = 1ll << 62;
+        else
+            span += (a[i].n - 1) * a[i].step;
+    }
+    return GATTN_OK;
+}
+
 gattn_status check_out(const char *name, const void *p, int64_t tok, int64_t head, int64_t d, int64_t rows,
                        int64_t heads)
 {
     CHECK(check_rows(name, p, tok, head));
-    // the nearer of the two steps spans a head row, the farther one all of the nearer's:
-    // out >= (n_in - 1) in + d
-    const int64_t in = tok < head ? tok : head, out = tok < head ? head : tok;
-    const int64_t n_in = tok < head ? rows : heads, n_out = tok < head ? heads : rows;
-    if ((n_in > 1 && in < d) || (n_out > 1 && out < d) ||
-        (n_in > 1 && n_out > 1 && (out - d) / in < n_in - 1))
-        return bad(GATTN_E_INVALID_ARG, "%s strides %lld, %lld make its rows overlap", name, (long long)tok,
-                   (long long)head);
-    return GATTN_OK;
+    return check_apart(name, d, {{tok, rows}, {head, heads}});
 }
 
 // Device arrays of 32-bit words; NULL passes.
@@ -122,12 +144,16 @@ gattn_status gattn_prompt_rows(const gattn_prompt_rows_desc *p, gattn_stream str
     CHECK(check_rows("v", p->v, p->v_stride_token, p->v_stride_head));
     CHECK(check_out("q_out", p->q_out, p->o_stride_token, p->o_stride_head, p->head_dim, p->total_rows,
                     p->num_heads));
-    CHECK(check_out("k_cache", p->k_cache, p->kc_stride_token, p->kc_stride_head, p->head_dim,
-                    p->cache_capacity, p->num_kv_heads));
-    CHECK(check_out("v_cache", p->v_cache, p->vc_stride_token, p->vc_stride_head, p->head_dim,
-                    p->cache_capacity, p->num_kv_heads));
+    CHECK(check_rows("k_cache", p->k_cache, p->kc_stride_token, p->kc_stride_head));
     CHECK(check_rows("k_cache", p->k_cache, p->kc_stride_batch, 8));
+    CHECK(check_rows("v_cache", p->v_cache, p->vc_stride_token, p->vc_stride_head));
     CHECK(check_rows("v_cache", p->v_cache, p->vc_stride_batch, 8));
+    CHECK(check_apart("k_cache", p->head_dim, {{p->kc_stride_token, p->cache_capacity},
+                                               {p->kc_stride_head, p->num_kv_heads},
+                                               {p->kc_stride_batch, p->cache_batch}}));
+    CHECK(check_apart("v_cache", p->head_dim, {{p->vc_stride_token, p->cache_capacity},
+                                               {p->vc_stride_head, p->num_kv_heads},
+                                               {p->vc_stride_batch, p->cache_batch}}));
     CHECK(check_words({p->cu_rows, p->cache_pos, p->slots, p->status}));
     if (misaligned(p->q_norm) || misaligned(p->k_norm))
         return bad(GATTN_E_INVALID_ARG, "q_norm and k_norm must be 16-byte aligned");
