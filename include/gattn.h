@@ -678,9 +678,8 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *desc, gat
  * gattn_delta_prompt is for prompts: it works through the rows in chunks.
  * gattn_delta_step is for one to a few new rows of many sequences: it works
  * row by row.  Both take any lengths and differ in rounding only: the step
- * computes in fp32; the prompt's state is as exact (products of operands with
- * 22 bits, fp32 sums), its out sums products of operands with 11 bits before
- * the rounding to bf16.
+ * computes in fp32; the prompt multiplies operands of 22 bits into fp32 sums,
+ * and both round out once, to bf16.
  * num_seqs > 0 with total_rows == 0 copies the states.  k_dim 64 or 128; v_dim a
  * multiple of 32 up to 256 (else GATTN_E_UNSUPPORTED).
  */

@@ -14,19 +14,17 @@
 // before it left there (S^T K^T, Y^T T^T, W^T K).
 //
 // Precision: the tensor cores multiply 16-bit floats.  K and Q rows are bf16 and
-// become fp16 exactly up to a power of two per row.  In the chain S, Y, W and T are
-// split into two fp16 parts each (22 bits; 11 + 11), two products where the other
-// operand is exact, three where both are split, so the state keeps fp32-like
-// accuracy.  The answers O are rounded to bf16 (8 bits) at the end and to nowhere
-// else, so for them S, W and A count with the upper part alone (11 bits, off by at
-// most 2^-12 a term; errors of the terms of a sum are independent, and stay an eighth
-// of the last rounding).  fp16's range is covered by a power of two per state column
-// that follows the column's size.
+// become fp16 exactly up to a power of two per row; S, Y, W, T and A are split
+// into two fp16 parts each (22 bits; 11 + 11), two products where the other
+// operand is exact, three where both are split.  The answers need both parts too: a
+// row that overwrites what the state held has Q S and A W cancel, and what is left
+// of 11 bits of each can be all wrong.  fp16's range is covered by a power of two per
+// state column that follows the column's size.
 //
-// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 221 us
-// (1.73 us a chunk; its mma.sync instructions alone 0.3 us of it, the rest what each
-// of them waits for), 8 sequences of 1 to 1024 rows 114 us, the 1024 rows being the
-// longest chain (3.5 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
+// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 231 us
+// (1.8 us a chunk; its mma.sync instructions alone 0.3 us of it, the rest what each
+// of them waits for), 8 sequences of 1 to 1024 rows 128 us, the 1024 rows being the
+// longest chain (4.0 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
 // slower: the state's update fused with the next chunk's K S (415 us: spills), rows
 // brought in by bulk copies (96 small ones a chunk), helpers with unrolled loops
 // (their code pushes the chain's out of the instruction cache: 267 to 320 us).
@@ -50,7 +48,8 @@ struct alignas(16) Stage {
     alignas(16) __nv_bfloat16 v[kC][16 * NCW + 8];
     alignas(16) __half t_hi[kC][kTS];              // T^T: [j][i]
     alignas(16) __half t_lo[kC][kTS];
-    alignas(16) __half aq[kC][kTS];                // A^T: [j][i]
+    alignas(16) __half a_hi[kC][kTS];              // A^T: [j][i]
+    alignas(16) __half a_lo[kC][kTS];
     alignas(16) float ar[kC];                      // per row, see the chain
     alignas(16) float beta[kC];
     alignas(16) float cr[kC];
@@ -79,10 +78,10 @@ struct Roles {
     static constexpr int THREADS = (CHAIN + OUT + HELP) * 32;
 };
 
-// What chain warps hand their output warp: S's upper parts, as operands, and W.
+// What chain warps hand their output warp: S in parts, as operands, and W.
 template <int DK>
 struct alignas(16) Handed {
-    uint4 s[DK / 16][32];
+    uint4 s[DK / 16][2][32];
     float4 w[4][32];
     float2 unit[32];
 };
@@ -98,12 +97,10 @@ template <int DK, int NCW>
 struct alignas(16) Shared {
     using R = Roles<NCW>;
     Stage<DK, NCW> st[R::HELP];
-    // by turns, so that nobody waits for what was handed on before to be read
-    Handed<DK> to[R::SPLIT ? NCW : 1][R::KH];
-    Share share[R::SPLIT ? NCW : 1][R::KH][R::KH];         // [columns][turn][half]
+    Handed<DK> to[R::SPLIT ? NCW : 1];
+    Share share[R::SPLIT ? NCW : 1][R::KH];
     uint64_t full[R::HELP], empty[R::HELP];
-    uint64_t s_full[2][2], w_full[2][2], taken[2][2];      // [columns][turn]
-    uint64_t shared[2][2][2];                              // [columns][turn][half]
+    uint64_t s_full[2], w_full[2], taken[2], shared[2][2], read[2][2];
     int abort;
 };
 static_assert((kTS * 2) % 16 == 0 && (kLS * 4) % 16 == 0 && sizeof(Stage<128, 2>) % 16 == 0 &&
@@ -317,8 +314,10 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
                     lt[1] = l1;
             } else
                 split_h2(l0, l1, vh[half], vl[half]);
-            *reinterpret_cast<uint32_t *>(&s.aq[j][i0]) =
-                pack_h2(i0 >= j ? d0 * kq[half * 2] : 0.f, i0 + 1 >= j ? d1 * kq[half * 2 + 1] : 0.f);
+            uint32_t wh, wl;
+            split_h2(i0 >= j ? d0 * kq[half * 2] : 0.f, i0 + 1 >= j ? d1 * kq[half * 2 + 1] : 0.f, wh, wl);
+            *reinterpret_cast<uint32_t *>(&s.a_hi[j][i0]) = wh;
+            *reinterpret_cast<uint32_t *>(&s.a_lo[j][i0]) = wl;
         }
         if (tile == 2) {
             bh[0][0] = vh[0], bl[0][0] = vl[0];
@@ -452,12 +451,12 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             mbar_init(&sh.empty[i], R::CHAIN + R::OUT);
         }
         for (int i = 0; i < R::OUT; ++i) {
+            mbar_init(&sh.s_full[i], R::KH);
+            mbar_init(&sh.w_full[i], 1);
+            mbar_init(&sh.taken[i], 1);
             for (int k = 0; k < 2; ++k) {
-                mbar_init(&sh.s_full[i][k], R::KH);
-                mbar_init(&sh.w_full[i][k], 1);
-                mbar_init(&sh.taken[i][k], 1);
-                mbar_init(&sh.shared[i][k][0], 1);
-                mbar_init(&sh.shared[i][k][1], 1);
+                mbar_init(&sh.shared[i][k], 1);
+                mbar_init(&sh.read[i][k], 1);
             }
         }
         sh.abort = 0;
@@ -541,12 +540,6 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 }
             }
     };
-    // one k16 step of Q S: the state's upper part alone
-    auto times_queries = [&](float (&D)[4][4], const uint32_t (&hi)[4], const uint32_t (&b)[2][4]) {
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-            mma(D[nt], hi, b[nt / 2][(nt & 1) * 2], b[nt / 2][(nt & 1) * 2 + 1]);
-    };
     // O = scale (a Q S + A W), O holding Q S, and its rows' way out through where
     // their values were: a row of 16 columns per lane
     auto finish_rows = [&](float (&O)[4][4], const float (&W)[4][4], Stage<DK, NCW> &st, int c, float u0,
@@ -559,19 +552,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             O[nt][2] *= aa.x;
             O[nt][3] *= aa.y;
         }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const float (&w0)[4] = W[2 * kk], (&w1)[4] = W[2 * kk + 1];
-            const uint32_t w[4] = {pack_h2(w0[0], w0[1]), pack_h2(w0[2], w0[3]), pack_h2(w1[0], w1[1]),
-                                   pack_h2(w1[2], w1[3])};
-#pragma unroll
-            for (int n2 = kk; n2 < 2; ++n2) {
-                uint32_t x[4];
-                ldsm_x4_trans(x, smem_u32(&st.aq[kk * 16 + tr][n2 * 16 + tc]));
-                mma(O[n2 * 2], w, x[0], x[1]);
-                mma(O[n2 * 2 + 1], w, x[2], x[3]);
-            }
-        }
+        times_lower(O, W, st.a_hi, st.a_lo);
 #pragma unroll
         for (int n2 = 0; n2 < 2; ++n2) {
             uint32_t x[4];
@@ -596,11 +577,11 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     unsigned phase = 0;                    // per stage
     if (R::SPLIT && warp >= R::CHAIN) {
         // ------------------------------------------------ output warps
-        for (int c = 0, use = 0; c < chunks; ++use) {
-            const int w = c % R::HELP, turn = use & 1, ph = use >> 1 & 1;
-            Handed<DK> &from = sh.to[R::SPLIT ? cw : 0][R::SPLIT ? turn : 0];
+        Handed<DK> &from = sh.to[R::SPLIT ? cw : 0];
+        for (int c = 0, turn = 0; c < chunks; turn ^= 1) {
+            const int w = c % R::HELP;
             ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort) &&
-                                             tc5_wait(&sh.s_full[cw & 1][turn], ph, abort));
+                                             tc5_wait(&sh.s_full[cw & 1], turn, abort));
             if (!ok)
                 break;
             phase ^= 1u << w;
@@ -608,13 +589,13 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             float O[4][4] = {}, W[4][4];
 #pragma unroll 2
             for (int ks = 0; ks < DK / 16; ++ks) {
-                const uint4 u = from.s[ks][lane];
-                const uint32_t hi[4] = {u.x, u.y, u.z, u.w};
+                const uint4 uh = from.s[ks][0][lane], ul = from.s[ks][1][lane];
+                const uint32_t hi[4] = {uh.x, uh.y, uh.z, uh.w}, lo[4] = {ul.x, ul.y, ul.z, ul.w};
                 uint32_t b[2][4];
                 load_rows(b, st.q, ks);
-                times_queries(O, hi, b);
+                times_rows(O, O, hi, lo, b);
             }
-            ok = __all_sync(0xffffffffu, tc5_wait(&sh.w_full[cw & 1][turn], ph, abort));
+            ok = __all_sync(0xffffffffu, tc5_wait(&sh.w_full[cw & 1], turn, abort));
             if (!ok)
                 break;
 #pragma unroll
@@ -628,7 +609,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             const float2 u = from.unit[lane];
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&sh.taken[cw & 1][turn]);
+                mbar_arrive(&sh.taken[cw & 1]);
             finish_rows(O, W, st, c, u.x, u.y);
             c += st.more ? 0 : 1;
             __syncwarp();
@@ -681,25 +662,21 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             top0[e >> 1] = fmaxf(top0[e >> 1], fabsf(S[j][e]));
-    // X and top of the column's two halves together; false if the wait ran out.  A
-    // buffer comes round again after the other half has answered for the one between.
-    // `tell`, if any, hears that this warp's S has been handed on
+    // X and top of the column's two halves together; false if the wait ran out
     int turns = 0;
-    auto add_shares = [&](float (&X)[4][4], float (&top)[2], uint64_t *tell) {
-        Share &mine = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? turns & 1 : 0][R::SPLIT ? half : 0];
-        Share &other = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? turns & 1 : 0][R::SPLIT ? half ^ 1 : 0];
-        uint64_t (&bar)[2] = sh.shared[cw & 1][turns & 1];
+    auto add_shares = [&](float (&X)[4][4], float (&top)[2]) {
+        Share &mine = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? half : 0];
+        Share &other = sh.share[R::SPLIT ? cw : 0][R::SPLIT ? half ^ 1 : 0];
+        if (turns > 0 && !__all_sync(0xffffffffu, tc5_wait(&sh.read[cw & 1][half], (turns - 1) & 1, abort)))
+            return false;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
             mine.x[nt][lane] = make_float4(X[nt][0], X[nt][1], X[nt][2], X[nt][3]);
         mine.top[lane] = make_float2(top[0], top[1]);
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&bar[half ^ 1]);
-            if (tell)
-                mbar_arrive(tell);
-        }
-        if (!__all_sync(0xffffffffu, tc5_wait(&bar[half], turns >> 1 & 1, abort)))
+        if (lane == 0)
+            mbar_arrive(&sh.shared[cw & 1][half ^ 1]);
+        if (!__all_sync(0xffffffffu, tc5_wait(&sh.shared[cw & 1][half], turns & 1, abort)))
             return false;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -711,19 +688,22 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         }
         top[0] = fmaxf(top[0], other.top[lane].x);
         top[1] = fmaxf(top[1], other.top[lane].y);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sh.read[cw & 1][half ^ 1]);
         ++turns;
         return true;
     };
     if (R::SPLIT) {
         float none[4][4] = {};
-        ok = add_shares(none, top0, nullptr);
+        ok = add_shares(none, top0);
     }
     top0[0] = quad_max(top0[0]);
     top0[1] = quad_max(top0[1]);
     bool first = true;
-    for (int c = 0, use = 0; ok && c < chunks; ++use) {
-        const int w = c % R::HELP, turn = use & 1;
-        Handed<DK> &to = sh.to[R::SPLIT ? cw : 0][R::SPLIT ? turn : 0];
+    Handed<DK> &to = sh.to[R::SPLIT ? cw : 0];
+    for (int c = 0, turn = 0; ok && c < chunks; turn ^= 1) {
+        const int w = c % R::HELP;
         ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
         if (!ok)
             break;
@@ -762,8 +742,8 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         // K S (and Q S)
         float X[4][4] = {}, O[4][4] = {};
         __half2 top[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
-        if (R::SPLIT && use >= 2) {
-            ok = __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1][turn], (use >> 1 & 1) ^ 1, abort));
+        if (R::SPLIT && !first) {
+            ok = __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1], turn ^ 1, abort));
             if (!ok)
                 break;
         }
@@ -779,8 +759,10 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             if (!R::SPLIT)
                 load_rows(bq, st.q, ks);
             split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
-            if (R::SPLIT)
-                to.s[ks0 + ks][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (R::SPLIT) {
+                to.s[ks0 + ks][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                to.s[ks0 + ks][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 top[e & 1] = __hmax2(top[e & 1], __habs2(*reinterpret_cast<const __half2 *>(&hi[e])));
@@ -789,7 +771,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             else
                 times_rows(X, X, hi, lo, bk[ks & 1]);
             if (!R::SPLIT)
-                times_queries(O, hi, bq);
+                times_rows(O, O, hi, lo, bq);
         }
         if (R::SPLIT)
 #pragma unroll
@@ -804,7 +786,10 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             m[hf] = fmaxf(th.x, th.y);
         }
         if (R::SPLIT) {
-            ok = add_shares(X, m, &sh.s_full[cw & 1][turn]);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.s_full[cw & 1]);
+            ok = add_shares(X, m);
             if (!ok)
                 break;
         }
@@ -829,7 +814,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             to.unit[lane] = make_float2(unit[0], unit[1]);
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&sh.w_full[cw & 1][turn]);
+                mbar_arrive(&sh.w_full[cw & 1]);
         }
         // S <- gamma S + (c r W)^T K
         float ounit[2];

@@ -1,0 +1,74 @@
+"""gattn_delta_prompt and gattn_delta_step over the whole range of the rule: keys of any
+size, rows that stretch the state, states and values of very different sizes, answers
+that are small differences.  Both forms are held to the same bounds."""
+import pytest
+import torch
+
+from tests.delta_walk import judge
+from tests.seq_refs import cu_of
+from tests.test_gpu_delta import _fn
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+BOTH = pytest.mark.parametrize("name", ["prompt", "step"])
+# 32, 64 and 128 state columns of a CTA: one sequence, and ten of eight heads
+SHAPES = [(1, 2, 64, 32, 1), (4, 8, 64, 64, 10), (4, 8, 128, 128, 10), (1, 2, 128, 96, 1)]
+SHAPE = pytest.mark.parametrize("Hk,Hv,dk,dv,n", SHAPES)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from qwen3_gated_attention_gb300 import build
+    build.build()
+
+
+def _inputs(Hk, Hv, dk, dv, n, rows, seed, decay=0.1):
+    """n sequences of `rows` rows; keys and queries of unit length but for their rounding."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)      # noqa: E731
+    T = n * rows
+    norm = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    return dict(q=norm(r(T, Hk, dk)).to(BF), k=norm(r(T, Hk, dk)).to(BF), v=r(T, Hv, dv).to(BF),
+                g=-decay * torch.rand(T, Hv, generator=g), beta=torch.sigmoid(r(T, Hv)),
+                S=0.3 * r(n, Hv, dk, dv), rows=rows, n=n)
+
+
+def _hold(name, x, scale=1.0, eps=None, state=True, bounded=True, only=None):
+    """Runs a form on the inputs and holds every sequence (or the ones in `only`)."""
+    dev = {key: t.cuda() for key, t in x.items() if isinstance(t, torch.Tensor)}
+    so = torch.full_like(dev["S"], 9.0)
+    out = _fn(name)(dev["q"], dev["k"], dev["v"], dev["g"], dev["beta"], cu_of([x["rows"]] * x["n"], "cuda"),
+                    state=dev["S"] if state else None, state_out=so, scale=scale, qk_l2norm=eps is not None,
+                    l2_eps=eps or 0.0)
+    torch.cuda.synchronize()
+    out, so = out.cpu(), so.cpu()
+    for s in range(x["n"]) if only is None else only:
+        a = slice(s * x["rows"], (s + 1) * x["rows"])
+        S0 = x["S"][s] if state else torch.zeros_like(x["S"][s])
+        judge([x[key][a] for key in ("q", "k", "v", "g", "beta")] + [S0], out[a], so[s], scale, eps, bounded)
+
+
+# --------------------------------------------- answers that are small differences
+
+@BOTH
+@SHAPE
+@pytest.mark.parametrize("size", [10.0, 1e3, 1e5])
+def test_answers_that_are_small_differences(name, Hk, Hv, dk, dv, n, size):
+    """The query is the key of a row that overwrites: its answer is the value, and what
+    the state held along that key cancels."""
+    x = _inputs(Hk, Hv, dk, dv, n, 70, 12, decay=0.0)
+    x["q"] = x["k"].clone()
+    x["beta"][:] = 1.0
+    x["S"] = x["S"] * size
+    _hold(name, x, eps=0.0, only=(0, n - 1))
+
+
+@BOTH
+@SHAPE
+@pytest.mark.parametrize("rows", [1, 31, 32, 33, 70, 129, 200])
+def test_every_length_to_fp32(name, Hk, Hv, dk, dv, n, rows):
+    x = _inputs(Hk, Hv, dk, dv, n, rows, 13 + rows)
+    _hold(name, x, dk ** -0.5, 1e-6, only=(0, n - 1))
+    _hold(name, x, dk ** -0.5, 1e-6, state=False, only=(0,))
