@@ -1,11 +1,15 @@
 // delta_chunk.cu -- the gated delta rule over prompts, 32 rows at a time.
 //
-// With G_i the running sum of the log decays inside a chunk, a_i = e^{G_i}, and S
-// the state before it, the rows of a chunk are
-//   W = T diag(beta) (V - diag(a) K S),  T = (I + L)^-1,
-//   L_ij = beta_i e^{G_i - G_j} k_i.k_j  (j < i),
-//   O = diag(a) Q S + A W,  A_ij = e^{G_i - G_j} q_i.k_j  (j <= i),
+// A key row is k_i = r_i K_i, K_i with its largest element in [1, 2) and r_i what is left
+// of its size (over its norm, where rows are normalized).  With G_i the running sum of
+// the log decays inside a chunk, a_i = e^{G_i}, b_i = beta_i r_i, W_i what row i adds to
+// the state along K_i, and S the state before it, the rows of a chunk are
+//   W = T diag(b) (V - diag(a r) K S),  T = (I + L)^-1,
+//   L_ij = b_i r_i e^{G_i - G_j} K_i.K_j  (j < i),
+//   O = diag(a) Q S + A W,  A_ij = e^{G_i - G_j} Q_i.K_j  (j <= i),
 //   S <- e^{G_C} S + K^T diag(e^{G_C - G_j}) W.
+// The sizes of keys stay in b and r, which are fp32 numbers: W has the state's size, and
+// T and A have none.
 // T and A depend on the rows alone, so helper warps prepare them (and the
 // tiles) four to six chunks ahead; what is serial is the chain over S.  The columns
 // of S are independent: a chain warp owns 16 of them and keeps S^T [16][k_dim] in
@@ -50,17 +54,17 @@ struct alignas(16) Stage {
     alignas(16) __half t_lo[kC][kTS];
     alignas(16) __half a_hi[kC][kTS];              // A^T: [j][i]
     alignas(16) __half a_lo[kC][kTS];
-    alignas(16) float ar[kC];                      // per row, see the chain
-    alignas(16) float beta[kC];
-    alignas(16) float cr[kC];
+    alignas(16) float ar[kC];                      // per row: a r, b, e^{G_C - G}, a, scale of q
+    alignas(16) float b[kC];
+    alignas(16) float c[kC];
     alignas(16) float a[kC];
     alignas(16) float sq[kC];
     // the helper's own
     alignas(16) float lt[kC][kLS];                 // diagonal blocks of L^T: [j][i - j - 1]
     alignas(16) float gh[kC];
     alignas(16) float gl[kC];
-    alignas(16) float r[kC];
-    float gamma, vtop;                             // decay of the chunk; largest |v|
+    alignas(16) float br[kC];                      // b r
+    float gamma, wtop;                             // decay of the chunk; largest |b v|
     int lo, hi, more;                              // rows of the chunk this is for; more of it follow
 };
 
@@ -257,20 +261,22 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     if (bads)
         return __ffs(bads) - 1;
     const float4 row = rows_to_half<DK>(&s.k[lane][0], &s.q[lane][0], topk, row_top<KU>(&s.q[lane][0]));
-    // k = K 2^e / sqrt(4^e sum + eps) in terms of the stored row, 2^-e at hand
+    // r of k = K 2^e / sqrt(4^e sum + eps), 2^-e at hand
     auto power = [](float inv) { return __int_as_float((254 << 23) - __float_as_int(inv)); };
     const float r = !on ? 0.f : a.l2norm ? rsqrtf(row.z + a.l2_eps * row.x * row.x) : power(row.x);
     const float rq = !on ? 0.f : a.l2norm ? rsqrtf(row.w + a.l2_eps * row.y * row.y) : power(row.y);
-    s.r[lane] = r;
-    s.beta[lane] = beta;
+    s.br[lane] = beta * r * r;
+    s.b[lane] = beta * r;
     s.a[lane] = ai;
     s.ar[lane] = ai * r;
-    s.cr[lane] = ci * r;
+    s.c[lane] = ci;
     s.sq[lane] = a.scale * rq;
-    const unsigned vtop = __reduce_max_sync(0xffffffffu, topv);
+    // the largest |b v|; as bits: order of non-negative floats, with NaN on top
+    const unsigned wtop = __reduce_max_sync(
+        0xffffffffu, __float_as_uint(fabsf(beta * r) * __uint_as_float(topv << 16)));
     if (lane == 31) {
         s.gamma = ai;
-        s.vtop = __uint_as_float(vtop << 16);
+        s.wtop = __uint_as_float(wtop);
     }
     __syncwarp();
     // The 16 x 8 tiles of K K^T and K Q^T (row j, column i) that hold some i >= j, and
@@ -295,17 +301,16 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
         const int i0 = nt * 8 + 2 * t;
         const float2 ghi = *reinterpret_cast<const float2 *>(&s.gh[i0]);
         const float2 gli = *reinterpret_cast<const float2 *>(&s.gl[i0]);
-        const float2 ri = *reinterpret_cast<const float2 *>(&s.r[i0]);
-        const float2 bi = *reinterpret_cast<const float2 *>(&s.beta[i0]);
+        const float2 bi = *reinterpret_cast<const float2 *>(&s.br[i0]);
         uint32_t vh[2], vl[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int j = mt * 16 + g + half * 8;
-            const float rj = s.r[j], ghj = s.gh[j], glj = s.gl[j];
-            const float d0 = i0 >= j ? ex2((ghi.x - ghj) + (gli.x - glj)) * rj : 0.f;
-            const float d1 = i0 + 1 >= j ? ex2((ghi.y - ghj) + (gli.y - glj)) * rj : 0.f;
-            const float l0 = d0 * (ri.x * bi.x) * kk[half * 2];
-            const float l1 = d1 * (ri.y * bi.y) * kk[half * 2 + 1];
+            const float ghj = s.gh[j], glj = s.gl[j];
+            const float d0 = i0 >= j ? ex2((ghi.x - ghj) + (gli.x - glj)) : 0.f;
+            const float d1 = i0 + 1 >= j ? ex2((ghi.y - ghj) + (gli.y - glj)) : 0.f;
+            const float l0 = d0 * bi.x * kk[half * 2];
+            const float l1 = d1 * bi.y * kk[half * 2 + 1];
             if (tile != 2 && tile != 3) {      // a diagonal block's: column j from its row j + 1 on
                 float *lt = &s.lt[j][i0 - j - 1];
                 if (i0 > j)
@@ -722,20 +727,23 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 v[nt][hf * 2 + 1] = bf16_hi(x[e]);
             }
         }
-        const float vtop = st.vtop;
-        if (__any_sync(0xffffffffu, first || vtop * inv_unit[0] > 4096.f || vtop * inv_unit[1] > 4096.f)) {
+        const float wtop = st.wtop;
+        if (__any_sync(0xffffffffu, first || wtop * inv_unit[0] > 4096.f || wtop * inv_unit[1] > 4096.f)) {
             // the first rows, or values far above the state: each column by its own
-            float f[2];
+            float f[2], m[2] = {0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const float2 be = *reinterpret_cast<const float2 *>(&st.b[nt * 8 + 2 * t]);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                    m[hf] = fmaxf(m[hf], fmaxf(fabsf(be.x * v[nt][2 * hf]), fabsf(be.y * v[nt][2 * hf + 1])));
+            }
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                float m = 0.f;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-                    m = fmaxf(m, fmaxf(fabsf(v[nt][2 * hf]), fabsf(v[nt][2 * hf + 1])));
-                m = quad_max(m);
-                f[hf] = first ? refit(hf, top0[hf] > 0.f ? top0[hf] : m) : 1.f;
-                m *= inv_unit[hf];
-                f[hf] *= refit(hf, m > 4096.f ? m : 0.f);
+                m[hf] = quad_max(m[hf]);
+                f[hf] = first ? refit(hf, top0[hf] > 0.f ? top0[hf] : m[hf]) : 1.f;
+                m[hf] *= inv_unit[hf];
+                f[hf] *= refit(hf, m[hf] > 4096.f ? m[hf] : 0.f);
             }
             scale_rows(f[0], f[1]);
         }
@@ -794,11 +802,11 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 break;
         }
         first = false;
-        // Y = beta (V - a K S), then W = T Y
+        // Y = b (V - a r K S), then W = T Y
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             const float2 ar = *reinterpret_cast<const float2 *>(&st.ar[nt * 8 + 2 * t]);
-            const float2 be = *reinterpret_cast<const float2 *>(&st.beta[nt * 8 + 2 * t]);
+            const float2 be = *reinterpret_cast<const float2 *>(&st.b[nt * 8 + 2 * t]);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 X[nt][2 * hf] = be.x * (v[nt][2 * hf] * inv_unit[hf] - ar.x * X[nt][2 * hf]);
@@ -816,17 +824,17 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             if (lane == 0)
                 mbar_arrive(&sh.w_full[cw & 1]);
         }
-        // S <- gamma S + (c r W)^T K
+        // S <- gamma S + (c W)^T K
         float ounit[2];
         {
             float P[4][4];
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
-                const float2 cr = *reinterpret_cast<const float2 *>(&st.cr[nt * 8 + 2 * t]);
-                P[nt][0] = W[nt][0] * cr.x;
-                P[nt][1] = W[nt][1] * cr.y;
-                P[nt][2] = W[nt][2] * cr.x;
-                P[nt][3] = W[nt][3] * cr.y;
+                const float2 cc = *reinterpret_cast<const float2 *>(&st.c[nt * 8 + 2 * t]);
+                P[nt][0] = W[nt][0] * cc.x;
+                P[nt][1] = W[nt][1] * cc.y;
+                P[nt][2] = W[nt][2] * cc.x;
+                P[nt][3] = W[nt][3] * cc.y;
             }
             // what S will hold: its decayed size, or what is written now
             const float gamma = st.gamma;

@@ -50,6 +50,39 @@ def _hold(name, x, scale=1.0, eps=None, state=True, bounded=True, only=None):
         judge([x[key][a] for key in ("q", "k", "v", "g", "beta")] + [S0], out[a], so[s], scale, eps, bounded)
 
 
+# ------------------------------------------------------------------ key scales
+
+@BOTH
+@SHAPE
+@pytest.mark.parametrize("e", [-27, -13, 10, 30])
+def test_keys_of_any_size(name, Hk, Hv, dk, dv, n, e):
+    """Keys of length 2^e with strengths of 4^-e: the state is 2^-e times the one of unit
+    keys, and nothing else changes."""
+    x = _inputs(Hk, Hv, dk, dv, n, 70, 1 + e + dv)
+    x["k"] = (x["k"].float() * 2.0 ** e).to(BF)
+    x["beta"], x["S"] = x["beta"] * 4.0 ** -e, x["S"] * 2.0 ** -e
+    _hold(name, x, 2.0 ** e, only=(0, n - 1))
+
+
+@BOTH
+def test_rows_of_different_key_sizes(name):
+    x = _inputs(1, 2, 128, 64, 1, 70, 2)
+    f = torch.exp2((torch.arange(70) * 5 % 13 - 6).float())[:, None]
+    x["k"] = (x["k"].float() * f[..., None]).to(BF)
+    x["beta"] = x["beta"] / f ** 2
+    _hold(name, x)
+
+
+@BOTH
+def test_large_keys_and_queries(name):
+    """One row from a zero state: q.k of 4.6e7 times a write of 2^-20."""
+    x = _inputs(1, 2, 128, 32, 1, 1, 3)
+    for key in ("q", "k"):
+        x[key] = torch.full_like(x[key], 600.0)
+    x["beta"] = torch.full_like(x["beta"], 2.0 ** -26)
+    _hold(name, x, state=False)
+
+
 # --------------------------------------------- answers that are small differences
 
 @BOTH
