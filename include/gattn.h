@@ -679,7 +679,9 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *desc, gat
  * gattn_delta_step is for one to a few new rows of many sequences: it works
  * row by row.  Both take any lengths and differ in rounding only: the step
  * computes in fp32; the prompt multiplies operands of 22 bits into fp32 sums,
- * and both round out once, to bf16.
+ * and both round out once, to bf16.  Rows that stretch the state (beta |k|^2 above
+ * 2.25, or g above 0) are within the rule; a prompt takes their chunks of 32 row by
+ * row, in a multiple of the time.
  * num_seqs > 0 with total_rows == 0 copies the states.  k_dim 64 or 128; v_dim a
  * multiple of 32 up to 256 (else GATTN_E_UNSUPPORTED).
  */

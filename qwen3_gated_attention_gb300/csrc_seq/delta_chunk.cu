@@ -23,11 +23,13 @@
 // operand is exact, three where both are split.  The answers need both parts too: a
 // row that overwrites what the state held has Q S and A W cancel, and what is left
 // of 11 bits of each can be all wrong.  fp16's range is covered by a power of two per
-// state column that follows the column's size.
+// state column that follows the column's size.  Rows that stretch the state (b r |K|^2
+// past 2.25, or an entry of T past 64, or a growing "decay") would leave that range: such
+// a part of a chunk is taken row by row in fp32, by the same warps on the same registers.
 //
-// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 231 us
-// (1.8 us a chunk; its mma.sync instructions alone 0.3 us of it, the rest what each
-// of them waits for), 8 sequences of 1 to 1024 rows 128 us, the 1024 rows being the
+// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 238 us
+// (1.9 us a chunk; its mma.sync instructions alone 0.3 us of it, the rest what each
+// of them waits for), 8 sequences of 1 to 1024 rows 127 us, the 1024 rows being the
 // longest chain (4.0 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
 // slower: the state's update fused with the next chunk's K S (415 us: spills), rows
 // brought in by bulk copies (96 small ones a chunk), helpers with unrolled loops
@@ -43,6 +45,10 @@ constexpr int kC = 32;             // rows of a chunk
 constexpr int kTS = 40;            // row stride of T and A (halves): conflict-free ldmatrix
 constexpr int kLS = 16;            // row stride of L's diagonal blocks (floats)
 constexpr float kMinG = -200.f;    // e^-200 is 0 in fp32
+// Parts with more than this go row by row.  A row's map I - b r K K^T does not stretch
+// the state up to 2, and then no entry of T passes |K_j| / |K_i| * 2 < 46.  Sums of
+// 32 products of such T, K and S in [0.5, 32] stay below fp16's 65504
+constexpr float kGain = 2.25f, kTopT = 64.f, kGrowth = 1.f / 256;
 
 // Every array starts on a 16-byte boundary: they are read in 16-byte vectors.
 template <int DK, int NCW>
@@ -59,6 +65,8 @@ struct alignas(16) Stage {
     alignas(16) float c[kC];
     alignas(16) float a[kC];
     alignas(16) float sq[kC];
+    alignas(16) float r[kC];                       // for rows one by one: r, e^g
+    alignas(16) float d[kC];
     // the helper's own
     alignas(16) float lt[kC][kLS];                 // diagonal blocks of L^T: [j][i - j - 1]
     alignas(16) float gh[kC];
@@ -66,6 +74,7 @@ struct alignas(16) Stage {
     alignas(16) float br[kC];                      // b r
     float gamma, wtop;                             // decay of the chunk; largest |b v|
     int lo, hi, more;                              // rows of the chunk this is for; more of it follow
+    int alone;                                     // row by row
 };
 
 // The warps of a CTA: a chain warp per 16 of its NCW * 16 state columns, and helper
@@ -237,6 +246,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     gr = gr < kMinG ? kMinG : gr;
     // the sums in units of log2 e and as float pairs: differences of far sums stay exact
     float gh = gr * 1.44269502f, gl = fmaf(gr, 1.44269502f, -gh) + gr * 1.92596299e-8f;
+    s.d[lane] = ex2(gh + gl);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float h2 = __shfl_up_sync(0xffffffffu, gh, o), l2 = __shfl_up_sync(0xffffffffu, gl, o);
@@ -265,7 +275,9 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     auto power = [](float inv) { return __int_as_float((254 << 23) - __float_as_int(inv)); };
     const float r = !on ? 0.f : a.l2norm ? rsqrtf(row.z + a.l2_eps * row.x * row.x) : power(row.x);
     const float rq = !on ? 0.f : a.l2norm ? rsqrtf(row.w + a.l2_eps * row.y * row.y) : power(row.y);
+    s.r[lane] = r;
     s.br[lane] = beta * r * r;
+    const bool stretch = !(fabsf(beta * r * r) * row.z <= kGain) || gr > kGrowth;
     s.b[lane] = beta * r;
     s.a[lane] = ai;
     s.ar[lane] = ai * r;
@@ -333,6 +345,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
         }
     }
     __syncwarp();
+    float top = 0.f;                   // T's largest entry
     // T = (I + L)^-1.  Its two 16 x 16 diagonal blocks by forward substitution, a
     // column per lane: x[0] is the next unknown, taken out of every later row while
     // those move up by one.  Rows past the block's last are never used
@@ -358,6 +371,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
                             x[i4 * 4 + k] = fmaf(-lv[k], xm[e], x[i4 * 4 + k + 1]);
                 }
             }
+            top = fmaxf(top, fmaxf(fabsf(xm[0]), fabsf(xm[1])));
             uint32_t xh, xl;
             split_h2(xm[0], xm[1], xh, xl);
             *reinterpret_cast<uint32_t *>(&s.t_hi[lane][base + m]) = xh;
@@ -394,10 +408,18 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half) {
+                top = fmaxf(top, fmaxf(fabsf(q[n][2 * half]), fabsf(q[n][2 * half + 1])));
                 split_h2(-q[n][2 * half], -q[n][2 * half + 1], xh[2 * n + half], xl[2 * n + half]);
+            }
         stsm_x4_trans(smem_u32(&s.t_hi[pr][16 + pc]), xh[0], xh[1], xh[2], xh[3]);
         stsm_x4_trans(smem_u32(&s.t_lo[pr][16 + pc]), xl[0], xl[1], xl[2], xl[3]);
+    }
+    const bool alone = __any_sync(0xffffffffu, (on && stretch) || !(top <= kTopT));
+    if (lane == 0) {
+        s.alone = alone;
+        if (alone)
+            s.wtop = INFINITY;         // what the chain looks at
     }
     return hi;
 }
@@ -545,10 +567,19 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 }
             }
     };
-    // O = scale (a Q S + A W), O holding Q S, and its rows' way out through where
-    // their values were: a row of 16 columns per lane
-    auto finish_rows = [&](float (&O)[4][4], const float (&W)[4][4], Stage<DK, NCW> &st, int c, float u0,
-                           float u1) {
+    // a part's rows on their way out, from where their values were: a row of 16
+    // columns per lane
+    auto rows_out = [&](Stage<DK, NCW> &st, int c) {
+        __syncwarp();
+        if (lane >= st.lo && lane < st.hi) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(&st.v[lane][cw * 16]);
+            uint4 *dst = reinterpret_cast<uint4 *>(out + (long long)c * kC * a.os.tok);
+            dst[0] = src[0];
+            dst[1] = src[1];
+        }
+    };
+    // O = scale (a Q S + A W), O holding Q S
+    auto finish_rows = [&](float (&O)[4][4], float (&W)[4][4], Stage<DK, NCW> &st, int c, float u0, float u1) {
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             const float2 aa = *reinterpret_cast<const float2 *>(&st.a[nt * 8 + 2 * t]);
@@ -556,6 +587,21 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             O[nt][1] *= aa.y;
             O[nt][2] *= aa.x;
             O[nt][3] *= aa.y;
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+            top = fmaxf(top, fmaxf(fmaxf(fabsf(W[nt][0]), fabsf(W[nt][1])), fmaxf(fabsf(W[nt][2]), fabsf(W[nt][3]))));
+        if (__any_sync(0xffffffffu, top > 32768.f)) {      // past fp16's range: in larger units
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    O[nt][e] *= 0x1p-12f;
+                    W[nt][e] *= 0x1p-12f;
+                }
+            u0 *= 0x1p12f;
+            u1 *= 0x1p12f;
         }
         times_lower(O, W, st.a_hi, st.a_lo);
 #pragma unroll
@@ -570,13 +616,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             }
             stsm_x4_trans(smem_u32(&st.v[n2 * 16 + pr][cw * 16 + pc]), x[0], x[1], x[2], x[3]);
         }
-        __syncwarp();
-        if (lane >= st.lo && lane < st.hi) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(&st.v[lane][cw * 16]);
-            uint4 *dst = reinterpret_cast<uint4 *>(out + (long long)c * kC * a.os.tok);
-            dst[0] = src[0];
-            dst[1] = src[1];
-        }
+        rows_out(st, c);
     };
     bool ok = true;
     unsigned phase = 0;                    // per stage
@@ -615,7 +655,8 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.taken[cw & 1]);
-            finish_rows(O, W, st, c, u.x, u.y);
+            if (u.x > 0.f)                 // else the chain wrote them row by row
+                finish_rows(O, W, st, c, u.x, u.y);
             c += st.more ? 0 : 1;
             __syncwarp();
             if (lane == 0)
@@ -661,12 +702,16 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     };
-    float top0[2] = {0.f, 0.f};        // the initial state's columns
+    float top0[2];                     // sizes of a state in units of 1: this warp's elements
+    auto column_tops = [&] {
+        top0[0] = top0[1] = 0.f;
 #pragma unroll
-    for (int j = 0; j < ROWS / 8; ++j)
+        for (int j = 0; j < ROWS / 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            top0[e >> 1] = fmaxf(top0[e >> 1], fabsf(S[j][e]));
+            for (int e = 0; e < 4; ++e)
+                top0[e >> 1] = fmaxf(top0[e >> 1], fabsf(S[j][e]));
+    };
+    column_tops();
     // X and top of the column's two halves together; false if the wait ran out
     int turns = 0;
     auto add_shares = [&](float (&X)[4][4], float (&top)[2]) {
@@ -699,188 +744,281 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         ++turns;
         return true;
     };
-    if (R::SPLIT) {
-        float none[4][4] = {};
-        ok = add_shares(none, top0);
-    }
-    top0[0] = quad_max(top0[0]);
-    top0[1] = quad_max(top0[1]);
-    bool first = true;
-    Handed<DK> &to = sh.to[R::SPLIT ? cw : 0];
-    for (int c = 0, turn = 0; ok && c < chunks; turn ^= 1) {
-        const int w = c % R::HELP;
-        ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
-        if (!ok)
-            break;
-        phase ^= 1u << w;
-        Stage<DK, NCW> &st = sh.st[w];
-        float v[4][4];
-#pragma unroll
-        for (int n2 = 0; n2 < 2; ++n2) {
-            uint32_t x[4];
-            // rows of the tile are packed rows, its columns ours: transposed
-            ldsm_x4_trans(x, smem_u32(&st.v[n2 * 16 + pr][cw * 16 + pc]));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int nt = n2 * 2 + (e >> 1), hf = e & 1;
-                v[nt][hf * 2] = bf16_lo(x[e]);
-                v[nt][hf * 2 + 1] = bf16_hi(x[e]);
-            }
+    // top0 from this warp's own elements to the column's
+    auto join_tops = [&] {
+        if (R::SPLIT) {
+            float none[4][4] = {};
+            if (!add_shares(none, top0))
+                return false;
         }
-        const float wtop = st.wtop;
-        if (__any_sync(0xffffffffu, first || wtop * inv_unit[0] > 4096.f || wtop * inv_unit[1] > 4096.f)) {
-            // the first rows, or values far above the state: each column by its own
-            float f[2], m[2] = {0.f, 0.f};
+        top0[0] = quad_max(top0[0]);
+        top0[1] = quad_max(top0[1]);
+        return true;
+    };
+    ok = join_tops();
+    // A part row by row, in fp32:
+    //   S <- e^g S + K w,  w = b (v - r e^g S^T K),  out = scale (e^g S^T Q + (Q.K) w).
+    // S leaves it in units of 1, with its sizes in top0
+    auto row_by_row = [&](Stage<DK, NCW> &st, int c) {
+        scale_rows(unit[0], unit[1]);
+        unit[0] = unit[1] = inv_unit[0] = inv_unit[1] = 1.f;
+        const int col = cw * 16 + g, k0 = half * ROWS + 2 * t;
+#pragma unroll 1
+        for (int i = st.lo; i < st.hi; ++i) {
+            // this lane's elements of S^T K, S^T Q (columns g and g + 8) and Q.K
+            float x[4][4] = {}, none[2] = {0.f, 0.f};
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const float2 be = *reinterpret_cast<const float2 *>(&st.b[nt * 8 + 2 * t]);
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-                    m[hf] = fmaxf(m[hf], fmaxf(fabsf(be.x * v[nt][2 * hf]), fabsf(be.y * v[nt][2 * hf + 1])));
+            for (int j = 0; j < ROWS / 8; ++j) {
+                const float2 k = __half22float2(*reinterpret_cast<const __half2 *>(&st.k[i][k0 + 8 * j]));
+                const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&st.q[i][k0 + 8 * j]));
+                x[0][0] = fmaf(S[j][0], k.x, fmaf(S[j][1], k.y, x[0][0]));
+                x[0][1] = fmaf(S[j][2], k.x, fmaf(S[j][3], k.y, x[0][1]));
+                x[0][2] = fmaf(S[j][0], q.x, fmaf(S[j][1], q.y, x[0][2]));
+                x[0][3] = fmaf(S[j][2], q.x, fmaf(S[j][3], q.y, x[0][3]));
+                x[1][0] = fmaf(k.x, q.x, fmaf(k.y, q.y, x[1][0]));
             }
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                m[hf] = quad_max(m[hf]);
-                f[hf] = first ? refit(hf, top0[hf] > 0.f ? top0[hf] : m[hf]) : 1.f;
-                m[hf] *= inv_unit[hf];
-                f[hf] *= refit(hf, m[hf] > 4096.f ? m[hf] : 0.f);
-            }
-            scale_rows(f[0], f[1]);
-        }
-        // K S (and Q S)
-        float X[4][4] = {}, O[4][4] = {};
-        __half2 top[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
-        if (R::SPLIT && !first) {
-            ok = __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1], turn ^ 1, abort));
-            if (!ok)
-                break;
-        }
-        uint32_t bk[2][2][4], bq[2][4];
-        float X2[4][4] = {};               // the low parts' sums, apart: shorter chains
-        const int ks0 = half * (ROWS / 16);
-        load_rows(bk[0], st.k, ks0);
-#pragma unroll
-        for (int ks = 0; ks < ROWS / 16; ++ks) {
-            uint32_t hi[4], lo[4];
-            if (ks + 1 < ROWS / 16)
-                load_rows(bk[(ks + 1) & 1], st.k, ks0 + ks + 1);
-            if (!R::SPLIT)
-                load_rows(bq, st.q, ks);
-            split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
-            if (R::SPLIT) {
-                to.s[ks0 + ks][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                to.s[ks0 + ks][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                top[e & 1] = __hmax2(top[e & 1], __habs2(*reinterpret_cast<const __half2 *>(&hi[e])));
-            if (R::SPLIT)
-                times_rows(X, X2, hi, lo, bk[ks & 1]);
-            else
-                times_rows(X, X, hi, lo, bk[ks & 1]);
-            if (!R::SPLIT)
-                times_rows(O, O, hi, lo, bq);
-        }
-        if (R::SPLIT)
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int o = 1; o < 4; o <<= 1) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    X[nt][e] += X2[nt][e];
-        float m[2];                        // the columns' largest elements
+                    x[0][e] += __shfl_xor_sync(0xffffffffu, x[0][e], o);
+                x[1][0] += __shfl_xor_sync(0xffffffffu, x[1][0], o);
+            }
+            const float v0 = __bfloat162float(st.v[i][col]), v1 = __bfloat162float(st.v[i][col + 8]);
+            if (R::SPLIT && !add_shares(x, none))
+                return false;
+            const float d = st.d[i], b = st.b[i], dr = d * st.r[i], sc = st.sq[i];
+            const float w0 = b * (v0 - dr * x[0][0]), w1 = b * (v1 - dr * x[0][1]);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const float2 th = __half22float2(top[hf]);
-            m[hf] = fmaxf(th.x, th.y);
+            for (int j = 0; j < ROWS / 8; ++j) {
+                const float2 k = __half22float2(*reinterpret_cast<const __half2 *>(&st.k[i][k0 + 8 * j]));
+                S[j][0] = fmaf(k.x, w0, d * S[j][0]);
+                S[j][1] = fmaf(k.y, w0, d * S[j][1]);
+                S[j][2] = fmaf(k.x, w1, d * S[j][2]);
+                S[j][3] = fmaf(k.y, w1, d * S[j][3]);
+            }
+            __syncwarp();                  // the row's values have been read
+            if (half == 0 && t == 0) {
+                st.v[i][col] = __float2bfloat16(sc * fmaf(x[1][0], w0, d * x[0][2]));
+                st.v[i][col + 8] = __float2bfloat16(sc * fmaf(x[1][0], w1, d * x[0][3]));
+            }
         }
-        if (R::SPLIT) {
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.s_full[cw & 1]);
-            ok = add_shares(X, m);
+        if (half == 0)
+            rows_out(st, c);
+        column_tops();
+        return join_tops();
+    };
+    bool first = true;
+    Handed<DK> &to = sh.to[R::SPLIT ? cw : 0];
+    for (int c = 0, use = 0; ok && c < chunks; ++use) {
+        // the loop proper, until a part has to go row by row: what that takes stands
+        // behind it, so that its registers and code are not in the way
+        bool apart = false;
+        for (; ok && c < chunks; ++use) {
+            const int w = c % R::HELP, turn = use & 1;
+            ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
             if (!ok)
                 break;
-        }
-        first = false;
-        // Y = b (V - a r K S), then W = T Y
+            phase ^= 1u << w;
+            Stage<DK, NCW> &st = sh.st[w];
+            float v[4][4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-            const float2 ar = *reinterpret_cast<const float2 *>(&st.ar[nt * 8 + 2 * t]);
-            const float2 be = *reinterpret_cast<const float2 *>(&st.b[nt * 8 + 2 * t]);
+            for (int n2 = 0; n2 < 2; ++n2) {
+                uint32_t x[4];
+                // rows of the tile are packed rows, its columns ours: transposed
+                ldsm_x4_trans(x, smem_u32(&st.v[n2 * 16 + pr][cw * 16 + pc]));
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                X[nt][2 * hf] = be.x * (v[nt][2 * hf] * inv_unit[hf] - ar.x * X[nt][2 * hf]);
-                X[nt][2 * hf + 1] = be.y * (v[nt][2 * hf + 1] * inv_unit[hf] - ar.y * X[nt][2 * hf + 1]);
+                for (int e = 0; e < 4; ++e) {
+                    const int nt = n2 * 2 + (e >> 1), hf = e & 1;
+                    v[nt][hf * 2] = bf16_lo(x[e]);
+                    v[nt][hf * 2 + 1] = bf16_hi(x[e]);
+                }
             }
-        }
-        float W[4][4] = {};
-        times_lower(W, X, st.t_hi, st.t_lo);
-        if (R::SPLIT && half == 0) {
+            const float wtop = st.wtop;
+            if (__any_sync(0xffffffffu, first || wtop * inv_unit[0] > 4096.f || wtop * inv_unit[1] > 4096.f)) {
+                if (__any_sync(0xffffffffu, st.alone)) {
+                    apart = true;
+                    break;
+                }
+                // the first rows, or values far above the state: each column by its own
+                float f[2], m[2] = {0.f, 0.f};
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                to.w[nt][lane] = make_float4(W[nt][0], W[nt][1], W[nt][2], W[nt][3]);
-            to.unit[lane] = make_float2(unit[0], unit[1]);
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.w_full[cw & 1]);
-        }
-        // S <- gamma S + (c W)^T K
-        float ounit[2];
-        {
-            float P[4][4];
+                for (int nt = 0; nt < 4; ++nt) {
+                    const float2 be = *reinterpret_cast<const float2 *>(&st.b[nt * 8 + 2 * t]);
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const float2 cc = *reinterpret_cast<const float2 *>(&st.c[nt * 8 + 2 * t]);
-                P[nt][0] = W[nt][0] * cc.x;
-                P[nt][1] = W[nt][1] * cc.y;
-                P[nt][2] = W[nt][2] * cc.x;
-                P[nt][3] = W[nt][3] * cc.y;
-            }
-            // what S will hold: its decayed size, or what is written now
-            const float gamma = st.gamma;
-            float f[2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                m[hf] *= gamma;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
-                    m[hf] = fmaxf(m[hf], fmaxf(fabsf(P[nt][2 * hf]), fabsf(P[nt][2 * hf + 1])));
-                m[hf] = quad_max(m[hf]);
-                f[hf] = gamma;
-            }
-            ounit[0] = unit[0];
-            ounit[1] = unit[1];
-            auto out_of = [](float x) { return x > 0.f && (x < 0.5f || x > 32.f); };
-            if (__any_sync(0xffffffffu, out_of(m[0]) || out_of(m[1]))) {
+                    for (int hf = 0; hf < 2; ++hf)
+                        m[hf] = fmaxf(m[hf], fmaxf(fabsf(be.x * v[nt][2 * hf]), fabsf(be.y * v[nt][2 * hf + 1])));
+                }
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const float x = refit(hf, out_of(m[hf]) ? m[hf] : 0.f);
-                    f[hf] *= x;
+                    m[hf] = quad_max(m[hf]);
+                    f[hf] = first ? refit(hf, top0[hf] > 0.f ? top0[hf] : m[hf]) : 1.f;
+                    m[hf] *= inv_unit[hf];
+                    f[hf] *= refit(hf, m[hf] > 4096.f ? m[hf] : 0.f);
+                }
+                scale_rows(f[0], f[1]);
+            }
+            // K S (and Q S)
+            float X[4][4] = {}, O[4][4] = {};
+            __half2 top[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
+            if (R::SPLIT && use > 0) {
+                ok = __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1], turn ^ 1, abort));
+                if (!ok)
+                    break;
+            }
+            uint32_t bk[2][2][4], bq[2][4];
+            float X2[4][4] = {};               // the low parts' sums, apart: shorter chains
+            const int ks0 = half * (ROWS / 16);
+            load_rows(bk[0], st.k, ks0);
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt) {
-                        P[nt][2 * hf] *= x;
-                        P[nt][2 * hf + 1] *= x;
-                    }
+            for (int ks = 0; ks < ROWS / 16; ++ks) {
+                uint32_t hi[4], lo[4];
+                if (ks + 1 < ROWS / 16)
+                    load_rows(bk[(ks + 1) & 1], st.k, ks0 + ks + 1);
+                if (!R::SPLIT)
+                    load_rows(bq, st.q, ks);
+                split_frag(S[2 * ks], S[2 * ks + 1], hi, lo);
+                if (R::SPLIT) {
+                    to.s[ks0 + ks][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    to.s[ks0 + ks][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top[e & 1] = __hmax2(top[e & 1], __habs2(*reinterpret_cast<const __half2 *>(&hi[e])));
+                if (R::SPLIT)
+                    times_rows(X, X2, hi, lo, bk[ks & 1]);
+                else
+                    times_rows(X, X, hi, lo, bk[ks & 1]);
+                if (!R::SPLIT)
+                    times_rows(O, O, hi, lo, bq);
+            }
+            if (R::SPLIT)
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        X[nt][e] += X2[nt][e];
+            float m[2];                        // the columns' largest elements
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const float2 th = __half22float2(top[hf]);
+                m[hf] = fmaxf(th.x, th.y);
+            }
+            if (R::SPLIT) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.s_full[cw & 1]);
+                ok = add_shares(X, m);
+                if (!ok)
+                    break;
+            }
+            first = false;
+            // Y = b (V - a r K S), then W = T Y
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const float2 ar = *reinterpret_cast<const float2 *>(&st.ar[nt * 8 + 2 * t]);
+                const float2 be = *reinterpret_cast<const float2 *>(&st.b[nt * 8 + 2 * t]);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    X[nt][2 * hf] = be.x * (v[nt][2 * hf] * inv_unit[hf] - ar.x * X[nt][2 * hf]);
+                    X[nt][2 * hf + 1] = be.y * (v[nt][2 * hf + 1] * inv_unit[hf] - ar.y * X[nt][2 * hf + 1]);
                 }
             }
-            uint32_t hi[2][4], lo[2][4];
-            split_frag(P[0], P[1], hi[0], lo[0]);
-            split_frag(P[2], P[3], hi[1], lo[1]);
-            scale_rows(f[0], f[1]);
+            float W[4][4] = {};
+            times_lower(W, X, st.t_hi, st.t_lo);
+            if (R::SPLIT && half == 0) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+                for (int nt = 0; nt < 4; ++nt)
+                    to.w[nt][lane] = make_float4(W[nt][0], W[nt][1], W[nt][2], W[nt][3]);
+                to.unit[lane] = make_float2(unit[0], unit[1]);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.w_full[cw & 1]);
+            }
+            // S <- gamma S + (c W)^T K
+            float ounit[2];
+            {
+                float P[4][4];
 #pragma unroll
-                for (int j2 = 0; j2 < ROWS / 16; ++j2) {
-                    uint32_t b[4];
-                    ldsm_x4_trans(b, smem_u32(&st.k[kk * 16 + tr][half * ROWS + j2 * 16 + tc]));
-                    mma(S[2 * j2], hi[kk], b[0], b[1]);
-                    mma(S[2 * j2 + 1], hi[kk], b[2], b[3]);
-                    mma(S[2 * j2], lo[kk], b[0], b[1]);
-                    mma(S[2 * j2 + 1], lo[kk], b[2], b[3]);
+                for (int nt = 0; nt < 4; ++nt) {
+                    const float2 cc = *reinterpret_cast<const float2 *>(&st.c[nt * 8 + 2 * t]);
+                    P[nt][0] = W[nt][0] * cc.x;
+                    P[nt][1] = W[nt][1] * cc.y;
+                    P[nt][2] = W[nt][2] * cc.x;
+                    P[nt][3] = W[nt][3] * cc.y;
                 }
+                // what S will hold: its decayed size, or what is written now
+                const float gamma = st.gamma;
+                float f[2];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    m[hf] *= gamma;
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+                        m[hf] = fmaxf(m[hf], fmaxf(fabsf(P[nt][2 * hf]), fabsf(P[nt][2 * hf + 1])));
+                    m[hf] = quad_max(m[hf]);
+                    f[hf] = gamma;
+                }
+                ounit[0] = unit[0];
+                ounit[1] = unit[1];
+                auto out_of = [](float x) { return x > 0.f && (x < 0.5f || x > 32.f); };
+                if (__any_sync(0xffffffffu, out_of(m[0]) || out_of(m[1]))) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float x = refit(hf, out_of(m[hf]) ? m[hf] : 0.f);
+                        f[hf] *= x;
+#pragma unroll
+                        for (int nt = 0; nt < 4; ++nt) {
+                            P[nt][2 * hf] *= x;
+                            P[nt][2 * hf + 1] *= x;
+                        }
+                    }
+                }
+                uint32_t hi[2][4], lo[2][4];
+                split_frag(P[0], P[1], hi[0], lo[0]);
+                split_frag(P[2], P[3], hi[1], lo[1]);
+                scale_rows(f[0], f[1]);
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int j2 = 0; j2 < ROWS / 16; ++j2) {
+                        uint32_t b[4];
+                        ldsm_x4_trans(b, smem_u32(&st.k[kk * 16 + tr][half * ROWS + j2 * 16 + tc]));
+                        mma(S[2 * j2], hi[kk], b[0], b[1]);
+                        mma(S[2 * j2 + 1], hi[kk], b[2], b[3]);
+                        mma(S[2 * j2], lo[kk], b[0], b[1]);
+                        mma(S[2 * j2 + 1], lo[kk], b[2], b[3]);
+                    }
+            }
+            if (!R::SPLIT)
+                finish_rows(O, W, st, c, ounit[0], ounit[1]);
+            c += st.more ? 0 : 1;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.empty[w]);
         }
-        if (!R::SPLIT)
-            finish_rows(O, W, st, c, ounit[0], ounit[1]);
+        if (!apart)
+            break;
+        const int w = c % R::HELP, turn = use & 1;
+        Stage<DK, NCW> &st = sh.st[w];
+        if (R::SPLIT) {
+            // nothing for the output warp this time: a unit of 0 says so
+            ok = use == 0 || __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1], turn ^ 1, abort));
+            if (!ok)
+                break;
+            if (half == 0)
+                to.unit[lane] = make_float2(0.f, 0.f);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.s_full[cw & 1]);
+                if (half == 0)
+                    mbar_arrive(&sh.w_full[cw & 1]);
+            }
+        }
+        ok = row_by_row(st, c);
+        if (!ok)
+            break;
+        first = true;
         c += st.more ? 0 : 1;
         __syncwarp();
         if (lane == 0)

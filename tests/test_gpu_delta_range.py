@@ -83,6 +83,45 @@ def test_large_keys_and_queries(name):
     _hold(name, x, state=False)
 
 
+# ------------------------------ rows that stretch the state
+
+@BOTH
+@SHAPE
+@pytest.mark.parametrize("size,beta,rows", [(128.0, 0.5, 10), (128.0, 0.5, 20), (32.0, 0.5, 33), (4.0, 0.9, 70)])
+def test_rows_that_stretch_the_state(name, Hk, Hv, dk, dv, n, size, beta, rows):
+    """Keys that nobody normalized: a row multiplies the state along its key by
+    1 - beta |k|^2.  It grows by orders of magnitude and stays a number of fp32."""
+    x = _inputs(Hk, Hv, dk, dv, n, rows, int(size) + rows)
+    x["k"] = (x["k"].float() * size ** 0.5).to(BF)
+    x["beta"][:] = beta
+    _hold(name, x, bounded=False, only=(0, n - 1))
+
+
+@BOTH
+def test_one_key_again_and_again_that_stretches_the_state(name):
+    x = _inputs(1, 2, 128, 64, 1, 40, 4, decay=0.0)
+    x["k"] = (2 * x["k"][:1].float()).to(BF).expand(40, 1, 128).contiguous()
+    x["beta"][:] = 0.9
+    _hold(name, x, bounded=False)
+
+
+@BOTH
+def test_one_row_that_stretches_the_state_by_a_million(name):
+    x = _inputs(1, 2, 64, 32, 1, 50, 5)
+    x["k"][21] = (x["k"][21].float() * 1000).to(BF)
+    _hold(name, x, bounded=False)
+
+
+@BOTH
+@SHAPE
+def test_states_that_grow_by_their_decay(name, Hk, Hv, dk, dv, n):
+    """A positive g is a growth: the state passes 2^40 and is a state like any other."""
+    x = _inputs(Hk, Hv, dk, dv, n, 40, 6)
+    x["g"] = x["g"] + 0.75
+    x["g"][7, 0] = 5.0
+    _hold(name, x, bounded=False, only=(0, n - 1))
+
+
 # --------------------------------------------- answers that are small differences
 
 @BOTH
