@@ -680,8 +680,10 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *desc, gat
  * row by row.  Both take any lengths and differ in rounding only: the step
  * computes in fp32; the prompt multiplies operands of 22 bits into fp32 sums,
  * and both round out once, to bf16.  Rows that stretch the state (beta |k|^2 above
- * 2.25, or g above 0) are within the rule; a prompt takes their chunks of 32 row by
- * row, in a multiple of the time.
+ * 2.25, or g above 1/256) and columns of it whose size changes by orders of
+ * magnitude within 32 rows are within the rule: a prompt takes such rows one by
+ * one, in a multiple of the time.  The errors of both are relative to norms (|q| times
+ * that of a column of S), as those of fp32 sums are.
  * num_seqs > 0 with total_rows == 0 copies the states.  k_dim 64 or 128; v_dim a
  * multiple of 32 up to 256 (else GATTN_E_UNSUPPORTED).
  */

@@ -23,17 +23,23 @@
 // operand is exact, three where both are split.  The answers need both parts too: a
 // row that overwrites what the state held has Q S and A W cancel, and what is left
 // of 11 bits of each can be all wrong.  fp16's range is covered by a power of two per
-// state column that follows the column's size.  Rows that stretch the state (b r |K|^2
-// past 2.25, or an entry of T past 64, or a growing "decay") would leave that range: such
-// a part of a chunk is taken row by row in fp32, by the same warps on the same registers.
+// state column that follows the column's size; an element of K or Q below 2^-14 of its
+// row's largest, and a product's operand below 2^-11 of its column's size, is off by up
+// to 2^-25 of that size instead of 2^-24 of itself.  Two kinds of parts of a chunk would
+// leave fp16's range and are taken row by row in fp32, by the same warps on the same
+// registers: rows that stretch the state (b r |K|^2 past 2.25, or an entry of T past 64,
+// or a growing "decay"), and columns whose size changes too far within the part (a row
+// that finds far less than the state the part began with, or than what is written later).
 //
-// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 238 us
+// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 242 us
 // (1.9 us a chunk; its mma.sync instructions alone 0.3 us of it, the rest what each
-// of them waits for), 8 sequences of 1 to 1024 rows 127 us, the 1024 rows being the
-// longest chain (4.0 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
+// of them waits for), 8 sequences of 1 to 1024 rows 126 us, the 1024 rows being the
+// longest chain (3.9 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
 // slower: the state's update fused with the next chunk's K S (415 us: spills), rows
 // brought in by bulk copies (96 small ones a chunk), helpers with unrolled loops
 // (their code pushes the chain's out of the instruction cache: 267 to 320 us).
+#include <climits>
+
 #include "seq.cuh"
 #include "tc5.cuh"
 
@@ -49,6 +55,12 @@ constexpr float kMinG = -200.f;    // e^-200 is 0 in fp32
 // the state up to 2, and then no entry of T passes |K_j| / |K_i| * 2 < 46.  Sums of
 // 32 products of such T, K and S in [0.5, 32] stay below fp16's 65504
 constexpr float kGain = 2.25f, kTopT = 64.f, kGrowth = 1.f / 256;
+// A column's unit is the state's, or that of what a part writes where that is more than
+// kMost of the state's.  Its size changes too far where an operand off by 2^-25 of the unit
+// is more than 2^-17 of what a row finds: the state decays below kFades within the part,
+// or the unit is not the state's, and at some row all that has been written so far is
+// less than kLeast (the state of a unit of its own begins between 0.5 and 32)
+constexpr float kMost = 4096.f, kFades = 1.f / 256, kLeast = 1.f / 256;
 
 // Every array starts on a 16-byte boundary: they are read in 16-byte vectors.
 template <int DK, int NCW>
@@ -72,7 +84,9 @@ struct alignas(16) Stage {
     alignas(16) float gh[kC];
     alignas(16) float gl[kC];
     alignas(16) float br[kC];                      // b r
-    float gamma, wtop;                             // decay of the chunk; largest |b v|
+    float gamma;                                   // decay of the part
+    float least;                                   // smallest size that some row finds written, over the largest
+    float most, low;                               // largest |b v|, infinite for `alone`; lowest_write() by least
     int lo, hi, more;                              // rows of the chunk this is for; more of it follow
     int alone;                                     // row by row
 };
@@ -165,6 +179,9 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     mma_f16(d, a, b0, b1, d);
 }
 
+// 2^(hi + lo), lo below a unit in the last place of hi
+__device__ __forceinline__ float ex2_pair(float hi, float lo) { return ex2(hi) * fmaf(lo, 0.693147181f, 1.f); }
+
 // Largest magnitude (bf16 bits) of a row of 16-byte units.
 template <int U>
 __device__ __forceinline__ unsigned row_top(const void *row)
@@ -211,6 +228,40 @@ __device__ __forceinline__ float4 rows_to_half(__half *krow, __half *qrow, unsig
     return make_float4(fk, fq, kk[0] + kk[1], qq[0] + qq[1]);
 }
 
+// At most the smallest, over the columns, of the largest |b v| of a column (by every
+// fourth row and to 2^-7, which is enough to tell when the chain has to look closer).
+template <int DK, int NCW>
+__device__ __forceinline__ float lowest_write(const Stage<DK, NCW> &s)
+{
+    // lanes side by side on pairs of columns, two rows at once where pairs are few
+    constexpr int PAIRS = 8 * NCW, PER = PAIRS > 32 ? PAIRS / 32 : 1, STEP = PAIRS < 32 ? 32 / PAIRS : 1;
+    const int lane = threadIdx.x & 31;
+    __nv_bfloat162 top[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        top[p] = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int r = 3 + 4 * (STEP > 1 ? lane / PAIRS : 0); r < kC; r += 4 * STEP) {
+        const __nv_bfloat162 b = __float2bfloat162_rn(s.b[r]);
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const __nv_bfloat162 v =
+                *reinterpret_cast<const __nv_bfloat162 *>(&s.v[r][2 * (lane % (PAIRS < 32 ? PAIRS : 32) + 32 * p)]);
+            top[p] = __hmax2(top[p], __habs2(__hmul2(v, b)));
+        }
+    }
+    unsigned low = 0xFFFFu;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        unsigned u = *reinterpret_cast<const unsigned *>(&top[p]);
+#pragma unroll
+        for (int o = PAIRS; o < 32; o <<= 1)
+            u = __vmaxu2(u, __shfl_xor_sync(0xffffffffu, u, o));
+        low = min(low, min(u & 0xFFFFu, u >> 16));
+    }
+    return __uint_as_float(__reduce_min_sync(0xffffffffu, low) << 16);
+}
+
 // Everything of rows [lo, hi) of the chunk at t0 that does not depend on the
 // state, by one warp; the chunk's other rows count as absent.  A row whose key,
 // value, decay or strength is not finite has to be the first of its part: 0 * NaN
@@ -246,7 +297,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     gr = gr < kMinG ? kMinG : gr;
     // the sums in units of log2 e and as float pairs: differences of far sums stay exact
     float gh = gr * 1.44269502f, gl = fmaf(gr, 1.44269502f, -gh) + gr * 1.92596299e-8f;
-    s.d[lane] = ex2(gh + gl);
+    s.d[lane] = expf(gr);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float h2 = __shfl_up_sync(0xffffffffu, gh, o), l2 = __shfl_up_sync(0xffffffffu, gl, o);
@@ -259,7 +310,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     const float gch = __shfl_sync(0xffffffffu, gh, 31), gcl = __shfl_sync(0xffffffffu, gl, 31);
     s.gh[lane] = gh;
     s.gl[lane] = gl;
-    const float ai = ex2(gh + gl), ci = ex2((gch - gh) + (gcl - gl));
+    const float ai = ex2_pair(gh, gl), ci = ex2((gch - gh) + (gcl - gl));
     cp_async_wait_all();
     __syncwarp();
     const unsigned topk = row_top<KU>(&s.k[lane][0]);
@@ -284,13 +335,29 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     s.c[lane] = ci;
     s.sq[lane] = a.scale * rq;
     // the largest |b v|; as bits: order of non-negative floats, with NaN on top
-    const unsigned wtop = __reduce_max_sync(
-        0xffffffffu, __float_as_uint(fabsf(beta * r) * __uint_as_float(topv << 16)));
+    const float write = fabsf(beta * r) * __uint_as_float(topv << 16);
+    const unsigned wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(write));
+    // what a row finds written, to a power of two: the largest so far with its decay
+    const int at = __float2int_rn(gh);
+    int size = write > 0.f ? (__float_as_int(write) >> 23) - at : INT_MIN / 2;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int s2 = __shfl_up_sync(0xffffffffu, size, o);
+        if (lane >= o)
+            size = max(size, s2);
+    }
+    const int most = __reduce_max_sync(0xffffffffu, on ? size + at : INT_MIN / 2);
+    const int fewest = __reduce_min_sync(0xffffffffu, on ? size + at : INT_MAX / 2);
+    const float least = fewest < most ? ex2((float)(fewest - most)) : 1.f;
     if (lane == 31) {
         s.gamma = ai;
-        s.wtop = __uint_as_float(wtop);
+        s.least = least;
+        s.most = __uint_as_float(wtop);
     }
     __syncwarp();
+    const float low = __shfl_sync(0xffffffffu, ai, 31) < kFades ? least * lowest_write(s) : INFINITY;
+    if (lane == 0)
+        s.low = low;
     // The 16 x 8 tiles of K K^T and K Q^T (row j, column i) that hold some i >= j, and
     // from each its part of L and of A.  A loop that stays rolled: with it the code of
     // all roles stays small enough for the SM's instruction cache
@@ -419,7 +486,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     if (lane == 0) {
         s.alone = alone;
         if (alone)
-            s.wtop = INFINITY;         // what the chain looks at
+            s.most = INFINITY;
     }
     return hi;
 }
@@ -677,14 +744,17 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         for (int e = 0; e < 4; ++e)
             S[j][e] = a.state ? a.state[so + (long long)(8 * j + 2 * t + (e & 1)) * a.dv + (e >> 1) * 8] : 0.f;
     // rows g and g + 8 of S are held in units of a power of two each, so that the
-    // parts fit fp16: what is dropped is below 2^-24 of the unit, as in an fp32 sum
+    // parts fit fp16
     float unit[2] = {1.f, 1.f}, inv_unit[2] = {1.f, 1.f};
-    // the power of two that takes m into [8, 16), within limits that keep units
-    // finite; 1 for 0, infinities and NaN
-    auto refit = [&](int hf, float m) {
-        int e = m > 0.f && m < INFINITY ? min(max((__float_as_int(m) >> 23) - 130, -60), 60) : 0;
+    // the exponent that takes m into [8, 16), within limits that keep units finite; 0 for
+    // 0, infinities and NaN
+    auto steps = [&](int hf, float m) {
+        const int e = m > 0.f && m < INFINITY ? min(max((__float_as_int(m) >> 23) - 130, -120), 120) : 0;
         const int ue = (__float_as_int(unit[hf]) >> 23) - 127;
-        e = min(max(e, -100 - ue), 100 - ue);
+        return min(max(e, -100 - ue), 120 - ue);
+    };
+    auto refit = [&](int hf, int e) {
+        const int ue = (__float_as_int(unit[hf]) >> 23) - 127;
         unit[hf] = __int_as_float((127 + ue + e) << 23);
         inv_unit[hf] = __int_as_float((127 - ue - e) << 23);
         return __int_as_float((127 - e) << 23);
@@ -702,7 +772,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     };
-    float top0[2];                     // sizes of a state in units of 1: this warp's elements
+    float top0[2];                     // sizes of the columns, while `first` holds
     auto column_tops = [&] {
         top0[0] = top0[1] = 0.f;
 #pragma unroll
@@ -810,8 +880,9 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     };
     bool first = true;
     Handed<DK> &to = sh.to[R::SPLIT ? cw : 0];
-    for (int c = 0, use = 0; ok && c < chunks; ++use) {
-        // the loop proper, until a part has to go row by row: what that takes stands
+    bool looked = false;
+    for (int c = 0, use = 0; ok && c < chunks;) {
+        // the loop proper, until a part wants a closer look: what that takes stands
         // behind it, so that its registers and code are not in the way
         bool apart = false;
         for (; ok && c < chunks; ++use) {
@@ -819,7 +890,6 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             ok = __all_sync(0xffffffffu, tc5_wait(&sh.full[w], phase >> w & 1, abort));
             if (!ok)
                 break;
-            phase ^= 1u << w;
             Stage<DK, NCW> &st = sh.st[w];
             float v[4][4];
 #pragma unroll
@@ -834,30 +904,14 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                     v[nt][hf * 2 + 1] = bf16_hi(x[e]);
                 }
             }
-            const float wtop = st.wtop;
-            if (__any_sync(0xffffffffu, first || wtop * inv_unit[0] > 4096.f || wtop * inv_unit[1] > 4096.f)) {
-                if (__any_sync(0xffffffffu, st.alone)) {
-                    apart = true;
-                    break;
-                }
-                // the first rows, or values far above the state: each column by its own
-                float f[2], m[2] = {0.f, 0.f};
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const float2 be = *reinterpret_cast<const float2 *>(&st.b[nt * 8 + 2 * t]);
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                        m[hf] = fmaxf(m[hf], fmaxf(fabsf(be.x * v[nt][2 * hf]), fabsf(be.y * v[nt][2 * hf + 1])));
-                }
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    m[hf] = quad_max(m[hf]);
-                    f[hf] = first ? refit(hf, top0[hf] > 0.f ? top0[hf] : m[hf]) : 1.f;
-                    m[hf] *= inv_unit[hf];
-                    f[hf] *= refit(hf, m[hf] > 4096.f ? m[hf] : 0.f);
-                }
-                scale_rows(f[0], f[1]);
+            if (__any_sync(0xffffffffu, first || !(st.most * fmaxf(inv_unit[0], inv_unit[1]) <= kMost) ||
+                                            st.low * fminf(inv_unit[0], inv_unit[1]) < 2.f * kLeast) &&
+                !looked) {
+                apart = true;
+                break;
             }
+            looked = false;
+            phase ^= 1u << w;
             // K S (and Q S)
             float X[4][4] = {}, O[4][4] = {};
             __half2 top[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
@@ -912,7 +966,6 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 if (!ok)
                     break;
             }
-            first = false;
             // Y = b (V - a r K S), then W = T Y
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
@@ -961,11 +1014,14 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 }
                 ounit[0] = unit[0];
                 ounit[1] = unit[1];
-                auto out_of = [](float x) { return x > 0.f && (x < 0.5f || x > 32.f); };
+                auto out_of = [](float x) { return !(x >= 0.5f && x <= 32.f); };
                 if (__any_sync(0xffffffffu, out_of(m[0]) || out_of(m[1]))) {
+                    // a column that is left with nothing takes the size of what comes
+                    first = __any_sync(0xffffffffu, m[0] == 0.f || m[1] == 0.f);
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const float x = refit(hf, out_of(m[hf]) ? m[hf] : 0.f);
+                        const float x = refit(hf, steps(hf, out_of(m[hf]) ? m[hf] : 0.f));
+                        top0[hf] = m[hf] * x;
                         f[hf] *= x;
 #pragma unroll
                         for (int nt = 0; nt < 4; ++nt) {
@@ -1001,6 +1057,38 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
             break;
         const int w = c % R::HELP, turn = use & 1;
         Stage<DK, NCW> &st = sh.st[w];
+        {
+            // what is written to each column, in its unit
+            float m[2] = {0.f, 0.f};
+            int e[2];
+            bool far = st.alone;
+#pragma unroll
+            for (int i = t; i < kC; i += 4) {
+                const float b = st.b[i];
+                m[0] = fmaxf(m[0], fabsf(b * __bfloat162float(st.v[i][cw * 16 + g])));
+                m[1] = fmaxf(m[1], fabsf(b * __bfloat162float(st.v[i][cw * 16 + g + 8])));
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                m[hf] = quad_max(m[hf]) * inv_unit[hf];
+                e[hf] = first ? steps(hf, top0[hf]) : 0;
+                float most = m[hf] * __int_as_float((127 - e[hf]) << 23);
+                // far above the state, or all there is: the unit is theirs
+                const bool theirs = most > kMost || (first && !(top0[hf] > 0.f));
+                if (theirs) {
+                    e[hf] = steps(hf, m[hf]);
+                    most = m[hf] * __int_as_float((127 - e[hf]) << 23);
+                }
+                far |= !(most <= kMost) || ((theirs ? most > 0.f : st.gamma < kFades) && most * st.least < kLeast);
+            }
+            if (!__any_sync(0xffffffffu, far)) {
+                scale_rows(refit(0, e[0]), refit(1, e[1]));
+                first = false;
+                looked = true;
+                continue;
+            }
+        }
+        phase ^= 1u << w;
         if (R::SPLIT) {
             // nothing for the output warp this time: a unit of 0 says so
             ok = use == 0 || __all_sync(0xffffffffu, tc5_wait(&sh.taken[cw & 1], turn ^ 1, abort));
@@ -1023,6 +1111,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sh.empty[w]);
+        ++use;
     }
     if (!ok) {
         if (lane == 0)

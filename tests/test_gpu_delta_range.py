@@ -122,6 +122,76 @@ def test_states_that_grow_by_their_decay(name, Hk, Hv, dk, dv, n):
     _hold(name, x, bounded=False, only=(0, n - 1))
 
 
+# ------------------------------------------- states and values of different sizes
+
+@BOTH
+@SHAPE
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e8])
+@pytest.mark.parametrize("how", ["reset", "strong", "steady", "last"])
+def test_small_values_after_a_large_state(name, Hk, Hv, dk, dv, n, size, how):
+    """What is written after the state has decayed is as exact as if it had been small."""
+    x = _inputs(Hk, Hv, dk, dv, n, 75, 7)
+    x["S"] = x["S"] * size
+    for s in range(n):
+        r = s * 75
+        if how == "reset":
+            x["g"][r + 13] = -float("inf")
+        elif how == "strong":
+            x["g"][r + 5] = -25.0
+            x["g"][r + 40] = -8.0
+        elif how == "steady":
+            x["g"][r:r + 75] = -1.0
+        else:
+            x["g"][r + 31] = -1e9
+    _hold(name, x, only=(0, n - 1))
+
+
+@BOTH
+@SHAPE
+@pytest.mark.parametrize("state", [True, False], ids=["state", "zeros"])
+@pytest.mark.parametrize("up", [True, False], ids=["up", "down"])
+def test_values_whose_size_jumps(name, Hk, Hv, dk, dv, n, state, up):
+    """Rows of 1e-6 and rows of 1e6 in one chunk, with a state that forgets."""
+    x = _inputs(Hk, Hv, dk, dv, n, 75, 8)
+    for s in range(n):
+        r = s * 75
+        for a, b in ((0, 9), (20, 45), (50, 75)):
+            x["v"][r + a:r + b] = (x["v"][r + a:r + b].float() * (1e-6 if up else 1e6)).to(BF)
+        x["g"][r:r + 75:10] = -40.0
+    _hold(name, x, state=state, only=(0, n - 1))
+
+
+@BOTH
+@SHAPE
+@pytest.mark.parametrize("size", [1e-30, 1e20, 1e30, 1e36])
+def test_states_of_any_size(name, Hk, Hv, dk, dv, n, size):
+    x = _inputs(Hk, Hv, dk, dv, n, 40, 9)
+    x["S"] = x["S"] * size
+    x["g"][:] = -0.5
+    _hold(name, x, only=(0, n - 1))
+
+
+@BOTH
+def test_states_that_nothing_is_written_to(name):
+    """Values of zero under a decay: the state fades out row by row."""
+    x = _inputs(1, 2, 64, 32, 1, 100, 10)
+    x["v"].zero_()
+    x["g"][:] = -0.7
+    _hold(name, x)
+    x["beta"].zero_()
+    _hold(name, x)
+
+
+@BOTH
+def test_a_state_that_was_wiped_out_takes_small_values(name):
+    """After a reset to exactly zero the next chunks' values are far below the old state."""
+    x = _inputs(1, 2, 64, 32, 1, 140, 11)
+    x["S"] = x["S"] * 1e12
+    x["g"][31] = -float("inf")
+    x["v"][:64] = 0
+    _hold(name, x)
+
+
 # --------------------------------------------- answers that are small differences
 
 @BOTH
