@@ -322,10 +322,14 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     if (bads)
         return __ffs(bads) - 1;
     const float4 row = rows_to_half<DK>(&s.k[lane][0], &s.q[lane][0], topk, row_top<KU>(&s.q[lane][0]));
-    // r of k = K 2^e / sqrt(4^e sum + eps), 2^-e at hand
+    // r of k = K 2^-e / sqrt(4^-e sum + eps), 2^e at hand; beside an eps 4^e past fp32 the
+    // sum of a row below 2^-50 counts for nothing
     auto power = [](float inv) { return __int_as_float((254 << 23) - __float_as_int(inv)); };
-    const float r = !on ? 0.f : a.l2norm ? rsqrtf(row.z + a.l2_eps * row.x * row.x) : power(row.x);
-    const float rq = !on ? 0.f : a.l2norm ? rsqrtf(row.w + a.l2_eps * row.y * row.y) : power(row.y);
+    auto norm = [&](float inv, float sum) {
+        const float e = a.l2_eps * inv * inv;
+        return !a.l2norm ? power(inv) : e < INFINITY ? rsqrtf(sum + e) : power(inv) * rsqrtf(a.l2_eps);
+    };
+    const float r = on ? norm(row.x, row.z) : 0.f, rq = on ? norm(row.y, row.w) : 0.f;
     s.r[lane] = r;
     s.br[lane] = beta * r * r;
     const bool stretch = !(fabsf(beta * r * r) * row.z <= kGain) || gr > kGrowth;

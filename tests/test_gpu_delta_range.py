@@ -83,6 +83,16 @@ def test_large_keys_and_queries(name):
     _hold(name, x, state=False)
 
 
+@BOTH
+@pytest.mark.parametrize("state", [True, False], ids=["state", "zeros"])
+def test_normalized_keys_far_below_epsilon(name, state):
+    """Keys and queries of 2^-90, divided by the root of an epsilon of 1e-6."""
+    x = _inputs(1, 2, 64, 32, 1, 40, 14)
+    for key in ("q", "k"):
+        x[key] = (x[key].float() * 2.0 ** -90).to(BF)
+    _hold(name, x, eps=1e-6, state=state)
+
+
 # ------------------------------ rows that stretch the state
 
 @BOTH
