@@ -611,7 +611,8 @@ gattn_status gattn_prompt_rows(const gattn_prompt_rows_desc *desc, gattn_stream 
  *                      key rows cu_kv[s] .. cu_kv[s+1]-1 (cu_kv NULL: cu_rows),
  *                      and its row i sees the first i + 1 + (keys - rows) of
  *                      them: the last row sees all.
- * A row that sees no key gives zeros.  Values and keys that a row does not see
+ * k and v NULL with kv_rows 0: a tensor without keys; only sequences that ask for
+ * none are within it.  A row that sees no key gives zeros.  Values and keys that a row does not see
  * do not reach it, whatever they hold (NaN and infinities included).
  *   q, k, v       bf16
  *   gate          gate_dtype (GATTN_DTYPE_F32 or _BF16), or NULL for no gate

@@ -1072,17 +1072,22 @@ cudaError_t launch(const PromptAttnArgs &a, cudaStream_t s)
     const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)a.H, (cuuint64_t)a.sq.total};
     const cuuint64_t qst[2] = {(cuuint64_t)a.qs.head * 2, (cuuint64_t)a.qs.tok * 2};
     const cuuint32_t qb[3] = {64, (cuuint32_t)hp, (cuuint32_t)tpt};
-    const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)a.kv_rows, (cuuint64_t)a.Hk, (cuuint64_t)a.kv_batch};
-    const cuuint64_t kst[3] = {(cuuint64_t)a.kt * 2, (cuuint64_t)a.kh * 2, (cuuint64_t)a.kb * 2};
-    const cuuint64_t vst[3] = {(cuuint64_t)a.vt * 2, (cuuint64_t)a.vh * 2, (cuuint64_t)a.vb * 2};
+    // without keys no sequence has blocks to copy: a map of one row stands in
+    const bool keys = a.kv_rows > 0;
+    const cuuint64_t kd[4] = {(cuuint64_t)D, keys ? (cuuint64_t)a.kv_rows : 1, keys ? (cuuint64_t)a.Hk : 1,
+                              keys ? (cuuint64_t)a.kv_batch : 1};
+    const cuuint64_t kst[3] = {keys ? (cuuint64_t)a.kt * 2 : 16, keys ? (cuuint64_t)a.kh * 2 : 16,
+                               keys ? (cuuint64_t)a.kb * 2 : 16};
+    const cuuint64_t vst[3] = {keys ? (cuuint64_t)a.vt * 2 : 16, keys ? (cuuint64_t)a.vh * 2 : 16,
+                               keys ? (cuuint64_t)a.vb * 2 : 16};
     const cuuint32_t kb[4] = {64, 64, 1, 1}, vb[4] = {64, C::VK, 1, 1};
     const bool gate = a.gate && !a.gate_f32;
     const cuuint64_t gst[2] = {(cuuint64_t)a.gs.head * 2, (cuuint64_t)a.gs.tok * 2};
     const cuuint64_t ost[2] = {(cuuint64_t)a.os.head * 2, (cuuint64_t)a.os.tok * 2};
     if (!encode(&gm, 3, gate ? a.gate : a.q, qd, gate ? gst : qst, qb) || !encode(&om, 3, a.out, qd, ost, qb))
         return cudaErrorInvalidValue;
-    if (!encode(&qm, 3, a.q, qd, qst, qb) || !encode(&km, 4, a.k, kd, kst, kb) ||
-        !encode(&vm, 4, a.v, kd, vst, vb))
+    if (!encode(&qm, 3, a.q, qd, qst, qb) || !encode(&km, 4, keys ? a.k : a.q, kd, kst, kb) ||
+        !encode(&vm, 4, keys ? a.v : a.q, kd, vst, vb))
         return cudaErrorInvalidValue;
     // tiles of a pair, at most one partly filled per sequence
     const long long tiles =

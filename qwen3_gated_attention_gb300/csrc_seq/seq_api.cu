@@ -218,10 +218,13 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *p, gattn_
     if (!(p->scale > 0.f) || !std::isfinite(p->scale))
         return bad(GATTN_E_INVALID_ARG, "scale must be finite and > 0");
     CHECK(check_rows("q", p->q, p->q_stride_token, p->q_stride_head));
-    CHECK(check_rows("k", p->k, p->k_stride_token, p->k_stride_head));
-    CHECK(check_rows("v", p->v, p->v_stride_token, p->v_stride_head));
-    CHECK(check_rows("k", p->k, p->k_stride_batch, 8));
-    CHECK(check_rows("v", p->v, p->v_stride_batch, 8));
+    const bool keys = p->k || p->v || p->kv_rows != 0;
+    if (keys) {
+        CHECK(check_rows("k", p->k, p->k_stride_token, p->k_stride_head));
+        CHECK(check_rows("v", p->v, p->v_stride_token, p->v_stride_head));
+        CHECK(check_rows("k", p->k, p->k_stride_batch, 8));
+        CHECK(check_rows("v", p->v, p->v_stride_batch, 8));
+    }
     CHECK(check_out("out", p->out, p->o_stride_token, p->o_stride_head, p->head_dim, p->total_rows,
                     p->num_heads));
     CHECK(check_words({p->cu_rows, p->cu_kv, p->cache_pos, p->slots, p->status}));
@@ -232,8 +235,8 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *p, gattn_
     }
     if (!p->cu_rows)
         return bad(GATTN_E_INVALID_ARG, "cu_rows is NULL");
-    if (p->kv_batch <= 0 || p->kv_rows <= 0 || p->max_kv < 0)
-        return bad(GATTN_E_INVALID_ARG, "kv_batch and kv_rows must be > 0, max_kv >= 0");
+    if (p->kv_batch <= 0 || (keys && p->kv_rows <= 0) || p->max_kv < 0)
+        return bad(GATTN_E_INVALID_ARG, "kv_batch and kv_rows must be > 0 (kv_rows 0 without k and v), max_kv >= 0");
     if (!p->cache_pos && (p->kv_batch != 1 || p->slots))
         return bad(GATTN_E_INVALID_ARG, "packed keys have kv_batch 1 and no slots");
     if (p->cache_pos && p->cu_kv)

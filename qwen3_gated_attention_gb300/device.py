@@ -359,9 +359,9 @@ def prompt_attention(q, k, v, cu_rows, *, cu_kv=None, cache_pos=None, slots=None
         if nk != n:
             _refuse(cu_kv, "cu_kv", dev, _I32, n + 1, "must have cu_rows's length")
     if rows == 0:
-        # no keys at all (every row is empty): q stands in for their address
-        ka = va = (qa[0], 8, 8, 8)
-        B, rows = 1, 1
+        # a tensor without keys: no address, and rows that ask for some are skipped
+        ka = va = (0, 8, 8, 8)
+        B = max(B, 1)
     desc = gattn.gattn_prompt_attention_desc.pack(
         H, Hk, d, d ** -0.5 if scale is None else scale, n, T, cu, ckv,
         _flat(cache_pos, "cache_pos", dev, _I32, n), _flat(slots, "slots", dev, _I32, n), qa[0],

@@ -3,7 +3,7 @@ not say about memory and sizes."""
 import pytest
 
 from qwen3_gated_attention_gb300 import gattn
-from tests.test_seq_args import _rows
+from tests.test_seq_args import P, _attn, _rows
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -41,3 +41,12 @@ def test_cache_slots_that_share_memory(which, strides, fine):
 
 def test_one_slot_needs_no_batch_stride():
     gattn.prompt_rows(_rows(kc_stride_batch=8, vc_stride_batch=8))
+
+
+def test_no_keys():
+    """Null keys and values with kv_rows 0: a tensor without keys."""
+    none = dict(k=None, v=None, kv_rows=0)
+    gattn.prompt_attention(_attn(**none))
+    gattn.prompt_attention(_attn(cache_pos=P, kv_batch=2, **none))
+    for change in (dict(k=P), dict(v=P), dict(kv_rows=8), dict(kv_rows=-1)):
+        _refuses(gattn.prompt_attention, _attn(**{**none, **change}), 1, "")
