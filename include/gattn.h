@@ -538,6 +538,7 @@ gattn_status gattn_layer_set_test_wait(gattn_layer *layer, int64_t wait_limit_ns
  *     different streams share nothing, and every call can be captured into a
  *     CUDA graph.  The launches go to the current device, which must be the
  *     one the pointers belong to.
+ *   - total_rows and kv_rows are at most 2^30, num_seqs 2^24.
  *   - num_seqs == 0 or total_rows == 0 launches nothing (but see gattn_delta_*).
  * Errors of every entry point, before anything is launched: GATTN_E_INVALID_ARG
  * for a NULL pointer, a size, stride or alignment outside these rules, and

@@ -103,7 +103,7 @@ struct Cfg {
 };
 
 // What the order of the tiles needs of a sequence.  All of it fits 32 bits: counts of
-// rows.  A tile of a pair has tp = 1 << tl tokens.
+// at most 2^30 rows and keys.  A tile of a pair has tp = 1 << tl tokens.
 struct SeqKeys {
     int r0, len, slot, kv0;
     int past;                   // keys before its first row (negative: rows that see none)
@@ -117,9 +117,10 @@ struct SeqKeys {
         const int n = tiles(tl);
         if (x == 0 || n == 0)
             return n;
-        const int need = (x - 1) * kN + 1 - past;       // tokens that reach x blocks
-        if (len < need)
+        const int keys = (x - 1) * kN + 1;              // that reach x blocks
+        if (past + len < keys)
             return 0;
+        const int need = keys - past;                   // tokens that see so many: at most len
         return n - min(need <= 0 ? 0 : ((need + (1 << tl) - 1) >> tl) - 1, n - 1);
     }
 };
@@ -141,7 +142,7 @@ __device__ __forceinline__ SeqKeys seq_keys(const PromptAttnArgs &a, int s)
         past = kv1 - kv0 - q.len;
         q.ok = kv0 >= 0 && kv1 >= kv0 && kv1 <= a.kv_rows;
     }
-    q.past = q.ok ? (int)past : -(1 << 30);             // a skipped sequence sees nothing
+    q.past = q.ok ? (int)past : -q.len;                 // a skipped sequence sees nothing
     q.kv0 = (int)kv0;
     return q;
 }

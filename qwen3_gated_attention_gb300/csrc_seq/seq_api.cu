@@ -237,6 +237,8 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *p, gattn_
         return bad(GATTN_E_INVALID_ARG, "cu_rows is NULL");
     if (p->kv_batch <= 0 || (keys && p->kv_rows <= 0) || p->max_kv < 0)
         return bad(GATTN_E_INVALID_ARG, "kv_batch and kv_rows must be > 0 (kv_rows 0 without k and v), max_kv >= 0");
+    if (p->kv_rows > (1 << 30))
+        return bad(GATTN_E_INVALID_ARG, "kv_rows is too large");
     if (!p->cache_pos && (p->kv_batch != 1 || p->slots))
         return bad(GATTN_E_INVALID_ARG, "packed keys have kv_batch 1 and no slots");
     if (p->cache_pos && p->cu_kv)

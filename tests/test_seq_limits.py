@@ -43,6 +43,11 @@ def test_one_slot_needs_no_batch_stride():
     gattn.prompt_rows(_rows(kc_stride_batch=8, vc_stride_batch=8))
 
 
+def test_more_key_rows_than_there_can_be():
+    gattn.prompt_attention(_attn(kv_rows=1 << 30))
+    _refuses(gattn.prompt_attention, _attn(kv_rows=(1 << 30) + 1), 1, "too large")
+
+
 def test_no_keys():
     """Null keys and values with kv_rows 0: a tensor without keys."""
     none = dict(k=None, v=None, kv_rows=0)
