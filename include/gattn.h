@@ -602,7 +602,10 @@ gattn_status gattn_prompt_rows(const gattn_prompt_rows_desc *desc, gattn_stream 
  * gate:
  *   out[row][h] = bf16( sum_j softmax_j(scale * q[row][h] . k_j) v_j  *  sigmoid(gate[row][h]) )
  * over the keys j of the row's sequence that it may see; query head h reads KV
- * head h / (num_heads / num_kv_heads).  Where the keys come from:
+ * head h / (num_heads / num_kv_heads).  Scores, sums and out up to its one rounding
+ * are fp32; 2^(score - the row's reference) is rounded to bf16 before it meets its
+ * value, and those rounded numbers are what the softmax divides by the sum of.
+ * Where the keys come from:
  *   cache_pos != NULL  a cache [kv_batch][num_kv_heads][kv_rows] by strides:
  *                      sequence s reads cache row slots[s] (NULL: s), and its
  *                      row i sees positions 0 .. cache_pos[s] + i (the new

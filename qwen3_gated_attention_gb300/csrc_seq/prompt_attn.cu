@@ -8,7 +8,8 @@
 // softmax (base 2):
 //   S = Q K^T,  p = 2^(c (s - m)),  l <- l a + sum p,  O <- O a + P V,
 // a = 2^(c (m_old - m)).  S and O stay in tensor memory; P goes back into S's
-// columns as bf16 (one rounding per probability) and is the A operand of P V.
+// columns as bf16 and is the A operand of P V: the tensor cores take no wider operand
+// beside bf16 values at this rate.  l sums the rounded p, so that they add up to one.
 // Each CTA loads half of a block: 64 of its keys, and half of the value columns.
 // That halves what one SM reads from L2 and from its own shared memory per MMA
 // (with one CTA a tile, M = 128, the MMAs waited for their operands: a block took
@@ -31,12 +32,12 @@
 // Few rows over many keys: clusters of 2, 4 or 8 CTAs, each pair taking a share of
 // the blocks; the partial (m, l, O) are joined through distributed shared memory.
 //
-// Measured: one prompt of 8192 rows, 16 heads of 256 over 4: 391 us, 1404 TFLOP/s, 74 % of
-// the library's matrix rate (a block takes 3050 cycles, 2048 of them its products: the
+// Measured: one prompt of 8192 rows, 16 heads of 256 over 4: 384 us, 1430 TFLOP/s, 75 % of
+// the library's matrix rate (a block takes 3000 cycles, 2048 of them its products: the
 // rest is the hand-over between scores, softmax and values, which two score buffers
-// cover only in part).  Eight prompts of 1 to 1500 rows, 24 heads over 2: 76 us, 690
+// cover only in part).  Eight prompts of 1 to 1500 rows, 24 heads over 2: 77 us, 682
 // TFLOP/s of visible products; 4.4 blocks a tile, against an epilogue of 6800 cycles
-// (gates, exponentials, rows out) per tile.  Heads of 64: 40 us for 3960 rows of 16 heads
+// (gates, exponentials, rows out) per tile.  Heads of 64: 41.5 us for 3960 rows of 16 heads
 // over 8, bound by the softmax (1800 of 2775 cycles a block).
 #include <algorithm>
 #include <cmath>
@@ -789,15 +790,10 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                     e1 = ex2(e1);
                     e2 = ex2(e2);
                     e3 = ex2(e3);
-                    sum0 = add2(sum0, pack2(e0, e1));
-                    sum1 = add2(sum1, pack2(e2, e3));
                     pk[i] = pack_bf16x2(e0, e1);
                     pk[16 + i] = pack_bf16x2(e2, e3);
                 }
                 tmem_st32(S, pk);
-                float s0, s1;
-                unpack2(add2(sum0, sum1), s0, s1);
-                l += s0 + s1;
                 if (part) {
                     // slots are filled in the order K0 [K1 V0] [K2 V1] ...
                     int n = n0 + min(b + 2, t.nb) * C::KS + b * C::VS;
@@ -815,6 +811,15 @@ prompt_attn_kernel(const __grid_constant__ PromptAttnArgs a, const __grid_consta
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_cluster(at_lead(&T.p_ready[pb]));
+                // the sum of what the values are multiplied by, while they are
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    sum0 = add2(sum0, pack2(bf16_lo(pk[i]), bf16_hi(pk[i])));
+                    sum1 = add2(sum1, pack2(bf16_lo(pk[16 + i]), bf16_hi(pk[16 + i])));
+                }
+                float s0, s1;
+                unpack2(add2(sum0, sum1), s0, s1);
+                l += s0 + s1;
             }
             pvs += max(0, t.nb - 1);
             // ------------------------------------------------------------- epilogue
