@@ -687,8 +687,9 @@ gattn_status gattn_prompt_attention(const gattn_prompt_attention_desc *desc, gat
  * and both round out once, to bf16.  Rows that stretch the state (beta |k|^2 above
  * 2.25, or g above 1/256) and columns of it whose size changes by orders of
  * magnitude within 32 rows are within the rule: a prompt takes such rows one by
- * one, in a multiple of the time.  The errors of both are relative to norms (|q| times
- * that of a column of S), as those of fp32 sums are.
+ * one, in a multiple of the time.  Errors are those of fp32 sums relative to norms (|q|
+ * times that of a column of S), in a prompt plus 2^-24 of the largest that the column
+ * held or was written within the same 32 rows, counted from the sequence's first.
  * num_seqs > 0 with total_rows == 0 copies the states.  k_dim 64 or 128; v_dim a
  * multiple of 32 up to 256 (else GATTN_E_UNSUPPORTED).
  */

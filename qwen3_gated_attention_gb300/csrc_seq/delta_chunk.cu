@@ -31,10 +31,10 @@
 // or a growing "decay"), and columns whose size changes too far within the part (a row
 // that finds far less than the state the part began with, or than what is written later).
 //
-// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 242 us
+// Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 247 us
 // (1.9 us a chunk; its mma.sync instructions alone 0.3 us of it, the rest what each
-// of them waits for), 8 sequences of 1 to 1024 rows 126 us, the 1024 rows being the
-// longest chain (3.9 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
+// of them waits for), 8 sequences of 1 to 1024 rows 129 us, the 1024 rows being the
+// longest chain (4.0 us a chunk of 128 columns, 1.6 us of tensor time).  Tried and
 // slower: the state's update fused with the next chunk's K S (415 us: spills), rows
 // brought in by bulk copies (96 small ones a chunk), helpers with unrolled loops
 // (their code pushes the chain's out of the instruction cache: 267 to 320 us).
@@ -56,11 +56,11 @@ constexpr float kMinG = -200.f;    // e^-200 is 0 in fp32
 // 32 products of such T, K and S in [0.5, 32] stay below fp16's 65504
 constexpr float kGain = 2.25f, kTopT = 64.f, kGrowth = 1.f / 256;
 // A column's unit is the state's, or that of what a part writes where that is more than
-// kMost of the state's.  Its size changes too far where an operand off by 2^-25 of the unit
-// is more than 2^-17 of what a row finds: the state decays below kFades within the part,
-// or the unit is not the state's, and at some row all that has been written so far is
-// less than kLeast (the state of a unit of its own begins between 0.5 and 32)
-constexpr float kMost = 4096.f, kFades = 1.f / 256, kLeast = 1.f / 256;
+// kMost of the state's.  An operand is off by up to 2^-25 of the unit: a part goes row by
+// row where a row finds less than kLeast of it, in what is left of the state the part
+// began with (0.5 to 32 in its own unit) and in what has been written by then.  For a row
+// that writes nothing, only answers in 8 bits, an eighth of that is enough
+constexpr float kMost = 4096.f, kLeast = 1.f / 2048;
 
 // Every array starts on a 16-byte boundary: they are read in 16-byte vectors.
 template <int DK, int NCW>
@@ -79,14 +79,15 @@ struct alignas(16) Stage {
     alignas(16) float sq[kC];
     alignas(16) float r[kC];                       // for rows one by one: r, e^g
     alignas(16) float d[kC];
+    alignas(16) float found[kC];                   // |b v| a row finds written, over the part's largest; negative
+                                                   // before any b.  While T and A are made: low parts of G
     // the helper's own
     alignas(16) float lt[kC][kLS];                 // diagonal blocks of L^T: [j][i - j - 1]
     alignas(16) float gh[kC];
-    alignas(16) float gl[kC];
     alignas(16) float br[kC];                      // b r
     float gamma;                                   // decay of the part
-    float least;                                   // smallest size that some row finds written, over the largest
-    float most, low;                               // largest |b v|, infinite for `alone`; lowest_write() by least
+    float most;                                    // largest |b v|, infinite for `alone`
+    float low[2][NCW];                             // smallest_writes(): with and without empty columns
     int lo, hi, more;                              // rows of the chunk this is for; more of it follow
     int alone;                                     // row by row
 };
@@ -228,38 +229,65 @@ __device__ __forceinline__ float4 rows_to_half(__half *krow, __half *qrow, unsig
     return make_float4(fk, fq, kk[0] + kk[1], qq[0] + qq[1]);
 }
 
-// At most the smallest, over the columns, of the largest |b v| of a column (by every
-// fourth row and to 2^-7, which is enough to tell when the chain has to look closer).
+// For each chain warp's columns what tells it when to look closer: at most the smallest
+// of the columns' largest |b v| (by every fourth row and to 2^-7), by `least`, what rows
+// find of it at their least (infinite: of no interest).  Columns nothing is written to
+// are left out; if the state may fade in one of them, low[0] is 0.
 template <int DK, int NCW>
-__device__ __forceinline__ float lowest_write(const Stage<DK, NCW> &s)
+__device__ __forceinline__ void smallest_writes(Stage<DK, NCW> &s, float least)
 {
     // lanes side by side on pairs of columns, two rows at once where pairs are few
-    constexpr int PAIRS = 8 * NCW, PER = PAIRS > 32 ? PAIRS / 32 : 1, STEP = PAIRS < 32 ? 32 / PAIRS : 1;
+    constexpr int PAIRS = 8 * NCW, SIDE = PAIRS < 32 ? PAIRS : 32, PER = PAIRS / SIDE, STEP = 32 / SIDE;
     const int lane = threadIdx.x & 31;
-    __nv_bfloat162 top[PER];
-#pragma unroll
-    for (int p = 0; p < PER; ++p)
-        top[p] = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll
-    for (int r = 3 + 4 * (STEP > 1 ? lane / PAIRS : 0); r < kC; r += 4 * STEP) {
+    unsigned top[PER];
+    auto row = [&](int r) {
         const __nv_bfloat162 b = __float2bfloat162_rn(s.b[r]);
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             const __nv_bfloat162 v =
-                *reinterpret_cast<const __nv_bfloat162 *>(&s.v[r][2 * (lane % (PAIRS < 32 ? PAIRS : 32) + 32 * p)]);
-            top[p] = __hmax2(top[p], __habs2(__hmul2(v, b)));
+                __habs2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&s.v[r][2 * (lane % SIDE + 32 * p)]), b));
+            top[p] = __vmaxu2(top[p], *reinterpret_cast<const unsigned *>(&v));
         }
+    };
+    auto join = [&] {
+        bool none = false;
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+#pragma unroll
+            for (int o = SIDE; o < 32; o <<= 1)
+                top[p] = __vmaxu2(top[p], __shfl_xor_sync(0xffffffffu, top[p], o));
+            none |= (top[p] & 0xFFFFu) == 0 || top[p] >> 16 == 0;
+        }
+        return none;
+    };
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        top[p] = 0;
+#pragma unroll
+    for (int r = 3; r < kC; r += 4 * STEP)
+        row(r + 4 * (lane / SIDE));
+    if (__any_sync(0xffffffffu, join())) {
+#pragma unroll 1
+        for (int r = lane / SIDE; r < kC; r += STEP)
+            row(r);
+        join();
     }
-    unsigned low = 0xFFFFu;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-        unsigned u = *reinterpret_cast<const unsigned *>(&top[p]);
+        const unsigned x = __vsub2(top[p], 0x00010001u);               // zeros go to the top
+        unsigned low = min(x & 0xFFFFu, x >> 16), high = max(x & 0xFFFFu, x >> 16);
 #pragma unroll
-        for (int o = PAIRS; o < 32; o <<= 1)
-            u = __vmaxu2(u, __shfl_xor_sync(0xffffffffu, u, o));
-        low = min(low, min(u & 0xFFFFu, u >> 16));
+        for (int o = 1; o < 8; o <<= 1) {
+            low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
+            high = max(high, __shfl_xor_sync(0xffffffffu, high, o));
+        }
+        const float f = __uint_as_float(low << 16);                     // NaN: none is written to
+        if (lane < SIDE && lane % 8 == 0) {
+            const int group = lane / 8 + 4 * p;
+            s.low[0][group] = high == 0xFFFFu && least < INFINITY ? 0.f : f * least;
+            s.low[1][group] = f * fminf(least, 1.f);
+        }
     }
-    return __uint_as_float(__reduce_min_sync(0xffffffffu, low) << 16);
 }
 
 // Everything of rows [lo, hi) of the chunk at t0 that does not depend on the
@@ -309,7 +337,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
     }
     const float gch = __shfl_sync(0xffffffffu, gh, 31), gcl = __shfl_sync(0xffffffffu, gl, 31);
     s.gh[lane] = gh;
-    s.gl[lane] = gl;
+    s.found[lane] = gl;
     const float ai = ex2_pair(gh, gl), ci = ex2((gch - gh) + (gcl - gl));
     cp_async_wait_all();
     __syncwarp();
@@ -351,17 +379,19 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
             size = max(size, s2);
     }
     const int most = __reduce_max_sync(0xffffffffu, on ? size + at : INT_MIN / 2);
-    const int fewest = __reduce_min_sync(0xffffffffu, on ? size + at : INT_MAX / 2);
-    const float least = fewest < most ? ex2((float)(fewest - most)) : 1.f;
+    const unsigned acts = __ballot_sync(0xffffffffu, on && beta != 0.f);
+    const bool still = (acts & ((2u << lane) - 1)) == 0;           // as if the state only decayed
+    const float answers = acts >> lane & 1 ? 1.f : 8.f;
+    const float found = still ? -1.f : ex2((float)(size + at - most)) * answers;
+    // where little is left of the state: the least that is found written
+    const unsigned least = __reduce_min_sync(
+        0xffffffffu, __float_as_uint(on && !still && ai * answers < 2.f * kLeast ? found : INFINITY));
     if (lane == 31) {
         s.gamma = ai;
-        s.least = least;
         s.most = __uint_as_float(wtop);
     }
     __syncwarp();
-    const float low = __shfl_sync(0xffffffffu, ai, 31) < kFades ? least * lowest_write(s) : INFINITY;
-    if (lane == 0)
-        s.low = low;
+    smallest_writes(s, __uint_as_float(least));
     // The 16 x 8 tiles of K K^T and K Q^T (row j, column i) that hold some i >= j, and
     // from each its part of L and of A.  A loop that stays rolled: with it the code of
     // all roles stays small enough for the SM's instruction cache
@@ -383,13 +413,13 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
         }
         const int i0 = nt * 8 + 2 * t;
         const float2 ghi = *reinterpret_cast<const float2 *>(&s.gh[i0]);
-        const float2 gli = *reinterpret_cast<const float2 *>(&s.gl[i0]);
+        const float2 gli = *reinterpret_cast<const float2 *>(&s.found[i0]);
         const float2 bi = *reinterpret_cast<const float2 *>(&s.br[i0]);
         uint32_t vh[2], vl[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int j = mt * 16 + g + half * 8;
-            const float ghj = s.gh[j], glj = s.gl[j];
+            const float ghj = s.gh[j], glj = s.found[j];
             const float d0 = i0 >= j ? ex2((ghi.x - ghj) + (gli.x - glj)) : 0.f;
             const float d1 = i0 + 1 >= j ? ex2((ghi.y - ghj) + (gli.y - glj)) : 0.f;
             const float l0 = d0 * bi.x * kk[half * 2];
@@ -416,6 +446,7 @@ __device__ __forceinline__ int prepare_rows(const DeltaArgs &a, Stage<DK, NCW> &
         }
     }
     __syncwarp();
+    s.found[lane] = found;             // the tiles are done with G
     float top = 0.f;                   // T's largest entry
     // T = (I + L)^-1.  Its two 16 x 16 diagonal blocks by forward substitution, a
     // column per lane: x[0] is the next unknown, taken out of every later row while
@@ -884,7 +915,23 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
     };
     bool first = true;
     Handed<DK> &to = sh.to[R::SPLIT ? cw : 0];
+    auto load_values = [&](float (&v)[4][4], const Stage<DK, NCW> &st) {
+#pragma unroll
+        for (int n2 = 0; n2 < 2; ++n2) {
+            uint32_t x[4];
+            // rows of the tile are packed rows, its columns ours: transposed
+            ldsm_x4_trans(x, smem_u32(&st.v[n2 * 16 + pr][cw * 16 + pc]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int nt = n2 * 2 + (e >> 1), hf = e & 1;
+                v[nt][hf * 2] = bf16_lo(x[e]);
+                v[nt][hf * 2 + 1] = bf16_hi(x[e]);
+            }
+        }
+    };
+    auto pow2 = [](int e) { return __int_as_float((127 + e) << 23); };
     bool looked = false;
+    int bare = 0, empty = 0;               // a column of the warp, which of the lane's, without a state
     for (int c = 0, use = 0; ok && c < chunks;) {
         // the loop proper, until a part wants a closer look: what that takes stands
         // behind it, so that its registers and code are not in the way
@@ -896,20 +943,10 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 break;
             Stage<DK, NCW> &st = sh.st[w];
             float v[4][4];
-#pragma unroll
-            for (int n2 = 0; n2 < 2; ++n2) {
-                uint32_t x[4];
-                // rows of the tile are packed rows, its columns ours: transposed
-                ldsm_x4_trans(x, smem_u32(&st.v[n2 * 16 + pr][cw * 16 + pc]));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int nt = n2 * 2 + (e >> 1), hf = e & 1;
-                    v[nt][hf * 2] = bf16_lo(x[e]);
-                    v[nt][hf * 2 + 1] = bf16_hi(x[e]);
-                }
-            }
+            load_values(v, st);
             if (__any_sync(0xffffffffu, first || !(st.most * fmaxf(inv_unit[0], inv_unit[1]) <= kMost) ||
-                                            st.low * fminf(inv_unit[0], inv_unit[1]) < 2.f * kLeast) &&
+                                            st.low[bare][cw] * fminf(inv_unit[0], inv_unit[1]) <
+                                                (bare ? 1.f / 1024 : 1.25f * kLeast)) &&
                 !looked) {
                 apart = true;
                 break;
@@ -1019,13 +1056,15 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 ounit[0] = unit[0];
                 ounit[1] = unit[1];
                 auto out_of = [](float x) { return !(x >= 0.5f && x <= 32.f); };
+                bare = 0;
                 if (__any_sync(0xffffffffu, out_of(m[0]) || out_of(m[1]))) {
-                    // a column that is left with nothing takes the size of what comes
-                    first = __any_sync(0xffffffffu, m[0] == 0.f || m[1] == 0.f);
+                    empty = (m[0] == 0.f) + 2 * (m[1] == 0.f);
+                    bare = __any_sync(0xffffffffu, empty);
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const float x = refit(hf, steps(hf, out_of(m[hf]) ? m[hf] : 0.f));
-                        top0[hf] = m[hf] * x;
+                        // left with nothing: a unit for what the other columns take
+                        const float size = m[hf] == 0.f ? st.most * inv_unit[hf] : m[hf];
+                        const float x = refit(hf, steps(hf, out_of(size) ? size : 0.f));
                         f[hf] *= x;
 #pragma unroll
                         for (int nt = 0; nt < 4; ++nt) {
@@ -1063,30 +1102,45 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
         Stage<DK, NCW> &st = sh.st[w];
         {
             // what is written to each column, in its unit
-            float m[2] = {0.f, 0.f};
+            float v[4][4], m[2] = {0.f, 0.f};
             int e[2];
             bool far = st.alone;
+            load_values(v, st);
 #pragma unroll
-            for (int i = t; i < kC; i += 4) {
-                const float b = st.b[i];
-                m[0] = fmaxf(m[0], fabsf(b * __bfloat162float(st.v[i][cw * 16 + g])));
-                m[1] = fmaxf(m[1], fabsf(b * __bfloat162float(st.v[i][cw * 16 + g + 8])));
+            for (int nt = 0; nt < 4; ++nt) {
+                const float2 be = *reinterpret_cast<const float2 *>(&st.b[nt * 8 + 2 * t]);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                    m[hf] = fmaxf(m[hf], fmaxf(fabsf(be.x * v[nt][2 * hf]), fabsf(be.y * v[nt][2 * hf + 1])));
             }
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 m[hf] = quad_max(m[hf]) * inv_unit[hf];
-                e[hf] = first ? steps(hf, top0[hf]) : 0;
-                float most = m[hf] * __int_as_float((127 - e[hf]) << 23);
+                // its state at the least; what fp32 may hold for good below 2^-118 is none
+                float state = !first ? (empty >> hf & 1 ? 0.f : 0.5f) : top0[hf];
+                state = first && state * unit[hf] < 0x1p-118f ? 0.f : state;
+                e[hf] = first ? steps(hf, state) : 0;
                 // far above the state, or all there is: the unit is theirs
-                const bool theirs = most > kMost || (first && !(top0[hf] > 0.f));
-                if (theirs) {
+                if (m[hf] * pow2(-e[hf]) > kMost || !(state > 0.f))
                     e[hf] = steps(hf, m[hf]);
-                    most = m[hf] * __int_as_float((127 - e[hf]) << 23);
-                }
-                far |= !(most <= kMost) || ((theirs ? most > 0.f : st.gamma < kFades) && most * st.least < kLeast);
+                m[hf] *= pow2(-e[hf]);
+                state *= pow2(-e[hf]);
+                far |= !(m[hf] <= kMost);
+                // the rows of this lane's quarter of the part
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const int i = nt * 8 + 2 * t + o;
+                        const float found = st.found[i];
+                        const float x = fmaxf(st.a[i] * state * (st.b[i] == 0.f ? 8.f : 1.f), m[hf] * found);
+                        far |= i >= st.lo && i < st.hi && found >= 0.f && x < kLeast && (x > 0.f || state > 0.f);
+                    }
             }
             if (!__any_sync(0xffffffffu, far)) {
                 scale_rows(refit(0, e[0]), refit(1, e[1]));
+                if (first)
+                    bare = empty = 0;
                 first = false;
                 looked = true;
                 continue;

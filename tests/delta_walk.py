@@ -19,9 +19,13 @@ def unit(x, eps):
     return x if eps is None else x / torch.sqrt((x * x).sum(-1, keepdim=True) + eps)
 
 
-def walk(q, k, v, g, beta, S, scale, eps=None, dtype=torch.float64):
+def walk(q, k, v, g, beta, S, scale, eps=None, dtype=torch.float64, chunk=0):
     """One sequence: q, k [n][Hk][dk], v [n][Hv][dv], S [Hv][dk][dv].  Returns (out, state,
-    bound of out before its rounding, bound of the state's columns [Hv][1][dv])."""
+    bound of out before its rounding, bound of the state's columns [Hv][1][dv]).  With
+    `chunk` rows that are taken at once, a row leaves in a column 2^-24 more of the largest
+    norm that the column, or a write to it, has in the chunk: a 16-bit operand's lower part
+    ends at 2^-25 of a unit of at most a quarter of the largest element, in two products
+    (W and, for answers, A W)."""
     n, Hk, dk = q.shape
     Hv = v.shape[1]
     own = torch.arange(Hv) // (Hv // Hk)
@@ -29,8 +33,9 @@ def walk(q, k, v, g, beta, S, scale, eps=None, dtype=torch.float64):
     q, k = unit(q, eps)[:, own], unit(k, eps)[:, own]
     out = torch.zeros(n, Hv, v.shape[2], dtype=dtype)
     eo = torch.zeros_like(out)
-    e = torch.zeros(Hv, v.shape[2], dtype=dtype)
+    sizes, local = [], []
     for t in range(n):
+        before = S.norm(dim=1)
         a = torch.exp(g[t])[:, None]
         S = a[..., None] * S
         size = S.norm(dim=1)
@@ -40,9 +45,14 @@ def walk(q, k, v, g, beta, S, scale, eps=None, dtype=torch.float64):
         out[t] = scale * torch.einsum("ha,hab->hb", q[t], S)
         # the row's map I - beta k k^T stretches by 1 or by |1 - beta |k|^2|
         stretch = a * torch.clamp((1 - beta[t][:, None] * kn * kn).abs(), min=1)
-        e = stretch * e + U_ROW * (size + b * kn * (v[t].abs() + kn * size))
-        qn = abs(scale) * q[t].norm(dim=-1)[:, None]
-        eo[t] = qn * (e + U_ROW * (size + kn * w.abs()))
+        sizes.append(torch.maximum(torch.maximum(before, S.norm(dim=1)), kn * torch.maximum(w.abs(), b * v[t].abs())))
+        local.append((stretch, U_ROW * (size + b * kn * (v[t].abs() + kn * size)),
+                      abs(scale) * q[t].norm(dim=-1)[:, None], U_ROW * (size + kn * w.abs())))
+    e = torch.zeros(Hv, v.shape[2], dtype=dtype)
+    for t, (stretch, row, qn, answer) in enumerate(local):
+        most = torch.stack(sizes[t // chunk * chunk:][:chunk]).amax(0) if chunk else 0
+        e = stretch * e + row + 2.0 ** -24 * most
+        eo[t] = qn * (e + answer + 2.0 ** -23 * most)
     return out, S, eo, e[:, None, :]
 
 

@@ -4,8 +4,8 @@ that are small differences.  Both forms are held to the same bounds."""
 import pytest
 import torch
 
-from tests.delta_walk import judge
-from tests.seq_refs import cu_of
+from tests.delta_walk import judge, walk
+from tests.seq_refs import U_BF16, cu_of
 from tests.test_gpu_delta import _fn
 
 pytestmark = pytest.mark.gpu
@@ -200,6 +200,60 @@ def test_a_state_that_was_wiped_out_takes_small_values(name):
     x["g"][31] = -float("inf")
     x["v"][:64] = 0
     _hold(name, x)
+
+
+@pytest.mark.parametrize("seed", range(36))
+def test_sizes_of_every_kind_at_once(seed):
+    """Rows, columns, states and keys of sizes far apart, resets, rows without a value or a
+    strength, in any mixture: the prompt form is as exact as the step is, up to 2^-24 of
+    the largest that a column held or was written within the same 32 rows."""
+    pick = torch.Generator().manual_seed(seed)
+    draw = lambda *x: x[int(torch.randint(len(x), (1,), generator=pick))]  # noqa: E731
+    yes = lambda: draw(0, 0, 1)                                            # noqa: E731
+    Hk, Hv, dk, dv, n = draw(*SHAPES, (4, 8, 64, 128, 10))
+    rows = int(torch.randint(1, 110, (1,), generator=pick))
+    x = _inputs(Hk, Hv, dk, dv, n, rows, 100 + seed, decay=draw(0.0, 0.01, 0.1, 0.5, 2.0, 8.0))
+    T = n * rows
+    two = lambda e, *s: torch.exp2(torch.randint(-e, e + 1, s, generator=pick).float())  # noqa: E731
+    some = lambda p, *s: torch.rand(*s, generator=pick) < p                # noqa: E731
+    eps = draw(None, 1e-6)
+    if yes():
+        x["v"] = (x["v"].float() * two(draw(2, 6, 14), T, 1, 1)).to(BF)
+    if yes():
+        f = two(draw(2, 10, 20), dv)
+        x["v"], x["S"] = (x["v"].float() * f).to(BF), x["S"] * f
+    if yes():
+        x["v"] = (x["v"].float() * two(12, dv)).to(BF)
+    if yes():
+        x["S"] = x["S"] * two(30, 1)
+    if yes():
+        x["g"][some(draw(0.02, 0.2), T, Hv)] = -draw(3.0, 10.0, 30.0, 1e5)
+    if yes():
+        x["beta"][some(0.5, T, Hv)] = 0
+    if yes():
+        x["v"][some(0.5, T)] = 0
+    if yes():
+        x["v"][:, :, -8:], x["S"][..., -8:] = 0, draw(0.0, 1.0)
+    if yes():
+        f = two(4, T, 1, 1)
+        x["k"], x["beta"], eps = (x["k"].float() * f).to(BF), x["beta"] / f[:, :, 0] ** 2, None
+    if yes():
+        x["q"] = x["k"].clone()
+    state = draw(True, True, False)
+    for name in ("prompt", "step"):
+        dev = {key: t.cuda() for key, t in x.items() if isinstance(t, torch.Tensor)}
+        so = torch.full_like(dev["S"], 9.0)
+        out = _fn(name)(dev["q"], dev["k"], dev["v"], dev["g"], dev["beta"], cu_of([rows] * n, "cuda"),
+                        state=dev["S"] if state else None, state_out=so, scale=1.0, qk_l2norm=eps is not None,
+                        l2_eps=eps or 0.0).cpu()
+        for s in {0, n - 1}:
+            a = slice(s * rows, (s + 1) * rows)
+            S0 = x["S"][s] if state else torch.zeros_like(x["S"][s])
+            want, last, eo, es = walk(*(x[key][a] for key in ("q", "k", "v", "g", "beta")), S0, 1.0, eps,
+                                      chunk=32 if name == "prompt" else 0)
+            tol = U_BF16 * want.abs() + (1 + U_BF16) * eo + 1e-37
+            assert ((out[a].double() - want).abs() <= tol).all(), (name, s)
+            assert ((so[s].cpu().double() - last).abs() <= es + 1e-37).all(), (name, s)
 
 
 # --------------------------------------------- answers that are small differences
