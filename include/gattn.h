@@ -520,8 +520,9 @@ gattn_status gattn_layer_set_test_wait(gattn_layer *layer, int64_t wait_limit_ns
  *     owns rows cu_rows[s] .. cu_rows[s+1]-1 of every row tensor.  cu_rows is
  *     (device) int32 [num_seqs + 1], non-decreasing, its last entry at most
  *     total_rows, the rows that the tensors hold.  Rows before cu_rows[0] and
- *     at or past cu_rows[num_seqs] are neither read nor written.  A sequence
- *     may have no rows.
+ *     at or past cu_rows[num_seqs] are not written and reach no result, whatever
+ *     they hold; like all total_rows they have to be readable memory (tiles and
+ *     early loads may take them along).  A sequence may have no rows.
  *   - Tensors are described by a base pointer and element strides of the row
  *     ("token") and of the head; the elements of a head are contiguous.  bf16
  *     and fp32 rows: base 16-byte aligned, strides positive multiples of 8
@@ -532,8 +533,11 @@ gattn_status gattn_layer_set_test_wait(gattn_layer *layer, int64_t wait_limit_ns
  *   - Outputs must not overlap inputs unless an entry point says so.
  *   - `status` (device) uint32 [1], may be NULL: the kernels OR GATTN_STATUS_*
  *     bits into it (never clear it), so that a caller can read it when it
- *     likes; GATTN_STATUS_RANGE marks a sequence that was skipped because its
- *     rows, positions or slot lie outside what the descriptor holds.
+ *     likes.  GATTN_STATUS_RANGE: a sequence was skipped because its rows,
+ *     positions or slot lie outside what the descriptor holds.
+ *     GATTN_STATUS_TIMEOUT: a wait inside a kernel gave up after two seconds, and
+ *     rows or states of the call are missing.  Without a status word a skipped
+ *     sequence shows in its zero rows only, and a time-out not at all.
  *   - No handle, no allocation, no synchronization, no workspace: calls on
  *     different streams share nothing, and every call can be captured into a
  *     CUDA graph.  The launches go to the current device, which must be the

@@ -30,6 +30,7 @@
 // registers: rows that stretch the state (b r |K|^2 past 2.25, or an entry of T past 64,
 // or a growing "decay"), and columns whose size changes too far within the part (a row
 // that finds far less than the state the part began with, or than what is written later).
+// 32 rows then take 15 to 18 us instead of 1.9 to 4.
 //
 // Bound by the chain: 4096 rows of one sequence, 32 heads of 128 x 128, take 247 us
 // (1.9 us a chunk; its mma.sync instructions alone 0.3 us of it, the rest what each

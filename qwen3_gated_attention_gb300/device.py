@@ -198,7 +198,9 @@ def bf16_tensor_to_f64(t: torch.Tensor) -> np.ndarray:
 # Torch forms of the packed-sequence entry points: shapes and strides are read
 # off the tensors, the launch goes to the current stream of their device (or to
 # `stream`, a cudaStream_t handle of that device).  Slices of a wider projection
-# output are passed as they are, nothing is copied.
+# output are passed as they are, nothing is copied.  `status`, an int32 tensor of one
+# entry that the caller zeroes and reads, collects gattn.STATUS_* bits; without it a
+# sequence that was skipped shows in its zero rows only, and a time-out not at all.
 
 _DTYPES = {torch.float32: gattn.DTYPE_F32, torch.bfloat16: gattn.DTYPE_BF16}
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
