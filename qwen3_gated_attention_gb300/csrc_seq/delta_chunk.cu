@@ -1216,9 +1216,8 @@ cudaError_t launch_dk(const DeltaArgs &a, cudaStream_t s)
         return e;
     // columns per CTA: as many as keep every SM busy, since a CTA's helpers do the
     // same work for any number of them.  Sequences of 1024 rows with 32 heads of 128 x
-    // 128, by 32, 64 and 128 columns: one 61, 77 and 110 us; two 120, 78 and 111; four
-    // 241, 157 and 113; sixteen 842, 543 and 446 (six helpers instead of four at 64
-    // columns take registers from the chain: 83 us)
+    // 128, by 32, 64 and 128 columns: one 70, 86 and 125 us; two 140, 86 and 125; four
+    // 277, 175 and 128; sixteen 982, 608 and 507
     const long long cols = (long long)a.sq.n * a.Hv * a.dv;
     if (a.dv % 128 == 0 && cols / 64 > sms)
         return launch<DK, 8>(a, s);

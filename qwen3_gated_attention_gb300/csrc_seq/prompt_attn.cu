@@ -32,7 +32,7 @@
 // Few rows over many keys: clusters of 2, 4 or 8 CTAs, each pair taking a share of
 // the blocks; the partial (m, l, O) are joined through distributed shared memory.
 //
-// Measured: one prompt of 8192 rows, 16 heads of 256 over 4: 384 us, 1430 TFLOP/s, 75 % of
+// Measured: one prompt of 8192 rows, 16 heads of 256 over 4: 385 us, 1430 TFLOP/s, 75 % of
 // the library's matrix rate (a block takes 3000 cycles, 2048 of them its products: the
 // rest is the hand-over between scores, softmax and values, which two score buffers
 // cover only in part).  Eight prompts of 1 to 1500 rows, 24 heads over 2: 77 us, 682
