@@ -1057,7 +1057,7 @@ delta_chunk_kernel(const __grid_constant__ DeltaArgs a)
                 ounit[0] = unit[0];
                 ounit[1] = unit[1];
                 auto out_of = [](float x) { return !(x >= 0.5f && x <= 32.f); };
-                bare = 0;
+                bare = empty = 0;
                 if (__any_sync(0xffffffffu, out_of(m[0]) || out_of(m[1]))) {
                     empty = (m[0] == 0.f) + 2 * (m[1] == 0.f);
                     bare = __any_sync(0xffffffffu, empty);

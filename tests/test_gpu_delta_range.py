@@ -202,6 +202,22 @@ def test_a_state_that_was_wiped_out_takes_small_values(name):
     _hold(name, x)
 
 
+@BOTH
+@SHAPE
+@pytest.mark.parametrize("cols", [1, 16])
+@pytest.mark.parametrize("size", [1e-8, 0.0])
+def test_columns_that_wake_up(name, Hk, Hv, dk, dv, n, cols, size):
+    """Columns without a state or values for 32 rows, then with values, then with hardly
+    any: what they hold by then is theirs."""
+    x = _inputs(Hk, Hv, dk, dv, n, 100, 15)
+    x["g"][:] = -0.5
+    for s in range(n):
+        r = s * 100
+        x["v"][r:r + 32, :, :cols] = 0
+        x["v"][r + 64:r + 100] = (x["v"][r + 64:r + 100].float() * size).to(BF)
+    _hold(name, x, state=False, only=(0, n - 1))
+
+
 @pytest.mark.parametrize("seed", range(36))
 def test_sizes_of_every_kind_at_once(seed):
     """Rows, columns, states and keys of sizes far apart, resets, rows without a value or a
