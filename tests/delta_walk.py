@@ -56,7 +56,7 @@ def walk(q, k, v, g, beta, S, scale, eps=None, dtype=torch.float64, chunk=0):
     return out, S, eo, e[:, None, :]
 
 
-def judge(case, out, state, scale, eps=None, bounded=True, chunk=32):
+def hold_to_rule(case, out, state, scale, eps=None, bounded=True, chunk=32):
     """Holds out [n][Hv][dv] and state [Hv][dk][dv] (or None) of one sequence to the rule.
     Element by element: the last rounding and the bound above, where no row stretches the
     state (`bounded`).  Always, per head and per `chunk` rows: the 2-norm of the error

@@ -4,7 +4,7 @@ that are small differences.  Both forms are held to the same bounds."""
 import pytest
 import torch
 
-from tests.delta_walk import judge, walk
+from tests.delta_walk import hold_to_rule, walk
 from tests.seq_refs import U_BF16, cu_of
 from tests.test_gpu_delta import _fn
 
@@ -47,7 +47,7 @@ def _hold(name, x, scale=1.0, eps=None, state=True, bounded=True, only=None):
     for s in range(x["n"]) if only is None else only:
         a = slice(s * x["rows"], (s + 1) * x["rows"])
         S0 = x["S"][s] if state else torch.zeros_like(x["S"][s])
-        judge([x[key][a] for key in ("q", "k", "v", "g", "beta")] + [S0], out[a], so[s], scale, eps, bounded)
+        hold_to_rule([x[key][a] for key in ("q", "k", "v", "g", "beta")] + [S0], out[a], so[s], scale, eps, bounded)
 
 
 # ------------------------------------------------------------------ key scales
