@@ -724,6 +724,210 @@ typedef struct gattn_delta_desc {
 gattn_status gattn_delta_prompt(const gattn_delta_desc *desc, gattn_stream stream);
 gattn_status gattn_delta_step(const gattn_delta_desc *desc, gattn_stream stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A key-value cache in pages: decoding for a server that hands out cache memory in
+ * pages, beside the contiguous caches above.  (The pages of the reference keep one
+ * contiguous cache per layer, Atlas LayerKvCache; pages, scaled frequencies and
+ * eviction have no counterpart there.)
+ *
+ * Position p of sequence s is row p % page_size of page table[s][p / page_size] of two
+ * pools; element (page, hk, row, j) of the keys at
+ *   k_pages + page*k_stride_page + hk*k_stride_head + row*k_stride_token + j
+ * and the values likewise with strides of their own (bf16; base 16-byte aligned, strides
+ * positive multiples of 8 elements; a call that writes the pools needs their rows apart).
+ *   table        (device) int32 [num_seqs][table_width], row stride table_stride.  Only
+ *                entries of positions that a call touches are read.
+ *   page_size    a multiple of 16; table_width * page_size <= 2^24 (else
+ *                GATTN_E_UNSUPPORTED)
+ * The conventions of packed sequences hold, and these:
+ *   - A sequence with rows whose positions, cache_pos[s] .. cache_pos[s] + rows - 1, do
+ *     not fit its table row is skipped: GATTN_STATUS_RANGE.
+ *   - An entry outside [0, num_pages) is no page: its positions hold no keys (none is
+ *     attended, written or moved), GATTN_STATUS_RANGE; the rest of the sequence counts.
+ *   - Reading calls may name a page twice, for prefixes that sequences share.  No page
+ *     and row may be written by two rows of a call.
+ *   - Rows are read by whoever comes later on the same stream; nothing else orders
+ *     calls that share a pool.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct gattn_pages {
+    void *k_pages, *v_pages;
+    int32_t num_pages, page_size;
+    int64_t k_stride_token, k_stride_head, k_stride_page;
+    int64_t v_stride_token, v_stride_head, v_stride_page;
+    const int32_t *table;
+    int32_t table_width;
+    int64_t table_stride;
+} gattn_pages;
+
+enum { GATTN_ROPE_PLAIN = 0, GATTN_ROPE_LINEAR = 1, GATTN_ROPE_YARN = 2 };
+
+/*
+ * New rows between the projections and the attention, as gattn_prompt_rows, into pages:
+ * per-head RMSNorm, rotary embedding and append.  Row i of sequence s goes to position
+ * cache_pos[s] + i and is turned by the angles of positions[row] (NULL: the same
+ * position; after gattn_paged_evict a sequence's next token is further on than its next
+ * place).
+ *   q_norm, k_norm  bf16 [head_dim], 16-byte aligned; NULL: no norm
+ *   rotary_dims     even, 2 .. head_dim: the first elements of a head, turned in pairs
+ *   rope_pairs      0: (y_i, y_{i + rotary_dims/2});  else neighbours (y_2i, y_{2i+1})
+ *   frequencies     f_i = rope_theta^(-2i / rotary_dims), angle = position * f_i;
+ *     GATTN_ROPE_LINEAR: f_i / rope_factor
+ *     GATTN_ROPE_YARN: f_i (1 - c_i) + f_i / rope_factor * c_i, c_i rising from 0 to 1 between
+ *       pair floor(b(rope_beta_fast)) and ceil(b(rope_beta_slow)), kept within 0 and
+ *       rotary_dims - 1; b(t) = rotary_dims ln(rope_original / (2 pi t)) / (2 ln rope_theta)
+ *       (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models")
+ *     rope_factor >= 1
+ *   rope_size       factor of cos and sin; 0: 0.1 ln(rope_factor) + 1 for YaRN, else 1
+ *   positions       (device) int32 [total_rows], 0 .. 2^24.  A row outside is skipped alone
+ *                   (q_out zero, nothing written, GATTN_STATUS_RANGE).
+ * A skipped sequence's q_out rows are zero; a row whose page does not exist has its q_out
+ * all the same.  head_dim: a multiple of 64 up to 256 (else GATTN_E_UNSUPPORTED).
+ */
+typedef struct gattn_paged_rows_desc {
+    int32_t num_heads, num_kv_heads, head_dim;
+    int32_t rotary_dims, rope_pairs, rope_scaling;
+    float rope_theta, rope_factor;
+    int32_t rope_original;
+    float rope_beta_fast, rope_beta_slow, rope_size, rms_eps;
+    int32_t x_dtype;
+    int32_t num_seqs;
+    int32_t total_rows;
+    const int32_t *cu_rows;
+    const int32_t *cache_pos;
+    const int32_t *positions;
+    const void *q, *k, *v;
+    int64_t q_stride_token, q_stride_head;
+    int64_t k_stride_token, k_stride_head;
+    int64_t v_stride_token, v_stride_head;
+    const uint16_t *q_norm, *k_norm;
+    void *q_out;
+    int64_t o_stride_token, o_stride_head;
+    gattn_pages pages;
+    uint32_t *status;
+} gattn_paged_rows_desc;
+
+gattn_status gattn_paged_rows(const gattn_paged_rows_desc *desc, gattn_stream stream);
+
+/*
+ * Causal attention of new rows over pages, with grouped heads and the output gate:
+ *   out[row][h] = bf16( sum_p softmax_p(scale * q[row][h] . k_p) v_p  *  sigmoid(gate[row][h]) )
+ * Row i of sequence s sees positions 0 .. cache_pos[s] + i (its own key is in the pages,
+ * see gattn_paged_rows).  Made for one to a few new rows of each sequence (decoding,
+ * drafted rows to verify), any number is taken; a prompt is faster through
+ * gattn_prompt_attention.  Scores, sums and out up to its one rounding are fp32;
+ * the softmax's numerators meet the values with 16 bits.
+ *   q             bf16
+ *   gate          gate_dtype (GATTN_DTYPE_F32 or _BF16), or NULL for no gate
+ *   lse           fp32 [total_rows][num_heads] or NULL: ln sum_p exp(scale * q . k_p)
+ *   workspace     (device) at least gattn_paged_attention_workspace(...) bytes, 16-byte
+ *                 aligned, for the parts of sequences that several CTAs share.  Its
+ *                 contents need not be set and mean nothing afterwards.  Calls that may
+ *                 run at once (other streams, graphs replayed side by side) need one each.
+ * A row that sees no position (its sequence is skipped, or none of its pages exists) gives
+ * zeros and lse -infinity.  What a row does not see does not reach it, whatever it holds.
+ * A value that it does see and that is infinite or NaN makes its output infinite or NaN.
+ * head_dim: a multiple of 64 up to 256; num_heads * head_dim <= 65536 (else
+ * GATTN_E_UNSUPPORTED).
+ */
+typedef struct gattn_paged_attention_desc {
+    int32_t num_heads, num_kv_heads, head_dim;
+    float scale;
+    int32_t num_seqs;
+    int32_t total_rows;
+    const int32_t *cu_rows;
+    const int32_t *cache_pos;
+    const void *q;
+    int64_t q_stride_token, q_stride_head;
+    gattn_pages pages;
+    const void *gate;
+    int32_t gate_dtype;
+    int64_t g_stride_token, g_stride_head;
+    void *out;
+    int64_t o_stride_token, o_stride_head;
+    float *lse;
+    void *workspace;
+    int64_t workspace_bytes;
+    uint32_t *status;
+} gattn_paged_attention_desc;
+
+/* Bytes of workspace for these shapes (num_seqs sequences, total_rows rows), -1 for
+ * shapes that gattn_paged_attention refuses.  No GPU is needed. */
+int64_t gattn_paged_attention_workspace(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t num_seqs, int32_t total_rows);
+gattn_status gattn_paged_attention(const gattn_paged_attention_desc *desc, gattn_stream stream);
+
+/*
+ * The softmax weight that each position received from a call's rows, per KV head:
+ *   weights_out[s][hk][p] = weights[s][hk][p]
+ *                         + sum_{rows i that see p} sum_{h of hk's group} exp(scale * q_ih . k_p - lse_ih)
+ * for the positions p < cache_pos[s] + rows of each sequence with rows; others are left as
+ * they are.  Positions from cache_pos[s] on are new: they had nothing, whatever `weights`
+ * holds there.
+ *   attention     shapes, rows, q, scale, pages and status as gattn_paged_attention got
+ *                 them, lse what it left there; v_pages, gate, out and workspace are not read.
+ *                 A row whose lse is -infinity gives nothing.
+ *   weights       fp32, element (s, hk, p) at s*w_stride_seq + hk*w_stride_head + p, or
+ *                 NULL for zeros
+ *   weights_out   fp32, the same strides (which keep weights_width positions apart);
+ *                 may be weights
+ * A sequence with more positions than weights_width is skipped (GATTN_STATUS_RANGE).
+ * The sums have one order: equal inputs give equal bits.
+ */
+typedef struct gattn_paged_weights_desc {
+    gattn_paged_attention_desc attention;
+    const float *weights;
+    float *weights_out;
+    int32_t weights_width;
+    int64_t w_stride_seq, w_stride_head;
+} gattn_paged_weights_desc;
+
+gattn_status gattn_paged_weights(const gattn_paged_weights_desc *desc, gattn_stream stream);
+
+/*
+ * Shortens sequences: of the lengths[s] positions of sequence s and each KV head, the
+ * newest min(recent, .) and those of the others with the largest weights, m =
+ * min(lengths[s], keep) in all, move to positions 0 .. m-1 in their order.  Among equal
+ * weights the lowest position is kept; a NaN counts as -infinity.
+ *   lengths       (device) int32 [num_seqs]
+ *   weights       fp32, element (s, hk, p) at s*w_stride_seq + hk*w_stride_head + p
+ *   weights_out   fp32 with strides of its own, or NULL: weights of the kept positions,
+ *                 in their new places; may be weights (equal strides)
+ *   kept          int32 [num_seqs][num_kv_heads][keep]: the positions that were kept, in
+ *                 order; -1 behind them
+ *   lengths_out   int32 [num_seqs]: m; not in lengths' memory
+ *   out_table     the pages that the kept positions move to, of the same pools; NULL or
+ *                 pages.table: in place.  Other pages must not be among those that the
+ *                 call reads.  A sequence that keeps everything is copied to them too.
+ * Heads move on their own: a position's keys are those of different tokens for different
+ * heads afterwards, which attention does not mind (rotary positions are in the keys).
+ * Pages that are written must belong to one sequence.  A sequence whose length is
+ * negative or beyond its table row or weights_width, or whose m does not fit out_table
+ * or weights_out_width, is skipped: kept -1, its length as it was, GATTN_STATUS_RANGE.
+ */
+typedef struct gattn_paged_evict_desc {
+    int32_t num_kv_heads, head_dim;
+    int32_t num_seqs;
+    int32_t keep, recent;
+    gattn_pages pages;
+    const int32_t *out_table;
+    int32_t out_table_width;
+    int64_t out_table_stride;
+    const int32_t *lengths;
+    int32_t *lengths_out;
+    const float *weights;
+    int32_t weights_width;
+    int64_t w_stride_seq, w_stride_head;
+    float *weights_out;
+    int32_t weights_out_width;
+    int64_t wo_stride_seq, wo_stride_head;
+    int32_t *kept;
+    uint32_t *status;
+} gattn_paged_evict_desc;
+
+gattn_status gattn_paged_evict(const gattn_paged_evict_desc *desc, gattn_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

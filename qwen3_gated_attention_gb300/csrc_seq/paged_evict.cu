@@ -1,0 +1,319 @@
+// paged_evict.cu -- shortening the sequences of a paged cache: per key head the newest
+// positions and, of the others, those with the most weight, moved to the front in order.
+//
+// One CTA per sequence and head finds the positions: the weight that the last kept one
+// has by a radix select on the ordered bits of the fp32 weights (11, 11 and 10 bits; the
+// first 32768 stay in shared memory), then the positions above it and the first of those
+// that equal it, in order, by prefix sums.  Integer counts only, so the order of the
+// atomics does not matter.
+//
+// Then the rows move, bound by memory.  Into other pages, rows are independent: a warp
+// takes kRows of them, all loads before the first store.  In place a row may land where
+// another one that has to move still is; but never in front of it (position j takes one
+// from j or behind), so a CTA walks down the kept rows in chunks, for a slice of 64
+// elements alone (slices do not meet), and stores a chunk only when every thread has
+// loaded it.
+#include "paged.cuh"
+
+namespace gattn {
+
+namespace {
+
+constexpr int kSel = 1024;             // threads that select
+constexpr int kCached = 32768;         // weights kept in shared memory
+constexpr int kBins = 2048;
+constexpr int kSmem = kCached * 4 + 2 * kBins * 4;
+
+// Larger weights, larger numbers; a NaN counts as -infinity, both zeros as one.
+__device__ __forceinline__ uint32_t order_of(float w)
+{
+    if (w != w)
+        w = -INFINITY;
+    const uint32_t b = __float_as_uint(w + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// How many positions a sequence keeps; -1 where it is skipped.
+__device__ __forceinline__ int kept_of(const PagedEvictArgs &a, int len)
+{
+    const int m = min(len, a.keep);
+    return len < 0 || len > a.cap || m > a.out_cap ? -1 : m;
+}
+
+// Exclusive sum over the block's threads; `total` the sum of all.
+__device__ __forceinline__ int block_scan(int v, int *sums, int &total)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += x;
+    }
+    __syncthreads();                   // readers of the last call's sums
+    if (lane == 31)
+        sums[warp] = incl;
+    __syncthreads();
+    int x = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    total = __shfl_sync(0xffffffffu, x, 31);
+    const int before = __shfl_sync(0xffffffffu, x, (warp + 31) & 31);
+    return incl - v + (warp ? before : 0);
+}
+
+__global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constant__ PagedEvictArgs a)
+{
+    extern __shared__ uint32_t dyn[];
+    __shared__ int sums[32];
+    __shared__ uint32_t chosen[2];
+    uint32_t *const keys = dyn, *const hist = dyn + kCached;
+    const int hk = blockIdx.x % a.Hk, s = blockIdx.x / a.Hk, tid = threadIdx.x;
+    const int len = a.lengths[s], m = kept_of(a, len);
+    int *const kept = a.kept + ((long long)s * a.Hk + hk) * a.keep;
+    const float *const w = a.w + s * a.w_seq + hk * a.w_head;
+    float *const wo = a.w_out ? a.w_out + s * a.wo_seq + hk * a.wo_head : nullptr;
+    for (int j = max(m, 0) + tid; j < a.keep; j += kSel)
+        kept[j] = -1;
+    if (hk == 0 && tid == 0) {
+        a.lengths_out[s] = m < 0 ? len : m;
+        if (m < 0 && a.status)
+            atomicOr(a.status, GATTN_STATUS_RANGE);
+    }
+    if (m <= 0)
+        return;
+    const int rec = min(a.recent, m), cand = len - rec, need = m - rec;
+    uint32_t edge = 0;                 // of the last kept one
+    int ties = cand;                   // how many of its equals are kept
+    if (need < cand && need > 0) {
+        uint32_t mask = 0;
+        int left = need;
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+            for (int i = tid; i < 2 * kBins; i += kSel)
+                hist[i] = 0;
+            __syncthreads();
+            // two counts a bin, by warp: weights fall into few bins of the first digit
+            uint32_t *const my = hist + ((tid >> 5) & 1) * kBins;
+            for (int i = tid; i < cand; i += kSel) {
+                const uint32_t k = pass > 0 && i < kCached ? keys[i] : order_of(w[i]);
+                if (pass == 0 && i < kCached)
+                    keys[i] = k;
+                if ((k & mask) == edge)
+                    atomicAdd(&my[(k >> shift) & (bins - 1)], 1u);
+            }
+            __syncthreads();
+            // from the largest digit down, two bins a thread
+            const int hi = bins - 1 - 2 * tid;
+            const int c0 = hi >= 0 ? (int)(hist[hi] + hist[kBins + hi]) : 0;
+            const int c1 = hi > 0 ? (int)(hist[hi - 1] + hist[kBins + hi - 1]) : 0;
+            int all;
+            const int before = block_scan(c0 + c1, sums, all);
+            if (before < left && before + c0 >= left) {
+                chosen[0] = hi;
+                chosen[1] = left - before;
+            } else if (before + c0 < left && before + c0 + c1 >= left) {
+                chosen[0] = hi - 1;
+                chosen[1] = left - before - c0;
+            }
+            __syncthreads();
+            edge |= chosen[0] << shift;
+            mask |= (uint32_t)(bins - 1) << shift;
+            left = (int)chosen[1];
+            __syncthreads();
+        }
+        ties = left;
+    }
+    // the kept ones of the candidates in order: four positions a thread
+    int above = 0, equal = 0;
+    if (need > 0)
+        for (int base = 0; base < cand && (above + min(equal, ties)) < need; base += kSel * 4) {
+            const int i0 = base + tid * 4;
+            float v[4];
+            int kind[4], c = 0;        // 1: above the edge, 1 << 16: equal to it
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = i0 + e < cand ? w[i0 + e] : 0.f;
+                const uint32_t k = order_of(v[e]);
+                kind[e] = i0 + e >= cand ? 0 : need == cand || k == edge ? 1 << 16 : k > edge ? 1 : 0;
+                c += kind[e];
+            }
+            int all;
+            int at = block_scan(c, sums, all);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int up = above + (at & 0xFFFF), eq = equal + (at >> 16);
+                if (kind[e] == 1 || (kind[e] && eq < ties)) {
+                    const int j = up + min(eq, ties);
+                    kept[j] = i0 + e;
+                    if (wo)
+                        wo[j] = v[e];
+                }
+                at += kind[e];
+            }
+            above += all & 0xFFFF;
+            equal += all >> 16;
+        }
+    // the newest; in place a weight may land where one of a later round is not yet read,
+    // never where one of this round or an earlier one is
+    for (int base = 0; base < rec; base += kSel) {
+        const int r = base + tid;
+        const float v = r < rec && wo ? w[len - rec + r] : 0.f;
+        __syncthreads();
+        if (r < rec) {
+            kept[need + r] = len - rec + r;
+            if (wo)
+                wo[need + r] = v;
+        }
+    }
+}
+
+// Where position t of a table's row is: page and row in it; page -1 if there is none.
+struct Place {
+    int page, row;
+};
+
+__device__ __forceinline__ Place place_of(const PagedEvictArgs &a, const int *row, int t)
+{
+    Place p{row[t / a.pg.page], t % a.pg.page};
+    if (p.page < 0 || p.page >= a.pg.pages) {
+        p.page = -1;
+        if (a.status)
+            atomicOr(a.status, GATTN_STATUS_RANGE);
+    }
+    return p;
+}
+
+constexpr int kMove = 256, kRows = 8;
+
+// Into other pages: a warp moves kRows (heads of 64 and 128: 4 or 2 times as many) rows.
+__global__ void __launch_bounds__(kMove) paged_move_kernel(const __grid_constant__ PagedEvictArgs a, int groups)
+{
+    const int warp = (int)((blockIdx.x * (long long)kMove + threadIdx.x) >> 5) % groups, lane = threadIdx.x & 31;
+    const int sh = (int)(((blockIdx.x * (long long)kMove + threadIdx.x) >> 5) / groups);
+    if (sh >= a.n * a.Hk)
+        return;
+    const int s = sh / a.Hk, hk = sh % a.Hk;
+    const int m = kept_of(a, a.lengths[s]);
+    const int lpr = a.d == 64 ? 8 : a.d == 128 ? 16 : 32, per = 32 / lpr;
+    const int j0 = warp * kRows * per;
+    if (j0 >= m)
+        return;
+    // a lane a row
+    Place from{-1, 0}, to{-1, 0};
+    const int mine = j0 + lane;
+    if (lane < kRows * per && mine < m) {
+        from = place_of(a, a.pg.table + s * a.pg.table_stride, a.kept[(long long)sh * a.keep + mine]);
+        to = place_of(a, a.out_table + s * a.out_stride, mine);
+        if (to.page < 0)
+            from.page = -1;
+    }
+    const int c = (lane & (lpr - 1)) * 8;
+    uint4 k[kRows], v[kRows];
+    const __nv_bfloat16 *const kp = static_cast<const __nv_bfloat16 *>(a.pg.kp) + hk * a.pg.k.head + c;
+    const __nv_bfloat16 *const vp = static_cast<const __nv_bfloat16 *>(a.pg.vp) + hk * a.pg.v.head + c;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int l = i * per + lane / lpr;
+        const int page = __shfl_sync(0xffffffffu, from.page, l), row = __shfl_sync(0xffffffffu, from.row, l);
+        if (page >= 0 && c < a.d) {
+            k[i] = __ldcs(reinterpret_cast<const uint4 *>(kp + page * a.pg.k.page + row * a.pg.k.tok));
+            v[i] = __ldcs(reinterpret_cast<const uint4 *>(vp + page * a.pg.v.page + row * a.pg.v.tok));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int l = i * per + lane / lpr;
+        const bool on = __shfl_sync(0xffffffffu, from.page, l) >= 0;
+        const int page = __shfl_sync(0xffffffffu, to.page, l), row = __shfl_sync(0xffffffffu, to.row, l);
+        if (on && c < a.d) {
+            *reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(kp) + page * a.pg.k.page + row * a.pg.k.tok) = k[i];
+            *reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(vp) + page * a.pg.v.page + row * a.pg.v.tok) = v[i];
+        }
+    }
+}
+
+// In place: a CTA has 64 elements of the keys (or values) of one sequence and head.
+constexpr int kStep = 4, kChunk = kMove / 8 * kStep;
+
+__global__ void __launch_bounds__(kMove) paged_close_kernel(const __grid_constant__ PagedEvictArgs a)
+{
+    const int slices = a.d / 64;
+    int x = blockIdx.x;
+    const int slice = x % slices;
+    x /= slices;
+    const bool val = x & 1;
+    const int sh = x >> 1, s = sh / a.Hk, hk = sh % a.Hk;
+    const int len = a.lengths[s], m = kept_of(a, len);
+    if (m <= 0 || m == len)
+        return;                        // nothing moves
+    const int *const row = a.pg.table + s * a.pg.table_stride, *const kept = a.kept + (long long)sh * a.keep;
+    const PageStride &st = val ? a.pg.v : a.pg.k;
+    __nv_bfloat16 *const base = static_cast<__nv_bfloat16 *>(val ? a.pg.vp : a.pg.kp) + hk * st.head + slice * 64 +
+                                (threadIdx.x & 7) * 8;
+    uint4 cur[kStep], nxt[kStep];
+    __nv_bfloat16 *to[kStep], *to_n[kStep];
+    auto load = [&](int j0, uint4 (&v)[kStep], __nv_bfloat16 *(&dst)[kStep]) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            const int j = j0 + i * (kMove / 8) + (threadIdx.x >> 3);
+            dst[i] = nullptr;
+            if (j >= m)
+                continue;
+            const int t = kept[j];
+            if (t == j)
+                continue;              // stays
+            const Place f = place_of(a, row, t), o = place_of(a, row, j);
+            if (f.page < 0 || o.page < 0)
+                continue;
+            v[i] = *reinterpret_cast<const uint4 *>(base + f.page * st.page + f.row * st.tok);
+            dst[i] = base + o.page * st.page + o.row * st.tok;
+        }
+    };
+    load(0, cur, to);
+    for (int j0 = 0; j0 < m; j0 += kChunk) {
+        load(j0 + kChunk, nxt, to_n);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            if (to[i])
+                *reinterpret_cast<uint4 *>(to[i]) = cur[i];
+            cur[i] = nxt[i];
+            to[i] = to_n[i];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t s)
+{
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(paged_select_kernel, kSmem, done);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.n * a.Hk));
+    cfg.blockDim = dim3(kSel);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    e = cudaLaunchKernelEx(&cfg, paged_select_kernel, a);
+    if (e != cudaSuccess)
+        return e;
+    if (!a.out_table)
+        return launch_seq(paged_close_kernel, dim3((unsigned)(a.n * a.Hk * 2 * (a.d / 64))), dim3(kMove), s, a);
+    // kept rows, at most
+    const long long most = a.keep < a.out_cap ? a.keep : a.out_cap;
+    const int per = kRows * (a.d == 64 ? 4 : a.d == 128 ? 2 : 1);
+    const int groups = (int)((most + per - 1) / per);
+    const long long warps = (long long)groups * a.n * a.Hk;
+    return launch_seq(paged_move_kernel, dim3((unsigned)((warps + kMove / 32 - 1) / (kMove / 32))), dim3(kMove), s, a,
+                      groups);
+}
+
+}  // namespace gattn

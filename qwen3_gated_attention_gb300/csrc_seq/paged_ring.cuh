@@ -1,0 +1,398 @@
+// paged_ring.cuh -- how the kernels that read pages share out and fetch their work.
+//
+// The work of a call is a line of units: U consecutive positions of one sequence and KV
+// head, met by a tile of up to M query rows (a segment: all units of one sequence, head
+// and tile).  Every CTA takes an equal run of the line, wherever it begins or ends, so
+// that the lengths of the sequences do not matter.  One warp of a CTA (the producer)
+// walks the run: it looks up pages, copies units into a ring of shared memory by TMA and
+// the segments' query rows and descriptions into two buffers; the other warps consume.
+#pragma once
+
+#include "paged.cuh"
+
+namespace gattn {
+namespace paged {
+
+// Positions of a unit: 16 KB of keys and values (12 KB for heads of 192).
+template <int D>
+constexpr int kUnit = D >= 192 ? 16 : D == 128 ? 32 : 64;
+
+constexpr int kMaxCtas = 160;
+
+// A segment's part within a CTA, as the consumers get it.
+struct Part {
+    int live;              // 0: no more parts
+    int s, hk, r0, p0, len;
+    int rowf, hf, nrows;   // query row i: row rowf + (hf + i) / group, head (hf + i) % group
+    int u0, u1;            // units that some row sees
+    int whole, slot;       // the segment's only part, or where the part goes
+    int pass;              // of the weights' blocks of rows
+};
+
+struct SeqUnits {
+    int r0, len, p0, units;
+    long long tiles;       // of rows
+    __device__ __forceinline__ long long all(int Hk) const { return tiles * Hk * units; }
+};
+
+// `bad`: rows whose positions do not fit the table
+__device__ __forceinline__ SeqUnits seq_units(const PagedAttnArgs &a, int s, int group, int M, int U, bool &bad)
+{
+    SeqUnits u;
+    seq_rows(a.sq, s, u.r0, u.len);
+    u.p0 = a.pos[s];
+    bad = u.len > 0 && (u.p0 < 0 || (long long)u.p0 + u.len > a.cap);
+    const bool on = u.len > 0 && !bad;
+    u.units = on ? (u.p0 + u.len + U - 1) / U : 0;
+    u.tiles = on ? M ? ((long long)u.len * group + M - 1) / M : 1 : 0;
+    return u;
+}
+
+// A CTA's run of units and where it begins.
+struct Run {
+    long long x0, x1, quota;
+    long long at;          // first unit of sequence s
+    int s;
+};
+
+// Called by every thread of the block (NT of them).  M: rows of a tile; 0: all rows
+// of a sequence are one tile.  `skipped` is called by one thread of one CTA for every
+// sequence that does not fit its table.
+template <int NT, int M, int U, class F>
+__device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int min_units, F skipped)
+{
+    __shared__ long long sums[32];
+    __shared__ long long found_at;
+    __shared__ int found;
+    constexpr int NW = NT / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n = a.sq.n;
+    long long mine = 0, first = 0;
+    for (int s = tid; s < n; s += NT) {
+        bool bad;
+        const SeqUnits u = seq_units(a, s, group, M, U, bad);
+        if (bad && s % gridDim.x == blockIdx.x)
+            skipped(s, u);
+        mine += u.all(a.Hk);
+        if (s == tid)
+            first = mine;
+    }
+    for (int o = 16; o; o >>= 1)
+        mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0)
+        sums[warp] = mine;
+    if (tid == 0)
+        found = -1;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < NW; ++w)
+        total += sums[w];
+    Run r;
+    r.quota = (total + gridDim.x - 1) / gridDim.x;
+    r.quota = r.quota > min_units ? r.quota : min_units;
+    r.x0 = r.quota * blockIdx.x;
+    r.x1 = r.x0 + r.quota < total ? r.x0 + r.quota : total;
+    r.s = 0;
+    r.at = 0;
+    if (r.x0 >= r.x1)
+        return r;                       // the whole block
+    long long before = 0;
+    for (int base = 0; base < n; base += NT) {
+        const int s = base + tid;
+        long long u = 0;
+        if (base == 0)
+            u = first;
+        else if (s < n) {
+            bool bad;
+            u = seq_units(a, s, group, M, U, bad).all(a.Hk);
+        }
+        long long incl = u;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        __syncthreads();
+        if (lane == 31)
+            sums[warp] = incl;
+        __syncthreads();
+        long long all = 0;
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp)
+                incl += sums[w];
+            all += sums[w];
+        }
+        incl += before;
+        if (u > 0 && r.x0 >= incl - u && r.x0 < incl) {
+            found = s;
+            found_at = incl - u;
+        }
+        before += all;
+        if (r.x0 < before)
+            break;                      // uniform
+    }
+    __syncthreads();
+    r.s = found;
+    r.at = found_at;
+    return r;
+}
+
+// ------------------------------------------------------------------ waiting
+
+// Waits for a phase, for two seconds at most; then (or once another wait of the CTA has
+// given up) false.
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, volatile int *abort, const SeqArgs &q)
+{
+    if (mbar_try(bar, parity))
+        return true;
+    const unsigned long long t0 = global_ns();
+    while (true) {
+        if (mbar_try(bar, parity))
+            return true;
+        if (*abort)
+            return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            seq_flag(q, GATTN_STATUS_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// 5-D tiled copy global -> shared: element, position in the page, block of 64
+// elements, head, page.
+__device__ __forceinline__ void box_g2s(uint32_t dst, const CUtensorMap *map, int y, int hk, int page, uint32_t bar,
+                                        uint64_t policy)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(0), "r"(hk), "r"(page), "r"(bar),
+                 "l"(policy)
+                 : "memory");
+}
+
+// 16 bytes to shared memory without waiting; zeros where !on
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
+// an arrival once the thread's copies so far have landed
+__device__ __forceinline__ void cp_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The ring and the two row buffers of a CTA.
+template <int D, int M_, bool V_, int SLOTS_, int READERS, int CONSUMERS>
+struct Ring {
+    static constexpr int U = kUnit<D>, DB = D / 64, M = M_, SLOTS = SLOTS_;
+    static constexpr bool V = V_;                      // values too
+    static constexpr int PLANE = U * D * 2, UNIT = V ? 2 * PLANE : PLANE;
+    static constexpr int QB = M * D * 2;               // query rows, 16-byte pieces swizzled by row
+    uint64_t full[SLOTS], empty[SLOTS];
+    uint64_t qfull[2], qempty[2];
+    Part part[2];
+    float lse[2][V ? 1 : M];
+    unsigned ok[SLOTS];                                // boxes of a unit whose page exists
+    volatile int abort;
+    int go;
+
+    __device__ __forceinline__ void init()
+    {
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], READERS);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&qfull[i], 64);
+            mbar_init(&qempty[i], CONSUMERS);
+        }
+        abort = 0;
+        fence_mbar_init();
+    }
+};
+
+// Positions of a box: what divides the page and the unit.
+__host__ __device__ inline int box_log2(int page, int U)
+{
+    int l = 4;
+    while (l < 6 && (2 << l) <= U && page % (2 << l) == 0)
+        ++l;
+    return l;
+}
+
+// The producer warp.  `units`: the ring's memory (1024-byte aligned), `qbuf` that of the
+// row buffers.  `seen` is told of the last segment, if it begins in this run and goes on
+// behind it: (part, CTA of its last unit).
+template <class R, class F>
+__device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t *units, uint8_t *qbuf,
+                                        const CUtensorMap *kmap, const CUtensorMap *vmap, const Run &run, int group,
+                                        F seen)
+{
+    constexpr int U = R::U, D = R::U > 0 ? R::DB * 64 : 0, M = R::M;
+    const int lane = threadIdx.x & 31;
+    const int btl = box_log2(a.pg.page, U), BT = 1 << btl, NB = U >> btl;
+    const uint32_t box_bytes = BT * D * 2;
+    const uint64_t pol = l2_evict_first_policy();
+    long long it = 0;                  // units so far
+    int parts = 0;
+    bool stop = false;
+    int s = run.s;
+    bool bad;
+    SeqUnits u = seq_units(a, s, group, R::V ? M : 0, U, bad);
+    long long seg = (run.x0 - run.at) / u.units;
+    int u0 = (int)((run.x0 - run.at) % u.units);
+    // pages of 32 boxes of sequence tab_s, one a lane
+    int tab_s = -1, tab_b = 0, tab_page = 0, tab_y = 0;
+    for (long long x = run.x0; x < run.x1 && !stop;) {
+        if (seg >= u.tiles * a.Hk) {
+            do
+                u = seq_units(a, ++s, group, R::V ? M : 0, U, bad);
+            while (u.units == 0);
+            seg = 0;
+            u0 = 0;
+        }
+        const int u1 = (int)(run.x1 - x < u.units - u0 ? u0 + (run.x1 - x) : u.units);
+        const int hk = (int)(seg / u.tiles);
+        const bool whole = u0 == 0 && u1 == u.units;
+        const long long passes = R::V ? 1 : ((long long)u.len * group + M - 1) / M;
+        for (long long pass = 0; pass < passes && !stop; ++pass, ++parts) {
+            // ---- the rows and the description
+            const int b = parts & 1;
+            Part p;
+            p.live = 1;
+            p.s = s;
+            p.hk = hk;
+            p.r0 = u.r0;
+            p.p0 = u.p0;
+            p.len = u.len;
+            const long long i0 = (R::V ? seg % u.tiles : pass) * M;
+            const long long left = (long long)u.len * group - i0;
+            p.rowf = (int)(i0 / group);
+            p.hf = (int)(i0 % group);
+            p.nrows = (int)(left < M ? left : M);
+            const int last = u.p0 + p.rowf + (p.hf + p.nrows - 1) / group;     // position the tile sees last
+            p.u0 = u0;
+            p.u1 = R::V ? min(u1, last / U + 1) : u1;
+            p.whole = whole;
+            p.slot = x == run.x0 ? 0 : 1;
+            p.pass = (int)min(pass, 1ll);
+            if (!ring_wait(&ring.qempty[b], (uint32_t)((parts >> 1) & 1) ^ 1u, &ring.abort, a.sq))
+                stop = true;
+            stop = __any_sync(0xffffffffu, stop);
+            if (stop)
+                break;
+            const uint32_t qdst = smem_u32(qbuf) + b * R::QB;
+            constexpr int CH = D / 8, RPI = 32 / CH > 0 ? 32 / CH : 1;          // rows of an iteration
+            for (int i = 0; i < M; i += RPI) {
+                const int row = i + (RPI > 1 ? lane / CH : 0);
+                const bool on = row < p.nrows;
+                const int h = p.hf + (on ? row : 0);
+                const __nv_bfloat16 *src =
+                    a.q + (p.r0 + p.rowf + h / group) * a.qs.tok + (hk * group + h % group) * a.qs.head;
+                for (int c = RPI > 1 ? lane % CH : lane; c < CH; c += 32)
+                    cp16(qdst + row * (D * 2) + ((c ^ (row & 7)) << 4), src + c * 8, on);
+            }
+            if constexpr (!R::V)
+                for (int i = lane; i < M; i += 32) {
+                    float v = -INFINITY;
+                    if (i < p.nrows)
+                        v = a.lse[(long long)(p.r0 + p.rowf + (p.hf + i) / group) * a.H + hk * group + (p.hf + i) % group];
+                    // 2^(score - v): a row that saw nothing gives nothing
+                    ring.lse[b][i] = v == -INFINITY ? INFINITY : v * 1.44269504f;
+                }
+            if (lane == 0)
+                ring.part[b] = p;
+            cp_arrive(&ring.qfull[b]);
+            mbar_arrive(&ring.qfull[b]);
+            // ---- the units
+            for (int n = p.u0; n < p.u1; ++n, ++it) {
+                const int b0 = n * NB;
+                if (tab_s != s || b0 < tab_b || b0 >= tab_b + 32) {
+                    tab_s = s;
+                    tab_b = b0 & ~31;
+                    const int t = (tab_b + lane) << btl;
+                    int page = -1;
+                    if (t < u.p0 + u.len) {
+                        page = a.pg.table[s * a.pg.table_stride + t / a.pg.page];
+                        if (page < 0 || page >= a.pg.pages) {
+                            page = -1;
+                            seq_flag(a.sq, GATTN_STATUS_RANGE);
+                        }
+                    }
+                    tab_page = page;
+                    tab_y = t % a.pg.page;
+                }
+                const int slot = (int)(it % R::SLOTS);
+                if (lane == 0 &&
+                    !ring_wait(&ring.empty[slot], (uint32_t)((it / R::SLOTS) & 1) ^ 1u, &ring.abort, a.sq))
+                    stop = true;
+                stop = __any_sync(0xffffffffu, stop);
+                if (stop)
+                    break;
+                // boxes that hold positions of the sequence
+                const int nb = min(NB, ((u.p0 + u.len - n * U) + BT - 1) >> btl);
+                const unsigned there = __ballot_sync(0xffffffffu, tab_page >= 0);
+                if (lane == 0) {
+                    ring.ok[slot] = (there >> (b0 - tab_b)) & ((1u << nb) - 1u);
+                    mbar_arrive_expect_tx(&ring.full[slot], nb * box_bytes * (R::V ? 2 : 1));
+                }
+                __syncwarp();
+                // a lane a box; a page that does not exist is one behind the last: zeros
+                const int from = b0 - tab_b + lane;
+                const int page = __shfl_sync(0xffffffffu, tab_page, from & 31);
+                const int y = __shfl_sync(0xffffffffu, tab_y, from & 31);
+                if (lane < nb) {
+                    const uint32_t dst = smem_u32(units) + slot * R::UNIT + lane * box_bytes;
+                    const uint32_t bar = smem_u32(&ring.full[slot]);
+                    box_g2s(dst, kmap, y, hk, page < 0 ? a.pg.pages : page, bar, pol);
+                    if (R::V)
+                        box_g2s(dst + R::PLANE, vmap, y, hk, page < 0 ? a.pg.pages : page, bar, pol);
+                }
+            }
+            if (lane == 0 && u0 == 0 && u1 < u.units)
+                seen(p, (int)((x + u.units - 1) / run.quota));
+        }
+        x += u1 - u0;
+        u0 = 0;
+        ++seg;
+    }
+    if (!stop) {
+        const int b = parts & 1;
+        stop = !ring_wait(&ring.qempty[b], (uint32_t)((parts >> 1) & 1) ^ 1u, &ring.abort, a.sq);
+        stop = __any_sync(0xffffffffu, stop);
+        if (!stop) {
+            if (lane == 0)
+                ring.part[b].live = 0;
+            cp_arrive(&ring.qfull[b]);
+            mbar_arrive(&ring.qfull[b]);
+        }
+    }
+    // no copy may be on its way when the block ends (where consumers gave up)
+    cp_async_wait_all();
+    if (lane == 0)
+        for (long long i = it > R::SLOTS ? it - R::SLOTS : 0; i < it; ++i) {
+            const unsigned long long t0 = global_ns();
+            while (!mbar_try(&ring.full[i % R::SLOTS], (uint32_t)((i / R::SLOTS) & 1)) &&
+                   global_ns() - t0 < kWaitLimitNs) {
+            }
+        }
+    __syncwarp();
+}
+
+// --------------------------------------------------------------- the products
+
+// m16n8k16 of bf16 operands into fp32; free to be scheduled between the loads
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+}  // namespace paged
+
+bool encode_pages(CUtensorMap *m, const Pages &pg, bool v, int Hk, int d, int box);
+
+}  // namespace gattn

@@ -1,0 +1,204 @@
+// paged_weights.cu -- how much softmax weight the positions of a paged cache received:
+//
+//   w_out[p] = w[p] + sum over rows i that see p and heads h of the group of
+//              exp(scale q_ih . k_p - lse_ih)
+//
+// with the logarithms of the softmax sums that the attention left.  Bound by memory: the
+// keys are read once for all rows and heads of a group (64 of them; more take another
+// pass over the CTA's own units, which L2 mostly still holds).  The work is cut as
+// paged_ring.cuh says; a warp alone takes a unit, sums over the rows in its registers and
+// writes each position once, so there are no atomics and the sums have one order.
+#include "paged_ring.cuh"
+
+namespace gattn {
+
+using namespace paged;
+
+namespace {
+
+template <int D>
+struct Cfg {
+    static constexpr int M = 64, CW = 8, THREADS = (CW + 1) * 32;
+    static constexpr int U = kUnit<D>, UNIT = U * D * 2;
+    static constexpr int FIT = (227 * 1024 - 2 * M * D * 2 - 4096) / UNIT;
+    // a slot always serves the same warp: a wait then cannot take the phase before last
+    // for the one it is about (copies land in any order)
+    static constexpr int SLOTS = (FIT > 24 ? 24 : FIT) / CW * CW;
+    static constexpr int SMEM = SLOTS * UNIT + 2 * M * D * 2 + 1024;
+    using R = Ring<D, M, false, SLOTS, 1, CW>;
+    static_assert(SMEM + sizeof(R) + 512 <= 227 * 1024 && SLOTS > 0, "");
+};
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+    paged_weights_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap, int min_units)
+{
+    using C = Cfg<D>;
+    using R = typename C::R;
+    constexpr int CW = C::CW, U = C::U;
+    extern __shared__ uint8_t raw[];
+    __shared__ R ring;
+    uint8_t *units = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *qbuf = units + C::SLOTS * C::UNIT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = a.H / a.Hk;
+    if (threadIdx.x == 0) {
+        ring.init();
+        prefetch_tensormap(&kmap);
+    }
+    const Run run = plan_run<C::THREADS, 0, U>(a, group, min_units,
+                                               [&](int, const SeqUnits &) { seq_flag(a.sq, GATTN_STATUS_RANGE); });
+    if (run.x0 >= run.x1)
+        return;
+    if (warp == CW) {
+        produce(a, ring, units, qbuf, &kmap, &kmap, run, group, [](const Part &, int) {});
+        return;
+    }
+    const int g = lane >> 2, cq = lane & 3;
+    const int btl = box_log2(a.pg.page, U), box = (1 << btl) * D * 2, dbs = (1 << btl) * 128;
+    long long it = 0;
+    for (int parts = 0;; ++parts) {
+        const int b = parts & 1;
+        // the barrier also orders a pass behind the one before it
+        if (threadIdx.x == 0)
+            ring.go = ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq) && ring.part[b].live;
+        named_bar_sync(1, CW * 32);
+        const int go = ring.go;
+        named_bar_sync(1, CW * 32);
+        if (!go)
+            break;
+        ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq);
+        const Part p = ring.part[b];
+        const int first_row = p.p0 + p.rowf, end = p.p0 + p.len;
+        const int count = p.u1 - p.u0, tiles = (p.nrows + 15) / 16;
+        const uint32_t qrow = smem_u32(qbuf) + b * R::QB + (lane & 15) * (D * 2);
+        const long long at = p.s * a.w_seq + p.hk * a.w_head;
+        const float *const from = p.pass ? a.w_out : a.w;
+        const int known = p.pass ? end : p.p0;          // positions that have a weight
+        for (int n = (int)((warp - it) & (CW - 1)); n < count; n += CW) {
+            const long long idx = it + n;
+            const int slot = (int)(idx % R::SLOTS);
+            const int t0 = (p.u0 + n) * U;
+            // what the positions have: this lane's 2 cq and 2 cq + 1 of each 8
+            float old[U / 8][2];
+#pragma unroll
+            for (int j = 0; j < U / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = t0 + j * 8 + 2 * cq + e;
+                    old[j][e] = g == 0 && from && t < known ? from[at + t] : 0.f;
+                }
+            const bool ok = ring_wait(&ring.full[slot], (uint32_t)((idx / R::SLOTS) & 1), &ring.abort, a.sq);
+            const uint32_t ks = smem_u32(units) + slot * C::UNIT;
+            if (ok) {
+                const unsigned there = ring.ok[slot];
+                const int kt = (lane & 7) + 8 * (lane >> 4);
+                const bool mask = t0 + U - 1 > first_row || there != (1u << (U >> btl)) - 1u;
+                float sum[U / 8][2];
+#pragma unroll
+                for (int j = 0; j < U / 8; ++j)
+                    sum[j][0] = sum[j][1] = 0.f;
+                for (int mt = 0; mt < tiles; ++mt) {
+                    constexpr int CHAINS = U == 16 ? 2 : 1;
+                    float sc[CHAINS][U / 8][4];
+#pragma unroll
+                    for (int c = 0; c < CHAINS; ++c)
+#pragma unroll
+                        for (int j = 0; j < U / 8; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                sc[c][j][e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t qa[4];
+                        ldsm_x4(qa, qrow + mt * 16 * (D * 2) + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
+                        const int ch = 2 * k + ((lane >> 3) & 1);
+#pragma unroll
+                        for (int q = 0; q < U / 16; ++q) {
+                            const int in = (q * 16) >> btl, off = (q * 16) & ((1 << btl) - 1);
+                            uint32_t kb[4];
+                            ldsm_x4(kb, ks + in * box + (ch >> 3) * dbs + (off + kt) * 128 + (((ch & 7) ^ (lane & 7)) << 4));
+                            mma(sc[k % CHAINS][2 * q], qa, kb[0], kb[1]);
+                            mma(sc[k % CHAINS][2 * q + 1], qa, kb[2], kb[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int hr = 0; hr < 2; ++hr) {
+                        const int i = mt * 16 + g + 8 * hr;
+                        const float lse = ring.lse[b][i];
+                        const int lim = i < p.nrows ? first_row + (p.hf + i) / group : -1;
+#pragma unroll
+                        for (int j = 0; j < U / 8; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int t = j * 8 + 2 * cq + e;
+                                float v = sc[0][j][2 * hr + e];
+                                if (CHAINS == 2)
+                                    v += sc[CHAINS - 1][j][2 * hr + e];
+                                v = exp2f(fmaf(v, a.scale_log2, -lse));
+                                if (lim < 0 || (mask && (t0 + t > lim || !((there >> (t >> btl)) & 1u))))
+                                    v = 0.f;
+                                sum[j][e] += v;
+                            }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < U / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v = sum[j][e];
+                        v += __shfl_xor_sync(0xffffffffu, v, 4);
+                        v += __shfl_xor_sync(0xffffffffu, v, 8);
+                        v += __shfl_xor_sync(0xffffffffu, v, 16);
+                        const int t = t0 + j * 8 + 2 * cq + e;
+                        if (g == 0 && t < end)
+                            a.w_out[at + t] = old[j][e] + v;
+                    }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ring.empty[slot]);
+        }
+        it += count;
+        if (lane == 0)
+            mbar_arrive(&ring.qempty[b]);
+    }
+}
+
+template <int D>
+cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
+{
+    using C = Cfg<D>;
+    auto *fn = paged_weights_kernel<D>;
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(fn, C::SMEM, done);
+    if (e != cudaSuccess)
+        return e;
+    int sms = 0;
+    e = sm_count(&sms);
+    if (e != cudaSuccess)
+        return e;
+    CUtensorMap km;
+    if (!encode_pages(&km, a.pg, false, a.Hk, D, 1 << box_log2(a.pg.page, C::U)))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms < kMaxCtas ? sms : kMaxCtas);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, fn, a, km, 4);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_weights(const PagedAttnArgs &a, cudaStream_t s)
+{
+    switch (a.d) {
+    case 64: return launch<64>(a, s);
+    case 128: return launch<128>(a, s);
+    case 192: return launch<192>(a, s);
+    default: return launch<256>(a, s);
+    }
+}
+
+}  // namespace gattn

@@ -12,7 +12,11 @@
 // barriers 144 us; a warp that loads, then works 88 us; one head row at a time 188 us);
 // more loads on their way or more warps cost registers: 82 us with 24 warps an SM.  37
 // rows of 16 + 4 + 4 heads: 4.5 us.
-#include "seq.cuh"
+//
+// The paged form (gattn_paged_rows) is the same kernel: the cache row is found through a
+// page table, the pairs (y_i, y_j) may be neighbours, the norms may be absent, the angles
+// may come from positions of their own, and cos and sin carry a factor.
+#include "paged.cuh"
 
 namespace gattn {
 
@@ -57,16 +61,25 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
+// Where the elements that are turned together sit.
+enum Form {
+    kFast,      // rd/2 apart, rd/2 a multiple of 4
+    kSwap,      // rd/2 apart
+    kPairs      // neighbours
+};
+
 // A group of d/8 lanes (padded to a power of two) per head row, eight elements a
-// lane, in two runs of four.  FAST: rd/2 is a multiple of 4; the first rd/8 lanes of
-// a group then take a run from each rotary half, so partners meet in a lane.
-// Otherwise the runs are neighbours and partners meet in shared memory.
-template <bool F32, bool FAST>
+// lane, in two runs of four.  kFast: the first rd/8 lanes of a group take a run from
+// each rotary half, so partners meet in a lane.  Otherwise the runs are neighbours;
+// partners that are not meet in shared memory (kSwap).
+template <bool F32, int FORM, bool PAGED>
 __global__ void __launch_bounds__(kWarps * 32, F32 ? 4 : 5)
-prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
+prompt_rows_kernel(const __grid_constant__ std::conditional_t<PAGED, PagedRowsArgs, PromptRowsArgs> a, int parts)
 {
+    constexpr bool FAST = FORM == kFast;
+    constexpr int NA = FORM == kSwap ? 8 : 4;       // angles of a lane
     __shared__ float2 table[kWarps][128];
-    __shared__ float swap[FAST ? 1 : kWarps][256];
+    __shared__ float swap[FORM == kSwap ? kWarps : 1][256];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long job = (long long)blockIdx.x * kWarps + warp;
     const int t = (int)(job / parts), part = (int)(job % parts);
@@ -104,18 +117,38 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
         return;
     int r0, len;
     seq_rows(a.sq, s, r0, len);
-    const int slot = seq_slot_warp(a.sq, s, true);
     const long long p0 = a.pos[s], p = p0 + (t - r0);
     // the last two hold for any row, if the offsets do not fall
-    const bool ok = slot >= 0 && p0 >= 0 && p0 + len <= a.cap && t >= r0 && t - r0 < len;
-    if (!ok && lane == 0)
+    bool ok = p0 >= 0 && p0 + len <= a.cap && t >= r0 && t - r0 < len;
+    long long kat = 0, vat = 0;            // the row's place in the caches
+    bool keep = true;                      // it has one
+    int at_pos = (int)p;                   // position of the angles
+    if constexpr (PAGED) {
+        if (a.positions) {
+            at_pos = a.positions[t];
+            ok = ok && at_pos >= 0 && at_pos <= kMaxPos;
+        }
+        int page = -1;
+        if (ok)
+            page = a.pg.table[s * a.pg.table_stride + (int)p / a.pg.page];
+        keep = page >= 0 && page < a.pg.pages;
+        const int in = ok ? (int)p % a.pg.page : 0;
+        kat = page * a.pg.k.page + in * a.pg.k.tok;
+        vat = page * a.pg.v.page + in * a.pg.v.tok;
+    } else {
+        const int slot = seq_slot_warp(a.sq, s, true);
+        ok = ok && slot >= 0;
+        kat = slot * a.kcb + p * a.kct;
+        vat = slot * a.vcb + p * a.vct;
+    }
+    if (!(ok && keep) && lane == 0)
         seq_flag(a.sq, GATTN_STATUS_RANGE);
     float2 *const cs = table[warp];
     for (int i = lane; i < half; i += 32) {
         // The angle p * inv_freq as an unevaluated float pair, reduced modulo
         // 2 pi in two steps: good to a few 1e-7 rad at far positions without
         // double arithmetic
-        const float pos = (float)p;
+        const float pos = (float)at_pos;
         const float2 fq = a.inv_freq[i];
         const float ph = pos * fq.x;
         const float pl = fmaf(pos, fq.x, -ph) + pos * fq.y;
@@ -125,22 +158,34 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
         red += pl;
         float sn, c;
         __sincosf(red, &sn, &c);
+        if constexpr (PAGED) {
+            c *= a.turn_size;
+            sn *= a.turn_size;
+        }
         cs[i] = make_float2(c, sn);
     }
     __syncwarp();
     const float inv_d = 1.f / (float)a.d;
-    float cosv[FAST ? 4 : 8], sinv[FAST ? 4 : 8];
+    float cosv[NA], sinv[NA];
     Raw<false> wq, wk;
     wq.clear();
     wk.clear();
+    // a norm that is absent: no weights, and nothing to divide by
+    const bool qn = !PAGED || a.q_norm, kn = !PAGED || a.k_norm;
     if (act) {
-        wq.load(a.q_norm, o0, o1);
-        wk.load(a.k_norm, o0, o1);
+        if (qn)
+            wq.load(a.q_norm, o0, o1);
+        if (kn)
+            wk.load(a.k_norm, o0, o1);
     }
 #pragma unroll
-    for (int i = 0; i < (FAST ? 4 : 8); ++i) {
+    for (int i = 0; i < NA; ++i) {
         const int j = FAST ? o0 + i : j0 + i;
-        if (FAST) {
+        if (FORM == kPairs) {
+            const bool in = j0 + 2 * i < a.rd;
+            cosv[i] = in ? cs[j0 / 2 + i].x : 1.f;
+            sinv[i] = in ? cs[j0 / 2 + i].y : 0.f;
+        } else if (FAST) {
             cosv[i] = rot ? cs[j].x : 1.f;
             sinv[i] = rot ? cs[j].y : 0.f;
         } else {
@@ -148,11 +193,11 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
             sinv[i] = j < a.rd ? (j < half ? -cs[j].y : cs[j - half].y) : 0.f;
         }
     }
-    float *const buf = FAST ? nullptr : swap[warp] + at * lpu * 8;
+    float *const buf = FORM == kSwap ? swap[FORM == kSwap ? warp : 0] + at * lpu * 8 : nullptr;
     // `heads` head rows from `src`, the first of them on their way, to `dst`, normed and
     // turned by weights w; `then` fetches what comes after
     auto normed = [&](const void *src, long long src_head, __nv_bfloat16 *dst, long long dst_head, int heads,
-                      const Raw<false> &weight, auto then) {
+                      const Raw<false> &weight, bool norm, auto then) {
         __nv_bfloat16 *to = dst + (long long)first * dst_head;
         for (int u0 = first; u0 - at < heads || u0 == first; u0 += kFly * step) {
             Raw<F32> raw[kFly];
@@ -186,8 +231,14 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
                 const float inv = ok ? rsqrtf(ss * inv_d + a.eps) : 0.f;   // skipped rows: zeros
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    y[i] = x[i] * (inv * w[i]);
-                if (FAST) {
+                    y[i] = norm ? x[i] * (inv * w[i]) : x[i];
+                if (FORM == kPairs) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[2 * i] = y[2 * i] * cosv[i] - y[2 * i + 1] * sinv[i];
+                        x[2 * i + 1] = y[2 * i + 1] * cosv[i] + y[2 * i] * sinv[i];
+                    }
+                } else if (FAST) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         x[i] = y[i];
@@ -206,8 +257,8 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int j = j0 + i;
-                        x[i] = j < a.rd ? y[i] * cosv[FAST ? 0 : i] +
-                                              buf[j < half ? j + half : j - half] * sinv[FAST ? 0 : i]
+                        x[i] = j < a.rd ? y[i] * cosv[FORM == kSwap ? i : 0] +
+                                              buf[j < half ? j + half : j - half] * sinv[FORM == kSwap ? i : 0]
                                         : y[i];
                     }
                 }
@@ -218,13 +269,21 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
             }
         }
     };
-    normed(qrow, a.qs.head, a.q_out + t * a.os.tok, a.os.head, a.H, wq,
+    normed(qrow, a.qs.head, a.q_out + t * a.os.tok, a.os.head, a.H, wq, qn,
            [&] { fetch(krow, a.ks.head, first, a.Hk, o0, o1); });
-    if (!ok)
+    if (!ok || !keep)
         return;
-    normed(krow, a.ks.head, a.kc + slot * a.kcb + p * a.kct, a.kch, a.Hk, wk,
+    __nv_bfloat16 *kc, *vc;
+    long long kch, vch;
+    if constexpr (PAGED) {
+        kc = static_cast<__nv_bfloat16 *>(a.pg.kp) + kat, kch = a.pg.k.head;
+        vc = static_cast<__nv_bfloat16 *>(a.pg.vp) + vat, vch = a.pg.v.head;
+    } else {
+        kc = a.kc + kat, kch = a.kch;
+        vc = a.vc + vat, vch = a.vch;
+    }
+    normed(krow, a.ks.head, kc, kch, a.Hk, wk, kn,
            [&] { fetch(vrow, a.vs.head, first, a.Hk, j0, j0 + 4); });
-    __nv_bfloat16 *const vc = a.vc + slot * a.vcb + p * a.vct;
     for (int u0 = first; u0 < a.Hk; u0 += kFly * step) {
         Raw<F32> raw[kFly];
 #pragma unroll
@@ -237,7 +296,7 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
             if (act && u0 + f * step < a.Hk) {
                 float x[8];
                 raw[f].get(x);
-                __nv_bfloat16 *to = vc + (u0 + f * step) * a.vch + j0;
+                __nv_bfloat16 *to = vc + (u0 + f * step) * vch + j0;
                 store4(to, x[0], x[1], x[2], x[3]);
                 store4(to + 4, x[4], x[5], x[6], x[7]);
             }
@@ -246,7 +305,9 @@ prompt_rows_kernel(const __grid_constant__ PromptRowsArgs a, int parts)
 
 }  // namespace
 
-cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t s)
+// The launch of either form's kernel.
+template <class Args>
+static cudaError_t launch_rows(void (*fn)(const Args, int), const Args &a, int x_f32, cudaStream_t s)
 {
     int sms = 0;
     const cudaError_t e = sm_count(&sms);
@@ -262,10 +323,25 @@ cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t 
         parts *= 2;
     const long long jobs = (long long)a.sq.total * parts;
     const dim3 grid((unsigned)((jobs + kWarps - 1) / kWarps)), block(kWarps * 32);
-    const bool fast = (a.rd / 2) % 4 == 0;
-    auto *fn = x_f32 ? (fast ? prompt_rows_kernel<true, true> : prompt_rows_kernel<true, false>)
-                     : (fast ? prompt_rows_kernel<false, true> : prompt_rows_kernel<false, false>);
     return launch_seq(fn, grid, block, s, a, parts);
+}
+
+cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t s)
+{
+    const bool fast = (a.rd / 2) % 4 == 0;
+    return launch_rows(x_f32 ? (fast ? prompt_rows_kernel<true, kFast, false> : prompt_rows_kernel<true, kSwap, false>)
+                             : (fast ? prompt_rows_kernel<false, kFast, false> : prompt_rows_kernel<false, kSwap, false>),
+                       a, x_f32, s);
+}
+
+cudaError_t launch_paged_rows(const PagedRowsArgs &a, int x_f32, cudaStream_t s)
+{
+    const int form = a.pairs ? kPairs : (a.rd / 2) % 4 == 0 ? kFast : kSwap;
+    using Fn = void (*)(const PagedRowsArgs, int);
+    static constexpr Fn fns[2][3] = {
+        {prompt_rows_kernel<false, kFast, true>, prompt_rows_kernel<false, kSwap, true>, prompt_rows_kernel<false, kPairs, true>},
+        {prompt_rows_kernel<true, kFast, true>, prompt_rows_kernel<true, kSwap, true>, prompt_rows_kernel<true, kPairs, true>}};
+    return launch_rows(fns[x_f32 ? 1 : 0][form], a, x_f32, s);
 }
 
 }  // namespace gattn

@@ -2,7 +2,8 @@
 interchange layout, bf16 caches, inputs, outputs); every computation goes
 through ``gattn.layer_step`` and friends.  ``DeviceLayer`` holds one layer;
 ``prompt_rows``, ``prompt_attention``, ``delta_prompt`` and ``delta_step`` call
-the packed-sequence operators on tensors."""
+the packed-sequence operators on tensors, ``paged_rows``, ``paged_attention``,
+``paged_weights`` and ``paged_evict`` those over a cache in pages."""
 from __future__ import annotations
 
 import numpy as np
@@ -266,14 +267,14 @@ def _cu(t, name, dev):
     return t.data_ptr(), t.shape[0] - 1
 
 
-def _output(shape, like, stream):
-    """A bf16 tensor whose memory belongs to the stream that will write it."""
+def _output(shape, like, stream, dtype=torch.bfloat16):
+    """A tensor whose memory belongs to the stream that will write it."""
     if stream is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     own = (torch.cuda.ExternalStream(stream, device=like.device) if stream
            else torch.cuda.default_stream(like.device))        # handle 0
     with torch.cuda.stream(own):
-        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _call(fn, desc, dev, stream):
@@ -455,3 +456,205 @@ def delta_step(q, k, v, g, beta, cu_rows=None, *, num_seqs=None, state=None, sta
     (gattn_delta_step); arguments as delta_prompt."""
     return _delta(gattn.delta_step, q, k, v, g, beta, cu_rows, num_seqs, state, state_out, slots,
                   scale, qk_l2norm, l2_eps, out, status, stream)
+
+
+# ------------------------------------------------------------- paged caches
+#
+# Torch forms of the paged-cache entry points, as those above.  k_pages and v_pages are
+# bf16 [pages][Hk][page_size][d] views, table int32 [n][width] with contiguous rows:
+# position p of sequence s is row p % page_size of page table[s, p // page_size].
+
+def _table(t, name, dev, n):
+    """(address, width, row stride) of a page table of n rows."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.int32 or
+            t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1)):
+        _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
+    w = t.shape[1]
+    return t.data_ptr(), w, t.stride(0) if n > 1 else max(w, 1)
+
+
+def _pool(k_pages, v_pages, table, dev, n):
+    """The fields of gattn_pages; v_pages None: keys only."""
+    kp, kt, kh, kb = _planes(k_pages, "k_pages", dev, _BF16)
+    vp, vt, vh, vb = ((0, 8, 8, 8) if v_pages is None else
+                      _planes(v_pages, "v_pages", dev, _BF16, k_pages.shape))
+    ta, w, ts = _table(table, "table", dev, n)
+    return kp, vp, k_pages.shape[0], k_pages.shape[2], kt, kh, kb, vt, vh, vb, ta, w, ts
+
+
+def _received(t, name, dev, n, Hk):
+    """(address, width, sequence, head stride) of a weight tensor [n][Hk][positions]."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.float32:
+        _refuse(t, name, dev, _F32, (n, Hk, "positions"))
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[0] != n or sh[1] != Hk or (st[2] != 1 and sh[2] > 1):
+        _refuse(t, name, dev, _F32, (n, Hk, "positions"))
+    w = sh[2]
+    return t.data_ptr(), w, st[0] if n > 1 else Hk * w, st[1] if Hk > 1 else w
+
+
+def paged_rows(q, k, v, k_pages, v_pages, table, cu_rows, cache_pos, *, rope_theta,
+               rotary_dims=None, rope_pairs=False, rope_factor=None, rope_yarn=None, rope_size=0.0,
+               q_norm=None, k_norm=None, rms_eps=1e-6, positions=None, q_out=None, status=None,
+               stream=None):
+    """RMSNorm, rotary embedding and append of packed rows to pages (gattn_paged_rows).
+
+    q [T][H][d], k and v [T][Hk][d] (fp32 or bf16); q_norm, k_norm bf16 [d] or None;
+    cu_rows int32 [n + 1], cache_pos int32 [n], positions int32 [T] (default: where the
+    rows go).  rotary_dims defaults to d; rope_pairs turns neighbours.  rope_factor
+    divides the frequencies; or rope_yarn is a dict of factor, original, beta_fast (32)
+    and beta_slow (1).  Returns q_out, bf16 [T][H][d]."""
+    dev = q.get_device()
+    qa = _rows(q, "q", dev, _DTYPES)
+    T, H, d = q.shape
+    dtype = q.dtype
+    Hk = k.shape[1] if k.dim() == 3 else 0
+    ka = _rows(k, "k", dev, (dtype,), (T, Hk, d))
+    va = _rows(v, "v", dev, (dtype,), (T, Hk, d))
+    cu, n = _cu(cu_rows, "cu_rows", dev)
+    pool = _pool(k_pages, v_pages, table, dev, n)
+    if k_pages.shape[1] != Hk or k_pages.shape[3] != d:
+        _refuse(k_pages, "k_pages", dev, _BF16, ("pages", Hk, "page_size", d))
+    if q_out is None:
+        q_out = _output((T, H, d), q, stream)
+    oa = _rows(q_out, "q_out", dev, _BF16, (T, H, d))
+    scaling, factor, original, fast, slow = gattn.ROPE_PLAIN, 1.0, 0, 0.0, 0.0
+    if rope_yarn is not None:
+        if rope_factor is not None:
+            raise ValueError("rope_factor is part of rope_yarn")
+        extra = rope_yarn.keys() - {"factor", "original", "beta_fast", "beta_slow"}
+        if extra or not {"factor", "original"} <= rope_yarn.keys():
+            raise ValueError("rope_yarn takes factor, original, beta_fast and beta_slow")
+        scaling, factor, original = gattn.ROPE_YARN, rope_yarn["factor"], rope_yarn["original"]
+        fast, slow = rope_yarn.get("beta_fast", 32.0), rope_yarn.get("beta_slow", 1.0)
+    elif rope_factor is not None:
+        scaling, factor = gattn.ROPE_LINEAR, rope_factor
+    desc = gattn.gattn_paged_rows_desc.pack(
+        H, Hk, d, d if rotary_dims is None else rotary_dims, 1 if rope_pairs else 0, scaling,
+        rope_theta, factor, original, fast, slow, rope_size, rms_eps, _DTYPES[dtype], n, T, cu,
+        _flat(cache_pos, "cache_pos", dev, _I32, n), _flat(positions, "positions", dev, _I32, T),
+        qa[0], ka[0], va[0], qa[1], qa[2], ka[1], ka[2], va[1], va[2],
+        _flat(q_norm, "q_norm", dev, _BF16, d), _flat(k_norm, "k_norm", dev, _BF16, d), oa[0],
+        oa[1], oa[2], *pool, _flat(status, "status", dev, _I32, 1))
+    if n and T:
+        _call(gattn.paged_rows, desc, dev, stream)
+    return q_out
+
+
+def paged_attention_workspace(q, k_pages, cu_rows):
+    """Device memory for paged_attention calls of these shapes, one after the other."""
+    T, H, d = q.shape
+    size = gattn.paged_attention_workspace(H, k_pages.shape[1], d, cu_rows.shape[0] - 1, T)
+    return torch.empty(size, dtype=torch.uint8, device=q.device)
+
+
+def _attended(q, k_pages, v_pages, table, cu_rows, cache_pos, scale, lse):
+    """What attention and weights have in common: (device, descriptor's head, lse)."""
+    dev = q.get_device()
+    qa = _rows(q, "q", dev, _BF16)
+    T, H, d = q.shape
+    cu, n = _cu(cu_rows, "cu_rows", dev)
+    pool = _pool(k_pages, v_pages, table, dev, n)
+    Hk = k_pages.shape[1]
+    if k_pages.shape[3] != d:
+        _refuse(k_pages, "k_pages", dev, _BF16, ("pages", Hk, "page_size", d))
+    la = 0
+    if lse is not None:
+        if (not isinstance(lse, torch.Tensor) or lse.get_device() != dev or
+                lse.dtype is not torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
+            _refuse(lse, "lse", dev, _F32, f"[{T}][{H}], contiguous")
+        la = lse.data_ptr()
+    return dev, (H, Hk, d, d ** -0.5 if scale is None else scale, n, T, cu,
+                 _flat(cache_pos, "cache_pos", dev, _I32, n), *qa, *pool), la
+
+
+def paged_attention(q, k_pages, v_pages, table, cu_rows, cache_pos, *, gate=None, scale=None,
+                    out=None, lse=None, workspace=None, status=None, stream=None):
+    """Causal gated attention of one to a few new rows a sequence over pages that hold
+    them already (gattn_paged_attention).
+
+    q [T][H][d] bf16; cu_rows int32 [n + 1]; cache_pos int32 [n]: row i of sequence s sees
+    positions up to cache_pos[s] + i.  gate [T][H][d] fp32 or bf16 before its sigmoid, or
+    None; lse fp32 [T][H] takes the softmax's log sums; workspace as
+    paged_attention_workspace gives it (allocated for the call otherwise).  scale defaults
+    to d ** -0.5.  Returns out, bf16 [T][H][d]."""
+    dev, head, la = _attended(q, k_pages, v_pages, table, cu_rows, cache_pos, scale, lse)
+    H, Hk, d, _, n, T = head[:6]
+    if gate is not None:
+        ga, gdt = _rows(gate, "gate", dev, _DTYPES, q.shape), _DTYPES[gate.dtype]
+    else:
+        ga, gdt = (0, 8, 8), gattn.DTYPE_BF16
+    if out is None:
+        out = _output(q.shape, q, stream)
+    oa = _rows(out, "out", dev, _BF16, q.shape)
+    if workspace is None:
+        size = gattn.paged_attention_workspace(H, Hk, d, n, T)
+        workspace = _output((size // 2,), q, stream)
+    elif (workspace.get_device() != dev or workspace.dtype is not torch.uint8 or
+          not workspace.is_contiguous()):
+        _refuse(workspace, "workspace", dev, (torch.uint8,), "bytes, contiguous")
+    desc = gattn.gattn_paged_attention_desc.pack(
+        *head, ga[0], gdt, ga[1], ga[2], oa[0], oa[1], oa[2], la, workspace.data_ptr(),
+        workspace.nbytes, _flat(status, "status", dev, _I32, 1))
+    if n and T:
+        _call(gattn.paged_attention, desc, dev, stream)
+    return out
+
+
+def paged_weights(q, k_pages, table, cu_rows, cache_pos, lse, *, scale=None, weights=None,
+                  weights_out=None, status=None, stream=None):
+    """Adds the softmax weight that each position received from the rows of a
+    paged_attention call, per KV head (gattn_paged_weights).
+
+    Arguments as there, lse as it left it; weights and weights_out fp32 [n][Hk][positions].
+    weights None: zeros; weights_out None: into weights.  Returns weights_out."""
+    dev, head, la = _attended(q, k_pages, None, table, cu_rows, cache_pos, scale, lse)
+    n, T = head[4:6]
+    if weights_out is None:
+        weights_out = weights
+    wo, width, ws, wh = _received(weights_out, "weights_out", dev, n, head[1])
+    wi = 0
+    if weights is not None and weights is not weights_out:
+        wi, width_in, ws_in, wh_in = _received(weights, "weights", dev, n, head[1])
+        if (width_in, ws_in, wh_in) != (width, ws, wh):
+            _refuse(weights, "weights", dev, _F32, "must have weights_out's shape and strides:")
+    elif weights is not None:
+        wi = wo
+    desc = gattn.gattn_paged_weights_desc.pack(
+        *head, 0, 0, 8, 8, 0, 8, 8, la, 0, 0, _flat(status, "status", dev, _I32, 1), wi, wo, width,
+        ws, wh)
+    if n and T:
+        _call(gattn.paged_weights, desc, dev, stream)
+    return weights_out
+
+
+def paged_evict(k_pages, v_pages, table, lengths, weights, *, keep, recent=0, out_table=None,
+                weights_out=None, kept=None, lengths_out=None, status=None, stream=None):
+    """Shortens sequences to `keep` positions a KV head: the `recent` newest and the most
+    attended of the others (gattn_paged_evict).
+
+    lengths int32 [n]; weights fp32 [n][Hk][positions]; weights_out [n][Hk][>= keep] takes
+    those of the kept positions (may be weights).  out_table: pages that they move to,
+    others than the table's; None: in place.  Returns (kept int32 [n][Hk][keep],
+    lengths_out int32 [n])."""
+    dev = k_pages.get_device()
+    n = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else 0
+    pool = _pool(k_pages, v_pages, table, dev, n)
+    Hk, d = k_pages.shape[1], k_pages.shape[3]
+    w = _received(weights, "weights", dev, n, Hk)
+    wo = (0, 0, 0, 0) if weights_out is None else _received(weights_out, "weights_out", dev, n, Hk)
+    ot = (0, 0, 0) if out_table is None else _table(out_table, "out_table", dev, n)
+    if kept is None:
+        kept = _output((n, Hk, keep), k_pages, stream, torch.int32)
+    elif (kept.get_device() != dev or kept.dtype is not torch.int32 or kept.shape != (n, Hk, keep) or
+          not kept.is_contiguous()):
+        _refuse(kept, "kept", dev, _I32, (n, Hk, keep), "must be contiguous, of shape")
+    if lengths_out is None:
+        lengths_out = _output((n,), k_pages, stream, torch.int32)
+    desc = gattn.gattn_paged_evict_desc.pack(
+        Hk, d, n, keep, recent, *pool, *ot, _flat(lengths, "lengths", dev, _I32, n),
+        _flat(lengths_out, "lengths_out", dev, _I32, n), *w, *wo, kept.data_ptr(),
+        _flat(status, "status", dev, _I32, 1))
+    if n:
+        _call(gattn.paged_evict, desc, dev, stream)
+    return kept, lengths_out

@@ -37,8 +37,12 @@ EXPORTS = (
     "gattn_turbo4_codebook", "gattn_turbo4_quantize_device", "gattn_layer_set_mask",
     "gattn_kv_register_turbo4", "gattn_layer_step_kernels", "gattn_layer_set_test_wait",
     "gattn_layer_step_host", "gattn_prompt_rows", "gattn_prompt_attention", "gattn_delta_prompt",
-    "gattn_delta_step",
+    "gattn_delta_step", "gattn_paged_rows", "gattn_paged_attention",
+    "gattn_paged_attention_workspace", "gattn_paged_weights", "gattn_paged_evict",
 )
+
+# stretched rotary frequencies (gattn_paged_rows)
+ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = 0, 1, 2
 
 # bits of the packed-sequence operators' status word
 STATUS_RANGE, STATUS_TIMEOUT = 1, 2
@@ -174,6 +178,77 @@ class gattn_delta_desc(C.Structure):
         ptr: status""")
 
 
+# gattn_pages within a descriptor is spelled out (same places); the pools' strides are kp_*
+# and vp_* here
+_PAGES = """
+        ptr: k_pages v_pages
+        i32: num_pages page_size
+        i64: kp_stride_token kp_stride_head kp_stride_page vp_stride_token vp_stride_head vp_stride_page
+        ptr: table
+        i32: table_width
+        i64: table_stride"""
+
+
+@_packer
+class gattn_paged_rows_desc(C.Structure):
+    _fields_ = _fields("""
+        i32: num_heads num_kv_heads head_dim rotary_dims rope_pairs rope_scaling
+        f32: rope_theta rope_factor
+        i32: rope_original
+        f32: rope_beta_fast rope_beta_slow rope_size rms_eps
+        i32: x_dtype num_seqs total_rows
+        ptr: cu_rows cache_pos positions q k v
+        i64: q_stride_token q_stride_head k_stride_token k_stride_head v_stride_token v_stride_head
+        ptr: q_norm k_norm q_out
+        i64: o_stride_token o_stride_head""" + _PAGES + """
+        ptr: status""")
+
+
+_PAGED_ATTENTION = """
+        i32: num_heads num_kv_heads head_dim
+        f32: scale
+        i32: num_seqs total_rows
+        ptr: cu_rows cache_pos q
+        i64: q_stride_token q_stride_head""" + _PAGES + """
+        ptr: gate
+        i32: gate_dtype
+        i64: g_stride_token g_stride_head
+        ptr: out
+        i64: o_stride_token o_stride_head
+        ptr: lse workspace
+        i64: workspace_bytes
+        ptr: status"""
+
+
+@_packer
+class gattn_paged_attention_desc(C.Structure):
+    _fields_ = _fields(_PAGED_ATTENTION)
+
+
+@_packer
+class gattn_paged_weights_desc(C.Structure):
+    _fields_ = _fields(_PAGED_ATTENTION + """
+        ptr: weights weights_out
+        i32: weights_width
+        i64: w_stride_seq w_stride_head""")
+
+
+@_packer
+class gattn_paged_evict_desc(C.Structure):
+    _fields_ = _fields("""
+        i32: num_kv_heads head_dim num_seqs keep recent""" + _PAGES + """
+        ptr: out_table
+        i32: out_table_width
+        i64: out_table_stride
+        ptr: lengths lengths_out weights
+        i32: weights_width
+        i64: w_stride_seq w_stride_head
+        ptr: weights_out
+        i32: weights_out_width
+        i64: wo_stride_seq wo_stride_head
+        ptr: kept status""")
+
+
 _lib = None
 
 
@@ -223,6 +298,12 @@ def lib():
         L.gattn_prompt_attention.argtypes = [p, p]
         L.gattn_delta_prompt.argtypes = [p, p]
         L.gattn_delta_step.argtypes = [p, p]
+        L.gattn_paged_rows.argtypes = [p, p]
+        L.gattn_paged_attention.argtypes = [p, p]
+        L.gattn_paged_attention_workspace.argtypes = [i32, i32, i32, i32, i32]
+        L.gattn_paged_attention_workspace.restype = i64
+        L.gattn_paged_weights.argtypes = [p, p]
+        L.gattn_paged_evict.argtypes = [p, p]
         for name in ("gattn_cfg_validate", "gattn_layer_create", "gattn_layer_set_weights",
                      "gattn_kv_register", "gattn_layer_step", "gattn_layer_poll_status",
                      "gattn_layer_set_taps", "gattn_pack_affine_host", "gattn_unpack_codes_device",
@@ -232,7 +313,9 @@ def lib():
                      "gattn_turbo4_codebook", "gattn_turbo4_quantize_device",
                      "gattn_layer_set_mask", "gattn_kv_register_turbo4",
                      "gattn_layer_set_test_wait", "gattn_layer_step_host", "gattn_prompt_rows",
-                     "gattn_prompt_attention", "gattn_delta_prompt", "gattn_delta_step"):
+                     "gattn_prompt_attention", "gattn_delta_prompt", "gattn_delta_step",
+                     "gattn_paged_rows", "gattn_paged_attention", "gattn_paged_weights",
+                     "gattn_paged_evict"):
             getattr(L, name).restype = C.c_int
         _lib = L
     return _lib
@@ -445,6 +528,38 @@ def delta_step(desc, stream: int = 0) -> None:
     """The gated delta rule for a few new rows of many sequences, row by row
     (gattn_delta_desc)."""
     _check(lib().gattn_delta_step(_desc(desc), stream))
+
+
+# ------------------------------------------------------------ paged caches
+
+def paged_rows(desc, stream: int = 0) -> None:
+    """RMSNorm, rotary embedding and append of new rows to pages (gattn_paged_rows_desc)."""
+    _check(lib().gattn_paged_rows(_desc(desc), stream))
+
+
+def paged_attention(desc, stream: int = 0) -> None:
+    """Causal gated attention of new rows over pages (gattn_paged_attention_desc)."""
+    _check(lib().gattn_paged_attention(_desc(desc), stream))
+
+
+def paged_attention_workspace(num_heads: int, num_kv_heads: int, head_dim: int, num_seqs: int,
+                              total_rows: int) -> int:
+    """Bytes of device memory that such a call works in."""
+    n = int(lib().gattn_paged_attention_workspace(num_heads, num_kv_heads, head_dim, num_seqs,
+                                                  total_rows))
+    if n < 0:
+        raise GattnError(1, lib().gattn_last_error().decode())
+    return n
+
+
+def paged_weights(desc, stream: int = 0) -> None:
+    """The softmax weight that positions received (gattn_paged_weights_desc)."""
+    _check(lib().gattn_paged_weights(_desc(desc), stream))
+
+
+def paged_evict(desc, stream: int = 0) -> None:
+    """Shortens sequences to their most attended positions (gattn_paged_evict_desc)."""
+    _check(lib().gattn_paged_evict(_desc(desc), stream))
 
 
 # ------------------------------------------------------------ host helpers
