@@ -27,18 +27,16 @@ namespace {
 
 template <int D, int MT>
 struct Cfg {
-    static constexpr int M = 16 * MT, NS = MT == 4 ? 2 : 4, CW = NS * MT, THREADS = (CW + 1) * 32;
+    static constexpr int M = 16 * MT, NS = MT == 4 ? 2 : 4, CW = NS * MT, NP = D * MT == 1024 || (D == 64 && MT == 4) ? 2 : 4, THREADS = (CW + NP) * 32;
     static constexpr int ROUNDS = CW * D >= 1024 ? CW * D / (MT == 1 ? 1024 : 512) : 1, DR = D / ROUNDS;   // columns joined at once
     static constexpr int XROW = DR + 8;                // floats of a joined row: rows 8 banks apart
     static constexpr int XB = CW * 16 * XROW * 4;
     static constexpr int U = kUnit<D>, UNIT = U * D * 4;
     static constexpr int FIXED = 2 * M * D * 2 + XB + 2048 + 1024;
     static constexpr int FIT = (227 * 1024 - FIXED) / UNIT;
-    // a slot always serves the same group of warps: a wait then cannot take the phase
-    // before last for the one it is about (copies land in any order)
-    static constexpr int SLOTS = (FIT > 12 ? 12 : FIT) / NS * NS;
+    static constexpr int SLOTS = (FIT > 12 ? 12 : FIT) / (NS > NP ? NS : NP) * (NS > NP ? NS : NP);
     static constexpr int SMEM = SLOTS * UNIT + 2 * M * D * 2 + XB + 1024;
-    using R = Ring<D, M, true, SLOTS, MT, CW>;
+    using R = Ring<D, M, true, SLOTS, NP, MT, CW>;
     static_assert(SMEM + 2048 <= 227 * 1024 && SLOTS >= 4 && DR % 8 == 0 && DR * ROUNDS == D && XROW % 32 == 8, "");
 };
 
@@ -51,25 +49,28 @@ struct Rec {
     int live, slot, last, r0, rowf, hf, nrows, hk;
 };
 
+// Four columns of a row's gate before its sigmoid.
+__device__ __forceinline__ float4 gate4(const PagedAttnArgs &a, long long row, int head, int col)
+{
+    if (!a.gate)
+        return make_float4(0.f, 0.f, 0.f, 0.f);
+    const long long at = row * a.gs.tok + head * a.gs.head + col;
+    if (a.gate_f32)
+        return *reinterpret_cast<const float4 *>(static_cast<const float *>(a.gate) + at);
+    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.gate) + at);
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+
 // Four finished columns of a row: divided, gated, rounded once.
-__device__ __forceinline__ void finish4(const PagedAttnArgs &a, long long row, int head, int col, float4 o, float l)
+__device__ __forceinline__ void finish4(const PagedAttnArgs &a, long long row, int head, int col, float4 o, float l,
+                                        const float4 &g)
 {
     const float inv = l == 0.f ? 0.f : 1.f / l;        // no position seen: zeros
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    if (a.gate) {
-        const long long at = row * a.gs.tok + head * a.gs.head + col;
-        float4 g;
-        if (a.gate_f32) {
-            g = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.gate) + at);
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.gate) + at);
-            g = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-        }
-        // a row that saw nothing stays zero whatever its gate holds
-        if (l != 0.f) {
-            o.x /= 1.f + __expf(-g.x), o.y /= 1.f + __expf(-g.y);
-            o.z /= 1.f + __expf(-g.z), o.w /= 1.f + __expf(-g.w);
-        }
+    // a row that saw nothing stays zero whatever its gate holds
+    if (a.gate && l != 0.f) {
+        o.x /= 1.f + __expf(-g.x), o.y /= 1.f + __expf(-g.y);
+        o.z /= 1.f + __expf(-g.z), o.w /= 1.f + __expf(-g.w);
     }
     *reinterpret_cast<uint2 *>(a.out + row * a.os.tok + head * a.os.head + col) =
         make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
@@ -119,12 +120,12 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, 1)
             recs[blockIdx.x].live = 0;
         return;
     }
-    if (warp == CW) {
+    if (warp >= CW) {
         Rec rec{};
-        produce(a, ring, units, qbuf, &kmap, &vmap, run, group, [&](const Part &p, int last) {
+        produce(a, ring, units, qbuf, &kmap, &vmap, run, group, warp - CW, [&](const Part &p, int last) {
             rec = {1, p.slot, last, p.r0, p.rowf, p.hf, p.nrows, p.hk};
         });
-        if (lane == 0)
+        if (warp == CW && lane == 0)
             recs[blockIdx.x] = rec;
         return;
     }
@@ -396,10 +397,11 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, 1)
                         xb + ((q * MT + row / 16) * 16 + row % 16) * C::XROW + c);
                     o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
                 }
-                if (p.whole)
-                    finish4(a, p.r0 + p.rowf + (p.hf + row) / group, p.hk * group + (p.hf + row) % group, r * DR + c, o,
-                            row_l[row]);
-                else
+                if (p.whole) {
+                    const long long to = p.r0 + p.rowf + (p.hf + row) / group;
+                    const int head = p.hk * group + (p.hf + row) % group;
+                    finish4(a, to, head, r * DR + c, o, row_l[row], gate4(a, to, head, r * DR + c));
+                } else
                     *reinterpret_cast<float4 *>(slot + row * D + r * DR + c) = o;
             }
             if (r + 1 < C::ROUNDS)
@@ -410,14 +412,17 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, 1)
 }
 
 // Joins the parts of the segment that begins in CTA blockIdx.x's run and goes on behind
-// it: M / 16 rows a block, the parts dealt to the warps of a row.
-constexpr int kJoin = 256;
+// it: M / 16 rows a block, the parts dealt to the warps of a row, kFly of them on their
+// way at a time.  Bound by three dependent loads (the record, the parts, and what the
+// launch itself takes).
+constexpr int kJoin = 256, kFly = 5;
 
 template <int D, int M>
 __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant__ PagedAttnArgs a)
 {
-    constexpr int ROWS = M / 16, W = kJoin / 32 / ROWS, N4 = D / 128 > 0 ? (D + 127) / 128 : 1;
-    __shared__ float fac[ROWS][kMaxCtas];
+    constexpr int ROWS = M / 16, W = kJoin / 32 / ROWS, N4 = (D + 127) / 128;
+    static_assert(W * 32 >= D / 4, "a thread finishes four columns");
+    __shared__ float red_m[kJoin / 32], red_l[kJoin / 32];
     __shared__ float4 sums[kJoin / 32][D / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rl = warp / W, w = warp % W;
     const float *const ws = static_cast<const float *>(a.ws);
@@ -427,62 +432,84 @@ __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant
     if (!rec.live || blockIdx.y * ROWS >= rec.nrows)
         return;
     const int first = blockIdx.x, parts = rec.last - first + 1;
-    auto part = [&](int k) { return ws + (2ll * (first + k) + (k ? 0 : rec.slot)) * kPartial<D, M>; };
-    // every warp of a row finds the reference; one leaves the factors
-    float top = -INFINITY, sum = 0.f, mk[kMaxCtas / 32];
-#pragma unroll
-    for (int q = 0; q < kMaxCtas / 32; ++q) {
-        mk[q] = q * 32 + lane < parts ? part(q * 32 + lane)[M * D + i] : -INFINITY;
-        top = fmaxf(top, mk[q]);
-    }
-    for (int o = 16; o; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll
-    for (int q = 0; q < kMaxCtas / 32; ++q)
-        if (q * 32 + lane < parts) {
-            const float f = mk[q] == top ? 1.f : exp2f(mk[q] - top);
-            sum += f * part(q * 32 + lane)[M * D + M + i];
-            if (w == 0)
-                fac[rl][q * 32 + lane] = f;
-        }
-    for (int o = 16; o; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncthreads();
+    const int group = a.H / a.Hk, h = rec.hf + i, head = rec.hk * group + h % group;
+    const long long row = rec.r0 + rec.rowf + h / group;
+    const int col = (w * 32 + lane) * 4;               // of the thread at the end
+    const bool mine = i < rec.nrows && col < D;
+    const float4 gate = mine ? gate4(a, row, head, col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = -INFINITY, sum = 0.f;
     float4 o[N4];
 #pragma unroll
     for (int c = 0; c < N4; ++c)
         o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = w; k < parts; k += W) {
-        const float f = fac[rl][k];
-        const float *src = part(k) + i * D;
+    for (int k0 = w; k0 < parts; k0 += W * kFly) {
+        float m[kFly], l[kFly];
+        float4 v[kFly][N4];
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const int k = k0 + f * W;
+            m[f] = -INFINITY;
+            l[f] = 0.f;
+            const float *const from = ws + (2ll * (first + k) + (k ? 0 : rec.slot)) * kPartial<D, M>;
+            if (k < parts) {
+                m[f] = from[M * D + i];
+                l[f] = from[M * D + M + i];
+            }
+#pragma unroll
+            for (int c = 0; c < N4; ++c) {
+                v[f][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < parts && c * 128 + lane * 4 < D)
+                    v[f][c] = *reinterpret_cast<const float4 *>(from + i * D + c * 128 + lane * 4);
+            }
+        }
+        float to = top;
+#pragma unroll
+        for (int f = 0; f < kFly; ++f)
+            to = fmaxf(to, m[f]);
+        const float keep = to == top ? 1.f : exp2f(top - to);
+        top = to;
+        sum *= keep;
 #pragma unroll
         for (int c = 0; c < N4; ++c)
-            if (c * 128 + lane * 4 < D) {
-                const float4 v = *reinterpret_cast<const float4 *>(src + c * 128 + lane * 4);
-                o[c].x = fmaf(f, v.x, o[c].x), o[c].y = fmaf(f, v.y, o[c].y);
-                o[c].z = fmaf(f, v.z, o[c].z), o[c].w = fmaf(f, v.w, o[c].w);
+            o[c].x *= keep, o[c].y *= keep, o[c].z *= keep, o[c].w *= keep;
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const float x = m[f] == to ? 1.f : exp2f(m[f] - to);
+            sum = fmaf(x, l[f], sum);
+#pragma unroll
+            for (int c = 0; c < N4; ++c) {
+                o[c].x = fmaf(x, v[f][c].x, o[c].x), o[c].y = fmaf(x, v[f][c].y, o[c].y);
+                o[c].z = fmaf(x, v[f][c].z, o[c].z), o[c].w = fmaf(x, v[f][c].w, o[c].w);
             }
+        }
     }
 #pragma unroll
     for (int c = 0; c < N4; ++c)
         if (c * 128 + lane * 4 < D)
             sums[warp][c * 32 + lane] = o[c];
-    __syncthreads();
-    if (i >= rec.nrows)
-        return;
-    const int group = a.H / a.Hk, h = rec.hf + i, head = rec.hk * group + h % group;
-    const long long row = rec.r0 + rec.rowf + h / group;
-    if (w == 0 && lane == 0 && a.lse)
-        a.lse[row * a.H + head] = lse_of(top, sum);
-    for (int c = w * 32 + lane; c < D / 4; c += W * 32) {
-        float4 v = sums[rl * W][c];
-        for (int q = 1; q < W; ++q) {
-            const float4 x = sums[rl * W + q][c];
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        }
-        finish4(a, row, head, c * 4, v, sum);
+    if (lane == 0) {
+        red_m[warp] = top;
+        red_l[warp] = sum;
     }
+    __syncthreads();
+    if (!mine)
+        return;
+    top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < W; ++q)
+        top = fmaxf(top, red_m[rl * W + q]);
+    sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < W; ++q) {
+        const float mq = red_m[rl * W + q], x = mq == top ? 1.f : exp2f(mq - top);
+        sum = fmaf(x, red_l[rl * W + q], sum);
+        const float4 p = sums[rl * W + q][col / 4];
+        v.x = fmaf(x, p.x, v.x), v.y = fmaf(x, p.y, v.y), v.z = fmaf(x, p.z, v.z), v.w = fmaf(x, p.w, v.w);
+    }
+    if (col == 0 && a.lse)
+        a.lse[row * a.H + head] = lse_of(top, sum);
+    finish4(a, row, head, col, v, sum, gate);
 }
 
 using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;

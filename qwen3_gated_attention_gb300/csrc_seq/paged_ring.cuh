@@ -3,9 +3,16 @@
 // The work of a call is a line of units: U consecutive positions of one sequence and KV
 // head, met by a tile of up to M query rows (a segment: all units of one sequence, head
 // and tile).  Every CTA takes an equal run of the line, wherever it begins or ends, so
-// that the lengths of the sequences do not matter.  One warp of a CTA (the producer)
-// walks the run: it looks up pages, copies units into a ring of shared memory by TMA and
-// the segments' query rows and descriptions into two buffers; the other warps consume.
+// that the lengths of the sequences do not matter.  NP warps of a CTA (producers) walk the
+// run: they look up pages and copy units by turns into a ring of shared memory by TMA, the
+// first one the segments' query rows and descriptions into two buffers too; the other
+// warps consume.  (One producer takes 700 cycles a unit and 90 more for every box beyond
+// two: as much as 16 KB take to arrive at an SM, twice that with boxes of 16 positions.)
+//
+// Every slot of the ring belongs to one producer and one group of consumers: SLOTS is
+// divided by the number of either.  A wait is for a phase's parity, so that it must never
+// be two phases ahead; copies land in any order, and only the slot's own users are known
+// to have seen its last phase.
 #pragma once
 
 #include "paged.cuh"
@@ -184,9 +191,10 @@ __device__ __forceinline__ void cp_arrive(uint64_t *bar)
 }
 
 // The ring and the two row buffers of a CTA.
-template <int D, int M_, bool V_, int SLOTS_, int READERS, int CONSUMERS>
+template <int D, int M_, bool V_, int SLOTS_, int NP_, int READERS, int CONSUMERS>
 struct Ring {
-    static constexpr int U = kUnit<D>, DB = D / 64, M = M_, SLOTS = SLOTS_;
+    static constexpr int U = kUnit<D>, DB = D / 64, M = M_, SLOTS = SLOTS_, NP = NP_;
+    static_assert(SLOTS > 0 && SLOTS % NP == 0 && SLOTS % (CONSUMERS / READERS) == 0, "");
     static constexpr bool V = V_;                      // values too
     static constexpr int PLANE = U * D * 2, UNIT = V ? 2 * PLANE : PLANE;
     static constexpr int QB = M * D * 2;               // query rows, 16-byte pieces swizzled by row
@@ -222,13 +230,44 @@ __host__ __device__ inline int box_log2(int page, int U)
     return l;
 }
 
-// The producer warp.  `units`: the ring's memory (1024-byte aligned), `qbuf` that of the
+// The query rows and the description of a part, by one warp.
+template <class R>
+__device__ __forceinline__ void put_rows(const PagedAttnArgs &a, R &ring, uint8_t *qbuf, const Part &p, int b, int group)
+{
+    constexpr int D = R::DB * 64, M = R::M;
+    const int lane = threadIdx.x & 31;
+    const uint32_t qdst = smem_u32(qbuf) + b * R::QB;
+    constexpr int CH = D / 8, RPI = 32 / CH > 0 ? 32 / CH : 1;          // rows of an iteration
+    for (int i = 0; i < M; i += RPI) {
+        const int row = i + (RPI > 1 ? lane / CH : 0);
+        const bool on = row < p.nrows;
+        const int h = p.hf + (on ? row : 0);
+        const __nv_bfloat16 *src =
+            a.q + (p.r0 + p.rowf + h / group) * a.qs.tok + (p.hk * group + h % group) * a.qs.head;
+        for (int c = RPI > 1 ? lane % CH : lane; c < CH; c += 32)
+            cp16(qdst + row * (D * 2) + ((c ^ (row & 7)) << 4), src + c * 8, on);
+    }
+    if constexpr (!R::V)
+        for (int i = lane; i < M; i += 32) {
+            float v = -INFINITY;
+            if (i < p.nrows)
+                v = a.lse[(long long)(p.r0 + p.rowf + (p.hf + i) / group) * a.H + p.hk * group + (p.hf + i) % group];
+            // 2^(score - v): a row that saw nothing gives nothing
+            ring.lse[b][i] = v == -INFINITY ? INFINITY : v * 1.44269504f;
+        }
+    if (lane == 0)
+        ring.part[b] = p;
+    cp_arrive(&ring.qfull[b]);
+    mbar_arrive(&ring.qfull[b]);
+}
+
+// Producer warp `pw` of R::NP.  `units`: the ring's memory (1024-byte aligned), `qbuf` that of the
 // row buffers.  `seen` is told of the last segment, if it begins in this run and goes on
 // behind it: (part, CTA of its last unit).
 template <class R, class F>
 __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t *units, uint8_t *qbuf,
                                         const CUtensorMap *kmap, const CUtensorMap *vmap, const Run &run, int group,
-                                        F seen)
+                                        int pw, F seen)
 {
     constexpr int U = R::U, D = R::U > 0 ? R::DB * 64 : 0, M = R::M;
     const int lane = threadIdx.x & 31;
@@ -278,36 +317,18 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
             p.whole = whole;
             p.slot = x == run.x0 ? 0 : 1;
             p.pass = (int)min(pass, 1ll);
-            if (!ring_wait(&ring.qempty[b], (uint32_t)((parts >> 1) & 1) ^ 1u, &ring.abort, a.sq))
-                stop = true;
-            stop = __any_sync(0xffffffffu, stop);
-            if (stop)
-                break;
-            const uint32_t qdst = smem_u32(qbuf) + b * R::QB;
-            constexpr int CH = D / 8, RPI = 32 / CH > 0 ? 32 / CH : 1;          // rows of an iteration
-            for (int i = 0; i < M; i += RPI) {
-                const int row = i + (RPI > 1 ? lane / CH : 0);
-                const bool on = row < p.nrows;
-                const int h = p.hf + (on ? row : 0);
-                const __nv_bfloat16 *src =
-                    a.q + (p.r0 + p.rowf + h / group) * a.qs.tok + (hk * group + h % group) * a.qs.head;
-                for (int c = RPI > 1 ? lane % CH : lane; c < CH; c += 32)
-                    cp16(qdst + row * (D * 2) + ((c ^ (row & 7)) << 4), src + c * 8, on);
+            if (pw == 0) {
+                if (!ring_wait(&ring.qempty[b], (uint32_t)((parts >> 1) & 1) ^ 1u, &ring.abort, a.sq))
+                    stop = true;
+                stop = __any_sync(0xffffffffu, stop);
+                if (stop)
+                    break;
+                put_rows(a, ring, qbuf, p, b, group);
             }
-            if constexpr (!R::V)
-                for (int i = lane; i < M; i += 32) {
-                    float v = -INFINITY;
-                    if (i < p.nrows)
-                        v = a.lse[(long long)(p.r0 + p.rowf + (p.hf + i) / group) * a.H + hk * group + (p.hf + i) % group];
-                    // 2^(score - v): a row that saw nothing gives nothing
-                    ring.lse[b][i] = v == -INFINITY ? INFINITY : v * 1.44269504f;
-                }
-            if (lane == 0)
-                ring.part[b] = p;
-            cp_arrive(&ring.qfull[b]);
-            mbar_arrive(&ring.qfull[b]);
             // ---- the units
             for (int n = p.u0; n < p.u1; ++n, ++it) {
+                if (it % R::NP != pw)
+                    continue;
                 const int b0 = n * NB;
                 if (tab_s != s || b0 < tab_b || b0 >= tab_b + 32) {
                     tab_s = s;
@@ -351,14 +372,14 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
                         box_g2s(dst + R::PLANE, vmap, y, hk, page < 0 ? a.pg.pages : page, bar, pol);
                 }
             }
-            if (lane == 0 && u0 == 0 && u1 < u.units)
+            if (pw == 0 && lane == 0 && u0 == 0 && u1 < u.units)
                 seen(p, (int)((x + u.units - 1) / run.quota));
         }
         x += u1 - u0;
         u0 = 0;
         ++seg;
     }
-    if (!stop) {
+    if (!stop && pw == 0) {
         const int b = parts & 1;
         stop = !ring_wait(&ring.qempty[b], (uint32_t)((parts >> 1) & 1) ^ 1u, &ring.abort, a.sq);
         stop = __any_sync(0xffffffffu, stop);
@@ -373,6 +394,8 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
     cp_async_wait_all();
     if (lane == 0)
         for (long long i = it > R::SLOTS ? it - R::SLOTS : 0; i < it; ++i) {
+            if (i % R::NP != pw)
+                continue;
             const unsigned long long t0 = global_ns();
             while (!mbar_try(&ring.full[i % R::SLOTS], (uint32_t)((i / R::SLOTS) & 1)) &&
                    global_ns() - t0 < kWaitLimitNs) {

@@ -18,14 +18,12 @@ namespace {
 
 template <int D>
 struct Cfg {
-    static constexpr int M = 64, CW = 8, THREADS = (CW + 1) * 32;
+    static constexpr int M = 64, CW = 8, NP = 4, THREADS = (CW + NP) * 32;
     static constexpr int U = kUnit<D>, UNIT = U * D * 2;
     static constexpr int FIT = (227 * 1024 - 2 * M * D * 2 - 4096) / UNIT;
-    // a slot always serves the same warp: a wait then cannot take the phase before last
-    // for the one it is about (copies land in any order)
     static constexpr int SLOTS = (FIT > 24 ? 24 : FIT) / CW * CW;
     static constexpr int SMEM = SLOTS * UNIT + 2 * M * D * 2 + 1024;
-    using R = Ring<D, M, false, SLOTS, 1, CW>;
+    using R = Ring<D, M, false, SLOTS, NP, 1, CW>;
     static_assert(SMEM + sizeof(R) + 512 <= 227 * 1024 && SLOTS > 0, "");
 };
 
@@ -50,8 +48,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                                                [&](int, const SeqUnits &) { seq_flag(a.sq, GATTN_STATUS_RANGE); });
     if (run.x0 >= run.x1)
         return;
-    if (warp == CW) {
-        produce(a, ring, units, qbuf, &kmap, &kmap, run, group, [](const Part &, int) {});
+    if (warp >= CW) {
+        produce(a, ring, units, qbuf, &kmap, &kmap, run, group, warp - CW, [](const Part &, int) {});
         return;
     }
     const int g = lane >> 2, cq = lane & 3;
