@@ -9,12 +9,18 @@
 // and a second kernel joins them.
 //
 // Within a CTA the units of a part go round NS groups of warps, each with its own
-// running maximum and sum, so that no warp waits for another until the part ends; a warp
-// of a group has 16 of the tile's rows.  The scores stay in registers: as the matrix
-// instruction leaves them they are what the product with the values takes.  p goes into
-// that product as two bf16 numbers, 16 bits of it: 8 bits alone would be an error of
-// the size of the output's own rounding, and the matrix units have the time.
-// The reference m of a row moves only when the maximum outgrows it by 2^8.
+// running maximum and sum; a warp of a group has eight of the tile's rows.  Warps wait for
+// units only, never for each other: at a part's end each leaves (m, sum, O) in shared
+// memory for two warps that join, divide, gate and write them, and goes on with the next.
+//
+// The matrix instructions run with the cache as their first operand (16 positions, or
+// 16 elements of the values) and the rows as their second, eight wide: one token's
+// heads of a group are mostly eight or fewer, and the other way round they would fill a
+// quarter of 16 rows and hold twice the registers (189 against 104 us for ... ).  The
+// scores stay in registers; turned over, eight by eight, they are what the product with
+// the values takes.  p goes into that product as two bf16 numbers, 16 bits of it: 8 bits
+// alone would be an error of the size of the output's own rounding, and the matrix units
+// have the time.  The reference m of a row moves only when the maximum outgrows it by 2^8.
 #include <cudaTypedefs.h>
 
 #include "paged_ring.cuh"
@@ -25,19 +31,24 @@ using namespace paged;
 
 namespace {
 
-template <int D, int MT>
+// RT: tiles of eight rows.
+template <int D, int RT>
 struct Cfg {
-    static constexpr int M = 16 * MT, NS = MT == 4 ? 2 : 4, CW = NS * MT, NP = D * MT == 1024 || (D == 64 && MT == 4) ? 2 : 4, THREADS = (CW + NP) * 32;
-    static constexpr int ROUNDS = CW * D >= 1024 ? CW * D / (MT == 1 ? 1024 : 512) : 1, DR = D / ROUNDS;   // columns joined at once
-    static constexpr int XROW = DR + 8;                // floats of a joined row: rows 8 banks apart
-    static constexpr int XB = CW * 16 * XROW * 4;
+    static constexpr int M = 8 * RT, CW = 8, NS = CW / RT, NE = 2, NP = 2;
+    static constexpr int THREADS = (CW + NE + NP) * 32;
+    // columns that are handed over at once: what leaves the ring enough slots
+    static constexpr int DR = RT <= 2 || D == 64 ? D : RT == 4 ? D / 2 : 64, ROUNDS = D / DR;
+    static constexpr int XROW = DR + 4;                // floats of a row: two rows 8 banks apart
+    static constexpr int XB = CW * 8 * XROW * 4;
+    static constexpr int ITEMS = M / NE * (DR / 4) / 32;   // of a joining lane, four columns each
     static constexpr int U = kUnit<D>, UNIT = U * D * 4;
-    static constexpr int FIXED = 2 * M * D * 2 + XB + 2048 + 1024;
-    static constexpr int FIT = (227 * 1024 - FIXED) / UNIT;
-    static constexpr int SLOTS = (FIT > 12 ? 12 : FIT) / (NS > NP ? NS : NP) * (NS > NP ? NS : NP);
+    static constexpr int FIXED = 2 * M * D * 2 + XB + 4096 + 1024;
+    static constexpr int FIT = (227 * 1024 - FIXED) / UNIT, STEP = NS > NP ? NS : NP;
+    static constexpr int SLOTS = (FIT > 12 ? 12 : FIT) / STEP * STEP;
     static constexpr int SMEM = SLOTS * UNIT + 2 * M * D * 2 + XB + 1024;
-    using R = Ring<D, M, true, SLOTS, NP, MT, CW>;
-    static_assert(SMEM + 2048 <= 227 * 1024 && SLOTS >= 4 && DR % 8 == 0 && DR * ROUNDS == D && XROW % 32 == 8, "");
+    using R = Ring<D, M, true, SLOTS, NP, NS, RT, CW + NE>;
+    static_assert(SMEM + 4096 <= 227 * 1024 && SLOTS >= 4 && DR * ROUNDS == D && XROW % 16 == 4 &&
+                      ITEMS * 32 * NE == M * (DR / 4), "");
 };
 
 // Floats of a partial result: rows, then their m and sums.
@@ -49,31 +60,29 @@ struct Rec {
     int live, slot, last, r0, rowf, hf, nrows, hk;
 };
 
-// Four columns of a row's gate before its sigmoid.
-__device__ __forceinline__ float4 gate4(const PagedAttnArgs &a, long long row, int head, int col)
+// Four columns of a row's gate before its sigmoid, as they are in memory.
+__device__ __forceinline__ uint4 gate4(const PagedAttnArgs &a, long long at)
 {
-    if (!a.gate)
-        return make_float4(0.f, 0.f, 0.f, 0.f);
-    const long long at = row * a.gs.tok + head * a.gs.head + col;
     if (a.gate_f32)
-        return *reinterpret_cast<const float4 *>(static_cast<const float *>(a.gate) + at);
+        return *reinterpret_cast<const uint4 *>(static_cast<const float *>(a.gate) + at);
     const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.gate) + at);
-    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+    return make_uint4(w.x, w.y, 0, 0);
 }
 
 // Four finished columns of a row: divided, gated, rounded once.
-__device__ __forceinline__ void finish4(const PagedAttnArgs &a, long long row, int head, int col, float4 o, float l,
-                                        const float4 &g)
+__device__ __forceinline__ void finish4(const PagedAttnArgs &a, long long to, float4 o, float l, const uint4 &raw)
 {
     const float inv = l == 0.f ? 0.f : 1.f / l;        // no position seen: zeros
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
     // a row that saw nothing stays zero whatever its gate holds
     if (a.gate && l != 0.f) {
+        const float4 g = a.gate_f32 ? make_float4(__uint_as_float(raw.x), __uint_as_float(raw.y), __uint_as_float(raw.z),
+                                                  __uint_as_float(raw.w))
+                                    : make_float4(bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y));
         o.x /= 1.f + __expf(-g.x), o.y /= 1.f + __expf(-g.y);
         o.z /= 1.f + __expf(-g.z), o.w /= 1.f + __expf(-g.w);
     }
-    *reinterpret_cast<uint2 *>(a.out + row * a.os.tok + head * a.os.head + col) =
-        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    *reinterpret_cast<uint2 *>(a.out + to) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 }
 
 __device__ __forceinline__ float lse_of(float m, float l)
@@ -81,23 +90,28 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(Cfg<D, MT>::THREADS, 1)
+template <int D, int RT>
+__global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, int min_units)
 {
-    using C = Cfg<D, MT>;
+    using C = Cfg<D, RT>;
     using R = typename C::R;
-    constexpr int M = C::M, NS = C::NS, CW = C::CW, U = C::U, DR = C::DR;
+    constexpr int M = C::M, NS = C::NS, CW = C::CW, NE = C::NE, U = C::U, DR = C::DR;
     extern __shared__ uint8_t raw[];
     __shared__ R ring;
-    __shared__ float red_m[CW * 16], red_l[CW * 16], row_m[M], row_l[M];
+    __shared__ float red_m[CW * 8], red_l[CW * 8];   // of the consumers' rows
+    __shared__ float fac[NS][M], row_l[M];             // the joining warps' own
+    __shared__ long long row_out[M], row_gate[M];      // where their rows are
+    __shared__ uint64_t xfull, xempty;                 // the hand-over buffer
     uint8_t *units = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *qbuf = units + C::SLOTS * C::UNIT;
     float *const xb = reinterpret_cast<float *>(qbuf + 2 * M * D * 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = a.H / a.Hk;
     if (threadIdx.x == 0) {
+        mbar_init(&xfull, CW);
+        mbar_init(&xempty, NE);
         ring.init();
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -120,140 +134,237 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, 1)
             recs[blockIdx.x].live = 0;
         return;
     }
-    if (warp >= CW) {
+    if (warp >= CW + NE) {
         Rec rec{};
-        produce(a, ring, units, qbuf, &kmap, &vmap, run, group, warp - CW, [&](const Part &p, int last) {
+        produce(a, ring, units, qbuf, &kmap, &vmap, run, group, warp - CW - NE, [&](const Part &p, int last) {
             rec = {1, p.slot, last, p.r0, p.rowf, p.hf, p.nrows, p.hk};
         });
-        if (warp == CW && lane == 0)
+        if (warp == CW + NE && lane == 0)
             recs[blockIdx.x] = rec;
         return;
     }
+    if (warp >= CW) {
+        // ------------------------------------------------------- the joining warps
+        const int e0 = (warp - CW) * (M / NE);          // first of its rows
+        uint32_t xr = 0;                                // hand-overs so far
+        for (int parts = 0;; ++parts) {
+            const int b = parts & 1;
+            if (!ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq))
+                return;
+            const Part p = ring.part[b];
+            if (!p.live)
+                break;
+            float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
+            const int mine = e0 + lane;                 // a lane a row
+            const int h = p.hf + mine, head = p.hk * group + h % group;
+            const long long to = p.r0 + p.rowf + h / group;
+            if (lane < M / NE) {
+                row_out[mine] = to * a.os.tok + head * a.os.head;
+                row_gate[mine] = to * a.gs.tok + head * a.gs.head;
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int r = 0; r < C::ROUNDS; ++r, ++xr) {
+                // the gates come while the consumers work
+                uint4 gate[C::ITEMS];
+#pragma unroll
+                for (int q = 0; q < C::ITEMS; ++q) {
+                    const int i = q * 32 + lane, row = e0 + i / (DR / 4);
+                    gate[q] = make_uint4(0, 0, 0, 0);
+                    if (p.whole && a.gate && row < p.nrows)
+                        gate[q] = gate4(a, row_gate[row] + r * DR + i % (DR / 4) * 4);
+                }
+                if (!ring_wait(&xfull, xr & 1, &ring.abort, a.sq))
+                    return;
+                if (r == 0) {
+                    if (lane < M / NE) {
+                        const float *const rm = red_m + mine, *const rl = red_l + mine;   // M apart by group
+                        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                        for (int q = 0; q < NS; ++q)
+                            top = fmaxf(top, rm[q * M]);
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) {
+                            const float f = rm[q * M] == top ? 1.f : exp2f(rm[q * M] - top);
+                            sum = fmaf(f, rl[q * M], sum);
+                            fac[q][mine] = f;
+                        }
+                        row_l[mine] = sum;
+                        if (!p.whole) {
+                            slot[M * D + mine] = top;
+                            slot[M * D + M + mine] = sum;
+                        } else if (a.lse && mine < p.nrows) {
+                            a.lse[to * a.H + head] = lse_of(top, sum);
+                        }
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int q = 0; q < C::ITEMS; ++q) {
+                    const int i = q * 32 + lane, row = e0 + i / (DR / 4), c = i % (DR / 4) * 4;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) {
+                        const float4 v = *reinterpret_cast<const float4 *>(
+                            xb + (n * M + row) * C::XROW + c);
+                        const float f = fac[n][row];
+                        o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+                        o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+                    }
+                    if (row < p.nrows) {
+                        if (p.whole)
+                            finish4(a, row_out[row] + r * DR + c, o, row_l[row], gate[q]);
+                        else
+                            *reinterpret_cast<float4 *>(slot + row * D + r * DR + c) = o;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&xempty);
+            }
+            if (lane == 0)
+                mbar_arrive(&ring.qempty[b]);
+        }
+        pdl_launch_dependents();
+        return;
+    }
     // --------------------------------------------------------------- consumers
-    const int st = warp / MT, mt = warp % MT;           // unit group, rows
+    const int st = warp / RT, row0 = warp % RT * 8;     // unit group, rows
     const int g = lane >> 2, cq = lane & 3;
     const int btl = box_log2(a.pg.page, U), box = (1 << btl) * D * 2, dbs = (1 << btl) * 128;
+    // a lane's position (of 16) and 16-byte piece in a load of keys and of values
+    const int ka = (lane & 15) * 128, kc = lane >> 4;
+    const int va = ((lane & 7) + 8 * (lane >> 4)) * 128, vc = (lane >> 3) & 1;
     long long it = 0;                                   // units of the CTA before this part
+    uint32_t xr = 0;                                    // hand-overs so far
     for (int parts = 0;; ++parts) {
         const int b = parts & 1;
-        // one thread decides for all, so that every warp meets the same barriers
-        if (threadIdx.x == 0)
-            ring.go = ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq) && ring.part[b].live;
-        named_bar_sync(1, CW * 32);
-        if (!ring.go)
-            break;
-        ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq);
+        if (!ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq))
+            return;
         const Part p = ring.part[b];
+        if (!p.live)
+            break;
         const int first_row = p.p0 + p.rowf;            // the last position that every row sees
         const int last_row = p.p0 + p.rowf + (p.hf + p.nrows - 1) / group;
-        int lim[2];                                     // of this lane's rows
+        int lim[2];                                     // of this lane's rows, 2 cq and the next
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            const int i = mt * 16 + g + 8 * hr;
-            lim[hr] = i < p.nrows ? first_row + (p.hf + i) / group : -1;
+        for (int e = 0; e < 2; ++e) {
+            const int i = row0 + 2 * cq + e;
+            lim[e] = i < p.nrows ? first_row + (p.hf + i) / group : -1;
         }
-        float O[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        const bool idle = row0 >= p.nrows;
+        uint32_t qf[D / 16][2];                         // the rows, as the products take them
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
+        for (int k = 0; k < D / 32; ++k) {
+            uint32_t r[4];
+            ldsm_x4(r, smem_u32(qbuf) + b * R::QB + (row0 + (lane & 7)) * (D * 2) +
+                           (((4 * k + (lane >> 3)) ^ (lane & 7)) << 4));
+            qf[2 * k][0] = r[0], qf[2 * k][1] = r[1];
+            qf[2 * k + 1][0] = r[2], qf[2 * k + 1][1] = r[3];
+        }
+        // O[j]: elements 16 j + g and 8 on, of rows 2 cq and the next
+        float O[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 O[j][e] = 0.f;
         const int count = max(p.u1 - p.u0, 0);
-        const uint32_t qrow = smem_u32(qbuf) + b * R::QB + (mt * 16 + (lane & 15)) * (D * 2);
         // this group's units: those of index st modulo NS within the CTA
         for (int n = (int)((st - it) & (NS - 1)); n < count; n += NS) {
             const long long idx = it + n;
             const int slot = (int)(idx % R::SLOTS);
-            const bool ok = ring_wait(&ring.full[slot], (uint32_t)((idx / R::SLOTS) & 1), &ring.abort, a.sq);
+            if (!ring_wait(&ring.full[slot], (uint32_t)((idx / R::SLOTS) & 1), &ring.abort, a.sq))
+                return;
             const uint32_t ks = smem_u32(units) + slot * C::UNIT, vs = ks + R::PLANE;
             const int t0 = (p.u0 + n) * U;
-            if (ok && mt * 16 < p.nrows) {
+            if (!idle) {
                 const unsigned there = ring.ok[slot];
-                // ---- scores
-                constexpr int CHAINS = U == 16 ? 2 : 1;  // sums of independent products
-                float sc[CHAINS][U / 8][4];
+                // ---- scores: positions g and 8 on of each 16, rows 2 cq and the next
+                constexpr int CHAINS = 64 / U;           // sums of independent products
+                float sc[CHAINS][U / 16][4];
 #pragma unroll
                 for (int c = 0; c < CHAINS; ++c)
 #pragma unroll
-                    for (int j = 0; j < U / 8; ++j)
+                    for (int q = 0; q < U / 16; ++q)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            sc[c][j][e] = 0.f;
-                // a lane's row of the unit for the keys (kt) and for the values (vt)
-                const int kt = (lane & 7) + 8 * (lane >> 4), vt = lane & 15;
+                            sc[c][q][e] = 0.f;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t qa[4];
-                    ldsm_x4(qa, qrow + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
-                    const int ch = 2 * k + ((lane >> 3) & 1);
+                for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                     for (int q = 0; q < U / 16; ++q) {
                         const int in = (q * 16) >> btl, at = (q * 16) & ((1 << btl) - 1);
-                        uint32_t kb[4];
-                        ldsm_x4(kb, ks + in * box + (ch >> 3) * dbs + (at + kt) * 128 + (((ch & 7) ^ (lane & 7)) << 4));
-                        mma(sc[k % CHAINS][2 * q], qa, kb[0], kb[1]);
-                        mma(sc[k % CHAINS][2 * q + 1], qa, kb[2], kb[3]);
+                        uint32_t ak[4];
+                        ldsm_x4(ak, ks + in * box + (k >> 2) * dbs + at * 128 + ka +
+                                        ((((2 * k + kc) & 7) ^ (lane & 7)) << 4));
+                        mma(sc[k % CHAINS][q], ak, qf[k][0], qf[k][1]);
                     }
-                }
 #pragma unroll
-                for (int j = 0; j < U / 8; ++j)
+                for (int q = 0; q < U / 16; ++q)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[0][j][e] = (CHAINS == 2 ? sc[0][j][e] + sc[CHAINS - 1][j][e] : sc[0][j][e]) * a.scale_log2;
+                    for (int e = 0; e < 4; ++e) {
+                        if (CHAINS == 4)
+                            sc[0][q][e] = (sc[0][q][e] + sc[1 % CHAINS][q][e]) + (sc[2 % CHAINS][q][e] + sc[3 % CHAINS][q][e]);
+                        else if (CHAINS == 2)
+                            sc[0][q][e] += sc[1 % CHAINS][q][e];
+                        sc[0][q][e] *= a.scale_log2;
+                    }
                 // ---- what a row does not see
                 const bool part = t0 + U - 1 > first_row;
                 if (part || there != (1u << (U >> btl)) - 1u) {
 #pragma unroll
-                    for (int j = 0; j < U / 8; ++j)
+                    for (int q = 0; q < U / 16; ++q)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int t = j * 8 + 2 * cq + (e & 1);
-                            if (t0 + t > lim[e >> 1] || !((there >> (t >> btl)) & 1u))
-                                sc[0][j][e] = -INFINITY;
+                            const int t = q * 16 + g + 8 * (e >> 1);
+                            if (t0 + t > lim[e & 1] || !((there >> (t >> btl)) & 1u))
+                                sc[0][q][e] = -INFINITY;
                         }
                 }
-                // ---- running maximum; rows of a quad of lanes
-                float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int j = 0; j < U / 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e >> 1] = fmaxf(mx[e >> 1], sc[0][j][e]);
-                bool grow = false;
+                // ---- running maximum, over the lanes that share rows
                 float to[2];
+                bool grow = false;
 #pragma unroll
-                for (int hr = 0; hr < 2; ++hr) {
-                    mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 1));
-                    mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(0xffffffffu, mx[hr], 2));
-                    to[hr] = mx[hr] > m[hr] + 8.f ? mx[hr] : m[hr];
-                    grow |= to[hr] != m[hr];
+                for (int e = 0; e < 2; ++e) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < U / 16; ++q)
+                        mx = fmaxf(mx, fmaxf(sc[0][q][e], sc[0][q][2 + e]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    to[e] = mx > m[e] + 8.f ? mx : m[e];
+                    grow |= to[e] != m[e];
                 }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                    for (int hr = 0; hr < 2; ++hr) {
-                        const float f = to[hr] == m[hr] ? 1.f : exp2f(m[hr] - to[hr]);
-                        m[hr] = to[hr];
-                        l[hr] *= f;
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = to[e] == m[e] ? 1.f : exp2f(m[e] - to[e]);
+                        m[e] = to[e];
+                        l[e] *= f;
 #pragma unroll
-                        for (int j = 0; j < D / 8; ++j) {
-                            O[j][2 * hr] *= f;
-                            O[j][2 * hr + 1] *= f;
+                        for (int j = 0; j < D / 16; ++j) {
+                            O[j][e] *= f;
+                            O[j][2 + e] *= f;
                         }
                     }
                 }
-                const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
                 // p, in place of the scores; hi + lo are its first 16 bits
-                uint32_t hi[U / 8][2], lo[U / 8][2];
+                uint32_t hi[U / 16][2], lo[U / 16][2];
+                const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-                for (int j = 0; j < U / 8; ++j)
+                for (int q = 0; q < U / 16; ++q)
 #pragma unroll
-                    for (int hr = 0; hr < 2; ++hr) {
-                        const float p0 = exp2f(sc[0][j][2 * hr] - base[hr]), p1 = exp2f(sc[0][j][2 * hr + 1] - base[hr]);
-                        l[hr] += p0 + p1;
-                        sc[0][j][2 * hr] = p0;
-                        sc[0][j][2 * hr + 1] = p1;
-                        hi[j][hr] = pack_bf16x2(p0, p1);
-                        lo[j][hr] = pack_bf16x2(p0 - bf16_lo(hi[j][hr]), p1 - bf16_hi(hi[j][hr]));
+                    for (int x = 0; x < 2; ++x) {
+                        const float p0 = exp2f(sc[0][q][2 * x] - base[0]), p1 = exp2f(sc[0][q][2 * x + 1] - base[1]);
+                        l[0] += p0;
+                        l[1] += p1;
+                        sc[0][q][2 * x] = p0;
+                        sc[0][q][2 * x + 1] = p1;
+                        const uint32_t h = pack_bf16x2(p0, p1);
+                        hi[q][x] = turned(h);
+                        lo[q][x] = turned(pack_bf16x2(p0 - bf16_lo(h), p1 - bf16_hi(h)));
                     }
                 // ---- values that no row of the tile sees are stale: zeros (every warp of the
                 //      group writes them); of those that some rows see, look for what is not
@@ -276,22 +387,27 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, 1)
                     __syncwarp();
                     odd = __any_sync(0xffffffffu, odd);
                 }
-                // ---- O += p V
+                // ---- O += V p, four loads ahead of their products
                 if (!odd) {
+                    constexpr int AHEAD = 4;
 #pragma unroll
                     for (int q = 0; q < U / 16; ++q) {
-                        const uint32_t h[4] = {hi[2 * q][0], hi[2 * q][1], hi[2 * q + 1][0], hi[2 * q + 1][1]};
-                        const uint32_t w[4] = {lo[2 * q][0], lo[2 * q][1], lo[2 * q + 1][0], lo[2 * q + 1][1]};
                         const int in = (q * 16) >> btl, at = (q * 16) & ((1 << btl) - 1);
+                        const uint32_t vrow = vs + in * box + at * 128 + va;
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j) {
-                            const int ch = 2 * j + (lane >> 4);
-                            uint32_t vb[4];
-                            ldsm_x4_trans(vb, vs + in * box + (ch >> 3) * dbs + (at + vt) * 128 + (((ch & 7) ^ (lane & 7)) << 4));
-                            mma(O[2 * j], h, vb[0], vb[1]);
-                            mma(O[2 * j + 1], h, vb[2], vb[3]);
-                            mma(O[2 * j], w, vb[0], vb[1]);
-                            mma(O[2 * j + 1], w, vb[2], vb[3]);
+                        for (int j0 = 0; j0 < D / 16; j0 += AHEAD) {
+                            uint32_t av[AHEAD][4];
+#pragma unroll
+                            for (int x = 0; x < AHEAD; ++x) {
+                                const int j = j0 + x;
+                                ldsm_x4_trans(av[x], vrow + (j >> 2) * dbs + ((((2 * j + vc) & 7) ^ (lane & 7)) << 4));
+                            }
+#pragma unroll
+                            for (int x = 0; x < AHEAD; ++x)
+                                mma(O[j0 + x], av[x], hi[q][0], hi[q][1]);
+#pragma unroll
+                            for (int x = 0; x < AHEAD; ++x)
+                                mma(O[j0 + x], av[x], lo[q][0], lo[q][1]);
                         }
                     }
                 } else {
@@ -300,28 +416,29 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, 1)
                     for (int t = 0; t < U; ++t) {
                         float pt[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int j = 0; j < U / 8; ++j)
-                            if (j == t >> 3)
+                        for (int q = 0; q < U / 16; ++q)
+                            if (q == t >> 4)
 #pragma unroll
-                                for (int hr = 0; hr < 2; ++hr)
-                                    pt[hr] = t & 1 ? sc[0][j][2 * hr + 1] : sc[0][j][2 * hr];
+                                for (int e = 0; e < 2; ++e)
+                                    pt[e] = t & 8 ? sc[0][q][2 + e] : sc[0][q][e];
 #pragma unroll
-                        for (int hr = 0; hr < 2; ++hr)
-                            pt[hr] = __shfl_sync(0xffffffffu, pt[hr], (lane & ~3) | ((t & 7) >> 1));
+                        for (int e = 0; e < 2; ++e) {
+                            pt[e] = __shfl_sync(0xffffffffu, pt[e], (t & 7) * 4 + cq);
+                            if (t0 + t > lim[e] || !((there >> (t >> btl)) & 1u))
+                                pt[e] = -1.f;            // not seen
+                        }
                         const uint32_t vrow = vs + (t >> btl) * box + (t & ((1 << btl) - 1)) * 128;
 #pragma unroll
-                        for (int j = 0; j < D / 8; ++j) {
-                            uint32_t v;
-                            asm volatile("ld.shared.u32 %0, [%1];"
-                                         : "=r"(v)
-                                         : "r"(vrow + (j >> 3) * dbs + (((j & 7) ^ (t & 7)) << 4) + cq * 4));
+                        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-                            for (int hr = 0; hr < 2; ++hr)
-                                if (t0 + t <= lim[hr] && ((there >> (t >> btl)) & 1u)) {
-                                    O[j][2 * hr] = fmaf(pt[hr], bf16_lo(v), O[j][2 * hr]);
-                                    O[j][2 * hr + 1] = fmaf(pt[hr], bf16_hi(v), O[j][2 * hr + 1]);
-                                }
-                        }
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t at = vrow + (j >> 2) * dbs + ((((2 * j + x) & 7) ^ (t & 7)) << 4) + g * 2;
+                                const float v = __uint_as_float(lds_u16(at) << 16);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (!(pt[e] < 0.f))
+                                        O[j][2 * x + e] = fmaf(pt[e], v, O[j][2 * x + e]);
+                            }
                     }
                 }
                 if (part)
@@ -332,95 +449,54 @@ __global__ void __launch_bounds__(Cfg<D, MT>::THREADS, 1)
                 mbar_arrive(&ring.empty[slot]);
         }
         it += count;
+        __syncwarp();
         if (lane == 0)
             mbar_arrive(&ring.qempty[b]);
-        // ---- join the groups
+        // ---- hand over
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 1);
-            l[hr] += __shfl_xor_sync(0xffffffffu, l[hr], 2);
-            if (cq == 0) {
-                red_m[warp * 16 + g + 8 * hr] = m[hr];
-                red_l[warp * 16 + g + 8 * hr] = l[hr];
-            }
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
         }
-        named_bar_sync(1, CW * 32);
-        float f[2];
+        float *const own = xb + (warp * 8 + 2 * cq) * C::XROW + g;
 #pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-            float top = -INFINITY;
+        for (int r = 0; r < C::ROUNDS; ++r, ++xr) {
+            if (!ring_wait(&xempty, (xr & 1) ^ 1u, &ring.abort, a.sq))
+                return;
+            if (r == 0 && g == 0) {
 #pragma unroll
-            for (int q = 0; q < NS; ++q)
-                top = fmaxf(top, red_m[(q * MT + mt) * 16 + g + 8 * hr]);
-            f[hr] = m[hr] == top ? 1.f : exp2f(m[hr] - top);
-        }
-        float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
-        if (threadIdx.x < M) {
-            const int i = threadIdx.x;
-            float top = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int q = 0; q < NS; ++q)
-                top = fmaxf(top, red_m[(q * MT + i / 16) * 16 + i % 16]);
-#pragma unroll
-            for (int q = 0; q < NS; ++q) {
-                const float mq = red_m[(q * MT + i / 16) * 16 + i % 16];
-                sum += red_l[(q * MT + i / 16) * 16 + i % 16] * (mq == top ? 1.f : exp2f(mq - top));
-            }
-            row_m[i] = top;
-            row_l[i] = sum;
-            if (!p.whole) {
-                slot[M * D + i] = top;
-                slot[M * D + M + i] = sum;
-            } else if (a.lse && i < p.nrows) {
-                a.lse[(long long)(p.r0 + p.rowf + (p.hf + i) / group) * a.H + p.hk * group + (p.hf + i) % group] =
-                    lse_of(top, sum);
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < C::ROUNDS; ++r) {
-            float *const own = xb + warp * 16 * C::XROW;
-#pragma unroll
-            for (int j = 0; j < DR / 8; ++j)
-#pragma unroll
-                for (int hr = 0; hr < 2; ++hr)
-                    *reinterpret_cast<float2 *>(own + (g + 8 * hr) * C::XROW + j * 8 + 2 * cq) =
-                        make_float2(O[r * (DR / 8) + j][2 * hr] * f[hr], O[r * (DR / 8) + j][2 * hr + 1] * f[hr]);
-            named_bar_sync(1, CW * 32);
-            for (int i = threadIdx.x; i < M * (DR / 4); i += CW * 32) {
-                const int row = i / (DR / 4), c = (i % (DR / 4)) * 4;
-                if (row >= p.nrows)
-                    break;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int q = 0; q < NS; ++q) {
-                    const float4 v = *reinterpret_cast<const float4 *>(
-                        xb + ((q * MT + row / 16) * 16 + row % 16) * C::XROW + c);
-                    o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+                for (int e = 0; e < 2; ++e) {
+                    red_m[warp * 8 + 2 * cq + e] = m[e];
+                    red_l[warp * 8 + 2 * cq + e] = l[e];
                 }
-                if (p.whole) {
-                    const long long to = p.r0 + p.rowf + (p.hf + row) / group;
-                    const int head = p.hk * group + (p.hf + row) % group;
-                    finish4(a, to, head, r * DR + c, o, row_l[row], gate4(a, to, head, r * DR + c));
-                } else
-                    *reinterpret_cast<float4 *>(slot + row * D + r * DR + c) = o;
             }
-            if (r + 1 < C::ROUNDS)
-                named_bar_sync(1, CW * 32);
+#pragma unroll
+            for (int j = 0; j < DR / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    own[(e & 1) * C::XROW + j * 16 + 8 * (e >> 1)] = O[r * (DR / 16) + j][e];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&xfull);
         }
     }
     pdl_launch_dependents();
 }
 
 // Joins the parts of the segment that begins in CTA blockIdx.x's run and goes on behind
-// it: M / 16 rows a block, the parts dealt to the warps of a row, kFly of them on their
+// it: ROWS rows a block, the parts dealt to the warps of a row, kFly of them on their
 // way at a time.  Bound by three dependent loads (the record, the parts, and what the
 // launch itself takes).
 constexpr int kJoin = 256, kFly = 5;
 
+template <int M>
+constexpr int kJoinRows = M > 16 ? M / 16 : 1;
+
 template <int D, int M>
 __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant__ PagedAttnArgs a)
 {
-    constexpr int ROWS = M / 16, W = kJoin / 32 / ROWS, N4 = (D + 127) / 128;
+    constexpr int ROWS = kJoinRows<M>, W = kJoin / 32 / ROWS, N4 = (D + 127) / 128;
     static_assert(W * 32 >= D / 4, "a thread finishes four columns");
     __shared__ float red_m[kJoin / 32], red_l[kJoin / 32];
     __shared__ float4 sums[kJoin / 32][D / 4];
@@ -436,7 +512,7 @@ __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant
     const long long row = rec.r0 + rec.rowf + h / group;
     const int col = (w * 32 + lane) * 4;               // of the thread at the end
     const bool mine = i < rec.nrows && col < D;
-    const float4 gate = mine ? gate4(a, row, head, col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint4 gate = mine && a.gate ? gate4(a, row * a.gs.tok + head * a.gs.head + col) : make_uint4(0, 0, 0, 0);
     float top = -INFINITY, sum = 0.f;
     float4 o[N4];
 #pragma unroll
@@ -509,7 +585,7 @@ __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant
     }
     if (col == 0 && a.lse)
         a.lse[row * a.H + head] = lse_of(top, sum);
-    finish4(a, row, head, col, v, sum, gate);
+    finish4(a, row * a.os.tok + head * a.os.head + col, v, sum, gate);
 }
 
 using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
@@ -528,19 +604,19 @@ EncodeFn encoder()
     return fn;
 }
 
-// Row tiles of 16: what an average sequence's rows fill (a larger tile than a
-// sequence needs costs products, a smaller one reads its keys again).
+// Tiles of eight rows: what an average sequence's rows fill (a larger tile than a
+// sequence needs leaves warps without work, a smaller one reads its keys again).
 int row_tiles(int group, int n, int total)
 {
     const long long rows = ((long long)total + n - 1) / n * group;
-    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
 }
 
-template <int D, int MT>
+template <int D, int RT>
 cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
 {
-    using C = Cfg<D, MT>;
-    auto *fn = paged_attn_kernel<D, MT>;
+    using C = Cfg<D, RT>;
+    auto *fn = paged_attn_kernel<D, RT>;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = allow_smem(fn, C::SMEM, done);
     if (e != cudaSuccess)
@@ -559,14 +635,14 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    e = cudaLaunchKernelEx(&cfg, fn, a, km, vm, C::NS);
+    e = cudaLaunchKernelEx(&cfg, fn, a, km, vm, 4);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t join = {};
-    join.gridDim = dim3(grid, 16);
+    join.gridDim = dim3(grid, C::M / kJoinRows<C::M>);
     join.blockDim = dim3(kJoin);
     join.stream = s;
     join.attrs = at;
@@ -580,7 +656,8 @@ cudaError_t launch_d(const PagedAttnArgs &a, cudaStream_t s)
     switch (row_tiles(a.H / a.Hk, a.sq.n, a.sq.total)) {
     case 1: return launch<D, 1>(a, s);
     case 2: return launch<D, 2>(a, s);
-    default: return launch<D, 4>(a, s);
+    case 4: return launch<D, 4>(a, s);
+    default: return launch<D, 8>(a, s);
     }
 }
 
@@ -602,7 +679,7 @@ bool encode_pages(CUtensorMap *m, const Pages &pg, bool v, int Hk, int d, int bo
 
 long long paged_attn_workspace(int d, int group, int n, int total)
 {
-    const int M = n > 0 ? 16 * row_tiles(group, n, total) : 16;
+    const int M = n > 0 ? 8 * row_tiles(group, n, total) : 8;
     return 2ll * kMaxCtas * M * (d + 2) * 4 + kMaxCtas * (long long)sizeof(Rec);
 }
 

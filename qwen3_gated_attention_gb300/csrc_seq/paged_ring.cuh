@@ -191,10 +191,11 @@ __device__ __forceinline__ void cp_arrive(uint64_t *bar)
 }
 
 // The ring and the two row buffers of a CTA.
-template <int D, int M_, bool V_, int SLOTS_, int NP_, int READERS, int CONSUMERS>
+// NS groups of READERS warps take the units; ROWREADERS warps read the rows' buffers.
+template <int D, int M_, bool V_, int SLOTS_, int NP_, int NS, int READERS, int ROWREADERS>
 struct Ring {
     static constexpr int U = kUnit<D>, DB = D / 64, M = M_, SLOTS = SLOTS_, NP = NP_;
-    static_assert(SLOTS > 0 && SLOTS % NP == 0 && SLOTS % (CONSUMERS / READERS) == 0, "");
+    static_assert(SLOTS > 0 && SLOTS % NP == 0 && SLOTS % NS == 0, "");
     static constexpr bool V = V_;                      // values too
     static constexpr int PLANE = U * D * 2, UNIT = V ? 2 * PLANE : PLANE;
     static constexpr int QB = M * D * 2;               // query rows, 16-byte pieces swizzled by row
@@ -204,7 +205,6 @@ struct Ring {
     float lse[2][V ? 1 : M];
     unsigned ok[SLOTS];                                // boxes of a unit whose page exists
     volatile int abort;
-    int go;
 
     __device__ __forceinline__ void init()
     {
@@ -214,7 +214,7 @@ struct Ring {
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qfull[i], 64);
-            mbar_init(&qempty[i], CONSUMERS);
+            mbar_init(&qempty[i], ROWREADERS);
         }
         abort = 0;
         fence_mbar_init();
@@ -412,6 +412,14 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// an 8 x 8 matrix of 16-bit elements, as the matrix instructions hold it, turned over
+__device__ __forceinline__ uint32_t turned(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
 }  // namespace paged

@@ -23,7 +23,7 @@ struct Cfg {
     static constexpr int FIT = (227 * 1024 - 2 * M * D * 2 - 4096) / UNIT;
     static constexpr int SLOTS = (FIT > 24 ? 24 : FIT) / CW * CW;
     static constexpr int SMEM = SLOTS * UNIT + 2 * M * D * 2 + 1024;
-    using R = Ring<D, M, false, SLOTS, NP, 1, CW>;
+    using R = Ring<D, M, false, SLOTS, NP, CW, 1, CW>;
     static_assert(SMEM + sizeof(R) + 512 <= 227 * 1024 && SLOTS > 0, "");
 };
 
@@ -57,19 +57,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     long long it = 0;
     for (int parts = 0;; ++parts) {
         const int b = parts & 1;
-        // the barrier also orders a pass behind the one before it
-        if (threadIdx.x == 0)
-            ring.go = ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq) && ring.part[b].live;
-        named_bar_sync(1, CW * 32);
-        const int go = ring.go;
-        named_bar_sync(1, CW * 32);
-        if (!go)
-            break;
-        ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq);
+        if (!ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq))
+            return;
         const Part p = ring.part[b];
+        if (!p.live)
+            return;
+        // a further pass over the same units adds to what the one before it wrote: every
+        // warp has left that one
+        if (p.pass && !ring_wait(&ring.qempty[b ^ 1], (uint32_t)(((parts - 1) >> 1) & 1), &ring.abort, a.sq))
+            return;
         const int first_row = p.p0 + p.rowf, end = p.p0 + p.len;
-        const int count = p.u1 - p.u0, tiles = (p.nrows + 15) / 16;
-        const uint32_t qrow = smem_u32(qbuf) + b * R::QB + (lane & 15) * (D * 2);
+        const int count = p.u1 - p.u0, tiles = (p.nrows + 7) / 8;
+        const uint32_t qrow = smem_u32(qbuf) + b * R::QB + (lane & 7) * (D * 2);
         const long long at = p.s * a.w_seq + p.hk * a.w_head;
         const float *const from = p.pass ? a.w_out : a.w;
         const int known = p.pass ? end : p.p0;          // positions that have a weight
@@ -77,87 +76,93 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const long long idx = it + n;
             const int slot = (int)(idx % R::SLOTS);
             const int t0 = (p.u0 + n) * U;
-            // what the positions have: this lane's 2 cq and 2 cq + 1 of each 8
-            float old[U / 8][2];
+            // what the positions have: g and 8 on of each 16
+            float old[U / 16][2];
 #pragma unroll
-            for (int j = 0; j < U / 8; ++j)
+            for (int q = 0; q < U / 16; ++q)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = t0 + j * 8 + 2 * cq + e;
-                    old[j][e] = g == 0 && from && t < known ? from[at + t] : 0.f;
+                for (int x = 0; x < 2; ++x) {
+                    const int t = t0 + q * 16 + g + 8 * x;
+                    old[q][x] = cq == 0 && from && t < known ? from[at + t] : 0.f;
                 }
-            const bool ok = ring_wait(&ring.full[slot], (uint32_t)((idx / R::SLOTS) & 1), &ring.abort, a.sq);
+            if (!ring_wait(&ring.full[slot], (uint32_t)((idx / R::SLOTS) & 1), &ring.abort, a.sq))
+                return;
             const uint32_t ks = smem_u32(units) + slot * C::UNIT;
-            if (ok) {
-                const unsigned there = ring.ok[slot];
-                const int kt = (lane & 7) + 8 * (lane >> 4);
-                const bool mask = t0 + U - 1 > first_row || there != (1u << (U >> btl)) - 1u;
-                float sum[U / 8][2];
+            const unsigned there = ring.ok[slot];
+            const bool mask = t0 + U - 1 > first_row || there != (1u << (U >> btl)) - 1u;
+            // the unit, once for all rows
+            uint32_t ak[D / 16][U / 16][4];
 #pragma unroll
-                for (int j = 0; j < U / 8; ++j)
-                    sum[j][0] = sum[j][1] = 0.f;
-                for (int mt = 0; mt < tiles; ++mt) {
-                    constexpr int CHAINS = U == 16 ? 2 : 1;
-                    float sc[CHAINS][U / 8][4];
+            for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                    for (int c = 0; c < CHAINS; ++c)
-#pragma unroll
-                        for (int j = 0; j < U / 8; ++j)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                sc[c][j][e] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        uint32_t qa[4];
-                        ldsm_x4(qa, qrow + mt * 16 * (D * 2) + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
-                        const int ch = 2 * k + ((lane >> 3) & 1);
-#pragma unroll
-                        for (int q = 0; q < U / 16; ++q) {
-                            const int in = (q * 16) >> btl, off = (q * 16) & ((1 << btl) - 1);
-                            uint32_t kb[4];
-                            ldsm_x4(kb, ks + in * box + (ch >> 3) * dbs + (off + kt) * 128 + (((ch & 7) ^ (lane & 7)) << 4));
-                            mma(sc[k % CHAINS][2 * q], qa, kb[0], kb[1]);
-                            mma(sc[k % CHAINS][2 * q + 1], qa, kb[2], kb[3]);
-                        }
-                    }
-#pragma unroll
-                    for (int hr = 0; hr < 2; ++hr) {
-                        const int i = mt * 16 + g + 8 * hr;
-                        const float lse = ring.lse[b][i];
-                        const int lim = i < p.nrows ? first_row + (p.hf + i) / group : -1;
-#pragma unroll
-                        for (int j = 0; j < U / 8; ++j)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int t = j * 8 + 2 * cq + e;
-                                float v = sc[0][j][2 * hr + e];
-                                if (CHAINS == 2)
-                                    v += sc[CHAINS - 1][j][2 * hr + e];
-                                v = exp2f(fmaf(v, a.scale_log2, -lse));
-                                if (lim < 0 || (mask && (t0 + t > lim || !((there >> (t >> btl)) & 1u))))
-                                    v = 0.f;
-                                sum[j][e] += v;
-                            }
-                    }
+                for (int q = 0; q < U / 16; ++q) {
+                    const int in = (q * 16) >> btl, off = (q * 16) & ((1 << btl) - 1);
+                    ldsm_x4(ak[k][q], ks + in * box + (k >> 2) * dbs + (off + (lane & 15)) * 128 +
+                                          ((((2 * k + (lane >> 4)) & 7) ^ (lane & 7)) << 4));
                 }
-#pragma unroll
-                for (int j = 0; j < U / 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float v = sum[j][e];
-                        v += __shfl_xor_sync(0xffffffffu, v, 4);
-                        v += __shfl_xor_sync(0xffffffffu, v, 8);
-                        v += __shfl_xor_sync(0xffffffffu, v, 16);
-                        const int t = t0 + j * 8 + 2 * cq + e;
-                        if (g == 0 && t < end)
-                            a.w_out[at + t] = old[j][e] + v;
-                    }
-            }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&ring.empty[slot]);
+                mbar_arrive(&ring.empty[slot]);         // the slot is free
+            float sum[U / 16][2];
+#pragma unroll
+            for (int q = 0; q < U / 16; ++q)
+                sum[q][0] = sum[q][1] = 0.f;
+            for (int rt = 0; rt < tiles; ++rt) {
+                constexpr int CHAINS = 64 / U;
+                float sc[CHAINS][U / 16][4];
+#pragma unroll
+                for (int c = 0; c < CHAINS; ++c)
+#pragma unroll
+                    for (int q = 0; q < U / 16; ++q)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[c][q][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 16; k += 2) {
+                    uint32_t qf[4];
+                    ldsm_x4(qf, qrow + rt * 8 * (D * 2) + (((2 * k + (lane >> 3)) ^ (lane & 7)) << 4));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int q = 0; q < U / 16; ++q)
+                            mma(sc[(k + x) % CHAINS][q], ak[k + x][q], qf[2 * x], qf[2 * x + 1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = rt * 8 + 2 * cq + e;
+                    const float lse = ring.lse[b][i];
+                    const int lim = i < p.nrows ? first_row + (p.hf + i) / group : -1;
+#pragma unroll
+                    for (int q = 0; q < U / 16; ++q)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int t = q * 16 + g + 8 * x;
+                            float v = sc[0][q][2 * x + e];
+                            if (CHAINS >= 2)
+                                v += sc[1 % CHAINS][q][2 * x + e];
+                            if (CHAINS == 4)
+                                v += sc[2 % CHAINS][q][2 * x + e] + sc[3 % CHAINS][q][2 * x + e];
+                            v = exp2f(fmaf(v, a.scale_log2, -lse));
+                            if (lim < 0 || (mask && (t0 + t > lim || !((there >> (t >> btl)) & 1u))))
+                                v = 0.f;
+                            sum[q][x] += v;
+                        }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < U / 16; ++q)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float v = sum[q][x];
+                    v += __shfl_xor_sync(0xffffffffu, v, 1);
+                    v += __shfl_xor_sync(0xffffffffu, v, 2);
+                    const int t = t0 + q * 16 + g + 8 * x;
+                    if (cq == 0 && t < end)
+                        a.w_out[at + t] = old[q][x] + v;
+                }
         }
         it += count;
+        __syncwarp();
         if (lane == 0)
             mbar_arrive(&ring.qempty[b]);
     }
