@@ -160,6 +160,8 @@ static gattn_status paged_args(const gattn_paged_attention_desc *p, bool values,
     CHECK(check_dim(p->head_dim));
     if (p->num_heads > 65536 / p->head_dim)
         return bad(GATTN_E_UNSUPPORTED, "num_heads * head_dim must be <= 65536");
+    if ((long long)p->total_rows * p->num_heads > 0x7fffffffll)
+        return bad(GATTN_E_UNSUPPORTED, "total_rows * num_heads must be below 2^31");
     if (!(p->scale > 0.f) || !std::isfinite(p->scale))
         return bad(GATTN_E_INVALID_ARG, "scale must be finite and > 0");
     CHECK(check_rows("q", p->q, p->q_stride_token, p->q_stride_head));

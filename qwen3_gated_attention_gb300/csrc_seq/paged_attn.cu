@@ -34,13 +34,17 @@ namespace {
 // RT: tiles of eight rows.
 template <int D, int RT>
 struct Cfg {
-    static constexpr int M = 8 * RT, CW = 8, NS = CW / RT, NE = 2, NP = 2;
+    // warps: consumers, joining ones (a tile of eight rows a warp joins nothing and
+    // finishes its own), producers; twelve have 168 registers each
+    static constexpr int M = 8 * RT, CW = RT == 1 ? 4 : 8, NS = CW / RT, NE = RT == 8 ? 0 : 2;
+    static constexpr int NP = RT == 1 || RT == 8 ? 4 : 2;
     static constexpr int THREADS = (CW + NE + NP) * 32;
     // columns that are handed over at once: what leaves the ring enough slots
     static constexpr int DR = RT <= 2 || D == 64 ? D : RT == 4 ? D / 2 : 64, ROUNDS = D / DR;
     static constexpr int XROW = DR + 4;                // floats of a row: two rows 8 banks apart
     static constexpr int XB = CW * 8 * XROW * 4;
-    static constexpr int ITEMS = M / NE * (DR / 4) / 32;   // of a joining lane, four columns each
+    static constexpr int ER = NE ? M / NE : 8;         // rows of a warp that finishes them
+    static constexpr int ITEMS = ER * (DR / 4) / 32;   // of its lanes, four columns each
     static constexpr int U = kUnit<D>, UNIT = U * D * 4;
     static constexpr int FIXED = 2 * M * D * 2 + XB + 4096 + 1024;
     static constexpr int FIT = (227 * 1024 - FIXED) / UNIT, STEP = NS > NP ? NS : NP;
@@ -48,7 +52,7 @@ struct Cfg {
     static constexpr int SMEM = SLOTS * UNIT + 2 * M * D * 2 + XB + 1024;
     using R = Ring<D, M, true, SLOTS, NP, NS, RT, CW + NE>;
     static_assert(SMEM + 4096 <= 227 * 1024 && SLOTS >= 4 && DR * ROUNDS == D && XROW % 16 == 4 &&
-                      ITEMS * 32 * NE == M * (DR / 4), "");
+                      ITEMS * 32 == ER * (DR / 4), "");
 };
 
 // Floats of a partial result: rows, then their m and sums.
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
     __shared__ R ring;
     __shared__ float red_m[CW * 8], red_l[CW * 8];   // of the consumers' rows
     __shared__ float fac[NS][M], row_l[M];             // the joining warps' own
-    __shared__ long long row_out[M], row_gate[M];      // where their rows are
+    __shared__ long long row_out[M], row_gate[M], row_lse[M];   // where their rows are
     __shared__ uint64_t xfull, xempty;                 // the hand-over buffer
     uint8_t *units = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *qbuf = units + C::SLOTS * C::UNIT;
@@ -111,7 +115,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
     const int group = a.H / a.Hk;
     if (threadIdx.x == 0) {
         mbar_init(&xfull, CW);
-        mbar_init(&xempty, NE);
+        mbar_init(&xempty, NE ? NE : 1);
         ring.init();
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -143,9 +147,62 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             recs[blockIdx.x] = rec;
         return;
     }
-    if (warp >= CW) {
+    // The finished rows of a part, ER of them by one warp from row e0 on, DR columns at a
+    // time: places() first, then gates() before and columns() after they are in xb.
+    constexpr int ER = C::ER, ITEMS = C::ITEMS;
+    auto places = [&](const Part &p, int e0) {
+        const int h = p.hf + e0 + lane, head = p.hk * group + h % group;        // a lane a row
+        const long long to = p.r0 + p.rowf + h / group;
+        if (lane < ER) {
+            row_out[e0 + lane] = to * a.os.tok + head * a.os.head;
+            row_gate[e0 + lane] = to * a.gs.tok + head * a.gs.head;
+            row_lse[e0 + lane] = to * a.H + head;
+        }
+        __syncwarp();
+    };
+    auto gates = [&](const Part &p, int e0, int r, uint4 (&gate)[ITEMS]) {
+#pragma unroll
+        for (int q = 0; q < ITEMS; ++q) {
+            const int i = q * 32 + lane, row = e0 + i / (DR / 4);
+            gate[q] = make_uint4(0, 0, 0, 0);
+            if (p.whole && a.gate && row < p.nrows)
+                gate[q] = gate4(a, row_gate[row] + r * DR + i % (DR / 4) * 4);
+        }
+    };
+    auto sums_of = [&](const Part &p, int row, float top, float sum) {
+        float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
+        row_l[row] = sum;
+        if (!p.whole) {
+            slot[M * D + row] = top;
+            slot[M * D + M + row] = sum;
+        } else if (a.lse && row < p.nrows) {
+            a.lse[row_lse[row]] = lse_of(top, sum);
+        }
+    };
+    auto columns = [&](const Part &p, int e0, int r, const uint4 (&gate)[ITEMS]) {
+        float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
+#pragma unroll
+        for (int q = 0; q < ITEMS; ++q) {
+            const int i = q * 32 + lane, row = e0 + i / (DR / 4), c = i % (DR / 4) * 4;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                const float4 v = *reinterpret_cast<const float4 *>(xb + (n * M + row) * C::XROW + c);
+                const float f = NS == 1 ? 1.f : fac[n][row];
+                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+                o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            }
+            if (row < p.nrows) {
+                if (p.whole)
+                    finish4(a, row_out[row] + r * DR + c, o, row_l[row], gate[q]);
+                else
+                    *reinterpret_cast<float4 *>(slot + row * D + r * DR + c) = o;
+            }
+        }
+    };
+    if (NE && warp >= CW) {
         // ------------------------------------------------------- the joining warps
-        const int e0 = (warp - CW) * (M / NE);          // first of its rows
+        const int e0 = (warp - CW) * ER;
         uint32_t xr = 0;                                // hand-overs so far
         for (int parts = 0;; ++parts) {
             const int b = parts & 1;
@@ -154,31 +211,16 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             const Part p = ring.part[b];
             if (!p.live)
                 break;
-            float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
-            const int mine = e0 + lane;                 // a lane a row
-            const int h = p.hf + mine, head = p.hk * group + h % group;
-            const long long to = p.r0 + p.rowf + h / group;
-            if (lane < M / NE) {
-                row_out[mine] = to * a.os.tok + head * a.os.head;
-                row_gate[mine] = to * a.gs.tok + head * a.gs.head;
-            }
-            __syncwarp();
+            places(p, e0);
 #pragma unroll 1
             for (int r = 0; r < C::ROUNDS; ++r, ++xr) {
-                // the gates come while the consumers work
-                uint4 gate[C::ITEMS];
-#pragma unroll
-                for (int q = 0; q < C::ITEMS; ++q) {
-                    const int i = q * 32 + lane, row = e0 + i / (DR / 4);
-                    gate[q] = make_uint4(0, 0, 0, 0);
-                    if (p.whole && a.gate && row < p.nrows)
-                        gate[q] = gate4(a, row_gate[row] + r * DR + i % (DR / 4) * 4);
-                }
+                uint4 gate[ITEMS];                      // come while the consumers work
+                gates(p, e0, r, gate);
                 if (!ring_wait(&xfull, xr & 1, &ring.abort, a.sq))
                     return;
                 if (r == 0) {
-                    if (lane < M / NE) {
-                        const float *const rm = red_m + mine, *const rl = red_l + mine;   // M apart by group
+                    if (lane < ER) {
+                        const float *const rm = red_m + e0 + lane, *const rl = red_l + e0 + lane;   // M apart by group
                         float top = -INFINITY, sum = 0.f;
 #pragma unroll
                         for (int q = 0; q < NS; ++q)
@@ -187,37 +229,13 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
                         for (int q = 0; q < NS; ++q) {
                             const float f = rm[q * M] == top ? 1.f : exp2f(rm[q * M] - top);
                             sum = fmaf(f, rl[q * M], sum);
-                            fac[q][mine] = f;
+                            fac[q][e0 + lane] = f;
                         }
-                        row_l[mine] = sum;
-                        if (!p.whole) {
-                            slot[M * D + mine] = top;
-                            slot[M * D + M + mine] = sum;
-                        } else if (a.lse && mine < p.nrows) {
-                            a.lse[to * a.H + head] = lse_of(top, sum);
-                        }
+                        sums_of(p, e0 + lane, top, sum);
                     }
                     __syncwarp();
                 }
-#pragma unroll
-                for (int q = 0; q < C::ITEMS; ++q) {
-                    const int i = q * 32 + lane, row = e0 + i / (DR / 4), c = i % (DR / 4) * 4;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        const float4 v = *reinterpret_cast<const float4 *>(
-                            xb + (n * M + row) * C::XROW + c);
-                        const float f = fac[n][row];
-                        o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
-                        o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
-                    }
-                    if (row < p.nrows) {
-                        if (p.whole)
-                            finish4(a, row_out[row] + r * DR + c, o, row_l[row], gate[q]);
-                        else
-                            *reinterpret_cast<float4 *>(slot + row * D + r * DR + c) = o;
-                    }
-                }
+                columns(p, e0, r, gate);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&xempty);
@@ -235,7 +253,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
     // a lane's position (of 16) and 16-byte piece in a load of keys and of values
     const int ka = (lane & 15) * 128, kc = lane >> 4;
     const int va = ((lane & 7) + 8 * (lane >> 4)) * 128, vc = (lane >> 3) & 1;
-    long long it = 0;                                   // units of the CTA before this part
+    int it = 0;                                         // units of the CTA before this part, modulo NS
+    int slot = st, phase = 0;                           // of this group's next unit
     uint32_t xr = 0;                                    // hand-overs so far
     for (int parts = 0;; ++parts) {
         const int b = parts & 1;
@@ -269,12 +288,19 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 O[j][e] = 0.f;
+        // the gates of rows that this warp finishes: into L2 meanwhile
+        if (!NE && p.whole && a.gate)
+            for (int i = lane; i < 8 * D / 64; i += 32) {
+                const int h = p.hf + row0 + i / (D / 64);
+                if (row0 + i / (D / 64) < p.nrows)
+                    prefetch_l2(static_cast<const char *>(a.gate) +
+                                ((p.r0 + p.rowf + h / group) * a.gs.tok + (p.hk * group + h % group) * a.gs.head + i % (D / 64) * 64) *
+                                    (a.gate_f32 ? 4 : 2));
+            }
         const int count = max(p.u1 - p.u0, 0);
         // this group's units: those of index st modulo NS within the CTA
-        for (int n = (int)((st - it) & (NS - 1)); n < count; n += NS) {
-            const long long idx = it + n;
-            const int slot = (int)(idx % R::SLOTS);
-            if (!ring_wait(&ring.full[slot], (uint32_t)((idx / R::SLOTS) & 1), &ring.abort, a.sq))
+        for (int n = (st - it) & (NS - 1); n < count; n += NS) {
+            if (!ring_wait(&ring.full[slot], phase, &ring.abort, a.sq))
                 return;
             const uint32_t ks = smem_u32(units) + slot * C::UNIT, vs = ks + R::PLANE;
             const int t0 = (p.u0 + n) * U;
@@ -322,26 +348,22 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
                                 sc[0][q][e] = -INFINITY;
                         }
                 }
-                // ---- running maximum, over the lanes that share rows
-                float to[2];
-                bool grow = false;
+                // ---- the reference: lanes that share a row look for scores 2^8 above it, and
+                //      agree on a new one only then
+                float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = -INFINITY;
+                for (int q = 0; q < U / 16; ++q)
 #pragma unroll
-                    for (int q = 0; q < U / 16; ++q)
-                        mx = fmaxf(mx, fmaxf(sc[0][q][e], sc[0][q][2 + e]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    to[e] = mx > m[e] + 8.f ? mx : m[e];
-                    grow |= to[e] != m[e];
-                }
-                if (__any_sync(0xffffffffu, grow)) {
+                    for (int e = 0; e < 2; ++e)
+                        mx[e] = fmaxf(mx[e], fmaxf(sc[0][q][e], sc[0][q][2 + e]));
+                if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float f = to[e] == m[e] ? 1.f : exp2f(m[e] - to[e]);
-                        m[e] = to[e];
+#pragma unroll
+                        for (int o = 4; o < 32; o *= 2)
+                            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+                        const float to = fmaxf(m[e], mx[e]), f = to == m[e] ? 1.f : exp2f(m[e] - to);
+                        m[e] = to;
                         l[e] *= f;
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) {
@@ -357,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
                 for (int q = 0; q < U / 16; ++q)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float p0 = exp2f(sc[0][q][2 * x] - base[0]), p1 = exp2f(sc[0][q][2 * x + 1] - base[1]);
+                        const float p0 = exp2_approx(sc[0][q][2 * x] - base[0]), p1 = exp2_approx(sc[0][q][2 * x + 1] - base[1]);
                         l[0] += p0;
                         l[1] += p1;
                         sc[0][q][2 * x] = p0;
@@ -447,8 +469,13 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&ring.empty[slot]);
+            slot += NS;
+            if (slot >= R::SLOTS) {
+                slot -= R::SLOTS;
+                phase ^= 1;
+            }
         }
-        it += count;
+        it = (it + count) & (NS - 1);
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&ring.qempty[b]);
@@ -460,11 +487,21 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
         }
         float *const own = xb + (warp * 8 + 2 * cq) * C::XROW + g;
+        if (!NE) {
+            places(p, row0);
+            if (g == 0)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    sums_of(p, row0 + 2 * cq + e, m[e], l[e]);
+        }
 #pragma unroll
         for (int r = 0; r < C::ROUNDS; ++r, ++xr) {
-            if (!ring_wait(&xempty, (xr & 1) ^ 1u, &ring.abort, a.sq))
+            uint4 gate[ITEMS];
+            if (!NE)
+                gates(p, row0, r, gate);
+            else if (!ring_wait(&xempty, (xr & 1) ^ 1u, &ring.abort, a.sq))
                 return;
-            if (r == 0 && g == 0) {
+            if (NE && r == 0 && g == 0) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     red_m[warp * 8 + 2 * cq + e] = m[e];
@@ -477,8 +514,13 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
                 for (int e = 0; e < 4; ++e)
                     own[(e & 1) * C::XROW + j * 16 + 8 * (e >> 1)] = O[r * (DR / 16) + j][e];
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&xfull);
+            if (NE) {
+                if (lane == 0)
+                    mbar_arrive(&xfull);
+            } else {
+                columns(p, row0, r, gate);
+                __syncwarp();
+            }
         }
     }
     pdl_launch_dependents();

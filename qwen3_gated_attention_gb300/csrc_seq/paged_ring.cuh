@@ -8,6 +8,8 @@
 // first one the segments' query rows and descriptions into two buffers too; the other
 // warps consume.  (One producer takes 700 cycles a unit and 90 more for every box beyond
 // two: as much as 16 KB take to arrive at an SM, twice that with boxes of 16 positions.)
+// A part costs a CTA some time whatever its length, so every segment counts kHead units
+// more than it has when the line is shared out.
 //
 // Every slot of the ring belongs to one producer and one group of consumers: SLOTS is
 // divided by the number of either.  A wait is for a phase's parity, so that it must never
@@ -24,7 +26,7 @@ namespace paged {
 template <int D>
 constexpr int kUnit = D >= 192 ? 16 : D == 128 ? 32 : 64;
 
-constexpr int kMaxCtas = 160;
+constexpr int kMaxCtas = 160, kHead = 3;
 
 // A segment's part within a CTA, as the consumers get it.
 struct Part {
@@ -38,8 +40,9 @@ struct Part {
 
 struct SeqUnits {
     int r0, len, p0, units;
-    long long tiles;       // of rows
-    __device__ __forceinline__ long long all(int Hk) const { return tiles * Hk * units; }
+    int tiles;             // of rows
+    // what it takes of the line
+    __device__ __forceinline__ long long all(int Hk) const { return units ? (long long)tiles * Hk * (units + kHead) : 0; }
 };
 
 // `bad`: rows whose positions do not fit the table
@@ -51,14 +54,15 @@ __device__ __forceinline__ SeqUnits seq_units(const PagedAttnArgs &a, int s, int
     bad = u.len > 0 && (u.p0 < 0 || (long long)u.p0 + u.len > a.cap);
     const bool on = u.len > 0 && !bad;
     u.units = on ? (u.p0 + u.len + U - 1) / U : 0;
-    u.tiles = on ? M ? ((long long)u.len * group + M - 1) / M : 1 : 0;
+    // (rows times heads fit 31 bits)
+    u.tiles = on ? M ? (int)(((unsigned)u.len * group + M - 1) / M) : 1 : 0;
     return u;
 }
 
-// A CTA's run of units and where it begins.
+// A CTA's run of the line and where it begins.
 struct Run {
     long long x0, x1, quota;
-    long long at;          // first unit of sequence s
+    long long at;          // where sequence s begins
     int s;
 };
 
@@ -178,6 +182,11 @@ __device__ __forceinline__ void box_g2s(uint32_t dst, const CUtensorMap *map, in
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // 16 bytes to shared memory without waiting; zeros where !on
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
 {
@@ -238,14 +247,19 @@ __device__ __forceinline__ void put_rows(const PagedAttnArgs &a, R &ring, uint8_
     const int lane = threadIdx.x & 31;
     const uint32_t qdst = smem_u32(qbuf) + b * R::QB;
     constexpr int CH = D / 8, RPI = 32 / CH > 0 ? 32 / CH : 1;          // rows of an iteration
-    for (int i = 0; i < M; i += RPI) {
-        const int row = i + (RPI > 1 ? lane / CH : 0);
-        const bool on = row < p.nrows;
-        const int h = p.hf + (on ? row : 0);
-        const __nv_bfloat16 *src =
-            a.q + (p.r0 + p.rowf + h / group) * a.qs.tok + (p.hk * group + h % group) * a.qs.head;
-        for (int c = RPI > 1 ? lane % CH : lane; c < CH; c += 32)
-            cp16(qdst + row * (D * 2) + ((c ^ (row & 7)) << 4), src + c * 8, on);
+    const int rows = (p.nrows + 7) & ~7;                // what the products take: zeros behind the last
+#pragma unroll
+    for (int i0 = 0; i0 < M; i0 += 32) {
+        // a lane a row
+        const int h = p.hf + min(i0 + lane, p.nrows - 1);
+        const long long off = (long long)(p.r0 + p.rowf + h / group) * a.qs.tok + (p.hk * group + h % group) * a.qs.head;
+        for (int i = i0; i < min(rows, i0 + 32); i += RPI) {
+            const int row = i + (RPI > 1 ? lane / CH : 0);
+            const __nv_bfloat16 *src = a.q + __shfl_sync(0xffffffffu, off, row & 31);
+            const int c = RPI > 1 ? lane % CH : lane;
+            if (c < CH)
+                cp16(qdst + row * (D * 2) + ((c ^ (row & 7)) << 4), src + c * 8, row < p.nrows);
+        }
     }
     if constexpr (!R::V)
         for (int i = lane; i < M; i += 32) {
@@ -274,14 +288,16 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
     const int btl = box_log2(a.pg.page, U), BT = 1 << btl, NB = U >> btl;
     const uint32_t box_bytes = BT * D * 2;
     const uint64_t pol = l2_evict_first_policy();
-    long long it = 0;                  // units so far
+    int it = 0;                        // units so far, modulo NP
+    int slot = pw, phase = 0;          // of this warp's next unit
+    int issued = 0;                    // units of its own
     int parts = 0;
     bool stop = false;
     int s = run.s;
     bool bad;
     SeqUnits u = seq_units(a, s, group, R::V ? M : 0, U, bad);
-    long long seg = (run.x0 - run.at) / u.units;
-    int u0 = (int)((run.x0 - run.at) % u.units);
+    int seg = (int)((run.x0 - run.at) / (u.units + kHead));
+    int v0 = (int)((run.x0 - run.at) % (u.units + kHead));       // place in the segment, its head counted
     // pages of 32 boxes of sequence tab_s, one a lane
     int tab_s = -1, tab_b = 0, tab_page = 0, tab_y = 0;
     for (long long x = run.x0; x < run.x1 && !stop;) {
@@ -290,13 +306,14 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
                 u = seq_units(a, ++s, group, R::V ? M : 0, U, bad);
             while (u.units == 0);
             seg = 0;
-            u0 = 0;
+            v0 = 0;
         }
-        const int u1 = (int)(run.x1 - x < u.units - u0 ? u0 + (run.x1 - x) : u.units);
-        const int hk = (int)(seg / u.tiles);
+        const int v1 = (int)min(run.x1 - x + v0, (long long)(u.units + kHead));
+        const int u0 = max(v0 - kHead, 0), u1 = max(v1 - kHead, 0);
+        const int hk = u.tiles == 1 ? seg : seg / u.tiles;
         const bool whole = u0 == 0 && u1 == u.units;
-        const long long passes = R::V ? 1 : ((long long)u.len * group + M - 1) / M;
-        for (long long pass = 0; pass < passes && !stop; ++pass, ++parts) {
+        const int passes = u1 <= u0 ? 0 : R::V ? 1 : (int)(((unsigned)u.len * group + M - 1) / M);
+        for (int pass = 0; pass < passes && !stop; ++pass, ++parts) {
             // ---- the rows and the description
             const int b = parts & 1;
             Part p;
@@ -306,17 +323,16 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
             p.r0 = u.r0;
             p.p0 = u.p0;
             p.len = u.len;
-            const long long i0 = (R::V ? seg % u.tiles : pass) * M;
-            const long long left = (long long)u.len * group - i0;
-            p.rowf = (int)(i0 / group);
-            p.hf = (int)(i0 % group);
-            p.nrows = (int)(left < M ? left : M);
+            const int i0 = (R::V ? seg - hk * u.tiles : pass) * M;
+            p.rowf = i0 / group;
+            p.hf = i0 - p.rowf * group;
+            p.nrows = min(u.len * group - i0, M);
             const int last = u.p0 + p.rowf + (p.hf + p.nrows - 1) / group;     // position the tile sees last
             p.u0 = u0;
             p.u1 = R::V ? min(u1, last / U + 1) : u1;
             p.whole = whole;
             p.slot = x == run.x0 ? 0 : 1;
-            p.pass = (int)min(pass, 1ll);
+            p.pass = min(pass, 1);
             if (pw == 0) {
                 if (!ring_wait(&ring.qempty[b], (uint32_t)((parts >> 1) & 1) ^ 1u, &ring.abort, a.sq))
                     stop = true;
@@ -325,10 +341,9 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
                     break;
                 put_rows(a, ring, qbuf, p, b, group);
             }
-            // ---- the units
-            for (int n = p.u0; n < p.u1; ++n, ++it) {
-                if (it % R::NP != pw)
-                    continue;
+            // ---- this warp's units
+            const int count = max(p.u1 - p.u0, 0);
+            for (int n = p.u0 + ((pw - it) & (R::NP - 1)); n < p.u1; n += R::NP) {
                 const int b0 = n * NB;
                 if (tab_s != s || b0 < tab_b || b0 >= tab_b + 32) {
                     tab_s = s;
@@ -345,9 +360,7 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
                     tab_page = page;
                     tab_y = t % a.pg.page;
                 }
-                const int slot = (int)(it % R::SLOTS);
-                if (lane == 0 &&
-                    !ring_wait(&ring.empty[slot], (uint32_t)((it / R::SLOTS) & 1) ^ 1u, &ring.abort, a.sq))
+                if (lane == 0 && !ring_wait(&ring.empty[slot], phase ^ 1, &ring.abort, a.sq))
                     stop = true;
                 stop = __any_sync(0xffffffffu, stop);
                 if (stop)
@@ -355,15 +368,15 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
                 // boxes that hold positions of the sequence
                 const int nb = min(NB, ((u.p0 + u.len - n * U) + BT - 1) >> btl);
                 const unsigned there = __ballot_sync(0xffffffffu, tab_page >= 0);
+                // a lane a box; a page that does not exist is one behind the last: zeros
+                const int from = b0 - tab_b + lane;
+                const int page = __shfl_sync(0xffffffffu, tab_page, from & 31);
+                const int y = __shfl_sync(0xffffffffu, tab_y, from & 31);
                 if (lane == 0) {
                     ring.ok[slot] = (there >> (b0 - tab_b)) & ((1u << nb) - 1u);
                     mbar_arrive_expect_tx(&ring.full[slot], nb * box_bytes * (R::V ? 2 : 1));
                 }
                 __syncwarp();
-                // a lane a box; a page that does not exist is one behind the last: zeros
-                const int from = b0 - tab_b + lane;
-                const int page = __shfl_sync(0xffffffffu, tab_page, from & 31);
-                const int y = __shfl_sync(0xffffffffu, tab_y, from & 31);
                 if (lane < nb) {
                     const uint32_t dst = smem_u32(units) + slot * R::UNIT + lane * box_bytes;
                     const uint32_t bar = smem_u32(&ring.full[slot]);
@@ -371,12 +384,19 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
                     if (R::V)
                         box_g2s(dst + R::PLANE, vmap, y, hk, page < 0 ? a.pg.pages : page, bar, pol);
                 }
+                ++issued;
+                slot += R::NP;
+                if (slot >= R::SLOTS) {
+                    slot -= R::SLOTS;
+                    phase ^= 1;
+                }
             }
+            it = (it + count) & (R::NP - 1);
             if (pw == 0 && lane == 0 && u0 == 0 && u1 < u.units)
-                seen(p, (int)((x + u.units - 1) / run.quota));
+                seen(p, (int)((x - v0 + u.units + kHead - 1) / run.quota));
         }
-        x += u1 - u0;
-        u0 = 0;
+        x += v1 - v0;
+        v0 = 0;
         ++seg;
     }
     if (!stop && pw == 0) {
@@ -390,15 +410,18 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
             mbar_arrive(&ring.qfull[b]);
         }
     }
-    // no copy may be on its way when the block ends (where consumers gave up)
+    // no copy may be on its way when the block ends (where consumers gave up): the last
+    // round of this warp's slots, from the newest back
     cp_async_wait_all();
     if (lane == 0)
-        for (long long i = it > R::SLOTS ? it - R::SLOTS : 0; i < it; ++i) {
-            if (i % R::NP != pw)
-                continue;
+        for (int i = 0; i < R::SLOTS / R::NP && i < issued; ++i) {
+            slot -= R::NP;
+            if (slot < 0) {
+                slot += R::SLOTS;
+                phase ^= 1;
+            }
             const unsigned long long t0 = global_ns();
-            while (!mbar_try(&ring.full[i % R::SLOTS], (uint32_t)((i / R::SLOTS) & 1)) &&
-                   global_ns() - t0 < kWaitLimitNs) {
+            while (!mbar_try(&ring.full[slot], phase) && global_ns() - t0 < kWaitLimitNs) {
             }
         }
     __syncwarp();
@@ -412,6 +435,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // an 8 x 8 matrix of 16-bit elements, as the matrix instructions hold it, turned over

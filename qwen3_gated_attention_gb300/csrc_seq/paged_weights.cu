@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
     const int g = lane >> 2, cq = lane & 3;
     const int btl = box_log2(a.pg.page, U), box = (1 << btl) * D * 2, dbs = (1 << btl) * 128;
-    long long it = 0;
+    int it = 0;                        // units of the CTA before this part, modulo CW
+    int slot = warp, phase = 0;        // of this warp's next unit
     for (int parts = 0;; ++parts) {
         const int b = parts & 1;
         if (!ring_wait(&ring.qfull[b], (uint32_t)((parts >> 1) & 1), &ring.abort, a.sq))
@@ -72,9 +73,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const long long at = p.s * a.w_seq + p.hk * a.w_head;
         const float *const from = p.pass ? a.w_out : a.w;
         const int known = p.pass ? end : p.p0;          // positions that have a weight
-        for (int n = (int)((warp - it) & (CW - 1)); n < count; n += CW) {
-            const long long idx = it + n;
-            const int slot = (int)(idx % R::SLOTS);
+        for (int n = (warp - it) & (CW - 1); n < count; n += CW) {
             const int t0 = (p.u0 + n) * U;
             // what the positions have: g and 8 on of each 16
             float old[U / 16][2];
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                     const int t = t0 + q * 16 + g + 8 * x;
                     old[q][x] = cq == 0 && from && t < known ? from[at + t] : 0.f;
                 }
-            if (!ring_wait(&ring.full[slot], (uint32_t)((idx / R::SLOTS) & 1), &ring.abort, a.sq))
+            if (!ring_wait(&ring.full[slot], phase, &ring.abort, a.sq))
                 return;
             const uint32_t ks = smem_u32(units) + slot * C::UNIT;
             const unsigned there = ring.ok[slot];
@@ -103,6 +102,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&ring.empty[slot]);         // the slot is free
+            slot += CW;
+            if (slot >= R::SLOTS) {
+                slot -= R::SLOTS;
+                phase ^= 1;
+            }
             float sum[U / 16][2];
 #pragma unroll
             for (int q = 0; q < U / 16; ++q)
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                                 v += sc[1 % CHAINS][q][2 * x + e];
                             if (CHAINS == 4)
                                 v += sc[2 % CHAINS][q][2 * x + e] + sc[3 % CHAINS][q][2 * x + e];
-                            v = exp2f(fmaf(v, a.scale_log2, -lse));
+                            v = exp2_approx(fmaf(v, a.scale_log2, -lse));
                             if (lim < 0 || (mask && (t0 + t > lim || !((there >> (t >> btl)) & 1u))))
                                 v = 0.f;
                             sum[q][x] += v;
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                         a.w_out[at + t] = old[q][x] + v;
                 }
         }
-        it += count;
+        it = (it + count) & (CW - 1);
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&ring.qempty[b]);
