@@ -86,3 +86,44 @@ def attention_bound(out, weight, error):
     exp(e) each; sums of up to 2^17 terms in fp32, in blocks, exponentials, the
     gate's exponential and division: below 2^-14 together."""
     return U_BF16 * out.abs() + (math.expm1(2 * error) + 2.0 ** -16 + 2.0 ** -14) * weight * (1 + U_BF16) + 1e-30
+
+
+def turn64(x, w, pos, rd, pairs, theta=1e6, eps=1e-6, rope_factor=None, rope_yarn=None, rope_size=0.0):
+    """One row [heads][d]: RMSNorm by w (None: as it is), the first rd elements turned."""
+    x = x.double()
+    if w is not None:
+        x = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * w.double()
+    size = rope_size
+    freq = []
+    for i in range(rd // 2):
+        f = theta ** (-2.0 * i / rd)
+        if rope_factor is not None:
+            f /= rope_factor
+        if rope_yarn is not None:
+            y = dict(beta_fast=32.0, beta_slow=1.0, **{k: v for k, v in rope_yarn.items() if not k.startswith("beta")})
+            y.update(rope_yarn)
+            at = lambda turns: rd * math.log(y["original"] / (2 * math.pi * turns)) / (2 * math.log(theta))  # noqa: E731
+            lo, hi = max(math.floor(at(y["beta_fast"])), 0), min(math.ceil(at(y["beta_slow"])), rd - 1)
+            c = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
+            f = f * (1 - c) + f / y["factor"] * c
+        freq.append(f)
+    if not size:
+        size = 0.1 * math.log(rope_yarn["factor"]) + 1 if rope_yarn is not None else 1.0
+    ang = torch.tensor(freq, dtype=torch.float64) * pos
+    cos, sin = ang.cos() * size, ang.sin() * size
+    out = x.clone()
+    a, b = (x[..., 0:rd:2], x[..., 1:rd:2]) if pairs else (x[..., :rd // 2], x[..., rd // 2:rd])
+    if pairs:
+        out[..., 0:rd:2], out[..., 1:rd:2] = a * cos - b * sin, b * cos + a * sin
+    else:
+        out[..., :rd // 2], out[..., rd // 2:rd] = a * cos - b * sin, b * cos + a * sin
+    return out
+
+
+def evicted(w, length, keep, recent):
+    """The kept positions of one head, in order; w [positions]."""
+    m = min(length, keep)
+    new = min(recent, m)
+    value = lambda i: -math.inf if math.isnan(w[i]) else w[i]      # noqa: E731
+    best = sorted(range(length - new), key=lambda i: (-value(i), i))[:m - new]
+    return sorted(best) + list(range(length - new, length))
