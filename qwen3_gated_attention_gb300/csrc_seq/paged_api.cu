@@ -73,8 +73,12 @@ gattn_status frequencies(const gattn_paged_rows_desc *p, int rd, float2 *to)
         lo = std::max(std::floor(pair(p->rope_beta_fast)), 0.);
         hi = std::min(std::ceil(pair(p->rope_beta_slow)), rd - 1.);
     }
+    // by the power anew every 8th time: a few ulp of a double apart
+    const double step = std::pow(theta, -2. / rd);
+    double plain = 1.;
     for (int i = 0; i < rd / 2; ++i) {
-        double f = std::pow(theta, -2. * i / rd);
+        plain = i % 8 ? plain * step : std::pow(theta, -2. * i / rd);
+        double f = plain;
         if (p->rope_scaling == GATTN_ROPE_LINEAR) {
             f /= p->rope_factor;
         } else if (p->rope_scaling == GATTN_ROPE_YARN) {

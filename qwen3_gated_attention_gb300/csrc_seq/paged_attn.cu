@@ -45,13 +45,13 @@ struct Cfg {
     static constexpr int XB = CW * 8 * XROW * 4;
     static constexpr int ER = NE ? M / NE : 8;         // rows of a warp that finishes them
     static constexpr int ITEMS = ER * (DR / 4) / 32;   // of its lanes, four columns each
-    static constexpr int U = kUnit<D>, UNIT = U * D * 4;
+    static constexpr int U = kUnit<D> * (RT == 8 ? 2 : 1), UNIT = U * D * 4;
     static constexpr int FIXED = 2 * M * D * 2 + XB + 4096 + 1024;
     static constexpr int FIT = (227 * 1024 - FIXED) / UNIT, STEP = NS > NP ? NS : NP;
     static constexpr int SLOTS = (FIT > 12 ? 12 : FIT) / STEP * STEP;
     static constexpr int SMEM = SLOTS * UNIT + 2 * M * D * 2 + XB + 1024;
-    using R = Ring<D, M, true, SLOTS, NP, NS, RT, CW + NE>;
-    static_assert(SMEM + 4096 <= 227 * 1024 && SLOTS >= 4 && DR * ROUNDS == D && XROW % 16 == 4 &&
+    using R = Ring<D, U, M, true, SLOTS, NP, NS, RT, CW + NE>;
+    static_assert(SMEM + 4096 <= 227 * 1024 && SLOTS >= 4 / (U / kUnit<D>) && DR * ROUNDS == D && XROW % 16 == 4 &&
                       ITEMS * 32 == ER * (DR / 4), "");
 };
 
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             if (!idle) {
                 const unsigned there = ring.ok[slot];
                 // ---- scores: positions g and 8 on of each 16, rows 2 cq and the next
-                constexpr int CHAINS = 64 / U;           // sums of independent products
+                constexpr int CHAINS = U < 64 ? 64 / U : 1;  // sums of independent products
                 float sc[CHAINS][U / 16][4];
 #pragma unroll
                 for (int c = 0; c < CHAINS; ++c)
@@ -330,9 +330,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
                 for (int q = 0; q < U / 16; ++q)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (CHAINS == 4)
+                        if constexpr (CHAINS == 4)
                             sc[0][q][e] = (sc[0][q][e] + sc[1 % CHAINS][q][e]) + (sc[2 % CHAINS][q][e] + sc[3 % CHAINS][q][e]);
-                        else if (CHAINS == 2)
+                        else if constexpr (CHAINS == 2)
                             sc[0][q][e] += sc[1 % CHAINS][q][e];
                         sc[0][q][e] *= a.scale_log2;
                     }

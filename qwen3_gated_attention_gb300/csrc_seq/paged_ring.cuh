@@ -22,11 +22,12 @@
 namespace gattn {
 namespace paged {
 
-// Positions of a unit: 16 KB of keys and values (12 KB for heads of 192).
+// Positions of a unit: 16 KB of keys and values (12 KB for heads of 192); kernels may
+// take twice as many.
 template <int D>
 constexpr int kUnit = D >= 192 ? 16 : D == 128 ? 32 : 64;
 
-constexpr int kMaxCtas = 160, kHead = 3;
+constexpr int kMaxCtas = 160, kHead = 10;
 
 // A segment's part within a CTA, as the consumers get it.
 struct Part {
@@ -201,9 +202,9 @@ __device__ __forceinline__ void cp_arrive(uint64_t *bar)
 
 // The ring and the two row buffers of a CTA.
 // NS groups of READERS warps take the units; ROWREADERS warps read the rows' buffers.
-template <int D, int M_, bool V_, int SLOTS_, int NP_, int NS, int READERS, int ROWREADERS>
+template <int D, int U_, int M_, bool V_, int SLOTS_, int NP_, int NS, int READERS, int ROWREADERS>
 struct Ring {
-    static constexpr int U = kUnit<D>, DB = D / 64, M = M_, SLOTS = SLOTS_, NP = NP_;
+    static constexpr int U = U_, DB = D / 64, M = M_, SLOTS = SLOTS_, NP = NP_;
     static_assert(SLOTS > 0 && SLOTS % NP == 0 && SLOTS % NS == 0, "");
     static constexpr bool V = V_;                      // values too
     static constexpr int PLANE = U * D * 2, UNIT = V ? 2 * PLANE : PLANE;

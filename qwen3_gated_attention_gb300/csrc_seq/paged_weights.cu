@@ -23,7 +23,7 @@ struct Cfg {
     static constexpr int FIT = (227 * 1024 - 2 * M * D * 2 - 4096) / UNIT;
     static constexpr int SLOTS = (FIT > 24 ? 24 : FIT) / CW * CW;
     static constexpr int SMEM = SLOTS * UNIT + 2 * M * D * 2 + 1024;
-    using R = Ring<D, M, false, SLOTS, NP, CW, 1, CW>;
+    using R = Ring<D, U, M, false, SLOTS, NP, CW, 1, CW>;
     static_assert(SMEM + sizeof(R) + 512 <= 227 * 1024 && SLOTS > 0, "");
 };
 

@@ -466,20 +466,22 @@ def delta_step(q, k, v, g, beta, cu_rows=None, *, num_seqs=None, state=None, sta
 
 def _table(t, name, dev, n):
     """(address, width, row stride) of a page table of n rows."""
-    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.int32 or
-            t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1)):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.int32:
         _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
-    w = t.shape[1]
-    return t.data_ptr(), w, t.stride(0) if n > 1 else max(w, 1)
+    sh, st = t.shape, t.stride()
+    if len(sh) != 2 or sh[0] != n or (st[1] != 1 and sh[1] > 1):
+        _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
+    return t.data_ptr(), sh[1], st[0] if n > 1 else max(sh[1], 1)
 
 
 def _pool(k_pages, v_pages, table, dev, n):
-    """The fields of gattn_pages; v_pages None: keys only."""
+    """(Hk, d) and the fields of gattn_pages; v_pages None: keys only."""
     kp, kt, kh, kb = _planes(k_pages, "k_pages", dev, _BF16)
+    pages, Hk, size, d = shape = k_pages.shape
     vp, vt, vh, vb = ((0, 8, 8, 8) if v_pages is None else
-                      _planes(v_pages, "v_pages", dev, _BF16, k_pages.shape))
+                      _planes(v_pages, "v_pages", dev, _BF16, shape))
     ta, w, ts = _table(table, "table", dev, n)
-    return kp, vp, k_pages.shape[0], k_pages.shape[2], kt, kh, kb, vt, vh, vb, ta, w, ts
+    return (Hk, d), (kp, vp, pages, size, kt, kh, kb, vt, vh, vb, ta, w, ts)
 
 
 def _received(t, name, dev, n, Hk):
@@ -506,18 +508,17 @@ def paged_rows(q, k, v, k_pages, v_pages, table, cu_rows, cache_pos, *, rope_the
     and beta_slow (1).  Returns q_out, bf16 [T][H][d]."""
     dev = q.get_device()
     qa = _rows(q, "q", dev, _DTYPES)
-    T, H, d = q.shape
+    T, H, d = shape = q.shape
     dtype = q.dtype
-    Hk = k.shape[1] if k.dim() == 3 else 0
+    cu, n = _cu(cu_rows, "cu_rows", dev)
+    (Hk, dp), pool = _pool(k_pages, v_pages, table, dev, n)
+    if dp != d:
+        _refuse(k_pages, "k_pages", dev, _BF16, d, "must have q's head_dim")
     ka = _rows(k, "k", dev, (dtype,), (T, Hk, d))
     va = _rows(v, "v", dev, (dtype,), (T, Hk, d))
-    cu, n = _cu(cu_rows, "cu_rows", dev)
-    pool = _pool(k_pages, v_pages, table, dev, n)
-    if k_pages.shape[1] != Hk or k_pages.shape[3] != d:
-        _refuse(k_pages, "k_pages", dev, _BF16, ("pages", Hk, "page_size", d))
     if q_out is None:
-        q_out = _output((T, H, d), q, stream)
-    oa = _rows(q_out, "q_out", dev, _BF16, (T, H, d))
+        q_out = _output(shape, q, stream)
+    oa = _rows(q_out, "q_out", dev, _BF16, shape)
     scaling, factor, original, fast, slow = gattn.ROPE_PLAIN, 1.0, 0, 0.0, 0.0
     if rope_yarn is not None:
         if rope_factor is not None:
@@ -549,23 +550,23 @@ def paged_attention_workspace(q, k_pages, cu_rows):
 
 
 def _attended(q, k_pages, v_pages, table, cu_rows, cache_pos, scale, lse):
-    """What attention and weights have in common: (device, descriptor's head, lse)."""
+    """What attention and weights have in common: (device, q's shape, descriptor's head,
+    lse's address)."""
     dev = q.get_device()
     qa = _rows(q, "q", dev, _BF16)
-    T, H, d = q.shape
+    T, H, d = shape = q.shape
     cu, n = _cu(cu_rows, "cu_rows", dev)
-    pool = _pool(k_pages, v_pages, table, dev, n)
-    Hk = k_pages.shape[1]
-    if k_pages.shape[3] != d:
-        _refuse(k_pages, "k_pages", dev, _BF16, ("pages", Hk, "page_size", d))
+    (Hk, dp), pool = _pool(k_pages, v_pages, table, dev, n)
+    if dp != d:
+        _refuse(k_pages, "k_pages", dev, _BF16, d, "must have q's head_dim")
     la = 0
     if lse is not None:
         if (not isinstance(lse, torch.Tensor) or lse.get_device() != dev or
                 lse.dtype is not torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
             _refuse(lse, "lse", dev, _F32, f"[{T}][{H}], contiguous")
         la = lse.data_ptr()
-    return dev, (H, Hk, d, d ** -0.5 if scale is None else scale, n, T, cu,
-                 _flat(cache_pos, "cache_pos", dev, _I32, n), *qa, *pool), la
+    return dev, shape, (H, Hk, d, d ** -0.5 if scale is None else scale, n, T, cu,
+                        _flat(cache_pos, "cache_pos", dev, _I32, n), *qa, *pool), la
 
 
 def paged_attention(q, k_pages, v_pages, table, cu_rows, cache_pos, *, gate=None, scale=None,
@@ -578,20 +579,21 @@ def paged_attention(q, k_pages, v_pages, table, cu_rows, cache_pos, *, gate=None
     None; lse fp32 [T][H] takes the softmax's log sums; workspace as
     paged_attention_workspace gives it (allocated for the call otherwise).  scale defaults
     to d ** -0.5.  Returns out, bf16 [T][H][d]."""
-    dev, head, la = _attended(q, k_pages, v_pages, table, cu_rows, cache_pos, scale, lse)
-    H, Hk, d, _, n, T = head[:6]
+    dev, shape, head, la = _attended(q, k_pages, v_pages, table, cu_rows, cache_pos, scale, lse)
+    n, T = head[4:6]
     if gate is not None:
-        ga, gdt = _rows(gate, "gate", dev, _DTYPES, q.shape), _DTYPES[gate.dtype]
+        ga, gdt = _rows(gate, "gate", dev, _DTYPES, shape), _DTYPES[gate.dtype]
     else:
         ga, gdt = (0, 8, 8), gattn.DTYPE_BF16
     if out is None:
-        out = _output(q.shape, q, stream)
-    oa = _rows(out, "out", dev, _BF16, q.shape)
+        out = _output(shape, q, stream)
+    oa = _rows(out, "out", dev, _BF16, shape)
     if workspace is None:
+        H, Hk, d = head[:3]
         size = gattn.paged_attention_workspace(H, Hk, d, n, T)
         workspace = _output((size // 2,), q, stream)
-    elif (workspace.get_device() != dev or workspace.dtype is not torch.uint8 or
-          not workspace.is_contiguous()):
+    elif (not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or
+          workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
         _refuse(workspace, "workspace", dev, (torch.uint8,), "bytes, contiguous")
     desc = gattn.gattn_paged_attention_desc.pack(
         *head, ga[0], gdt, ga[1], ga[2], oa[0], oa[1], oa[2], la, workspace.data_ptr(),
@@ -608,7 +610,7 @@ def paged_weights(q, k_pages, table, cu_rows, cache_pos, lse, *, scale=None, wei
 
     Arguments as there, lse as it left it; weights and weights_out fp32 [n][Hk][positions].
     weights None: zeros; weights_out None: into weights.  Returns weights_out."""
-    dev, head, la = _attended(q, k_pages, None, table, cu_rows, cache_pos, scale, lse)
+    dev, _, head, la = _attended(q, k_pages, None, table, cu_rows, cache_pos, scale, lse)
     n, T = head[4:6]
     if weights_out is None:
         weights_out = weights
@@ -639,15 +641,14 @@ def paged_evict(k_pages, v_pages, table, lengths, weights, *, keep, recent=0, ou
     lengths_out int32 [n])."""
     dev = k_pages.get_device()
     n = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else 0
-    pool = _pool(k_pages, v_pages, table, dev, n)
-    Hk, d = k_pages.shape[1], k_pages.shape[3]
+    (Hk, d), pool = _pool(k_pages, v_pages, table, dev, n)
     w = _received(weights, "weights", dev, n, Hk)
     wo = (0, 0, 0, 0) if weights_out is None else _received(weights_out, "weights_out", dev, n, Hk)
     ot = (0, 0, 0) if out_table is None else _table(out_table, "out_table", dev, n)
     if kept is None:
         kept = _output((n, Hk, keep), k_pages, stream, torch.int32)
-    elif (kept.get_device() != dev or kept.dtype is not torch.int32 or kept.shape != (n, Hk, keep) or
-          not kept.is_contiguous()):
+    elif (not isinstance(kept, torch.Tensor) or kept.get_device() != dev or
+          kept.dtype is not torch.int32 or kept.shape != (n, Hk, keep) or not kept.is_contiguous()):
         _refuse(kept, "kept", dev, _I32, (n, Hk, keep), "must be contiguous, of shape")
     if lengths_out is None:
         lengths_out = _output((n,), k_pages, stream, torch.int32)
