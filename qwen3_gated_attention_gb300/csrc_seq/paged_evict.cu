@@ -2,8 +2,9 @@
 // positions and, of the others, those with the most weight, moved to the front in order.
 //
 // One CTA per sequence and head finds the positions: the weight that the last kept one
-// has by a radix select on the ordered bits of the fp32 weights (11, 11 and 10 bits; the
-// first 32768 stay in shared memory), then the positions above it and the first of those
+// has by a radix select on the ordered bits of the fp32 weights (eight at a time; the
+// first 32768 stay in shared memory; a count for every bin and lane, because
+// weights fall into few bins of the first digits and lanes that meet there wait), then the positions above it and the first of those
 // that equal it, in order, by prefix sums.  Integer counts only, so the order of the
 // atomics does not matter.
 //
@@ -21,8 +22,8 @@ namespace {
 
 constexpr int kSel = 1024;             // threads that select
 constexpr int kCached = 32768;         // weights kept in shared memory
-constexpr int kBins = 2048;
-constexpr int kSmem = kCached * 4 + 2 * kBins * 4;
+constexpr int kBins = 256;
+constexpr int kSmem = kCached * 4 + kBins * 32 * 4;
 
 // Larger weights, larger numbers; a NaN counts as -infinity, both zeros as one.
 __device__ __forceinline__ uint32_t order_of(float w)
@@ -69,10 +70,12 @@ __device__ __forceinline__ int block_scan(int v, int *sums, int &total)
 
 __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constant__ PagedEvictArgs a)
 {
-    extern __shared__ uint32_t dyn[];
+    extern __shared__ __align__(16) uint32_t dyn[];
     __shared__ int sums[32];
-    __shared__ uint32_t chosen[2];
+    __shared__ int counts[kBins], chosen[2];
     uint32_t *const keys = dyn, *const hist = dyn + kCached;
+    // the rows' moves may be set up meanwhile
+    pdl_launch_dependents();
     const int hk = blockIdx.x % a.Hk, s = blockIdx.x / a.Hk, tid = threadIdx.x;
     const int len = a.lengths[s], m = kept_of(a, len);
     int *const kept = a.kept + ((long long)s * a.Hk + hk) * a.keep;
@@ -88,59 +91,114 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
     if (m <= 0)
         return;
     const int rec = min(a.recent, m), cand = len - rec, need = m - rec;
+    // the order of the candidates, eight loads of a thread on their way at a time
+    const int cached = min(cand, kCached);
+    for (int i0 = tid; i0 < cached; i0 += kSel * 8) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = i0 + e * kSel < cached ? w[i0 + e * kSel] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (i0 + e * kSel < cached)
+                keys[i0 + e * kSel] = order_of(v[e]);
+    }
+    __syncthreads();
+    // that of i .. i + 3, i a multiple of four
+    auto four = [&](int i, uint32_t (&k)[4]) {
+        if (i < kCached) {             // (what lies behind the last candidate is not used)
+            const uint4 x = *reinterpret_cast<const uint4 *>(keys + i);
+            k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                k[e] = order_of(i + e < cand ? w[i + e] : 0.f);
+        }
+    };
     uint32_t edge = 0;                 // of the last kept one
     int ties = cand;                   // how many of its equals are kept
     if (need < cand && need > 0) {
         uint32_t mask = 0;
         int left = need;
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-            for (int i = tid; i < 2 * kBins; i += kSel)
+        const int lane = tid & 31;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = tid; i < kBins * 32; i += kSel)
                 hist[i] = 0;
             __syncthreads();
-            // two counts a bin, by warp: weights fall into few bins of the first digit
-            uint32_t *const my = hist + ((tid >> 5) & 1) * kBins;
-            for (int i = tid; i < cand; i += kSel) {
-                const uint32_t k = pass > 0 && i < kCached ? keys[i] : order_of(w[i]);
-                if (pass == 0 && i < kCached)
-                    keys[i] = k;
-                if ((k & mask) == edge)
-                    atomicAdd(&my[(k >> shift) & (bins - 1)], 1u);
+            for (int i = tid * 4; i < cand; i += kSel * 4) {
+                uint32_t k[4];
+                four(i, k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((k[e] & mask) == edge && i + e < cand)
+                        atomicAdd(&hist[((k[e] >> shift) & (kBins - 1)) * 32 + lane], 1u);
             }
             __syncthreads();
-            // from the largest digit down, two bins a thread
-            const int hi = bins - 1 - 2 * tid;
-            const int c0 = hi >= 0 ? (int)(hist[hi] + hist[kBins + hi]) : 0;
-            const int c1 = hi > 0 ? (int)(hist[hi - 1] + hist[kBins + hi - 1]) : 0;
-            int all;
-            const int before = block_scan(c0 + c1, sums, all);
-            if (before < left && before + c0 >= left) {
-                chosen[0] = hi;
-                chosen[1] = left - before;
-            } else if (before + c0 < left && before + c0 + c1 >= left) {
-                chosen[0] = hi - 1;
-                chosen[1] = left - before - c0;
+            // four threads a bin, from banks that differ
+            const int bin = tid >> 2;
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                c += (int)hist[bin * 32 + (tid & 3) * 8 + ((i + bin) & 7)];
+            c += __shfl_xor_sync(0xffffffffu, c, 1);
+            c += __shfl_xor_sync(0xffffffffu, c, 2);
+            if ((tid & 3) == 0)
+                counts[bin] = c;
+            __syncthreads();
+            // from the largest digit down, eight bins a lane
+            if (tid < 32) {
+                const int top = kBins - 1 - 8 * lane;
+                int n[8], all = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    n[i] = counts[top - i];
+                    all += n[i];
+                }
+                int before = all;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o)
+                        before += x;
+                }
+                before -= all;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (before < left && before + n[i] >= left) {
+                        chosen[0] = top - i;
+                        chosen[1] = left - before;
+                    }
+                    before += n[i];
+                }
             }
             __syncthreads();
-            edge |= chosen[0] << shift;
-            mask |= (uint32_t)(bins - 1) << shift;
-            left = (int)chosen[1];
-            __syncthreads();
+            edge |= (uint32_t)chosen[0] << shift;
+            mask |= (uint32_t)(kBins - 1) << shift;
+            left = chosen[1];
         }
         ties = left;
     }
-    // the kept ones of the candidates in order: four positions a thread
+    // the kept ones of the candidates in order: four positions a thread.  Their weights
+    // are read a round ahead: in place a round writes in front of the next one only.
     int above = 0, equal = 0;
+    float v[4], nxt[4];
+    auto read = [&](int i, float (&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[e] = wo && i + e < cand ? w[i + e] : 0.f;
+    };
+    read(tid * 4, v);
     if (need > 0)
-        for (int base = 0; base < cand && (above + min(equal, ties)) < need; base += kSel * 4) {
+        for (int base = 0; base < cand && above + min(equal, ties) < need; base += kSel * 4) {
             const int i0 = base + tid * 4;
-            float v[4];
+            read(i0 + kSel * 4, nxt);
+            uint32_t k[4];
             int kind[4], c = 0;        // 1: above the edge, 1 << 16: equal to it
+            if (i0 < cand)
+                four(i0, k);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                v[e] = i0 + e < cand ? w[i0 + e] : 0.f;
-                const uint32_t k = order_of(v[e]);
-                kind[e] = i0 + e >= cand ? 0 : need == cand || k == edge ? 1 << 16 : k > edge ? 1 : 0;
+                kind[e] = i0 + e >= cand ? 0 : need == cand || k[e] == edge ? 1 << 16 : k[e] > edge ? 1 : 0;
                 c += kind[e];
             }
             int all;
@@ -155,6 +213,7 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
                         wo[j] = v[e];
                 }
                 at += kind[e];
+                v[e] = nxt[e];
             }
             above += all & 0xFFFF;
             equal += all >> 16;
@@ -194,6 +253,7 @@ constexpr int kMove = 256, kRows = 8;
 // Into other pages: a warp moves kRows (heads of 64 and 128: 4 or 2 times as many) rows.
 __global__ void __launch_bounds__(kMove) paged_move_kernel(const __grid_constant__ PagedEvictArgs a, int groups)
 {
+    pdl_wait();
     const int warp = (int)((blockIdx.x * (long long)kMove + threadIdx.x) >> 5) % groups, lane = threadIdx.x & 31;
     const int sh = (int)(((blockIdx.x * (long long)kMove + threadIdx.x) >> 5) / groups);
     if (sh >= a.n * a.Hk)
@@ -243,6 +303,7 @@ constexpr int kStep = 4, kChunk = kMove / 8 * kStep;
 
 __global__ void __launch_bounds__(kMove) paged_close_kernel(const __grid_constant__ PagedEvictArgs a)
 {
+    pdl_wait();
     const int slices = a.d / 64;
     int x = blockIdx.x;
     const int slice = x % slices;
@@ -305,15 +366,24 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t s)
     e = cudaLaunchKernelEx(&cfg, paged_select_kernel, a);
     if (e != cudaSuccess)
         return e;
-    if (!a.out_table)
-        return launch_seq(paged_close_kernel, dim3((unsigned)(a.n * a.Hk * 2 * (a.d / 64))), dim3(kMove), s, a);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(kMove);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (!a.out_table) {
+        cfg.gridDim = dim3((unsigned)(a.n * a.Hk * 2 * (a.d / 64)));
+        return cudaLaunchKernelEx(&cfg, paged_close_kernel, a);
+    }
     // kept rows, at most
     const long long most = a.keep < a.out_cap ? a.keep : a.out_cap;
     const int per = kRows * (a.d == 64 ? 4 : a.d == 128 ? 2 : 1);
     const int groups = (int)((most + per - 1) / per);
     const long long warps = (long long)groups * a.n * a.Hk;
-    return launch_seq(paged_move_kernel, dim3((unsigned)((warps + kMove / 32 - 1) / (kMove / 32))), dim3(kMove), s, a,
-                      groups);
+    cfg.gridDim = dim3((unsigned)((warps + kMove / 32 - 1) / (kMove / 32)));
+    return cudaLaunchKernelEx(&cfg, paged_move_kernel, a, groups);
 }
 
 }  // namespace gattn

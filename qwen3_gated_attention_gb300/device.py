@@ -224,9 +224,12 @@ def _refuse(t, name, dev, dtypes, shape, what="must have shape"):
 
 def _rows(t, name, dev, dtypes, shape=None):
     """(address, token stride, head stride) of a [rows][heads][elements] tensor."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes:
+    try:
+        if t.get_device() != dev or t.dtype not in dtypes:
+            _refuse(t, name, dev, dtypes, shape)
+        sh, st = t.shape, t.stride()
+    except AttributeError:
         _refuse(t, name, dev, dtypes, shape)
-    sh, st = t.shape, t.stride()
     if len(sh) != 3 or (shape is not None and sh != shape):
         _refuse(t, name, dev, dtypes, shape or "[rows][heads][elements]")
     if st[2] != 1 and sh[2] > 1:
@@ -237,9 +240,12 @@ def _rows(t, name, dev, dtypes, shape=None):
 
 def _planes(t, name, dev, dtypes, shape=None):
     """(address, token, head, batch stride) of a [batch][heads][tokens][elements] tensor."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes:
+    try:
+        if t.get_device() != dev or t.dtype not in dtypes:
+            _refuse(t, name, dev, dtypes, shape)
+        sh, st = t.shape, t.stride()
+    except AttributeError:
         _refuse(t, name, dev, dtypes, shape)
-    sh, st = t.shape, t.stride()
     if len(sh) != 4 or (shape is not None and sh != shape):
         _refuse(t, name, dev, dtypes, shape or "[batch][heads][tokens][elements]")
     if st[3] != 1 and sh[3] > 1:
@@ -253,18 +259,25 @@ def _flat(t, name, dev, dtypes, n):
     """Address of a contiguous vector of n entries; 0 for None."""
     if t is None:
         return 0
-    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype not in dtypes or
-            t.shape != (n,) or not t.is_contiguous()):
+    try:
+        if (t.get_device() != dev or t.dtype not in dtypes or t.shape != (n,) or
+                not t.is_contiguous()):
+            _refuse(t, name, dev, dtypes, f"[{n}], contiguous")
+    except AttributeError:
         _refuse(t, name, dev, dtypes, f"[{n}], contiguous")
     return t.data_ptr()
 
 
 def _cu(t, name, dev):
     """(address, sequences) of the row offsets."""
-    if (not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.int32 or
-            t.dim() != 1 or t.shape[0] < 1 or not t.is_contiguous()):
+    try:
+        sh = t.shape
+        if (t.get_device() != dev or t.dtype is not torch.int32 or len(sh) != 1 or sh[0] < 1 or
+                not t.is_contiguous()):
+            _refuse(t, name, dev, _I32, "[num_seqs + 1], contiguous")
+    except AttributeError:
         _refuse(t, name, dev, _I32, "[num_seqs + 1], contiguous")
-    return t.data_ptr(), t.shape[0] - 1
+    return t.data_ptr(), sh[0] - 1
 
 
 def _output(shape, like, stream, dtype=torch.bfloat16):
@@ -466,9 +479,12 @@ def delta_step(q, k, v, g, beta, cu_rows=None, *, num_seqs=None, state=None, sta
 
 def _table(t, name, dev, n):
     """(address, width, row stride) of a page table of n rows."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.int32:
+    try:
+        if t.get_device() != dev or t.dtype is not torch.int32:
+            _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
+        sh, st = t.shape, t.stride()
+    except AttributeError:
         _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
-    sh, st = t.shape, t.stride()
     if len(sh) != 2 or sh[0] != n or (st[1] != 1 and sh[1] > 1):
         _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
     return t.data_ptr(), sh[1], st[0] if n > 1 else max(sh[1], 1)
@@ -486,9 +502,12 @@ def _pool(k_pages, v_pages, table, dev, n):
 
 def _received(t, name, dev, n, Hk):
     """(address, width, sequence, head stride) of a weight tensor [n][Hk][positions]."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not torch.float32:
+    try:
+        if t.get_device() != dev or t.dtype is not torch.float32:
+            _refuse(t, name, dev, _F32, (n, Hk, "positions"))
+        sh, st = t.shape, t.stride()
+    except AttributeError:
         _refuse(t, name, dev, _F32, (n, Hk, "positions"))
-    sh, st = t.shape, t.stride()
     if len(sh) != 3 or sh[0] != n or sh[1] != Hk or (st[2] != 1 and sh[2] > 1):
         _refuse(t, name, dev, _F32, (n, Hk, "positions"))
     w = sh[2]
