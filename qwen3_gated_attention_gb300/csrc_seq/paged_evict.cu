@@ -2,11 +2,11 @@
 // positions and, of the others, those with the most weight, moved to the front in order.
 //
 // One CTA per sequence and head finds the positions: the weight that the last kept one
-// has by a radix select on the ordered bits of the fp32 weights (eight at a time; the
-// first 32768 stay in shared memory; a count for every bin and lane, because
-// weights fall into few bins of the first digits and lanes that meet there wait), then the positions above it and the first of those
-// that equal it, in order, by prefix sums.  Integer counts only, so the order of the
-// atomics does not matter.
+// has by a radix select on the ordered bits of the fp32 weights (eight at a time until 256
+// or fewer are alike; the first 32768 stay in shared memory; a count for every bin and
+// lane, because weights fall into few bins of the first digit and lanes that meet there
+// wait), then the positions above it and the first of those that equal it, in order, by
+// sums within warps.  Integer counts only, so the order of the atomics does not matter.
 //
 // Then the rows move, bound by memory.  Into other pages, rows are independent: a warp
 // takes kRows of them, all loads before the first store.  In place a row may land where
@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kSel = 1024;             // threads that select
 constexpr int kCached = 32768;         // weights kept in shared memory
-constexpr int kBins = 256;
+constexpr int kBins = 256, kList = 256;
 constexpr int kSmem = kCached * 4 + kBins * 32 * 4;
 
 // Larger weights, larger numbers; a NaN counts as -infinity, both zeros as one.
@@ -41,46 +41,18 @@ __device__ __forceinline__ int kept_of(const PagedEvictArgs &a, int len)
     return len < 0 || len > a.cap || m > a.out_cap ? -1 : m;
 }
 
-// Exclusive sum over the block's threads; `total` the sum of all.
-__device__ __forceinline__ int block_scan(int v, int *sums, int &total)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += x;
-    }
-    __syncthreads();                   // readers of the last call's sums
-    if (lane == 31)
-        sums[warp] = incl;
-    __syncthreads();
-    int x = sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    total = __shfl_sync(0xffffffffu, x, 31);
-    const int before = __shfl_sync(0xffffffffu, x, (warp + 31) & 31);
-    return incl - v + (warp ? before : 0);
-}
-
 __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constant__ PagedEvictArgs a)
 {
     extern __shared__ __align__(16) uint32_t dyn[];
-    __shared__ int sums[32];
-    __shared__ int counts[kBins], chosen[2];
+    __shared__ int counts[kBins], above_of[32], equal_of[32], chosen[3], listed;
+    __shared__ uint32_t list[kList];
     uint32_t *const keys = dyn, *const hist = dyn + kCached;
     // the rows' moves may be set up meanwhile
     pdl_launch_dependents();
-    const int hk = blockIdx.x % a.Hk, s = blockIdx.x / a.Hk, tid = threadIdx.x;
+    const int hk = blockIdx.x % a.Hk, s = blockIdx.x / a.Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int len = a.lengths[s], m = kept_of(a, len);
     int *const kept = a.kept + ((long long)s * a.Hk + hk) * a.keep;
     const float *const w = a.w + s * a.w_seq + hk * a.w_head;
-    float *const wo = a.w_out ? a.w_out + s * a.wo_seq + hk * a.wo_head : nullptr;
     for (int j = max(m, 0) + tid; j < a.keep; j += kSel)
         kept[j] = -1;
     if (hk == 0 && tid == 0) {
@@ -91,48 +63,58 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
     if (m <= 0)
         return;
     const int rec = min(a.recent, m), cand = len - rec, need = m - rec;
-    // the order of the candidates, eight loads of a thread on their way at a time
+    // the order of the candidates, sixteen loads of a thread on their way at a time
     const int cached = min(cand, kCached);
-    for (int i0 = tid; i0 < cached; i0 += kSel * 8) {
-        float v[8];
+    for (int i0 = tid; i0 < cached; i0 += kSel * 16) {
+        float v[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 16; ++e)
             v[e] = i0 + e * kSel < cached ? w[i0 + e * kSel] : 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 16; ++e)
             if (i0 + e * kSel < cached)
                 keys[i0 + e * kSel] = order_of(v[e]);
     }
+    if (tid < 4 && cached + tid < kCached)
+        keys[cached + tid] = 0u;       // orders are above zero: -infinity's is 0x7fffff
+    if (tid == 0)
+        listed = 0;
     __syncthreads();
-    // that of i .. i + 3, i a multiple of four
+    // the order of i .. i + 3, i a multiple of four; zeros behind the last candidate
     auto four = [&](int i, uint32_t (&k)[4]) {
-        if (i < kCached) {             // (what lies behind the last candidate is not used)
+        if (i < kCached) {
             const uint4 x = *reinterpret_cast<const uint4 *>(keys + i);
             k[0] = x.x, k[1] = x.y, k[2] = x.z, k[3] = x.w;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                k[e] = order_of(i + e < cand ? w[i + e] : 0.f);
+                k[e] = i + e < cand ? order_of(w[i + e]) : 0u;
+        }
+    };
+    // calls f for this thread's candidates
+    auto each = [&](auto f) {
+        for (int i = tid * 4; i < cand; i += kSel * 4) {
+            uint32_t k[4];
+            four(i, k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < cand)
+                    f(k[e]);
         }
     };
     uint32_t edge = 0;                 // of the last kept one
-    int ties = cand;                   // how many of its equals are kept
+    int ties = 0;                      // how many of its equals are kept
     if (need < cand && need > 0) {
         uint32_t mask = 0;
-        int left = need;
-        const int lane = tid & 31;
-        for (int shift = 24; shift >= 0; shift -= 8) {
+        int left = need, alike = cand; // of those with edge's first digits: to keep, and all
+        for (int shift = 24; shift >= 0 && alike > kList; shift -= 8) {
             for (int i = tid; i < kBins * 32; i += kSel)
                 hist[i] = 0;
             __syncthreads();
-            for (int i = tid * 4; i < cand; i += kSel * 4) {
-                uint32_t k[4];
-                four(i, k);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if ((k[e] & mask) == edge && i + e < cand)
-                        atomicAdd(&hist[((k[e] >> shift) & (kBins - 1)) * 32 + lane], 1u);
-            }
+            each([&](uint32_t k) {
+                if ((k & mask) == edge)
+                    atomicAdd(&hist[((k >> shift) & (kBins - 1)) * 32 + lane], 1u);
+            });
             __syncthreads();
             // four threads a bin, from banks that differ
             const int bin = tid >> 2;
@@ -146,7 +128,7 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
                 counts[bin] = c;
             __syncthreads();
             // from the largest digit down, eight bins a lane
-            if (tid < 32) {
+            if (warp == 0) {
                 const int top = kBins - 1 - 8 * lane;
                 int n[8], all = 0;
 #pragma unroll
@@ -167,6 +149,7 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
                     if (before < left && before + n[i] >= left) {
                         chosen[0] = top - i;
                         chosen[1] = left - before;
+                        chosen[2] = n[i];
                     }
                     before += n[i];
                 }
@@ -175,59 +158,123 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
             edge |= (uint32_t)chosen[0] << shift;
             mask |= (uint32_t)(kBins - 1) << shift;
             left = chosen[1];
+            alike = chosen[2];
+        }
+        if (mask != 0xffffffffu) {
+            // few are left: each counts those in front of it
+            each([&](uint32_t k) {
+                if ((k & mask) == edge)
+                    list[atomicAdd(&listed, 1)] = k;
+            });
+            __syncthreads();
+            if (tid < alike) {
+                const uint32_t k = list[tid];
+                int more = 0, same = 0;
+                for (int i = 0; i < alike; ++i) {
+                    more += list[i] > k;
+                    same += list[i] == k;
+                }
+                if (more < left && more + same >= left) {      // its equals write the same
+                    chosen[0] = (int)k;
+                    chosen[1] = left - more;
+                }
+            }
+            __syncthreads();
+            edge = (uint32_t)chosen[0];
+            left = chosen[1];
         }
         ties = left;
     }
-    // the kept ones of the candidates in order: four positions a thread.  Their weights
-    // are read a round ahead: in place a round writes in front of the next one only.
-    int above = 0, equal = 0;
-    float v[4], nxt[4];
-    auto read = [&](int i, float (&x)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            x[e] = wo && i + e < cand ? w[i + e] : 0.f;
-    };
-    read(tid * 4, v);
-    if (need > 0)
-        for (int base = 0; base < cand && above + min(equal, ties) < need; base += kSel * 4) {
-            const int i0 = base + tid * 4;
-            read(i0 + kSel * 4, nxt);
+    // the kept ones of the candidates in order: a run of them for each warp, which counts
+    // those above the edge and those equal to it, then writes behind the warps before it
+    if (need > 0) {
+        const int run = (cand + kSel * 4 - 1) / (kSel * 4) * 128, i0 = warp * run, i1 = min(cand, i0 + run);
+        // all are kept: every one is above an edge of zero
+        auto above = [&](uint32_t k) { return k > edge; };
+        auto equal = [&](uint32_t k) { return k == edge && k != 0u; };
+        int up = 0, eq = 0;
+        for (int i = i0 + lane * 4; i < i1; i += 128) {
             uint32_t k[4];
-            int kind[4], c = 0;        // 1: above the edge, 1 << 16: equal to it
-            if (i0 < cand)
-                four(i0, k);
+            four(i, k);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                kind[e] = i0 + e >= cand ? 0 : need == cand || k[e] == edge ? 1 << 16 : k[e] > edge ? 1 : 0;
-                c += kind[e];
+                up += above(k[e]);
+                eq += equal(k[e]);
             }
-            int all;
-            int at = block_scan(c, sums, all);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int up = above + (at & 0xFFFF), eq = equal + (at >> 16);
-                if (kind[e] == 1 || (kind[e] && eq < ties)) {
-                    const int j = up + min(eq, ties);
-                    kept[j] = i0 + e;
-                    if (wo)
-                        wo[j] = v[e];
-                }
-                at += kind[e];
-                v[e] = nxt[e];
-            }
-            above += all & 0xFFFF;
-            equal += all >> 16;
         }
-    // the newest; in place a weight may land where one of a later round is not yet read,
-    // never where one of this round or an earlier one is
-    for (int base = 0; base < rec; base += kSel) {
-        const int r = base + tid;
-        const float v = r < rec && wo ? w[len - rec + r] : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            up += __shfl_xor_sync(0xffffffffu, up, o);
+            eq += __shfl_xor_sync(0xffffffffu, eq, o);
+        }
+        if (lane == 0) {
+            above_of[warp] = up;
+            equal_of[warp] = eq;
+        }
         __syncthreads();
-        if (r < rec) {
-            kept[need + r] = len - rec + r;
-            if (wo)
-                wo[need + r] = v;
+        up = lane < warp ? above_of[lane] : 0;
+        eq = lane < warp ? equal_of[lane] : 0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            up += __shfl_xor_sync(0xffffffffu, up, o);
+            eq += __shfl_xor_sync(0xffffffffu, eq, o);
+        }
+        for (int j = i0; j < i1; j += 128) {
+            const int i = j + lane * 4;
+            uint32_t k[4] = {0u, 0u, 0u, 0u};
+            if (i < i1)
+                four(i, k);
+            int c = 0;                 // above, and equal from bit 16 on
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                c += above(k[e]) + (equal(k[e]) << 16);
+            int at = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o)
+                    at += x;
+            }
+            const int all = __shfl_sync(0xffffffffu, at, 31);
+            at -= c;
+            if (c) {
+                int u = up + (at & 0xFFFF), q = eq + (at >> 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (above(k[e]))
+                        kept[min(q, ties) + u++] = i + e;
+                    else if (equal(k[e])) {
+                        if (q < ties)
+                            kept[q + u] = i + e;
+                        ++q;
+                    }
+                }
+            }
+            up += all & 0xFFFF;
+            eq += all >> 16;
+        }
+    }
+    for (int r = tid; r < rec; r += kSel)
+        kept[need + r] = len - rec + r;
+    if (!a.w_out)
+        return;
+    // the weights follow.  In place a round reads all of its own before it writes, and what
+    // later rounds read lies behind what it writes.
+    float *const wo = a.w_out + s * a.wo_seq + hk * a.wo_head;
+    for (int base = 0; base < m; base += kSel * 4) {
+        __syncthreads();
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = base + e * kSel + tid;
+            v[e] = j < m ? w[kept[j]] : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = base + e * kSel + tid;
+            if (j < m)
+                wo[j] = v[e];
         }
     }
 }
