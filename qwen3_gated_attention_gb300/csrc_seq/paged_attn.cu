@@ -530,15 +530,17 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
 // it: ROWS rows a block, the parts dealt to the warps of a row, kFly of them on their
 // way at a time.  Bound by three dependent loads (the record, the parts, and what the
 // launch itself takes).
-constexpr int kJoin = 256, kFly = 5;
+constexpr int kJoin = 256;
 
 template <int M>
 constexpr int kJoinRows = M > 16 ? M / 16 : 1;
+template <int M>
+constexpr int kFlying = M > 32 ? 10 : 5;               // two warps a row, or four and eight
 
 template <int D, int M>
 __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant__ PagedAttnArgs a)
 {
-    constexpr int ROWS = kJoinRows<M>, W = kJoin / 32 / ROWS, N4 = (D + 127) / 128;
+    constexpr int ROWS = kJoinRows<M>, kFly = kFlying<M>, W = kJoin / 32 / ROWS, N4 = (D + 127) / 128;
     static_assert(W * 32 >= D / 4, "a thread finishes four columns");
     __shared__ float red_m[kJoin / 32], red_l[kJoin / 32];
     __shared__ float4 sums[kJoin / 32][D / 4];

@@ -298,24 +298,32 @@ __device__ __forceinline__ Place place_of(const PagedEvictArgs &a, const int *ro
 constexpr int kMove = 256, kRows = 8;
 
 // Into other pages: a warp moves kRows (heads of 64 and 128: 4 or 2 times as many) rows.
+// Blocks take the last rows of all sequences first: the newest positions and sequences
+// that keep everything need no selection, so they move while it runs (67 us -> .. us for eight
+// sequences of 9001 to 16384 positions, a quarter of the kept ones new).
 __global__ void __launch_bounds__(kMove) paged_move_kernel(const __grid_constant__ PagedEvictArgs a, int groups)
 {
-    pdl_wait();
-    const int warp = (int)((blockIdx.x * (long long)kMove + threadIdx.x) >> 5) % groups, lane = threadIdx.x & 31;
-    const int sh = (int)(((blockIdx.x * (long long)kMove + threadIdx.x) >> 5) / groups);
-    if (sh >= a.n * a.Hk)
-        return;
+    const int lane = threadIdx.x & 31, heads = a.n * a.Hk;
+    const long long job = (blockIdx.x * (long long)kMove + threadIdx.x) >> 5;
+    const int sh = (int)(job % heads), group = groups - 1 - (int)(job / heads);
     const int s = sh / a.Hk, hk = sh % a.Hk;
-    const int m = kept_of(a, a.lengths[s]);
+    const int len = a.lengths[s], m = kept_of(a, len);
     const int lpr = a.d == 64 ? 8 : a.d == 128 ? 16 : 32, per = 32 / lpr;
-    const int j0 = warp * kRows * per;
-    if (j0 >= m)
+    const int j0 = group * kRows * per;
+    if (group < 0 || j0 >= m) {
+        pdl_wait();
         return;
+    }
+    // the first row of the newest; with nothing left out all rows are where they were
+    const int need = m == len ? 0 : m - min(a.recent, m);
+    const bool known = j0 >= need;
+    if (!known)
+        pdl_wait();
     // a lane a row
     Place from{-1, 0}, to{-1, 0};
     const int mine = j0 + lane;
     if (lane < kRows * per && mine < m) {
-        from = place_of(a, a.pg.table + s * a.pg.table_stride, a.kept[(long long)sh * a.keep + mine]);
+        from = place_of(a, a.pg.table + s * a.pg.table_stride, known ? len - m + mine : a.kept[(long long)sh * a.keep + mine]);
         to = place_of(a, a.out_table + s * a.out_stride, mine);
         if (to.page < 0)
             from.page = -1;
@@ -343,6 +351,8 @@ __global__ void __launch_bounds__(kMove) paged_move_kernel(const __grid_constant
             *reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(vp) + page * a.pg.v.page + row * a.pg.v.tok) = v[i];
         }
     }
+    if (known)
+        pdl_wait();                    // no later work starts before the selection has ended
 }
 
 // In place: a CTA has 64 elements of the keys (or values) of one sequence and head.
