@@ -1,4 +1,5 @@
-"""Build libgattn.so (sm_103a) in-tree with nvcc, one process per translation unit.
+"""Build libgattn.so (sm_103a) in-tree with nvcc, one process per translation unit, and
+the module _paged beside it (tensor arguments of the paged-cache calls).
 
 Usage: ``python -m qwen3_gated_attention_gb300.build [--force] [--verbose-ptxas]``
 """
@@ -19,6 +20,9 @@ CSRC_SEQ = os.path.join(PKG, "csrc_seq")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgattn.so")
+# host code that reads torch tensors
+TENSORS = os.path.join(PKG, "csrc_torch", "paged_tensors.cpp")
+MODULE = os.path.join(PKG, "_paged.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -62,18 +66,54 @@ def _compile(src, nvcc, verbose_ptxas):
     return obj, None
 
 
+def _compile_module(src):
+    """The object of the tensor module (C++ against torch's headers, no CUDA)."""
+    import sysconfig
+
+    import torch
+    obj = os.path.join(BUILD, os.path.basename(src) + ".o")
+    dep = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "gattn.h"), __file__,
+                                            torch.__file__))
+    if os.path.exists(obj) and os.path.getmtime(obj) >= dep:
+        return obj, None
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE, "-I",
+           inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I",
+           sysconfig.get_paths()["include"], "-c", src, "-o", obj + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        return obj, f"{' '.join(cmd)}\n{r.stdout}\n{r.stderr}"
+    os.replace(obj + ".tmp", obj)
+    return obj, None
+
+
+def _link_module(obj):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MODULE + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libgattn.so", "-L",
+           lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MODULE)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     srcs = _sources()
     if force:
-        for s in srcs:
+        for s in srcs + [TENSORS]:
             o = os.path.join(BUILD, os.path.basename(s) + ".o")
             if os.path.exists(o):
                 os.remove(o)
-    with ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        tensors = ex.submit(_compile_module, TENSORS)
         results = list(ex.map(lambda s: _compile(s, nvcc, verbose_ptxas), srcs))
-    errors = [e for _, e in results if e]
+        tensors = tensors.result()
+    errors = [e for _, e in results + [tensors] if e]
     if errors:
         raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
     objs = [o for o, _ in results]
@@ -85,6 +125,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if (not os.path.exists(MODULE) or force or
+            os.path.getmtime(MODULE) < max(os.path.getmtime(LIB), os.path.getmtime(tensors[0]))):
+        _link_module(tensors[0])
     return LIB
 
 

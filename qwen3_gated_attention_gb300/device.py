@@ -473,45 +473,36 @@ def delta_step(q, k, v, g, beta, cu_rows=None, *, num_seqs=None, state=None, sta
 
 # ------------------------------------------------------------- paged caches
 #
-# Torch forms of the paged-cache entry points, as those above.  k_pages and v_pages are
-# bf16 [pages][Hk][page_size][d] views, table int32 [n][width] with contiguous rows:
-# position p of sequence s is row p % page_size of page table[s, p // page_size].
+# Torch forms of the paged-cache entry points, as those above; what reads and checks the
+# tensors is native (csrc_torch/paged_tensors.cpp).  k_pages and v_pages are bf16
+# [pages][Hk][page_size][d] views, table int32 [n][width] with contiguous rows: position p
+# of sequence s is row p % page_size of page table[s, p // page_size].
 
-def _table(t, name, dev, n):
-    """(address, width, row stride) of a page table of n rows."""
-    try:
-        if t.get_device() != dev or t.dtype is not torch.int32:
-            _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
-        sh, st = t.shape, t.stride()
-    except AttributeError:
-        _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
-    if len(sh) != 2 or sh[0] != n or (st[1] != 1 and sh[1] > 1):
-        _refuse(t, name, dev, _I32, f"[{n}][width], contiguous rows")
-    return t.data_ptr(), sh[1], st[0] if n > 1 else max(sh[1], 1)
+_calls = {}
 
 
-def _pool(k_pages, v_pages, table, dev, n):
-    """(Hk, d) and the fields of gattn_pages; v_pages None: keys only."""
-    kp, kt, kh, kb = _planes(k_pages, "k_pages", dev, _BF16)
-    pages, Hk, size, d = shape = k_pages.shape
-    vp, vt, vh, vb = ((0, 8, 8, 8) if v_pages is None else
-                      _planes(v_pages, "v_pages", dev, _BF16, shape))
-    ta, w, ts = _table(table, "table", dev, n)
-    return (Hk, d), (kp, vp, pages, size, kt, kh, kb, vt, vh, vb, ta, w, ts)
+def _native(name):
+    """A call of the module _paged, which is built with the library."""
+    gattn.lib()                       # says so if it is not
+    from . import _paged as module
+    return getattr(module, name)
 
 
-def _received(t, name, dev, n, Hk):
-    """(address, width, sequence, head stride) of a weight tensor [n][Hk][positions]."""
-    try:
-        if t.get_device() != dev or t.dtype is not torch.float32:
-            _refuse(t, name, dev, _F32, (n, Hk, "positions"))
-        sh, st = t.shape, t.stride()
-    except AttributeError:
-        _refuse(t, name, dev, _F32, (n, Hk, "positions"))
-    if len(sh) != 3 or sh[0] != n or sh[1] != Hk or (st[2] != 1 and sh[2] > 1):
-        _refuse(t, name, dev, _F32, (n, Hk, "positions"))
-    w = sh[2]
-    return t.data_ptr(), w, st[0] if n > 1 else Hk * w, st[1] if Hk > 1 else w
+def _paged(name, dev, stream, *args):
+    """Runs a call of the native module on a stream of the tensors' device."""
+    fn = _calls.get(name)
+    if fn is None:
+        fn = _calls[name] = _native(name)
+    if stream is None:
+        stream = 0 if dev < 0 else (_raw_stream(dev) if _raw_stream else
+                                    torch.cuda.current_stream(dev).cuda_stream)
+    if dev < 0 or _current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st:
+        gattn._check(st)
 
 
 def paged_rows(q, k, v, k_pages, v_pages, table, cu_rows, cache_pos, *, rope_theta,
@@ -524,40 +515,26 @@ def paged_rows(q, k, v, k_pages, v_pages, table, cu_rows, cache_pos, *, rope_the
     cu_rows int32 [n + 1], cache_pos int32 [n], positions int32 [T] (default: where the
     rows go).  rotary_dims defaults to d; rope_pairs turns neighbours.  rope_factor
     divides the frequencies; or rope_yarn is a dict of factor, original, beta_fast (32)
-    and beta_slow (1).  Returns q_out, bf16 [T][H][d]."""
-    dev = q.get_device()
-    qa = _rows(q, "q", dev, _DTYPES)
-    T, H, d = shape = q.shape
-    dtype = q.dtype
-    cu, n = _cu(cu_rows, "cu_rows", dev)
-    (Hk, dp), pool = _pool(k_pages, v_pages, table, dev, n)
-    if dp != d:
-        _refuse(k_pages, "k_pages", dev, _BF16, d, "must have q's head_dim")
-    ka = _rows(k, "k", dev, (dtype,), (T, Hk, d))
-    va = _rows(v, "v", dev, (dtype,), (T, Hk, d))
+    and beta_slow (1).  status int32 [1].  Returns q_out, bf16 [T][H][d]."""
     if q_out is None:
-        q_out = _output(shape, q, stream)
-    oa = _rows(q_out, "q_out", dev, _BF16, shape)
-    scaling, factor, original, fast, slow = gattn.ROPE_PLAIN, 1.0, 0, 0.0, 0.0
+        q_out = _output(q.shape, q, stream)
+    if rotary_dims is None:
+        rotary_dims = q.shape[-1]
     if rope_yarn is not None:
         if rope_factor is not None:
             raise ValueError("rope_factor is part of rope_yarn")
-        extra = rope_yarn.keys() - {"factor", "original", "beta_fast", "beta_slow"}
-        if extra or not {"factor", "original"} <= rope_yarn.keys():
+        if (not {"factor", "original"} <= rope_yarn.keys() or
+                rope_yarn.keys() - {"factor", "original", "beta_fast", "beta_slow"}):
             raise ValueError("rope_yarn takes factor, original, beta_fast and beta_slow")
-        scaling, factor, original = gattn.ROPE_YARN, rope_yarn["factor"], rope_yarn["original"]
-        fast, slow = rope_yarn.get("beta_fast", 32.0), rope_yarn.get("beta_slow", 1.0)
+        rope = (gattn.ROPE_YARN, rope_theta, rope_yarn["factor"], rope_yarn["original"],
+                rope_yarn.get("beta_fast", 32.0), rope_yarn.get("beta_slow", 1.0))
     elif rope_factor is not None:
-        scaling, factor = gattn.ROPE_LINEAR, rope_factor
-    desc = gattn.gattn_paged_rows_desc.pack(
-        H, Hk, d, d if rotary_dims is None else rotary_dims, 1 if rope_pairs else 0, scaling,
-        rope_theta, factor, original, fast, slow, rope_size, rms_eps, _DTYPES[dtype], n, T, cu,
-        _flat(cache_pos, "cache_pos", dev, _I32, n), _flat(positions, "positions", dev, _I32, T),
-        qa[0], ka[0], va[0], qa[1], qa[2], ka[1], ka[2], va[1], va[2],
-        _flat(q_norm, "q_norm", dev, _BF16, d), _flat(k_norm, "k_norm", dev, _BF16, d), oa[0],
-        oa[1], oa[2], *pool, _flat(status, "status", dev, _I32, 1))
-    if n and T:
-        _call(gattn.paged_rows, desc, dev, stream)
+        rope = (gattn.ROPE_LINEAR, rope_theta, rope_factor, 0, 0.0, 0.0)
+    else:
+        rope = (gattn.ROPE_PLAIN, rope_theta, 1.0, 0, 0.0, 0.0)
+    _paged("paged_rows", q.get_device(), stream, q, k, v, k_pages, v_pages, table, cu_rows, cache_pos,
+           positions, q_norm, k_norm, q_out, status, rotary_dims, 1 if rope_pairs else 0, *rope,
+           rope_size, rms_eps)
     return q_out
 
 
@@ -566,26 +543,6 @@ def paged_attention_workspace(q, k_pages, cu_rows):
     T, H, d = q.shape
     size = gattn.paged_attention_workspace(H, k_pages.shape[1], d, cu_rows.shape[0] - 1, T)
     return torch.empty(size, dtype=torch.uint8, device=q.device)
-
-
-def _attended(q, k_pages, v_pages, table, cu_rows, cache_pos, scale, lse):
-    """What attention and weights have in common: (device, q's shape, descriptor's head,
-    lse's address)."""
-    dev = q.get_device()
-    qa = _rows(q, "q", dev, _BF16)
-    T, H, d = shape = q.shape
-    cu, n = _cu(cu_rows, "cu_rows", dev)
-    (Hk, dp), pool = _pool(k_pages, v_pages, table, dev, n)
-    if dp != d:
-        _refuse(k_pages, "k_pages", dev, _BF16, d, "must have q's head_dim")
-    la = 0
-    if lse is not None:
-        if (not isinstance(lse, torch.Tensor) or lse.get_device() != dev or
-                lse.dtype is not torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
-            _refuse(lse, "lse", dev, _F32, f"[{T}][{H}], contiguous")
-        la = lse.data_ptr()
-    return dev, shape, (H, Hk, d, d ** -0.5 if scale is None else scale, n, T, cu,
-                        _flat(cache_pos, "cache_pos", dev, _I32, n), *qa, *pool), la
 
 
 def paged_attention(q, k_pages, v_pages, table, cu_rows, cache_pos, *, gate=None, scale=None,
@@ -597,28 +554,15 @@ def paged_attention(q, k_pages, v_pages, table, cu_rows, cache_pos, *, gate=None
     positions up to cache_pos[s] + i.  gate [T][H][d] fp32 or bf16 before its sigmoid, or
     None; lse fp32 [T][H] takes the softmax's log sums; workspace as
     paged_attention_workspace gives it (allocated for the call otherwise).  scale defaults
-    to d ** -0.5.  Returns out, bf16 [T][H][d]."""
-    dev, shape, head, la = _attended(q, k_pages, v_pages, table, cu_rows, cache_pos, scale, lse)
-    n, T = head[4:6]
-    if gate is not None:
-        ga, gdt = _rows(gate, "gate", dev, _DTYPES, shape), _DTYPES[gate.dtype]
-    else:
-        ga, gdt = (0, 8, 8), gattn.DTYPE_BF16
+    to d ** -0.5.  status int32 [1].  Returns out, bf16 [T][H][d]."""
     if out is None:
-        out = _output(shape, q, stream)
-    oa = _rows(out, "out", dev, _BF16, shape)
+        out = _output(q.shape, q, stream)
     if workspace is None:
-        H, Hk, d = head[:3]
-        size = gattn.paged_attention_workspace(H, Hk, d, n, T)
-        workspace = _output((size // 2,), q, stream)
-    elif (not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or
-          workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
-        _refuse(workspace, "workspace", dev, (torch.uint8,), "bytes, contiguous")
-    desc = gattn.gattn_paged_attention_desc.pack(
-        *head, ga[0], gdt, ga[1], ga[2], oa[0], oa[1], oa[2], la, workspace.data_ptr(),
-        workspace.nbytes, _flat(status, "status", dev, _I32, 1))
-    if n and T:
-        _call(gattn.paged_attention, desc, dev, stream)
+        T, H, d = q.shape
+        size = gattn.paged_attention_workspace(H, k_pages.shape[1], d, cu_rows.shape[0] - 1, T)
+        workspace = _output((size,), q, stream, torch.uint8)
+    _paged("paged_attention", q.get_device(), stream, q, k_pages, v_pages, table, cu_rows, cache_pos,
+           lse, scale, gate, out, workspace, status)
     return out
 
 
@@ -629,23 +573,10 @@ def paged_weights(q, k_pages, table, cu_rows, cache_pos, lse, *, scale=None, wei
 
     Arguments as there, lse as it left it; weights and weights_out fp32 [n][Hk][positions].
     weights None: zeros; weights_out None: into weights.  Returns weights_out."""
-    dev, _, head, la = _attended(q, k_pages, None, table, cu_rows, cache_pos, scale, lse)
-    n, T = head[4:6]
     if weights_out is None:
         weights_out = weights
-    wo, width, ws, wh = _received(weights_out, "weights_out", dev, n, head[1])
-    wi = 0
-    if weights is not None and weights is not weights_out:
-        wi, width_in, ws_in, wh_in = _received(weights, "weights", dev, n, head[1])
-        if (width_in, ws_in, wh_in) != (width, ws, wh):
-            _refuse(weights, "weights", dev, _F32, "must have weights_out's shape and strides:")
-    elif weights is not None:
-        wi = wo
-    desc = gattn.gattn_paged_weights_desc.pack(
-        *head, 0, 0, 8, 8, 0, 8, 8, la, 0, 0, _flat(status, "status", dev, _I32, 1), wi, wo, width,
-        ws, wh)
-    if n and T:
-        _call(gattn.paged_weights, desc, dev, stream)
+    _paged("paged_weights", q.get_device(), stream, q, k_pages, None, table, cu_rows, cache_pos, lse,
+           scale, weights, weights_out, status)
     return weights_out
 
 
@@ -658,23 +589,12 @@ def paged_evict(k_pages, v_pages, table, lengths, weights, *, keep, recent=0, ou
     those of the kept positions (may be weights).  out_table: pages that they move to,
     others than the table's; None: in place.  Returns (kept int32 [n][Hk][keep],
     lengths_out int32 [n])."""
-    dev = k_pages.get_device()
-    n = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else 0
-    (Hk, d), pool = _pool(k_pages, v_pages, table, dev, n)
-    w = _received(weights, "weights", dev, n, Hk)
-    wo = (0, 0, 0, 0) if weights_out is None else _received(weights_out, "weights_out", dev, n, Hk)
-    ot = (0, 0, 0) if out_table is None else _table(out_table, "out_table", dev, n)
     if kept is None:
-        kept = _output((n, Hk, keep), k_pages, stream, torch.int32)
-    elif (not isinstance(kept, torch.Tensor) or kept.get_device() != dev or
-          kept.dtype is not torch.int32 or kept.shape != (n, Hk, keep) or not kept.is_contiguous()):
-        _refuse(kept, "kept", dev, _I32, (n, Hk, keep), "must be contiguous, of shape")
+        if keep <= 0:
+            raise ValueError("keep must be > 0")
+        kept = _output((table.shape[0], k_pages.shape[1], keep), k_pages, stream, torch.int32)
     if lengths_out is None:
-        lengths_out = _output((n,), k_pages, stream, torch.int32)
-    desc = gattn.gattn_paged_evict_desc.pack(
-        Hk, d, n, keep, recent, *pool, *ot, _flat(lengths, "lengths", dev, _I32, n),
-        _flat(lengths_out, "lengths_out", dev, _I32, n), *w, *wo, kept.data_ptr(),
-        _flat(status, "status", dev, _I32, 1))
-    if n:
-        _call(gattn.paged_evict, desc, dev, stream)
+        lengths_out = _output((table.shape[0],), k_pages, stream, torch.int32)
+    _paged("paged_evict", k_pages.get_device(), stream, k_pages, v_pages, table, lengths, weights,
+           keep, recent, out_table, weights_out, kept, lengths_out, status)
     return kept, lengths_out

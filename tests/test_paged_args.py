@@ -153,48 +153,67 @@ def _t(shape, dtype=torch.bfloat16):
 
 
 def test_tensor_forms_refuse():
+    """What the tensors get wrong names the argument; all right otherwise, they lie on the CPU."""
     i32, f32 = torch.int32, torch.float32
     q, kv, pool, table = _t((3, 4, 64)), _t((3, 2, 64)), _t((5, 2, 16, 64)), _t((1, 3), i32)
     cu, pos = _t((2,), i32), _t((1,), i32)
-    ok = dict(rope_theta=1e4)
-    for args, kw in [
-            ((q, kv, kv, pool, pool, table, cu, pos), ok),                            # on the CPU
-            ((q, kv, kv, pool, pool[:4], table, cu, pos), ok),
-            ((q, kv, kv, pool.float(), pool, table, cu, pos), ok),
-            ((q, kv[:2], kv, pool, pool, table, cu, pos), ok),
-            ((q, kv, kv, pool, pool, table.long(), cu, pos), ok),
-            ((q, kv, kv, pool, pool, table[0], cu, pos), ok),
-            ((q, kv, kv, pool, pool, _t((2, 3), i32), cu, pos), ok),
-            ((q, kv, kv, pool, pool, _t((3, 1), i32).t(), cu, _t((2,), i32)), ok),
-            ((q, kv, kv, pool, pool, table, cu, pos), dict(ok, rope_factor=2.0, rope_yarn=dict(factor=2.0, original=8))),
-            ((q, kv, kv, pool, pool, table, cu, pos), dict(ok, rope_yarn=dict(factor=2.0))),
-            ((q, kv, kv, pool, pool, table, cu, pos), dict(ok, rope_yarn=dict(factor=2.0, original=8, mscale=1))),
-            ((q, kv, kv, pool, pool, table, cu, pos), dict(ok, positions=_t((2,), i32)))]:
-        with pytest.raises((ValueError, RuntimeError)):
-            device.paged_rows(*args, **kw)
+
+    def bad(fn, ok, text, *change, **kw):
+        args = list(ok)
+        for i, x in change:
+            args[i] = x
+        with pytest.raises(ValueError, match=text):
+            fn(*args, **kw)
+
+    rows = (q, kv, kv, pool, pool, table, cu, pos)
+    th = dict(rope_theta=1e4)
+    bad(device.paged_rows, rows, "CUDA device", **th)
+    out = _t((3, 4, 64))
+    for i, x, text in [(0, q.double(), "q has type"), (0, q[0], "q must have shape"), (0, q.transpose(1, 2), "q needs contiguous|k_pages must have"),
+                       (0, q.to_sparse(), "dense"), (1, kv[:2], "k must have shape"), (1, kv.float(), "k has type"),
+                       (1, 3, "k must be a tensor"), (2, _t((3, 3, 64)), "v must have shape"), (3, pool.float(), "k_pages has type"),
+                       (3, pool[0], "k_pages must have shape"), (3, _t((5, 2, 16, 128)), "v_pages must have k_pages"),
+                       (4, pool[:4], "v_pages must have k_pages"), (4, None, "v_pages must be a tensor"),
+                       (5, table.long(), "table has type"), (5, table[0], "table must have shape"),
+                       (5, _t((2, 3), i32), "table must have shape"), (5, _t((1, 6), i32)[:, ::2], "table must have shape"),
+                       (6, cu.long(), "cu_rows has type"), (6, cu[:0], "cu_rows must have shape"), (7, _t((2,), i32), "cache_pos must have shape"),
+                       (7, pos.float(), "cache_pos has type")]:
+        bad(device.paged_rows, rows, text, (i, x), q_out=out, rotary_dims=64, **th)
+    for kw, text in [(dict(rope_factor=2.0, rope_yarn=dict(factor=2.0, original=8)), "part of rope_yarn"),
+                     (dict(rope_yarn=dict(factor=2.0)), "rope_yarn takes"),
+                     (dict(rope_yarn=dict(factor=2.0, original=8, mscale=1)), "rope_yarn takes"),
+                     (dict(positions=_t((2,), i32)), "positions must have shape"), (dict(q_norm=_t((32,))), "q_norm must have shape"),
+                     (dict(k_norm=_t((64,), f32)), "k_norm has type"), (dict(q_out=_t((3, 4, 32))), "q_out must have shape"),
+                     (dict(q_out=out.float()), "q_out has type"), (dict(status=_t((2,), i32)), "status must have shape"),
+                     (dict(rotary_dims=1 << 40), "rotary_dims is out of range")]:
+        bad(device.paged_rows, rows, text, **dict(th, **kw))
+    with pytest.raises(TypeError):
+        device.paged_rows(*rows, rope_theta="1e4")
+    attn = (q, pool, pool, table, cu, pos)
     lse, w = _t((3, 4), f32), _t((1, 2, 48), f32)
-    for args, kw in [
-            ((q, pool, pool, table, cu, pos), {}),
-            ((q.float(), pool, pool, table, cu, pos), {}),
-            ((q, pool, pool, table, cu, pos), dict(lse=lse.t())),
-            ((q, pool, pool, table, cu, pos), dict(lse=lse[:2])),
-            ((q, pool, pool, table, cu, pos), dict(gate=q[..., :32])),
-            ((q, pool, pool, table, cu, pos), dict(workspace=lse)),
-            ((_t((3, 4, 128)), pool, pool, table, cu, pos), {})]:
-        with pytest.raises((ValueError, RuntimeError)):
-            device.paged_attention(*args, **kw)
-    for kw in [dict(weights=w), dict(), dict(weights=w[..., :40], weights_out=w), dict(weights=w.double()),
-               dict(weights=w[0])]:
-        with pytest.raises((ValueError, RuntimeError)):
-            device.paged_weights(q, pool, table, cu, pos, lse, **kw)
-    with pytest.raises((ValueError, RuntimeError)):
-        device.paged_weights(q, pool, table, cu, pos, None, weights=w)
-    for args, kw in [
-            ((pool, pool, table, pos, w), dict(keep=8)),
-            ((pool, pool, table, pos, w), dict(keep=8, kept=_t((1, 2, 7), i32))),
-            ((pool, pool, table, pos, w), dict(keep=8, lengths_out=_t((2,), i32))),
-            ((pool, pool, table, pos, w[:, :1]), dict(keep=8)),
-            ((pool, pool, table, 3, w), dict(keep=8)),
-            ((pool, pool, table, pos, w), dict(keep=8, out_table=table.long()))]:
-        with pytest.raises((ValueError, RuntimeError)):
-            device.paged_evict(*args, **kw)
+    bad(device.paged_attention, attn, "CUDA device")
+    bad(device.paged_attention, attn, "q has type", (0, q.float()), out=out)
+    bad(device.paged_attention, attn, "q's head_dim", (0, _t((3, 4, 128))))
+    for kw, text in [(dict(lse=_t((4, 3), f32).t()), "lse must have shape"), (dict(lse=lse[:2]), "lse must have shape"),
+                     (dict(lse=lse.double()), "lse has type"), (dict(gate=q[..., :32]), "gate must have shape"),
+                     (dict(gate=q.half()), "gate has type"), (dict(workspace=lse), "workspace has type"),
+                     (dict(workspace=_t((4, 4), torch.uint8).t()), "workspace must be contiguous"),
+                     (dict(out=out[:2]), "out must have shape")]:
+        bad(device.paged_attention, attn, text, **kw)
+    weigh = (q, pool, table, cu, pos, lse)
+    bad(device.paged_weights, weigh, "CUDA device", weights=w)
+    for kw, text in [(dict(), "weights_out must be a tensor"), (dict(weights=w[..., :40], weights_out=w), "weights_out's shape"),
+                     (dict(weights=w.double()), "weights_out has type"), (dict(weights=w[0]), "weights_out must have shape"),
+                     (dict(weights=_t((1, 3, 48), f32)), "weights_out must have shape"),
+                     (dict(weights_out=_t((1, 2, 96), f32)[..., ::2]), "weights_out must have shape")]:
+        bad(device.paged_weights, weigh, text, **kw)
+    bad(device.paged_weights, weigh, "lse must be a tensor", (5, None), weights=w)
+    evict = (pool, pool, table, pos, w)
+    bad(device.paged_evict, evict, "CUDA device", keep=8)
+    for kw, text in [(dict(keep=8, kept=_t((1, 2, 7), i32)), "kept must be"), (dict(keep=8, lengths_out=_t((2,), i32)), "lengths_out must"),
+                     (dict(keep=0), "keep must be"), (dict(keep=8, out_table=table.long()), "out_table has type"),
+                     (dict(keep=8, weights_out=w[:, :1]), "weights_out must have shape")]:
+        bad(device.paged_evict, evict, text, **kw)
+    bad(device.paged_evict, evict, "lengths must be a tensor", (3, 3), keep=8)
+    bad(device.paged_evict, evict, "weights must have shape", (4, w[:, :1]), keep=8)
+    bad(device.paged_evict, evict, "table must have shape", (2, _t((2, 3), i32)), keep=8)
