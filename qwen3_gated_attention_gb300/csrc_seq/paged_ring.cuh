@@ -79,6 +79,41 @@ __device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int m
     constexpr int NW = NT / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n = a.sq.n;
+    Run r;
+    // its share of a line of this length
+    auto share = [&](long long total) {
+        r.quota = total <= 0x7fffffff ? (long long)(((unsigned)total + gridDim.x - 1) / gridDim.x)
+                                      : (total + gridDim.x - 1) / gridDim.x;
+        r.quota = r.quota > min_units ? r.quota : min_units;
+        r.x0 = r.quota * blockIdx.x;
+        r.x1 = r.x0 + r.quota < total ? r.x0 + r.quota : total;
+        r.s = 0;
+        r.at = 0;
+    };
+    if (n <= 32) {
+        // every warp by itself, a lane a sequence
+        long long u = 0;
+        if (lane < n) {
+            bool bad;
+            const SeqUnits q = seq_units(a, lane, group, M, U, bad);
+            if (bad && warp == 0 && lane % gridDim.x == blockIdx.x)
+                skipped(lane, q);
+            u = q.all(a.Hk);
+        }
+        long long incl = u;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        share(__shfl_sync(0xffffffffu, incl, 31));
+        __syncthreads();                // (what the caller set up)
+        if (r.x0 < r.x1) {
+            r.s = __ffs(__ballot_sync(0xffffffffu, r.x0 < incl)) - 1;
+            r.at = __shfl_sync(0xffffffffu, incl - u, r.s);
+        }
+        return r;
+    }
     long long mine = 0, first = 0;
     for (int s = tid; s < n; s += NT) {
         bool bad;
@@ -99,13 +134,7 @@ __device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int m
     long long total = 0;
     for (int w = 0; w < NW; ++w)
         total += sums[w];
-    Run r;
-    r.quota = (total + gridDim.x - 1) / gridDim.x;
-    r.quota = r.quota > min_units ? r.quota : min_units;
-    r.x0 = r.quota * blockIdx.x;
-    r.x1 = r.x0 + r.quota < total ? r.x0 + r.quota : total;
-    r.s = 0;
-    r.at = 0;
+    share(total);
     if (r.x0 >= r.x1)
         return r;                       // the whole block
     long long before = 0;
