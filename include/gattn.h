@@ -31,6 +31,9 @@
  * attention masks (gattn_layer_set_mask; DS4Server issue 113, broadcast and
  * head-specific masks of the verify route).
  *
+ * Beside the layer stand operators without a handle, described where they are declared:
+ * packed sequences (prompts and the gated delta rule) and caches in pages.
+ *
  * Conventions for every entry point:
  *   - Pointers marked (device) are CUDA device addresses, (host) host memory.
  *   - Weights, caches, x, out and cache_pos are BORROWED: the library never

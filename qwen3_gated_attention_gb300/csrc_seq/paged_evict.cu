@@ -14,6 +14,11 @@
 // from j or behind), so a CTA walks down the kept rows in chunks, for a slice of 64
 // elements alone (slices do not meet), and stores a chunk only when every thread has
 // loaded it.
+//
+// Measured: eight sequences of 4000 to 16384 positions cut to 4096, 4 heads of 256, into other
+// pages: 52 us for 40 us of bytes (the selection alone takes 11 us on 32 SMs, the rows 45
+// us, 88 % of the copy rate).  One sequence of 2500 cut to 1024: 10.6 us, two launches
+// and the steps of the selection.
 #include "paged.cuh"
 
 namespace gattn {
@@ -299,8 +304,8 @@ constexpr int kMove = 256, kRows = 8;
 
 // Into other pages: a warp moves kRows (heads of 64 and 128: 4 or 2 times as many) rows.
 // Blocks take the last rows of all sequences first: the newest positions and sequences
-// that keep everything need no selection, so they move while it runs (67 us -> .. us for eight
-// sequences of 9001 to 16384 positions, a quarter of the kept ones new).
+// that keep everything need no selection, so they move while it runs (60 us -> 52 us for
+// eight sequences of 4000 to 16384 positions, a quarter of the 4096 kept ones new).
 __global__ void __launch_bounds__(kMove) paged_move_kernel(const __grid_constant__ PagedEvictArgs a, int groups)
 {
     const int lane = threadIdx.x & 31, heads = a.n * a.Hk;
