@@ -104,6 +104,24 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
 }
 
+// The rows of skipped sequences, by every thread of the grid.
+__device__ __noinline__ void zero_skipped(const PagedAttnArgs &a)
+{
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        seq_flag(a.sq, GATTN_STATUS_RANGE);
+    const int ch = a.d / 8, row16 = a.H * ch;           // 16-byte pieces of a head and a row
+    each_skipped(a, [&](int r0, int len) {
+        const long long step = (long long)gridDim.x * blockDim.x;
+        for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < (long long)len * row16; i += step) {
+            const long long row = r0 + i / row16;
+            const int x = (int)(i % row16), h = x / ch, c = x % ch;
+            *reinterpret_cast<uint4 *>(a.out + row * a.os.tok + h * a.os.head + c * 8) = make_uint4(0, 0, 0, 0);
+            if (c == 0 && a.lse)
+                a.lse[row * a.H + h] = -INFINITY;
+        }
+    });
+}
+
 template <int D, int RT>
 __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
     paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -131,17 +149,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
         prefetch_tensormap(&vmap);
     }
     // (the barriers of the plan make the ring's known)
-    const Run run = plan_run<C::THREADS, M, U>(a, group, min_units, [&](int, const SeqUnits &u) {
-        seq_flag(a.sq, GATTN_STATUS_RANGE);
-        for (long long i = 0; i < (long long)u.len * a.H; ++i) {
-            const long long row = u.r0 + i / a.H;
-            const int h = (int)(i % a.H);
-            for (int c = 0; c < D; c += 8)
-                *reinterpret_cast<uint4 *>(a.out + row * a.os.tok + h * a.os.head + c) = make_uint4(0, 0, 0, 0);
-            if (a.lse)
-                a.lse[row * a.H + h] = -INFINITY;
-        }
-    });
+    const Run run = plan_run<C::THREADS, M, U>(a, group, min_units);
+    if (run.bad)
+        zero_skipped(a);
     Rec *const recs = reinterpret_cast<Rec *>(static_cast<float *>(a.ws) + 2ll * kMaxCtas * kPartial<D, M>);
     if (run.x0 >= run.x1) {
         if (threadIdx.x == 0)

@@ -328,7 +328,9 @@ __global__ void __launch_bounds__(kMove) paged_move_kernel(const __grid_constant
     Place from{-1, 0}, to{-1, 0};
     const int mine = j0 + lane;
     if (lane < kRows * per && mine < m) {
-        from = place_of(a, a.pg.table + s * a.pg.table_stride, known ? len - m + mine : a.kept[(long long)sh * a.keep + mine]);
+        const int t = known ? len - m + mine : a.kept[(long long)sh * a.keep + mine];
+        if ((unsigned)t < (unsigned)len)
+            from = place_of(a, a.pg.table + s * a.pg.table_stride, t);
         to = place_of(a, a.out_table + s * a.out_stride, mine);
         if (to.page < 0)
             from.page = -1;
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kMove) paged_close_kernel(const __grid_constan
             if (j >= m)
                 continue;
             const int t = kept[j];
-            if (t == j)
+            if (t == j || (unsigned)t >= (unsigned)len)
                 continue;              // stays
             const Place f = place_of(a, row, t), o = place_of(a, row, j);
             if (f.page < 0 || o.page < 0)

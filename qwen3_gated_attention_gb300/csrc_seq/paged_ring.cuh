@@ -65,13 +65,13 @@ struct Run {
     long long x0, x1, quota;
     long long at;          // where sequence s begins
     int s;
+    bool bad;              // some sequence does not fit its table
 };
 
 // Called by every thread of the block (NT of them).  M: rows of a tile; 0: all rows
-// of a sequence are one tile.  `skipped` is called by one thread of one CTA for every
-// sequence that does not fit its table.
-template <int NT, int M, int U, class F>
-__device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int min_units, F skipped)
+// of a sequence are one tile.
+template <int NT, int M, int U>
+__device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int min_units)
 {
     __shared__ long long sums[32];
     __shared__ long long found_at;
@@ -93,13 +93,11 @@ __device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int m
     if (n <= 32) {
         // every warp by itself, a lane a sequence
         long long u = 0;
+        bool bad = false;
         if (lane < n) {
-            bool bad;
-            const SeqUnits q = seq_units(a, lane, group, M, U, bad);
-            if (bad && warp == 0 && lane % gridDim.x == blockIdx.x)
-                skipped(lane, q);
-            u = q.all(a.Hk);
+            u = seq_units(a, lane, group, M, U, bad).all(a.Hk);
         }
+        r.bad = __any_sync(0xffffffffu, bad);
         long long incl = u;
         for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -115,12 +113,11 @@ __device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int m
         return r;
     }
     long long mine = 0, first = 0;
+    bool any = false;
     for (int s = tid; s < n; s += NT) {
         bool bad;
-        const SeqUnits u = seq_units(a, s, group, M, U, bad);
-        if (bad && s % gridDim.x == blockIdx.x)
-            skipped(s, u);
-        mine += u.all(a.Hk);
+        mine += seq_units(a, s, group, M, U, bad).all(a.Hk);
+        any |= bad;
         if (s == tid)
             first = mine;
     }
@@ -130,7 +127,7 @@ __device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int m
         sums[warp] = mine;
     if (tid == 0)
         found = -1;
-    __syncthreads();
+    r.bad = __syncthreads_or(any);
     long long total = 0;
     for (int w = 0; w < NW; ++w)
         total += sums[w];
@@ -176,6 +173,23 @@ __device__ __forceinline__ Run plan_run(const PagedAttnArgs &a, int group, int m
     r.s = found;
     r.at = found_at;
     return r;
+}
+
+// Calls f(first row, rows) for the sequences that do not fit their tables, whole warps.
+template <class F>
+__device__ __forceinline__ void each_skipped(const PagedAttnArgs &a, F f)
+{
+    const int lane = threadIdx.x & 31;
+    for (int base = 0; base < a.sq.n; base += 32) {
+        SeqUnits u{};
+        bool bad = false;
+        if (base + lane < a.sq.n)
+            u = seq_units(a, base + lane, 1, 1, 1, bad);
+        for (unsigned m = __ballot_sync(0xffffffffu, bad); m; m &= m - 1) {
+            const int l = __ffs(m) - 1;
+            f(__shfl_sync(0xffffffffu, u.r0, l), __shfl_sync(0xffffffffu, u.len, l));
+        }
+    }
 }
 
 // ------------------------------------------------------------------ waiting
@@ -334,9 +348,11 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
         if (seg >= u.tiles * a.Hk) {
             do
                 u = seq_units(a, ++s, group, R::V ? M : 0, U, bad);
-            while (u.units == 0);
+            while (u.units == 0 && s + 1 < a.sq.n);
             seg = 0;
             v0 = 0;
+            if (u.units == 0)
+                break;                 // lengths that changed meanwhile
         }
         const int v1 = (int)min(run.x1 - x + v0, (long long)(u.units + kHead));
         const int u0 = max(v0 - kHead, 0), u1 = max(v1 - kHead, 0);

@@ -46,8 +46,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         ring.init();
         prefetch_tensormap(&kmap);
     }
-    const Run run = plan_run<C::THREADS, 0, U>(a, group, min_units,
-                                               [&](int, const SeqUnits &) { seq_flag(a.sq, GATTN_STATUS_RANGE); });
+    const Run run = plan_run<C::THREADS, 0, U>(a, group, min_units);
+    if (run.bad && blockIdx.x == 0 && threadIdx.x == 0)
+        seq_flag(a.sq, GATTN_STATUS_RANGE);
     if (run.x0 >= run.x1)
         return;
     if (warp >= CW) {

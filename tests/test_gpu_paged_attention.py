@@ -193,6 +193,18 @@ def test_sequences_that_do_not_fit_their_table():
     assert (out[1:] == 0).all() and (lse[1:] == -math.inf).all()
 
 
+def test_a_long_prompt_that_does_not_fit():
+    """Its rows are zeroed by the whole grid, beside sequences that do fit."""
+    c = _case(4, 2, 64, 16, [1, 300, 1], [20, 0, 9], seed=12)
+    big = 200000
+    c["lens"], c["cu"] = [1, big, 1], cu_of([1, big, 1])
+    c["q"] = torch.randn(big + 2, 4, 64).to(BF)
+    c["gate"] = torch.randn(big + 2, 4, 64).to(BF)
+    out, lse, st = _run(c)
+    assert st == 1 and (out[1:-1] == 0).all() and (lse[1:-1] == -math.inf).all()
+    _check(c, out, lse, seqs={0, 2})
+
+
 def test_peaked_scores():
     """Scores of very different sizes: the reference moves often, and far."""
     c = _case(8, 2, 128, 16, [1, 3], [500, 77], seed=6)
