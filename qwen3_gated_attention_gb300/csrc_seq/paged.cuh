@@ -76,6 +76,26 @@ struct PagedEvictArgs {
     unsigned *status;
 };
 
+// Launches that may be set up while the work before them on the stream ends: each of
+// these kernels waits for it (pdl_wait) before it touches memory, in every block, and lets
+// the next one be set up after that (pdl_launch_dependents).  So a kernel that has started
+// behind one of them knows that all work before that one has ended too.
+template <class... K, class... A>
+inline cudaError_t launch_paged(void (*f)(K...), dim3 grid, dim3 block, int smem, cudaStream_t s, A &&...args)
+{
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, f, static_cast<A &&>(args)...);
+}
+
 cudaError_t launch_paged_rows(const PagedRowsArgs &a, int x_f32, cudaStream_t s);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, cudaStream_t s);
 cudaError_t launch_paged_weights(const PagedAttnArgs &a, cudaStream_t s);

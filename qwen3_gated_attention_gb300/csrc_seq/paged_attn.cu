@@ -148,6 +148,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
     }
+    pdl_wait();
+    pdl_launch_dependents();
     // (the barriers of the plan make the ring's known)
     const Run run = plan_run<C::THREADS, M, U>(a, group, min_units);
     if (run.bad)
@@ -263,7 +265,6 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             if (lane == 0)
                 mbar_arrive(&ring.qempty[b]);
         }
-        pdl_launch_dependents();
         return;
     }
     // --------------------------------------------------------------- consumers
@@ -543,7 +544,6 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             }
         }
     }
-    pdl_launch_dependents();
 }
 
 // Joins the parts of the segment that begins in CTA blockIdx.x's run and goes on behind
@@ -567,6 +567,7 @@ __global__ void __launch_bounds__(kJoin) paged_join_kernel(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rl = warp / W, w = warp % W;
     const float *const ws = static_cast<const float *>(a.ws);
     pdl_wait();
+    pdl_launch_dependents();
     const Rec rec = reinterpret_cast<const Rec *>(ws + 2ll * kMaxCtas * kPartial<D, M>)[blockIdx.x];
     const int i = blockIdx.y * ROWS + rl;
     if (!rec.live || blockIdx.y * ROWS >= rec.nrows)
@@ -694,24 +695,10 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
     if (!encode_pages(&km, a.pg, false, a.Hk, D, box) || !encode_pages(&vm, a.pg, true, a.Hk, D, box))
         return cudaErrorInvalidValue;
     const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = s;
-    e = cudaLaunchKernelEx(&cfg, fn, a, km, vm, 4);
+    e = launch_paged(fn, dim3(grid), dim3(C::THREADS), C::SMEM, s, a, km, vm, 4);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t join = {};
-    join.gridDim = dim3(grid, C::M / kJoinRows<C::M>);
-    join.blockDim = dim3(kJoin);
-    join.stream = s;
-    join.attrs = at;
-    join.numAttrs = 1;
-    return cudaLaunchKernelEx(&join, paged_join_kernel<D, C::M>, a);
+    return launch_paged(paged_join_kernel<D, C::M>, dim3(grid, C::M / kJoinRows<C::M>), dim3(kJoin), 0, s, a);
 }
 
 template <int D>

@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
     __shared__ int counts[kBins], above_of[32], equal_of[32], chosen[3], listed;
     __shared__ uint32_t list[kList];
     uint32_t *const keys = dyn, *const hist = dyn + kCached;
-    // the rows' moves may be set up meanwhile
+    // the rows' moves start meanwhile, but not before what came before this kernel has ended
+    pdl_wait();
     pdl_launch_dependents();
     const int hk = blockIdx.x % a.Hk, s = blockIdx.x / a.Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int len = a.lengths[s], m = kept_of(a, len);
@@ -422,32 +423,18 @@ cudaError_t launch_paged_evict(const PagedEvictArgs &a, cudaStream_t s)
     cudaError_t e = allow_smem(paged_select_kernel, kSmem, done);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.n * a.Hk));
-    cfg.blockDim = dim3(kSel);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = s;
-    e = cudaLaunchKernelEx(&cfg, paged_select_kernel, a);
+    e = launch_paged(paged_select_kernel, dim3((unsigned)(a.n * a.Hk)), dim3(kSel), kSmem, s, a);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(kMove);
-    cfg.dynamicSmemBytes = 0;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (!a.out_table) {
-        cfg.gridDim = dim3((unsigned)(a.n * a.Hk * 2 * (a.d / 64)));
-        return cudaLaunchKernelEx(&cfg, paged_close_kernel, a);
-    }
+    if (!a.out_table)
+        return launch_paged(paged_close_kernel, dim3((unsigned)(a.n * a.Hk * 2 * (a.d / 64))), dim3(kMove), 0, s, a);
     // kept rows, at most
     const long long most = a.keep < a.out_cap ? a.keep : a.out_cap;
     const int per = kRows * (a.d == 64 ? 4 : a.d == 128 ? 2 : 1);
     const int groups = (int)((most + per - 1) / per);
     const long long warps = (long long)groups * a.n * a.Hk;
-    cfg.gridDim = dim3((unsigned)((warps + kMove / 32 - 1) / (kMove / 32)));
-    return cudaLaunchKernelEx(&cfg, paged_move_kernel, a, groups);
+    return launch_paged(paged_move_kernel, dim3((unsigned)((warps + kMove / 32 - 1) / (kMove / 32))), dim3(kMove), 0, s, a,
+                        groups);
 }
 
 }  // namespace gattn

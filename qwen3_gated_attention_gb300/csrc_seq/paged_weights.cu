@@ -46,6 +46,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         ring.init();
         prefetch_tensormap(&kmap);
     }
+    pdl_wait();
+    pdl_launch_dependents();
     const Run run = plan_run<C::THREADS, 0, U>(a, group, min_units);
     if (run.bad && blockIdx.x == 0 && threadIdx.x == 0)
         seq_flag(a.sq, GATTN_STATUS_RANGE);
@@ -191,12 +193,7 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t s)
     CUtensorMap km;
     if (!encode_pages(&km, a.pg, false, a.Hk, D, 1 << box_log2(a.pg.page, C::U)))
         return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sms < kMaxCtas ? sms : kMaxCtas);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, fn, a, km, 4);
+    return launch_paged(fn, dim3(sms < kMaxCtas ? sms : kMaxCtas), dim3(C::THREADS), C::SMEM, s, a, km, 4);
 }
 
 }  // namespace

@@ -83,6 +83,10 @@ prompt_rows_kernel(const __grid_constant__ std::conditional_t<PAGED, PagedRowsAr
     constexpr int NA = FORM == kSwap ? 8 : 4;       // angles of a lane
     __shared__ float2 table[kWarps][128];
     __shared__ float swap[FORM == kSwap ? kWarps : 1][256];
+    if constexpr (PAGED) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long job = (long long)blockIdx.x * kWarps + warp;
     const int t = (int)(job / parts), part = (int)(job % parts);
@@ -326,7 +330,10 @@ static cudaError_t launch_rows(void (*fn)(const Args, int), const Args &a, int x
         parts *= 2;
     const long long jobs = (long long)a.sq.total * parts;
     const dim3 grid((unsigned)((jobs + kWarps - 1) / kWarps)), block(kWarps * 32);
-    return launch_seq(fn, grid, block, s, a, parts);
+    if constexpr (std::is_same_v<Args, PagedRowsArgs>)
+        return launch_paged(fn, grid, block, 0, s, a, parts);
+    else
+        return launch_seq(fn, grid, block, s, a, parts);
 }
 
 cudaError_t launch_prompt_rows(const PromptRowsArgs &a, int x_f32, cudaStream_t s)
