@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
     }
+    // (no early start for the join: its blocks would sit on the SMs that are done first, 1 us
+    // more for a verify step)
     pdl_wait();
-    pdl_launch_dependents();
     // (the barriers of the plan make the ring's known)
     const Run run = plan_run<C::THREADS, M, U>(a, group, min_units);
     if (run.bad)
