@@ -46,7 +46,7 @@ template <int D, int RT>
 struct Cfg {
     // warps: consumers, joining ones (a tile of eight rows a warp joins nothing and
     // finishes its own), producers; twelve have 168 registers each
-    static constexpr int M = 8 * RT, CW = RT == 1 ? 4 : 8, NS = CW / RT, NE = RT == 8 ? 0 : 2;
+    static constexpr int M = 8 * RT, CW = RT == 1 ? 4 : 8, NS = CW / RT, NE = RT == 8 ? 0 : RT == 1 ? 4 : 2;
     static constexpr int NP = RT == 1 || RT == 8 ? 4 : 2;
     static constexpr int THREADS = (CW + NE + NP) * 32;
     // columns that are handed over at once: what leaves the ring enough slots
@@ -204,6 +204,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
     };
     auto columns = [&](const Part &p, int e0, int r, const uint4 (&gate)[ITEMS]) {
         float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
+        // all sums before the first store, which the loads might not pass
+        float4 sum[ITEMS];
 #pragma unroll
         for (int q = 0; q < ITEMS; ++q) {
             const int i = q * 32 + lane, row = e0 + i / (DR / 4), c = i % (DR / 4) * 4;
@@ -215,11 +217,16 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
                 o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
                 o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
             }
+            sum[q] = o;
+        }
+#pragma unroll
+        for (int q = 0; q < ITEMS; ++q) {
+            const int i = q * 32 + lane, row = e0 + i / (DR / 4), c = i % (DR / 4) * 4;
             if (row < p.nrows) {
                 if (p.whole)
-                    finish4(a, row_out[row] + r * DR + c, o, row_l[row], gate[q]);
+                    finish4(a, row_out[row] + r * DR + c, sum[q], row_l[row], gate[q]);
                 else
-                    *reinterpret_cast<float4 *>(slot + row * D + r * DR + c) = o;
+                    *reinterpret_cast<float4 *>(slot + row * D + r * DR + c) = sum[q];
             }
         }
     };

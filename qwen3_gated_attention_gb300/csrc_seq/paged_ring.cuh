@@ -340,10 +340,25 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
     int s = run.s;
     bool bad;
     SeqUnits u = seq_units(a, s, group, R::V ? M : 0, U, bad);
-    int seg = (int)((run.x0 - run.at) / (u.units + kHead));
-    int v0 = (int)((run.x0 - run.at) % (u.units + kHead));       // place in the segment, its head counted
-    // pages of 32 boxes of sequence tab_s, one a lane
+    // first segment, and place in it, its head counted
+    const long long off = run.x0 - run.at;
+    const unsigned length = u.units + kHead;
+    int seg = off >> 32 ? (int)(off / length) : (int)((unsigned)off / length);
+    int v0 = (int)(off - (long long)seg * length);
+    // pages of 32 boxes of sequence tab_s, one a lane; not looked at before they are used,
+    // so that the load is on its way meanwhile
     int tab_s = -1, tab_b = 0, tab_page = 0, tab_y = 0;
+    auto window = [&](int b0) {
+        if (tab_s == s && b0 >= tab_b && b0 < tab_b + 32)
+            return;
+        tab_s = s;
+        tab_b = b0 & ~31;
+        const int t = (tab_b + lane) << btl;
+        tab_page = -1;
+        if (t < u.p0 + u.len)
+            tab_page = a.pg.table[s * a.pg.table_stride + t / a.pg.page];
+        tab_y = t % a.pg.page;
+    };
     for (long long x = run.x0; x < run.x1 && !stop;) {
         if (seg >= u.tiles * a.Hk) {
             do
@@ -379,6 +394,9 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
             p.whole = whole;
             p.slot = x == run.x0 ? 0 : 1;
             p.pass = min(pass, 1);
+            const int n0 = p.u0 + ((pw - it) & (R::NP - 1));            // this warp's first unit
+            if (n0 < p.u1)
+                window(n0 * NB);
             if (pw == 0) {
                 if (!ring_wait(&ring.qempty[b], (uint32_t)((parts >> 1) & 1) ^ 1u, &ring.abort, a.sq))
                     stop = true;
@@ -389,23 +407,9 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
             }
             // ---- this warp's units
             const int count = max(p.u1 - p.u0, 0);
-            for (int n = p.u0 + ((pw - it) & (R::NP - 1)); n < p.u1; n += R::NP) {
+            for (int n = n0; n < p.u1; n += R::NP) {
                 const int b0 = n * NB;
-                if (tab_s != s || b0 < tab_b || b0 >= tab_b + 32) {
-                    tab_s = s;
-                    tab_b = b0 & ~31;
-                    const int t = (tab_b + lane) << btl;
-                    int page = -1;
-                    if (t < u.p0 + u.len) {
-                        page = a.pg.table[s * a.pg.table_stride + t / a.pg.page];
-                        if (page < 0 || page >= a.pg.pages) {
-                            page = -1;
-                            seq_flag(a.sq, GATTN_STATUS_RANGE);
-                        }
-                    }
-                    tab_page = page;
-                    tab_y = t % a.pg.page;
-                }
+                window(b0);
                 if (lane == 0 && !ring_wait(&ring.empty[slot], phase ^ 1, &ring.abort, a.sq))
                     stop = true;
                 stop = __any_sync(0xffffffffu, stop);
@@ -413,22 +417,26 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
                     break;
                 // boxes that hold positions of the sequence
                 const int nb = min(NB, ((u.p0 + u.len - n * U) + BT - 1) >> btl);
-                const unsigned there = __ballot_sync(0xffffffffu, tab_page >= 0);
+                const unsigned there = __ballot_sync(0xffffffffu, (unsigned)tab_page < (unsigned)a.pg.pages);
+                const unsigned ok = (there >> (b0 - tab_b)) & ((1u << nb) - 1u);
                 // a lane a box; a page that does not exist is one behind the last: zeros
                 const int from = b0 - tab_b + lane;
                 const int page = __shfl_sync(0xffffffffu, tab_page, from & 31);
                 const int y = __shfl_sync(0xffffffffu, tab_y, from & 31);
                 if (lane == 0) {
-                    ring.ok[slot] = (there >> (b0 - tab_b)) & ((1u << nb) - 1u);
+                    ring.ok[slot] = ok;
+                    if (ok != (1u << nb) - 1u)
+                        seq_flag(a.sq, GATTN_STATUS_RANGE);
                     mbar_arrive_expect_tx(&ring.full[slot], nb * box_bytes * (R::V ? 2 : 1));
                 }
                 __syncwarp();
                 if (lane < nb) {
                     const uint32_t dst = smem_u32(units) + slot * R::UNIT + lane * box_bytes;
                     const uint32_t bar = smem_u32(&ring.full[slot]);
-                    box_g2s(dst, kmap, y, hk, page < 0 ? a.pg.pages : page, bar, pol);
+                    const int from_page = ok >> lane & 1u ? page : a.pg.pages;
+                    box_g2s(dst, kmap, y, hk, from_page, bar, pol);
                     if (R::V)
-                        box_g2s(dst + R::PLANE, vmap, y, hk, page < 0 ? a.pg.pages : page, bar, pol);
+                        box_g2s(dst + R::PLANE, vmap, y, hk, from_page, bar, pol);
                 }
                 ++issued;
                 slot += R::NP;
