@@ -16,8 +16,8 @@
 // loaded it.
 //
 // Measured: eight sequences of 4000 to 16384 positions cut to 4096, 4 heads of 256, into other
-// pages: 52 us for 40 us of bytes (the selection alone takes 11 us on 32 SMs, the rows 45
-// us, 88 % of the copy rate).  One sequence of 2500 cut to 1024: 10.6 us, two launches
+// pages: 53 us for 40 us of bytes (the selection alone takes 11 us on 32 SMs, the rows 45
+// us, 88 % of the copy rate).  One sequence of 2500 cut to 1024: 10.5 us, two launches
 // and the steps of the selection.
 #include "paged.cuh"
 

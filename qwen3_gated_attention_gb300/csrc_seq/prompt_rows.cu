@@ -17,8 +17,8 @@
 // page table, the pairs (y_i, y_j) may be neighbours, the norms may be absent, the angles
 // may come from positions of their own, and cos and sin carry a factor.  8240 rows of 32 +
 // 8 + 8 heads of 256 into pages of 16: 78 us, 78 % of the copy rate; 2766 fp32 rows of 16 +
-// 8 + 8 heads of 128, neighbours turned: 17.4 us (58 %; 692 CTAs are 1.1 times what fits
-// at once, and more warps a row cost more than they fill); 8 single rows: 4.8 us.
+// 8 + 8 heads of 128, neighbours turned: 17.7 us (58 %; 692 CTAs are 1.1 times what fits
+// at once, and more warps a row cost more than they fill); 8 single rows: 4.6 us.
 #include "paged.cuh"
 
 namespace gattn {
