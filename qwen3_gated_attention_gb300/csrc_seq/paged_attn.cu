@@ -345,16 +345,29 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             sc[c][q][e] = 0.f;
+                // step i: 16 elements k of 16 positions q; four loads ahead of their products
+                constexpr int STEPS = D / 16 * (U / 16), AHEAD = 4;
+                uint32_t ak[2][AHEAD][4];
+                auto keys = [&](int i, uint32_t (&r)[4]) {
+                    const int k = i / (U / 16), q = i % (U / 16);
+                    ldsm_x4(r, ks + ((q * 16) >> btl) * box + (k >> 2) * dbs + ((q * 16) & ((1 << btl) - 1)) * 128 + ka +
+                                   ((((2 * k + kc) & 7) ^ (lane & 7)) << 4));
+                };
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
+                for (int x = 0; x < AHEAD; ++x)
+                    keys(x, ak[0][x]);
 #pragma unroll
-                    for (int q = 0; q < U / 16; ++q) {
-                        const int in = (q * 16) >> btl, at = (q * 16) & ((1 << btl) - 1);
-                        uint32_t ak[4];
-                        ldsm_x4(ak, ks + in * box + (k >> 2) * dbs + at * 128 + ka +
-                                        ((((2 * k + kc) & 7) ^ (lane & 7)) << 4));
-                        mma(sc[k % CHAINS][q], ak, qf[k][0], qf[k][1]);
+                for (int i = 0; i < STEPS; i += AHEAD) {
+                    if (i + AHEAD < STEPS)
+#pragma unroll
+                        for (int x = 0; x < AHEAD; ++x)
+                            keys(i + AHEAD + x, ak[(i / AHEAD + 1) & 1][x]);
+#pragma unroll
+                    for (int x = 0; x < AHEAD; ++x) {
+                        const int k = (i + x) / (U / 16), q = (i + x) % (U / 16);
+                        mma(sc[k % CHAINS][q], ak[(i / AHEAD) & 1][x], qf[k][0], qf[k][1]);
                     }
+                }
 #pragma unroll
                 for (int q = 0; q < U / 16; ++q)
 #pragma unroll
@@ -440,25 +453,30 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
                 }
                 // ---- O += V p, four loads ahead of their products
                 if (!odd) {
-                    constexpr int AHEAD = 4;
+                    // step i: 16 positions q, 16 elements j
+                    auto values = [&](int i, uint32_t (&r)[4]) {
+                        const int q = i / (D / 16), j = i % (D / 16);
+                        ldsm_x4_trans(r, vs + ((q * 16) >> btl) * box + (j >> 2) * dbs + ((q * 16) & ((1 << btl) - 1)) * 128 + va +
+                                             ((((2 * j + vc) & 7) ^ (lane & 7)) << 4));
+                    };
 #pragma unroll
-                    for (int q = 0; q < U / 16; ++q) {
-                        const int in = (q * 16) >> btl, at = (q * 16) & ((1 << btl) - 1);
-                        const uint32_t vrow = vs + in * box + at * 128 + va;
+                    for (int x = 0; x < AHEAD; ++x)
+                        values(x, ak[0][x]);
 #pragma unroll
-                        for (int j0 = 0; j0 < D / 16; j0 += AHEAD) {
-                            uint32_t av[AHEAD][4];
-#pragma unroll
-                            for (int x = 0; x < AHEAD; ++x) {
-                                const int j = j0 + x;
-                                ldsm_x4_trans(av[x], vrow + (j >> 2) * dbs + ((((2 * j + vc) & 7) ^ (lane & 7)) << 4));
-                            }
-#pragma unroll
-                            for (int x = 0; x < AHEAD; ++x)
-                                mma(O[j0 + x], av[x], hi[q][0], hi[q][1]);
+                    for (int i = 0; i < STEPS; i += AHEAD) {
+                        if (i + AHEAD < STEPS)
 #pragma unroll
                             for (int x = 0; x < AHEAD; ++x)
-                                mma(O[j0 + x], av[x], lo[q][0], lo[q][1]);
+                                values(i + AHEAD + x, ak[(i / AHEAD + 1) & 1][x]);
+#pragma unroll
+                        for (int x = 0; x < AHEAD; ++x) {
+                            const int q = (i + x) / (D / 16);
+                            mma(O[(i + x) % (D / 16)], ak[(i / AHEAD) & 1][x], hi[q][0], hi[q][1]);
+                        }
+#pragma unroll
+                        for (int x = 0; x < AHEAD; ++x) {
+                            const int q = (i + x) / (D / 16);
+                            mma(O[(i + x) % (D / 16)], ak[(i / AHEAD) & 1][x], lo[q][0], lo[q][1]);
                         }
                     }
                 } else {
