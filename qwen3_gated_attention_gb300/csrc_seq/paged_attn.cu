@@ -28,8 +28,10 @@
 // over 2: 51 us, of which the join takes 6 and the start 3.  64 sequences of 211 to 4200,
 // 16 heads of 64 over 8, in pages of 16: 52 us, 5.0 TB/s (2 KB a copy; CTAs whose copies
 // are slow end 10 us after the others).  Eight sequences of four drafted rows, 24 heads over
-// 2: 55 us for 20 us of bytes: 48 rows are six warps of eight, two of them on one scheduler,
-// whose matrix instructions take 1536 of the 2200 cycles that 32 positions take.  One token
+// 2: 50 us for 20 us of bytes: 48 rows are six warps of eight, two of them on one scheduler;
+// for 32 positions its matrix instructions take 1536 cycles, and so do the reads of keys and
+// values that every warp makes from shared memory (rows loaded anew for each unit instead
+// of kept in registers change nothing).  One token
 // over 1004 positions: 9.4 us, two launches and five dependent loads.
 #include <cudaTypedefs.h>
 
