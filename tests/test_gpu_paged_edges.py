@@ -261,3 +261,103 @@ def test_equal_bits_from_equal_calls(H, lens):
         if first is None:
             first = got
         assert all(torch.equal(a, b) for a, b in zip(first, got)), i
+
+
+def test_captured_behind_copies_and_other_streams():
+    """In a graph the calls follow copies, fills and work of another stream that joins, and
+    precede such; each finds what came before it finished."""
+    s = _state(6, 12)
+    src = {k: torch.randn_like(s[k].float()).to(BF) for k in ("q", "k", "v", "gate")}
+    eager = _clone(s)
+
+    def go(x, side):
+        for k in ("q", "k"):
+            x[k].copy_(src[k])              # a copy node
+        x["w"].zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for k in ("v", "gate"):
+                x[k].copy_(src[k])
+                x[k].mul_(0.5)
+        torch.cuda.current_stream().wait_stream(side)
+        first = _step(x)
+        x["pos"].add_(1)
+        x["q"].copy_(first)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):       # beside the next step's rows
+            twice = first * 2
+        second = _step(x)
+        torch.cuda.current_stream().wait_stream(side)
+        return first, twice, second
+
+    side = torch.cuda.Stream()
+    warm = torch.cuda.Stream()
+    with torch.cuda.stream(warm):
+        go(_clone(s), side)
+    torch.cuda.synchronize()
+    want = go(eager, side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    keep = _clone(s)
+    with torch.cuda.graph(graph):
+        got = go(s, side)
+    for _ in range(3):
+        for k, v in keep.items():
+            s[k].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and _same(s, eager)
+
+
+def test_calls_in_a_row_without_waiting():
+    """A chain of small calls, each set up while the one before it ends, against the same
+    with a wait after every call."""
+    a = _state(3, 13, width=30)
+    b = _clone(a)
+    d = _dev()
+    outs = [[], []]
+    for x, wait, out in ((a, False, outs[0]), (b, True, outs[1])):
+        length = x["pos"].clamp(min=60)
+        x["pos"].copy_(length)
+        for i in range(40):
+            out.append(_step(x))
+            if wait:
+                torch.cuda.synchronize()
+            x["pos"].add_(1)
+            if i % 8 == 7:
+                kept, lens = d.paged_evict(x["kp"], x["vp"], x["table"], x["pos"], x["w"], keep=55, recent=11,
+                                           weights_out=x["w"])
+                if wait:
+                    torch.cuda.synchronize()
+                x["pos"].copy_(lens)
+                out.append(kept)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*outs)) and _same(a, b)
+
+
+def test_the_longest_table():
+    """2^24 positions, in pages that repeat: as many keys as pages differ, each counted."""
+    Hk, d, P = 1, 64, 16
+    g = torch.Generator().manual_seed(14)
+    kp, vp = (pool(4, Hk, P, d, g) for _ in range(2))
+    width = (1 << 24) // P
+    table = (torch.arange(width, dtype=torch.int32) % 4)[None].contiguous()
+    q = torch.randn(1, 4, d, generator=g).to(BF)
+    lse = torch.empty(1, 4, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    past = (1 << 24) - 1
+    out = _dev().paged_attention(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), _i32([0, 1]), _i32([past]), lse=lse, status=st)
+    k, v = (x[:, 0].reshape(-1, d).double() for x in (kp, vp))
+    s = (k @ q[0].double().t()).t() / 8
+    p = torch.softmax(s, -1)
+    want, weight = p @ v, p @ v.abs()
+    e = score_error(d, float((k.abs() @ q[0].double().abs().t()).max()) / 8, 1.0, 25.0)
+    # a CTA adds 2^24 / 152 terms, in runs of 64: 2^-14 more than the shorter ones
+    assert ((out[0].cpu().double() - want).abs() <= attention_bound(want, weight, e) + 2.0 ** -14 * weight).all()
+    assert (lse[0].cpu().double() - torch.logsumexp(s, -1) - torch.log(torch.tensor(2.0 ** 18))).abs().max() < 2.0 ** -13
+    w = _dev().paged_weights(q.cuda(), kp.cuda(), table.cuda(), _i32([0, 1]), _i32([past]), lse,
+                             weights_out=torch.zeros(1, 1, 1 << 24, device="cuda"), status=st)
+    got = w.view(-1, 64).double().sum(0).cpu()
+    assert (got - p.sum(0)).abs().max() < 4 * 2.0 ** -12 and int(st) == 0
+    _dev().paged_attention(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), _i32([0, 1]), _i32([past + 1]), status=st)
+    assert int(st) == 1
