@@ -730,9 +730,9 @@ gattn_status gattn_delta_step(const gattn_delta_desc *desc, gattn_stream stream)
 /*
  * ---------------------------------------------------------------------------
  * A key-value cache in pages: decoding for a server that hands out cache memory in
- * pages, beside the contiguous caches above.  (The pages of the reference keep one
- * contiguous cache per layer, Atlas LayerKvCache; pages, scaled frequencies and
- * eviction have no counterpart there.)
+ * pages, beside the contiguous caches above.  (The reference has one contiguous cache
+ * a layer, Atlas LayerKvCache: a cache in pages, scaled frequencies and eviction have no
+ * counterpart there.)
  *
  * Position p of sequence s is row p % page_size of page table[s][p / page_size] of two
  * pools; element (page, hk, row, j) of the keys at

@@ -16,8 +16,8 @@
 // loaded it.
 //
 // Measured: eight sequences of 4000 to 16384 positions cut to 4096, 4 heads of 256, into other
-// pages: 53 us for 40 us of bytes (the selection alone takes 11 us on 32 SMs, the rows 45
-// us, 88 % of the copy rate).  One sequence of 2500 cut to 1024: 10.5 us, two launches
+// pages: 52 us for 40 us of bytes (the selection alone takes 10 us on 32 SMs, the rows 45
+// us, 88 % of the copy rate).  One sequence of 2500 cut to 1024: 9.8 us, two launches
 // and the steps of the selection.
 #include "paged.cuh"
 
@@ -46,6 +46,9 @@ __device__ __forceinline__ int kept_of(const PagedEvictArgs &a, int len)
     return len < 0 || len > a.cap || m > a.out_cap ? -1 : m;
 }
 
+// Whether the rows' moves take the weights along.
+__device__ __forceinline__ bool weights_move(const PagedEvictArgs &a) { return a.out_table && a.w_out != a.w; }
+
 __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constant__ PagedEvictArgs a)
 {
     extern __shared__ __align__(16) uint32_t dyn[];
@@ -69,8 +72,15 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
     if (m <= 0)
         return;
     const int rec = min(a.recent, m), cand = len - rec, need = m - rec;
-    // the order of the candidates, sixteen loads of a thread on their way at a time
+    auto clear = [&] {
+        for (int i = tid; i < kBins * 32; i += kSel)
+            hist[i] = 0;
+        __syncthreads();
+    };
+    // the order of the candidates, sixteen loads of a thread on their way at a time, and how
+    // many have which first digit
     const int cached = min(cand, kCached);
+    clear();
     for (int i0 = tid; i0 < cached; i0 += kSel * 16) {
         float v[16];
 #pragma unroll
@@ -78,9 +88,14 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
             v[e] = i0 + e * kSel < cached ? w[i0 + e * kSel] : 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            if (i0 + e * kSel < cached)
-                keys[i0 + e * kSel] = order_of(v[e]);
+            if (i0 + e * kSel < cached) {
+                const uint32_t k = order_of(v[e]);
+                keys[i0 + e * kSel] = k;
+                atomicAdd(&hist[(k >> 24) * 32 + lane], 1u);
+            }
     }
+    for (int i = kCached + tid; i < cand; i += kSel)
+        atomicAdd(&hist[(order_of(w[i]) >> 24) * 32 + lane], 1u);
     if (tid < 4 && cached + tid < kCached)
         keys[cached + tid] = 0u;       // orders are above zero: -infinity's is 0x7fffff
     if (tid == 0)
@@ -114,14 +129,14 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
         uint32_t mask = 0;
         int left = need, alike = cand; // of those with edge's first digits: to keep, and all
         for (int shift = 24; shift >= 0 && alike > kList; shift -= 8) {
-            for (int i = tid; i < kBins * 32; i += kSel)
-                hist[i] = 0;
-            __syncthreads();
-            each([&](uint32_t k) {
-                if ((k & mask) == edge)
-                    atomicAdd(&hist[((k >> shift) & (kBins - 1)) * 32 + lane], 1u);
-            });
-            __syncthreads();
+            if (shift < 24) {
+                clear();
+                each([&](uint32_t k) {
+                    if ((k & mask) == edge)
+                        atomicAdd(&hist[((k >> shift) & (kBins - 1)) * 32 + lane], 1u);
+                });
+                __syncthreads();
+            }
             // four threads a bin, from banks that differ
             const int bin = tid >> 2;
             int c = 0;
@@ -262,10 +277,11 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
     }
     for (int r = tid; r < rec; r += kSel)
         kept[need + r] = len - rec + r;
-    if (!a.w_out)
-        return;
-    // the weights follow.  In place a round reads all of its own before it writes, and what
+    // the weights follow: where rows move to other pages, with them, but for weights in
+    // place.  In place a round reads all of its own before it writes, and what
     // later rounds read lies behind what it writes.
+    if (!a.w_out || weights_move(a))
+        return;
     float *const wo = a.w_out + s * a.wo_seq + hk * a.wo_head;
     for (int base = 0; base < m; base += kSel * 4) {
         __syncthreads();
@@ -330,8 +346,11 @@ __global__ void __launch_bounds__(kMove) paged_move_kernel(const __grid_constant
     const int mine = j0 + lane;
     if (lane < kRows * per && mine < m) {
         const int t = known ? len - m + mine : a.kept[(long long)sh * a.keep + mine];
-        if ((unsigned)t < (unsigned)len)
+        if ((unsigned)t < (unsigned)len) {
             from = place_of(a, a.pg.table + s * a.pg.table_stride, t);
+            if (a.w_out && weights_move(a))
+                a.w_out[s * a.wo_seq + hk * a.wo_head + mine] = a.w[s * a.w_seq + hk * a.w_head + t];
+        }
         to = place_of(a, a.out_table + s * a.out_stride, mine);
         if (to.page < 0)
             from.page = -1;
