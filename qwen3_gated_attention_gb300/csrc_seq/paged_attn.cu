@@ -46,18 +46,19 @@ namespace {
 // RT: tiles of eight rows.
 template <int D, int RT>
 struct Cfg {
-    // warps: consumers, joining ones (a tile of eight rows a warp joins nothing and
-    // finishes its own), producers; twelve have 168 registers each
-    static constexpr int M = 8 * RT, CW = RT == 1 ? 4 : 8, NS = CW / RT, NE = RT == 8 ? 0 : RT == 1 ? 4 : 2;
-    static constexpr int NP = RT == 1 || RT == 8 ? 4 : 2;
+    // warps: consumers, joining ones (WIDE: none, the consumers join), producers; twelve
+    // have 168 registers each
+    static constexpr bool WIDE = RT == 8;
+    static constexpr int M = 8 * RT, CW = RT == 1 ? 4 : 8, NS = CW / RT, NE = WIDE ? 0 : RT == 1 ? 4 : 2;
+    static constexpr int NP = RT == 2 ? 2 : 4;
     static constexpr int THREADS = (CW + NE + NP) * 32;
     // columns that are handed over at once: what leaves the ring enough slots
-    static constexpr int DR = RT <= 2 || D == 64 ? D : RT == 4 ? D / 2 : 64, ROUNDS = D / DR;
+    static constexpr int DR = WIDE ? 64 : D, ROUNDS = D / DR;
     static constexpr int XROW = DR + 4;                // floats of a row: two rows 8 banks apart
     static constexpr int XB = CW * 8 * XROW * 4;
     static constexpr int ER = NE ? M / NE : 8;         // rows of a warp that finishes them
     static constexpr int ITEMS = ER * (DR / 4) / 32;   // of its lanes, four columns each
-    static constexpr int U = kUnit<D> * (RT == 8 ? 2 : 1), UNIT = U * D * 4;
+    static constexpr int U = kUnit<D> * (WIDE ? 2 : 1), UNIT = U * D * 4;
     static constexpr int FIXED = 2 * M * D * 2 + XB + 4096 + 1024;
     static constexpr int FIT = (227 * 1024 - FIXED) / UNIT, STEP = NS > NP ? NS : NP;
     static constexpr int SLOTS = (FIT > 12 ? 12 : FIT) / STEP * STEP;
@@ -132,10 +133,11 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
     using C = Cfg<D, RT>;
     using R = typename C::R;
     constexpr int M = C::M, NS = C::NS, CW = C::CW, NE = C::NE, U = C::U, DR = C::DR;
+    constexpr bool WIDE = C::WIDE;
     extern __shared__ uint8_t raw[];
     __shared__ R ring;
     __shared__ float red_m[CW * 8], red_l[CW * 8];   // of the consumers' rows
-    __shared__ float fac[NS][M], row_l[M];             // the joining warps' own
+    __shared__ float fac[CW * 8], row_l[M];            // what the joining warps make of them
     __shared__ long long row_out[M], row_gate[M], row_lse[M];   // where their rows are
     __shared__ uint64_t xfull, xempty;                 // the hand-over buffer
     uint8_t *units = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
     const int group = a.H / a.Hk;
     if (threadIdx.x == 0) {
         mbar_init(&xfull, CW);
-        mbar_init(&xempty, NE ? NE : 1);
+        mbar_init(&xempty, WIDE ? CW : NE);
         ring.init();
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
@@ -172,69 +174,87 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             recs[blockIdx.x] = rec;
         return;
     }
-    // The finished rows of a part, ER of them by one warp from row e0 on, DR columns at a
-    // time: places() first, then gates() before and columns() after they are in xb.
-    constexpr int ER = C::ER, ITEMS = C::ITEMS;
-    auto places = [&](const Part &p, int e0) {
+    // The finished rows of a part: `er` of them (C::ER, or fewer in a wide tile) by one warp
+    // from row e0 on, DR columns at a time: places() first, then gates() before, sums() and
+    // columns() after they are in xb, where `ns` groups have left `rows` rows each.  What a
+    // warp keeps of its rows is its own: in a wide tile the next part's rows are others.
+    constexpr int ITEMS = C::ITEMS;
+    const int mine = WIDE ? warp * 8 : (warp - CW) * C::ER;            // its first place
+    auto places = [&](const Part &p, int e0, int er) {
         const int h = p.hf + e0 + lane, head = p.hk * group + h % group;        // a lane a row
         const long long to = p.r0 + p.rowf + h / group;
-        if (lane < ER) {
-            row_out[e0 + lane] = to * a.os.tok + head * a.os.head;
-            row_gate[e0 + lane] = to * a.gs.tok + head * a.gs.head;
-            row_lse[e0 + lane] = to * a.H + head;
+        if (lane < er) {
+            row_out[mine + lane] = to * a.os.tok + head * a.os.head;
+            row_gate[mine + lane] = to * a.gs.tok + head * a.gs.head;
+            row_lse[mine + lane] = to * a.H + head;
         }
         __syncwarp();
     };
-    auto gates = [&](const Part &p, int e0, int r, uint4 (&gate)[ITEMS]) {
+    auto gates = [&](const Part &p, int e0, int er, int r, uint4 (&gate)[ITEMS]) {
 #pragma unroll
         for (int q = 0; q < ITEMS; ++q) {
             const int i = q * 32 + lane, row = e0 + i / (DR / 4);
             gate[q] = make_uint4(0, 0, 0, 0);
-            if (p.whole && a.gate && row < p.nrows)
-                gate[q] = gate4(a, row_gate[row] + r * DR + i % (DR / 4) * 4);
+            if (p.whole && a.gate && row < p.nrows && i < er * (DR / 4))
+                gate[q] = gate4(a, row_gate[mine + row - e0] + r * DR + i % (DR / 4) * 4);
         }
     };
-    auto sums_of = [&](const Part &p, int row, float top, float sum) {
-        float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
-        row_l[row] = sum;
-        if (!p.whole) {
-            slot[M * D + row] = top;
-            slot[M * D + M + row] = sum;
-        } else if (a.lse && row < p.nrows) {
-            a.lse[row_lse[row]] = lse_of(top, sum);
+    auto sums = [&](const Part &p, int e0, int er, int ns, int rows) {
+        if (lane < er) {
+            float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
+            const int row = e0 + lane;
+            float top = -INFINITY, sum = 0.f;
+            for (int q = 0; q < ns; ++q)
+                top = fmaxf(top, red_m[q * rows + row]);
+            for (int q = 0; q < ns; ++q) {
+                const float f = red_m[q * rows + row] == top ? 1.f : exp2f(red_m[q * rows + row] - top);
+                sum = fmaf(f, red_l[q * rows + row], sum);
+                fac[mine + q * (WIDE ? er : M) + lane] = f;
+            }
+            row_l[mine + lane] = sum;
+            if (!p.whole) {
+                slot[M * D + row] = top;
+                slot[M * D + M + row] = sum;
+            } else if (a.lse && row < p.nrows) {
+                a.lse[row_lse[mine + lane]] = lse_of(top, sum);
+            }
         }
+        __syncwarp();
     };
-    auto columns = [&](const Part &p, int e0, int r, const uint4 (&gate)[ITEMS]) {
+    auto columns = [&](const Part &p, int e0, int er, int ns, int rows, int r, const uint4 (&gate)[ITEMS]) {
         float *const slot = static_cast<float *>(a.ws) + (2ll * blockIdx.x + p.slot) * kPartial<D, M>;
         // all sums before the first store, which the loads might not pass
         float4 sum[ITEMS];
 #pragma unroll
         for (int q = 0; q < ITEMS; ++q) {
             const int i = q * 32 + lane, row = e0 + i / (DR / 4), c = i % (DR / 4) * 4;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            sum[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < er * (DR / 4))
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const float4 v = *reinterpret_cast<const float4 *>(xb + (n * M + row) * C::XROW + c);
-                const float f = NS == 1 ? 1.f : fac[n][row];
-                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
-                o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
-            }
-            sum[q] = o;
+                for (int n = 0; n < (WIDE ? CW : NS); ++n) {
+                    if (WIDE && n >= ns)
+                        break;
+                    const float4 v = *reinterpret_cast<const float4 *>(xb + (n * rows + row) * C::XROW + c);
+                    const float f = fac[mine + n * (WIDE ? er : M) + row - e0];
+                    sum[q].x = fmaf(f, v.x, sum[q].x), sum[q].y = fmaf(f, v.y, sum[q].y);
+                    sum[q].z = fmaf(f, v.z, sum[q].z), sum[q].w = fmaf(f, v.w, sum[q].w);
+                }
         }
 #pragma unroll
         for (int q = 0; q < ITEMS; ++q) {
             const int i = q * 32 + lane, row = e0 + i / (DR / 4), c = i % (DR / 4) * 4;
-            if (row < p.nrows) {
+            if (row < p.nrows && i < er * (DR / 4)) {
                 if (p.whole)
-                    finish4(a, row_out[row] + r * DR + c, sum[q], row_l[row], gate[q]);
+                    finish4(a, row_out[mine + row - e0] + r * DR + c, sum[q], row_l[mine + row - e0], gate[q]);
                 else
                     *reinterpret_cast<float4 *>(slot + row * D + r * DR + c) = sum[q];
             }
         }
+        __syncwarp();
     };
     if (NE && warp >= CW) {
         // ------------------------------------------------------- the joining warps
-        const int e0 = (warp - CW) * ER;
+        const int e0 = (warp - CW) * C::ER;
         uint32_t xr = 0;                                // hand-overs so far
         for (int parts = 0;; ++parts) {
             const int b = parts & 1;
@@ -243,32 +263,16 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             const Part p = ring.part[b];
             if (!p.live)
                 break;
-            places(p, e0);
+            places(p, e0, C::ER);
 #pragma unroll 1
             for (int r = 0; r < C::ROUNDS; ++r, ++xr) {
                 uint4 gate[ITEMS];                      // come while the consumers work
-                gates(p, e0, r, gate);
+                gates(p, e0, C::ER, r, gate);
                 if (!ring_wait(&xfull, xr & 1, &ring.abort, a.sq))
                     return;
-                if (r == 0) {
-                    if (lane < ER) {
-                        const float *const rm = red_m + e0 + lane, *const rl = red_l + e0 + lane;   // M apart by group
-                        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-                        for (int q = 0; q < NS; ++q)
-                            top = fmaxf(top, rm[q * M]);
-#pragma unroll
-                        for (int q = 0; q < NS; ++q) {
-                            const float f = rm[q * M] == top ? 1.f : exp2f(rm[q * M] - top);
-                            sum = fmaf(f, rl[q * M], sum);
-                            fac[q][e0 + lane] = f;
-                        }
-                        sums_of(p, e0 + lane, top, sum);
-                    }
-                    __syncwarp();
-                }
-                columns(p, e0, r, gate);
-                __syncwarp();
+                if (r == 0)
+                    sums(p, e0, C::ER, NS, M);
+                columns(p, e0, C::ER, NS, M, r, gate);
                 if (lane == 0)
                     mbar_arrive(&xempty);
             }
@@ -278,14 +282,16 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
         return;
     }
     // --------------------------------------------------------------- consumers
-    const int st = warp / RT, row0 = warp % RT * 8;     // unit group, rows
+    // warps of a group: in a wide tile as many as the part's rows need, two for a token of
+    // 12 heads
+    auto tiles_of = [](const Part &p) { return !WIDE ? RT : p.nrows <= 8 ? 1 : p.nrows <= 16 ? 2 : p.nrows <= 32 ? 4 : 8; };
     const int g = lane >> 2, cq = lane & 3;
     const int btl = box_log2(a.pg.page, U), box = (1 << btl) * D * 2, dbs = (1 << btl) * 128;
     // a lane's position (of 16) and 16-byte piece in a load of keys and of values
     const int ka = (lane & 15) * 128, kc = lane >> 4;
     const int va = ((lane & 7) + 8 * (lane >> 4)) * 128, vc = (lane >> 3) & 1;
     int it = 0;                                         // units of the CTA before this part, modulo NS
-    int slot = st, phase = 0;                           // of this group's next unit
+    int slot = warp / RT, phase = 0;                    // of this group's next unit
     uint32_t xr = 0;                                    // hand-overs so far
     for (int parts = 0;; ++parts) {
         const int b = parts & 1;
@@ -294,6 +300,14 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
         const Part p = ring.part[b];
         if (!p.live)
             break;
+        const int row0 = warp % tiles_of(p) * 8;        // this warp's rows
+        // units that it takes, by their index modulo 8 (a wide tile's groups change: every
+        // warp sees every unit) or all that it sees
+        unsigned take = row0 < p.nrows ? 0xffu : 0u;
+        if (WIDE)
+            for (int i = 0; i < 8; ++i)
+                if ((i & (CW / tiles_of(p) - 1)) != warp / tiles_of(p))
+                    take &= ~(1u << i);
         const int first_row = p.p0 + p.rowf;            // the last position that every row sees
         const int last_row = p.p0 + p.rowf + (p.hf + p.nrows - 1) / group;
         int lim[2];                                     // of this lane's rows, 2 cq and the next
@@ -302,7 +316,6 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             const int i = row0 + 2 * cq + e;
             lim[e] = i < p.nrows ? first_row + (p.hf + i) / group : -1;
         }
-        const bool idle = row0 >= p.nrows;
         uint32_t qf[D / 16][2];                         // the rows, as the products take them
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
@@ -320,22 +333,22 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             for (int e = 0; e < 4; ++e)
                 O[j][e] = 0.f;
         // the gates of rows that this warp finishes: into L2 meanwhile
-        if (!NE && p.whole && a.gate)
-            for (int i = lane; i < 8 * D / 64; i += 32) {
-                const int h = p.hf + row0 + i / (D / 64);
-                if (row0 + i / (D / 64) < p.nrows)
+        if (WIDE && p.whole && a.gate)
+            for (int i = lane; i < tiles_of(p) * (D / 64); i += 32) {
+                const int row = warp * tiles_of(p) + i / (D / 64), h = p.hf + row;
+                if (row < p.nrows)
                     prefetch_l2(static_cast<const char *>(a.gate) +
                                 ((p.r0 + p.rowf + h / group) * a.gs.tok + (p.hk * group + h % group) * a.gs.head + i % (D / 64) * 64) *
                                     (a.gate_f32 ? 4 : 2));
             }
         const int count = max(p.u1 - p.u0, 0);
-        // this group's units: those of index st modulo NS within the CTA
-        for (int n = (st - it) & (NS - 1); n < count; n += NS) {
+        // units of index warp / RT modulo NS within the CTA (NS is 1 in a wide tile)
+        for (int n = (warp / RT - it) & (NS - 1); n < count; n += NS) {
             if (!ring_wait(&ring.full[slot], phase, &ring.abort, a.sq))
                 return;
             const uint32_t ks = smem_u32(units) + slot * C::UNIT, vs = ks + R::PLANE;
             const int t0 = (p.u0 + n) * U;
-            if (!idle) {
+            if (take >> (WIDE ? n & 7 : 0) & 1u) {
                 const unsigned there = ring.ok[slot];
                 // ---- scores: positions g and 8 on of each 16, rows 2 cq and the next
                 constexpr int CHAINS = U < 64 ? 64 / U : 1;  // sums of independent products
@@ -536,21 +549,19 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
         }
         float *const own = xb + (warp * 8 + 2 * cq) * C::XROW + g;
-        if (!NE) {
-            places(p, row0);
-            if (g == 0)
+        const int tiles = tiles_of(p), groups = WIDE ? CW / tiles : NS;
+        if (WIDE)
+            places(p, warp * tiles, tiles);
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    sums_of(p, row0 + 2 * cq + e, m[e], l[e]);
-        }
-#pragma unroll
-        for (int r = 0; r < C::ROUNDS; ++r, ++xr) {
+        for (int r = 0; r < C::ROUNDS; ++r) {
             uint4 gate[ITEMS];
-            if (!NE)
-                gates(p, row0, r, gate);
-            else if (!ring_wait(&xempty, (xr & 1) ^ 1u, &ring.abort, a.sq))
+            if (WIDE)
+                gates(p, warp * tiles, tiles, r, gate);
+            // (one group: every warp finishes its own rows, but others may still read what it
+            // left them of the part before)
+            if ((!WIDE || groups > 1 || r == 0) && !ring_wait(&xempty, (xr & 1) ^ 1u, &ring.abort, a.sq))
                 return;
-            if (NE && r == 0 && g == 0) {
+            if (r == 0 && g == 0) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     red_m[warp * 8 + 2 * cq + e] = m[e];
@@ -563,12 +574,19 @@ __global__ void __launch_bounds__(Cfg<D, RT>::THREADS, 1)
                 for (int e = 0; e < 4; ++e)
                     own[(e & 1) * C::XROW + j * 16 + 8 * (e >> 1)] = O[r * (DR / 16) + j][e];
             __syncwarp();
-            if (NE) {
+            if (!WIDE || groups > 1) {
                 if (lane == 0)
                     mbar_arrive(&xfull);
-            } else {
-                columns(p, row0, r, gate);
-                __syncwarp();
+                if (WIDE && !ring_wait(&xfull, xr & 1, &ring.abort, a.sq))
+                    return;
+                ++xr;
+            }
+            if (WIDE) {
+                if (r == 0)
+                    sums(p, warp * tiles, tiles, groups, tiles * 8);
+                columns(p, warp * tiles, tiles, groups, tiles * 8, r, gate);
+                if (groups > 1 && lane == 0)
+                    mbar_arrive(&xempty);
             }
         }
     }
@@ -697,12 +715,12 @@ EncodeFn encoder()
     return fn;
 }
 
-// Tiles of eight rows: what an average sequence's rows fill (a larger tile than a
-// sequence needs leaves warps without work, a smaller one reads its keys again).
+// Tiles of eight rows, 1, 2 or 8 by the rows of an average sequence.  A larger tile than a
+// sequence needs costs some of the shared memory, a smaller one reads its keys again.
 int row_tiles(int group, int n, int total)
 {
     const long long rows = ((long long)total + n - 1) / n * group;
-    return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+    return rows <= 8 ? 1 : rows <= 16 ? 2 : 8;
 }
 
 template <int D, int RT>
@@ -735,7 +753,6 @@ cudaError_t launch_d(const PagedAttnArgs &a, cudaStream_t s)
     switch (row_tiles(a.H / a.Hk, a.sq.n, a.sq.total)) {
     case 1: return launch<D, 1>(a, s);
     case 2: return launch<D, 2>(a, s);
-    case 4: return launch<D, 4>(a, s);
     default: return launch<D, 8>(a, s);
     }
 }

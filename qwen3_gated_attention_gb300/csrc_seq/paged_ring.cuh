@@ -9,7 +9,7 @@
 // warps consume.  (One producer takes 700 cycles a unit and 90 more for every box beyond
 // two: as much as 16 KB take to arrive at an SM, twice that with boxes of 16 positions.)
 // A part costs a CTA some time whatever its length, so every segment counts kHead units
-// more than it has when the line is shared out.
+// more than it has when the line is shared out, and units that meet many rows count double.
 //
 // Every slot of the ring belongs to one producer and one group of consumers: SLOTS is
 // divided by the number of either.  A wait is for a phase's parity, so that it must never
@@ -42,8 +42,12 @@ struct Part {
 struct SeqUnits {
     int r0, len, p0, units;
     int tiles;             // of rows
-    // what it takes of the line
-    __device__ __forceinline__ long long all(int Hk) const { return units ? (long long)tiles * Hk * (units + kHead) : 0; }
+    int cost;              // of a unit: more than four eighths of a tile of 64 rows count double
+    // what a segment takes of the line, and the sequence
+    __device__ __forceinline__ int length() const { return (units + kHead) * cost; }
+    __device__ __forceinline__ long long all(int Hk) const { return units ? (long long)tiles * Hk * length() : 0; }
+    // units in front of a place in the segment
+    __device__ __forceinline__ int units_at(int v) const { return max(v / cost - kHead, 0); }
 };
 
 // `bad`: rows whose positions do not fit the table
@@ -57,6 +61,7 @@ __device__ __forceinline__ SeqUnits seq_units(const PagedAttnArgs &a, int s, int
     u.units = on ? (u.p0 + u.len + U - 1) / U : 0;
     // (rows times heads fit 31 bits)
     u.tiles = on ? M ? (int)(((unsigned)u.len * group + M - 1) / M) : 1 : 0;
+    u.cost = M == 64 && (unsigned)u.len * group > 32 ? 2 : 1;
     return u;
 }
 
@@ -342,7 +347,7 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
     SeqUnits u = seq_units(a, s, group, R::V ? M : 0, U, bad);
     // first segment, and place in it, its head counted
     const long long off = run.x0 - run.at;
-    const unsigned length = u.units + kHead;
+    const unsigned length = u.length();
     int seg = off >> 32 ? (int)(off / length) : (int)((unsigned)off / length);
     int v0 = (int)(off - (long long)seg * length);
     // pages of 32 boxes of sequence tab_s, one a lane; not looked at before they are used,
@@ -369,8 +374,9 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
             if (u.units == 0)
                 break;                 // lengths that changed meanwhile
         }
-        const int v1 = (int)min(run.x1 - x + v0, (long long)(u.units + kHead));
-        const int u0 = max(v0 - kHead, 0), u1 = max(v1 - kHead, 0);
+        // (rounded down: whoever has a segment's last place has its last unit)
+        const int v1 = (int)min(run.x1 - x + v0, (long long)u.length());
+        const int u0 = u.units_at(v0), u1 = u.units_at(v1);
         const int hk = u.tiles == 1 ? seg : seg / u.tiles;
         const bool whole = u0 == 0 && u1 == u.units;
         const int passes = u1 <= u0 ? 0 : R::V ? 1 : (int)(((unsigned)u.len * group + M - 1) / M);
@@ -447,7 +453,7 @@ __device__ __forceinline__ void produce(const PagedAttnArgs &a, R &ring, uint8_t
             }
             it = (it + count) & (R::NP - 1);
             if (pw == 0 && lane == 0 && u0 == 0 && u1 < u.units)
-                seen(p, (int)((x - v0 + u.units + kHead - 1) / run.quota));
+                seen(p, (int)((x - v0 + u.length() - 1) / run.quota));
         }
         x += v1 - v0;
         v0 = 0;
