@@ -11,7 +11,10 @@
 // Within a CTA the units of a part go round NS groups of warps, each with its own
 // running maximum and sum; a warp of a group has eight of the tile's rows.  Warps wait for
 // units only, never for each other: at a part's end each leaves (m, sum, O) in shared
-// memory for two warps that join, divide, gate and write them, and goes on with the next.
+// memory for other warps that join, divide, gate and write them, and goes on with the next.
+// Tiles are of 8, 16 or 64 rows.  The eight warps of a wide one form as many groups as a
+// part's rows leave (four for a token of twelve heads beside drafts of other sequences: 42
+// us instead of 50), and join among themselves.
 //
 // The matrix instructions run with the cache as their first operand (16 positions, or
 // 16 elements of the values) and the rows as their second, eight wide: one token's
@@ -28,7 +31,7 @@
 // over 2: 51 us, of which the join takes 6 and the start 3.  64 sequences of 211 to 4200,
 // 16 heads of 64 over 8, in pages of 16: 52 us, 5.0 TB/s (2 KB a copy; CTAs whose copies
 // are slow end 10 us after the others).  Eight sequences of four drafted rows, 24 heads over
-// 2: 50 us for 20 us of bytes: 48 rows are six warps of eight, two of them on one scheduler;
+// 2: 47 us for 20 us of bytes: 48 rows are six warps of eight, two of them on one scheduler;
 // for 32 positions its matrix instructions take 1536 cycles, and so do the reads of keys and
 // values that every warp makes from shared memory (rows loaded anew for each unit instead
 // of kept in registers change nothing).  One token
@@ -716,7 +719,18 @@ EncodeFn encoder()
 }
 
 // Tiles of eight rows, 1, 2 or 8 by the rows of an average sequence.  A larger tile than a
-// sequence needs costs some of the shared memory, a smaller one reads its keys again.
+// sequence needs costs shared memory, a smaller one meets its keys again.  Eight sequences
+// of 256 to 30000 positions, heads of 256, by 1, 2 and 8 tiles, in us:
+//    8 rows (32 heads over 4)   47.3   48.2   60.9
+//   12 rows (24 over 2)         46.4   32.4   39.2
+//   16 rows (32 over 8)        159.0   88.6  109.9
+//   24 rows (24 over 2)         63.6   49.5   41.1
+//   32 rows (32 over 8)        304.8  164.3  123.9
+//   48 rows (24 over 2)        116.6   66.4   55.8
+// One tile and two are equal up to four rows (84 us).  Heads of 64 shift the second bound
+// a little: 20 rows 18.6, 19.1 and 21.5 us, 48 rows 59.6, 44.5 and 39.9.
+// The rule cannot see the lengths: of uneven drafts, 1 to 6 tokens of 12 heads, it takes
+// 8 tiles (42.2 us) where 2 would do (35.0).
 int row_tiles(int group, int n, int total)
 {
     const long long rows = ((long long)total + n - 1) / n * group;

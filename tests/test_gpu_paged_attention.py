@@ -124,6 +124,23 @@ def test_many_sequences_share_the_work(P):
     _check(c, out, lse, seqs=set(range(0, 300, 17)) | {7, 150})
 
 
+@pytest.mark.parametrize("d", [64, 128, 192, 256])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_rows_of_all_numbers_side_by_side(d, seed):
+    """Parts of one to 72 rows in turn in every CTA: groups of one to eight warps, some of
+    them whole, some joined."""
+    g = torch.Generator().manual_seed(seed)
+    lens = [int(x) for x in torch.randint(1, 7, (150,), generator=g)]
+    past = [int(x) for x in torch.randint(0, 400, (150,), generator=g)]
+    past[40] = 6000
+    c = _case(24, 2, d, 16, lens, past, seed=d + seed)
+    out, lse, st = _run(c)
+    assert st == 0
+    _check(c, out, lse, seqs=set(range(seed, 150, 7)) | {40})
+    again, lse2, _ = _run(c)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("H,Hk,d,lens,past", [(24, 2, 256, [1], [20000]), (24, 2, 256, [3], [9999]),
                                               (16, 1, 64, [2, 1], [30000, 1]), (4, 4, 128, [1], [70000])])
 def test_long_contexts(H, Hk, d, lens, past):
