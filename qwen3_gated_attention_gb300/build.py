@@ -1,5 +1,5 @@
-"""Build libgattn.so (sm_103a) in-tree with nvcc, one process per translation unit, and
-the module _paged beside it (tensor arguments of the paged-cache calls).
+"""Build libgattn.so (sm_103a) in-tree with nvcc, one process per translation unit, and,
+where torch is found, the module _paged beside it (tensor arguments of the paged-cache calls).
 
 Usage: ``python -m qwen3_gated_attention_gb300.build [--force] [--verbose-ptxas]``
 """
@@ -66,10 +66,22 @@ def _compile(src, nvcc, verbose_ptxas):
     return obj, None
 
 
+def has_torch():
+    """Whether there is a torch to build the tensor module against."""
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
+
+
 def _compile_module(src):
-    """The object of the tensor module (C++ against torch's headers, no CUDA)."""
+    """The object of the tensor module (C++ against torch's headers, no CUDA); None without
+    torch."""
     import sysconfig
 
+    if not has_torch():
+        return None, None
     import torch
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     dep = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "gattn.h"), __file__,
@@ -112,8 +124,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     with ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         tensors = ex.submit(_compile_module, TENSORS)
         results = list(ex.map(lambda s: _compile(s, nvcc, verbose_ptxas), srcs))
-        tensors = tensors.result()
-    errors = [e for _, e in results + [tensors] if e]
+    errors = [e for _, e in results if e]
     if errors:
         raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
     objs = [o for o, _ in results]
@@ -125,9 +136,13 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    if (not os.path.exists(MODULE) or force or
-            os.path.getmtime(MODULE) < max(os.path.getmtime(LIB), os.path.getmtime(tensors[0]))):
-        _link_module(tensors[0])
+    # the library stands by now, whatever becomes of the module
+    module, error = tensors.result()
+    if error:
+        raise RuntimeError("tensor module: " + error)
+    if module and (not os.path.exists(MODULE) or force or
+            os.path.getmtime(MODULE) < max(os.path.getmtime(LIB), os.path.getmtime(module))):
+        _link_module(module)
     return LIB
 
 

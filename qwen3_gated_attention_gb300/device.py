@@ -484,7 +484,11 @@ _calls = {}
 def _native(name):
     """A call of the module _paged, which is built with the library."""
     gattn.lib()                       # says so if it is not
-    from . import _paged as module
+    try:
+        from . import _paged as module
+    except ImportError as e:
+        raise OSError("the module _paged is missing or was built for another torch: build it with "
+                      "`python -m qwen3_gated_attention_gb300.build` where torch is found") from e
     return getattr(module, name)
 
 
