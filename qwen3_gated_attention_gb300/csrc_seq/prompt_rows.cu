@@ -8,17 +8,17 @@
 // nothing waits at a barrier, and always has kFly head rows on their way while it works
 // on the kFly before them, from the queries through the keys to the values; the first
 // set out before the row's sequence and angles are known.  8240 rows of 32 + 8 + 8 heads
-// of 256 take 75 us, 5.4 TB/s or 80 % of the copy rate (a CTA per row and head with
+// of 256 take 73.3 us, 5.5 TB/s or 83 % of the copy rate (a CTA per row and head with
 // barriers 144 us; a warp that loads, then works 88 us; one head row at a time 188 us);
 // more loads on their way or more warps cost registers: 82 us with 24 warps an SM.  37
-// rows of 16 + 4 + 4 heads: 4.5 us.
+// rows of 16 + 4 + 4 heads: 4.2 us.
 //
 // The paged form (gattn_paged_rows) is the same kernel: the cache row is found through a
 // page table, the pairs (y_i, y_j) may be neighbours, the norms may be absent, the angles
 // may come from positions of their own, and cos and sin carry a factor.  8240 rows of 32 +
-// 8 + 8 heads of 256 into pages of 16: 78 us, 78 % of the copy rate; 2766 fp32 rows of 16 +
-// 8 + 8 heads of 128, neighbours turned: 17.7 us (58 %; 692 CTAs are 1.1 times what fits
-// at once, and more warps a row cost more than they fill); 8 single rows: 4.6 us.
+// 8 + 8 heads of 256 into pages of 16: 75.8 us, 80 % of the copy rate; 2766 fp32 rows of 16 +
+// 8 + 8 heads of 128, neighbours turned: 17.3 us (59 %; 692 CTAs are 1.1 times what fits
+// at once, and more warps a row cost more than they fill); 8 single rows: 4.5 us.
 #include "paged.cuh"
 
 namespace gattn {
@@ -127,7 +127,9 @@ prompt_rows_kernel(const __grid_constant__ std::conditional_t<PAGED, PagedRowsAr
     const long long p0 = a.pos[s], p = p0 + (t - r0);
     // the last two hold for any row, if the offsets do not fall
     bool ok = p0 >= 0 && p0 + len <= a.cap && t >= r0 && t - r0 < len;
-    long long kat = 0, vat = 0;            // the row's place in the caches
+    // the row's place in the caches: slot or page, and row in it.  (As two offsets in
+    // 64 bits it spills: 8240 rows of 32 + 8 + 8 heads 75.1 us instead of 73.3)
+    int in = -1, at_row = (int)p;
     bool keep = true;                      // it has one
     int at_pos = (int)p;                   // position of the angles
     if constexpr (PAGED) {
@@ -135,18 +137,13 @@ prompt_rows_kernel(const __grid_constant__ std::conditional_t<PAGED, PagedRowsAr
             at_pos = a.positions[t];
             ok = ok && at_pos >= 0 && at_pos <= kMaxPos;
         }
-        int page = -1;
         if (ok)
-            page = a.pg.table[s * a.pg.table_stride + (int)p / a.pg.page];
-        keep = page >= 0 && page < a.pg.pages;
-        const int in = ok ? (int)p % a.pg.page : 0;
-        kat = page * a.pg.k.page + in * a.pg.k.tok;
-        vat = page * a.pg.v.page + in * a.pg.v.tok;
+            in = a.pg.table[s * a.pg.table_stride + at_row / a.pg.page];
+        keep = in >= 0 && in < a.pg.pages;
+        at_row %= a.pg.page;
     } else {
-        const int slot = seq_slot_warp(a.sq, s, true);
-        ok = ok && slot >= 0;
-        kat = slot * a.kcb + p * a.kct;
-        vat = slot * a.vcb + p * a.vct;
+        in = seq_slot_warp(a.sq, s, true);
+        ok = ok && in >= 0;
     }
     if (!(ok && keep) && lane == 0)
         seq_flag(a.sq, GATTN_STATUS_RANGE);
@@ -283,11 +280,11 @@ prompt_rows_kernel(const __grid_constant__ std::conditional_t<PAGED, PagedRowsAr
     __nv_bfloat16 *kc, *vc;
     long long kch, vch;
     if constexpr (PAGED) {
-        kc = static_cast<__nv_bfloat16 *>(a.pg.kp) + kat, kch = a.pg.k.head;
-        vc = static_cast<__nv_bfloat16 *>(a.pg.vp) + vat, vch = a.pg.v.head;
+        kc = static_cast<__nv_bfloat16 *>(a.pg.kp) + in * a.pg.k.page + at_row * a.pg.k.tok, kch = a.pg.k.head;
+        vc = static_cast<__nv_bfloat16 *>(a.pg.vp) + in * a.pg.v.page + at_row * a.pg.v.tok, vch = a.pg.v.head;
     } else {
-        kc = a.kc + kat, kch = a.kch;
-        vc = a.vc + vat, vch = a.vch;
+        kc = a.kc + in * a.kcb + at_row * a.kct, kch = a.kch;
+        vc = a.vc + in * a.vcb + at_row * a.vct, vch = a.vch;
     }
     normed(krow, a.ks.head, kc, kch, a.Hk, wk, kn,
            [&] { fetch(vrow, a.vs.head, first, a.Hk, j0, j0 + 4); });
