@@ -896,7 +896,8 @@ gattn_status gattn_paged_weights(const gattn_paged_weights_desc *desc, gattn_str
  *   lengths       (device) int32 [num_seqs]
  *   weights       fp32, element (s, hk, p) at s*w_stride_seq + hk*w_stride_head + p
  *   weights_out   fp32 with strides of its own, or NULL: weights of the kept positions,
- *                 in their new places; may be weights (equal strides)
+ *                 in their new places; may be weights (equal strides over what there is more
+ *                 than one of)
  *   kept          int32 [num_seqs][num_kv_heads][keep]: the positions that were kept, in
  *                 order; -1 behind them
  *   lengths_out   int32 [num_seqs]: m; not in lengths' memory

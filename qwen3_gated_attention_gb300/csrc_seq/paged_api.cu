@@ -273,7 +273,9 @@ gattn_status gattn_paged_evict(const gattn_paged_evict_desc *p, gattn_stream str
             return bad(GATTN_E_INVALID_ARG, "weights_out_width must be > 0");
         CHECK(check_apart("weights_out", p->weights_out_width,
                           {{p->wo_stride_head, p->num_kv_heads}, {p->wo_stride_seq, p->num_seqs}}));
-        if (p->weights_out == p->weights && (p->wo_stride_seq != p->w_stride_seq || p->wo_stride_head != p->w_stride_head))
+        // (a stride over one sequence or head is none)
+        if (p->weights_out == p->weights && ((p->num_seqs != 1 && p->wo_stride_seq != p->w_stride_seq) ||
+                                             (p->num_kv_heads != 1 && p->wo_stride_head != p->w_stride_head)))
             return bad(GATTN_E_INVALID_ARG, "weights_out in place of weights must have its strides");
     }
     if (p->out_table && (p->out_table_width <= 0 || p->out_table_stride < p->out_table_width ||

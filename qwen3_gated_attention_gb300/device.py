@@ -590,9 +590,9 @@ def paged_evict(k_pages, v_pages, table, lengths, weights, *, keep, recent=0, ou
     attended of the others (gattn_paged_evict).
 
     lengths int32 [n]; weights fp32 [n][Hk][positions]; weights_out [n][Hk][>= keep] takes
-    those of the kept positions (may be weights).  out_table: pages that they move to,
-    others than the table's; None: in place.  Returns (kept int32 [n][Hk][keep],
-    lengths_out int32 [n])."""
+    those of the kept positions (may be weights, or their first `keep` places or more).
+    out_table: pages that they move to, others than the table's; None: in place.  Returns
+    (kept int32 [n][Hk][keep], lengths_out int32 [n])."""
     if kept is None:
         if keep <= 0:
             raise ValueError("keep must be > 0")

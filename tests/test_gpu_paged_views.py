@@ -1,0 +1,37 @@
+"""Eviction through views: weights and pages in place, narrower than what they are views of."""
+import pytest
+import torch
+
+from tests.test_gpu_paged_evict import _check_evict, _dev, _evict_case, _i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from qwen3_gated_attention_gb300 import build
+    build.build()
+
+
+def _evict(c, recent, weights_out, out_table=None):
+    """weights_out and out_table are made from the weights and the table on the GPU."""
+    x = {k: c[k].cuda() for k in ("kp", "vp", "table", "out", "w")}
+    wo = weights_out(x["w"])
+    to = x["out"] if out_table == "others" else None if out_table is None else out_table(x["table"])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept, lens = _dev().paged_evict(x["kp"], x["vp"], x["table"], _i32(c["lengths"]), x["w"], keep=c["keep"], recent=recent,
+                                    out_table=to, weights_out=wo, status=st)
+    torch.cuda.synchronize()
+    return {k: v.cpu() for k, v in dict(kept=kept, lens=lens, kp=x["kp"], vp=x["vp"], w=wo, status=st, all=x["w"]).items()}
+
+
+@pytest.mark.parametrize("into_pages", [True, False])
+@pytest.mark.parametrize("n,Hk", [(1, 1), (1, 3), (3, 1), (2, 2)])
+def test_weights_in_place_through_a_narrower_view(n, Hk, into_pages):
+    c = _evict_case(Hk, 64, 16, [300, 77, 130][:n], 100, seed=10 * n + Hk)
+    got = _evict(c, 20, lambda w: w[:, :, :100], "others" if into_pages else None)
+    assert int(got["status"]) == 0
+    _check_evict(c, 20, got, into_pages)
+    assert torch.equal(got["all"][:, :, 100:], c["w"][:, :, 100:])
