@@ -309,7 +309,7 @@ gattn_status gattn_paged_evict(const gattn_paged_evict_desc *p, gattn_stream str
     a.recent = p->recent;
     const long long room = (long long)a.pg.width * a.pg.page;
     a.cap = std::min<long long>(room, p->weights_width);
-    a.out_cap = in_place ? room : (long long)p->out_table_width * a.pg.page;
+    a.out_cap = p->out_table ? (long long)p->out_table_width * a.pg.page : room;
     if (p->weights_out)
         a.out_cap = std::min<long long>(a.out_cap, p->weights_out_width);
     a.status = p->status;

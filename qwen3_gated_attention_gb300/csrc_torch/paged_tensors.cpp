@@ -395,7 +395,11 @@ PyObject *paged_evict(PyObject *, PyObject *const *v, Py_ssize_t n)
         p.recent = a.i32(6, "recent");
         if (!a.none(7)) {
             const Table t = page_table(a, 7, "out_table", p.num_seqs);
-            p.out_table = t.p, p.out_table_width = t.width, p.out_table_stride = t.stride;
+            p.out_table = t.p, p.out_table_width = t.width;
+            p.out_table_stride = t.stride;
+            // one sequence's table and a view of it: neither has a stride of its own
+            if (p.num_seqs == 1 && t.p == p.pages.table)
+                p.pages.table_stride = p.out_table_stride = std::max(p.pages.table_stride, t.stride);
         }
         if (!a.none(8)) {
             const Received o = received(a, 8, "weights_out", p.num_seqs, p.num_kv_heads);

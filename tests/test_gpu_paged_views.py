@@ -35,3 +35,29 @@ def test_weights_in_place_through_a_narrower_view(n, Hk, into_pages):
     assert int(got["status"]) == 0
     _check_evict(c, 20, got, into_pages)
     assert torch.equal(got["all"][:, :, 100:], c["w"][:, :, 100:])
+
+
+@pytest.mark.parametrize("n", [1, 2])
+def test_pages_in_place_through_a_narrower_table(n):
+    """out_table as a view of the table: in place, and as wide as the view is."""
+    c = _evict_case(2, 64, 16, [300, 77][:n], 100, seed=20 + n)
+    weights = lambda w: torch.zeros(n, 2, 100, device="cuda")      # noqa: E731
+    for width in (c["table"].shape[1], 7):
+        got = _evict(c, 20, weights, lambda t: t[:, :width])
+        assert int(got["status"]) == 0
+        _check_evict(c, 20, got, False)
+    # 6 pages hold 96 positions: the first sequence would keep 100, the other one has fewer
+    got = _evict(c, 20, weights, lambda t: t[:, :6])
+    assert int(got["status"]) == 1
+    _check_evict(c, 20, got, False, skipped=(0,))
+
+
+def test_pages_in_place_through_a_wider_table():
+    c = _evict_case(2, 64, 16, [100], 40, seed=23)
+    x = {k: c[k].cuda() for k in ("kp", "vp", "w")}
+    wide = torch.cat((c["table"], torch.full((1, 5), 1 << 30, dtype=torch.int32)), 1).cuda()
+    wo = torch.zeros(1, 2, 40, device="cuda")
+    kept, lens = _dev().paged_evict(x["kp"], x["vp"], wide[:, :c["table"].shape[1]], _i32([100]), x["w"], keep=40, recent=8,
+                                    out_table=wide, weights_out=wo)
+    got = {k: v.cpu() for k, v in dict(kept=kept, lens=lens, kp=x["kp"], vp=x["vp"], w=wo).items()}
+    _check_evict(c, 8, got, False)
