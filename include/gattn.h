@@ -874,7 +874,7 @@ gattn_status gattn_paged_attention(const gattn_paged_attention_desc *desc, gattn
  *   weights       fp32, element (s, hk, p) at s*w_stride_seq + hk*w_stride_head + p, or
  *                 NULL for zeros
  *   weights_out   fp32, the same strides (which keep weights_width positions apart);
- *                 may be weights
+ *                 may be weights, else shares no memory with them
  * A sequence with more positions than weights_width is skipped (GATTN_STATUS_RANGE).
  * The sums have one order: equal inputs give equal bits.
  */
@@ -897,7 +897,7 @@ gattn_status gattn_paged_weights(const gattn_paged_weights_desc *desc, gattn_str
  *   weights       fp32, element (s, hk, p) at s*w_stride_seq + hk*w_stride_head + p
  *   weights_out   fp32 with strides of its own, or NULL: weights of the kept positions,
  *                 in their new places; may be weights (equal strides over what there is more
- *                 than one of)
+ *                 than one of), else shares no memory with them
  *   kept          int32 [num_seqs][num_kv_heads][keep]: the positions that were kept, in
  *                 order; -1 behind them
  *   lengths_out   int32 [num_seqs]: m; not in lengths' memory

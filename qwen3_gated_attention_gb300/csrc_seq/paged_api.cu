@@ -54,6 +54,73 @@ Pages pages_of(const gattn_pages &g)
             g.num_pages, g.page_size, g.table_width};
 }
 
+// Received weights as they lie in memory: n sequences of Hk heads of `width` floats.
+struct Received {
+    const float *p;
+    int64_t width, seq, head;
+};
+
+int64_t floor_div(int64_t x, int64_t y) { return x / y - (x % y < 0); }
+
+struct Found {
+    int64_t first, last;
+};
+
+// The i in [0, n) whose rows, `len` elements from i * step on, meet [x, x + width).
+Found rows_met(int64_t x, int64_t width, int64_t step, int64_t n, int64_t len)
+{
+    return {std::max<int64_t>(floor_div(x - len, step) + 1, 0), std::min(floor_div(x + width - 1, step), n - 1)};
+}
+
+// Weights that are written share no memory with those that are read, unless they are the
+// same ones.
+gattn_status check_beside(const Received &in, const Received &out, int64_t n, int64_t Hk)
+{
+    // what there is one of has no stride
+    const int64_t is = n == 1 ? 0 : in.seq, ih = Hk == 1 ? 0 : in.head, os = n == 1 ? 0 : out.seq, oh = Hk == 1 ? 0 : out.head;
+    if (!in.p || (in.p == out.p && is == os && ih == oh))
+        return GATTN_OK;
+    if (in.p == out.p)
+        return bad(GATTN_E_INVALID_ARG, "weights_out in place of weights must have its strides");
+    if (n == 0)
+        return GATTN_OK;
+    for (const int64_t step : {is, os})
+        if (step > (1ll << 60) / n)
+            return bad(GATTN_E_INVALID_ARG, "weights strides are too large");
+    for (const int64_t step : {ih, oh})
+        if (step > (1ll << 60) / Hk)
+            return bad(GATTN_E_INVALID_ARG, "weights strides are too large");
+    const int64_t from = (reinterpret_cast<intptr_t>(in.p) - reinterpret_cast<intptr_t>(out.p)) / 4;
+    const int64_t in_span = (n - 1) * is + (Hk - 1) * ih + in.width, out_span = (n - 1) * os + (Hk - 1) * oh + out.width;
+    if (from >= out_span || from + in_span <= 0)
+        return GATTN_OK;
+    bool meet = false;
+    if (is == os && ih == oh) {
+        // rows between each other: only how far apart they are counts
+        for (int64_t h = 1 - Hk; h < Hk && !meet; ++h) {
+            const Found f = rows_met(from + (n - 1) * is + h * ih, in.width, std::max<int64_t>(is, 1), 2 * n - 1, out.width);
+            meet = f.first <= f.last;
+        }
+    } else {
+        // the axis of out whose steps are further apart, and the nearer one within it
+        const bool by_seq = os >= oh;
+        const int64_t S = std::max<int64_t>(by_seq ? os : oh, 1), N = by_seq ? n : Hk;
+        const int64_t T = std::max<int64_t>(by_seq ? oh : os, 1), M = by_seq ? Hk : n;
+        for (int64_t i = 0; i < n * Hk && !meet; ++i) {
+            const int64_t x = from + i / Hk * is + i % Hk * ih;
+            const Found f = rows_met(x, in.width, S, N, (M - 1) * T + out.width);
+            meet = f.last - f.first >= 2;      // whatever lies between is covered
+            for (int64_t j = f.first; j <= f.last && !meet; ++j) {
+                const Found g = rows_met(x - j * S, in.width, T, M, out.width);
+                meet = g.first <= g.last;
+            }
+        }
+    }
+    if (meet)
+        return bad(GATTN_E_INVALID_ARG, "weights_out overlaps weights and is not the same: it is written while weights are read");
+    return GATTN_OK;
+}
+
 // Frequencies as float pairs, theta^(-2i/rd) stretched as the descriptor asks.
 gattn_status frequencies(const gattn_paged_rows_desc *p, int rd, float2 *to)
 {
@@ -239,6 +306,8 @@ gattn_status gattn_paged_weights(const gattn_paged_weights_desc *p, gattn_stream
     if (p->weights_width <= 0)
         return bad(GATTN_E_INVALID_ARG, "weights_width must be > 0");
     CHECK(check_apart("weights", p->weights_width, {{p->w_stride_head, a.Hk}, {p->w_stride_seq, a.sq.n}}));
+    CHECK(check_beside({p->weights, p->weights_width, p->w_stride_seq, p->w_stride_head},
+                       {p->weights_out, p->weights_width, p->w_stride_seq, p->w_stride_head}, a.sq.n, a.Hk));
     if (a.sq.n == 0 || a.sq.total == 0)
         return GATTN_OK;
     a.cap = std::min<long long>(a.cap, p->weights_width);
@@ -277,6 +346,9 @@ gattn_status gattn_paged_evict(const gattn_paged_evict_desc *p, gattn_stream str
         if (p->weights_out == p->weights && ((p->num_seqs != 1 && p->wo_stride_seq != p->w_stride_seq) ||
                                              (p->num_kv_heads != 1 && p->wo_stride_head != p->w_stride_head)))
             return bad(GATTN_E_INVALID_ARG, "weights_out in place of weights must have its strides");
+        CHECK(check_beside({p->weights, p->weights_width, p->w_stride_seq, p->w_stride_head},
+                           {p->weights_out, p->weights_out_width, p->wo_stride_seq, p->wo_stride_head}, p->num_seqs,
+                           p->num_kv_heads));
     }
     if (p->out_table && (p->out_table_width <= 0 || p->out_table_stride < p->out_table_width ||
                          p->out_table_width > (1 << 24) / p->pages.page_size))

@@ -61,3 +61,27 @@ def test_pages_in_place_through_a_wider_table():
                                     out_table=wide, weights_out=wo)
     got = {k: v.cpu() for k, v in dict(kept=kept, lens=lens, kp=x["kp"], vp=x["vp"], w=wo).items()}
     _check_evict(c, 8, got, False)
+
+
+@pytest.mark.parametrize("into_pages", [True, False])
+def test_weights_between_those_that_are_read(into_pages):
+    """Read from one half of each row of a buffer, written to the other."""
+    c = _evict_case(3, 64, 16, [300, 77], 100, seed=31)
+    x = {k: c[k].cuda() for k in ("kp", "vp", "table", "out")}
+    both = torch.full((2, 3, 2, 300), 7.0, device="cuda")
+    both[:, :, 0] = c["w"].cuda()
+    kept, lens = _dev().paged_evict(x["kp"], x["vp"], x["table"], _i32(c["lengths"]), both[:, :, 0], keep=100, recent=20,
+                                    out_table=x["out"] if into_pages else None, weights_out=both[:, :, 1, :100])
+    got = {k: v.cpu() for k, v in dict(kept=kept, lens=lens, kp=x["kp"], vp=x["vp"], w=both[:, :, 1]).items()}
+    _check_evict(c, 20, got, into_pages)
+    assert torch.equal(both[:, :, 0].cpu(), c["w"]) and bool((both[:, :, 1, 100:] == 7).all())
+
+
+def test_received_weights_between_those_that_are_read():
+    from tests.test_gpu_paged_evict import _run_weights, _weights_case
+    c = _weights_case(8, 2, 64, 16, [2, 1], [40, 90], seed=32)
+    want = _run_weights(c)
+    both = torch.full((2, 2, 2, c["w"].shape[2]), 7.0, device="cuda")
+    both[:, :, 1] = c["w"].cuda()
+    assert torch.equal(_run_weights(c, w=both[:, :, 1], out=both[:, :, 0]), want)
+    assert torch.equal(both[:, :, 1].cpu(), c["w"])
