@@ -221,18 +221,25 @@ gattn_status gattn_paged_rows(const gattn_paged_rows_desc *p, gattn_stream strea
                                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Shapes that the attention takes.
+static gattn_status check_attended(int32_t H, int32_t Hk, int32_t d, int32_t n, int32_t total)
+{
+    CHECK(check_heads(H, Hk));
+    CHECK(check_seqs(n, total));
+    CHECK(check_dim(d));
+    if (H > 65536 / d)
+        return bad(GATTN_E_UNSUPPORTED, "num_heads * head_dim must be <= 65536");
+    if ((long long)total * H > 0x7fffffffll)
+        return bad(GATTN_E_UNSUPPORTED, "total_rows * num_heads must be below 2^31");
+    return GATTN_OK;
+}
+
 // What attention and weights have in common.
 static gattn_status paged_args(const gattn_paged_attention_desc *p, bool values, PagedAttnArgs &a)
 {
     if (!p)
         return bad(GATTN_E_INVALID_ARG, "desc is NULL");
-    CHECK(check_heads(p->num_heads, p->num_kv_heads));
-    CHECK(check_seqs(p->num_seqs, p->total_rows));
-    CHECK(check_dim(p->head_dim));
-    if (p->num_heads > 65536 / p->head_dim)
-        return bad(GATTN_E_UNSUPPORTED, "num_heads * head_dim must be <= 65536");
-    if ((long long)p->total_rows * p->num_heads > 0x7fffffffll)
-        return bad(GATTN_E_UNSUPPORTED, "total_rows * num_heads must be below 2^31");
+    CHECK(check_attended(p->num_heads, p->num_kv_heads, p->head_dim, p->num_seqs, p->total_rows));
     if (!(p->scale > 0.f) || !std::isfinite(p->scale))
         return bad(GATTN_E_INVALID_ARG, "scale must be finite and > 0");
     CHECK(check_rows("q", p->q, p->q_stride_token, p->q_stride_head));
@@ -258,8 +265,7 @@ static gattn_status paged_args(const gattn_paged_attention_desc *p, bool values,
 int64_t gattn_paged_attention_workspace(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_seqs,
                                         int32_t total_rows)
 {
-    if (check_heads(num_heads, num_kv_heads) != GATTN_OK || check_seqs(num_seqs, total_rows) != GATTN_OK ||
-        check_dim(head_dim) != GATTN_OK)
+    if (check_attended(num_heads, num_kv_heads, head_dim, num_seqs, total_rows) != GATTN_OK)
         return -1;
     return paged_attn_workspace(head_dim, num_heads / num_kv_heads, num_seqs, total_rows);
 }
