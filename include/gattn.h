@@ -855,8 +855,8 @@ typedef struct gattn_paged_attention_desc {
     uint32_t *status;
 } gattn_paged_attention_desc;
 
-/* Bytes of workspace for these shapes (num_seqs sequences, total_rows rows), -1 for
- * shapes that gattn_paged_attention refuses.  No GPU is needed. */
+/* Bytes of workspace for calls of these heads with up to num_seqs sequences and up to
+ * total_rows rows, -1 for shapes that gattn_paged_attention refuses.  No GPU is needed. */
 int64_t gattn_paged_attention_workspace(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
                                         int32_t num_seqs, int32_t total_rows);
 gattn_status gattn_paged_attention(const gattn_paged_attention_desc *desc, gattn_stream stream);

@@ -267,7 +267,9 @@ int64_t gattn_paged_attention_workspace(int32_t num_heads, int32_t num_kv_heads,
 {
     if (check_attended(num_heads, num_kv_heads, head_dim, num_seqs, total_rows) != GATTN_OK)
         return -1;
-    return paged_attn_workspace(head_dim, num_heads / num_kv_heads, num_seqs, total_rows);
+    // what all rows in one sequence need: tiles go by the rows of an average sequence, so fewer
+    // sequences may need more
+    return paged_attn_workspace(head_dim, num_heads / num_kv_heads, 1, total_rows);
 }
 
 gattn_status gattn_paged_attention(const gattn_paged_attention_desc *p, gattn_stream stream)

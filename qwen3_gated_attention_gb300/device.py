@@ -543,7 +543,8 @@ def paged_rows(q, k, v, k_pages, v_pages, table, cu_rows, cache_pos, *, rope_the
 
 
 def paged_attention_workspace(q, k_pages, cu_rows):
-    """Device memory for paged_attention calls of these shapes, one after the other."""
+    """Device memory for paged_attention calls of these shapes or with fewer sequences or
+    rows, one after the other."""
     T, H, d = q.shape
     size = gattn.paged_attention_workspace(H, k_pages.shape[1], d, cu_rows.shape[0] - 1, T)
     return torch.empty(size, dtype=torch.uint8, device=q.device)

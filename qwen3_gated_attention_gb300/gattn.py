@@ -544,7 +544,7 @@ def paged_attention(desc, stream: int = 0) -> None:
 
 def paged_attention_workspace(num_heads: int, num_kv_heads: int, head_dim: int, num_seqs: int,
                               total_rows: int) -> int:
-    """Bytes of device memory that such a call works in."""
+    """Bytes of device memory that calls of up to so many sequences and rows work in."""
     n = int(lib().gattn_paged_attention_workspace(num_heads, num_kv_heads, head_dim, num_seqs,
                                                   total_rows))
     if n < 0:
