@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int i = rt * 8 + 2 * cq + e;
                     const float lse = ring.lse[b][i];
-                    const int lim = i < p.nrows ? first_row + (p.hf + i) / group : -1;
+                    // (a row that saw nothing gives nothing, whatever its keys hold)
+                    const int lim = i < p.nrows && lse != INFINITY ? first_row + (p.hf + i) / group : -1;
 #pragma unroll
                     for (int q = 0; q < U / 16; ++q)
 #pragma unroll
