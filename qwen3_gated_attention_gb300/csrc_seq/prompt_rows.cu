@@ -176,7 +176,7 @@ prompt_rows_kernel(const __grid_constant__ std::conditional_t<PAGED, PagedRowsAr
     wk.clear();
     // a norm that is absent: no weights, and nothing to divide by
     const bool qn = !PAGED || a.q_norm, kn = !PAGED || a.k_norm;
-    if (act) {
+    if (act && ok) {                       // (skipped rows: zeros, whatever the weights are)
         if (qn)
             wq.load(a.q_norm, o0, o1);
         if (kn)

@@ -30,3 +30,26 @@ def test_a_row_without_a_log_sum_gives_nothing(H, Hk, d, value):
     got = _run_weights(c)
     assert torch.equal(got[1], want[1])
     assert torch.equal(got[0, :, :70], c["w"][0, :, :70]) and bool((got[0, :, 70:72] == 0).all())
+
+
+@pytest.mark.parametrize("rd", [64, 20])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_skipped_rows_are_zero_whatever_the_norms_hold(rd, value):
+    """Of gattn_paged_rows and of gattn_prompt_rows, without an epsilon."""
+    from qwen3_gated_attention_gb300 import device
+    g = torch.Generator().manual_seed(rd)
+    q, k = (torch.randn(5, h, 64, generator=g).to(BF).cuda() for h in (4, 2))
+    w = torch.full((64,), value, dtype=BF, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")      # noqa: E731
+    cu = i32([0, 3, 5])
+    pages, caches = torch.zeros(4, 2, 16, 64, dtype=BF, device="cuda"), torch.zeros(2, 2, 32, 64, dtype=BF, device="cuda")
+    st = i32([0])
+    out = device.paged_rows(q, k, k, pages, pages.clone(), i32([[0, 1], [2, 3]]), cu, i32([0, 31]), rope_theta=1e6, rotary_dims=rd,
+                            q_norm=w, k_norm=w, rms_eps=0.0, status=st)
+    assert bool((out[3:] == 0).all()) and not bool(out[:3].isfinite().any()) and int(st) == 1
+    out = device.paged_rows(q, k, k, pages, pages.clone(), i32([[0, 1], [2, 3]]), cu, i32([0, 0]), rope_theta=1e6, rotary_dims=rd,
+                            q_norm=w, k_norm=w, rms_eps=0.0, positions=i32([0, -1, 2, (1 << 24) + 1, 1 << 24]), status=st)
+    assert bool((out[[1, 3]] == 0).all()) and not bool(out[[0, 2, 4]].isfinite().any())
+    out = device.prompt_rows(q, k, k, w, w, caches, caches.clone(), cu, i32([0, 31]), partial_rotary_factor=rd / 64, rope_theta=1e6,
+                             rms_eps=0.0, status=st)
+    assert bool((out[3:] == 0).all()) and not bool(out[:3].isfinite().any())
