@@ -76,10 +76,15 @@ struct PagedEvictArgs {
     unsigned *status;
 };
 
-// Launches that may be set up while the work before them on the stream ends: each of
-// these kernels waits for it (pdl_wait) before it touches memory, in every block, and lets
-// the next one be set up after that (pdl_launch_dependents).  So a kernel that has started
-// behind one of them knows that all work before that one has ended too.
+// Launches that may be set up while the work before them on the stream ends.  The rules of
+// these kernels:
+//   - Every block waits for that work (pdl_wait) before it ends, and before it touches
+//     memory; but see paged_move_kernel.
+//   - A kernel that lets the next one be set up early (pdl_launch_dependents; attention,
+//     moves and the close in place do not) does so in every block behind its own wait.
+// So a kernel that has started behind one of them knows, before its own wait, that all work
+// in front of that one has ended: paged_move_kernel, always behind paged_select_kernel, reads
+// and writes what the selection does not write or read.
 template <class... K, class... A>
 inline cudaError_t launch_paged(void (*f)(K...), dim3 grid, dim3 block, int smem, cudaStream_t s, A &&...args)
 {

@@ -16,9 +16,10 @@
 // loaded it.
 //
 // Measured: eight sequences of 4000 to 16384 positions cut to 4096, 4 heads of 256, into other
-// pages: 52 us for 40 us of bytes (the selection alone takes 10 us on 32 SMs, the rows 45
-// us, 88 % of the copy rate).  One sequence of 2500 cut to 1024: 9.8 us, two launches
-// and the steps of the selection.
+// pages: 52 us for 40 us of bytes (each alone, under a profiler with cold caches: the
+// selection 14 us on 32 SMs, the rows 45 us, 88 % of the copy rate).  One sequence of 2500
+// cut to 1024: 10 us, two launches and the steps of the selection.  In place: 134 us and 27 us
+// (128 rows a step, each behind three dependent loads, and none while the selection runs).
 #include "paged.cuh"
 
 namespace gattn {
@@ -55,7 +56,8 @@ __global__ void __launch_bounds__(kSel) paged_select_kernel(const __grid_constan
     __shared__ int counts[kBins], above_of[32], equal_of[32], chosen[3], listed;
     __shared__ uint32_t list[kList];
     uint32_t *const keys = dyn, *const hist = dyn + kCached;
-    // the rows' moves start meanwhile, but not before what came before this kernel has ended
+    // the rows' moves start meanwhile, but not before what came before this kernel has ended:
+    // they move rows in front of their own wait, so that this order must stay
     pdl_wait();
     pdl_launch_dependents();
     const int hk = blockIdx.x % a.Hk, s = blockIdx.x / a.Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -323,6 +325,9 @@ constexpr int kMove = 256, kRows = 8;
 // Blocks take the last rows of all sequences first: the newest positions and sequences
 // that keep everything need no selection, so they move while it runs (60 us -> 52 us for
 // eight sequences of 4000 to 16384 positions, a quarter of the 4096 kept ones new).
+// (In front of the wait: lengths, tables, the pages and weights that are read, and those
+// that are written; of these the selection reads weights, which other weights_out never
+// share, and writes none.)
 __global__ void __launch_bounds__(kMove) paged_move_kernel(const __grid_constant__ PagedEvictArgs a, int groups)
 {
     const int lane = threadIdx.x & 31, heads = a.n * a.Hk;
