@@ -827,7 +827,8 @@ gattn_status gattn_paged_rows(const gattn_paged_rows_desc *desc, gattn_stream st
  *   workspace     (device) at least gattn_paged_attention_workspace(...) bytes, 16-byte
  *                 aligned, for the parts of sequences that several CTAs share.  Its
  *                 contents need not be set and mean nothing afterwards.  Calls that may
- *                 run at once (other streams, graphs replayed side by side) need one each.
+ *                 run at once (other streams, graphs replayed side by side, other
+ *                 threads: a call is two launches) need one each.
  * A row that sees no position (its sequence is skipped, or none of its pages exists) gives
  * zeros and lse -infinity.  What a row does not see does not reach it, whatever it holds.
  * A value that it does see and that is infinite or NaN makes its output infinite or NaN.

@@ -35,7 +35,8 @@
 // for 32 positions its matrix instructions take 1536 cycles, and so do the reads of keys and
 // values that every warp makes from shared memory (rows loaded anew for each unit instead
 // of kept in registers change nothing).  One token
-// over 1004 positions: 9.4 us, two launches and five dependent loads.
+// over 1004 positions: 9.6 us, two launches and five dependent loads.  Chunks of 30 to 500 rows
+// of 16 heads over 4, behind 256 to 30000 positions: 618 us for 61 us of products.
 #include <cudaTypedefs.h>
 
 #include "paged_ring.cuh"

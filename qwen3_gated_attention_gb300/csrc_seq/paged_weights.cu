@@ -9,7 +9,10 @@
 // paged_ring.cuh says; a warp alone takes a unit, sums over the rows in its registers and
 // writes each position once, so there are no atomics and the sums have one order.
 // Measured: 16 sequences of 64 to 15001 positions, one to four rows of 32 heads of 256 over
-// 8: 66 us, 6.3 TB/s, 94 % of the copy rate.  One token over 4001 positions: 5.4 us.
+// 8: 66 us, 6.3 TB/s, 94 % of the copy rate.  One token over 4001 positions: 5.4 us.  Many rows
+// are slow: chunks of 30 to 500 rows of 16 heads over 4, behind 256 to 30000 positions, 1.6
+// ms; one of 200 rows among seven single ones 1.2 ms, because the line counts a unit once
+// however many passes it takes.
 #include "paged_ring.cuh"
 
 namespace gattn {

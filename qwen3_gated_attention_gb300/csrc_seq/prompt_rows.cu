@@ -19,6 +19,7 @@
 // 8 + 8 heads of 256 into pages of 16: 75.8 us, 80 % of the copy rate; 2766 fp32 rows of 16 +
 // 8 + 8 heads of 128, neighbours turned: 17.3 us (59 %; 692 CTAs are 1.1 times what fits
 // at once, and more warps a row cost more than they fill); 8 single rows: 4.5 us.
+// Halves that are no multiple of four apart (kSwap) take 103 us for the 8240 rows.
 #include "paged.cuh"
 
 namespace gattn {
