@@ -832,6 +832,7 @@ gattn_status gattn_paged_rows(const gattn_paged_rows_desc *desc, gattn_stream st
  * A row that sees no position (its sequence is skipped, or none of its pages exists) gives
  * zeros and lse -infinity.  What a row does not see does not reach it, whatever it holds.
  * A value that it does see and that is infinite or NaN makes its output infinite or NaN.
+ * Scores of -infinity add nothing; a row that has no others is one that sees nothing.
  * head_dim: a multiple of 64 up to 256; num_heads * head_dim <= 65536; total_rows *
  * num_heads below 2^31 (else GATTN_E_UNSUPPORTED).
  */
